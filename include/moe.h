@@ -347,6 +347,161 @@ moe_status moe_forward_views(const moe_problem* p, const void* ws, size_t ws_byt
 moe_status moe_forward_views_ex(const moe_problem* p, const moe_forward_options* opt, const void* ws,
                                 size_t ws_bytes, moe_views* out);
 
+/* ---------------------------------------------------------------- around the routed FFN
+ * The operators that a model runs next to the forward above: other routing
+ * rules, the norms at a block's two ends, and a linear layer (the router's
+ * logits, projections, dense FFN layers), each with its gradient.  They follow
+ * the conventions at the top of this file (the entry points that take no
+ * workspace detect nothing on the device).  Rows may be strided where a descriptor
+ * has an `ld`: elements between the starts of two rows, 0 for contiguous rows. */
+
+/* Element types of the arrays whose type a descriptor names. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+
+/* ---------------------------------------------------------------- routing rules
+ * moe_route_ex - routing with a score function, a selection bias, expert groups
+ * and renormalised, scaled weights:
+ *   p_e = softmax over all E scores, or sigmoid(s_e)
+ *   key_e = p_e + bias_e (with a bias: it takes part in the selection only), else s_e
+ *   groups: the experts are n_group runs of E / n_group; a group ranks by its best
+ *     key (group_best = 1) or by the sum of its two best keys (2; p in the place of
+ *     s without a bias); experts of the topk_group best groups can be selected
+ *   ids[t, 0..k-1] = the k largest keys, descending; w = p[ids], divided by their
+ *     sum if renormalise, then times scale.
+ * Ties, among experts and among groups, go to the lower index; -0.0 == +0.0.
+ * A score of -inf (or NaN) masks its expert: p = 0, it comes after every other
+ * expert of the selectable groups and counts as absent in its group's rank (a
+ * group of masked experts ranks last).  If fewer than k experts are left, masked
+ * ones fill the slots in id order with weight 0; a row that is masked as a whole
+ * gets valid ids and weights 0.  +inf counts as the largest finite fp32.  bias
+ * values are finite.  p and keys are computed in fp32 (expf, IEEE division).
+ *   scores [T, E] of dtype, ld elements between rows
+ *   ids    [T, k] int32 out;  w [T, k] fp32 out
+ * Limits: those of moe_route, n_group <= 32 (UNSUPPORTED); n_group divides E,
+ * 1 <= topk_group <= n_group, k <= topk_group * (E / n_group) (INVALID_ARG).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_fn;
+typedef struct {
+  int score_fn;      /* moe_score_fn */
+  int renormalise;   /* 0 or 1 */
+  float scale;       /* factor of the weights, finite and not 0 */
+  int n_group;       /* 1: every expert can be selected */
+  int topk_group;
+  int group_best;    /* 1 or 2 */
+  const float* bias; /* [E] or NULL */
+  int dtype;         /* moe_dtype of scores (and of dscores) */
+  long long ld;      /* of scores */
+  long long ld_grad; /* of dscores */
+} moe_route_options;
+moe_status moe_route_ex(const moe_route_options* opt, const void* scores, int T, int E, int k, int32_t* ids, float* w,
+                        moe_stream_t stream);
+
+/* moe_route_backward - the gradient of moe_route_ex's weights into the scores, for
+ * the selection it made (which has no gradient, and the bias with it):
+ *   ids [T, k] as moe_route_ex wrote them (a row's ids differ; an id outside [0, E)
+ *       has no part in the result), dw [T, k] fp32
+ *   dscores [T, E] of dtype, every element written (0 where the score has no part).
+ * Nothing of the forward but ids is needed.  Errors: as moe_route_ex. */
+moe_status moe_route_backward(const moe_route_options* opt, const void* scores, int T, int E, int k,
+                              const int32_t* ids, const float* dw, void* dscores, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- block norms
+ * moe_norm_forward - the boundary between two blocks of a model in one pass over
+ * the residual stream h and a block's output o:
+ *   h_out = beta * h + alpha * gate * N_post(o)
+ *   x_out = N_pre(h_out)                          (the next block's input)
+ * N(v) = (v - mu) / sqrt(mean((v - mu)^2) + eps) * w + b over the H columns of a
+ * row; mu = 0 for MOE_NORM_RMS, the row's mean for MOE_NORM_LAYER; N_post = identity
+ * for MOE_NORM_NONE, and no x_out for a pre_norm of MOE_NORM_NONE.
+ * x_out is taken from h_out before h_out is rounded to its type.
+ *   h, h_out     [T, H] of h_dtype, ld_h between rows (h_out == h is allowed)
+ *   o, x_out     [T, H] of o_dtype, ld_o between rows (x_out == o is allowed)
+ *   gate         by `gate`: NULL | [H] of w_dtype | [T] fp32 | [T, H] of o_dtype, ld_o
+ *   w_*, b_*     [H] of w_dtype, each may be NULL (ones / zeros)
+ * o_dtype is h_dtype, or any type under an fp32 h.  1 <= H <= 16384.
+ * Any address, ld and H is taken; rows whose addresses and strides are
+ * multiples of 16 bytes (and H of 8) are read 16 bytes at a time.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_kind;
+typedef struct {
+  int T, H;
+  int post_norm, pre_norm; /* moe_norm_kind */
+  int gate;                /* moe_gate_kind */
+  int h_dtype, o_dtype, w_dtype;
+  float eps, alpha, beta;
+  long long ld_h, ld_o;
+} moe_norm_problem;
+moe_status moe_norm_forward(const moe_norm_problem* p, const void* h, const void* o, const void* gate,
+                            const void* w_post, const void* b_post, const void* w_pre, const void* b_pre, void* h_out,
+                            void* x_out, moe_stream_t stream);
+
+/* moe_norm_backward - its gradient.
+ *   dh_out [T, H] of h_dtype (gradient into h_out from what follows; NULL: zero),
+ *   dx_out [T, H] of o_dtype (with a pre_norm), h_out (with a pre_norm) and o as the
+ *   forward left and read them, gate and vectors as in the forward
+ *   dh [T, H] of h_dtype, d_o [T, H] of o_dtype: outputs, either may be NULL
+ *   dgate: [H] fp32 | [T] fp32 | [T, H] of o_dtype, ld_o;  dw_*, db_*: [H] fp32;
+ *   each may be NULL and is written, not added to.
+ * dgate needs b_post and w_post, the others only what the formulas hold.
+ * Sums over tokens are in fp32 in a fixed order.  dh may be dh_out, d_o may be o or
+ * dx_out.  T == 0 writes zeros to the [H] outputs.
+ * ws: moe_norm_backward_workspace_size(p) bytes, 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+size_t moe_norm_backward_workspace_size(const moe_norm_problem* p);
+moe_status moe_norm_backward(const moe_norm_problem* p, const void* dh_out, const void* dx_out, const void* h_out,
+                             const void* o, const void* gate, const void* w_post, const void* b_post,
+                             const void* w_pre, void* dh, void* d_o, void* dgate, float* dw_post, float* db_post,
+                             float* dw_pre, float* db_pre, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- linear layer
+ * moe_linear - y = alpha * act(z) + residual, z = x W^T + bias, fp32 accumulation,
+ * one rounding each of y and z:
+ *   x [M, K], w [N, K] of dtype (bf16 or fp16), ld_x / ld_w between rows: multiples of
+ *     8, bases 16-byte aligned (a TMA requirement; K itself is free)
+ *   bias [N] of bias_dtype or NULL;  residual [M, N] of out_dtype, ld_y, or NULL
+ *   y [M, N] of out_dtype, ld_y (y == residual is allowed)
+ *   z [M, N] of dtype, contiguous, or NULL (kept for the gradient of an activation)
+ * act: MOE_ACT_GELU is the erf form, MOE_ACT_GELU_TANH the tanh form.
+ * K == 0 is INVALID_ARG; M == 0 or N == 0 a no-op.
+ * ws: moe_linear_workspace_size(p) bytes, 256-byte aligned: the status word
+ * (moe_read_device_status), cleared by the call.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+} moe_act;
+typedef struct {
+  int M, N, K;
+  int dtype;      /* of x, w, z (and dx, dw): MOE_DTYPE_BF16 or MOE_DTYPE_F16 */
+  int out_dtype;  /* of y, residual (and dy) */
+  int bias_dtype;
+  int act;        /* moe_act */
+  float alpha;
+  long long ld_x, ld_w, ld_y;
+} moe_linear_problem;
+size_t moe_linear_workspace_size(const moe_linear_problem* p);
+moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w, const void* bias,
+                      const void* residual, void* y, void* z, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_linear_backward - dz = alpha * dy * act'(z), dx = dz W, dw = dz^T x,
+ * dbias = the column sums of dz (the residual's gradient is dy itself):
+ *   dy [M, N] of out_dtype, ld_y;  x, w as in the forward;  z as the forward kept it
+ *   (NULL without an activation)
+ *   dx [M, K] and dw [N, K] of dtype, contiguous;  dbias [N] fp32;  each may be NULL.
+ * dz is rounded to dtype for the two products (the tensor cores' operand type; dy
+ * itself is read where it already is dz), dbias sums it unrounded in fp32, in a
+ * fixed order.  M == 0 writes zeros to dw and dbias.
+ * ws: moe_linear_backward_workspace_size(p) bytes, 256-byte aligned, status word at
+ * its head.  Errors: as moe_linear. */
+size_t moe_linear_backward_workspace_size(const moe_linear_problem* p);
+moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, const void* x, const void* w,
+                               const void* z, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
 /* ---------------------------------------------------------------- diagnostics
  * moe_read_device_status - synchronises `stream`, then returns the status
  * recorded on the device in the status word at the head of `ws` (MOE_OK,
@@ -374,7 +529,8 @@ moe_status moe_read_device_status(const void* ws, moe_stream_t stream);
  * Stage names: route_rank (with the per-tensor FP8 amax of x), scan_tiles,
  * scatter_gather, gateup_gemm, quant_h, down_gemm, combine (grouped path);
  * rd_prep, rd_gateup, rd_reduce, rd_down, combine (route-direct path); scatter,
- * tile_map, header_reset. */
+ * tile_map, header_reset; route_ex, route_backward, norm_forward, norm_backward,
+ * linear, linear_dz, linear_dx, linear_dw, column_sums. */
 typedef struct {
   char name[32];
   double total_ms;

@@ -36,6 +36,29 @@ MOE_PATH_AUTO = 0
 MOE_PATH_GROUPED = 1
 MOE_PATH_ROUTE_DIRECT = 2
 
+# moe_dtype
+MOE_DTYPE_F32 = 0
+MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F16 = 2
+# moe_score_fn
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+# moe_norm_kind
+MOE_NORM_NONE = 0
+MOE_NORM_RMS = 1
+MOE_NORM_LAYER = 2
+# moe_gate_kind
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_FULL = 3
+# moe_act
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_SILU = 2
+MOE_ACT_GELU = 3
+MOE_ACT_GELU_TANH = 4
+
 QUANT_BY_NAME = {"bf16": MOE_BF16, "fp8_tensor": MOE_FP8_PER_TENSOR, "fp8_block": MOE_FP8_BLOCK128,
                  "mxfp8": MOE_MXFP8}
 GEMM_BM = 128  # row-tile height of the grouped GEMMs (tile map of moe_forward)
@@ -63,8 +86,30 @@ class moe_stage_time(ctypes.Structure):
 
 
 _vp, _sz, _i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+_ll, _f = ctypes.c_longlong, ctypes.c_float
+
+
+class moe_route_options(ctypes.Structure):
+    _fields_ = [("score_fn", _i), ("renormalise", _i), ("scale", _f), ("n_group", _i), ("topk_group", _i),
+                ("group_best", _i), ("bias", _vp), ("dtype", _i), ("ld", _ll), ("ld_grad", _ll)]
+
+
+class moe_norm_problem(ctypes.Structure):
+    _fields_ = [("T", _i), ("H", _i), ("post_norm", _i), ("pre_norm", _i), ("gate", _i), ("h_dtype", _i),
+                ("o_dtype", _i), ("w_dtype", _i), ("eps", _f), ("alpha", _f), ("beta", _f), ("ld_h", _ll),
+                ("ld_o", _ll)]
+
+
+class moe_linear_problem(ctypes.Structure):
+    _fields_ = [("M", _i), ("N", _i), ("K", _i), ("dtype", _i), ("out_dtype", _i), ("bias_dtype", _i), ("act", _i),
+                ("alpha", _f), ("ld_x", _ll), ("ld_w", _ll), ("ld_y", _ll)]
+
+
 _P = ctypes.POINTER(moe_problem)
 _O = ctypes.POINTER(moe_forward_options)
+_RO = ctypes.POINTER(moe_route_options)
+_NP = ctypes.POINTER(moe_norm_problem)
+_LP = ctypes.POINTER(moe_linear_problem)
 _SIGS = {
     "moe_route": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "moe_shuffle_workspace_size": (_sz, [_i, _i, _i]),
@@ -84,6 +129,15 @@ _SIGS = {
     "moe_mx_weight_scales": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
     "moe_mx_blocked_workspace_size": (_sz, [_i, _i]),
     "moe_mx_blocked_scales": (_i, [_vp, _i, _i, _vp, _i, _vp, _sz, _vp, _vp, _sz, _vp]),
+    "moe_route_ex": (_i, [_RO, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_route_backward": (_i, [_RO, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "moe_norm_forward": (_i, [_NP] + [_vp] * 10),
+    "moe_norm_backward_workspace_size": (_sz, [_NP]),
+    "moe_norm_backward": (_i, [_NP] + [_vp] * 16 + [_sz, _vp]),
+    "moe_linear_workspace_size": (_sz, [_LP]),
+    "moe_linear": (_i, [_LP] + [_vp] * 7 + [_sz, _vp]),
+    "moe_linear_backward_workspace_size": (_sz, [_LP]),
+    "moe_linear_backward": (_i, [_LP] + [_vp] * 8 + [_sz, _vp]),
     "moe_read_device_status": (_i, [_vp, _vp]),
     "moe_profile_start": (_i, []),
     "moe_profile_start_stage": (_i, [ctypes.c_char_p]),
@@ -265,6 +319,91 @@ def moe_forward_views(p: moe_problem, ws, ws_bytes=None) -> moe_views:
     v = moe_views()
     _check(lib().moe_forward_views(ctypes.byref(p), _ptr(ws), nb, ctypes.byref(v)), "moe_forward_views")
     return v
+
+
+def _rows(t, name: str = "tensor") -> Optional[int]:
+    """Device pointer of a CUDA tensor whose rows are contiguous (the row stride is the
+    descriptor's ld); None -> NULL; ints pass through."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError(f"{name}: device tensor expected")
+    if not t.is_contiguous() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    return t.data_ptr()
+
+
+def route_options(score="softmax", bias=None, n_group=1, topk_group=1, group_best=1, renormalise=True, scale=1.0,
+                  dtype=MOE_DTYPE_F32, ld=0, ld_grad=0) -> moe_route_options:
+    """Routing rule of moe_route_ex (see include/moe.h).  The bias tensor must outlive the options."""
+    fn = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score] if isinstance(score, str) else int(score)
+    return moe_route_options(fn, 1 if renormalise else 0, float(scale), int(n_group), int(topk_group),
+                             int(group_best), _ptr(bias), int(dtype), int(ld), int(ld_grad))
+
+
+def moe_route_ex(opt: moe_route_options, scores, T, E, k, ids, w, stream=None) -> None:
+    """Routing with a score function, selection bias, expert groups and renormalised weights."""
+    _check(lib().moe_route_ex(opt, _rows(scores), T, E, k, _ptr(ids), _ptr(w), _stream(stream)), "moe_route_ex")
+
+
+def moe_route_backward(opt: moe_route_options, scores, T, E, k, ids, dw, dscores, stream=None) -> None:
+    """Gradient of moe_route_ex's weights into the scores."""
+    _check(lib().moe_route_backward(opt, _rows(scores), T, E, k, _ptr(ids), _ptr(dw), _rows(dscores),
+                                    _stream(stream)), "moe_route_backward")
+
+
+def norm_problem(T, H, post_norm=MOE_NORM_RMS, pre_norm=MOE_NORM_RMS, gate=MOE_GATE_NONE, h_dtype=MOE_DTYPE_BF16,
+                 o_dtype=MOE_DTYPE_BF16, w_dtype=MOE_DTYPE_F32, eps=1e-6, alpha=1.0, beta=1.0, ld_h=0,
+                 ld_o=0) -> moe_norm_problem:
+    return moe_norm_problem(T, H, post_norm, pre_norm, gate, h_dtype, o_dtype, w_dtype, eps, alpha, beta, ld_h, ld_o)
+
+
+def moe_norm_forward(p: moe_norm_problem, h, o, gate, w_post, b_post, w_pre, b_pre, h_out, x_out,
+                     stream=None) -> None:
+    """h_out = beta h + alpha gate N_post(o), x_out = N_pre(h_out)."""
+    _check(lib().moe_norm_forward(p, _rows(h), _rows(o), _rows(gate), _ptr(w_post), _ptr(b_post), _ptr(w_pre),
+                                  _ptr(b_pre), _rows(h_out), _rows(x_out), _stream(stream)), "moe_norm_forward")
+
+
+def moe_norm_backward_workspace_size(p: moe_norm_problem) -> int:
+    return int(lib().moe_norm_backward_workspace_size(p))
+
+
+def moe_norm_backward(p: moe_norm_problem, dh_out, dx_out, h_out, o, gate, w_post, b_post, w_pre, dh, d_o, dgate,
+                      dw_post, db_post, dw_pre, db_pre, ws, ws_bytes=None, stream=None) -> None:
+    """Gradient of moe_norm_forward; outputs given as None are left out."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(lib().moe_norm_backward(p, _rows(dh_out), _rows(dx_out), _rows(h_out), _rows(o), _rows(gate),
+                                   _ptr(w_post), _ptr(b_post), _ptr(w_pre), _rows(dh), _rows(d_o), _rows(dgate),
+                                   _ptr(dw_post), _ptr(db_post), _ptr(dw_pre), _ptr(db_pre), _ptr(ws), nb,
+                                   _stream(stream)), "moe_norm_backward")
+
+
+def linear_problem(M, N, K, dtype=MOE_DTYPE_BF16, out_dtype=MOE_DTYPE_BF16, bias_dtype=MOE_DTYPE_F32,
+                   act=MOE_ACT_NONE, alpha=1.0, ld_x=0, ld_w=0, ld_y=0) -> moe_linear_problem:
+    return moe_linear_problem(M, N, K, dtype, out_dtype, bias_dtype, act, alpha, ld_x, ld_w, ld_y)
+
+
+def moe_linear_workspace_size(p: moe_linear_problem) -> int:
+    return int(lib().moe_linear_workspace_size(p))
+
+
+def moe_linear(p: moe_linear_problem, x, w, bias, residual, y, z, ws, ws_bytes=None, stream=None) -> None:
+    """y = alpha act(x w^T + bias) + residual; z keeps the pre-activation."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(lib().moe_linear(p, _rows(x), _rows(w), _ptr(bias), _rows(residual), _rows(y), _ptr(z), _ptr(ws), nb,
+                            _stream(stream)), "moe_linear")
+
+
+def moe_linear_backward_workspace_size(p: moe_linear_problem) -> int:
+    return int(lib().moe_linear_backward_workspace_size(p))
+
+
+def moe_linear_backward(p: moe_linear_problem, dy, x, w, z, dx, dw, dbias, ws, ws_bytes=None, stream=None) -> None:
+    """Gradient of moe_linear; outputs given as None are left out."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(lib().moe_linear_backward(p, _rows(dy), _rows(x), _rows(w), _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias),
+                                     _ptr(ws), nb, _stream(stream)), "moe_linear_backward")
 
 
 def moe_read_device_status(ws, stream=None) -> int:

@@ -19,6 +19,7 @@ constexpr int kMaxE = 512;
 constexpr int kMaxK = 32;
 constexpr int kMaxShared = 16;        // shared experts of moe_forward_ex
 constexpr int kRouteDirectMaxRoutes = 1024;
+constexpr int kNormMaxH = 16384;      // columns of a row of the block norms
 
 // Tokens handled by one block of the route/rank kernel (its routes are that times k).
 inline int route_tokens_per_block(int k) { return k >= kMaxRoutesPerBlock ? 1 : kMaxRoutesPerBlock / k; }
@@ -200,6 +201,88 @@ struct DecodeArgs {
 };
 cudaError_t launch_route_direct(const DecodeArgs& a, cudaStream_t s);
 size_t route_direct_uniq_bytes(int T, int E, int k);
+
+// Routing rules and their gradient (router.cu).
+struct RouteArgs {
+  int T, E, k;
+  int score_fn, renormalise;  // moe_score_fn, 0 / 1
+  float scale;
+  int n_group, topk_group, group_best;  // n_group 1: no limit to groups
+  const float* bias;
+  long long ld;  // elements between rows of the scores
+  int32_t* ids;  // forward
+  float* w;
+};
+cudaError_t launch_route_ex(const void* scores, int dtype, const RouteArgs& a, cudaStream_t s);
+cudaError_t launch_route_backward(const void* scores, int dtype, const RouteArgs& a, const int32_t* ids,
+                                  const float* dw, void* dscores, long long ld_d, cudaStream_t s);
+
+// Block norms (norm.cu).  `vec`: every row and vector can be read 16 bytes at a time.
+struct NormArgs {
+  int T, H;
+  int post, pre, gate_kind;  // moe_norm_kind, moe_gate_kind
+  int w_dtype;
+  float eps, alpha, beta;
+  long long ld_h, ld_o;
+  const void* h;  // forward: h; backward: h_out
+  const void* o;
+  const void* gate;
+  const void *w_post, *b_post, *w_pre, *b_pre;
+  void *h_out, *x_out;  // forward
+  const void *dh_out, *dx_out;  // backward
+  void *dh, *d_o, *dgate;
+  float* partials;  // column sums per block: [blocks][nacc][H]
+  int nacc, acc_in_smem;
+  int acc_dw_post, acc_db_post, acc_dw_pre, acc_db_pre, acc_dgate;  // index among the sums, -1: not wanted
+};
+size_t norm_partials_bytes(int T, int H);
+cudaError_t launch_norm_forward(const NormArgs& a, int h_dtype, int o_dtype, bool vec, cudaStream_t s);
+// sums: dw_post, db_post, dw_pre, db_pre, dgate (per channel), each fp32 [H] or null.
+cudaError_t launch_norm_backward(const NormArgs& a, int h_dtype, int o_dtype, bool vec, float* const (&sums)[5],
+                                 cudaStream_t s);
+// out.p[c / width][c % width] = sum over p of partials[p * stride + c], c < n, in a fixed order.
+struct ColumnOutputs {
+  float* p[5];
+};
+cudaError_t launch_column_sums(const float* partials, int nparts, size_t stride, int n, const ColumnOutputs& out,
+                               int width, cudaStream_t s);
+
+// Linear layer with a fused epilogue (linear.cu).
+struct LinearArgs {
+  int M, N, K;
+  int dtype, out_dtype, bias_dtype, act;
+  float alpha;
+  long long ld_x, ld_w, ld_y;
+  const void* x;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* z;
+  DeviceHeader* hdr;
+};
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+struct LinearBackwardArgs {
+  int M, N, K;
+  int dtype, dy_dtype, act;
+  float alpha;
+  long long ld_x, ld_w, ld_y;
+  const void* dy;
+  const void* x;
+  const void* w;
+  const void* z;
+  void* dx;
+  void* dw;
+  float* dbias;
+  void* dz;           // [M][ld_dz] of dtype, where dy itself cannot serve
+  float* partials;    // column sums of dz per row chunk
+  DeviceHeader* hdr;
+};
+// Whether dy can be read as dz (no activation, factor 1, rows that TMA can read).
+bool linear_dz_is_dy(const LinearBackwardArgs& a);
+size_t linear_dz_bytes(int M, int N);
+size_t linear_partials_bytes(int M, int N);
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s);
 
 // Launch `kernel` as a programmatic dependent of the previous work on the stream:
 // its launch is prepared while the predecessor runs, and it waits for the

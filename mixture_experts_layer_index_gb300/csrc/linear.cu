@@ -1,0 +1,632 @@
+// Linear layer with bias, activation and residual in its epilogue (moe_linear) and
+// its gradient (moe_linear_backward) on the 5th-generation tensor cores:
+//   z = x W^T + b,   y = alpha act(z) + residual
+//   dz = alpha dy act'(z),   db = sum_m dz,   dx = dz W,   dW = dz^T x
+//
+// One kernel computes all three products.  Its output is out[r][c] (row-major):
+// operand A supplies the 128 columns c of a tile on the 128 TMEM lanes, operand B
+// the BN rows r on the TMEM columns, so that the lanes of an epilogue warp hold
+// neighbouring addresses of one output row and few rows (decode) cost a narrow
+// BN instead of a mostly empty 128-row tile.
+//   y : A = W  [N][K],  B = x  [M][K]; both contiguous along the sum (K-major)
+//   dx: A = W  [N][K] contiguous along its columns (MN-major), B = dz [M][N] K-major
+//   dW: A = x  [M][K] MN-major,                                B = dz [M][N] MN-major
+// so no operand is ever transposed in memory.  All operands come by TMA in boxes of
+// 128-byte rows with the 128-byte swizzle; edges are zero-filled by TMA.
+//
+// Few tiles and a long sum: `splits` blocks of one cluster share a tile, each takes
+// a range of the sum, and after a cluster barrier each adds its share of the rows
+// over all partials, read from the others' shared memory in rank order: no
+// workspace, no atomics, the same result every time.
+#include <cuda_fp16.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace lin {
+
+constexpr int BM = 128;  // output columns per tile (TMEM lanes)
+constexpr int BK = 64;   // values of the sum per stage: 128 bytes
+constexpr int THREADS = 128;
+constexpr int MAX_SPLITS = 8;
+constexpr int A_BYTES = BM * BK * 2;
+
+// Stages: two blocks per SM up to BN = 128 (one loads while the other stores), one
+// block with a deep ring at BN = 256.
+__host__ __device__ constexpr int stages_of(int BN) { return BN <= 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 3 : 4; }
+__host__ __device__ constexpr int stage_bytes(int BN) { return A_BYTES + BN * BK * 2; }
+// 1 KB to align the ring, the barriers after it
+__host__ __device__ constexpr int smem_bytes(int BN) { return 1024 + stages_of(BN) * stage_bytes(BN) + 256; }
+
+struct Params {
+  int C, R;        // output columns and rows
+  int nk;          // stages of the whole sum
+  int splits;      // blocks per tile (cluster size)
+  int nC, nR;      // tiles
+  int nacc;        // accumulators that a block's part of the sum is spread over
+  uint32_t tmem_cols;
+  int type;        // 0 = f16, 1 = bf16 operands
+  int act, bias_dtype, out_dtype, z_dtype;
+  float alpha;
+  long long ld_y, ld_z;
+  const void* bias;
+  const void* residual;
+  void* y;
+  void* z;
+  int reset_status;
+  DeviceHeader* hdr;
+};
+
+// Descriptor of an MN-major operand in the layout of TMA boxes of 64 values along MN
+// (128 bytes, 128-byte swizzle) x 64 along the sum: 8-row groups along the sum 1024
+// bytes apart (stride byte offset), the next 64 along MN one box = 8192 bytes on
+// (leading byte offset).
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// fp32 at shared-memory address `addr` of block `rank` of the cluster
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// ------------------------------------------------------------------ activations
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return fmaxf(z, 0.0f);
+    case MOE_ACT_SILU: return z / (1.0f + expf(-z));
+    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+    case MOE_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
+    default: return z;
+  }
+}
+__device__ __forceinline__ float act_grad(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case MOE_ACT_SILU: {
+      const float s = 1.0f / (1.0f + expf(-z));
+      return s * (1.0f + z * (1.0f - s));
+    }
+    case MOE_ACT_GELU: return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
+    case MOE_ACT_GELU_TANH: {
+      const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
+      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+    }
+    default: return 1.0f;
+  }
+}
+
+__device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i) {
+  if (dtype == MOE_DTYPE_F32) return static_cast<const float*>(p)[i];
+  if (dtype == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+// n values of one output column, rows r0.. of an array with ld elements between rows.
+template <int CH>
+__device__ __forceinline__ void store_rows(void* out, int dtype, size_t at, long long ld, int n, const float (&v)[CH]) {
+  if (dtype == MOE_DTYPE_F32) {
+    float* p = static_cast<float*>(out) + at;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (i < n) p[i * ld] = v[i];
+  } else if (dtype == MOE_DTYPE_BF16) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out) + at;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (i < n) p[i * ld] = __float2bfloat16_rn(v[i]);
+  } else {
+    __half* p = static_cast<__half*>(out) + at;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (i < n) p[i * ld] = __float2half_rn(v[i]);
+  }
+}
+
+template <int CH>
+__device__ __forceinline__ void add_rows(float (&v)[CH], const void* in, int dtype, size_t at, long long ld, int n) {
+  float r[CH];
+  if (dtype == MOE_DTYPE_F32) {
+    const float* p = static_cast<const float*>(in) + at;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) r[i] = i < n ? p[i * ld] : 0.0f;
+  } else if (dtype == MOE_DTYPE_BF16) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(in) + at;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) r[i] = i < n ? __bfloat162float(p[i * ld]) : 0.0f;
+  } else {
+    const __half* p = static_cast<const __half*>(in) + at;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) r[i] = i < n ? __half2float(p[i * ld]) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) v[i] += r[i];
+}
+
+// The fused epilogue of n rows from r0 of output column c (one thread's values).
+template <int CH>
+__device__ __forceinline__ void finish(const Params& p, float (&v)[CH], int r0, int n, int c) {
+  if (c >= p.C || n <= 0) return;
+  if (p.bias) {
+    const float b = load_as_f32(p.bias, p.bias_dtype, c);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] += b;
+  }
+  if (p.z) store_rows<CH>(p.z, p.z_dtype, static_cast<size_t>(r0) * p.ld_z + c, p.ld_z, n, v);
+  if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = act_value(v[i], p.act);
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) v[i] *= p.alpha;
+  const size_t at = static_cast<size_t>(r0) * p.ld_y + c;
+  if (p.residual) add_rows<CH>(v, p.residual, p.out_dtype, at, p.ld_y, n);
+  store_rows<CH>(p.y, p.out_dtype, at, p.ld_y, n, v);
+}
+
+template <int CH>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[CH]) {
+  static_assert(CH == 16 || CH == 32, "16 or 32 columns");
+  if constexpr (CH == 16) tmem_ld16(addr, v);
+  else tmem_ld32(addr, v);
+}
+
+// Warp 0 loads, warp 1 issues the MMAs, then all four warps (one per 32 TMEM lanes)
+// run the epilogue.
+template <int BN, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__ CUtensorMap tmA,
+                                                         const __grid_constant__ CUtensorMap tmB, const Params p) {
+  static_assert(!B_MN || BN >= 64, "an MN-major box is 64 wide");
+  constexpr int STAGES = stages_of(BN), STAGE = stage_bytes(BN);
+  constexpr int CH = BN < 32 ? BN : 32;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES), done = smem_u32(bars + 2 * STAGES);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+    // a wait that records a timeout lasts seconds: nothing of this launch is lost here
+    if (p.reset_status && blockIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // tiles: 16 row tiles side by side, then the next column tile, so that the blocks in
+  // flight share both operands in L2
+  const int rank = p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / p.splits;
+  constexpr int GR = 16;
+  const int group = tile / (GR * p.nC), in_group = tile - group * (GR * p.nC);
+  const int rows_here = min(GR, p.nR - group * GR);
+  const int c0 = in_group / rows_here * BM;
+  const int r0 = (group * GR + in_group % rows_here) * BN;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.nk) * rank / p.splits);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / p.splits);
+  const int n = kb1 - kb0;
+  const int nacc = min(p.nacc, n);  // accumulators that this block fills
+
+  if (warp == 0 && lane == 0) {
+    int issued = 0;
+    bool ok = true;
+    for (; issued < n; ++issued) {
+      const int s = issued % STAGES;
+      if (!mbar_wait(empty0 + 8 * s, ((issued / STAGES) & 1) ^ 1, abort_flag, p.hdr, 0x510000u)) {
+        ok = false;
+        break;
+      }
+      const uint32_t full = full0 + 8 * s, a = smem_u32(smem + s * STAGE), b = a + A_BYTES;
+      const int k = (kb0 + issued) * BK;
+      mbar_arrive_expect_tx(full, STAGE);
+      if (A_MN) {
+        tma_load_2d(a, &tmA, c0, k, full);
+        tma_load_2d(a + A_BYTES / 2, &tmA, c0 + 64, k, full);
+      } else {
+        tma_load_2d(a, &tmA, k, c0, full);
+      }
+      if (B_MN) {
+#pragma unroll
+        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &tmB, r0 + j * 64, k, full);
+      } else {
+        tma_load_2d(b, &tmB, k, r0, full);
+      }
+    }
+    if (!ok)  // let the copies already issued land before shared memory is given up
+      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+        mbar_wait_quiet(full0 + 8 * (i % STAGES), (i / STAGES) & 1, 50000000ull);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = make_idesc(p.type, p.type, BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+    // kind::f16 codes: 0 = f16, 1 = bf16
+    int acc = -1;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % STAGES;
+      if (!mbar_wait(full0 + 8 * s, (i / STAGES) & 1, abort_flag, p.hdr, 0x520000u)) break;
+      tc_fence_after();
+      const uint32_t a = smem_u32(smem + s * STAGE), b = a + A_BYTES;
+      const int now = i * nacc / n;
+      const bool fresh = now != acc;
+      acc = now;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t da = A_MN ? sw128_mnmajor_desc(a + kk * 2048) : sw128_kmajor_desc(a + kk * 32);
+        const uint64_t db = B_MN ? sw128_mnmajor_desc(b + kk * 2048) : sw128_kmajor_desc(b + kk * 32);
+        mma_f16(tmem + acc * BN, da, db, idesc, !(fresh && kk == 0));
+      }
+      mma_commit(empty0 + 8 * s);
+    }
+    mma_commit(done);
+  }
+  __syncwarp();
+  if (lane == 0) mbar_wait(done, 0, abort_flag, p.hdr, 0x530000u);
+  __syncthreads();
+  tc_fence_after();
+  const bool good = *abort_flag == 0;
+  const uint32_t quad = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+  const int cl = warp * 32 + lane;
+
+  auto gather = [&](int j, float (&v)[CH]) {
+    tmem_load<CH>(quad + j, v);
+    tmem_ld_wait();
+    for (int q = 1; q < nacc; ++q) {
+      float u[CH];
+      tmem_load<CH>(quad + q * BN + j, u);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < CH; ++i) v[i] += u[i];
+    }
+  };
+  if (p.splits == 1) {
+    if (good) {
+#pragma unroll 1
+      for (int j = 0; j < BN; j += CH) {
+        if (r0 + j >= p.R) break;
+        float v[CH];
+        gather(j, v);
+        finish<CH>(p, v, r0 + j, min(CH, p.R - r0 - j), c0 + cl);
+      }
+    }
+  } else {
+    float* part = reinterpret_cast<float*>(smem);  // [BN][128], over the ring: every MMA has read it
+    if (good) {
+#pragma unroll 1
+      for (int j = 0; j < BN; j += CH) {
+        float v[CH];
+        gather(j, v);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) part[(j + i) * BM + cl] = v[i];
+      }
+    }
+    cluster_sync_all();
+    if (good) {
+      const int per = BN / p.splits;  // rows that this block adds up and finishes
+      const uint32_t mine = smem_u32(part) + cl * 4;
+      constexpr int RB = 2;  // rows at a time: with up to 8 ranks, 16 loads in flight
+      for (int j = rank * per; j < (rank + 1) * per; j += RB) {
+        if (r0 + j >= p.R) break;
+        float v[RB] = {};
+#pragma unroll
+        for (int q = 0; q < MAX_SPLITS; ++q)
+          if (q < p.splits)
+#pragma unroll
+            for (int i = 0; i < RB; ++i) v[i] += ld_cluster_f32(mine + (j + i) * (BM * 4), q);
+        finish<RB>(p, v, r0 + j, min(RB, p.R - r0 - j), c0 + cl);
+      }
+    }
+    cluster_sync_all();  // no block leaves while another still reads its partial
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// A 16-bit matrix of `outer` rows of `inner` values, ld values apart, in boxes.
+bool encode(CUtensorMap* map, const void* base, int type, uint64_t inner, uint64_t outer, long long ld,
+            uint32_t box_inner, uint32_t box_outer) {
+  EncodeTiledFn fn = get_encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {inner, outer};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, type ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operand {
+  const void* base;
+  long long ld;
+  int inner, outer;  // inner: contiguous extent
+};
+
+template <int BN, bool A_MN, bool B_MN>
+cudaError_t launch_tile(const Operand& a, const Operand& b, Params p, cudaStream_t s) {
+  CUtensorMap ta, tb;
+  if (!encode(&ta, a.base, p.type, a.inner, a.outer, a.ld, 64, A_MN ? 64 : BM) ||
+      !encode(&tb, b.base, p.type, b.inner, b.outer, b.ld, 64, B_MN ? 64 : BN))
+    return cudaErrorInvalidValue;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      linear_kernel<BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
+  if (attr != cudaSuccess) return attr;
+  p.nC = (p.C + BM - 1) / BM;
+  p.nR = (p.R + BN - 1) / BN;
+  int cols = 32;
+  while (cols < BN * p.nacc) cols *= 2;
+  p.tmem_cols = cols;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeClusterDimension;
+  la[0].val.clusterDim.x = p.splits;
+  la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.nC) * p.nR * p.splits);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cfg.stream = s;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<BN, A_MN, B_MN>, ta, tb, p);
+}
+
+// out[r][c] = sum_k A[c][k] B[r][k], tile and split chosen by the shape.
+template <bool A_MN, bool B_MN>
+cudaError_t product(const Operand& a, const Operand& b, int K, Params p, cudaStream_t s) {
+  p.nk = (K + BK - 1) / BK;
+  int bn = p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
+  if (B_MN && bn < 64) bn = 64;
+  const long long nC = (p.C + BM - 1) / BM;
+  if (p.R > 128 && nC * ((p.R + 255) / 256) >= 152) bn = 256;
+  const long long tiles = nC * ((p.R + bn - 1) / bn);
+  const int slots = 152 * (bn == 256 ? 1 : 2);
+  p.splits = 1;
+  while (p.splits < MAX_SPLITS && tiles * p.splits * 2 <= slots && p.nk / (p.splits * 2) >= 2) p.splits *= 2;
+  // fp32 output: the tensor core's running sum rounds at every step, so its length is
+  // kept short by spreading the sum over up to four accumulators
+  p.nacc = 1;
+  if (p.out_dtype == MOE_DTYPE_F32) p.nacc = bn <= 64 ? 4 : 2;
+  switch (bn) {
+    case 16:
+      if constexpr (!B_MN) return launch_tile<16, A_MN, B_MN>(a, b, p, s);
+    case 32:
+      if constexpr (!B_MN) return launch_tile<32, A_MN, B_MN>(a, b, p, s);
+    case 64: return launch_tile<64, A_MN, B_MN>(a, b, p, s);
+    case 128: return launch_tile<128, A_MN, B_MN>(a, b, p, s);
+    default: return launch_tile<256, A_MN, B_MN>(a, b, p, s);
+  }
+}
+
+// ------------------------------------------------------------------ dz
+// dz = alpha dy act'(z) in the operands' type, and per chunk of rows the fp32 sums
+// of its unrounded columns.  Thread (x, y): columns 8 x .. 8 x + 7 of every 8th row.
+struct DzArgs {
+  int M, N, rows;  // rows per chunk
+  int dy_dtype, dtype, act;
+  float alpha;
+  long long ld_dy, ld_dz;
+  const void* dy;
+  const void* z;
+  void* dz;
+  float* partials;  // [chunks][N], null: not wanted
+  bool vec;
+};
+
+__device__ __forceinline__ void load8(float (&v)[8], const void* p, int dtype, size_t at, int n, bool vec) {
+  if (vec) {
+    if (dtype == MOE_DTYPE_F32) {
+      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      const float4 a = __ldg(q), b = __ldg(q + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = dtype == MOE_DTYPE_BF16
+                             ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
+                             : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? load_as_f32(p, dtype, at + i) : 0.0f;
+  }
+}
+
+__global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
+  __shared__ float s_sum[8][256 + 8];
+  const int c = blockIdx.x * 256 + threadIdx.x * 8;
+  const int n = min(8, a.N - c);
+  const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
+  float sum[8] = {};
+  if (n > 0) {
+    for (int m = m0 + threadIdx.y; m < m1; m += 8) {
+      float g[8], z[8];
+      load8(g, a.dy, a.dy_dtype, static_cast<size_t>(m) * a.ld_dy + c, n, a.vec);
+      if (a.act != MOE_ACT_NONE) load8(z, a.z, a.dtype, static_cast<size_t>(m) * a.N + c, n, a.vec);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] *= a.alpha;
+        if (a.act != MOE_ACT_NONE) g[i] *= act_grad(z[i], a.act);
+        sum[i] += g[i];
+      }
+      if (a.dz) {  // rows of the workspace are padded to 8 values: a whole store even at the edge
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (a.dtype == MOE_DTYPE_BF16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(g[2 * i], g[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+          } else {
+            const __half2 b = __floats2half2_rn(g[2 * i], g[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  if (!a.partials) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_sum[threadIdx.y][threadIdx.x * 8 + i] = sum[i];
+  __syncthreads();
+  const int col = threadIdx.y * 32 + threadIdx.x;
+  if (blockIdx.x * 256 + col < a.N) {
+    float v = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 8; ++y) v += s_sum[y][col];
+    a.partials[static_cast<size_t>(blockIdx.y) * a.N + blockIdx.x * 256 + col] = v;
+  }
+}
+
+// Rows per chunk: at least 64, at most 256 chunks.
+inline int dz_rows(int M) {
+  const int r = (M + 255) / 256;
+  return r < 64 ? 64 : (r + 7) / 8 * 8;
+}
+inline long long dz_ld(int N) { return (N + 7) / 8 * 8; }
+
+}  // namespace lin
+
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+  using namespace lin;
+  Params p{};
+  p.C = a.N;
+  p.R = a.M;
+  p.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
+  p.act = a.act;
+  p.bias_dtype = a.bias_dtype;
+  p.out_dtype = a.out_dtype;
+  p.z_dtype = a.dtype;
+  p.alpha = a.alpha;
+  p.ld_y = a.ld_y;
+  p.ld_z = a.N;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.y = a.y;
+  p.z = a.z;
+  p.reset_status = 1;
+  p.hdr = a.hdr;
+  stage_begin("linear", s);
+  const cudaError_t err = product<false, false>({a.w, a.ld_w, a.K, a.N}, {a.x, a.ld_x, a.K, a.M}, a.K, p, s);
+  stage_end(s);
+  return err;
+}
+
+size_t linear_dz_bytes(int M, int N) { return static_cast<size_t>(M) * lin::dz_ld(N) * 2; }
+size_t linear_partials_bytes(int M, int N) {
+  const int rows = lin::dz_rows(M);
+  return static_cast<size_t>((M + rows - 1) / rows) * N * sizeof(float);
+}
+
+bool linear_dz_is_dy(const LinearBackwardArgs& a) {
+  return a.act == MOE_ACT_NONE && a.alpha == 1.0f && a.dy_dtype == a.dtype && a.ld_y % 8 == 0 &&
+         reinterpret_cast<uintptr_t>(a.dy) % 16 == 0;
+}
+
+cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) {
+  using namespace lin;
+  const bool direct = linear_dz_is_dy(a);
+  const bool products = a.dx || a.dw;
+  cudaError_t err = cudaSuccess;
+  if ((!direct && products) || a.dbias) {
+    DzArgs d{};
+    d.M = a.M;
+    d.N = a.N;
+    d.rows = dz_rows(a.M);
+    d.dy_dtype = a.dy_dtype;
+    d.dtype = a.dtype;
+    d.act = a.act;
+    d.alpha = a.alpha;
+    d.ld_dy = a.ld_y;
+    d.ld_dz = dz_ld(a.N);
+    d.dy = a.dy;
+    d.z = a.z;
+    d.dz = direct || !products ? nullptr : a.dz;
+    d.partials = a.dbias ? a.partials : nullptr;
+    d.vec = a.N % 8 == 0 && a.ld_y % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
+            reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
+    const int chunks = (a.M + d.rows - 1) / d.rows;
+    stage_begin("linear_dz", s);
+    linear_dz_kernel<<<dim3((a.N + 255) / 256, chunks), dim3(32, 8), 0, s>>>(d);
+    err = cudaGetLastError();
+    stage_end(s);
+    if (err == cudaSuccess && a.dbias) {
+      ColumnOutputs out{};
+      out.p[0] = a.dbias;
+      err = launch_column_sums(a.partials, chunks, a.N, a.N, out, a.N, s);
+    }
+  }
+  const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};
+  Params p{};
+  p.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
+  p.out_dtype = p.z_dtype = a.dtype;
+  p.alpha = 1.0f;
+  p.act = MOE_ACT_NONE;
+  p.C = a.K;
+  p.ld_y = a.K;
+  p.hdr = a.hdr;
+  p.reset_status = 1;
+  if (err == cudaSuccess && a.dx) {
+    p.R = a.M;
+    p.y = a.dx;
+    stage_begin("linear_dx", s);
+    err = product<true, false>({a.w, a.ld_w, a.K, a.N}, dz, a.N, p, s);
+    stage_end(s);
+    p.reset_status = 0;
+  }
+  if (err == cudaSuccess && a.dw) {
+    p.R = a.N;
+    p.y = a.dw;
+    stage_begin("linear_dw", s);
+    err = product<true, true>({a.x, a.ld_x, a.K, a.M}, dz, a.M, p, s);
+    stage_end(s);
+  }
+  return err;
+}
+
+}  // namespace moe
