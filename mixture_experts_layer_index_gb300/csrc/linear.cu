@@ -18,18 +18,12 @@
 // a range of the sum, and after a cluster barrier each adds its share of the rows
 // over all partials, read from the others' shared memory in rank order: no
 // workspace, no atomics, the same result every time.
-#include <cuda_fp16.h>
-
-#include <mutex>
-
-#include "common.cuh"
-#include "internal.h"
+#include "linear.cuh"
 
 namespace moe {
 namespace lin {
 
 constexpr int BM = 128;  // output columns per tile (TMEM lanes)
-constexpr int BK = 64;   // values of the sum per stage: 128 bytes
 constexpr int THREADS = 128;
 constexpr int MAX_SPLITS = 8;
 constexpr int A_BYTES = BM * BK * 2;
@@ -49,40 +43,11 @@ struct Params {
   int nacc;        // accumulators that a block's part of the sum is spread over
   uint32_t tmem_cols;
   int type;        // 0 = f16, 1 = bf16 operands
-  int act, bias_dtype, out_dtype, z_dtype;
-  float alpha;
-  long long ld_y, ld_z;
-  const void* bias;
-  const void* residual;
-  void* y;
-  void* z;
+  Epilogue ep;
   int reset_status;
   DeviceHeader* hdr;
 };
 
-// Descriptor of an MN-major operand in the layout of TMA boxes of 64 values along MN
-// (128 bytes, 128-byte swizzle) x 64 along the sum: 8-row groups along the sum 1024
-// bytes apart (stride byte offset), the next 64 along MN one box = 8192 bytes on
-// (leading byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(8192u >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 // fp32 at shared-memory address `addr` of block `rank` of the cluster
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   uint32_t remote;
@@ -90,38 +55,6 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
   return v;
-}
-
-// ------------------------------------------------------------------ activations
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return fmaxf(z, 0.0f);
-    case MOE_ACT_SILU: return z / (1.0f + expf(-z));
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MOE_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-    default: return z;
-  }
-}
-__device__ __forceinline__ float act_grad(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case MOE_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case MOE_ACT_GELU: return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
-    case MOE_ACT_GELU_TANH: {
-      const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
-    }
-    default: return 1.0f;
-  }
-}
-
-__device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i) {
-  if (dtype == MOE_DTYPE_F32) return static_cast<const float*>(p)[i];
-  if (dtype == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
 }
 
 // n values of one output column, rows r0.. of an array with ld elements between rows.
@@ -169,21 +102,21 @@ __device__ __forceinline__ void add_rows(float (&v)[CH], const void* in, int dty
 template <int CH>
 __device__ __forceinline__ void finish(const Params& p, float (&v)[CH], int r0, int n, int c) {
   if (c >= p.C || n <= 0) return;
-  if (p.bias) {
-    const float b = load_as_f32(p.bias, p.bias_dtype, c);
+  if (p.ep.bias) {
+    const float b = load_as_f32(p.ep.bias, p.ep.bias_dtype, c);
 #pragma unroll
     for (int i = 0; i < CH; ++i) v[i] += b;
   }
-  if (p.z) store_rows<CH>(p.z, p.z_dtype, static_cast<size_t>(r0) * p.ld_z + c, p.ld_z, n, v);
-  if (p.act != MOE_ACT_NONE) {
+  if (p.ep.z) store_rows<CH>(p.ep.z, p.ep.z_dtype, static_cast<size_t>(r0) * p.ep.ld_z + c, p.ep.ld_z, n, v);
+  if (p.ep.act != MOE_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) v[i] = act_value(v[i], p.act);
+    for (int i = 0; i < CH; ++i) v[i] = act_value(v[i], p.ep.act);
   }
 #pragma unroll
-  for (int i = 0; i < CH; ++i) v[i] *= p.alpha;
-  const size_t at = static_cast<size_t>(r0) * p.ld_y + c;
-  if (p.residual) add_rows<CH>(v, p.residual, p.out_dtype, at, p.ld_y, n);
-  store_rows<CH>(p.y, p.out_dtype, at, p.ld_y, n, v);
+  for (int i = 0; i < CH; ++i) v[i] *= p.ep.alpha;
+  const size_t at = static_cast<size_t>(r0) * p.ep.ld_y + c;
+  if (p.ep.residual) add_rows<CH>(v, p.ep.residual, p.ep.out_dtype, at, p.ep.ld_y, n);
+  store_rows<CH>(p.ep.y, p.ep.out_dtype, at, p.ep.ld_y, n, v);
 }
 
 template <int CH>
@@ -361,31 +294,11 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   }
 }
 
-// A 16-bit matrix of `outer` rows of `inner` values, ld values apart, in boxes.
-bool encode(CUtensorMap* map, const void* base, int type, uint64_t inner, uint64_t outer, long long ld,
-            uint32_t box_inner, uint32_t box_outer) {
-  EncodeTiledFn fn = get_encode_tiled();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {box_inner, box_outer};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, type ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Operand {
-  const void* base;
-  long long ld;
-  int inner, outer;  // inner: contiguous extent
-};
-
 template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch_tile(const Operand& a, const Operand& b, Params p, cudaStream_t s) {
+cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
   CUtensorMap ta, tb;
-  if (!encode(&ta, a.base, p.type, a.inner, a.outer, a.ld, 64, A_MN ? 64 : BM) ||
-      !encode(&tb, b.base, p.type, b.inner, b.outer, b.ld, 64, B_MN ? 64 : BN))
+  if (!encode(&ta, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, A_MN ? 64 : BM) ||
+      !encode(&tb, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, B_MN ? 64 : BN))
     return cudaErrorInvalidValue;
   static const cudaError_t attr = cudaFuncSetAttribute(
       linear_kernel<BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
@@ -409,10 +322,17 @@ cudaError_t launch_tile(const Operand& a, const Operand& b, Params p, cudaStream
   return cudaLaunchKernelEx(&cfg, linear_kernel<BN, A_MN, B_MN>, ta, tb, p);
 }
 
-// out[r][c] = sum_k A[c][k] B[r][k], tile and split chosen by the shape.
+// Tile and split by the shape.
 template <bool A_MN, bool B_MN>
-cudaError_t product(const Operand& a, const Operand& b, int K, Params p, cudaStream_t s) {
-  p.nk = (K + BK - 1) / BK;
+cudaError_t launch_shape(const Product& q, cudaStream_t s) {
+  Params p{};
+  p.C = q.C;
+  p.R = q.R;
+  p.type = q.type;
+  p.ep = q.ep;
+  p.reset_status = q.reset_status;
+  p.hdr = q.hdr;
+  p.nk = (q.K + BK - 1) / BK;
   int bn = p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
   if (B_MN && bn < 64) bn = 64;
   const long long nC = (p.C + BM - 1) / BM;
@@ -424,16 +344,22 @@ cudaError_t product(const Operand& a, const Operand& b, int K, Params p, cudaStr
   // fp32 output: the tensor core's running sum rounds at every step, so its length is
   // kept short by spreading the sum over up to four accumulators
   p.nacc = 1;
-  if (p.out_dtype == MOE_DTYPE_F32) p.nacc = bn <= 64 ? 4 : 2;
+  if (p.ep.out_dtype == MOE_DTYPE_F32) p.nacc = bn <= 64 ? 4 : 2;
   switch (bn) {
     case 16:
-      if constexpr (!B_MN) return launch_tile<16, A_MN, B_MN>(a, b, p, s);
+      if constexpr (!B_MN) return launch_tile<16, A_MN, B_MN>(q, p, s);
     case 32:
-      if constexpr (!B_MN) return launch_tile<32, A_MN, B_MN>(a, b, p, s);
-    case 64: return launch_tile<64, A_MN, B_MN>(a, b, p, s);
-    case 128: return launch_tile<128, A_MN, B_MN>(a, b, p, s);
-    default: return launch_tile<256, A_MN, B_MN>(a, b, p, s);
+      if constexpr (!B_MN) return launch_tile<32, A_MN, B_MN>(q, p, s);
+    case 64: return launch_tile<64, A_MN, B_MN>(q, p, s);
+    case 128: return launch_tile<128, A_MN, B_MN>(q, p, s);
+    default: return launch_tile<256, A_MN, B_MN>(q, p, s);
   }
+}
+
+cudaError_t launch_product(const Product& q, cudaStream_t s) {
+  if (pair_takes(q)) return launch_pair(q, s);
+  if (!q.cols_mn) return launch_shape<false, false>(q, s);
+  return q.rows_mn ? launch_shape<true, true>(q, s) : launch_shape<true, false>(q, s);
 }
 
 // ------------------------------------------------------------------ dz
@@ -534,25 +460,18 @@ inline long long dz_ld(int N) { return (N + 7) / 8 * 8; }
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   using namespace lin;
-  Params p{};
-  p.C = a.N;
-  p.R = a.M;
-  p.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
-  p.act = a.act;
-  p.bias_dtype = a.bias_dtype;
-  p.out_dtype = a.out_dtype;
-  p.z_dtype = a.dtype;
-  p.alpha = a.alpha;
-  p.ld_y = a.ld_y;
-  p.ld_z = a.N;
-  p.bias = a.bias;
-  p.residual = a.residual;
-  p.y = a.y;
-  p.z = a.z;
-  p.reset_status = 1;
-  p.hdr = a.hdr;
+  Product q{};
+  q.R = a.M;
+  q.C = a.N;
+  q.K = a.K;
+  q.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
+  q.rows = {a.x, a.ld_x, a.K, a.M};
+  q.cols = {a.w, a.ld_w, a.K, a.N};
+  q.ep = {a.act, a.bias_dtype, a.out_dtype, a.dtype, a.alpha, a.ld_y, a.N, a.bias, a.residual, a.y, a.z};
+  q.reset_status = 1;
+  q.hdr = a.hdr;
   stage_begin("linear", s);
-  const cudaError_t err = product<false, false>({a.w, a.ld_w, a.K, a.N}, {a.x, a.ld_x, a.K, a.M}, a.K, p, s);
+  const cudaError_t err = launch_product(q, s);
   stage_end(s);
   return err;
 }
@@ -602,28 +521,33 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     }
   }
   const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};
-  Params p{};
-  p.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
-  p.out_dtype = p.z_dtype = a.dtype;
-  p.alpha = 1.0f;
-  p.act = MOE_ACT_NONE;
-  p.C = a.K;
-  p.ld_y = a.K;
-  p.hdr = a.hdr;
-  p.reset_status = 1;
+  Product q{};
+  q.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
+  q.C = a.K;
+  q.cols_mn = true;
+  q.ep = {MOE_ACT_NONE, MOE_DTYPE_F32, a.dtype, a.dtype, 1.0f, a.K, 0, nullptr, nullptr, nullptr, nullptr};
+  q.reset_status = 1;
+  q.hdr = a.hdr;
+  q.rows = dz;
   if (err == cudaSuccess && a.dx) {
-    p.R = a.M;
-    p.y = a.dx;
+    q.R = a.M;
+    q.K = a.N;
+    q.cols = {a.w, a.ld_w, a.K, a.N};
+    q.rows_mn = false;
+    q.ep.y = a.dx;
     stage_begin("linear_dx", s);
-    err = product<true, false>({a.w, a.ld_w, a.K, a.N}, dz, a.N, p, s);
+    err = launch_product(q, s);
     stage_end(s);
-    p.reset_status = 0;
+    q.reset_status = 0;
   }
   if (err == cudaSuccess && a.dw) {
-    p.R = a.N;
-    p.y = a.dw;
+    q.R = a.N;
+    q.K = a.M;
+    q.cols = {a.x, a.ld_x, a.K, a.M};
+    q.rows_mn = true;
+    q.ep.y = a.dw;
     stage_begin("linear_dw", s);
-    err = product<true, true>({a.x, a.ld_x, a.K, a.M}, dz, a.M, p, s);
+    err = launch_product(q, s);
     stage_end(s);
   }
   return err;

@@ -1,0 +1,457 @@
+// The linear layer's products at sizes that fill the GPU: out[r][c] in tiles of
+// 256 x 256 by pairs of SMs (tcgen05.mma with cta_group::2, M = 256, N = 256).
+//
+// Each block of a pair (a cluster of two) loads 128 rows r and 128 columns c per
+// stage, 32 KB instead of the 48 KB of a 128 x 256 tile on one SM for the same
+// arithmetic, because the tensor cores of both read both halves of the column
+// operand.  A 128 x 256 tile on one SM asks 96 bytes per clock and SM of the L2 at the full
+// MMA rate; the pair asks 64.  The even block issues the MMAs for both; operand loads
+// of both count on its barriers, and its commits arrive on the barriers of both.
+//
+// Persistent pairs walk over the tiles.  Rows r lie on the TMEM lanes, 128 per
+// block, 2 x 256 accumulator columns, so that the epilogue of one tile
+// overlaps the MMAs of the next.  Warps: 0 loads, 1 issues MMAs (even block), 2
+// owns TMEM, 4-11 run the epilogue (two warps per 32 lanes, 128 columns each): 32
+// columns at a time are loaded from TMEM, finished in fp32, rounded once, staged in
+// shared memory as a 128-byte-swizzled box of 32 rows and stored by TMA, which
+// clips the edges.
+#include "linear.cuh"
+
+namespace moe {
+namespace lin {
+namespace {
+
+constexpr int TILE = 256;       // rows and columns of a pair's tile
+constexpr int HALF = 128;       // rows (and loaded columns) of one block
+constexpr int STAGES = 5;
+constexpr int OP_BYTES = HALF * BK * 2;
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (4 + EPI_WARPS);
+constexpr int BOX_BYTES = 32 * 128;            // 32 rows of 128 bytes
+constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
+// ring | two boxes per epilogue warp | barriers
+constexpr int BOX_OFFSET = STAGES * STAGE_BYTES;
+constexpr int BAR_OFFSET = BOX_OFFSET + EPI_WARPS * 2 * BOX_BYTES;
+constexpr size_t SMEM_BYTES = 1024 + BAR_OFFSET + 256;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one block");
+
+struct PairParams {
+  int R, C, nk;
+  int nR, nC;
+  int type;
+  Epilogue ep;
+  int reset_status;
+  DeviceHeader* hdr;
+};
+
+// ------------------------------------------------------------------ two-SM forms
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// A load into this block's shared memory that counts on a barrier of the pair's even block.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both blocks once the MMAs issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_group_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+
+// Tile t's first row and column: groups of 8 row tiles, column by column within a
+// group, so that the pairs in flight share both operands in L2.
+__device__ __forceinline__ void tile_origin(const PairParams& p, int t, int& r0, int& c0) {
+  constexpr int GR = 8;
+  const int group = t / (GR * p.nC), in_group = t - group * (GR * p.nC);
+  const int rows_here = min(GR, p.nR - group * GR);
+  c0 = in_group / rows_here * TILE;
+  r0 = (group * GR + in_group % rows_here) * TILE;
+}
+
+// 32 values (columns c.. of one row) as one row of a swizzled box: 16-byte chunk j of
+// row `lane` sits at chunk j ^ (lane & 7).  16-bit types fill half a box row.
+__device__ __forceinline__ void put_box(uint8_t* box, int lane, int half, int dtype, const float (&v)[32]) {
+  uint8_t* row = box + lane * 128;
+  if (dtype == MOE_DTYPE_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4)) =
+          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (dtype == MOE_DTYPE_BF16) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+          const __half2 b = __floats2half2_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+      *reinterpret_cast<uint4*>(row + (((half * 4 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// v[i] = p[at + i], 32 values of which `n` exist; `wide`: p + at is 16-byte aligned.
+__device__ __forceinline__ void load32(float (&v)[32], const void* p, int dtype, size_t at, int n, bool wide) {
+  if (n < 32 || !wide) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = i < n ? load_as_f32(p, dtype, at + i) : 0.0f;
+  } else if (dtype == MOE_DTYPE_F32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 f = q[j];
+      v[4 * j] = f.x; v[4 * j + 1] = f.y; v[4 * j + 2] = f.z; v[4 * j + 3] = f.w;
+    }
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 raw = q[j];
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = dtype == MOE_DTYPE_BF16
+                             ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
+                             : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[8 * j + 2 * i] = f.x;
+        v[8 * j + 2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
+template <bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
+                       const PairParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFFSET);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
+  const uint32_t tfull0 = smem_u32(bars + 2 * STAGES), tempty0 = smem_u32(bars + 2 * STAGES + 2);
+  const uint32_t mma_done = smem_u32(bars + 2 * STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 2 * EPI_WARPS);  // the epilogue warps of both blocks
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+    // a wait that records a timeout lasts seconds: nothing of this launch is lost here
+    if (p.reset_status && blockIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(2 * TILE)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the other block's barriers are set up
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int total = p.nR * p.nC;
+  const int npairs = static_cast<int>(gridDim.x) >> 1, pair = static_cast<int>(blockIdx.x) >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t lead_full0 = map_rank(full0, 0);
+      uint32_t stage = 0, phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        int r0, c0;
+        tile_origin(p, t, r0, c0);
+        r0 += rank * HALF;
+        c0 += rank * HALF;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.hdr, 0x610000u)) {
+            ok = false;
+            break;
+          }
+          // the even block's barrier expects the bytes of both blocks
+          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
+          const uint32_t bar = lead_full0 + 8 * stage;
+          const uint32_t a = smem_u32(smem + stage * STAGE_BYTES), b = a + OP_BYTES;
+          const int k = kb * BK;
+          if (A_MN) {
+            tma_load_2d_pair(a, &tmA, r0, k, bar);
+            tma_load_2d_pair(a + OP_BYTES / 2, &tmA, r0 + 64, k, bar);
+          } else {
+            tma_load_2d_pair(a, &tmA, k, r0, bar);
+          }
+          if (B_MN) {
+            tma_load_2d_pair(b, &tmB, c0, k, bar);
+            tma_load_2d_pair(b + OP_BYTES / 2, &tmB, c0 + 64, k, bar);
+          } else {
+            tma_load_2d_pair(b, &tmB, k, c0, bar);
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok && rank == 0) {  // let the copies already issued land before shared memory is given up
+        for (int i = 0; i < min(issued, STAGES); ++i) {
+          stage = (stage + STAGES - 1) % STAGES;
+          if (stage == STAGES - 1) phase ^= 1;
+          mbar_wait_quiet(full0 + 8 * stage, phase, 50000000ull);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc =
+          make_idesc(p.type, p.type, TILE, TILE) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += npairs) {
+        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.hdr, 0x620000u)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * TILE;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x630000u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + stage * STAGE_BYTES), b = a + OP_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t da = A_MN ? sw128_mnmajor_desc(a + kk * 2048) : sw128_kmajor_desc(a + kk * 32);
+            const uint64_t db = B_MN ? sw128_mnmajor_desc(b + kk * 2048) : sw128_kmajor_desc(b + kk * 32);
+            mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
+          }
+          mma_commit_pair(empty0 + 8 * stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(tfull0 + 8 * acc);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      mma_commit_pair(mma_done);
+      mbar_wait_quiet(mma_done, 0, 1000000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int e = warp - 4, q = warp & 3, h = e >> 2;
+    uint8_t* box0 = smem + BOX_OFFSET + e * 2 * BOX_BYTES;
+    const uint32_t lead_tempty0 = map_rank(tempty0, 0);
+    const Epilogue& ep = p.ep;
+    const bool wide = ep.out_dtype == MOE_DTYPE_F32;
+    const bool bias_wide = reinterpret_cast<uintptr_t>(ep.bias) % 16 == 0;
+    const bool residual_wide = reinterpret_cast<uintptr_t>(ep.residual) % 16 == 0;
+    uint32_t acc = 0, acc_phase = 0;
+    for (int t = pair; t < total; t += npairs) {
+      int r0, c0;
+      tile_origin(p, t, r0, c0);
+      r0 += rank * HALF + q * 32;  // this warp's rows and columns
+      c0 += h * HALF;
+      int good = 1;
+      if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x640000u);
+      good = __shfl_sync(0xffffffffu, good, 0);
+      if (!good) break;
+      tc_fence_after();
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * HALF;
+      const bool row_in = r0 + lane < p.R;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * 32;
+        float v[32], b[32];
+        tmem_ld32(tb + j * 32, v);
+        if (ep.bias) load32(b, ep.bias, ep.bias_dtype, c, p.C - c, bias_wide);  // the same for every lane
+        tmem_ld_wait_regs(v);
+        if (j == 3) {  // this warp's accumulator columns are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+        }
+        if (ep.bias) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += b[i];
+        }
+        const int half = j & 1;
+        // boxes: y in the first, z (or the next fp32 y) in the second; a box is written
+        // only after the store that last read it has done so
+        uint8_t* ybox = box0 + (wide && !ep.z ? half * BOX_BYTES : 0);
+        if (wide || half == 0) {
+          if (lane == 0) {
+            if (wide && !ep.z) bulk_wait_group_read1();
+            else bulk_wait_group_read0();
+          }
+          __syncwarp();
+        }
+        if (ep.z) put_box(box0 + BOX_BYTES, lane, half, ep.z_dtype, v);
+        switch (ep.act) {
+          case MOE_ACT_NONE: break;
+          case MOE_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
+            break;
+          case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_SILU);
+            break;
+          case MOE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
+            break;
+          default:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_GELU_TANH);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= ep.alpha;
+        if (ep.residual && row_in) {  // its rows are aligned as y's, which TMA stores
+          load32(b, ep.residual, ep.out_dtype, static_cast<size_t>(r0 + lane) * ep.ld_y + c, p.C - c, residual_wide);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += b[i];
+        }
+        put_box(ybox, lane, wide ? 0 : half, ep.out_dtype, v);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0 && r0 < p.R) {
+          if (wide) {
+            if (c < p.C) tma_store_2d(&tmY, smem_u32(ybox), c, r0);
+          } else if (half && c - 32 < p.C) {
+            tma_store_2d(&tmY, smem_u32(ybox), c - 32, r0);
+          }
+          if (ep.z && half && c - 32 < p.C) tma_store_2d(&tmZ, smem_u32(box0 + BOX_BYTES), c - 32, r0);
+        }
+        if (lane == 0 && (wide || half)) bulk_commit_group();
+        __syncwarp();
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+    if (lane == 0) {
+      bulk_wait_group0();
+      // the last commit arrives in both blocks: the odd one stays until it has
+      if (rank == 1 && warp == 4) mbar_wait_quiet(mma_done, 0, 1000000000ull);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither block's barriers or tensor memory are in use any more
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * TILE) : "memory");
+  }
+}
+
+// A store map: boxes of 32 rows of 128 bytes.
+bool encode_store(CUtensorMap* map, void* base, int dtype, int cols, int rows, long long ld) {
+  EncodeTiledFn fn = get_encode_tiled();
+  if (!fn) return false;
+  const uint32_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  const cuuint32_t box[2] = {128 / es, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType type = dtype == MOE_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool storable(const void* base, int dtype, long long ld) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t launch_pair_of(const Product& q, cudaStream_t s) {
+  const int sms = num_sms();
+  if (sms < 2) return cudaErrorNoDevice;
+  CUtensorMap ta, tb, ty, tz;
+  if (!encode(&ta, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, A_MN ? 64 : HALF) ||
+      !encode(&tb, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, B_MN ? 64 : HALF) ||
+      !encode_store(&ty, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y))
+    return cudaErrorInvalidValue;
+  tz = ty;
+  if (q.ep.z && !encode_store(&tz, q.ep.z, q.ep.z_dtype, q.C, q.R, q.ep.ld_z)) return cudaErrorInvalidValue;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      linear_pair_kernel<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+  if (attr != cudaSuccess) return attr;
+  PairParams p{};
+  p.R = q.R;
+  p.C = q.C;
+  p.nk = (q.K + BK - 1) / BK;
+  p.nR = (q.R + TILE - 1) / TILE;
+  p.nC = (q.C + TILE - 1) / TILE;
+  p.type = q.type;
+  p.ep = q.ep;
+  p.reset_status = q.reset_status;
+  p.hdr = q.hdr;
+  const long long tiles = static_cast<long long>(p.nR) * p.nC;
+  const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+  linear_pair_kernel<A_MN, B_MN><<<2 * pairs, THREADS, SMEM_BYTES, s>>>(ta, tb, ty, tz, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool pair_takes(const Product& q) {
+  if (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) || (q.ep.z && !storable(q.ep.z, q.ep.z_dtype, q.ep.ld_z)))
+    return false;
+  const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + TILE - 1) / TILE);
+  return q.R > HALF && q.C > HALF && tiles >= 38;
+}
+
+cudaError_t launch_pair(const Product& q, cudaStream_t s) {
+  if (!q.cols_mn) return launch_pair_of<false, false>(q, s);
+  return q.rows_mn ? launch_pair_of<true, true>(q, s) : launch_pair_of<false, true>(q, s);
+}
+
+}  // namespace lin
+}  // namespace moe

@@ -384,6 +384,14 @@ def test_linear_many_tiles(m, M, N, K):
     _linear_case(m, M, N, K, "silu", bias="f32", residual=True, keep_z=True)
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "bf16")])
+def test_linear_large_tiles(m, act, dtype, out):
+    # over 38 tiles of 256 x 256, ragged in every direction
+    _linear_case(m, 1500, 2056, 200, act, dtype, out, "f32", residual=True, keep_z=act != "none", alpha=0.5,
+                 in_place=True)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 64, 4096), (8, 4096, 4096), (40, 128, 7168), (3000, 64, 2048)])
 def test_linear_long_sums(m, M, N, K):
     _linear_case(m, M, N, K, out="f32", bias="f32")
