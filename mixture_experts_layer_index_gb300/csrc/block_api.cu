@@ -66,6 +66,8 @@ NormArgs norm_args(const moe_norm_problem& p) {
   NormArgs a{};
   a.T = p.T;
   a.H = p.H;
+  a.h_dtype = p.h_dtype;
+  a.o_dtype = p.o_dtype;
   a.post = p.post_norm;
   a.pre = p.pre_norm;
   a.gate_kind = p.gate;
@@ -182,9 +184,9 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const void* h, const void
   a.b_pre = b_pre;
   a.h_out = h_out;
   a.x_out = x_out;
-  const bool vec = norm_vec(a, h, o, p->gate == MOE_GATE_TOKEN ? nullptr : gate, w_post, b_post, w_pre, b_pre,
+  a.vec = norm_vec(a, h, o, p->gate == MOE_GATE_TOKEN ? nullptr : gate, w_post, b_post, w_pre, b_pre,
                             static_cast<const void*>(h_out), static_cast<const void*>(x_out));
-  return from_cuda(launch_norm_forward(a, p->h_dtype, p->o_dtype, vec, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_norm_forward(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_norm_backward_workspace_size(const moe_norm_problem* p) {
@@ -237,10 +239,10 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const void* dh_out, cons
   a.d_o = d_o;
   a.dgate = dgate;
   a.partials = static_cast<float*>(ws);
-  const bool vec = norm_vec(a, dh_out, dx_out, h_out, o, p->gate == MOE_GATE_TOKEN ? nullptr : gate, w_post, b_post,
+  a.vec = norm_vec(a, dh_out, dx_out, h_out, o, p->gate == MOE_GATE_TOKEN ? nullptr : gate, w_post, b_post,
                             w_pre, static_cast<const void*>(dh), static_cast<const void*>(d_o),
                             p->gate == MOE_GATE_FULL ? static_cast<const void*>(dgate) : nullptr);
-  return from_cuda(launch_norm_backward(a, p->h_dtype, p->o_dtype, vec, sums, s));
+  return from_cuda(launch_norm_backward(a, sums, s));
 }
 
 size_t moe_linear_workspace_size(const moe_linear_problem* p) { return check_linear(p) == MOE_OK ? kHeaderBytes : 0; }

@@ -141,6 +141,10 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
 // kernels trigger no early launch: a persistent GEMM's CTAs resident during the
 // previous kernel's tail cost more than the earlier start gains.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Let a dependent kernel be launched while this one still runs (once every block has
+// said so or ended).  The operators around the FFN say so as they start: their
+// successor's set-up then overlaps their run, its dep_wait still waits for their end.
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Tiled TMA store of the box at {c0, c1} of `map` from shared memory at src
 // (a bulk async-group of the issuing thread; src aligned as the map's swizzle needs).

@@ -217,9 +217,13 @@ cudaError_t launch_route_ex(const void* scores, int dtype, const RouteArgs& a, c
 cudaError_t launch_route_backward(const void* scores, int dtype, const RouteArgs& a, const int32_t* ids,
                                   const float* dw, void* dscores, long long ld_d, cudaStream_t s);
 
-// Block norms (norm.cu).  `vec`: every row and vector can be read 16 bytes at a time.
+// Block norms (norm_forward.cu, norm_backward.cu).
 struct NormArgs {
   int T, H;
+  int h_dtype, o_dtype;
+  bool vec;   // every row and vector can be read 16 bytes at a time
+  int depth;  // rows in a block's ring
+  int blocks; // backward: blocks launched, one set of partial sums each
   int post, pre, gate_kind;  // moe_norm_kind, moe_gate_kind
   int w_dtype;
   float eps, alpha, beta;
@@ -236,16 +240,15 @@ struct NormArgs {
   int acc_dw_post, acc_db_post, acc_dw_pre, acc_db_pre, acc_dgate;  // index among the sums, -1: not wanted
 };
 size_t norm_partials_bytes(int T, int H);
-cudaError_t launch_norm_forward(const NormArgs& a, int h_dtype, int o_dtype, bool vec, cudaStream_t s);
+cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
 // sums: dw_post, db_post, dw_pre, db_pre, dgate (per channel), each fp32 [H] or null.
-cudaError_t launch_norm_backward(const NormArgs& a, int h_dtype, int o_dtype, bool vec, float* const (&sums)[5],
-                                 cudaStream_t s);
-// out.p[c / width][c % width] = sum over p of partials[p * stride + c], c < n, in a fixed order.
+cudaError_t launch_norm_backward(const NormArgs& a, float* const (&sums)[5], cudaStream_t s);
+// out.p[j][c] = sum over i of partials[i * stride + j * pitch + c], c < width, in a fixed order.
 struct ColumnOutputs {
   float* p[5];
 };
-cudaError_t launch_column_sums(const float* partials, int nparts, size_t stride, int n, const ColumnOutputs& out,
-                               int width, cudaStream_t s);
+cudaError_t launch_column_sums(const float* partials, int nparts, size_t stride, int nsums, int width, size_t pitch,
+                               const ColumnOutputs& out, cudaStream_t s);
 
 // Linear layer with a fused epilogue (linear.cu).
 struct LinearArgs {

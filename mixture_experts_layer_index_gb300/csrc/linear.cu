@@ -152,8 +152,6 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
     fence_mbar_init();
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
-    // a wait that records a timeout lasts seconds: nothing of this launch is lost here
-    if (p.reset_status && blockIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
@@ -163,6 +161,10 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dep_wait();
+  dep_launch();
+  // a wait that records a timeout lasts seconds: nothing of this launch is lost here
+  if (p.reset_status && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
 
   // tiles: 16 row tiles side by side, then the next column tile, so that the blocks in
   // flight share both operands in L2
@@ -308,7 +310,9 @@ cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
   int cols = 32;
   while (cols < BN * p.nacc) cols *= 2;
   p.tmem_cols = cols;
-  cudaLaunchAttribute la[1];
+  cudaLaunchAttribute la[2];
+  la[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[1].val.programmaticStreamSerializationAllowed = 1;
   la[0].id = cudaLaunchAttributeClusterDimension;
   la[0].val.clusterDim.x = p.splits;
   la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
@@ -318,7 +322,7 @@ cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
   cfg.dynamicSmemBytes = smem_bytes(BN);
   cfg.stream = s;
   cfg.attrs = la;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, linear_kernel<BN, A_MN, B_MN>, ta, tb, p);
 }
 
@@ -404,6 +408,8 @@ __device__ __forceinline__ void load8(float (&v)[8], const void* p, int dtype, s
 
 __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][256 + 8];
+  dep_wait();
+  dep_launch();
   const int c = blockIdx.x * 256 + threadIdx.x * 8;
   const int n = min(8, a.N - c);
   const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
@@ -511,13 +517,12 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
             reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
     const int chunks = (a.M + d.rows - 1) / d.rows;
     stage_begin("linear_dz", s);
-    linear_dz_kernel<<<dim3((a.N + 255) / 256, chunks), dim3(32, 8), 0, s>>>(d);
-    err = cudaGetLastError();
+    err = launch_dependent(linear_dz_kernel, dim3((a.N + 255) / 256, chunks), dim3(32, 8), 0, s, d);
     stage_end(s);
     if (err == cudaSuccess && a.dbias) {
       ColumnOutputs out{};
       out.p[0] = a.dbias;
-      err = launch_column_sums(a.partials, chunks, a.N, a.N, out, a.N, s);
+      err = launch_column_sums(a.partials, chunks, a.N, 1, a.N, 0, out, s);
     }
   }
   const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};

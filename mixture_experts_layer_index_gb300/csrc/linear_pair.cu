@@ -178,8 +178,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     fence_mbar_init();
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
-    // a wait that records a timeout lasts seconds: nothing of this launch is lost here
-    if (p.reset_status && blockIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -192,6 +190,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // the other block's barriers are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dep_wait();
+  dep_launch();
+  // a wait that records a timeout lasts seconds: nothing of this launch is lost here
+  if (p.reset_status && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
 
   const int total = p.nR * p.nC;
   const int npairs = static_cast<int>(gridDim.x) >> 1, pair = static_cast<int>(blockIdx.x) >> 1;
@@ -435,8 +437,7 @@ cudaError_t launch_pair_of(const Product& q, cudaStream_t s) {
   p.hdr = q.hdr;
   const long long tiles = static_cast<long long>(p.nR) * p.nC;
   const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-  linear_pair_kernel<A_MN, B_MN><<<2 * pairs, THREADS, SMEM_BYTES, s>>>(ta, tb, ty, tz, p);
-  return cudaGetLastError();
+  return launch_dependent(linear_pair_kernel<A_MN, B_MN>, dim3(2 * pairs), dim3(THREADS), SMEM_BYTES, s, ta, tb, ty, tz, p);
 }
 
 }  // namespace

@@ -1,0 +1,255 @@
+// Parts shared by the block norms' forward (norm_forward.cu) and gradient
+// (norm_backward.cu) kernels: how rows come in and go out, and block-wide sums.
+//
+// A block takes whole rows, a thread eight columns of a row (or two runs of
+// eight), and blocks walk over rows.  Where rows can be read asynchronously
+// (cp.async), each block keeps a ring of rows in shared memory: a thread copies
+// exactly the columns it will read itself, so the ring needs no barrier and the
+// rows in flight cost no registers.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace norms {
+
+constexpr int EPT = 8;  // columns per thread and run
+
+// How a thread's columns of a row lie and come in.
+//   VEC16: columns [run*8*NT + tid*8, + 8), 16-byte copies into the ring (widths,
+//          strides and addresses that are multiples of 16 bytes)
+//   WORD4: columns run*8*NT + i*NT + tid, 4-byte copies into the ring (fp32 rows)
+//   PLAIN: like WORD4, or like VEC16 where the row allows it (`vec`), loaded when
+//          they are used, any type: 16-bit rows at odd addresses, and rows too long for a ring
+enum Access { VEC16, WORD4, PLAIN };
+
+template <Access A>
+__device__ __forceinline__ int col_of(int run, int i, bool vec) {
+  const bool together = A == VEC16 || (A == PLAIN && vec);
+  return together ? (run * blockDim.x + threadIdx.x) * EPT + i : (run * EPT + i) * blockDim.x + threadIdx.x;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most `depth - 1` of the newest rows are still on their way.
+__device__ __forceinline__ void cp_async_wait(int depth) {
+  if (depth >= 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
+
+// Eight values from 16-byte aligned memory (16 or 32 bytes).
+__device__ __forceinline__ void unpack(float (&v)[EPT], const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void unpack(float (&v)[EPT], const __nv_bfloat16* p) {
+  const uint4 raw = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack(float (&v)[EPT], const __half* p) {
+  const uint4 raw = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void pack(float* p, const float (&v)[EPT]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void pack(__nv_bfloat16* p, const float (&v)[EPT]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack(__half* p, const float (&v)[EPT]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float load_one(const void* p, int dtype, size_t i) {
+  if (dtype == MOE_DTYPE_F32) return static_cast<const float*>(p)[i];
+  if (dtype == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+__device__ __forceinline__ void store_one(void* p, int dtype, size_t i, float v) {
+  if (dtype == MOE_DTYPE_F32) static_cast<float*>(p)[i] = v;
+  else if (dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+__device__ __forceinline__ void unpack_any(float (&v)[EPT], const void* p, int dtype, size_t at) {
+  if (dtype == MOE_DTYPE_F32) unpack(v, static_cast<const float*>(p) + at);
+  else if (dtype == MOE_DTYPE_BF16) unpack(v, static_cast<const __nv_bfloat16*>(p) + at);
+  else unpack(v, static_cast<const __half*>(p) + at);
+}
+__device__ __forceinline__ void pack_any(void* p, int dtype, size_t at, const float (&v)[EPT]) {
+  if (dtype == MOE_DTYPE_F32) pack(static_cast<float*>(p) + at, v);
+  else if (dtype == MOE_DTYPE_BF16) pack(static_cast<__nv_bfloat16*>(p) + at, v);
+  else pack(static_cast<__half*>(p) + at, v);
+}
+
+// A thread's columns of the row at element `at` of p; 0 past column H.
+template <Access A>
+__device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, int dtype, size_t at, int run, int H, bool vec) {
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    const int c = col_of<A>(run, 0, vec);
+    if (c < H) unpack_any(v, p, dtype, at + c);
+    else
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(run, i, vec);
+      v[i] = c < H ? load_one(p, dtype, at + c) : 0.0f;
+    }
+  }
+}
+template <Access A>
+__device__ __forceinline__ void store_row(void* p, int dtype, size_t at, int run, int H, bool vec,
+                                          const float (&v)[EPT]) {
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    const int c = col_of<A>(run, 0, vec);
+    if (c < H) pack_any(p, dtype, at + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(run, i, vec);
+      if (c < H) store_one(p, dtype, at + c, v[i]);
+    }
+  }
+}
+
+// A thread's columns of a per-column vector (16-byte aligned where the rows are read
+// 16 bytes at a time); `none` where there is no vector.
+template <Access A>
+__device__ __forceinline__ void load_columns(float (&v)[EPT], const void* p, int dtype, int run, int H, bool vec,
+                                             float none) {
+  if (p != nullptr) {
+    load_row<A>(v, p, dtype, 0, run, H, vec);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) v[i] = none;
+  }
+}
+
+// The ring: slots of one row each of up to four arrays.
+template <typename T, Access A>
+__device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H) {
+  const T* row = static_cast<const T*>(p) + at;
+  if (A == VEC16) {
+    const int c = col_of<A>(0, 0, true);
+    if (c < H)
+#pragma unroll
+      for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q) cp_async16(slot + c + q * (16 / sizeof(T)), row + c + q * (16 / sizeof(T)));
+  } else if (A == WORD4) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(0, i, false);
+      if (c < H) cp_async4(slot + c, row + c);
+    }
+  }
+}
+template <typename T, Access A>
+__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int H) {
+  if (A == VEC16) {
+    const int c = col_of<A>(0, 0, true);
+    if (c < H) unpack(v, slot + c);
+    else
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(0, i, false);
+      v[i] = c < H ? as_f32(slot[c]) : 0.0f;
+    }
+  }
+}
+
+// Sums of N (1 or 4) values over the block, for every thread, in a fixed order: a
+// butterfly in each warp (for four values one in which lanes trade values, so that it
+// takes 6 shuffles instead of 20), then every thread adds the warps' sums from shared
+// memory.  Two buffers taken in turn: a warp can be at most one sum ahead of the
+// others' reads.  buf: zeroed before the first use.
+template <int N>
+struct BlockSum {
+  float (*buf)[N][32];
+  int turn;
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if constexpr (N == 4) {
+      const bool hi = lane & 16, mid = lane & 8;
+      float a0 = hi ? v[2] : v[0], a1 = hi ? v[3] : v[1];
+      a0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+      a1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+      float b = mid ? a1 : a0;
+      b += __shfl_xor_sync(0xffffffffu, mid ? a0 : a1, 8);
+      b += __shfl_xor_sync(0xffffffffu, b, 4);
+      b += __shfl_xor_sync(0xffffffffu, b, 2);
+      b += __shfl_xor_sync(0xffffffffu, b, 1);
+      if ((lane & 7) == 0) buf[turn][lane >> 3][warp] = b;
+    } else {
+      float b = v[0];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+      if (lane == 0) buf[turn][0][warp] = b;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float s = 0.0f;
+      for (int w = 0; w < nw; w += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&buf[turn][j][w]);
+        s += (f.x + f.y) + (f.z + f.w);
+      }
+      v[j] = s;
+    }
+    turn ^= 1;
+  }
+};
+
+// 1 / sqrt of the second moment, whose sum over H columns is given, plus eps.
+__device__ __forceinline__ float inv_std(float sum, float inv_h, float eps) { return 1.0f / sqrtf(sum * inv_h + eps); }
+
+// Threads of a block for rows of H columns: one run of eight columns each up to
+// 8192 columns, two beyond.
+inline int norm_threads(int H) {
+  const int t = (H + EPT - 1) / EPT;
+  return t >= 1024 ? 1024 : (t + 31) / 32 * 32;
+}
+
+}  // namespace norms
+}  // namespace moe

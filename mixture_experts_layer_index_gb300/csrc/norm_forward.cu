@@ -1,0 +1,176 @@
+// The boundary between two blocks (moe_norm_forward):
+//   h' = beta h + alpha g * N_post(o),   x' = N_pre(h')
+// with N(v) = (v - mu) r w + b, r = 1 / sqrt(mean((v - mu)^2) + eps); mu = 0 for RMS norms.
+//
+// Bound by memory: h and o are read once, h' and x' written once.  A row stays in
+// registers between its two norms, the mean and the second moment about it are
+// two sums over registers.  All sums are in fp32, at most 16 values per thread,
+// then a tree over the block in a fixed order.
+#include "norm.cuh"
+
+namespace moe {
+namespace norms {
+namespace {
+
+template <typename HT, typename OT, Access A, int RUNS, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_forward_kernel(NormArgs a) {
+  __shared__ __align__(16) float s_sum[2][1][32];
+  extern __shared__ __align__(16) uint8_t s_ring[];
+  static_assert(A == PLAIN || RUNS == 1, "a ring holds one run per thread");
+  const int H = a.H;
+  const bool vec = A == VEC16 || (A == PLAIN && a.vec);
+  const float inv_h = 1.0f / static_cast<float>(H);
+  const size_t pitch = static_cast<size_t>((H + EPT - 1) / EPT * EPT);
+  HT* ring_h = reinterpret_cast<HT*>(s_ring);
+  OT* ring_o = reinterpret_cast<OT*>(s_ring + a.depth * pitch * sizeof(HT));
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+  __syncthreads();
+  BlockSum<1> block_sum{s_sum, 0};
+  dep_wait();
+  dep_launch();
+
+  auto fetch = [&](int t, int slot) {
+    if (t < a.T) {
+      copy_in<OT, A>(ring_o + slot * pitch, a.o, static_cast<size_t>(t) * a.ld_o, H);
+      copy_in<HT, A>(ring_h + slot * pitch, a.h, static_cast<size_t>(t) * a.ld_h, H);
+    }
+    cp_async_commit();
+  };
+  int slot = 0;
+  if (A != PLAIN)
+    for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
+
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
+    float v[RUNS][EPT];
+    if constexpr (A != PLAIN) {
+      const int ahead = slot + a.depth - 1;
+      fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
+      cp_async_wait(a.depth);
+      copy_out<OT, A>(v[0], ring_o + slot * pitch, H);
+    } else {
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r) load_row<A>(v[r], a.o, a.o_dtype, at_o, r, H, vec);
+    }
+
+    // v = N(v): moments over the block, then the affine part
+    auto normalise = [&](int kind, const void* w, const void* b) {
+      if (kind == MOE_NORM_LAYER) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) s[0] += v[r][i];
+        block_sum(s);
+        const float mu = s[0] * inv_h;
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) v[r][i] = col_of<A>(r, i, vec) < H ? v[r][i] - mu : 0.0f;
+      }
+      float q[1] = {0.0f};
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) q[0] = fmaf(v[r][i], v[r][i], q[0]);
+      block_sum(q);
+      const float rs = inv_std(q[0], inv_h, a.eps);
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r) {
+        float c[EPT];
+        load_columns<A>(c, w, a.w_dtype, r, H, vec, 1.0f);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) v[r][i] *= rs * c[i];
+        if (b) {
+          load_columns<A>(c, b, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) v[r][i] += c[i];
+        }
+      }
+    };
+
+    if (a.post != MOE_NORM_NONE) normalise(a.post, a.w_post, a.b_post);
+    const float scale =
+        a.gate_kind == MOE_GATE_TOKEN ? a.alpha * __ldg(static_cast<const float*>(a.gate) + t) : a.alpha;
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      float c[EPT];
+      if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
+        if (a.gate_kind == MOE_GATE_CHANNEL) load_columns<A>(c, a.gate, a.w_dtype, r, H, vec, 0.0f);
+        else load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) v[r][i] *= c[i];
+      }
+      if constexpr (A != PLAIN) copy_out<HT, A>(c, ring_h + slot * pitch, H);
+      else load_row<A>(c, a.h, a.h_dtype, at_h, r, H, vec);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i)
+        v[r][i] = col_of<A>(r, i, vec) < H ? fmaf(scale, v[r][i], a.beta * c[i]) : 0.0f;
+      store_row<A>(a.h_out, a.h_dtype, at_h, r, H, vec, v[r]);
+    }
+    // x' is taken from h' before its rounding: one rounding each
+    if (a.pre != MOE_NORM_NONE) {
+      normalise(a.pre, a.w_pre, a.b_pre);
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r) store_row<A>(a.x_out, a.o_dtype, at_o, r, H, vec, v[r]);
+    }
+    if (++slot >= a.depth) slot = 0;
+  }
+}
+
+template <typename HT, typename OT, Access A, int RUNS, int MAXT>
+cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
+  size_t smem = 0;
+  if (A != PLAIN) {
+    const size_t row = static_cast<size_t>((a.H + EPT - 1) / EPT * EPT) * (sizeof(HT) + sizeof(OT));
+    a.depth = 3;
+    smem = a.depth * row;  // at most 3 rows of 8192 fp32 pairs: 192 KB
+    static const cudaError_t attr = cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, RUNS, MAXT>,
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * 8192 * 8);
+    if (attr != cudaSuccess) return attr;
+  }
+  const int cap = 152 * (1024 / threads > 32 ? 32 : 1024 / threads);
+  return launch_dependent(norm_forward_kernel<HT, OT, A, RUNS, MAXT>, dim3(a.T < cap ? a.T : cap), dim3(threads), smem,
+                          s, a);
+}
+
+template <typename HT, typename OT, Access A>
+cudaError_t forward_ring(const NormArgs& a, int threads, cudaStream_t s) {
+  if (threads <= 256) return forward_of<HT, OT, A, 1, 256>(a, threads, s);
+  if (threads <= 512) return forward_of<HT, OT, A, 1, 512>(a, threads, s);
+  return forward_of<HT, OT, A, 1, 1024>(a, threads, s);
+}
+
+}  // namespace
+}  // namespace norms
+
+cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
+  using namespace norms;
+  const int threads = norm_threads(a.H);
+  const int pair = a.h_dtype * 3 + a.o_dtype;
+  stage_begin("norm_forward", s);
+  cudaError_t err;
+  if (a.H > threads * EPT) {
+    err = forward_of<float, float, PLAIN, 2, 1024>(a, threads, s);
+  } else if (a.vec) {
+    switch (pair) {
+      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32: err = forward_ring<float, float, VEC16>(a, threads, s); break;
+      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_BF16: err = forward_ring<float, __nv_bfloat16, VEC16>(a, threads, s); break;
+      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F16: err = forward_ring<float, __half, VEC16>(a, threads, s); break;
+      case MOE_DTYPE_BF16 * 3 + MOE_DTYPE_BF16:
+        err = forward_ring<__nv_bfloat16, __nv_bfloat16, VEC16>(a, threads, s);
+        break;
+      default: err = forward_ring<__half, __half, VEC16>(a, threads, s);
+    }
+  } else if (pair == MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32) {
+    err = forward_ring<float, float, WORD4>(a, threads, s);
+  } else if (threads <= 512) {
+    err = forward_of<float, float, PLAIN, 1, 512>(a, threads, s);
+  } else {
+    err = forward_of<float, float, PLAIN, 1, 1024>(a, threads, s);
+  }
+  stage_end(s);
+  return err;
+}
+
+}  // namespace moe

@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_ex_kernel(const ST* _
   extern __shared__ float s_rows[];  // group limits only: one row of E ranking values per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouterWarps + warp;
+  dep_wait();
+  dep_launch();
   if (t >= a.T) return;  // no block-wide barrier below
   const ST* row = scores + static_cast<size_t>(t) * a.ld;
   const int E = a.E, k = a.k;
@@ -223,6 +225,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
   extern __shared__ float s_rows[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouterWarps + warp;
+  dep_wait();
+  dep_launch();
   if (t >= a.T) return;
   const int E = a.E, k = a.k;
   const ST* row = scores + static_cast<size_t>(t) * a.ld;
@@ -307,43 +311,40 @@ inline int slots_of(int E) {
 
 template <typename ST>
 cudaError_t route_ex_of(const void* scores, const RouteArgs& a, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.T + kRouterWarps - 1) / kRouterWarps);
+  const dim3 grid((a.T + kRouterWarps - 1) / kRouterWarps);
   const size_t smem = a.n_group > 1 ? static_cast<size_t>(kRouterWarps) * a.E * sizeof(float) : 0;
   const ST* sc = static_cast<const ST*>(scores);
   switch (slots_of(a.E)) {
-    case 1: route_ex_kernel<1, ST><<<grid, kRouterWarps * 32, smem, s>>>(sc, a); break;
-    case 2: route_ex_kernel<2, ST><<<grid, kRouterWarps * 32, smem, s>>>(sc, a); break;
-    case 4: route_ex_kernel<4, ST><<<grid, kRouterWarps * 32, smem, s>>>(sc, a); break;
-    case 8: route_ex_kernel<8, ST><<<grid, kRouterWarps * 32, smem, s>>>(sc, a); break;
-    default: route_ex_kernel<16, ST><<<grid, kRouterWarps * 32, smem, s>>>(sc, a); break;
+    case 1: return launch_dependent(route_ex_kernel<1, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
+    case 2: return launch_dependent(route_ex_kernel<2, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
+    case 4: return launch_dependent(route_ex_kernel<4, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
+    case 8: return launch_dependent(route_ex_kernel<8, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
+    default: return launch_dependent(route_ex_kernel<16, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
   }
-  return cudaGetLastError();
 }
 
 template <int MAXV, typename ST>
-void route_backward_of(const ST* sc, const RouteArgs& a, const int32_t* ids, const float* dw, ST* ds, long long ld_d,
-                       unsigned grid, size_t smem, cudaStream_t s) {
+cudaError_t route_backward_of(const ST* sc, const RouteArgs& a, const int32_t* ids, const float* dw, ST* ds, long long ld_d,
+                              dim3 grid, size_t smem, cudaStream_t s) {
   if (a.score_fn == MOE_SCORE_SOFTMAX && !a.renormalise)
-    route_backward_kernel<MAXV, ST, true><<<grid, kRouterWarps * 32, smem, s>>>(sc, ids, dw, ds, a, ld_d);
-  else
-    route_backward_kernel<MAXV, ST, false><<<grid, kRouterWarps * 32, smem, s>>>(sc, ids, dw, ds, a, ld_d);
+    return launch_dependent(route_backward_kernel<MAXV, ST, true>, grid, kRouterWarps * 32, smem, s, sc, ids, dw, ds, a, ld_d);
+  return launch_dependent(route_backward_kernel<MAXV, ST, false>, grid, kRouterWarps * 32, smem, s, sc, ids, dw, ds, a, ld_d);
 }
 
 template <typename ST>
 cudaError_t route_backward_of(const void* scores, const RouteArgs& a, const int32_t* ids, const float* dw,
                               void* dscores, long long ld_d, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((a.T + kRouterWarps - 1) / kRouterWarps);
+  const dim3 grid((a.T + kRouterWarps - 1) / kRouterWarps);
   const size_t smem = static_cast<size_t>(kRouterWarps) * a.E * sizeof(float);
   const ST* sc = static_cast<const ST*>(scores);
   ST* ds = static_cast<ST*>(dscores);
   switch (slots_of(a.E)) {
-    case 1: route_backward_of<1, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s); break;
-    case 2: route_backward_of<2, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s); break;
-    case 4: route_backward_of<4, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s); break;
-    case 8: route_backward_of<8, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s); break;
-    default: route_backward_of<16, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s); break;
+    case 1: return route_backward_of<1, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
+    case 2: return route_backward_of<2, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
+    case 4: return route_backward_of<4, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
+    case 8: return route_backward_of<8, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
+    default: return route_backward_of<16, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
