@@ -210,11 +210,11 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const void* dh_out, cons
       !aligned(db_pre, 4))
     return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  float* const sums[5] = {dw_post, db_post, dw_pre, db_pre,
-                          p->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr};
+  const NormSums sums{dw_post, db_post, dw_pre, db_pre,
+                      p->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr};
   if (p->T == 0) {
     cudaError_t e = cudaSuccess;
-    for (float* v : sums)
+    for (float* v : {sums.dw_post, sums.db_post, sums.dw_pre, sums.db_pre, sums.dgate})
       if (v && e == cudaSuccess) e = cudaMemsetAsync(v, 0, static_cast<size_t>(p->H) * 4, s);
     return from_cuda(e);
   }

@@ -237,18 +237,17 @@ struct NormArgs {
   void *dh, *d_o, *dgate;
   float* partials;  // column sums per block: [blocks][nacc][H]
   int nacc, acc_in_smem;
-  int acc_dw_post, acc_db_post, acc_dw_pre, acc_db_pre, acc_dgate;  // index among the sums, -1: not wanted
+  int acc_post1, acc_post0, acc_pre1, acc_pre0;  // index among the sums, -1: not wanted
 };
 size_t norm_partials_bytes(int T, int H);
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s);
-// sums: dw_post, db_post, dw_pre, db_pre, dgate (per channel), each fp32 [H] or null.
-cudaError_t launch_norm_backward(const NormArgs& a, float* const (&sums)[5], cudaStream_t s);
-// out.p[j][c] = sum over i of partials[i * stride + j * pitch + c], c < width, in a fixed order.
-struct ColumnOutputs {
-  float* p[5];
+// Per-column outputs of the gradient, fp32 [H], each may be null (dgate: per channel).
+struct NormSums {
+  float *dw_post, *db_post, *dw_pre, *db_pre, *dgate;
 };
-cudaError_t launch_column_sums(const float* partials, int nparts, size_t stride, int nsums, int width, size_t pitch,
-                               const ColumnOutputs& out, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormArgs& a, const NormSums& out, cudaStream_t s);
+// out[c] = sum over i < nparts of partials[i * width + c], in a fixed order.
+cudaError_t launch_column_sums(const float* partials, int nparts, int width, float* out, cudaStream_t s);
 
 // Linear layer with a fused epilogue (linear.cu).
 struct LinearArgs {

@@ -519,11 +519,7 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     stage_begin("linear_dz", s);
     err = launch_dependent(linear_dz_kernel, dim3((a.N + 255) / 256, chunks), dim3(32, 8), 0, s, d);
     stage_end(s);
-    if (err == cudaSuccess && a.dbias) {
-      ColumnOutputs out{};
-      out.p[0] = a.dbias;
-      err = launch_column_sums(a.partials, chunks, a.N, 1, a.N, 0, out, s);
-    }
+    if (err == cudaSuccess && a.dbias) err = launch_column_sums(a.partials, chunks, a.N, a.dbias, s);
   }
   const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};
   Product q{};

@@ -137,10 +137,21 @@ __device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, int dty
     }
   }
 }
-template <Access A>
+// T names the type where the rows come through a ring, `dtype` where they do not.
+template <typename T, Access A>
 __device__ __forceinline__ void store_row(void* p, int dtype, size_t at, int run, int H, bool vec,
                                           const float (&v)[EPT]) {
-  if (A == VEC16 || (A == PLAIN && vec)) {
+  if constexpr (A == VEC16) {
+    const int c = col_of<A>(run, 0, true);
+    if (c < H) pack(static_cast<T*>(p) + at + c, v);
+  } else if constexpr (A == WORD4) {
+    float* row = static_cast<float*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(run, i, false);
+      if (c < H) row[c] = v[i];
+    }
+  } else if (vec) {
     const int c = col_of<A>(run, 0, vec);
     if (c < H) pack_any(p, dtype, at + c, v);
   } else {
@@ -149,6 +160,20 @@ __device__ __forceinline__ void store_row(void* p, int dtype, size_t at, int run
       const int c = col_of<A>(run, i, vec);
       if (c < H) store_one(p, dtype, at + c, v[i]);
     }
+  }
+}
+
+// v = 0 for columns past H (after a mean was taken off).
+template <Access A>
+__device__ __forceinline__ void clear_past(float (&v)[EPT], int run, int H, bool vec) {
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    if (col_of<A>(run, 0, vec) >= H)
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i)
+      if (col_of<A>(run, i, vec) >= H) v[i] = 0.0f;
   }
 }
 
@@ -199,17 +224,17 @@ __device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int H) 
   }
 }
 
-// Sums of N (1 or 4) values over the block, for every thread, in a fixed order: a
-// butterfly in each warp (for four values one in which lanes trade values, so that it
-// takes 6 shuffles instead of 20), then every thread adds the warps' sums from shared
-// memory.  Two buffers taken in turn: a warp can be at most one sum ahead of the
-// others' reads.  buf: zeroed before the first use.
-template <int N>
+// Sums of N (1 or 4) values over a block of up to MAXT threads, for every thread, in a
+// fixed order: a butterfly in each warp (for four values one in which lanes trade
+// values, so that it takes 6 shuffles instead of 20), then every thread adds the
+// warps' sums from shared memory.  Two buffers taken in turn: a warp can be at most
+// one sum ahead of the others' reads.  buf: zeroed before the first use.
+template <int N, int MAXT>
 struct BlockSum {
-  float (*buf)[N][32];
+  float (*buf)[N][MAXT / 32];
   int turn;
   __device__ __forceinline__ void operator()(float (&v)[N]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if constexpr (N == 4) {
       const bool hi = lane & 16, mid = lane & 8;
       float a0 = hi ? v[2] : v[0], a1 = hi ? v[3] : v[1];
@@ -231,7 +256,8 @@ struct BlockSum {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       float s = 0.0f;
-      for (int w = 0; w < nw; w += 4) {
+#pragma unroll
+      for (int w = 0; w < MAXT / 32; w += 4) {
         const float4 f = *reinterpret_cast<const float4*>(&buf[turn][j][w]);
         s += (f.x + f.y) + (f.z + f.w);
       }

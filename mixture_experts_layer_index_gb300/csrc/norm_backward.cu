@@ -7,9 +7,9 @@
 // Bound by memory: four rows in, two out.  A row's moments and the means of its
 // gradient come from the same sum over the block (the means of RMS norms need no
 // second look), so a row takes two block-wide sums, three with a layer norm.
-// Column sums stay in shared memory, each column with the thread that owns
-// it; a block writes them to the workspace once and a second kernel adds the
-// blocks' sums in block order.
+// Column sums stay with the thread that owns the column, in registers up to
+// 4096 columns, else in shared memory; a block writes them to the workspace once
+// and a second kernel adds the blocks' sums in a fixed order.
 #include "norm.cuh"
 
 namespace moe {
@@ -37,39 +37,40 @@ __device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec
   }
 }
 
+// HOLD: column sums and per-column factors (of up to 4096 columns) stay in registers.
+// Sums over tokens, per column: post1 = sum alpha G' u, post0 = sum alpha G', with G'
+// = G for a per-column gate g (then dw = g post1, db = g post0, dg = w post1 + b post0)
+// and G' = g G otherwise (dw = post1, db = post0); pre1 = sum dx u, pre0 = sum dx.
+constexpr int min_blocks(int maxt) { return maxt <= 256 ? 2 : 1; }
+
 template <typename HT, typename OT, Access A, int RUNS, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_backward_kernel(NormArgs a) {
-  __shared__ __align__(16) float s_sum[2][4][32];
+__global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(NormArgs a) {
+  constexpr bool HOLD = A != PLAIN && MAXT <= 512;
+  __shared__ __align__(16) float s_sum[2][4][MAXT / 32];
   extern __shared__ __align__(16) uint8_t s_mem[];
   static_assert(A == PLAIN || RUNS == 1, "a ring holds one run per thread");
   const int H = a.H;
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const size_t pitch = static_cast<size_t>((H + EPT - 1) / EPT * EPT);
+  const int pitch = (H + EPT - 1) / EPT * EPT;
   const bool pre = a.pre != MOE_NORM_NONE, post = a.post != MOE_NORM_NONE;
   const bool layer_pre = a.pre == MOE_NORM_LAYER, layer_post = a.post == MOE_NORM_LAYER;
+  const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
+  const bool gate_t = a.gate_kind == MOE_GATE_TOKEN;
   // ring slots: o | dh' | h' | dx', then the column sums
+  const int rows = a.depth * pitch;
   OT* ring_o = reinterpret_cast<OT*>(s_mem);
-  HT* ring_g = reinterpret_cast<HT*>(ring_o + a.depth * pitch);
-  HT* ring_h = ring_g + (a.dh_out ? a.depth * pitch : 0);
-  OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? a.depth * pitch : 0));
-  uint8_t* after = reinterpret_cast<uint8_t*>(ring_x + (pre ? a.depth * pitch : 0));
+  HT* ring_g = reinterpret_cast<HT*>(ring_o + rows);
+  HT* ring_h = ring_g + (a.dh_out ? rows : 0);
+  OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? rows : 0));
   float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.nacc * pitch;
-  float* acc = a.acc_in_smem ? reinterpret_cast<float*>(A == PLAIN ? s_mem : after) : part;
+  float* acc = !a.acc_in_smem ? part : reinterpret_cast<float*>(A == PLAIN ? s_mem : reinterpret_cast<uint8_t*>(ring_x + (pre ? rows : 0)));
 
-  for (int i = threadIdx.x; i < 256; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < 8 * (MAXT / 32); i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
   __syncthreads();
-  BlockSum<4> block_sum{s_sum, 0};
+  BlockSum<4, MAXT> block_sum{s_sum, 0};
   dep_wait();
   dep_launch();
-  for (int j = 0; j < a.nacc; ++j)
-#pragma unroll
-    for (int r = 0; r < RUNS; ++r)
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        const int c = col_of<A>(r, i, vec);
-        if (c < H) acc[j * pitch + c] = 0.0f;
-      }
 
   auto fetch = [&](int t, int slot) {
     if (t < a.T) {
@@ -87,6 +88,34 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_backward_kernel(NormAr
   if (A != PLAIN)
     for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
 
+  // factors of dn: the pre norm's weight; the post norm's, with a per-column gate
+  auto post_factor = [&](float(&f)[EPT], int r) {
+    load_columns<A>(f, a.w_post, a.w_dtype, r, H, vec, 1.0f);
+    if (gate_c) {
+      float g[EPT];
+      load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) f[i] *= g[i];
+    }
+  };
+  float f_post[EPT], f_pre[EPT];
+  if (HOLD) {
+    post_factor(f_post, 0);
+    load_columns<A>(f_pre, a.w_pre, a.w_dtype, 0, H, vec, 1.0f);
+  }
+  float post1[EPT], post0[EPT], pre1[EPT], pre0[EPT];  // HOLD
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) post1[i] = post0[i] = pre1[i] = pre0[i] = 0.0f;
+  if (!HOLD)
+    for (int j = 0; j < a.nacc; ++j)
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          const int c = col_of<A>(r, i, vec);
+          if (c < H) acc[j * pitch + c] = 0.0f;
+        }
+
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
     if constexpr (A != PLAIN) {
@@ -94,35 +123,19 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_backward_kernel(NormAr
       fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
     }
-    auto get_o = [&](float(&v)[EPT], int r) {
-      if constexpr (A != PLAIN) copy_out<OT, A>(v, ring_o + slot * pitch, H);
-      else load_row<A>(v, a.o, a.o_dtype, at_o, r, H, vec);
-    };
-    auto get_g = [&](float(&v)[EPT], int r) {
-      if constexpr (A != PLAIN) copy_out<HT, A>(v, ring_g + slot * pitch, H);
-      else load_row<A>(v, a.dh_out, a.h_dtype, at_h, r, H, vec);
-    };
-    auto get_h = [&](float(&v)[EPT], int r) {
-      if constexpr (A != PLAIN) copy_out<HT, A>(v, ring_h + slot * pitch, H);
-      else load_row<A>(v, a.h, a.h_dtype, at_h, r, H, vec);
-    };
-    auto get_x = [&](float(&v)[EPT], int r) {
-      if constexpr (A != PLAIN) copy_out<OT, A>(v, ring_x + slot * pitch, H);
-      else load_row<A>(v, a.dx_out, a.o_dtype, at_o, r, H, vec);
-    };
     float hc[RUNS][EPT], oc[RUNS][EPT], dx[RUNS][EPT], G[RUNS][EPT];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      get_o(oc[r], r);
+      if constexpr (A != PLAIN) copy_out<OT, A>(oc[r], ring_o + slot * pitch, H);
+      else load_row<A>(oc[r], a.o, a.o_dtype, at_o, r, H, vec);
       if (pre) {
-        get_h(hc[r], r);
-        get_x(dx[r], r);
-      }
-      if (a.dh_out) {
-        get_g(G[r], r);
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) G[r][i] = 0.0f;
+        if constexpr (A != PLAIN) {
+          copy_out<HT, A>(hc[r], ring_h + slot * pitch, H);
+          copy_out<OT, A>(dx[r], ring_x + slot * pitch, H);
+        } else {
+          load_row<A>(hc[r], a.h, a.h_dtype, at_h, r, H, vec);
+          load_row<A>(dx[r], a.dx_out, a.o_dtype, at_o, r, H, vec);
+        }
       }
     }
     if (layer_pre || layer_post) {
@@ -135,125 +148,161 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_backward_kernel(NormAr
           s[1] += oc[r][i];
         }
       block_sum(s);
-      const float mh = s[0] * inv_h, mo = layer_post ? s[1] * inv_h : 0.0f;
+      const float mh = s[0] * inv_h, mo = s[1] * inv_h;
 #pragma unroll
-      for (int r = 0; r < RUNS; ++r)
+      for (int r = 0; r < RUNS; ++r) {
+        if (layer_pre) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          const bool in = col_of<A>(r, i, vec) < H;
-          if (layer_pre) hc[r][i] = in ? hc[r][i] - mh : 0.0f;
-          oc[r][i] = in ? oc[r][i] - mo : 0.0f;
+          for (int i = 0; i < EPT; ++i) hc[r][i] -= mh;
+          clear_past<A>(hc[r], r, H, vec);
         }
+        if (layer_post) {
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) oc[r][i] -= mo;
+          clear_past<A>(oc[r], r, H, vec);
+        }
+      }
     }
     // second moments, and the two means of the pre norm's gradient
-    float ro = 1.0f;
+    float ro = 1.0f, rs = 0.0f, m1 = 0.0f, m0 = 0.0f;
     if (pre || post) {
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
         if (pre) {
-          float w[EPT];
-          load_columns<A>(w, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+          if (!HOLD) load_columns<A>(f_pre, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
 #pragma unroll
           for (int i = 0; i < EPT; ++i) {
-            const float dxw = dx[r][i] * w[i];
+            const float dxw = dx[r][i] * f_pre[i];
             s[0] = fmaf(hc[r][i], hc[r][i], s[0]);
             s[1] = fmaf(dxw, hc[r][i], s[1]);
-            s[2] += dxw;
+            if (layer_pre) s[2] += dxw;
           }
         }
 #pragma unroll
         for (int i = 0; i < EPT; ++i) s[3] = fmaf(oc[r][i], oc[r][i], s[3]);
       }
       block_sum(s);
+      if (post) ro = inv_std(s[3], inv_h, a.eps);
       if (pre) {
-        const float rs = inv_std(s[0], inv_h, a.eps);
-        const float m1 = s[1] * rs * inv_h;                // mean(dx w u)
-        const float m0 = layer_pre ? s[2] * inv_h : 0.0f;  // mean(dx w)
-#pragma unroll
-        for (int r = 0; r < RUNS; ++r) {
-          float w[EPT];
-          load_columns<A>(w, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-          if (a.acc_db_pre >= 0) add_columns<A>(acc + a.acc_db_pre * pitch, r, H, vec, dx[r]);
-#pragma unroll
-          for (int i = 0; i < EPT; ++i) {
-            const float u = hc[r][i] * rs;
-            G[r][i] = fmaf(rs, fmaf(-u, m1, fmaf(dx[r][i], w[i], -m0)), G[r][i]);
-            dx[r][i] *= u;
-          }
-          if (a.acc_dw_pre >= 0) add_columns<A>(acc + a.acc_dw_pre * pitch, r, H, vec, dx[r]);
-        }
-      }
-      if (post) {
-        ro = inv_std(s[3], inv_h, a.eps);
-#pragma unroll
-        for (int r = 0; r < RUNS; ++r)
-#pragma unroll
-          for (int i = 0; i < EPT; ++i) oc[r][i] *= ro;  // u of the post norm
+        rs = inv_std(s[0], inv_h, a.eps);
+        m1 = s[1] * rs * inv_h;  // mean(dx w u)
+        m0 = s[2] * inv_h;       // mean(dx w); 0 for RMS
       }
     }
-    if (a.dh) {
 #pragma unroll
-      for (int r = 0; r < RUNS; ++r) {
+    for (int r = 0; r < RUNS; ++r) {
+      if (a.dh_out) {
+        if constexpr (A != PLAIN) copy_out<HT, A>(G[r], ring_g + slot * pitch, H);
+        else load_row<A>(G[r], a.dh_out, a.h_dtype, at_h, r, H, vec);
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) G[r][i] = 0.0f;
+      }
+      if (pre) {
+        if (!HOLD) load_columns<A>(f_pre, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          const float u = hc[r][i] * rs;
+          G[r][i] = fmaf(rs, fmaf(-u, m1, fmaf(dx[r][i], f_pre[i], -m0)), G[r][i]);
+          hc[r][i] = u;
+        }
+        clear_past<A>(G[r], r, H, vec);
+        if (HOLD) {
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) pre1[i] = fmaf(dx[r][i], hc[r][i], pre1[i]);
+          if (a.acc_pre0 >= 0)
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) pre0[i] += dx[r][i];
+        } else {
+          if (a.acc_pre0 >= 0) add_columns<A>(acc + a.acc_pre0 * pitch, r, H, vec, dx[r]);
+          if (a.acc_pre1 >= 0) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) dx[r][i] *= hc[r][i];
+            add_columns<A>(acc + a.acc_pre1 * pitch, r, H, vec, dx[r]);
+          }
+        }
+      }
+      if (a.dh) {
         float d[EPT];
 #pragma unroll
         for (int i = 0; i < EPT; ++i) d[i] = a.beta * G[r][i];
-        store_row<A>(a.dh, a.h_dtype, at_h, r, H, vec, d);
+        store_row<HT, A>(a.dh, a.h_dtype, at_h, r, H, vec, d);
       }
     }
-    // the block's side: ag = alpha G is the gradient of g N(o); G becomes dn w
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
+    // the block's side: alpha G is the gradient of g N(o); G becomes dn w
+    const float gt = gate_t ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
     float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      float w[EPT], dn[EPT], c[EPT];
-      load_columns<A>(w, post ? a.w_post : nullptr, a.w_dtype, r, H, vec, 1.0f);
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) dn[i] = col_of<A>(r, i, vec) < H ? a.alpha * G[r][i] : 0.0f;
-      if (a.dgate) {
-        load_columns<A>(c, post ? a.b_post : nullptr, a.w_dtype, r, H, vec, 0.0f);
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          c[i] = dn[i] * fmaf(oc[r][i], w[i], c[i]);
-          d[2] += c[i];
-        }
-        if (a.gate_kind == MOE_GATE_CHANNEL) add_columns<A>(acc + a.acc_dgate * pitch, r, H, vec, c);
-        else if (a.gate_kind == MOE_GATE_FULL) store_row<A>(a.dgate, a.o_dtype, at_o, r, H, vec, c);
-      }
-      if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
-        if (a.gate_kind == MOE_GATE_CHANNEL) load_columns<A>(c, a.gate, a.w_dtype, r, H, vec, 0.0f);
-        else load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) dn[i] *= c[i];
-      } else if (a.gate_kind == MOE_GATE_TOKEN) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) dn[i] *= gt;
-      }
-      if (a.acc_db_post >= 0) add_columns<A>(acc + a.acc_db_post * pitch, r, H, vec, dn);
+      float c[EPT];
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        c[i] = dn[i] * oc[r][i];
-        G[r][i] = dn[i] * w[i];
-        d[0] = fmaf(c[i], w[i], d[0]);
-        d[1] += G[r][i];
+        G[r][i] *= a.alpha;
+        oc[r][i] *= ro;  // u of the post norm, or o itself
       }
-      if (a.acc_dw_post >= 0) add_columns<A>(acc + a.acc_dw_post * pitch, r, H, vec, c);
+      if (a.dgate && !gate_c) {  // gradient of a gate per token or value: alpha G N(o)
+        float w[EPT];
+        load_columns<A>(w, a.w_post, a.w_dtype, r, H, vec, 1.0f);
+        load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          c[i] = G[r][i] * fmaf(oc[r][i], w[i], c[i]);
+          d[2] += c[i];
+        }
+        if (gate_f) store_row<OT, A>(a.dgate, a.o_dtype, at_o, r, H, vec, c);
+      }
+      if (gate_f) {
+        load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) G[r][i] *= c[i];
+      } else if (gate_t) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) G[r][i] *= gt;
+      }
+      if (HOLD) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) post1[i] = fmaf(G[r][i], oc[r][i], post1[i]);
+        if (a.acc_post0 >= 0)
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) post0[i] += G[r][i];
+      } else {
+        if (a.acc_post0 >= 0) add_columns<A>(acc + a.acc_post0 * pitch, r, H, vec, G[r]);
+        if (a.acc_post1 >= 0) {
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) c[i] = G[r][i] * oc[r][i];
+          add_columns<A>(acc + a.acc_post1 * pitch, r, H, vec, c);
+        }
+        post_factor(f_post, r);
+      }
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        G[r][i] *= f_post[i];
+        d[0] = fmaf(G[r][i], oc[r][i], d[0]);
+        if (layer_post) d[1] += G[r][i];
+      }
     }
-    const bool token_sum = a.dgate && a.gate_kind == MOE_GATE_TOKEN;
+    const bool token_sum = a.dgate && gate_t;
     if (post || token_sum) block_sum(d);
     if (token_sum && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = d[2];
     if (a.d_o) {
-      const float m1 = post ? d[0] * inv_h : 0.0f, m0 = layer_post ? d[1] * inv_h : 0.0f;
+      const float n1 = post ? d[0] * inv_h : 0.0f, n0 = layer_post ? d[1] * inv_h : 0.0f;
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) G[r][i] = ro * (fmaf(-oc[r][i], m1, G[r][i]) - m0);
-        store_row<A>(a.d_o, a.o_dtype, at_o, r, H, vec, G[r]);
+        for (int i = 0; i < EPT; ++i) G[r][i] = ro * (fmaf(-oc[r][i], n1, G[r][i]) - n0);
+        store_row<OT, A>(a.d_o, a.o_dtype, at_o, r, H, vec, G[r]);
       }
     }
     if (++slot >= a.depth) slot = 0;
   }
-  if (a.acc_in_smem) {  // each thread hands over the columns that it summed
+  // each thread hands over the columns that it summed
+  if (HOLD) {
+    if (a.acc_post1 >= 0) store_row<float, A>(part + a.acc_post1 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, post1);
+    if (a.acc_post0 >= 0) store_row<float, A>(part + a.acc_post0 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, post0);
+    if (a.acc_pre1 >= 0) store_row<float, A>(part + a.acc_pre1 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, pre1);
+    if (a.acc_pre0 >= 0) store_row<float, A>(part + a.acc_pre0 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, pre0);
+  } else if (a.acc_in_smem) {
     for (int j = 0; j < a.nacc; ++j)
 #pragma unroll
       for (int r = 0; r < RUNS; ++r)
@@ -265,20 +314,19 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_backward_kernel(NormAr
   }
 }
 
-// out[j][c] = sum over the blocks' partials, 32 columns per block; 32 rows of
-// threads add every 32nd partial in ascending order and the 32 sums are added in
-// order, so the result does not depend on timing.
-__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ partials, int nparts, size_t stride,
-                                                           int width, size_t pitch, ColumnOutputs out) {
+// out[c] = sum over the blocks' partials, 32 columns per block; 32 rows of threads add
+// every 32nd partial in ascending order and the 32 sums are added in order, so the
+// result does not depend on timing.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ partials, int nparts, int width,
+                                                           float* __restrict__ out) {
   __shared__ float s[32][33];
   dep_wait();
   dep_launch();
   const int c = blockIdx.x * 32 + threadIdx.x;
-  const float* p = partials + blockIdx.y * pitch + c;
   float v = 0.0f;
   if (c < width) {
 #pragma unroll 4
-    for (int i = threadIdx.y; i < nparts; i += 32) v += p[static_cast<size_t>(i) * stride];
+    for (int i = threadIdx.y; i < nparts; i += 32) v += partials[static_cast<size_t>(i) * width + c];
   }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
@@ -286,15 +334,52 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restri
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) sum += s[i][threadIdx.x];
-    out.p[blockIdx.y][c] = sum;
+    out[c] = sum;
   }
 }
 
-// At most as many blocks as are resident at 1024 threads per SM of a 152-SM part (a
-// pure function of the problem: the workspace holds one set of sums for each).
+// The same for the up to four sums of the norms' gradient, which the outputs share.
+__global__ void __launch_bounds__(1024) norm_sums_kernel(NormArgs a, NormSums out) {
+  __shared__ float s[4][32][33];
+  dep_wait();
+  dep_launch();
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  const size_t pitch = (a.H + EPT - 1) / EPT * EPT;
+  for (int j = 0; j < a.nacc; ++j) {
+    const float* p = a.partials + j * pitch + c;
+    float v = 0.0f;
+    if (c < a.H) {
+#pragma unroll 4
+      for (int i = threadIdx.y; i < a.blocks; i += 32) v += p[static_cast<size_t>(i) * a.nacc * pitch];
+    }
+    s[j][threadIdx.y][threadIdx.x] = v;
+  }
+  __syncthreads();
+  // row j of the threads adds up sum j
+  if (threadIdx.y < a.nacc) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += s[threadIdx.y][i][threadIdx.x];
+    s[threadIdx.y][0][threadIdx.x] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= a.H) return;
+  auto total = [&](int j) { return j >= 0 ? s[j][0][threadIdx.x] : 0.0f; };
+  auto value = [&](const void* v, float none) { return v ? load_one(v, a.w_dtype, c) : none; };
+  const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL;
+  const float g = gate_c ? value(a.gate, 1.0f) : 1.0f;
+  if (out.dw_post) out.dw_post[c] = g * total(a.acc_post1);
+  if (out.db_post) out.db_post[c] = g * total(a.acc_post0);
+  if (out.dw_pre) out.dw_pre[c] = total(a.acc_pre1);
+  if (out.db_pre) out.db_pre[c] = total(a.acc_pre0);
+  if (out.dgate) out.dgate[c] = value(a.w_post, 1.0f) * total(a.acc_post1) + value(a.b_post, 0.0f) * total(a.acc_post0);
+}
+
+// At most as many blocks as the registers of a 152-SM part hold (a pure function of
+// the problem: the workspace has room for the sums of each).
 inline int most_blocks_per_sm(int H) {
-  const int n = 1024 / norm_threads(H);
-  return n > 8 ? 8 : n;
+  const int n = min_blocks(256) * 256 / norm_threads(H);
+  return n > 16 ? 16 : n < 1 ? 1 : n;
 }
 
 constexpr size_t kSmemMax = 224 * 1024;  // of one block's dynamic shared memory
@@ -307,15 +392,17 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
                            static_cast<int>(kSmemMax));
   if (attr != cudaSuccess) return attr;
   const size_t pitch = static_cast<size_t>((a.H + EPT - 1) / EPT * EPT);
-  const size_t sums = a.nacc * pitch * sizeof(float);
+  constexpr bool HOLD = A != PLAIN && MAXT <= 512;
+  const size_t sums = HOLD ? 0 : a.nacc * pitch * sizeof(float);
   int per_sm = most_blocks_per_sm(a.H);
   size_t ring = 0;
   a.depth = 0;
   if (A != PLAIN) {
-    // rows of the ring: two, a third if it costs no block, one if two do not fit
+    // as many rows as fit with the resident blocks, up to four: two thirds of them on
+    // their way keep the memory busy
     const size_t row = pitch * (sizeof(OT) + (a.dh_out ? sizeof(HT) : 0) + (a.pre ? sizeof(HT) + sizeof(OT) : 0));
-    auto fit = [&](int depth) { return static_cast<int>(kSmemSm / (depth * row + sums + 2048)); };
-    a.depth = fit(2) < 1 ? 1 : fit(3) >= (fit(2) < per_sm ? fit(2) : per_sm) ? 3 : 2;
+    a.depth = 4;
+    while (a.depth > 1 && (a.depth * row + sums + 2048) * per_sm > kSmemSm) --a.depth;
     ring = a.depth * row;
   }
   a.acc_in_smem = ring + sums <= kSmemMax;  // else the sums are kept in the workspace itself
@@ -339,20 +426,18 @@ cudaError_t backward_ring(NormArgs& a, int threads, cudaStream_t s) {
 size_t norm_partials_bytes(int T, int H) {
   const size_t pitch = static_cast<size_t>((H + norms::EPT - 1) / norms::EPT * norms::EPT);
   const int most = 152 * norms::most_blocks_per_sm(H);
-  return static_cast<size_t>(T < most ? T : most) * 5 * pitch * sizeof(float);
+  return static_cast<size_t>(T < most ? T : most) * 4 * pitch * sizeof(float);
 }
 
-cudaError_t launch_norm_backward(const NormArgs& args, float* const (&sums)[5], cudaStream_t s) {
+cudaError_t launch_norm_backward(const NormArgs& args, const NormSums& out, cudaStream_t s) {
   using namespace norms;
   NormArgs a = args;
-  // the sums that are wanted, packed: vector j of a block's partials is out.p[j]
-  int* slot[5] = {&a.acc_dw_post, &a.acc_db_post, &a.acc_dw_pre, &a.acc_db_pre, &a.acc_dgate};
-  ColumnOutputs out{};
   a.nacc = 0;
-  for (int j = 0; j < 5; ++j) {
-    *slot[j] = sums[j] ? a.nacc : -1;
-    if (sums[j]) out.p[a.nacc++] = sums[j];
-  }
+  auto want = [&](bool yes) { return yes ? a.nacc++ : -1; };
+  a.acc_post1 = want(out.dw_post || out.dgate);
+  a.acc_post0 = want(out.db_post || (out.dgate && a.b_post));
+  a.acc_pre1 = want(out.dw_pre);
+  a.acc_pre0 = want(out.db_pre);
   const int threads = norm_threads(a.H);
   const int pair = a.h_dtype * 3 + a.o_dtype;
   stage_begin("norm_backward", s);
@@ -378,17 +463,17 @@ cudaError_t launch_norm_backward(const NormArgs& args, float* const (&sums)[5], 
   }
   stage_end(s);
   if (err == cudaSuccess && a.nacc > 0) {
-    const size_t pitch = static_cast<size_t>((a.H + EPT - 1) / EPT * EPT);
-    err = launch_column_sums(a.partials, a.blocks, a.nacc * pitch, a.nacc, a.H, pitch, out, s);
+    stage_begin("column_sums", s);
+    err = launch_dependent(norm_sums_kernel, dim3((a.H + 31) / 32), dim3(32, 32), 0, s, a, out);
+    stage_end(s);
   }
   return err;
 }
 
-cudaError_t launch_column_sums(const float* partials, int nparts, size_t stride, int nsums, int width, size_t pitch,
-                               const ColumnOutputs& out, cudaStream_t s) {
+cudaError_t launch_column_sums(const float* partials, int nparts, int width, float* out, cudaStream_t s) {
   stage_begin("column_sums", s);
-  const cudaError_t err = launch_dependent(norms::column_sums_kernel, dim3((width + 31) / 32, nsums), dim3(32, 32), 0, s,
-                                           partials, nparts, stride, width, pitch, out);
+  const cudaError_t err =
+      launch_dependent(norms::column_sums_kernel, dim3((width + 31) / 32), dim3(32, 32), 0, s, partials, nparts, width, out);
   stage_end(s);
   return err;
 }

@@ -12,20 +12,25 @@ namespace moe {
 namespace norms {
 namespace {
 
+// HOLD: the per-column factors (of up to 4096 columns) stay in registers, alpha and a
+// per-column gate folded into the post norm's.
+constexpr int min_blocks(int maxt) { return maxt <= 256 ? 3 : 1; }
+
 template <typename HT, typename OT, Access A, int RUNS, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_forward_kernel(NormArgs a) {
-  __shared__ __align__(16) float s_sum[2][1][32];
+__global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(NormArgs a) {
+  constexpr bool HOLD = A != PLAIN && MAXT <= 512;
+  __shared__ __align__(16) float s_sum[2][1][MAXT / 32];
   extern __shared__ __align__(16) uint8_t s_ring[];
   static_assert(A == PLAIN || RUNS == 1, "a ring holds one run per thread");
   const int H = a.H;
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const size_t pitch = static_cast<size_t>((H + EPT - 1) / EPT * EPT);
+  const int pitch = (H + EPT - 1) / EPT * EPT;
   HT* ring_h = reinterpret_cast<HT*>(s_ring);
-  OT* ring_o = reinterpret_cast<OT*>(s_ring + a.depth * pitch * sizeof(HT));
-  for (int i = threadIdx.x; i < 64; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+  OT* ring_o = reinterpret_cast<OT*>(ring_h + a.depth * pitch);
+  for (int i = threadIdx.x; i < 2 * (MAXT / 32); i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
   __syncthreads();
-  BlockSum<1> block_sum{s_sum, 0};
+  BlockSum<1, MAXT> block_sum{s_sum, 0};
   dep_wait();
   dep_launch();
 
@@ -40,6 +45,23 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_forward_kernel(NormArg
   if (A != PLAIN)
     for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
 
+  // factor of the normalised (or plain) o, and of the normalised h'
+  const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
+  auto post_factor = [&](float(&f)[EPT], int r) {
+    load_columns<A>(f, a.w_post, a.w_dtype, r, H, vec, 1.0f);
+    if (gate_c) {
+      float g[EPT];
+      load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) f[i] *= g[i];
+    }
+  };
+  float f_post[EPT], f_pre[EPT];
+  if (HOLD) {
+    post_factor(f_post, 0);
+    load_columns<A>(f_pre, a.w_pre, a.w_dtype, 0, H, vec, 1.0f);
+  }
+
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
     float v[RUNS][EPT];
@@ -53,8 +75,8 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_forward_kernel(NormArg
       for (int r = 0; r < RUNS; ++r) load_row<A>(v[r], a.o, a.o_dtype, at_o, r, H, vec);
     }
 
-    // v = N(v): moments over the block, then the affine part
-    auto normalise = [&](int kind, const void* w, const void* b) {
+    // takes the mean off v (layer norms) and returns 1 / std
+    auto moments = [&](int kind) {
       if (kind == MOE_NORM_LAYER) {
         float s[1] = {0.0f};
 #pragma unroll
@@ -64,9 +86,11 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_forward_kernel(NormArg
         block_sum(s);
         const float mu = s[0] * inv_h;
 #pragma unroll
-        for (int r = 0; r < RUNS; ++r)
+        for (int r = 0; r < RUNS; ++r) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) v[r][i] = col_of<A>(r, i, vec) < H ? v[r][i] - mu : 0.0f;
+          for (int i = 0; i < EPT; ++i) v[r][i] -= mu;
+          clear_past<A>(v[r], r, H, vec);
+        }
       }
       float q[1] = {0.0f};
 #pragma unroll
@@ -74,45 +98,56 @@ __global__ void __launch_bounds__(MAXT, 1024 / MAXT) norm_forward_kernel(NormArg
 #pragma unroll
         for (int i = 0; i < EPT; ++i) q[0] = fmaf(v[r][i], v[r][i], q[0]);
       block_sum(q);
-      const float rs = inv_std(q[0], inv_h, a.eps);
-#pragma unroll
-      for (int r = 0; r < RUNS; ++r) {
-        float c[EPT];
-        load_columns<A>(c, w, a.w_dtype, r, H, vec, 1.0f);
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) v[r][i] *= rs * c[i];
-        if (b) {
-          load_columns<A>(c, b, a.w_dtype, r, H, vec, 0.0f);
-#pragma unroll
-          for (int i = 0; i < EPT; ++i) v[r][i] += c[i];
-        }
-      }
+      return inv_std(q[0], inv_h, a.eps);
     };
 
-    if (a.post != MOE_NORM_NONE) normalise(a.post, a.w_post, a.b_post);
-    const float scale =
-        a.gate_kind == MOE_GATE_TOKEN ? a.alpha * __ldg(static_cast<const float*>(a.gate) + t) : a.alpha;
+    float scale = a.alpha;
+    if (a.gate_kind == MOE_GATE_TOKEN) scale *= __ldg(static_cast<const float*>(a.gate) + t);
+    const float rs = a.post != MOE_NORM_NONE ? scale * moments(a.post) : scale;
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float c[EPT];
-      if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
-        if (a.gate_kind == MOE_GATE_CHANNEL) load_columns<A>(c, a.gate, a.w_dtype, r, H, vec, 0.0f);
-        else load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
+      if (!HOLD) post_factor(f_post, r);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) v[r][i] *= rs * f_post[i];
+      if (a.b_post) {
+        load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+        if (gate_c) {
+          float g[EPT];
+          load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) c[i] *= g[i];
+        }
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) v[r][i] = fmaf(scale, c[i], v[r][i]);
+      }
+      if (gate_f) {
+        load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
 #pragma unroll
         for (int i = 0; i < EPT; ++i) v[r][i] *= c[i];
       }
       if constexpr (A != PLAIN) copy_out<HT, A>(c, ring_h + slot * pitch, H);
       else load_row<A>(c, a.h, a.h_dtype, at_h, r, H, vec);
 #pragma unroll
-      for (int i = 0; i < EPT; ++i)
-        v[r][i] = col_of<A>(r, i, vec) < H ? fmaf(scale, v[r][i], a.beta * c[i]) : 0.0f;
-      store_row<A>(a.h_out, a.h_dtype, at_h, r, H, vec, v[r]);
+      for (int i = 0; i < EPT; ++i) v[r][i] = fmaf(a.beta, c[i], v[r][i]);
+      store_row<HT, A>(a.h_out, a.h_dtype, at_h, r, H, vec, v[r]);
     }
     // x' is taken from h' before its rounding: one rounding each
     if (a.pre != MOE_NORM_NONE) {
-      normalise(a.pre, a.w_pre, a.b_pre);
+      const float rp = moments(a.pre);
 #pragma unroll
-      for (int r = 0; r < RUNS; ++r) store_row<A>(a.x_out, a.o_dtype, at_o, r, H, vec, v[r]);
+      for (int r = 0; r < RUNS; ++r) {
+        if (!HOLD) load_columns<A>(f_pre, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) v[r][i] *= rp * f_pre[i];
+        if (a.b_pre) {
+          float c[EPT];
+          load_columns<A>(c, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) v[r][i] += c[i];
+        }
+        store_row<OT, A>(a.x_out, a.o_dtype, at_o, r, H, vec, v[r]);
+      }
     }
     if (++slot >= a.depth) slot = 0;
   }
@@ -129,7 +164,8 @@ cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * 8192 * 8);
     if (attr != cudaSuccess) return attr;
   }
-  const int cap = 152 * (1024 / threads > 32 ? 32 : 1024 / threads);
+  const int per_sm = MAXT <= 256 ? min_blocks(MAXT) * 256 / threads : 1;  // resident blocks
+  const int cap = 152 * (per_sm > 32 ? 32 : per_sm);
   return launch_dependent(norm_forward_kernel<HT, OT, A, RUNS, MAXT>, dim3(a.T < cap ? a.T : cap), dim3(threads), smem,
                           s, a);
 }
