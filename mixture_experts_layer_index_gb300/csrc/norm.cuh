@@ -1,8 +1,10 @@
 // Parts shared by the block norms' forward (norm_forward.cu) and gradient
 // (norm_backward.cu) kernels: how rows come in and go out, and block-wide sums.
 //
-// A block takes whole rows, a thread eight columns of a row (or two runs of
-// eight), and blocks walk over rows.  Where rows can be read asynchronously
+// A block takes whole rows, a thread two runs of eight columns of a row, and blocks
+// walk over rows.  (Sixteen columns per thread halve what the block-wide sums and
+// the addresses cost per column against eight: the gradient kernel is bound by
+// instructions as much as by memory.)  Where rows can be read asynchronously
 // (cp.async), each block keeps a ring of rows in shared memory: a thread copies
 // exactly the columns it will read itself, so the ring needs no barrier and the
 // rows in flight cost no registers.
@@ -16,12 +18,15 @@
 namespace moe {
 namespace norms {
 
-constexpr int EPT = 8;  // columns per thread and run
+constexpr int EPT = 8;   // columns per thread and run
+constexpr int RUNS = 2;
 
 // How a thread's columns of a row lie and come in.
 //   VEC16: columns [run*8*NT + tid*8, + 8), 16-byte copies into the ring (widths,
 //          strides and addresses that are multiples of 16 bytes)
-//   WORD4: columns run*8*NT + i*NT + tid, 4-byte copies into the ring (fp32 rows)
+//   WORD4: a warp takes 512 columns, its lane l columns (run*8 + i)*32 + l of them: whole
+//          128-byte lines, and constant distances between a thread's columns; 4-byte
+//          copies into the ring (fp32 rows)
 //   PLAIN: like WORD4, or like VEC16 where the row allows it (`vec`), loaded when
 //          they are used, any type: 16-bit rows at odd addresses, and rows too long for a ring
 enum Access { VEC16, WORD4, PLAIN };
@@ -29,7 +34,8 @@ enum Access { VEC16, WORD4, PLAIN };
 template <Access A>
 __device__ __forceinline__ int col_of(int run, int i, bool vec) {
   const bool together = A == VEC16 || (A == PLAIN && vec);
-  return together ? (run * blockDim.x + threadIdx.x) * EPT + i : (run * EPT + i) * blockDim.x + threadIdx.x;
+  if (together) return (run * blockDim.x + threadIdx.x) * EPT + i;
+  return static_cast<int>(threadIdx.x >> 5) * (32 * RUNS * EPT) + (threadIdx.x & 31) + (run * EPT + i) * 32;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -163,6 +169,17 @@ __device__ __forceinline__ void store_row(void* p, int dtype, size_t at, int run
   }
 }
 
+// A thread's columns of an fp32 vector in shared memory, for itself.
+template <Access A>
+__device__ __forceinline__ void put_shared(float* slot, int run, int H, const float (&v)[EPT]) {
+  if (A == WORD4) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) slot[col_of<A>(run, i, false)] = v[i];
+  } else {
+    store_row<float, A>(slot, MOE_DTYPE_F32, 0, run, H, true, v);
+  }
+}
+
 // v = 0 for columns past H (after a mean was taken off).
 template <Access A>
 __device__ __forceinline__ void clear_past(float (&v)[EPT], int run, int H, bool vec) {
@@ -194,23 +211,37 @@ __device__ __forceinline__ void load_columns(float (&v)[EPT], const void* p, int
 template <typename T, Access A>
 __device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H) {
   const T* row = static_cast<const T*>(p) + at;
-  if (A == VEC16) {
-    const int c = col_of<A>(0, 0, true);
-    if (c < H)
+  constexpr int PER = 16 / sizeof(T);
 #pragma unroll
-      for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q) cp_async16(slot + c + q * (16 / sizeof(T)), row + c + q * (16 / sizeof(T)));
-  } else if (A == WORD4) {
+  for (int r = 0; r < RUNS; ++r) {
+    if (A == VEC16) {
+      const int c = col_of<A>(r, 0, true);
+      if (c < H)
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(0, i, false);
-      if (c < H) cp_async4(slot + c, row + c);
+        for (int q = 0; q < EPT / PER; ++q) cp_async16(slot + c + q * PER, row + c + q * PER);
+    } else if (A == WORD4) {
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        const int c = col_of<A>(r, i, false);
+        if (c < H) cp_async4(slot + c, row + c);
+      }
     }
   }
 }
+// (WORD4: zeros are put past column H once, so that reads need no test.)
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int H) {
+__device__ __forceinline__ void clear_slot(T* slot, int H) {
+  if (A == WORD4)
+#pragma unroll
+    for (int i = 0; i < RUNS * EPT; ++i) {
+      const int c = col_of<A>(0, i, false);
+      if (c >= H) slot[c] = T(0.0f);
+    }
+}
+template <typename T, Access A>
+__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, int H) {
   if (A == VEC16) {
-    const int c = col_of<A>(0, 0, true);
+    const int c = col_of<A>(r, 0, true);
     if (c < H) unpack(v, slot + c);
     else
 #pragma unroll
@@ -218,20 +249,20 @@ __device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int H) 
   } else {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(0, i, false);
-      v[i] = c < H ? as_f32(slot[c]) : 0.0f;
+      v[i] = as_f32(slot[col_of<A>(r, i, false)]);  // past column H the ring holds zeros
     }
   }
 }
 
 // Sums of N (1 or 4) values over a block of up to MAXT threads, for every thread, in a
-// fixed order: a butterfly in each warp (for four values one in which lanes trade
-// values, so that it takes 6 shuffles instead of 20), then every thread adds the
-// warps' sums from shared memory.  Two buffers taken in turn: a warp can be at most
-// one sum ahead of the others' reads.  buf: zeroed before the first use.
+// fixed order: a butterfly in each warp, then one over the warps' sums, which every
+// warp reads from shared memory.  For four values the lanes trade values on the way (6
+// shuffles instead of 20).  Two buffers taken in turn: a warp can be at most one sum
+// ahead of the others' reads.  buf: zeroed before the first use.
 template <int N, int MAXT>
 struct BlockSum {
-  float (*buf)[N][MAXT / 32];
+  static constexpr int W = MAXT / 32 < 8 ? 8 : MAXT / 32;
+  float (*buf)[N][W];
   int turn;
   __device__ __forceinline__ void operator()(float (&v)[N]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -242,39 +273,48 @@ struct BlockSum {
       a1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
       float b = mid ? a1 : a0;
       b += __shfl_xor_sync(0xffffffffu, mid ? a0 : a1, 8);
-      b += __shfl_xor_sync(0xffffffffu, b, 4);
-      b += __shfl_xor_sync(0xffffffffu, b, 2);
-      b += __shfl_xor_sync(0xffffffffu, b, 1);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
       if ((lane & 7) == 0) buf[turn][lane >> 3][warp] = b;
+      __syncthreads();
+      // eight lanes per value
+      const float* from = &buf[turn][lane >> 3][(lane & 7) * (W / 8)];
+      b = from[0];
+#pragma unroll
+      for (int i = 1; i < W / 8; ++i) b += from[i];
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __shfl_sync(0xffffffffu, b, j * 8);
     } else {
       float b = v[0];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
       if (lane == 0) buf[turn][0][warp] = b;
-    }
-    __syncthreads();
+      __syncthreads();
+      b = buf[turn][0][lane & (W - 1)];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < MAXT / 32; w += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&buf[turn][j][w]);
-        s += (f.x + f.y) + (f.z + f.w);
-      }
-      v[j] = s;
+      for (int o = W / 2; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+      v[0] = b;
     }
     turn ^= 1;
   }
 };
 
-// 1 / sqrt of the second moment, whose sum over H columns is given, plus eps.
-__device__ __forceinline__ float inv_std(float sum, float inv_h, float eps) { return 1.0f / sqrtf(sum * inv_h + eps); }
+// 1 / sqrt of the second moment, whose sum over H columns is given, plus eps.  rsqrtf
+// is within 2 ulp, a tenth of the instructions of a square root and a division.
+__device__ __forceinline__ float inv_std(float sum, float inv_h, float eps) { return rsqrtf(sum * inv_h + eps); }
 
-// Threads of a block for rows of H columns: one run of eight columns each up to
-// 8192 columns, two beyond.
+// Threads of a block for rows of H columns.
 inline int norm_threads(int H) {
-  const int t = (H + EPT - 1) / EPT;
-  return t >= 1024 ? 1024 : (t + 31) / 32 * 32;
+  const int t = (H + EPT * RUNS - 1) / (EPT * RUNS);
+  return (t + 31) / 32 * 32;
+}
+inline size_t norm_pitch(int H) { return static_cast<size_t>(H + EPT - 1) / EPT * EPT; }
+// Elements of a row's slot in shared memory.
+template <Access A>
+__host__ __device__ inline int slot_pitch(int H, int threads) {
+  return A == WORD4 ? threads * EPT * RUNS : (H + EPT - 1) / EPT * EPT;
 }
 
 }  // namespace norms

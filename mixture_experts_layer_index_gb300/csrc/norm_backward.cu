@@ -8,7 +8,7 @@
 // gradient come from the same sum over the block (the means of RMS norms need no
 // second look), so a row takes two block-wide sums, three with a layer norm.
 // Column sums stay with the thread that owns the column, in registers up to
-// 4096 columns, else in shared memory; a block writes them to the workspace once
+// 8192 columns, else in shared memory; a block writes them to the workspace once
 // and a second kernel adds the blocks' sums in a fixed order.
 #include "norm.cuh"
 
@@ -37,41 +37,53 @@ __device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec
   }
 }
 
-// HOLD: column sums and per-column factors (of up to 4096 columns) stay in registers.
 // Sums over tokens, per column: post1 = sum alpha G' u, post0 = sum alpha G', with G'
 // = G for a per-column gate g (then dw = g post1, db = g post0, dg = w post1 + b post0)
 // and G' = g G otherwise (dw = post1, db = post0); pre1 = sum dx u, pre0 = sum dx.
-constexpr int min_blocks(int maxt) { return maxt <= 256 ? 2 : 1; }
+// ZERO: post0 or pre0 are wanted (their registers cost a resident block).
+constexpr int min_blocks(int maxt, bool zero) { return maxt <= 128 ? (zero ? 3 : 4) : maxt <= 256 && !zero ? 2 : 1; }
 
-template <typename HT, typename OT, Access A, int RUNS, int MAXT>
-__global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(NormArgs a) {
-  constexpr bool HOLD = A != PLAIN && MAXT <= 512;
-  __shared__ __align__(16) float s_sum[2][4][MAXT / 32];
+template <typename HT, typename OT, Access A, int MAXT, bool ZERO>
+__global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_kernel(NormArgs a) {
+  constexpr bool RING = A != PLAIN;
+  using Sum = BlockSum<4, MAXT>;
+  __shared__ __align__(16) float s_sum[2][4][Sum::W];
   extern __shared__ __align__(16) uint8_t s_mem[];
-  static_assert(A == PLAIN || RUNS == 1, "a ring holds one run per thread");
   const int H = a.H;
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const int pitch = (H + EPT - 1) / EPT * EPT;
+  const int pitch = slot_pitch<A>(H, blockDim.x), sums_pitch = (H + EPT - 1) / EPT * EPT;
   const bool pre = a.pre != MOE_NORM_NONE, post = a.post != MOE_NORM_NONE;
   const bool layer_pre = a.pre == MOE_NORM_LAYER, layer_post = a.post == MOE_NORM_LAYER;
   const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
   const bool gate_t = a.gate_kind == MOE_GATE_TOKEN;
-  // ring slots: o | dh' | h' | dx', then the column sums
+  // ring slots: o | dh' | h' | dx', then the factors of the post and of the pre norm;
+  // without a ring, the column sums (in the workspace itself where they do not fit)
   const int rows = a.depth * pitch;
   OT* ring_o = reinterpret_cast<OT*>(s_mem);
   HT* ring_g = reinterpret_cast<HT*>(ring_o + rows);
   HT* ring_h = ring_g + (a.dh_out ? rows : 0);
   OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? rows : 0));
-  float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.nacc * pitch;
-  float* acc = !a.acc_in_smem ? part : reinterpret_cast<float*>(A == PLAIN ? s_mem : reinterpret_cast<uint8_t*>(ring_x + (pre ? rows : 0)));
+  float* s_post = reinterpret_cast<float*>(ring_x + (pre ? rows : 0));
+  float* s_pre = s_post + pitch;
+  float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.nacc * sums_pitch;
+  float* acc = a.acc_in_smem ? reinterpret_cast<float*>(s_mem) : part;
 
-  for (int i = threadIdx.x; i < 8 * (MAXT / 32); i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < 8 * Sum::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
   __syncthreads();
-  BlockSum<4, MAXT> block_sum{s_sum, 0};
+  Sum block_sum{s_sum, 0};
   dep_wait();
   dep_launch();
 
+  if (A == WORD4)
+    for (int d = 0; d < a.depth; ++d) {
+      clear_slot<OT, A>(ring_o + d * pitch, H);
+      if (a.dh_out) clear_slot<HT, A>(ring_g + d * pitch, H);
+      if (pre) {
+        clear_slot<HT, A>(ring_h + d * pitch, H);
+        clear_slot<OT, A>(ring_x + d * pitch, H);
+      }
+    }
   auto fetch = [&](int t, int slot) {
     if (t < a.T) {
       const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
@@ -85,7 +97,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
     cp_async_commit();
   };
   int slot = 0;
-  if (A != PLAIN)
+  if (RING)
     for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
 
   // factors of dn: the pre norm's weight; the post norm's, with a per-column gate
@@ -98,27 +110,38 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
       for (int i = 0; i < EPT; ++i) f[i] *= g[i];
     }
   };
-  float f_post[EPT], f_pre[EPT];
-  if (HOLD) {
-    post_factor(f_post, 0);
-    load_columns<A>(f_pre, a.w_pre, a.w_dtype, 0, H, vec, 1.0f);
-  }
-  float post1[EPT], post0[EPT], pre1[EPT], pre0[EPT];  // HOLD
+  if (RING)
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) post1[i] = post0[i] = pre1[i] = pre0[i] = 0.0f;
-  if (!HOLD)
+    for (int r = 0; r < RUNS; ++r) {
+      float f[EPT];
+      post_factor(f, r);
+      put_shared<A>(s_post, r, H, f);
+      load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+      put_shared<A>(s_pre, r, H, f);
+    }
+  auto factor = [&](float(&f)[EPT], bool of_post, int r) {
+    if constexpr (RING) copy_out<float, A>(f, of_post ? s_post : s_pre, r, H);
+    else if (of_post) post_factor(f, r);
+    else load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+  };
+  float post1[RUNS][EPT], post0[RUNS][EPT], pre1[RUNS][EPT], pre0[RUNS][EPT];  // with a ring
+#pragma unroll
+  for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) post1[r][i] = post0[r][i] = pre1[r][i] = pre0[r][i] = 0.0f;
+  if (!RING)
     for (int j = 0; j < a.nacc; ++j)
 #pragma unroll
       for (int r = 0; r < RUNS; ++r)
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
           const int c = col_of<A>(r, i, vec);
-          if (c < H) acc[j * pitch + c] = 0.0f;
+          if (c < H) acc[j * sums_pitch + c] = 0.0f;
         }
 
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
-    if constexpr (A != PLAIN) {
+    if (RING) {
       const int ahead = slot + a.depth - 1;
       fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
@@ -126,12 +149,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
     float hc[RUNS][EPT], oc[RUNS][EPT], dx[RUNS][EPT], G[RUNS][EPT];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if constexpr (A != PLAIN) copy_out<OT, A>(oc[r], ring_o + slot * pitch, H);
+      if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r, H);
       else load_row<A>(oc[r], a.o, a.o_dtype, at_o, r, H, vec);
       if (pre) {
-        if constexpr (A != PLAIN) {
-          copy_out<HT, A>(hc[r], ring_h + slot * pitch, H);
-          copy_out<OT, A>(dx[r], ring_x + slot * pitch, H);
+        if constexpr (RING) {
+          copy_out<HT, A>(hc[r], ring_h + slot * pitch, r, H);
+          copy_out<OT, A>(dx[r], ring_x + slot * pitch, r, H);
         } else {
           load_row<A>(hc[r], a.h, a.h_dtype, at_h, r, H, vec);
           load_row<A>(dx[r], a.dx_out, a.o_dtype, at_o, r, H, vec);
@@ -170,10 +193,11 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
         if (pre) {
-          if (!HOLD) load_columns<A>(f_pre, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+          float f[EPT];
+          factor(f, false, r);
 #pragma unroll
           for (int i = 0; i < EPT; ++i) {
-            const float dxw = dx[r][i] * f_pre[i];
+            const float dxw = dx[r][i] * f[i];
             s[0] = fmaf(hc[r][i], hc[r][i], s[0]);
             s[1] = fmaf(dxw, hc[r][i], s[1]);
             if (layer_pre) s[2] += dxw;
@@ -193,33 +217,34 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       if (a.dh_out) {
-        if constexpr (A != PLAIN) copy_out<HT, A>(G[r], ring_g + slot * pitch, H);
+        if constexpr (RING) copy_out<HT, A>(G[r], ring_g + slot * pitch, r, H);
         else load_row<A>(G[r], a.dh_out, a.h_dtype, at_h, r, H, vec);
       } else {
 #pragma unroll
         for (int i = 0; i < EPT; ++i) G[r][i] = 0.0f;
       }
       if (pre) {
-        if (!HOLD) load_columns<A>(f_pre, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+        float f[EPT];
+        factor(f, false, r);
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
           const float u = hc[r][i] * rs;
-          G[r][i] = fmaf(rs, fmaf(-u, m1, fmaf(dx[r][i], f_pre[i], -m0)), G[r][i]);
+          G[r][i] = fmaf(rs, fmaf(-u, m1, fmaf(dx[r][i], f[i], -m0)), G[r][i]);
           hc[r][i] = u;
         }
         clear_past<A>(G[r], r, H, vec);
-        if (HOLD) {
+        if (RING) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) pre1[i] = fmaf(dx[r][i], hc[r][i], pre1[i]);
-          if (a.acc_pre0 >= 0)
+          for (int i = 0; i < EPT; ++i) pre1[r][i] = fmaf(dx[r][i], hc[r][i], pre1[r][i]);
+          if (ZERO)
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) pre0[i] += dx[r][i];
+            for (int i = 0; i < EPT; ++i) pre0[r][i] += dx[r][i];
         } else {
-          if (a.acc_pre0 >= 0) add_columns<A>(acc + a.acc_pre0 * pitch, r, H, vec, dx[r]);
+          if (a.acc_pre0 >= 0) add_columns<A>(acc + a.acc_pre0 * sums_pitch, r, H, vec, dx[r]);
           if (a.acc_pre1 >= 0) {
 #pragma unroll
             for (int i = 0; i < EPT; ++i) dx[r][i] *= hc[r][i];
-            add_columns<A>(acc + a.acc_pre1 * pitch, r, H, vec, dx[r]);
+            add_columns<A>(acc + a.acc_pre1 * sums_pitch, r, H, vec, dx[r]);
           }
         }
       }
@@ -260,24 +285,24 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
 #pragma unroll
         for (int i = 0; i < EPT; ++i) G[r][i] *= gt;
       }
-      if (HOLD) {
+      if (RING) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) post1[i] = fmaf(G[r][i], oc[r][i], post1[i]);
-        if (a.acc_post0 >= 0)
+        for (int i = 0; i < EPT; ++i) post1[r][i] = fmaf(G[r][i], oc[r][i], post1[r][i]);
+        if (ZERO)
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) post0[i] += G[r][i];
+          for (int i = 0; i < EPT; ++i) post0[r][i] += G[r][i];
       } else {
-        if (a.acc_post0 >= 0) add_columns<A>(acc + a.acc_post0 * pitch, r, H, vec, G[r]);
+        if (a.acc_post0 >= 0) add_columns<A>(acc + a.acc_post0 * sums_pitch, r, H, vec, G[r]);
         if (a.acc_post1 >= 0) {
 #pragma unroll
           for (int i = 0; i < EPT; ++i) c[i] = G[r][i] * oc[r][i];
-          add_columns<A>(acc + a.acc_post1 * pitch, r, H, vec, c);
+          add_columns<A>(acc + a.acc_post1 * sums_pitch, r, H, vec, c);
         }
-        post_factor(f_post, r);
       }
+      factor(c, true, r);
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        G[r][i] *= f_post[i];
+        G[r][i] *= c[i];
         d[0] = fmaf(G[r][i], oc[r][i], d[0]);
         if (layer_post) d[1] += G[r][i];
       }
@@ -297,11 +322,14 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
     if (++slot >= a.depth) slot = 0;
   }
   // each thread hands over the columns that it summed
-  if (HOLD) {
-    if (a.acc_post1 >= 0) store_row<float, A>(part + a.acc_post1 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, post1);
-    if (a.acc_post0 >= 0) store_row<float, A>(part + a.acc_post0 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, post0);
-    if (a.acc_pre1 >= 0) store_row<float, A>(part + a.acc_pre1 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, pre1);
-    if (a.acc_pre0 >= 0) store_row<float, A>(part + a.acc_pre0 * pitch, MOE_DTYPE_F32, 0, 0, H, vec, pre0);
+  if (RING) {
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      if (a.acc_post1 >= 0) store_row<float, A>(part + a.acc_post1 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, post1[r]);
+      if (a.acc_post0 >= 0) store_row<float, A>(part + a.acc_post0 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, post0[r]);
+      if (a.acc_pre1 >= 0) store_row<float, A>(part + a.acc_pre1 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, pre1[r]);
+      if (a.acc_pre0 >= 0) store_row<float, A>(part + a.acc_pre0 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, pre0[r]);
+    }
   } else if (a.acc_in_smem) {
     for (int j = 0; j < a.nacc; ++j)
 #pragma unroll
@@ -309,7 +337,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_backward_kernel(N
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
           const int c = col_of<A>(r, i, vec);
-          if (c < H) part[j * pitch + c] = acc[j * pitch + c];
+          if (c < H) part[j * sums_pitch + c] = acc[j * sums_pitch + c];
         }
   }
 }
@@ -338,95 +366,104 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restri
   }
 }
 
-// The same for the up to four sums of the norms' gradient, which the outputs share.
+// The same for the sums of the norms' gradient, one per row of blocks, with the factors of
+// the outputs that they go into.
 __global__ void __launch_bounds__(1024) norm_sums_kernel(NormArgs a, NormSums out) {
-  __shared__ float s[4][32][33];
+  __shared__ float s[32][33];
   dep_wait();
   dep_launch();
   const int c = blockIdx.x * 32 + threadIdx.x;
   const size_t pitch = (a.H + EPT - 1) / EPT * EPT;
-  for (int j = 0; j < a.nacc; ++j) {
-    const float* p = a.partials + j * pitch + c;
+  auto total = [&](int j) {
     float v = 0.0f;
     if (c < a.H) {
-#pragma unroll 4
+      const float* p = a.partials + j * pitch + c;
+#pragma unroll 8
       for (int i = threadIdx.y; i < a.blocks; i += 32) v += p[static_cast<size_t>(i) * a.nacc * pitch];
     }
-    s[j][threadIdx.y][threadIdx.x] = v;
-  }
-  __syncthreads();
-  // row j of the threads adds up sum j
-  if (threadIdx.y < a.nacc) {
+    __syncthreads();
+    s[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
     float sum = 0.0f;
+    if (threadIdx.y == 0)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += s[threadIdx.y][i][threadIdx.x];
-    s[threadIdx.y][0][threadIdx.x] = sum;
-  }
-  __syncthreads();
+      for (int i = 0; i < 32; ++i) sum += s[i][threadIdx.x];
+    return sum;
+  };
+  const int j = blockIdx.y;
+  const float sum = total(j);
+  const float other = j == a.acc_post1 && out.dgate && a.acc_post0 >= 0 ? total(a.acc_post0) : 0.0f;
   if (threadIdx.y != 0 || c >= a.H) return;
-  auto total = [&](int j) { return j >= 0 ? s[j][0][threadIdx.x] : 0.0f; };
   auto value = [&](const void* v, float none) { return v ? load_one(v, a.w_dtype, c) : none; };
-  const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL;
-  const float g = gate_c ? value(a.gate, 1.0f) : 1.0f;
-  if (out.dw_post) out.dw_post[c] = g * total(a.acc_post1);
-  if (out.db_post) out.db_post[c] = g * total(a.acc_post0);
-  if (out.dw_pre) out.dw_pre[c] = total(a.acc_pre1);
-  if (out.db_pre) out.db_pre[c] = total(a.acc_pre0);
-  if (out.dgate) out.dgate[c] = value(a.w_post, 1.0f) * total(a.acc_post1) + value(a.b_post, 0.0f) * total(a.acc_post0);
+  const float g = a.gate_kind == MOE_GATE_CHANNEL ? load_one(a.gate, a.w_dtype, c) : 1.0f;
+  if (j == a.acc_post1) {
+    if (out.dw_post) out.dw_post[c] = g * sum;
+    if (out.dgate) out.dgate[c] = value(a.w_post, 1.0f) * sum + value(a.b_post, 0.0f) * other;
+  }
+  if (j == a.acc_post0 && out.db_post) out.db_post[c] = g * sum;
+  if (j == a.acc_pre1) out.dw_pre[c] = sum;
+  if (j == a.acc_pre0) out.db_pre[c] = sum;
 }
 
 // At most as many blocks as the registers of a 152-SM part hold (a pure function of
 // the problem: the workspace has room for the sums of each).
 inline int most_blocks_per_sm(int H) {
-  const int n = min_blocks(256) * 256 / norm_threads(H);
+  const int n = 512 / norm_threads(H);
   return n > 16 ? 16 : n < 1 ? 1 : n;
 }
 
 constexpr size_t kSmemMax = 224 * 1024;  // of one block's dynamic shared memory
 constexpr size_t kSmemSm = 228 * 1024;   // of an SM; a block takes 1 KB of its own and 1 KB static
 
-template <typename HT, typename OT, Access A, int RUNS, int MAXT>
+template <typename HT, typename OT, Access A, int MAXT, bool ZERO>
 cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
   static const cudaError_t attr =
-      cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, RUNS, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, MAXT, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemMax));
   if (attr != cudaSuccess) return attr;
-  const size_t pitch = static_cast<size_t>((a.H + EPT - 1) / EPT * EPT);
-  constexpr bool HOLD = A != PLAIN && MAXT <= 512;
-  const size_t sums = HOLD ? 0 : a.nacc * pitch * sizeof(float);
-  int per_sm = most_blocks_per_sm(a.H);
-  size_t ring = 0;
+  const size_t pitch = slot_pitch<A>(a.H, threads);
+  int per_sm = min_blocks(MAXT, ZERO) * MAXT / threads;
+  if (per_sm > most_blocks_per_sm(a.H)) per_sm = most_blocks_per_sm(a.H);
+  size_t smem = 0;
   a.depth = 0;
   if (A != PLAIN) {
-    // as many rows as fit with the resident blocks, up to four: two thirds of them on
-    // their way keep the memory busy
+    // a row that is worked on and, where they fit with the resident blocks, one or two
+    // on their way; 128 KB at most for one row, beside 64 KB of factors
     const size_t row = pitch * (sizeof(OT) + (a.dh_out ? sizeof(HT) : 0) + (a.pre ? sizeof(HT) + sizeof(OT) : 0));
-    a.depth = 4;
-    while (a.depth > 1 && (a.depth * row + sums + 2048) * per_sm > kSmemSm) --a.depth;
-    ring = a.depth * row;
+    const size_t factors = 2 * pitch * sizeof(float);
+    a.depth = 3;
+    auto fits = [&](size_t bytes, int blocks) { return bytes <= kSmemMax && (bytes + 2048) * blocks <= kSmemSm; };
+    while (a.depth > 1 && !fits(a.depth * row + factors, per_sm)) --a.depth;
+    smem = a.depth * row + factors;
+    while (per_sm > 1 && (smem + 2048) * per_sm > kSmemSm) --per_sm;
+  } else {
+    smem = a.nacc * pitch * sizeof(float);
+    a.acc_in_smem = smem <= kSmemMax;  // else the sums are kept in the workspace itself
+    if (!a.acc_in_smem) smem = 0;
+    while (per_sm > 1 && (smem + 2048) * per_sm > kSmemSm) --per_sm;
   }
-  a.acc_in_smem = ring + sums <= kSmemMax;  // else the sums are kept in the workspace itself
-  const size_t smem = ring + (a.acc_in_smem ? sums : 0);
-  const int fits = static_cast<int>(kSmemSm / (smem + 2048));
-  if (fits < per_sm) per_sm = fits;
   a.blocks = a.T < 152 * per_sm ? a.T : 152 * per_sm;
-  return launch_dependent(norm_backward_kernel<HT, OT, A, RUNS, MAXT>, dim3(a.blocks), dim3(threads), smem, s, a);
+  return launch_dependent(norm_backward_kernel<HT, OT, A, MAXT, ZERO>, dim3(a.blocks), dim3(threads), smem, s, a);
 }
 
 template <typename HT, typename OT, Access A>
 cudaError_t backward_ring(NormArgs& a, int threads, cudaStream_t s) {
-  if (threads <= 256) return backward_of<HT, OT, A, 1, 256>(a, threads, s);
-  if (threads <= 512) return backward_of<HT, OT, A, 1, 512>(a, threads, s);
-  return backward_of<HT, OT, A, 1, 1024>(a, threads, s);
+  if (a.acc_post0 >= 0 || a.acc_pre0 >= 0) {
+    if (threads <= 128) return backward_of<HT, OT, A, 128, true>(a, threads, s);
+    if (threads <= 256) return backward_of<HT, OT, A, 256, true>(a, threads, s);
+    return backward_of<HT, OT, A, 512, true>(a, threads, s);
+  }
+  if (threads <= 128) return backward_of<HT, OT, A, 128, false>(a, threads, s);
+  if (threads <= 256) return backward_of<HT, OT, A, 256, false>(a, threads, s);
+  return backward_of<HT, OT, A, 512, false>(a, threads, s);
 }
 
 }  // namespace
 }  // namespace norms
 
 size_t norm_partials_bytes(int T, int H) {
-  const size_t pitch = static_cast<size_t>((H + norms::EPT - 1) / norms::EPT * norms::EPT);
   const int most = 152 * norms::most_blocks_per_sm(H);
-  return static_cast<size_t>(T < most ? T : most) * 4 * pitch * sizeof(float);
+  return static_cast<size_t>(T < most ? T : most) * 4 * norms::norm_pitch(H) * sizeof(float);
 }
 
 cudaError_t launch_norm_backward(const NormArgs& args, const NormSums& out, cudaStream_t s) {
@@ -442,8 +479,8 @@ cudaError_t launch_norm_backward(const NormArgs& args, const NormSums& out, cuda
   const int pair = a.h_dtype * 3 + a.o_dtype;
   stage_begin("norm_backward", s);
   cudaError_t err;
-  if (a.H > threads * EPT) {
-    err = backward_of<float, float, PLAIN, 2, 1024>(a, threads, s);
+  if (threads > 512) {
+    err = backward_of<float, float, PLAIN, 1024, true>(a, threads, s);
   } else if (a.vec) {
     switch (pair) {
       case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32: err = backward_ring<float, float, VEC16>(a, threads, s); break;
@@ -456,15 +493,13 @@ cudaError_t launch_norm_backward(const NormArgs& args, const NormSums& out, cuda
     }
   } else if (pair == MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32) {
     err = backward_ring<float, float, WORD4>(a, threads, s);
-  } else if (threads <= 512) {
-    err = backward_of<float, float, PLAIN, 1, 512>(a, threads, s);
   } else {
-    err = backward_of<float, float, PLAIN, 1, 1024>(a, threads, s);
+    err = backward_of<float, float, PLAIN, 512, true>(a, threads, s);
   }
   stage_end(s);
   if (err == cudaSuccess && a.nacc > 0) {
     stage_begin("column_sums", s);
-    err = launch_dependent(norm_sums_kernel, dim3((a.H + 31) / 32), dim3(32, 32), 0, s, a, out);
+    err = launch_dependent(norm_sums_kernel, dim3((a.H + 31) / 32, a.nacc), dim3(32, 32), 0, s, a, out);
     stage_end(s);
   }
   return err;

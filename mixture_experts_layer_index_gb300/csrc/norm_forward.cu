@@ -12,28 +12,35 @@ namespace moe {
 namespace norms {
 namespace {
 
-// HOLD: the per-column factors (of up to 4096 columns) stay in registers, alpha and a
-// per-column gate folded into the post norm's.
-constexpr int min_blocks(int maxt) { return maxt <= 256 ? 3 : 1; }
+// Blocks per SM: 64 registers for up to 8192 columns.
+constexpr int min_blocks(int maxt) { return maxt <= 512 ? 1024 / maxt : 1; }
 
-template <typename HT, typename OT, Access A, int RUNS, int MAXT>
+template <typename HT, typename OT, Access A, int MAXT>
 __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(NormArgs a) {
-  constexpr bool HOLD = A != PLAIN && MAXT <= 512;
-  __shared__ __align__(16) float s_sum[2][1][MAXT / 32];
+  constexpr bool RING = A != PLAIN;
+  using Sum = BlockSum<1, MAXT>;
+  __shared__ __align__(16) float s_sum[2][1][Sum::W];
   extern __shared__ __align__(16) uint8_t s_ring[];
-  static_assert(A == PLAIN || RUNS == 1, "a ring holds one run per thread");
   const int H = a.H;
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const int pitch = (H + EPT - 1) / EPT * EPT;
+  const int pitch = slot_pitch<A>(H, blockDim.x);
+  // ring | factors of the post and of the pre norm, each column with its thread
   HT* ring_h = reinterpret_cast<HT*>(s_ring);
   OT* ring_o = reinterpret_cast<OT*>(ring_h + a.depth * pitch);
-  for (int i = threadIdx.x; i < 2 * (MAXT / 32); i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+  float* s_post = reinterpret_cast<float*>(ring_o + a.depth * pitch);
+  float* s_pre = s_post + pitch;
+  for (int i = threadIdx.x; i < 2 * Sum::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
   __syncthreads();
-  BlockSum<1, MAXT> block_sum{s_sum, 0};
+  Sum block_sum{s_sum, 0};
   dep_wait();
   dep_launch();
 
+  if (A == WORD4)
+    for (int d = 0; d < a.depth; ++d) {
+      clear_slot<HT, A>(ring_h + d * pitch, H);
+      clear_slot<OT, A>(ring_o + d * pitch, H);
+    }
   auto fetch = [&](int t, int slot) {
     if (t < a.T) {
       copy_in<OT, A>(ring_o + slot * pitch, a.o, static_cast<size_t>(t) * a.ld_o, H);
@@ -42,7 +49,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
     cp_async_commit();
   };
   int slot = 0;
-  if (A != PLAIN)
+  if (RING)
     for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
 
   // factor of the normalised (or plain) o, and of the normalised h'
@@ -56,23 +63,28 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       for (int i = 0; i < EPT; ++i) f[i] *= g[i];
     }
   };
-  float f_post[EPT], f_pre[EPT];
-  if (HOLD) {
-    post_factor(f_post, 0);
-    load_columns<A>(f_pre, a.w_pre, a.w_dtype, 0, H, vec, 1.0f);
-  }
+  if (RING)
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      float f[EPT];
+      post_factor(f, r);
+      put_shared<A>(s_post, r, H, f);
+      load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+      put_shared<A>(s_pre, r, H, f);
+    }
 
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
     float v[RUNS][EPT];
-    if constexpr (A != PLAIN) {
+    if (RING) {
       const int ahead = slot + a.depth - 1;
       fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
-      copy_out<OT, A>(v[0], ring_o + slot * pitch, H);
-    } else {
+    }
 #pragma unroll
-      for (int r = 0; r < RUNS; ++r) load_row<A>(v[r], a.o, a.o_dtype, at_o, r, H, vec);
+    for (int r = 0; r < RUNS; ++r) {
+      if constexpr (RING) copy_out<OT, A>(v[r], ring_o + slot * pitch, r, H);
+      else load_row<A>(v[r], a.o, a.o_dtype, at_o, r, H, vec);
     }
 
     // takes the mean off v (layer norms) and returns 1 / std
@@ -107,9 +119,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float c[EPT];
-      if (!HOLD) post_factor(f_post, r);
+      if constexpr (RING) copy_out<float, A>(c, s_post, r, H);
+      else post_factor(c, r);
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) v[r][i] *= rs * f_post[i];
+      for (int i = 0; i < EPT; ++i) v[r][i] *= rs * c[i];
       if (a.b_post) {
         load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
         if (gate_c) {
@@ -126,7 +139,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
         for (int i = 0; i < EPT; ++i) v[r][i] *= c[i];
       }
-      if constexpr (A != PLAIN) copy_out<HT, A>(c, ring_h + slot * pitch, H);
+      if constexpr (RING) copy_out<HT, A>(c, ring_h + slot * pitch, r, H);
       else load_row<A>(c, a.h, a.h_dtype, at_h, r, H, vec);
 #pragma unroll
       for (int i = 0; i < EPT; ++i) v[r][i] = fmaf(a.beta, c[i], v[r][i]);
@@ -137,11 +150,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       const float rp = moments(a.pre);
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
-        if (!HOLD) load_columns<A>(f_pre, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+        float c[EPT];
+        if constexpr (RING) copy_out<float, A>(c, s_pre, r, H);
+        else load_columns<A>(c, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[r][i] *= rp * f_pre[i];
+        for (int i = 0; i < EPT; ++i) v[r][i] *= rp * c[i];
         if (a.b_pre) {
-          float c[EPT];
           load_columns<A>(c, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
 #pragma unroll
           for (int i = 0; i < EPT; ++i) v[r][i] += c[i];
@@ -153,28 +167,33 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
   }
 }
 
-template <typename HT, typename OT, Access A, int RUNS, int MAXT>
+template <typename HT, typename OT, Access A, int MAXT>
 cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
+  constexpr size_t kSmemMax = 224 * 1024;
+  // 64 registers a thread; at most 32 blocks on an SM
+  int per_sm = min_blocks(MAXT) * MAXT / threads;
+  if (per_sm > 32) per_sm = 32;
   size_t smem = 0;
   if (A != PLAIN) {
-    const size_t row = static_cast<size_t>((a.H + EPT - 1) / EPT * EPT) * (sizeof(HT) + sizeof(OT));
-    a.depth = 3;
-    smem = a.depth * row;  // at most 3 rows of 8192 fp32 pairs: 192 KB
-    static const cudaError_t attr = cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, RUNS, MAXT>,
-                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * 8192 * 8);
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemMax));
     if (attr != cudaSuccess) return attr;
+    const size_t pitch = slot_pitch<A>(a.H, threads), row = pitch * (sizeof(HT) + sizeof(OT)), factors = 2 * pitch * sizeof(float);
+    a.depth = 3;  // two rows on their way; one where shared memory has no room for them beside the resident blocks
+    if ((3 * row + factors + 2048) * per_sm > kSmemMax) a.depth = 2;
+    smem = a.depth * row + factors;  // at most 2 x 64 KB + 64 KB
+    while (per_sm > 1 && (smem + 2048) * per_sm > kSmemMax) --per_sm;
   }
-  const int per_sm = MAXT <= 256 ? min_blocks(MAXT) * 256 / threads : 1;  // resident blocks
-  const int cap = 152 * (per_sm > 32 ? 32 : per_sm);
-  return launch_dependent(norm_forward_kernel<HT, OT, A, RUNS, MAXT>, dim3(a.T < cap ? a.T : cap), dim3(threads), smem,
-                          s, a);
+  const int cap = 152 * per_sm;
+  return launch_dependent(norm_forward_kernel<HT, OT, A, MAXT>, dim3(a.T < cap ? a.T : cap), dim3(threads), smem, s, a);
 }
 
 template <typename HT, typename OT, Access A>
 cudaError_t forward_ring(const NormArgs& a, int threads, cudaStream_t s) {
-  if (threads <= 256) return forward_of<HT, OT, A, 1, 256>(a, threads, s);
-  if (threads <= 512) return forward_of<HT, OT, A, 1, 512>(a, threads, s);
-  return forward_of<HT, OT, A, 1, 1024>(a, threads, s);
+  if (threads <= 128) return forward_of<HT, OT, A, 128>(a, threads, s);
+  if (threads <= 256) return forward_of<HT, OT, A, 256>(a, threads, s);
+  return forward_of<HT, OT, A, 512>(a, threads, s);
 }
 
 }  // namespace
@@ -186,8 +205,8 @@ cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
   const int pair = a.h_dtype * 3 + a.o_dtype;
   stage_begin("norm_forward", s);
   cudaError_t err;
-  if (a.H > threads * EPT) {
-    err = forward_of<float, float, PLAIN, 2, 1024>(a, threads, s);
+  if (threads > 512) {
+    err = forward_of<float, float, PLAIN, 1024>(a, threads, s);
   } else if (a.vec) {
     switch (pair) {
       case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32: err = forward_ring<float, float, VEC16>(a, threads, s); break;
@@ -200,10 +219,8 @@ cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
     }
   } else if (pair == MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32) {
     err = forward_ring<float, float, WORD4>(a, threads, s);
-  } else if (threads <= 512) {
-    err = forward_of<float, float, PLAIN, 1, 512>(a, threads, s);
   } else {
-    err = forward_of<float, float, PLAIN, 1, 1024>(a, threads, s);
+    err = forward_of<float, float, PLAIN, 512>(a, threads, s);
   }
   stage_end(s);
   return err;
