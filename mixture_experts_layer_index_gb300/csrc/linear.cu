@@ -222,9 +222,7 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       acc = now;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t da = A_MN ? sw128_mnmajor_desc(a + kk * 2048) : sw128_kmajor_desc(a + kk * 32);
-        const uint64_t db = B_MN ? sw128_mnmajor_desc(b + kk * 2048) : sw128_kmajor_desc(b + kk * 32);
-        mma_f16(tmem + acc * BN, da, db, idesc, !(fresh && kk == 0));
+        mma_f16(tmem + acc * BN, OperandDesc<A_MN>::at(a, kk), OperandDesc<B_MN>::at(b, kk), idesc, !(fresh && kk == 0));
       }
       mma_commit(empty0 + 8 * s);
     }
@@ -406,8 +404,10 @@ __device__ __forceinline__ void load8(float (&v)[8], const void* p, int dtype, s
   }
 }
 
+// Four rows' loads are issued before the first is used.
 __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][256 + 8];
+  constexpr int AHEAD = 4;
   dep_wait();
   dep_launch();
   const int c = blockIdx.x * 256 + threadIdx.x * 8;
@@ -415,30 +415,57 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
   float sum[8] = {};
   if (n > 0) {
-    for (int m = m0 + threadIdx.y; m < m1; m += 8) {
-      float g[8], z[8];
-      load8(g, a.dy, a.dy_dtype, static_cast<size_t>(m) * a.ld_dy + c, n, a.vec);
-      if (a.act != MOE_ACT_NONE) load8(z, a.z, a.dtype, static_cast<size_t>(m) * a.N + c, n, a.vec);
+    for (int mb = m0 + threadIdx.y; mb < m1; mb += 8 * AHEAD) {
+      float g[AHEAD][8], z[AHEAD][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] *= a.alpha;
-        if (a.act != MOE_ACT_NONE) g[i] *= act_grad(z[i], a.act);
-        sum[i] += g[i];
-      }
-      if (a.dz) {  // rows of the workspace are padded to 8 values: a whole store even at the edge
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (a.dtype == MOE_DTYPE_BF16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(g[2 * i], g[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-          } else {
-            const __half2 b = __floats2half2_rn(g[2 * i], g[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-          }
+      for (int q = 0; q < AHEAD; ++q) {
+        const int m = mb + 8 * q;
+        if (m < m1) {
+          load8(g[q], a.dy, a.dy_dtype, static_cast<size_t>(m) * a.ld_dy + c, n, a.vec);
+          if (a.act != MOE_ACT_NONE) load8(z[q], a.z, a.dtype, static_cast<size_t>(m) * a.N + c, n, a.vec);
         }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) {
+        const int m = mb + 8 * q;
+        if (m >= m1) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[q][i] *= a.alpha;
+        switch (a.act) {
+          case MOE_ACT_NONE: break;
+          case MOE_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_RELU);
+            break;
+          case MOE_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_SILU);
+            break;
+          case MOE_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_GELU);
+            break;
+          default:
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_GELU_TANH);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += g[q][i];
+        if (a.dz) {  // rows of the workspace are padded to 8 values: a whole store even at the edge
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (a.dtype == MOE_DTYPE_BF16) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(g[q][2 * i], g[q][2 * i + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+              const __half2 b = __floats2half2_rn(g[q][2 * i], g[q][2 * i + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
   }

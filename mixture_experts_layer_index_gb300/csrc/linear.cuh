@@ -12,19 +12,21 @@ namespace lin {
 
 constexpr int BK = 64;  // values of the sum per stage: 128 bytes
 
-// Descriptor of an MN-major operand in the layout of TMA boxes of 64 values along MN
-// (128 bytes, 128-byte swizzle) x 64 along the sum: 8-row groups along the sum 1024
-// bytes apart (stride byte offset), the next 64 along MN one box = 8192 bytes on
-// (leading byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(8192u >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
+// Shared-memory descriptor of an operand in TMA boxes of 128-byte rows with the
+// 128-byte swizzle, and how it moves along the sum.  K-major: as sw128_kmajor_desc, 16
+// values of the sum are 32 bytes on.  MN-major: boxes of 64 values along MN x 64 along
+// the sum; 8-row groups along the sum 1024 bytes apart (stride byte offset), the next
+// 64 along MN one box = 8192 bytes on (leading byte offset); 16 values of the sum are
+// 2048 bytes on.  Only the address field changes, and it never carries out of its bits.
+template <bool MN>
+struct OperandDesc {
+  static constexpr uint64_t kFixed = (static_cast<uint64_t>(MN ? 8192u >> 4 : 1u) << 16) |
+                                     (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+  static constexpr uint32_t kStep = (MN ? 2048u : 32u) >> 4;
+  static __device__ __forceinline__ uint64_t at(uint32_t smem_addr, int kk) {
+    return kFixed | (((smem_addr & 0x3FFFFu) >> 4) + kk * kStep);
+  }
+};
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -36,12 +38,38 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // ------------------------------------------------------------------ activations
+// An epilogue has about as many instructions per output value as the tensor cores leave
+// time for, so the activations use the hardware's exponential and reciprocal
+// (__expf, __fdividef: relative errors of a few 2^-23 over the range that matters) and,
+// for erf, the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook of
+// Mathematical Functions: absolute error at most 1.5e-7.
+
+// 1 / (1 + e^-z)
+__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// The upper tail of the normal distribution, (1 - erf(x / sqrt 2)) / 2 for x >= 0, and e = e^(-x^2 / 2).
+__device__ __forceinline__ float normal_tail(float x, float& e) {
+  const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, x, 1.0f));
+  e = __expf(-0.5f * x * x);
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  return 0.5f * p * t * e;
+}
+// 2 u of the tanh form: (1 + tanh u) / 2 = sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ float gelu_tanh_2u(float z) { return 1.59576912f * z * fmaf(0.044715f * z, z, 1.0f); }
+
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return fmaxf(z, 0.0f);
-    case MOE_ACT_SILU: return z / (1.0f + expf(-z));
-    case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MOE_ACT_GELU_TANH: return 0.5f * z * (1.0f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
+    case MOE_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
+    case MOE_ACT_GELU: {
+      float e;
+      const float tail = z * normal_tail(fabsf(z), e);
+      return z > 0.0f ? z - tail : tail;
+    }
+    case MOE_ACT_GELU_TANH: return z * fast_sigmoid(gelu_tanh_2u(z));
     default: return z;
   }
 }
@@ -49,13 +77,17 @@ __device__ __forceinline__ float act_grad(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
     case MOE_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
+      const float s = fast_sigmoid(z);
+      return s * fmaf(z, 1.0f - s, 1.0f);
     }
-    case MOE_ACT_GELU: return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
+    case MOE_ACT_GELU: {
+      float e;
+      const float tail = normal_tail(fabsf(z), e);
+      return fmaf(0.39894228f * z, e, z > 0.0f ? 1.0f - tail : tail);
+    }
     case MOE_ACT_GELU_TANH: {
-      const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-      return 0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * 0.79788456f * (1.0f + 0.134145f * z * z);
+      const float s = fast_sigmoid(gelu_tanh_2u(z));
+      return s * fmaf(z * (1.0f - s), 1.59576912f * fmaf(0.134145f * z, z, 1.0f), 1.0f);
     }
     default: return 1.0f;
   }

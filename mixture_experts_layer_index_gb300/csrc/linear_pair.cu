@@ -11,7 +11,7 @@
 // Persistent pairs walk over the tiles.  Rows r lie on the TMEM lanes, 128 per
 // block, 2 x 256 accumulator columns, so that the epilogue of one tile
 // overlaps the MMAs of the next.  Warps: 0 loads, 1 issues MMAs (even block), 2
-// owns TMEM, 4-11 run the epilogue (two warps per 32 lanes, 128 columns each): 32
+// owns TMEM, 4-19 run the epilogue (four warps per 32 lanes, 64 columns each): 32
 // columns at a time are loaded from TMEM, finished in fp32, rounded once, staged in
 // shared memory as a 128-byte-swizzled box of 32 rows and stored by TMA, which
 // clips the edges.
@@ -26,13 +26,15 @@ constexpr int HALF = 128;       // rows (and loaded columns) of one block
 constexpr int STAGES = 5;
 constexpr int OP_BYTES = HALF * BK * 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
 constexpr int BOX_BYTES = 32 * 128;            // 32 rows of 128 bytes
 constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
-// ring | two boxes per epilogue warp | barriers
+constexpr int EPI_COLS = TILE / (EPI_WARPS / 4);  // columns per epilogue warp
+static_assert(EPI_COLS == 64, "an epilogue warp fills one box of 16-bit values");
+// ring | one box per epilogue warp | barriers
 constexpr int BOX_OFFSET = STAGES * STAGE_BYTES;
-constexpr int BAR_OFFSET = BOX_OFFSET + EPI_WARPS * 2 * BOX_BYTES;
+constexpr int BAR_OFFSET = BOX_OFFSET + EPI_WARPS * BOX_BYTES;
 constexpr size_t SMEM_BYTES = 1024 + BAR_OFFSET + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one block");
 
@@ -78,7 +80,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
-__device__ __forceinline__ void bulk_wait_group_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 // Tile t's first row and column: groups of 8 row tiles, column by column within a
 // group, so that the pairs in flight share both operands in L2.
@@ -90,59 +91,65 @@ __device__ __forceinline__ void tile_origin(const PairParams& p, int t, int& r0,
   r0 = (group * GR + in_group % rows_here) * TILE;
 }
 
-// 32 values (columns c.. of one row) as one row of a swizzled box: 16-byte chunk j of
-// row `lane` sits at chunk j ^ (lane & 7).  16-bit types fill half a box row.
-__device__ __forceinline__ void put_box(uint8_t* box, int lane, int half, int dtype, const float (&v)[32]) {
+// 16 values (columns c.. of one row) into row `lane` of a swizzled box: 16-byte chunk j of a
+// row sits at chunk j ^ (lane & 7).  `part`: which 16 of the box's columns.
+__device__ __forceinline__ void put_box(uint8_t* box, int lane, int part, int dtype, const float (&v)[16]) {
   uint8_t* row = box + lane * 128;
   if (dtype == MOE_DTYPE_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      *reinterpret_cast<float4*>(row + ((j ^ (lane & 7)) << 4)) =
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(row + (((part * 4 + j) ^ (lane & 7)) << 4)) =
           make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       uint32_t w[4];
+      if (dtype == MOE_DTYPE_BF16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (dtype == MOE_DTYPE_BF16) {
+        for (int i = 0; i < 4; ++i) {
           const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
           w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        } else {
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const __half2 b = __floats2half2_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
           w[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
       }
-      *reinterpret_cast<uint4*>(row + (((half * 4 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(row + (((part * 2 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
-// v[i] = p[at + i], 32 values of which `n` exist; `wide`: p + at is 16-byte aligned.
-__device__ __forceinline__ void load32(float (&v)[32], const void* p, int dtype, size_t at, int n, bool wide) {
-  if (n < 32 || !wide) {
+// v[i] += p[at + i], 16 values of which `n` exist; `wide`: p + at is 16-byte aligned.
+__device__ __forceinline__ void add16(float (&v)[16], const void* p, int dtype, size_t at, int n, bool wide) {
+  if (n < 16 || !wide) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = i < n ? load_as_f32(p, dtype, at + i) : 0.0f;
+    for (int i = 0; i < 16; ++i)
+      if (i < n) v[i] += load_as_f32(p, dtype, at + i);
   } else if (dtype == MOE_DTYPE_F32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    float4 f[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 f = q[j];
-      v[4 * j] = f.x; v[4 * j + 1] = f.y; v[4 * j + 2] = f.z; v[4 * j + 3] = f.w;
-    }
-  } else {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    for (int j = 0; j < 4; ++j) f[j] = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[j];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint4 raw = q[j];
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      v[4 * j] += f[j].x; v[4 * j + 1] += f[j].y; v[4 * j + 2] += f[j].z; v[4 * j + 3] += f[j].w;
+    }
+  } else {
+    uint4 raw[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) raw[j] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at)[j];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 f = dtype == MOE_DTYPE_BF16
                              ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
                              : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[8 * j + 2 * i] = f.x;
-        v[8 * j + 2 * i + 1] = f.y;
+        v[8 * j + 2 * i] += f.x;
+        v[8 * j + 2 * i + 1] += f.y;
       }
     }
   }
@@ -199,25 +206,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int npairs = static_cast<int>(gridDim.x) >> 1, pair = static_cast<int>(blockIdx.x) >> 1;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t lead_full0 = map_rank(full0, 0);
-      uint32_t stage = 0, phase = 0;
-      int issued = 0;
-      bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
-        int r0, c0;
-        tile_origin(p, t, r0, c0);
-        r0 += rank * HALF;
-        c0 += rank * HALF;
-        for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, p.hdr, 0x610000u)) {
-            ok = false;
-            break;
-          }
+    // Like the MMA warp: uniform control, one lane issues, the next slot's barrier is
+    // looked at ahead.
+    const bool leader = elect_one();
+    const uint32_t lead_full0 = map_rank(full0, 0), ring = smem_u32(smem);
+    uint32_t stage = 0, phase = 1;
+    int issued = 0;
+    bool ok = true;
+    bool ready = mbar_try_wait(empty0, phase);
+    for (int t = pair; t < total && ok; t += npairs) {
+      int r0, c0;
+      tile_origin(p, t, r0, c0);
+      r0 += rank * HALF;
+      c0 += rank * HALF;
+      for (int kb = 0; kb < p.nk; ++kb) {
+        if (!ready && !mbar_wait(empty0 + 8 * stage, phase, abort_flag, p.hdr, 0x610000u)) {
+          ok = false;
+          break;
+        }
+        const uint32_t full = full0 + 8 * stage, bar = lead_full0 + 8 * stage;
+        const uint32_t a = ring + stage * STAGE_BYTES, b = a + OP_BYTES;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (leader) {
           // the even block's barrier expects the bytes of both blocks
-          if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * stage, 2 * STAGE_BYTES);
-          const uint32_t bar = lead_full0 + 8 * stage;
-          const uint32_t a = smem_u32(smem + stage * STAGE_BYTES), b = a + OP_BYTES;
+          if (rank == 0) mbar_arrive_expect_tx(full, 2 * STAGE_BYTES);
           const int k = kb * BK;
           if (A_MN) {
             tma_load_2d_pair(a, &tmA, r0, k, bar);
@@ -231,146 +246,158 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           } else {
             tma_load_2d_pair(b, &tmB, k, c0, bar);
           }
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-      }
-      if (!ok && rank == 0) {  // let the copies already issued land before shared memory is given up
-        for (int i = 0; i < min(issued, STAGES); ++i) {
-          stage = (stage + STAGES - 1) % STAGES;
-          if (stage == STAGES - 1) phase ^= 1;
-          mbar_wait_quiet(full0 + 8 * stage, phase, 50000000ull);
-        }
+        __syncwarp();
+        ++issued;
+        ready = mbar_try_wait(empty0 + 8 * stage, phase);
       }
     }
+    if (!ok && rank == 0 && leader) {  // let the copies already issued land before shared memory is given up
+      for (int i = 0; i < min(issued, STAGES); ++i) {
+        stage = (stage + STAGES - 1) % STAGES;
+        if (stage == STAGES - 1) phase ^= 1;
+        mbar_wait_quiet(full0 + 8 * stage, phase ^ 1, 50000000ull);
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    // The whole warp walks the loop, so that addresses and descriptors stay in uniform
+    // registers; one lane issues.  The next stage's barrier is looked at before this
+    // stage's MMAs are issued: the look takes longer than an MMA.
+    if (rank == 0) {
+      const bool leader = elect_one();
       const uint32_t idesc =
           make_idesc(p.type, p.type, TILE, TILE) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+      const uint32_t ring = smem_u32(smem);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (int t = pair; t < total && ok; t += npairs) {
         if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.hdr, 0x620000u)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * TILE;
+        bool ready = mbar_try_wait(full0 + 8 * stage, phase);
         for (int kb = 0; kb < p.nk; ++kb) {
-          if (!mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x630000u)) {
+          if (!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x630000u)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + stage * STAGE_BYTES), b = a + OP_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t da = A_MN ? sw128_mnmajor_desc(a + kk * 2048) : sw128_kmajor_desc(a + kk * 32);
-            const uint64_t db = B_MN ? sw128_mnmajor_desc(b + kk * 2048) : sw128_kmajor_desc(b + kk * 32);
-            mma_f16_pair(d, da, db, idesc, (kb | kk) != 0);
-          }
-          mma_commit_pair(empty0 + 8 * stage);
+          const uint32_t a = ring + stage * STAGE_BYTES, empty = empty0 + 8 * stage;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
+          ready = kb + 1 < p.nk && mbar_try_wait(full0 + 8 * stage, phase);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_pair(d, OperandDesc<A_MN>::at(a, kk), OperandDesc<B_MN>::at(a + OP_BYTES, kk), idesc,
+                           (kb | kk) != 0);
+            mma_commit_pair(empty);
+          }
+          __syncwarp();
         }
         if (!ok) break;
-        mma_commit_pair(tfull0 + 8 * acc);
+        if (leader) mma_commit_pair(tfull0 + 8 * acc);
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
-      mma_commit_pair(mma_done);
-      mbar_wait_quiet(mma_done, 0, 1000000000ull);
+      if (leader) {
+        mma_commit_pair(mma_done);
+        mbar_wait_quiet(mma_done, 0, 1000000000ull);
+      }
     }
     __syncwarp();
   } else if (warp >= 4) {
     const int e = warp - 4, q = warp & 3, h = e >> 2;
-    uint8_t* box0 = smem + BOX_OFFSET + e * 2 * BOX_BYTES;
+    uint8_t* box = smem + BOX_OFFSET + e * BOX_BYTES;
     const uint32_t lead_tempty0 = map_rank(tempty0, 0);
     const Epilogue& ep = p.ep;
     const bool wide = ep.out_dtype == MOE_DTYPE_F32;
     const bool bias_wide = reinterpret_cast<uintptr_t>(ep.bias) % 16 == 0;
     const bool residual_wide = reinterpret_cast<uintptr_t>(ep.residual) % 16 == 0;
     uint32_t acc = 0, acc_phase = 0;
+    // the box may be written again once the store that read it has done so
+    auto box_free = [&]() {
+      if (lane == 0) bulk_wait_group_read0();
+      __syncwarp();
+    };
     for (int t = pair; t < total; t += npairs) {
       int r0, c0;
       tile_origin(p, t, r0, c0);
       r0 += rank * HALF + q * 32;  // this warp's rows and columns
-      c0 += h * HALF;
+      c0 += h * EPI_COLS;
       int good = 1;
       if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x640000u);
       good = __shfl_sync(0xffffffffu, good, 0);
       if (!good) break;
       tc_fence_after();
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * HALF;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * EPI_COLS;
       const bool row_in = r0 + lane < p.R;
+      // sum + bias of 16 columns from c0 + j * 16
+      auto load_z = [&](int j, float(&v)[16]) {
+        tmem_ld16(tb + j * 16, v);
+        tmem_ld_wait_regs16(v);
+        if (ep.bias) add16(v, ep.bias, ep.bias_dtype, c0 + j * 16, p.C - c0 - j * 16, bias_wide);  // same for every lane
+      };
+      auto store_box = [&](const CUtensorMap* map, int c) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (r0 < p.R && c < p.C) tma_store_2d(map, smem_u32(box), c, r0);
+          bulk_commit_group();
+        }
+      };
+      // z goes out first: its store reads the box while the activation is computed (the
+      // accumulator is read a second time instead of being kept)
+      if (ep.z) {
+        box_free();
+#pragma unroll 2
+        for (int j = 0; j < 4; ++j) {
+          float v[16];
+          load_z(j, v);
+          put_box(box, lane, j, ep.z_dtype, v);
+        }
+        store_box(&tmZ, c0);
+      }
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
-        const int c = c0 + j * 32;
-        float v[32], b[32];
-        tmem_ld32(tb + j * 32, v);
-        if (ep.bias) load32(b, ep.bias, ep.bias_dtype, c, p.C - c, bias_wide);  // the same for every lane
-        tmem_ld_wait_regs(v);
+        const int c = c0 + j * 16;
+        float v[16];
+        load_z(j, v);
         if (j == 3) {  // this warp's accumulator columns are read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
         }
-        if (ep.bias) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += b[i];
-        }
-        const int half = j & 1;
-        // boxes: y in the first, z (or the next fp32 y) in the second; a box is written
-        // only after the store that last read it has done so
-        uint8_t* ybox = box0 + (wide && !ep.z ? half * BOX_BYTES : 0);
-        if (wide || half == 0) {
-          if (lane == 0) {
-            if (wide && !ep.z) bulk_wait_group_read1();
-            else bulk_wait_group_read0();
-          }
-          __syncwarp();
-        }
-        if (ep.z) put_box(box0 + BOX_BYTES, lane, half, ep.z_dtype, v);
         switch (ep.act) {
           case MOE_ACT_NONE: break;
           case MOE_ACT_RELU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
+            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
             break;
           case MOE_ACT_SILU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_SILU);
+            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_SILU);
             break;
           case MOE_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
+            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
             break;
           default:
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], MOE_ACT_GELU_TANH);
+            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_GELU_TANH);
         }
+        if (ep.alpha != 1.0f) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= ep.alpha;
-        if (ep.residual && row_in) {  // its rows are aligned as y's, which TMA stores
-          load32(b, ep.residual, ep.out_dtype, static_cast<size_t>(r0 + lane) * ep.ld_y + c, p.C - c, residual_wide);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += b[i];
+          for (int i = 0; i < 16; ++i) v[i] *= ep.alpha;
         }
-        put_box(ybox, lane, wide ? 0 : half, ep.out_dtype, v);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0 && r0 < p.R) {
-          if (wide) {
-            if (c < p.C) tma_store_2d(&tmY, smem_u32(ybox), c, r0);
-          } else if (half && c - 32 < p.C) {
-            tma_store_2d(&tmY, smem_u32(ybox), c - 32, r0);
-          }
-          if (ep.z && half && c - 32 < p.C) tma_store_2d(&tmZ, smem_u32(box0 + BOX_BYTES), c - 32, r0);
-        }
-        if (lane == 0 && (wide || half)) bulk_commit_group();
-        __syncwarp();
+        if (ep.residual && row_in)  // its rows are aligned as y's, which TMA stores
+          add16(v, ep.residual, ep.out_dtype, static_cast<size_t>(r0 + lane) * ep.ld_y + c, p.C - c, residual_wide);
+        if (j == 0 || (wide && j == 2)) box_free();
+        put_box(box, lane, wide ? j & 1 : j, ep.out_dtype, v);
+        if (j == 3 || (wide && j == 1)) store_box(&tmY, wide ? c - 16 : c0);
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
