@@ -530,7 +530,7 @@ moe_status moe_read_device_status(const void* ws, moe_stream_t stream);
  * scatter_gather, gateup_gemm, quant_h, down_gemm, combine (grouped path);
  * rd_prep, rd_gateup, rd_reduce, rd_down, combine (route-direct path); scatter,
  * tile_map, header_reset; route_ex, route_backward, norm_forward, norm_backward,
- * linear, linear_dz, linear_dx, linear_dw, column_sums. */
+ * linear, linear_dz, linear_dx, linear_dw, linear_dx_dw, column_sums. */
 typedef struct {
   char name[32];
   double total_ms;

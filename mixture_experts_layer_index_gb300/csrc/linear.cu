@@ -28,16 +28,20 @@ constexpr int THREADS = 128;
 constexpr int MAX_SPLITS = 8;
 constexpr int A_BYTES = BM * BK * 2;
 
-// Stages: two blocks per SM up to BN = 128 (one loads while the other stores), one
-// block with a deep ring at BN = 256.
-__host__ __device__ constexpr int stages_of(int BN) { return BN <= 32 ? 5 : BN == 64 ? 4 : BN == 128 ? 3 : 4; }
+constexpr int MAX_STAGES = 12;
 __host__ __device__ constexpr int stage_bytes(int BN) { return A_BYTES + BN * BK * 2; }
-// 1 KB to align the ring, the barriers after it
-__host__ __device__ constexpr int smem_bytes(int BN) { return 1024 + stages_of(BN) * stage_bytes(BN) + 256; }
+// 1 KB to align the ring, 256 bytes of barriers before it
+__host__ __device__ constexpr int smem_bytes(int BN, int stages) { return 1024 + 256 + stages * stage_bytes(BN); }
+// Stages with `blocks` blocks on an SM (one loads while another stores): all that fit.
+constexpr int stages_of(int BN, int blocks) {
+  const int n = (228 * 1024 / blocks - 1024 - smem_bytes(BN, 0)) / stage_bytes(BN);
+  return n > MAX_STAGES ? MAX_STAGES : n;
+}
 
 struct Params {
   int C, R;        // output columns and rows
   int nk;          // stages of the whole sum
+  int stages;      // of the ring
   int splits;      // blocks per tile (cluster size)
   int nC, nR;      // tiles
   int nacc;        // accumulators that a block's part of the sum is spread over
@@ -132,18 +136,19 @@ template <int BN, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__ CUtensorMap tmA,
                                                          const __grid_constant__ CUtensorMap tmB, const Params p) {
   static_assert(!B_MN || BN >= 64, "an MN-major box is 64 wide");
-  constexpr int STAGES = stages_of(BN), STAGE = stage_bytes(BN);
+  constexpr int STAGE = stage_bytes(BN);
   constexpr int CH = BN < 32 ? BN : 32;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[2 * MAX_STAGES + 1];
+  __shared__ uint32_t tmem_slot[1];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES), done = smem_u32(bars + 2 * STAGES);
+  const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + MAX_STAGES), done = smem_u32(bars + 2 * MAX_STAGES);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
@@ -180,53 +185,72 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   const int n = kb1 - kb0;
   const int nacc = min(p.nacc, n);  // accumulators that this block fills
 
-  if (warp == 0 && lane == 0) {
+  // Both roles: uniform control flow (addresses and descriptors stay in uniform
+  // registers), one lane issues, the next barrier is looked at ahead.
+  if (warp == 0) {
+    const bool leader = elect_one();
+    const uint32_t ring = smem_u32(smem);
+    uint32_t stage = 0, phase = 1;
     int issued = 0;
-    bool ok = true;
+    bool ready = true;  // the ring starts empty
     for (; issued < n; ++issued) {
-      const int s = issued % STAGES;
-      if (!mbar_wait(empty0 + 8 * s, ((issued / STAGES) & 1) ^ 1, abort_flag, p.hdr, 0x510000u)) {
-        ok = false;
-        break;
+      if (!ready && !mbar_wait(empty0 + 8 * stage, phase, abort_flag, p.hdr, 0x510000u)) break;
+      const uint32_t full = full0 + 8 * stage, a = ring + stage * STAGE, b = a + A_BYTES;
+      if (++stage == static_cast<uint32_t>(p.stages)) {
+        stage = 0;
+        phase ^= 1;
       }
-      const uint32_t full = full0 + 8 * s, a = smem_u32(smem + s * STAGE), b = a + A_BYTES;
-      const int k = (kb0 + issued) * BK;
-      mbar_arrive_expect_tx(full, STAGE);
-      if (A_MN) {
-        tma_load_2d(a, &tmA, c0, k, full);
-        tma_load_2d(a + A_BYTES / 2, &tmA, c0 + 64, k, full);
-      } else {
-        tma_load_2d(a, &tmA, k, c0, full);
-      }
-      if (B_MN) {
+      if (leader) {
+        const int k = (kb0 + issued) * BK;
+        mbar_arrive_expect_tx(full, STAGE);
+        if (A_MN) {
+          tma_load_2d(a, &tmA, c0, k, full);
+          tma_load_2d(a + A_BYTES / 2, &tmA, c0 + 64, k, full);
+        } else {
+          tma_load_2d(a, &tmA, k, c0, full);
+        }
+        if (B_MN) {
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &tmB, r0 + j * 64, k, full);
-      } else {
-        tma_load_2d(b, &tmB, k, r0, full);
+          for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &tmB, r0 + j * 64, k, full);
+        } else {
+          tma_load_2d(b, &tmB, k, r0, full);
+        }
       }
+      __syncwarp();
+      ready = mbar_try_wait(empty0 + 8 * stage, phase);
     }
-    if (!ok)  // let the copies already issued land before shared memory is given up
-      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-        mbar_wait_quiet(full0 + 8 * (i % STAGES), (i / STAGES) & 1, 50000000ull);
-  } else if (warp == 1 && lane == 0) {
+    if (issued < n && leader)  // let the copies already issued land before shared memory is given up
+      for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+        mbar_wait_quiet(full0 + 8 * (i % p.stages), (i / p.stages) & 1, 50000000ull);
+  } else if (warp == 1) {
+    const bool leader = elect_one();
     const uint32_t idesc = make_idesc(p.type, p.type, BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-    // kind::f16 codes: 0 = f16, 1 = bf16
+    const uint32_t ring = smem_u32(smem);
+    uint32_t stage = 0, phase = 0;
     int acc = -1;
+    bool ready = mbar_try_wait(full0, 0);
     for (int i = 0; i < n; ++i) {
-      const int s = i % STAGES;
-      if (!mbar_wait(full0 + 8 * s, (i / STAGES) & 1, abort_flag, p.hdr, 0x520000u)) break;
+      if (!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x520000u)) break;
       tc_fence_after();
-      const uint32_t a = smem_u32(smem + s * STAGE), b = a + A_BYTES;
-      const int now = i * nacc / n;
+      const uint32_t a = ring + stage * STAGE, b = a + A_BYTES, empty = empty0 + 8 * stage;
+      if (++stage == static_cast<uint32_t>(p.stages)) {
+        stage = 0;
+        phase ^= 1;
+      }
+      ready = i + 1 < n && mbar_try_wait(full0 + 8 * stage, phase);
+      const int now = nacc == 1 ? 0 : i * nacc / n;
       const bool fresh = now != acc;
       acc = now;
+      if (leader) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        mma_f16(tmem + acc * BN, OperandDesc<A_MN>::at(a, kk), OperandDesc<B_MN>::at(b, kk), idesc, !(fresh && kk == 0));
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16(tmem + acc * BN, OperandDesc<A_MN>::at(a, kk), OperandDesc<B_MN>::at(b, kk), idesc,
+                  !(fresh && kk == 0));
+        mma_commit(empty);
       }
-      mma_commit(empty0 + 8 * s);
+      __syncwarp();
     }
-    mma_commit(done);
+    if (leader) mma_commit(done);
   }
   __syncwarp();
   if (lane == 0) mbar_wait(done, 0, abort_flag, p.hdr, 0x530000u);
@@ -270,18 +294,28 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
     }
     cluster_sync_all();
     if (good) {
-      const int per = BN / p.splits;  // rows that this block adds up and finishes
+      // its share of the rows, RB at a time: all ranks' values of RB rows are on their way
+      // before the first is added
+      const int per = BN / p.splits;
+      constexpr int RB = 8;
       const uint32_t mine = smem_u32(part) + cl * 4;
-      constexpr int RB = 2;  // rows at a time: with up to 8 ranks, 16 loads in flight
-      for (int j = rank * per; j < (rank + 1) * per; j += RB) {
-        if (r0 + j >= p.R) break;
+      const int end = min((rank + 1) * per, p.R - r0);
+      for (int j = rank * per; j < end; j += RB) {
+        const int cnt = min(RB, end - j);
+        float u[MAX_SPLITS][RB];
+#pragma unroll
+        for (int q = 0; q < MAX_SPLITS; ++q)
+          if (q < p.splits)
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+              if (i < cnt) u[q][i] = ld_cluster_f32(mine + (j + i) * (BM * 4), q);
         float v[RB] = {};
 #pragma unroll
         for (int q = 0; q < MAX_SPLITS; ++q)
           if (q < p.splits)
 #pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] += ld_cluster_f32(mine + (j + i) * (BM * 4), q);
-        finish<RB>(p, v, r0 + j, min(RB, p.R - r0 - j), c0 + cl);
+            for (int i = 0; i < RB; ++i) v[i] += u[q][i];
+        finish<RB>(p, v, r0 + j, cnt, c0 + cl);
       }
     }
     cluster_sync_all();  // no block leaves while another still reads its partial
@@ -300,11 +334,16 @@ cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
   if (!encode(&ta, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, A_MN ? 64 : BM) ||
       !encode(&tb, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, B_MN ? 64 : BN))
     return cudaErrorInvalidValue;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      linear_kernel<BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(linear_kernel<BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem_bytes(BN, stages_of(BN, 1)));
   if (attr != cudaSuccess) return attr;
   p.nC = (p.C + BM - 1) / BM;
   p.nR = (p.R + BN - 1) / BN;
+  // one block per SM where the grid leaves no second one: its ring takes all of shared
+  // memory (not in large clusters, which then no longer find enough free SMs together)
+  const long long blocks = static_cast<long long>(p.nC) * p.nR * p.splits;
+  p.stages = stages_of(BN, BN == 256 || (blocks <= 152 && p.splits <= 2) ? 1 : 2);
   int cols = 32;
   while (cols < BN * p.nacc) cols *= 2;
   p.tmem_cols = cols;
@@ -315,18 +354,60 @@ cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
   la[0].val.clusterDim.x = p.splits;
   la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.nC) * p.nR * p.splits);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cfg.dynamicSmemBytes = smem_bytes(BN, p.stages);
   cfg.stream = s;
   cfg.attrs = la;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, linear_kernel<BN, A_MN, B_MN>, ta, tb, p);
 }
 
-// Tile and split by the shape.
+// About how long a launch takes (us), for tiles of 128 x bn split over `splits` blocks.
+// Measured on GB300: 2.6 us of launch, set-up and drain; a block's stage takes 0.17 us
+// (bn = 16) to 0.20 us (128), 0.45 us at 256, or as long as the SM's blocks together need
+// for their operands at 143 GB/s per SM; each further wave adds 2 us and 0.04 us per row
+// for the epilogue that nothing overlaps; joining partials costs 1 us, 0.4 us per doubling and
+// 0.02 us per row.  Within 15% of the measured times of the shapes it was fitted to (8 x
+// 4096 x 4096 to 2048 x 2048 x 2048 and the gradient of a 128-column router over 16384
+// tokens), which is near enough to tell 17 us (bn = 64, 8 splits) from 54 us (128, 1).
+float tile_estimate(const Product& q, int bn, int splits) {
+  const long long nk = (q.K + BK - 1) / BK;
+  const long long blocks = static_cast<long long>((q.C + BM - 1) / BM) * ((q.R + bn - 1) / bn) * splits;
+  // a cluster's blocks lie in one group of SMs: clusters of 8 reach 128 of 152 SMs
+  const int occupancy = bn == 256 ? 1 : 2, sms = splits == 8 ? 128 : 152;
+  const long long waves = (blocks + sms * occupancy - 1) / (sms * occupancy);
+  const int together = blocks > sms ? occupancy : 1;
+  float stage = bn <= 32 ? 0.175f : bn <= 128 ? 0.20f : 0.45f;
+  const float load = together * stage_bytes(bn) / 143000.0f;
+  if (load > stage) stage = load;
+  float t = waves * static_cast<float>((nk + splits - 1) / splits) * stage;
+  const float memory = 2.0f * (static_cast<float>(q.R) + q.C) * q.K / 6.5e6f;
+  if (memory > t) t = memory;
+  t += 2.6f + 0.01f * bn + (waves - 1) * (2.0f + 0.04f * bn);
+  for (int s = splits; s > 1; s /= 2) t += 0.4f;
+  return splits > 1 ? t + 1.0f + 0.02f * bn : t;
+}
+
+struct Choice {
+  int bn, splits;
+  float us;
+};
+Choice choose_tile(const Product& q) {
+  const long long nk = (q.K + BK - 1) / BK;
+  Choice best{0, 1, 0.0f};
+  for (int bn = q.rows_mn ? 64 : 16; bn <= 256; bn *= 2) {
+    for (int splits = 1; splits <= MAX_SPLITS && (splits == 1 || nk / splits >= 2); splits *= 2) {
+      const float us = tile_estimate(q, bn, splits);
+      if (best.bn == 0 || us < best.us) best = {bn, splits, us};
+    }
+    if (bn >= q.R) break;
+  }
+  return best;
+}
+
 template <bool A_MN, bool B_MN>
-cudaError_t launch_shape(const Product& q, cudaStream_t s) {
+cudaError_t launch_shape(const Product& q, const Choice& c, cudaStream_t s) {
   Params p{};
   p.C = q.C;
   p.R = q.R;
@@ -335,19 +416,12 @@ cudaError_t launch_shape(const Product& q, cudaStream_t s) {
   p.reset_status = q.reset_status;
   p.hdr = q.hdr;
   p.nk = (q.K + BK - 1) / BK;
-  int bn = p.R <= 16 ? 16 : p.R <= 32 ? 32 : p.R <= 64 ? 64 : 128;
-  if (B_MN && bn < 64) bn = 64;
-  const long long nC = (p.C + BM - 1) / BM;
-  if (p.R > 128 && nC * ((p.R + 255) / 256) >= 152) bn = 256;
-  const long long tiles = nC * ((p.R + bn - 1) / bn);
-  const int slots = 152 * (bn == 256 ? 1 : 2);
-  p.splits = 1;
-  while (p.splits < MAX_SPLITS && tiles * p.splits * 2 <= slots && p.nk / (p.splits * 2) >= 2) p.splits *= 2;
+  p.splits = c.splits;
   // fp32 output: the tensor core's running sum rounds at every step, so its length is
   // kept short by spreading the sum over up to four accumulators
   p.nacc = 1;
-  if (p.ep.out_dtype == MOE_DTYPE_F32) p.nacc = bn <= 64 ? 4 : 2;
-  switch (bn) {
+  if (p.ep.out_dtype == MOE_DTYPE_F32) p.nacc = c.bn <= 64 ? 4 : 2;
+  switch (c.bn) {
     case 16:
       if constexpr (!B_MN) return launch_tile<16, A_MN, B_MN>(q, p, s);
     case 32:
@@ -358,53 +432,56 @@ cudaError_t launch_shape(const Product& q, cudaStream_t s) {
   }
 }
 
+bool takes_pair(const Product& q, const Choice& c) { return pair_storable(q) && pair_estimate(q) < c.us; }
+
 cudaError_t launch_product(const Product& q, cudaStream_t s) {
-  if (pair_takes(q)) return launch_pair(q, s);
-  if (!q.cols_mn) return launch_shape<false, false>(q, s);
-  return q.rows_mn ? launch_shape<true, true>(q, s) : launch_shape<true, false>(q, s);
+  const Choice c = choose_tile(q);
+  if (takes_pair(q, c)) return launch_pair(q, nullptr, s);
+  if (!q.cols_mn) return launch_shape<false, false>(q, c, s);
+  return q.rows_mn ? launch_shape<true, true>(q, c, s) : launch_shape<true, false>(q, c, s);
 }
 
 // ------------------------------------------------------------------ dz
 // dz = alpha dy act'(z) in the operands' type, and per chunk of rows the fp32 sums
-// of its unrounded columns.  Thread (x, y): columns 8 x .. 8 x + 7 of every 8th row.
+// of its unrounded columns.  Thread (x, y): columns 8 x .. 8 x + 7 of every 8th row,
+// four rows' loads issued before the first is used (bound by memory: dy and z in, dz
+// out).  DT, T: types of dy and of z and dz.  VEC: rows that 16-byte accesses fit.
 struct DzArgs {
   int M, N, rows;  // rows per chunk
-  int dy_dtype, dtype, act;
+  int act;
   float alpha;
   long long ld_dy, ld_dz;
   const void* dy;
   const void* z;
   void* dz;
   float* partials;  // [chunks][N], null: not wanted
-  bool vec;
 };
 
-__device__ __forceinline__ void load8(float (&v)[8], const void* p, int dtype, size_t at, int n, bool vec) {
-  if (vec) {
-    if (dtype == MOE_DTYPE_F32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-      const float4 a = __ldg(q), b = __ldg(q + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ float value_of(float v) { return v; }
+__device__ __forceinline__ float value_of(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float value_of(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(T (&v)[8], const void* p, size_t at, int n) {
+  const T* q = static_cast<const T*>(p) + at;
+  if (VEC) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = dtype == MOE_DTYPE_BF16
-                             ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
-                             : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
-    }
+    for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j)
+      reinterpret_cast<uint4*>(v)[j] = __ldg(reinterpret_cast<const uint4*>(q) + j);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? load_as_f32(p, dtype, at + i) : 0.0f;
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v[i] = q[i];
   }
 }
 
-// Four rows' loads are issued before the first is used.
+template <typename DT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   __shared__ float s_sum[8][256 + 8];
   constexpr int AHEAD = 4;
@@ -416,55 +493,43 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   float sum[8] = {};
   if (n > 0) {
     for (int mb = m0 + threadIdx.y; mb < m1; mb += 8 * AHEAD) {
-      float g[AHEAD][8], z[AHEAD][8];
+      alignas(16) DT g[AHEAD][8];
+      alignas(16) T z[AHEAD][8];
 #pragma unroll
       for (int q = 0; q < AHEAD; ++q) {
         const int m = mb + 8 * q;
         if (m < m1) {
-          load8(g[q], a.dy, a.dy_dtype, static_cast<size_t>(m) * a.ld_dy + c, n, a.vec);
-          if (a.act != MOE_ACT_NONE) load8(z[q], a.z, a.dtype, static_cast<size_t>(m) * a.N + c, n, a.vec);
+          load8<DT, VEC>(g[q], a.dy, static_cast<size_t>(m) * a.ld_dy + c, n);
+          if (a.act != MOE_ACT_NONE) load8<T, VEC>(z[q], a.z, static_cast<size_t>(m) * a.N + c, n);
         }
       }
 #pragma unroll
       for (int q = 0; q < AHEAD; ++q) {
         const int m = mb + 8 * q;
         if (m >= m1) break;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[q][i] *= a.alpha;
+        for (int i = 0; i < 8; ++i) v[i] = VEC || i < n ? a.alpha * value_of(g[q][i]) : 0.0f;
+        auto times = [&](int act) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (VEC || i < n) v[i] *= act_grad(value_of(z[q][i]), act);
+        };
         switch (a.act) {
           case MOE_ACT_NONE: break;
-          case MOE_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_RELU);
-            break;
-          case MOE_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_SILU);
-            break;
-          case MOE_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_GELU);
-            break;
-          default:
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[q][i] *= act_grad(z[q][i], MOE_ACT_GELU_TANH);
+          case MOE_ACT_RELU: times(MOE_ACT_RELU); break;
+          case MOE_ACT_SILU: times(MOE_ACT_SILU); break;
+          case MOE_ACT_GELU: times(MOE_ACT_GELU); break;
+          default: times(MOE_ACT_GELU_TANH);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += g[q][i];
+        for (int i = 0; i < 8; ++i) sum[i] += v[i];
         if (a.dz) {  // rows of the workspace are padded to 8 values: a whole store even at the edge
-          uint32_t w[4];
+          alignas(16) T out[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (a.dtype == MOE_DTYPE_BF16) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(g[q][2 * i], g[q][2 * i + 1]);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            } else {
-              const __half2 b = __floats2half2_rn(g[q][2 * i], g[q][2 * i + 1]);
-              w[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-          }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 8; ++i) out[i] = rounded<T>(v[i]);
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c) =
+              *reinterpret_cast<const uint4*>(out);
         }
       }
     }
@@ -480,6 +545,19 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
     for (int y = 0; y < 8; ++y) v += s_sum[y][col];
     a.partials[static_cast<size_t>(blockIdx.y) * a.N + blockIdx.x * 256 + col] = v;
   }
+}
+
+template <typename DT, typename T>
+cudaError_t launch_dz(const DzArgs& d, bool vec, int chunks, cudaStream_t s) {
+  const dim3 grid((d.N + 255) / 256, chunks), block(32, 8);
+  return vec ? launch_dependent(linear_dz_kernel<DT, T, true>, grid, block, 0, s, d)
+             : launch_dependent(linear_dz_kernel<DT, T, false>, grid, block, 0, s, d);
+}
+template <typename T>
+cudaError_t launch_dz(const DzArgs& d, int dy_dtype, bool vec, int chunks, cudaStream_t s) {
+  if (dy_dtype == MOE_DTYPE_F32) return launch_dz<float, T>(d, vec, chunks, s);
+  if (dy_dtype == MOE_DTYPE_BF16) return launch_dz<__nv_bfloat16, T>(d, vec, chunks, s);
+  return launch_dz<__half, T>(d, vec, chunks, s);
 }
 
 // Rows per chunk: at least 64, at most 256 chunks.
@@ -530,8 +608,6 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     d.M = a.M;
     d.N = a.N;
     d.rows = dz_rows(a.M);
-    d.dy_dtype = a.dy_dtype;
-    d.dtype = a.dtype;
     d.act = a.act;
     d.alpha = a.alpha;
     d.ld_dy = a.ld_y;
@@ -540,11 +616,12 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     d.z = a.z;
     d.dz = direct || !products ? nullptr : a.dz;
     d.partials = a.dbias ? a.partials : nullptr;
-    d.vec = a.N % 8 == 0 && a.ld_y % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
-            reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
+    const bool vec = a.N % 8 == 0 && a.ld_y % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
     const int chunks = (a.M + d.rows - 1) / d.rows;
     stage_begin("linear_dz", s);
-    err = launch_dependent(linear_dz_kernel, dim3((a.N + 255) / 256, chunks), dim3(32, 8), 0, s, d);
+    err = a.dtype == MOE_DTYPE_BF16 ? launch_dz<__nv_bfloat16>(d, a.dy_dtype, vec, chunks, s)
+                                    : launch_dz<__half>(d, a.dy_dtype, vec, chunks, s);
     stage_end(s);
     if (err == cudaSuccess && a.dbias) err = launch_column_sums(a.partials, chunks, a.N, a.dbias, s);
   }
@@ -557,25 +634,32 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
   q.reset_status = 1;
   q.hdr = a.hdr;
   q.rows = dz;
-  if (err == cudaSuccess && a.dx) {
-    q.R = a.M;
-    q.K = a.N;
-    q.cols = {a.w, a.ld_w, a.K, a.N};
-    q.rows_mn = false;
-    q.ep.y = a.dx;
-    stage_begin("linear_dx", s);
-    err = launch_product(q, s);
+  Product dx = q, dw = q;
+  dx.R = a.M;
+  dx.K = a.N;
+  dx.cols = {a.w, a.ld_w, a.K, a.N};
+  dx.rows_mn = false;
+  dx.ep.y = a.dx;
+  dw.R = a.N;
+  dw.K = a.M;
+  dw.cols = {a.x, a.ld_x, a.K, a.M};
+  dw.rows_mn = true;
+  dw.ep.y = a.dw;
+  if (err == cudaSuccess && a.dx && a.dw && takes_pair(dx, choose_tile(dx)) && takes_pair(dw, choose_tile(dw))) {
+    stage_begin("linear_dx_dw", s);
+    err = launch_pair(dx, &dw, s);
     stage_end(s);
-    q.reset_status = 0;
+    return err;
+  }
+  if (err == cudaSuccess && a.dx) {
+    stage_begin("linear_dx", s);
+    err = launch_product(dx, s);
+    stage_end(s);
+    dw.reset_status = 0;
   }
   if (err == cudaSuccess && a.dw) {
-    q.R = a.N;
-    q.K = a.M;
-    q.cols = {a.x, a.ld_x, a.K, a.M};
-    q.rows_mn = true;
-    q.ep.y = a.dw;
     stage_begin("linear_dw", s);
-    err = launch_product(q, s);
+    err = launch_product(dw, s);
     stage_end(s);
   }
   return err;

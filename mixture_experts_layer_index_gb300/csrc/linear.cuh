@@ -142,9 +142,11 @@ struct Product {
   DeviceHeader* hdr;
 };
 
-// Whether launch_pair takes the product: outputs that TMA can store, enough work.
-bool pair_takes(const Product& p);
-cudaError_t launch_pair(const Product& p, cudaStream_t s);
+// linear_pair.cu: whether TMA can store the outputs; about how long a launch takes (us);
+// the product, or two of a gradient (the same type, no bias, activation, residual or z).
+bool pair_storable(const Product& p);
+float pair_estimate(const Product& p);
+cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s);
 
 }  // namespace lin
 }  // namespace moe

@@ -38,14 +38,51 @@ constexpr int BAR_OFFSET = BOX_OFFSET + EPI_WARPS * BOX_BYTES;
 constexpr size_t SMEM_BYTES = 1024 + BAR_OFFSET + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one block");
 
-struct PairParams {
+// One product of a launch.
+struct PairProduct {
   int R, C, nk;
   int nR, nC;
+  int a_mn, b_mn;  // operand rows / cols contiguous along r / c
+};
+// A launch computes one product, or two whose epilogues differ in their output only
+// (the gradient's two), `prod[0]` the one with the longer sum.
+struct PairParams {
+  PairProduct prod[2];
+  int tiles[2];
+  int ratio;  // tiles of prod[1] that take about as long as one of prod[0]
   int type;
   Epilogue ep;
   int reset_status;
   DeviceHeader* hdr;
 };
+struct PairMaps {
+  CUtensorMap a, b, y;
+};
+
+// The i-th tile of a pair: (product, tile), false after its last.  Tiles of prod[0] go
+// round the pairs first; pairs left without one in the last round take `ratio` tiles of
+// prod[1] instead; the rest of prod[1] goes round again.  So the two products of a
+// gradient, each of which would leave part of the GPU idle in its last round, share one.
+__device__ __forceinline__ bool pair_item(const PairParams& p, int pair, int npairs, int i, int& prod, int& tile) {
+  const int heavy = pair < p.tiles[0] ? (p.tiles[0] - pair - 1) / npairs + 1 : 0;
+  prod = 0;
+  tile = pair + i * npairs;
+  if (i < heavy) return true;
+  prod = 1;
+  i -= heavy;
+  const int last = p.tiles[0] % npairs;  // pairs with a tile of the last round
+  int gap = (npairs - last) * p.ratio;
+  if (pair >= last) {
+    if (i < p.ratio) {
+      tile = pair - last + i * (npairs - last);
+      return tile < p.tiles[1];
+    }
+    i -= p.ratio;
+  }
+  if (gap > p.tiles[1]) gap = p.tiles[1];
+  tile = gap + pair + i * npairs;
+  return tile < p.tiles[1];
+}
 
 // ------------------------------------------------------------------ two-SM forms
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
@@ -83,7 +120,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
 
 // Tile t's first row and column: groups of 8 row tiles, column by column within a
 // group, so that the pairs in flight share both operands in L2.
-__device__ __forceinline__ void tile_origin(const PairParams& p, int t, int& r0, int& c0) {
+__device__ __forceinline__ void tile_origin(const PairProduct& p, int t, int& r0, int& c0) {
   constexpr int GR = 8;
   const int group = t / (GR * p.nC), in_group = t - group * (GR * p.nC);
   const int rows_here = min(GR, p.nR - group * GR);
@@ -155,11 +192,9 @@ __device__ __forceinline__ void add16(float (&v)[16], const void* p, int dtype, 
   }
 }
 
-template <bool A_MN, bool B_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    linear_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
-                       const PairParams p) {
+    linear_pair_kernel(const __grid_constant__ PairMaps m0, const __grid_constant__ PairMaps m1,
+                       const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ PairParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFFSET);
@@ -183,8 +218,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
+    prefetch_tensormap(&m0.a);
+    prefetch_tensormap(&m0.b);
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -202,7 +237,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   // a wait that records a timeout lasts seconds: nothing of this launch is lost here
   if (p.reset_status && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->status = p.hdr->info = 0u;
 
-  const int total = p.nR * p.nC;
   const int npairs = static_cast<int>(gridDim.x) >> 1, pair = static_cast<int>(blockIdx.x) >> 1;
 
   if (warp == 0) {
@@ -214,12 +248,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     int issued = 0;
     bool ok = true;
     bool ready = mbar_try_wait(empty0, phase);
-    for (int t = pair; t < total && ok; t += npairs) {
+    int prod, tile;
+    for (int i = 0; ok && pair_item(p, pair, npairs, i, prod, tile); ++i) {
+      const PairProduct& q = p.prod[prod];
+      const CUtensorMap* ma = prod ? &m1.a : &m0.a;
+      const CUtensorMap* mb = prod ? &m1.b : &m0.b;
+      const bool a_mn = q.a_mn, b_mn = q.b_mn;
       int r0, c0;
-      tile_origin(p, t, r0, c0);
+      tile_origin(q, tile, r0, c0);
       r0 += rank * HALF;
       c0 += rank * HALF;
-      for (int kb = 0; kb < p.nk; ++kb) {
+      const int nk = q.nk;
+      for (int kb = 0; kb < nk; ++kb) {
         if (!ready && !mbar_wait(empty0 + 8 * stage, phase, abort_flag, p.hdr, 0x610000u)) {
           ok = false;
           break;
@@ -234,17 +274,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           // the even block's barrier expects the bytes of both blocks
           if (rank == 0) mbar_arrive_expect_tx(full, 2 * STAGE_BYTES);
           const int k = kb * BK;
-          if (A_MN) {
-            tma_load_2d_pair(a, &tmA, r0, k, bar);
-            tma_load_2d_pair(a + OP_BYTES / 2, &tmA, r0 + 64, k, bar);
+          if (a_mn) {
+            tma_load_2d_pair(a, ma, r0, k, bar);
+            tma_load_2d_pair(a + OP_BYTES / 2, ma, r0 + 64, k, bar);
           } else {
-            tma_load_2d_pair(a, &tmA, k, r0, bar);
+            tma_load_2d_pair(a, ma, k, r0, bar);
           }
-          if (B_MN) {
-            tma_load_2d_pair(b, &tmB, c0, k, bar);
-            tma_load_2d_pair(b + OP_BYTES / 2, &tmB, c0 + 64, k, bar);
+          if (b_mn) {
+            tma_load_2d_pair(b, mb, c0, k, bar);
+            tma_load_2d_pair(b + OP_BYTES / 2, mb, c0 + 64, k, bar);
           } else {
-            tma_load_2d_pair(b, &tmB, k, c0, bar);
+            tma_load_2d_pair(b, mb, k, c0, bar);
           }
         }
         __syncwarp();
@@ -266,32 +306,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // stage's MMAs are issued: the look takes longer than an MMA.
     if (rank == 0) {
       const bool leader = elect_one();
-      const uint32_t idesc =
-          make_idesc(p.type, p.type, TILE, TILE) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
       const uint32_t ring = smem_u32(smem);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
+      int prod, tile;
+      for (int i = 0; ok && pair_item(p, pair, npairs, i, prod, tile); ++i) {
+        const bool a_mn = p.prod[prod].a_mn, b_mn = p.prod[prod].b_mn;
+        const int nk = p.prod[prod].nk;
+        const uint32_t idesc =
+            make_idesc(p.type, p.type, TILE, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        const uint64_t fixed_a = a_mn ? OperandDesc<true>::kFixed : OperandDesc<false>::kFixed;
+        const uint64_t fixed_b = b_mn ? OperandDesc<true>::kFixed : OperandDesc<false>::kFixed;
+        const uint32_t step_a = a_mn ? OperandDesc<true>::kStep : OperandDesc<false>::kStep;
+        const uint32_t step_b = b_mn ? OperandDesc<true>::kStep : OperandDesc<false>::kStep;
         if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.hdr, 0x620000u)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * TILE;
         bool ready = mbar_try_wait(full0 + 8 * stage, phase);
-        for (int kb = 0; kb < p.nk; ++kb) {
+        for (int kb = 0; kb < nk; ++kb) {
           if (!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x630000u)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = ring + stage * STAGE_BYTES, empty = empty0 + 8 * stage;
+          const uint32_t slot = (ring + stage * STAGE_BYTES) >> 4, empty = empty0 + 8 * stage;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
-          ready = kb + 1 < p.nk && mbar_try_wait(full0 + 8 * stage, phase);
+          ready = kb + 1 < nk && mbar_try_wait(full0 + 8 * stage, phase);
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_pair(d, OperandDesc<A_MN>::at(a, kk), OperandDesc<B_MN>::at(a + OP_BYTES, kk), idesc,
+              mma_f16_pair(d, fixed_a | (slot + kk * step_a), fixed_b | (slot + (OP_BYTES >> 4) + kk * step_b), idesc,
                            (kb | kk) != 0);
             mma_commit_pair(empty);
           }
@@ -323,9 +370,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) bulk_wait_group_read0();
       __syncwarp();
     };
-    for (int t = pair; t < total; t += npairs) {
+    int prod, tile;
+    for (int i = 0; pair_item(p, pair, npairs, i, prod, tile); ++i) {
+      const int R = p.prod[prod].R, C = p.prod[prod].C;
+      const CUtensorMap* my = prod ? &m1.y : &m0.y;
       int r0, c0;
-      tile_origin(p, t, r0, c0);
+      tile_origin(p.prod[prod], tile, r0, c0);
       r0 += rank * HALF + q * 32;  // this warp's rows and columns
       c0 += h * EPI_COLS;
       int good = 1;
@@ -334,18 +384,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!good) break;
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * EPI_COLS;
-      const bool row_in = r0 + lane < p.R;
+      const bool row_in = r0 + lane < R;
       // sum + bias of 16 columns from c0 + j * 16
       auto load_z = [&](int j, float(&v)[16]) {
         tmem_ld16(tb + j * 16, v);
         tmem_ld_wait_regs16(v);
-        if (ep.bias) add16(v, ep.bias, ep.bias_dtype, c0 + j * 16, p.C - c0 - j * 16, bias_wide);  // same for every lane
+        if (ep.bias) add16(v, ep.bias, ep.bias_dtype, c0 + j * 16, C - c0 - j * 16, bias_wide);  // same for every lane
       };
       auto store_box = [&](const CUtensorMap* map, int c) {
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          if (r0 < p.R && c < p.C) tma_store_2d(map, smem_u32(box), c, r0);
+          if (r0 < R && c < C) tma_store_2d(map, smem_u32(box), c, r0);
           bulk_commit_group();
         }
       };
@@ -394,10 +444,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int i = 0; i < 16; ++i) v[i] *= ep.alpha;
         }
         if (ep.residual && row_in)  // its rows are aligned as y's, which TMA stores
-          add16(v, ep.residual, ep.out_dtype, static_cast<size_t>(r0 + lane) * ep.ld_y + c, p.C - c, residual_wide);
+          add16(v, ep.residual, ep.out_dtype, static_cast<size_t>(r0 + lane) * ep.ld_y + c, C - c, residual_wide);
         if (j == 0 || (wide && j == 2)) box_free();
         put_box(box, lane, wide ? j & 1 : j, ep.out_dtype, v);
-        if (j == 3 || (wide && j == 1)) store_box(&tmY, wide ? c - 16 : c0);
+        if (j == 3 || (wide && j == 1)) store_box(my, wide ? c - 16 : c0);
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
@@ -438,47 +488,63 @@ bool storable(const void* base, int dtype, long long ld) {
   return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
 }
 
-template <bool A_MN, bool B_MN>
-cudaError_t launch_pair_of(const Product& q, cudaStream_t s) {
-  const int sms = num_sms();
-  if (sms < 2) return cudaErrorNoDevice;
-  CUtensorMap ta, tb, ty, tz;
-  if (!encode(&ta, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, A_MN ? 64 : HALF) ||
-      !encode(&tb, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, B_MN ? 64 : HALF) ||
-      !encode_store(&ty, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y))
-    return cudaErrorInvalidValue;
-  tz = ty;
-  if (q.ep.z && !encode_store(&tz, q.ep.z, q.ep.z_dtype, q.C, q.R, q.ep.ld_z)) return cudaErrorInvalidValue;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      linear_pair_kernel<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
-  if (attr != cudaSuccess) return attr;
-  PairParams p{};
-  p.R = q.R;
-  p.C = q.C;
-  p.nk = (q.K + BK - 1) / BK;
-  p.nR = (q.R + TILE - 1) / TILE;
-  p.nC = (q.C + TILE - 1) / TILE;
-  p.type = q.type;
-  p.ep = q.ep;
-  p.reset_status = q.reset_status;
-  p.hdr = q.hdr;
-  const long long tiles = static_cast<long long>(p.nR) * p.nC;
-  const int pairs = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_dependent(linear_pair_kernel<A_MN, B_MN>, dim3(2 * pairs), dim3(THREADS), SMEM_BYTES, s, ta, tb, ty, tz, p);
+bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
+  pp->R = q.R;
+  pp->C = q.C;
+  pp->nk = (q.K + BK - 1) / BK;
+  pp->nR = (q.R + TILE - 1) / TILE;
+  pp->nC = (q.C + TILE - 1) / TILE;
+  pp->a_mn = q.rows_mn;
+  pp->b_mn = q.cols_mn;
+  return encode(&m->a, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : HALF) &&
+         encode(&m->b, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn ? 64 : HALF) &&
+         encode_store(&m->y, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y);
 }
 
 }  // namespace
 
-bool pair_takes(const Product& q) {
-  if (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) || (q.ep.z && !storable(q.ep.z, q.ep.z_dtype, q.ep.ld_z)))
-    return false;
-  const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + TILE - 1) / TILE);
-  return q.R > HALF && q.C > HALF && tiles >= 38;
+bool pair_storable(const Product& q) {
+  return storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) && (!q.ep.z || storable(q.ep.z, q.ep.z_dtype, q.ep.ld_z));
 }
 
-cudaError_t launch_pair(const Product& q, cudaStream_t s) {
-  if (!q.cols_mn) return launch_pair_of<false, false>(q, s);
-  return q.rows_mn ? launch_pair_of<true, true>(q, s) : launch_pair_of<false, true>(q, s);
+float pair_estimate(const Product& q) {
+  const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + TILE - 1) / TILE);
+  const float stages = 0.30f * ((q.K + BK - 1) / BK);
+  return 6.0f + ((tiles + 75) / 76) * (stages > 2.5f ? stages : 2.5f);
+}
+
+cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s) {
+  const int sms = num_sms();
+  if (sms < 2) return cudaErrorNoDevice;
+  const Product* q0 = &first;
+  if (second && second->K > first.K) {
+    q0 = second;
+    second = &first;
+  }
+  PairParams p{};
+  PairMaps m0, m1;
+  CUtensorMap tz;
+  if (!encode_product(&m0, &p.prod[0], *q0)) return cudaErrorInvalidValue;
+  p.tiles[0] = p.prod[0].nR * p.prod[0].nC;
+  p.ratio = 1;
+  m1 = m0;
+  tz = m0.y;
+  if (second) {
+    if (!encode_product(&m1, &p.prod[1], *second)) return cudaErrorInvalidValue;
+    p.tiles[1] = p.prod[1].nR * p.prod[1].nC;
+    p.ratio = (p.prod[0].nk + p.prod[1].nk / 2) / p.prod[1].nk;
+  }
+  if (q0->ep.z && !encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z)) return cudaErrorInvalidValue;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+  if (attr != cudaSuccess) return attr;
+  p.type = q0->type;
+  p.ep = q0->ep;
+  p.reset_status = first.reset_status;
+  p.hdr = q0->hdr;
+  const int tiles = p.tiles[0] + p.tiles[1];
+  const int pairs = tiles < sms / 2 ? tiles : sms / 2;
+  return launch_dependent(linear_pair_kernel, dim3(2 * pairs), dim3(THREADS), SMEM_BYTES, s, m0, m1, tz, p);
 }
 
 }  // namespace lin
