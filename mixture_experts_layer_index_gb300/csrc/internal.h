@@ -210,6 +210,7 @@ struct RouteArgs {
   int n_group, topk_group, group_best;  // n_group 1: no limit to groups
   const float* bias;
   long long ld;  // elements between rows of the scores
+  bool vec, bias_vec;  // rows, bias can be read 16 bytes at a time
   int32_t* ids;  // forward
   float* w;
 };

@@ -16,21 +16,22 @@
 //   softmax                 ds_e = p_e (g_e - sum_j p_j g_j)            every e
 // Only the last needs the scores of the experts that were not selected.
 //
-// One warp per token in both directions.  The bytes are one row of E scores in
-// and k pairs out (a row of E gradients out); the arithmetic per row (exp, a
-// division where p is needed for every expert, k selection rounds) is of the
-// same size, which is why rows are spread one per warp with eight warps a block:
-// the long selection chains of many warps overlap.
+// The bytes are one row of E scores in and k pairs out (a row of E gradients out), but
+// the selection rounds, and p where the keys need it for every expert, are some hundred
+// instructions per row: rows in large numbers are bound by instructions, few rows by the
+// length of the chain of rounds.  So the forward gives a row few lanes with 16 experts
+// each when there are many rows (a round's bookkeeping is then shared by the 2 to 16 rows
+// of a warp), and a whole warp when there are few.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "internal.h"
-#include "routing.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kRouterWarps = 8;
+constexpr int kFewWarps = 4 * 152;  // below: a warp per row leaves no scheduler without one
 
 template <typename ST>
 __device__ __forceinline__ float to_f32(ST v);
@@ -59,55 +60,95 @@ __device__ __forceinline__ float clean_score(ST raw) {
 }
 
 __device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + expf(-x)); }
+// For the keys, which every expert needs: within 2e-7 of the sigmoid, a third of the instructions.
+__device__ __forceinline__ float sigmoid_key(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 // sigmoid(x) e^-m for x <= m <= 0; sigmoid(x) for m = 0.
 __device__ __forceinline__ float scaled_sigmoid(float x, float m) {
   return m < 0.0f ? expf(x - m) / (1.0f + expf(x)) : sigmoid_f32(x);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+template <int SUB>
+__device__ __forceinline__ float sub_max(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = SUB / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int SUB>
+__device__ __forceinline__ float sub_sum(float v) {
+#pragma unroll
+  for (int o = SUB / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Selection keys: 0 = not to be taken (no such expert, group not kept, already
-// taken), 1 = masked expert (taken only after every other), else the
-// order-preserving image of the key.
-constexpr uint32_t kKeyTaken = 0u, kKeyMasked = 1u;
-__device__ __forceinline__ uint32_t live_key(float v) {
-  const uint32_t b = score_bits(v);
-  return b < 2u ? 2u : b;
-}
-
-template <int MAXV>
-__device__ __forceinline__ void local_best(const uint32_t (&key)[MAXV], uint32_t& best, int& slot) {
-  best = key[0];
-  slot = 0;
+template <int VPL>
+__device__ __forceinline__ float best_of(const float (&key)[VPL]) {
+  float b = key[0];
 #pragma unroll
-  for (int i = 1; i < MAXV; ++i)
-    if (key[i] > best) {
-      best = key[i];
-      slot = i;
-    }
+  for (int i = 1; i < VPL; ++i) b = fmaxf(b, key[i]);
+  return b;
 }
 
-template <int MAXV, typename ST>
+// A lane's VPL consecutive scores, cleaned; -inf past expert E.
+template <int VPL, typename ST>
+__device__ __forceinline__ void load_scores(float (&x)[VPL], const ST* __restrict__ row, int e0, int E, bool vec) {
+  constexpr int PER = 16 / sizeof(ST);  // scores per 16-byte load
+  if (VPL % PER == 0 && vec) {          // E is a multiple of PER too
+#pragma unroll
+    for (int q = 0; q < VPL / PER; ++q) {
+      alignas(16) ST raw[PER];
+      if (e0 + q * PER < E) {
+        *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + e0 + q * PER));
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[q * PER + i] = clean_score(raw[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[q * PER + i] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? clean_score(row[e0 + i]) : -INFINITY;
+  }
+}
+
+template <int VPL>
+__device__ __forceinline__ void load_bias(float (&b)[VPL], const float* __restrict__ bias, int e0, int E, bool vec) {
+  if (VPL % 4 == 0 && vec) {
+#pragma unroll
+    for (int q = 0; q < VPL / 4; ++q) {
+      const float4 f = e0 + 4 * q < E ? __ldg(reinterpret_cast<const float4*>(bias + e0) + q) : make_float4(0, 0, 0, 0);
+      b[4 * q] = f.x; b[4 * q + 1] = f.y; b[4 * q + 2] = f.z; b[4 * q + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) b[i] = e0 + i < E ? __ldg(bias + e0 + i) : 0.0f;
+  }
+}
+
+// SUB lanes per token with VPL consecutive experts each.  A key is the fp32 value that
+// ranks its expert; -inf: masked (taken only after every other); NaN: not to be taken
+// (no such expert, group not kept, already taken), which fmaxf passes over and no
+// comparison matches.  Equal keys: the lowest lane holds the lowest ids.
+template <int VPL, int SUB, typename ST>
 __global__ void __launch_bounds__(kRouterWarps * 32) route_ex_kernel(const ST* __restrict__ scores, RouteArgs a) {
-  extern __shared__ float s_rows[];  // group limits only: one row of E ranking values per warp
+  constexpr int TOKENS = 32 / SUB;  // per warp
+  __shared__ int s_ids[kRouterWarps][TOKENS][kMaxK];
+  // group limits only: per token VPL x SUB ranking values, one word of padding for each
+  // VPL, and the ranks of up to 32 groups
+  extern __shared__ float s_rows[];
+  constexpr int PITCH = SUB * (VPL + 1), GPITCH = 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRouterWarps + warp;
+  const int tok = lane / SUB, sub = lane & (SUB - 1);
+  const int t = (blockIdx.x * kRouterWarps + warp) * TOKENS + tok;
   dep_wait();
   dep_launch();
-  if (t >= a.T) return;  // no block-wide barrier below
-  const ST* row = scores + static_cast<size_t>(t) * a.ld;
-  const int E = a.E, k = a.k;
-  float x[MAXV];
-#pragma unroll
-  for (int i = 0; i < MAXV; ++i) {
-    const int e = i * 32 + lane;
-    x[i] = e < E ? clean_score(row[e]) : -INFINITY;
-  }
+  if ((blockIdx.x * kRouterWarps + warp) * TOKENS >= a.T) return;  // no block-wide barrier below
+  const bool mine = t < a.T;  // a warp's last tokens may be missing: they shadow token T - 1
+  const ST* row = scores + static_cast<size_t>(mine ? t : a.T - 1) * a.ld;
+  const int E = a.E, k = a.k, e0 = sub * VPL;
+  float x[VPL];
+  load_scores<VPL, ST>(x, row, e0, E, a.vec);
   const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
   const bool sum_ranked = a.n_group > 1 && a.group_best == 2;
   const bool need_p = a.bias != nullptr || sum_ranked;
@@ -115,236 +156,325 @@ __global__ void __launch_bounds__(kRouterWarps * 32) route_ex_kernel(const ST* _
   // softmax over the whole row: maximum and sum over the experts that are not masked
   float top = 0.0f, total = 0.0f;
   if (softmax && (need_p || !a.renormalise)) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < MAXV; ++i) m = fmaxf(m, x[i]);
-    m = warp_max(m);
+    const float m = sub_max<SUB>(best_of<VPL>(x));
     top = m > -INFINITY ? m : 0.0f;
 #pragma unroll
-    for (int i = 0; i < MAXV; ++i) total += x[i] > -INFINITY ? expf(x[i] - top) : 0.0f;
-    total = warp_sum(total);
+    for (int i = 0; i < VPL; ++i) total += expf(x[i] - top);  // a masked score adds expf(-inf) = 0
+    total = sub_sum<SUB>(total);
   }
 
-  uint32_t key[MAXV];
+  // x becomes the key
+  float* ranked = s_rows + (warp * TOKENS + tok) * (PITCH + GPITCH);
+  if (need_p) {
+    const float inv_total = total > 0.0f ? __fdividef(1.0f, total) : 0.0f;
+    float bias[VPL];
+    if (a.bias) load_bias<VPL>(bias, a.bias, e0, E, a.bias_vec);
 #pragma unroll
-  for (int i = 0; i < MAXV; ++i) {
-    const int e = i * 32 + lane;
-    const bool live = x[i] > -INFINITY;
-    float v = x[i], ranked = x[i];
-    if (need_p) {
-      const float p = !live ? 0.0f : softmax ? expf(x[i] - top) / total : sigmoid_f32(x[i]);
-      if (a.bias) v = p + (e < E ? __ldg(a.bias + e) : 0.0f);
-      ranked = sum_ranked && !a.bias ? p : v;
+    for (int i = 0; i < VPL; ++i) {
+      const bool live = x[i] > -INFINITY;  // p of a masked score comes out as 0
+      const float p = softmax ? __expf(x[i] - top) * inv_total : sigmoid_key(x[i]);
+      float v = x[i];
+      if (a.bias) {
+        v = p + bias[i];
+        v = v == v ? v : -3.402823466e38f;  // a key that is no number (infinite bias) still has a place
+      }
+      if (sum_ranked) ranked[sub * (VPL + 1) + i] = !live ? -INFINITY : a.bias ? v : p;
+      x[i] = live ? v : -INFINITY;
     }
-    key[i] = e >= E ? kKeyTaken : live ? live_key(v) : kKeyMasked;
-    if (a.n_group > 1 && e < E) s_rows[warp * E + e] = live ? ranked : -INFINITY;
+  }
+  if (a.n_group > 1 && !sum_ranked) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) ranked[sub * (VPL + 1) + i] = x[i];
+  }
+  if (SUB * VPL != E) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (e0 + i >= E) x[i] = NAN;
   }
 
   if (a.n_group > 1) {
-    // lpg lanes per group (a power of two) rank it: best key, or sum of the best
-    // two keys of experts that are not masked
+    // Rank of each group: best key, or sum of the best two keys of experts that are not
+    // masked.  Few groups: lpg lanes per group; many: several groups per lane.
     __syncwarp();
+    float* rank = ranked + PITCH;
     const int G = a.n_group, gs = E / G;
     int lpg = 1;
-    while (lpg * 2 * G <= 32) lpg *= 2;
-    const int g = lane / lpg, sub = lane & (lpg - 1);
-    float b1 = -INFINITY, b2 = -INFINITY;
-    if (g < G)
-      for (int e = sub; e < gs; e += lpg) {
-        const float v = s_rows[warp * E + g * gs + e];
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
+    while (lpg * 2 * G <= SUB) lpg *= 2;
+    const int per_pass = SUB / lpg;
+    for (int g0 = 0; g0 < G; g0 += per_pass) {
+      const int g = g0 + sub / lpg;
+      float b1 = -INFINITY, b2 = -INFINITY;
+      if (g < G)
+        for (int i = sub & (lpg - 1); i < gs; i += lpg) {
+          const int e = g * gs + i;
+          const float v = ranked[e + e / VPL];
+          b2 = fmaxf(b2, fminf(b1, v));
+          b1 = fmaxf(b1, v);
+        }
+      for (int o = 1; o < lpg; o <<= 1) {
+        const float c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+        b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+        b1 = fmaxf(b1, c1);
       }
-    for (int o = 1; o < lpg; o <<= 1) {
-      const float c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
-      b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
-      b1 = fmaxf(b1, c1);
+      if (g < G && (sub & (lpg - 1)) == 0) rank[g] = a.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     }
-    float rank = b1;
-    if (a.group_best == 2 && b2 > -INFINITY) rank = b1 + b2;
-    const uint32_t mine = rank > -INFINITY ? live_key(rank) : kKeyMasked;
-    int before = 0;  // groups that come before this one
-    for (int h = 0; h < G; ++h) {
-      const uint32_t other = __shfl_sync(0xffffffffu, mine, h * lpg);
-      before += (other > mine || (other == mine && h < g)) ? 1 : 0;
+    __syncwarp();
+    // groups that fewer than topk_group others come before
+    unsigned kept = 0u;
+    for (int g = sub; g < G; g += SUB) {
+      const float r = rank[g];
+      int before = 0;
+      for (int h = 0; h < G; ++h) {
+        const float o = rank[h];
+        before += (o > r || (o == r && h < g)) ? 1 : 0;
+      }
+      if (before < a.topk_group) kept |= 1u << g;
     }
-    const unsigned kept = __ballot_sync(0xffffffffu, g < G && sub == 0 && before < a.topk_group);
-    // e / gs by a multiplication: e < 512, so e * ceil(2^22 / gs) is exact after the shift
-    const unsigned inv = ((1u << 22) + gs - 1) / gs;
 #pragma unroll
-    for (int i = 0; i < MAXV; ++i) {
-      const unsigned ge = (static_cast<unsigned>(i * 32 + lane) * inv) >> 22;
-      if (key[i] != kKeyTaken && !((kept >> (ge * lpg)) & 1u)) key[i] = kKeyTaken;
+    for (int o = SUB / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(0xffffffffu, kept, o);
+    int g = e0 / gs, left = (g + 1) * gs - e0;  // experts of group g from here on
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (g < 32 && !((kept >> g) & 1u)) x[i] = NAN;
+      if (--left == 0) {
+        ++g;
+        left = gs;
+      }
     }
   }
 
-  // k rounds: the warp-wide largest key, then the lowest id that holds it
-  uint32_t best;
-  int slot, my_id = 0;
-  local_best(key, best, slot);
+  // k rounds: the token's largest key, the lowest lane that holds it, its first expert with it
+  float best = best_of<VPL>(x);
+  const int base = lane & ~(SUB - 1);
   for (int j = 0; j < k; ++j) {
-    const uint32_t b = __reduce_max_sync(0xffffffffu, best);
-    const unsigned cand = best == b ? static_cast<unsigned>(slot * 32 + lane) : 0xffffffffu;
-    const int id = static_cast<int>(__reduce_min_sync(0xffffffffu, cand));
-    if (lane == j) my_id = id;
-    if ((id & 31) == lane) {
+    const float b = sub_max<SUB>(best);
+    unsigned holders = __ballot_sync(0xffffffffu, best == b);
+    if (SUB < 32) holders = (holders >> base) & ((1u << (SUB & 31)) - 1u);
+    if (holders != 0u && sub == __ffs(holders) - 1) {
+      int at = 0;
 #pragma unroll
-      for (int i = 0; i < MAXV; ++i)
-        if (i == (id >> 5)) key[i] = kKeyTaken;
-      local_best(key, best, slot);
+      for (int i = VPL - 1; i >= 0; --i) at = x[i] == b ? i : at;
+      s_ids[warp][tok][j] = e0 + at;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) x[i] = i == at ? NAN : x[i];
+      best = best_of<VPL>(x);
     }
+    __syncwarp();
   }
 
-  // weights: lane j holds slot j
-  const float xj = lane < k ? clean_score(row[my_id]) : -INFINITY;
-  const bool live = xj > -INFINITY;
-  float p;
-  if (softmax) {
-    if (a.renormalise) top = warp_max(xj);
-    p = live ? expf(xj - top) : 0.0f;
-    if (!a.renormalise) p = live ? p / total : 0.0f;
-  } else {
-    const float m = a.renormalise ? fminf(warp_max(xj), 0.0f) : 0.0f;
-    p = live ? scaled_sigmoid(xj, m) : 0.0f;
+  // weights: lane sub holds slots sub, sub + SUB, ..
+  constexpr int SLOTS = (kMaxK + SUB - 1) / SUB;
+  float xs[SLOTS];
+  float m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    const int j = sub + q * SUB;
+    if (q * SUB >= k) break;
+    xs[q] = j < k ? clean_score(row[s_ids[warp][tok][j]]) : -INFINITY;
+    m = fmaxf(m, xs[q]);
   }
   if (a.renormalise) {
-    const float sum = warp_sum(p);
-    p = sum > 0.0f ? p / sum : 0.0f;
+    m = sub_max<SUB>(m);
+    top = m > -INFINITY ? m : 0.0f;
   }
-  if (lane < k) {
-    a.ids[static_cast<size_t>(t) * k + lane] = my_id;
-    a.w[static_cast<size_t>(t) * k + lane] = p * a.scale;
+  float sum = 0.0f;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    if (q * SUB >= k) break;
+    const bool live = xs[q] > -INFINITY;
+    xs[q] = !live ? 0.0f : softmax ? expf(xs[q] - top) : scaled_sigmoid(xs[q], a.renormalise ? fminf(m, 0.0f) : 0.0f);
+    sum += xs[q];
+  }
+  float factor = a.scale;
+  if (a.renormalise) {
+    sum = sub_sum<SUB>(sum);
+    factor = sum > 0.0f ? a.scale / sum : 0.0f;
+  } else if (softmax) {
+    factor = total > 0.0f ? a.scale / total : 0.0f;
+  }
+  if (!mine) return;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    const int j = sub + q * SUB;
+    if (q * SUB >= k) break;
+    if (j < k) {
+      a.ids[static_cast<size_t>(t) * k + j] = s_ids[warp][tok][j];
+      a.w[static_cast<size_t>(t) * k + j] = xs[q] * factor;
+    }
   }
 }
 
-// The gradient row is put together in shared memory and written once, coalesced.
-template <int MAXV, typename ST, bool WHOLE>
+// SUB lanes per token with VPL experts each, in runs of 16 bytes that alternate between the
+// lanes (whole lines are written).  Every lane writes its part of the row (0, or the
+// part that every expert has), then the selected experts' values are written over it:
+// __syncwarp orders the two.
+template <int VPL, int SUB, typename ST, bool WHOLE>
 __global__ void __launch_bounds__(kRouterWarps * 32)
     route_backward_kernel(const ST* __restrict__ scores, const int32_t* __restrict__ ids, const float* __restrict__ dw,
-                          ST* __restrict__ dscores, RouteArgs a, long long ld_d) {
-  extern __shared__ float s_rows[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kRouterWarps + warp;
+                          ST* __restrict__ dscores, RouteArgs a, long long ld_d, bool vec_d) {
+  constexpr int TOKENS = 32 / SUB;
+  constexpr int SLOTS = (kMaxK + SUB - 1) / SUB;  // lane sub holds slots sub, sub + SUB, ..
+  constexpr int PER = 16 / sizeof(ST);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & (SUB - 1);
+  const int t = (blockIdx.x * kRouterWarps + warp) * TOKENS + lane / SUB;
   dep_wait();
   dep_launch();
-  if (t >= a.T) return;
+  if ((blockIdx.x * kRouterWarps + warp) * TOKENS >= a.T) return;
+  const bool mine = t < a.T;  // a warp's last tokens may be missing: they shadow token T - 1 and write nothing
+  const int tr = mine ? t : a.T - 1;
+  static_assert(VPL % PER == 0, "whole runs");
   const int E = a.E, k = a.k;
-  const ST* row = scores + static_cast<size_t>(t) * a.ld;
-  float* g = s_rows + warp * E;
-  int id = -1;
-  float gj = 0.0f;
-  if (lane < k) {
-    id = ids[static_cast<size_t>(t) * k + lane];
-    gj = a.scale * dw[static_cast<size_t>(t) * k + lane];
-    if (id < 0 || id >= E) id = -1;  // no such expert: no part in the sums, nothing written
-  }
-  const float xj = id >= 0 ? clean_score(row[id]) : -INFINITY;
-  const bool live = xj > -INFINITY;
-  float x[MAXV];
+  const ST* row = scores + static_cast<size_t>(tr) * a.ld;
+  auto first = [&](int q) { return (q * SUB + sub) * PER; };  // expert of run q
+  float x[VPL];
   if (WHOLE) {
 #pragma unroll
-    for (int i = 0; i < MAXV; ++i) {
-      const int e = i * 32 + lane;
-      x[i] = e < E ? clean_score(row[e]) : -INFINITY;
+    for (int q = 0; q < VPL / PER; ++q) {
+      float run[PER];
+      load_scores<PER, ST>(run, row, first(q), E, a.vec);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) x[q * PER + i] = run[i];
     }
   }
+  int id[SLOTS];
+  float g[SLOTS], xs[SLOTS];
+  float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < MAXV; ++i)
-    if (i * 32 + lane < E) g[i * 32 + lane] = 0.0f;
-  __syncwarp();
+  for (int q = 0; q < SLOTS; ++q) {
+    if (q * SUB >= k) break;
+    const int j = sub + q * SUB;
+    id[q] = j < k ? ids[static_cast<size_t>(tr) * k + j] : -1;
+    if (id[q] < 0 || id[q] >= E) id[q] = -1;  // no such expert: no part in the sums, nothing written
+    g[q] = j < k ? a.scale * dw[static_cast<size_t>(tr) * k + j] : 0.0f;
+    xs[q] = id[q] >= 0 ? clean_score(row[id[q]]) : -INFINITY;
+    m = fmaxf(m, xs[q]);
+  }
 
-  float top = 0.0f, total = 0.0f, d = 0.0f;
+  // r: the weights before the constant (p, or p over its sum); d: factor of what they multiply
+  float top = 0.0f, total = 0.0f;
   if (WHOLE) {
-    float m = -INFINITY;
+    top = sub_max<SUB>(best_of<VPL>(x));
+    top = top > -INFINITY ? top : 0.0f;
 #pragma unroll
-    for (int i = 0; i < MAXV; ++i) m = fmaxf(m, x[i]);
-    m = warp_max(m);
-    top = m > -INFINITY ? m : 0.0f;
-#pragma unroll
-    for (int i = 0; i < MAXV; ++i) {
-      x[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.0f;
+    for (int i = 0; i < VPL; ++i) {
+      x[i] = expf(x[i] - top);  // 0 for a masked score
       total += x[i];
     }
-    total = warp_sum(total);
-    const float pj = live ? expf(xj - top) / total : 0.0f;
-    const float dot = warp_sum(pj * gj);
-    if (id >= 0) atomicAdd(g + id, gj);
-    __syncwarp();
+    total = sub_sum<SUB>(total);
+  } else if (a.renormalise) {
+    m = sub_max<SUB>(m);
+    top = m > -INFINITY ? m : 0.0f;
+  }
+  const bool softmax = a.score_fn == MOE_SCORE_SOFTMAX;
+  float r[SLOTS], sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < MAXV; ++i) {
-      const int e = i * 32 + lane;
-      if (e < E) g[e] = x[i] > 0.0f ? x[i] / total * (g[e] - dot) : 0.0f;
-    }
-  } else {
-    if (a.score_fn == MOE_SCORE_SOFTMAX) {  // renormalised
-      const float m = warp_max(xj);
-      const float e = live ? expf(xj - m) : 0.0f;
-      const float sum = warp_sum(e);
-      const float r = live ? e / sum : 0.0f;
-      d = r * (gj - warp_sum(r * gj));
-    } else {
-      const float m = a.renormalise ? fminf(warp_max(xj), 0.0f) : 0.0f;
-      const float p = live ? scaled_sigmoid(xj, m) : 0.0f;
-      const float q = live ? sigmoid_f32(-xj) : 0.0f;  // 1 - sigmoid without cancellation
-      if (a.renormalise) {
-        const float sum = warp_sum(p);
-        const float r = sum > 0.0f ? p / sum : 0.0f;
-        d = r * (gj - warp_sum(r * gj)) * q;
+  for (int q = 0; q < SLOTS; ++q) {
+    if (q * SUB >= k) break;
+    const bool live = xs[q] > -INFINITY;
+    r[q] = !live ? 0.0f : softmax ? expf(xs[q] - top) : scaled_sigmoid(xs[q], a.renormalise ? fminf(m, 0.0f) : 0.0f);
+    sum += r[q];
+  }
+  if (a.renormalise) sum = sub_sum<SUB>(sum);
+  if (WHOLE) sum = total;
+  const float inv = (WHOLE || a.renormalise) ? (sum > 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+  float dot = 0.0f;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    if (q * SUB >= k) break;
+    r[q] *= inv;
+    dot = fmaf(r[q], g[q], dot);
+  }
+  dot = WHOLE || a.renormalise ? sub_sum<SUB>(dot) : 0.0f;
+
+  ST* out = dscores + static_cast<size_t>(tr) * ld_d;
+  if (mine) {
+    const float rest = -dot * inv;
+#pragma unroll
+    for (int q = 0; q < VPL / PER; ++q) {
+      const int e = first(q);
+      alignas(16) ST v[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = from_f32<ST>(WHOLE ? x[q * PER + i] * rest : 0.0f);
+      if (vec_d) {
+        if (e < E) *reinterpret_cast<uint4*>(out + e) = *reinterpret_cast<const uint4*>(v);
       } else {
-        d = gj * p * q;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (e + i < E) out[e + i] = v[i];
       }
     }
-    if (id >= 0) atomicAdd(g + id, d);  // ids of a row differ, so each value is added to a zero once
   }
   __syncwarp();
-  ST* out = dscores + static_cast<size_t>(t) * ld_d;
 #pragma unroll
-  for (int i = 0; i < MAXV; ++i)
-    if (i * 32 + lane < E) out[i * 32 + lane] = from_f32<ST>(g[i * 32 + lane]);
+  for (int q = 0; q < SLOTS; ++q) {
+    if (q * SUB >= k) break;
+    float d = r[q] * (g[q] - dot);
+    if (!softmax) d *= xs[q] > -INFINITY ? sigmoid_f32(-xs[q]) : 0.0f;  // 1 - p without cancellation
+    if (mine && id[q] >= 0) out[id[q]] = from_f32<ST>(d);
+  }
 }
 
-inline int slots_of(int E) {
-  int v = 1;
-  while (v * 32 < E) v *= 2;
-  return v;
+template <int VPL, int SUB, typename ST>
+cudaError_t route_ex_of(const ST* scores, RouteArgs a, cudaStream_t s) {
+  constexpr int TOKENS = 32 / SUB * kRouterWarps;  // per block
+  const size_t smem = a.n_group > 1 ? TOKENS * (SUB * (VPL + 1) + 32) * sizeof(float) : 0;  // at most 37 KB
+  a.vec = a.ld % (16 / sizeof(ST)) == 0 && a.E % (16 / sizeof(ST)) == 0 && reinterpret_cast<uintptr_t>(scores) % 16 == 0;
+  a.bias_vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+  return launch_dependent(route_ex_kernel<VPL, SUB, ST>, dim3((a.T + TOKENS - 1) / TOKENS), dim3(kRouterWarps * 32),
+                          smem, s, scores, a);
 }
 
 template <typename ST>
 cudaError_t route_ex_of(const void* scores, const RouteArgs& a, cudaStream_t s) {
-  const dim3 grid((a.T + kRouterWarps - 1) / kRouterWarps);
-  const size_t smem = a.n_group > 1 ? static_cast<size_t>(kRouterWarps) * a.E * sizeof(float) : 0;
   const ST* sc = static_cast<const ST*>(scores);
-  switch (slots_of(a.E)) {
-    case 1: return launch_dependent(route_ex_kernel<1, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
-    case 2: return launch_dependent(route_ex_kernel<2, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
-    case 4: return launch_dependent(route_ex_kernel<4, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
-    case 8: return launch_dependent(route_ex_kernel<8, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
-    default: return launch_dependent(route_ex_kernel<16, ST>, grid, kRouterWarps * 32, smem, s, sc, a);
+  int lanes = 2;  // with 16 experts each
+  while (lanes * 16 < a.E) lanes *= 2;
+  // few rows: a warp each
+  if (static_cast<long long>(a.T) * lanes / 32 < kFewWarps) {
+    if (a.E <= 32) return route_ex_of<1, 32, ST>(sc, a, s);
+    if (a.E <= 64) return route_ex_of<2, 32, ST>(sc, a, s);
+    if (a.E <= 128) return route_ex_of<4, 32, ST>(sc, a, s);
+    if (a.E <= 256) return route_ex_of<8, 32, ST>(sc, a, s);
+    return route_ex_of<16, 32, ST>(sc, a, s);
+  }
+  switch (lanes) {
+    case 2: return route_ex_of<16, 2, ST>(sc, a, s);
+    case 4: return route_ex_of<16, 4, ST>(sc, a, s);
+    case 8: return route_ex_of<16, 8, ST>(sc, a, s);
+    case 16: return route_ex_of<16, 16, ST>(sc, a, s);
+    default: return route_ex_of<16, 32, ST>(sc, a, s);
   }
 }
 
-template <int MAXV, typename ST>
-cudaError_t route_backward_of(const ST* sc, const RouteArgs& a, const int32_t* ids, const float* dw, ST* ds, long long ld_d,
-                              dim3 grid, size_t smem, cudaStream_t s) {
-  if (a.score_fn == MOE_SCORE_SOFTMAX && !a.renormalise)
-    return launch_dependent(route_backward_kernel<MAXV, ST, true>, grid, kRouterWarps * 32, smem, s, sc, ids, dw, ds, a, ld_d);
-  return launch_dependent(route_backward_kernel<MAXV, ST, false>, grid, kRouterWarps * 32, smem, s, sc, ids, dw, ds, a, ld_d);
+template <int VPL, int SUB, typename ST, bool WHOLE>
+cudaError_t route_backward_of(const ST* sc, RouteArgs a, const int32_t* ids, const float* dw, ST* ds, long long ld_d,
+                              cudaStream_t s) {
+  constexpr int TOKENS = 32 / SUB * kRouterWarps;  // per block
+  constexpr int PER = 16 / sizeof(ST);
+  a.vec = a.ld % PER == 0 && a.E % PER == 0 && reinterpret_cast<uintptr_t>(sc) % 16 == 0;
+  const bool vec_d = ld_d % PER == 0 && a.E % PER == 0 && reinterpret_cast<uintptr_t>(ds) % 16 == 0;
+  const dim3 grid((a.T + TOKENS - 1) / TOKENS);
+  return launch_dependent(route_backward_kernel<VPL, SUB, ST, WHOLE>, grid, dim3(kRouterWarps * 32), 0, s, sc, ids, dw,
+                          ds, a, ld_d, vec_d);
 }
 
 template <typename ST>
 cudaError_t route_backward_of(const void* scores, const RouteArgs& a, const int32_t* ids, const float* dw,
                               void* dscores, long long ld_d, cudaStream_t s) {
-  const dim3 grid((a.T + kRouterWarps - 1) / kRouterWarps);
-  const size_t smem = static_cast<size_t>(kRouterWarps) * a.E * sizeof(float);
   const ST* sc = static_cast<const ST*>(scores);
   ST* ds = static_cast<ST*>(dscores);
-  switch (slots_of(a.E)) {
-    case 1: return route_backward_of<1, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
-    case 2: return route_backward_of<2, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
-    case 4: return route_backward_of<4, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
-    case 8: return route_backward_of<8, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
-    default: return route_backward_of<16, ST>(sc, a, ids, dw, ds, ld_d, grid, smem, s);
+  if (a.score_fn == MOE_SCORE_SOFTMAX && !a.renormalise) {
+    // 16 experts per lane, 8 lanes at least (a token's slots then take four registers at most)
+    if (a.E <= 64) return route_backward_of<8, 8, ST, true>(sc, a, ids, dw, ds, ld_d, s);
+    if (a.E <= 128) return route_backward_of<16, 8, ST, true>(sc, a, ids, dw, ds, ld_d, s);
+    if (a.E <= 256) return route_backward_of<16, 16, ST, true>(sc, a, ids, dw, ds, ld_d, s);
+    return route_backward_of<16, 32, ST, true>(sc, a, ids, dw, ds, ld_d, s);
   }
+  // only the selected scores are read, a chain of two loads: many warps
+  if (a.E <= 64) return route_backward_of<8, 8, ST, false>(sc, a, ids, dw, ds, ld_d, s);
+  if (a.E <= 128) return route_backward_of<8, 16, ST, false>(sc, a, ids, dw, ds, ld_d, s);
+  if (a.E <= 256) return route_backward_of<8, 32, ST, false>(sc, a, ids, dw, ds, ld_d, s);
+  return route_backward_of<16, 32, ST, false>(sc, a, ids, dw, ds, ld_d, s);
 }
 
 }  // namespace
