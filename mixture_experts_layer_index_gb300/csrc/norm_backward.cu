@@ -37,6 +37,10 @@ __device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec
   }
 }
 
+__host__ __device__ inline bool bias_in_smem(const NormArgs& a) {
+  return a.b_post && a.dgate && a.gate_kind != MOE_GATE_CHANNEL;
+}
+
 // Sums over tokens, per column: post1 = sum alpha G' u, post0 = sum alpha G', with G'
 // = G for a per-column gate g (then dw = g post1, db = g post0, dg = w post1 + b post0)
 // and G' = g G otherwise (dw = post1, db = post0); pre1 = sum dx u, pre0 = sum dx.
@@ -66,6 +70,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
   OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? rows : 0));
   float* s_post = reinterpret_cast<float*>(ring_x + (pre ? rows : 0));
   float* s_pre = s_post + pitch;
+  float* s_bias = s_pre + pitch;  // post norm's bias, for the gradient of a gate per token or value
   float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.nacc * sums_pitch;
   float* acc = a.acc_in_smem ? reinterpret_cast<float*>(s_mem) : part;
 
@@ -118,6 +123,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
       put_shared<A>(s_post, r, H, f);
       load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
       put_shared<A>(s_pre, r, H, f);
+      if (bias_in_smem(a)) {
+        load_columns<A>(f, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+        put_shared<A>(s_bias, r, H, f);
+      }
     }
   auto factor = [&](float(&f)[EPT], bool of_post, int r) {
     if constexpr (RING) copy_out<float, A>(f, of_post ? s_post : s_pre, r, H);
@@ -268,11 +277,18 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
       }
       if (a.dgate && !gate_c) {  // gradient of a gate per token or value: alpha G N(o)
         float w[EPT];
-        load_columns<A>(w, a.w_post, a.w_dtype, r, H, vec, 1.0f);
-        load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+        factor(w, true, r);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) w[i] *= oc[r][i];
+        if (a.b_post) {
+          if constexpr (RING) copy_out<float, A>(c, s_bias, r, H);
+          else load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+#pragma unroll
+          for (int i = 0; i < EPT; ++i) w[i] += c[i];
+        }
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-          c[i] = G[r][i] * fmaf(oc[r][i], w[i], c[i]);
+          c[i] = G[r][i] * w[i];
           d[2] += c[i];
         }
         if (gate_f) store_row<OT, A>(a.dgate, a.o_dtype, at_o, r, H, vec, c);
@@ -428,9 +444,9 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
   a.depth = 0;
   if (A != PLAIN) {
     // a row that is worked on and, where they fit with the resident blocks, one or two
-    // on their way; 128 KB at most for one row, beside 64 KB of factors
+    // on their way; 128 KB at most for one row, beside 96 KB of factors
     const size_t row = pitch * (sizeof(OT) + (a.dh_out ? sizeof(HT) : 0) + (a.pre ? sizeof(HT) + sizeof(OT) : 0));
-    const size_t factors = 2 * pitch * sizeof(float);
+    const size_t factors = (bias_in_smem(a) ? 3 : 2) * pitch * sizeof(float);
     a.depth = 3;
     auto fits = [&](size_t bytes, int blocks) { return bytes <= kSmemMax && (bytes + 2048) * blocks <= kSmemSm; };
     while (a.depth > 1 && !fits(a.depth * row + factors, per_sm)) --a.depth;

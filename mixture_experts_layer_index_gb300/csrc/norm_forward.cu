@@ -25,11 +25,14 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
   const int pitch = slot_pitch<A>(H, blockDim.x);
-  // ring | factors of the post and of the pre norm, each column with its thread
+  // ring | factors of the post and of the pre norm, then their biases where there are any;
+  // each column with its thread
   HT* ring_h = reinterpret_cast<HT*>(s_ring);
   OT* ring_o = reinterpret_cast<OT*>(ring_h + a.depth * pitch);
   float* s_post = reinterpret_cast<float*>(ring_o + a.depth * pitch);
   float* s_pre = s_post + pitch;
+  float* s_bpost = s_pre + pitch;
+  float* s_bpre = s_bpost + (a.b_post ? pitch : 0);
   for (int i = threadIdx.x; i < 2 * Sum::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
   __syncthreads();
   Sum block_sum{s_sum, 0};
@@ -54,8 +57,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 
   // factor of the normalised (or plain) o, and of the normalised h'
   const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
-  auto post_factor = [&](float(&f)[EPT], int r) {
-    load_columns<A>(f, a.w_post, a.w_dtype, r, H, vec, 1.0f);
+  auto post_column = [&](float(&f)[EPT], const void* v, float none, int r) {
+    load_columns<A>(f, v, a.w_dtype, r, H, vec, none);
     if (gate_c) {
       float g[EPT];
       load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
@@ -67,10 +70,18 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
-      post_factor(f, r);
+      post_column(f, a.w_post, 1.0f, r);
       put_shared<A>(s_post, r, H, f);
       load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
       put_shared<A>(s_pre, r, H, f);
+      if (a.b_post) {
+        post_column(f, a.b_post, 0.0f, r);
+        put_shared<A>(s_bpost, r, H, f);
+      }
+      if (a.b_pre) {
+        load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
+        put_shared<A>(s_bpre, r, H, f);
+      }
     }
 
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
@@ -120,17 +131,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
     for (int r = 0; r < RUNS; ++r) {
       float c[EPT];
       if constexpr (RING) copy_out<float, A>(c, s_post, r, H);
-      else post_factor(c, r);
+      else post_column(c, a.w_post, 1.0f, r);
 #pragma unroll
       for (int i = 0; i < EPT; ++i) v[r][i] *= rs * c[i];
       if (a.b_post) {
-        load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
-        if (gate_c) {
-          float g[EPT];
-          load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
-#pragma unroll
-          for (int i = 0; i < EPT; ++i) c[i] *= g[i];
-        }
+        if constexpr (RING) copy_out<float, A>(c, s_bpost, r, H);
+        else post_column(c, a.b_post, 0.0f, r);
 #pragma unroll
         for (int i = 0; i < EPT; ++i) v[r][i] = fmaf(scale, c[i], v[r][i]);
       }
@@ -156,7 +162,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
         for (int i = 0; i < EPT; ++i) v[r][i] *= rp * c[i];
         if (a.b_pre) {
-          load_columns<A>(c, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
+          if constexpr (RING) copy_out<float, A>(c, s_bpre, r, H);
+          else load_columns<A>(c, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
 #pragma unroll
           for (int i = 0; i < EPT; ++i) v[r][i] += c[i];
         }
@@ -179,10 +186,11 @@ cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
         cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemMax));
     if (attr != cudaSuccess) return attr;
-    const size_t pitch = slot_pitch<A>(a.H, threads), row = pitch * (sizeof(HT) + sizeof(OT)), factors = 2 * pitch * sizeof(float);
-    a.depth = 3;  // two rows on their way; one where shared memory has no room for them beside the resident blocks
-    if ((3 * row + factors + 2048) * per_sm > kSmemMax) a.depth = 2;
-    smem = a.depth * row + factors;  // at most 2 x 64 KB + 64 KB
+    const size_t pitch = slot_pitch<A>(a.H, threads), row = pitch * (sizeof(HT) + sizeof(OT));
+    const size_t factors = (2 + (a.b_post ? 1 : 0) + (a.b_pre ? 1 : 0)) * pitch * sizeof(float);
+    // two rows on their way; one, or none, where shared memory has no room for them beside the resident blocks
+    a.depth = (3 * row + factors + 2048) * per_sm <= kSmemMax ? 3 : 2 * row + factors <= kSmemMax ? 2 : 1;
+    smem = a.depth * row + factors;  // at most 64 KB + 128 KB
     while (per_sm > 1 && (smem + 2048) * per_sm > kSmemMax) --per_sm;
   }
   const int cap = 152 * per_sm;
