@@ -122,6 +122,7 @@ _SIGS = {
     "moe_forward_views": (_i, [_P, _vp, _sz, ctypes.POINTER(moe_views)]),
     "moe_workspace_size_ex": (_sz, [_P, _O]),
     "moe_forward_ex": (_i, [_P, _O, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_forward_routed": (_i, [_P, _O, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_forward_views_ex": (_i, [_P, _O, _vp, _sz, ctypes.POINTER(moe_views)]),
     "moe_round_bf16": (_i, [_vp, _vp, _sz, _vp]),
     "moe_mx_blocked_bytes": (_sz, [_i, _i, _i]),
@@ -274,6 +275,15 @@ def moe_forward_ex(p: moe_problem, opt: Optional[moe_forward_options], x, scores
     _check(lib().moe_forward_ex(ctypes.byref(p), _opt_ref(opt), _ptr(x), _ptr(scores), _ptr(w1), _ptr(w2),
                                _ptr(w1_scale), _ptr(w2_scale), _ptr(y), _ptr(ws), nb, _stream(stream)),
            "moe_forward_ex")
+
+
+def moe_forward_routed(p: moe_problem, opt: Optional[moe_forward_options], x, ids, w, w1, w2, w1_scale, w2_scale, y,
+                       ws, ws_bytes=None, stream=None) -> None:
+    """moe_forward_ex with a given routing (ids, w), e.g. of moe_route_ex."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    _check(lib().moe_forward_routed(ctypes.byref(p), _opt_ref(opt), _ptr(x), _ptr(ids), _ptr(w), _ptr(w1), _ptr(w2),
+                                    _ptr(w1_scale), _ptr(w2_scale), _ptr(y), _ptr(ws), nb, _stream(stream)),
+           "moe_forward_routed")
 
 
 def moe_forward_views_ex(p: moe_problem, opt: Optional[moe_forward_options], ws, ws_bytes=None) -> moe_views:

@@ -109,6 +109,22 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ rd_prep
+// The given routing of tokens handled by this block's warps: ids into s_ids.  An id
+// outside [0, E) is replaced by expert 0 with weight 0, so that it adds nothing; the
+// block that owns the outputs (hdr given) records it and writes ids and weights.
+__device__ __forceinline__ void take_routes(const DecodeArgs& a, int* s_ids, DeviceHeader* hdr) {
+  for (int r = threadIdx.x; r < a.R; r += blockDim.x) {
+    const int e = a.ids_in[r];
+    const bool ok = e >= 0 && e < a.E;
+    s_ids[r] = ok ? e : 0;
+    if (hdr) {
+      if (!ok) record_status(hdr, kStatusBounds, static_cast<unsigned int>(r));
+      a.ids[r] = s_ids[r];
+      a.w[r] = ok ? a.w_in[r] : 0.0f;
+    }
+  }
+}
+
 template <int MAXV>
 __global__ void __launch_bounds__(1024) rd_prep_kernel(DecodeArgs a) {
   __shared__ int s_ids[kRouteDirectMaxRoutes];
@@ -131,8 +147,11 @@ __global__ void __launch_bounds__(1024) rd_prep_kernel(DecodeArgs a) {
     // a few hundred GB/s, hence the spread over many CTAs.
     if (warp == 0)
       for (int i = lane; i < kMaxE / 32; i += 32) s_seen[i] = 0u;
-    for (int t = warp; t < T; t += nwarps)
-      route_one_token<MAXV>(a.scores + static_cast<size_t>(t) * E, E, k, nullptr, nullptr, s_ids + t * k);
+    if (a.ids_in)
+      take_routes(a, s_ids, nullptr);
+    else
+      for (int t = warp; t < T; t += nwarps)
+        route_one_token<MAXV>(a.scores + static_cast<size_t>(t) * E, E, k, nullptr, nullptr, s_ids + t * k);
     __syncthreads();
     const long long w1_bytes = 2ll * a.I * H;
     const int maxp = static_cast<int>(kW1PrefetchBytes / w1_bytes < kMaxE ? kW1PrefetchBytes / w1_bytes : kMaxE);
@@ -190,10 +209,15 @@ __global__ void __launch_bounds__(1024) rd_prep_kernel(DecodeArgs a) {
       xv[j] = i < n8 ? __ldg(x8 + i) : make_uint4(0, 0, 0, 0);
     }
   }
-  // 1. routing: one warp per token
-  for (int t = warp; t < T; t += nwarps)
-    route_one_token<MAXV>(a.scores + static_cast<size_t>(t) * E, E, k, a.ids + static_cast<size_t>(t) * k,
-                           a.w + static_cast<size_t>(t) * k, s_ids + t * k);
+  // 1. routing: one warp per token (or the given one; the header is cleared first)
+  if (a.ids_in) {
+    __syncthreads();
+    take_routes(a, s_ids, a.hdr);
+  } else {
+    for (int t = warp; t < T; t += nwarps)
+      route_one_token<MAXV>(a.scores + static_cast<size_t>(t) * E, E, k, a.ids + static_cast<size_t>(t) * k,
+                             a.w + static_cast<size_t>(t) * k, s_ids + t * k);
+  }
   __syncthreads();
   if (warp == 0) {
     // 2a. distinct experts in first-use order and the routes of each in route

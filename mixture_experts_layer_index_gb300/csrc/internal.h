@@ -72,11 +72,13 @@ bool plan_forward(const moe_problem& p, ForwardLayout* out, int S = 0);
 
 // ------------------------------------------------------------------ launchers
 // All return cudaSuccess or the launch error; none synchronises.
+// Without `route`, ids_in is ranked (and copied to ids_out, with w_in to w_out, where given).
 // amax_x (bf16, amax_n values) non-null: the same launch also records the
 // per-tensor amax of x in hdr->amax_x (FP8 per-tensor forward).
 cudaError_t launch_route_rank(const float* scores, const int32_t* ids_in, int T, int E, int k, int32_t* ids_out,
                               float* w_out, int32_t* lrank, int32_t* blockcounts, DeviceHeader* hdr, bool route,
-                              bool rank, cudaStream_t s, const void* amax_x = nullptr, size_t amax_n = 0);
+                              bool rank, cudaStream_t s, const void* amax_x = nullptr, size_t amax_n = 0,
+                              const float* w_in = nullptr);
 // With tiles: the routed experts' tiles, then (S > 0) ceil(T/BM) tiles per shared
 // expert s, numbered expert E + s, over rows [Rr + s*T, Rr + (s+1)*T) (Rr = T*k).
 cudaError_t launch_scan_tiles(int32_t* blockcounts, int nblk, int E, int32_t* counts, int32_t* offsets,
@@ -183,6 +185,8 @@ struct DecodeArgs {
   moe_quant quant;
   const void* x;
   const float* scores;
+  const int32_t* ids_in;  // a given routing (with w_in) in the place of scores, or null
+  const float* w_in;
   const uint8_t* w1;
   const uint8_t* w2;
   const float* w1_scale;

@@ -393,9 +393,11 @@ size_t moe_workspace_size_ex(const moe_problem* p, const moe_forward_options* op
   return L.total;
 }
 
-moe_status moe_forward_ex(const moe_problem* pp, const moe_forward_options* opt, const void* x, const float* scores,
-                          const void* w1, const void* w2, const float* w1_scale, const float* w2_scale, void* y,
-                          void* ws, size_t ws_bytes, moe_stream_t stream) {
+// The forward with routing from `scores`, or with the given routing (ids_in, w_in).
+static moe_status forward_impl(const moe_problem* pp, const moe_forward_options* opt, const void* x,
+                               const float* scores, const int32_t* ids_in, const float* w_in, const void* w1,
+                               const void* w2, const float* w1_scale, const float* w2_scale, void* y, void* ws,
+                               size_t ws_bytes, moe_stream_t stream) {
   if (!pp) return MOE_ERR_INVALID_ARG;
   const moe_problem p = *pp;
   const moe_forward_options o = opt ? *opt : moe_forward_options{};
@@ -407,7 +409,8 @@ moe_status moe_forward_ex(const moe_problem* pp, const moe_forward_options* opt,
   const moe_status vs = validate_shape(p, S);
   if (vs != MOE_OK) return vs;
   if (p.T == 0) return MOE_OK;
-  if (!x || !scores || !w1 || !w2 || !y) return MOE_ERR_INVALID_ARG;
+  if (!x || (!scores && (!ids_in || !w_in)) || !w1 || !w2 || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned(ids_in, 4) || !aligned(w_in, 4)) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(scores, 4))
     return MOE_ERR_INVALID_ARG;
   if (p.quant == MOE_BF16) {
@@ -446,8 +449,8 @@ moe_status moe_forward_ex(const moe_problem* pp, const moe_forward_options* opt,
     int32_t* num_tiles = at<int32_t*>(ws, L.num_tiles);
     e = launch_reset_header(hdr, s);
     if (e == cudaSuccess)
-      e = launch_route_rank(scores, nullptr, p.T, p.E, p.k, ids, w, lrank, bc, hdr, true, true, s,
-                            p.quant == MOE_FP8_PER_TENSOR ? x : nullptr, static_cast<size_t>(p.T) * p.H);
+      e = launch_route_rank(scores, ids_in, p.T, p.E, p.k, ids, w, lrank, bc, hdr, ids_in == nullptr, true, s,
+                            p.quant == MOE_FP8_PER_TENSOR ? x : nullptr, static_cast<size_t>(p.T) * p.H, w_in);
     if (e == cudaSuccess)
       e = launch_scan_tiles(bc, L.shuf.nblk, p.E, counts, offsets, tiles, num_tiles, L.max_tiles, kGemmBM, nullptr,
                             hdr, s, p.T, S, p.T * p.k, p.quant == MOE_MXFP8 ? at<int32_t*>(ws, L.padbase) : nullptr);
@@ -535,6 +538,7 @@ moe_status moe_forward_ex(const moe_problem* pp, const moe_forward_options* opt,
     d.T = p.T; d.E = p.E; d.k = p.k; d.H = p.H; d.I = p.I; d.R = p.T * p.k;
     d.quant = p.quant;
     d.x = x; d.scores = scores;
+    d.ids_in = ids_in; d.w_in = w_in;
     d.w1 = static_cast<const uint8_t*>(w1);
     d.w2 = static_cast<const uint8_t*>(w2);
     d.w1_scale = w1_scale; d.w2_scale = w2_scale;
@@ -556,6 +560,19 @@ moe_status moe_forward_ex(const moe_problem* pp, const moe_forward_options* opt,
     }
   }
   return from_cuda(e);
+}
+
+moe_status moe_forward_ex(const moe_problem* p, const moe_forward_options* opt, const void* x, const float* scores,
+                          const void* w1, const void* w2, const float* w1_scale, const float* w2_scale, void* y,
+                          void* ws, size_t ws_bytes, moe_stream_t stream) {
+  return forward_impl(p, opt, x, scores, nullptr, nullptr, w1, w2, w1_scale, w2_scale, y, ws, ws_bytes, stream);
+}
+
+moe_status moe_forward_routed(const moe_problem* p, const moe_forward_options* opt, const void* x, const int32_t* ids,
+                              const float* w, const void* w1, const void* w2, const float* w1_scale,
+                              const float* w2_scale, void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (p && p->T > 0 && (!ids || !w)) return MOE_ERR_INVALID_ARG;
+  return forward_impl(p, opt, x, nullptr, ids, w, w1, w2, w1_scale, w2_scale, y, ws, ws_bytes, stream);
 }
 
 size_t moe_mx_weight_scales_bytes(int E, int H, int I, int which) {

@@ -101,9 +101,12 @@ __device__ void amax_blocks(const uint4* __restrict__ x, size_t n8, int b, int n
   }
 }
 
+// ROUTE: ids and weights from the scores; otherwise the given ids (and, for the forward
+// with a given routing, weights), copied to ids_out / w_out where those are given.
 template <int MAXV, bool ROUTE, bool RANK>
 __global__ void __launch_bounds__(kRouteThreads) route_rank_kernel(
-    const float* __restrict__ scores, const int32_t* __restrict__ ids_in, int T, int E, int k, int TB,
+    const float* __restrict__ scores, const int32_t* __restrict__ ids_in, const float* __restrict__ w_in, int T, int E,
+    int k, int TB,
     int32_t* __restrict__ ids_out, float* __restrict__ w_out, int32_t* __restrict__ lrank,
     int32_t* __restrict__ blockcounts, DeviceHeader* hdr, const uint4* __restrict__ amax_x, size_t amax_n8,
     int nblk) {
@@ -138,7 +141,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_rank_kernel(
       for (int i = 0; i < MAXV; ++i) cur[i] = nxt[i];
     }
   } else {
-    for (int i = tid; i < nr; i += kRouteThreads) s_ids[i] = ids_in[r0 + i];
+    for (int i = tid; i < nr; i += kRouteThreads) {
+      const int e = ids_in[r0 + i];
+      s_ids[i] = e;
+      if (ids_out) ids_out[r0 + i] = e;
+      if (w_out) w_out[r0 + i] = e >= 0 && e < E ? w_in[r0 + i] : 0.0f;  // no such expert: adds nothing
+    }
   }
   if constexpr (RANK) rank_block(s_ids, s_lr, hist, E, TB * k, nr, r0, blk, lrank, blockcounts, hdr);
 }
@@ -348,11 +356,11 @@ static cudaError_t rr_smem_attr() {
 
 template <bool ROUTE, bool RANK>
 static cudaError_t launch_rr(int maxv, dim3 grid, size_t smem, cudaStream_t s, const float* scores,
-                             const int32_t* ids_in, int T, int E, int k, int TB, int32_t* ids_out, float* w_out,
+                             const int32_t* ids_in, const float* w_in, int T, int E, int k, int TB, int32_t* ids_out, float* w_out,
                              int32_t* lrank, int32_t* bc, DeviceHeader* hdr, const uint4* ax, size_t an8, int nblk) {
 #define MOE_RR(V)                                                                                          \
   if (const cudaError_t ae = rr_smem_attr<V, ROUTE, RANK>()) return ae;                                    \
-  route_rank_kernel<V, ROUTE, RANK><<<grid, kRouteThreads, smem, s>>>(scores, ids_in, T, E, k, TB, ids_out, \
+  route_rank_kernel<V, ROUTE, RANK><<<grid, kRouteThreads, smem, s>>>(scores, ids_in, w_in, T, E, k, TB, ids_out, \
                                                                      w_out, lrank, bc, hdr, ax, an8, nblk)
   switch (maxv) {
     case 1: MOE_RR(1); break;
@@ -367,7 +375,7 @@ static cudaError_t launch_rr(int maxv, dim3 grid, size_t smem, cudaStream_t s, c
 
 cudaError_t launch_route_rank(const float* scores, const int32_t* ids_in, int T, int E, int k, int32_t* ids_out,
                               float* w_out, int32_t* lrank, int32_t* blockcounts, DeviceHeader* hdr, bool route,
-                              bool rank, cudaStream_t s, const void* amax_x, size_t amax_n) {
+                              bool rank, cudaStream_t s, const void* amax_x, size_t amax_n, const float* w_in) {
   if (T <= 0) return cudaSuccess;
   const int TB = route_tokens_per_block(k);
   const int nblk = (T + TB - 1) / TB;
@@ -382,9 +390,9 @@ cudaError_t launch_route_rank(const float* scores, const int32_t* ids_in, int T,
   const uint4* ax = static_cast<const uint4*>(amax_x);
   stage_begin("route_rank", s);
   cudaError_t err;
-  if (route && rank) err = launch_rr<true, true>(maxv, grid, smem, s, scores, ids_in, T, E, k, TB, ids_out, w_out, lrank, blockcounts, hdr, ax, an8, nblk);
-  else if (route) err = launch_rr<true, false>(maxv, grid, smem, s, scores, ids_in, T, E, k, TB, ids_out, w_out, lrank, blockcounts, hdr, ax, an8, nblk);
-  else err = launch_rr<false, true>(maxv, grid, smem, s, scores, ids_in, T, E, k, TB, ids_out, w_out, lrank, blockcounts, hdr, ax, an8, nblk);
+  if (route && rank) err = launch_rr<true, true>(maxv, grid, smem, s, scores, ids_in, w_in, T, E, k, TB, ids_out, w_out, lrank, blockcounts, hdr, ax, an8, nblk);
+  else if (route) err = launch_rr<true, false>(maxv, grid, smem, s, scores, ids_in, w_in, T, E, k, TB, ids_out, w_out, lrank, blockcounts, hdr, ax, an8, nblk);
+  else err = launch_rr<false, true>(maxv, grid, smem, s, scores, ids_in, w_in, T, E, k, TB, ids_out, w_out, lrank, blockcounts, hdr, ax, an8, nblk);
   stage_end(s);
   return err;
 }
