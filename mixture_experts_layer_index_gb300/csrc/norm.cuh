@@ -52,6 +52,40 @@ __device__ __forceinline__ void cp_async_wait(int depth) {
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Two fp32 values that packed instructions (mul / add / fma .rn.f32x2, each half rounded
+// like the scalar one) work on: half the instructions of the elementwise parts.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v)); }
+__device__ __forceinline__ float halves_sum(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+constexpr int PPT = EPT / 2;  // pairs per run
+
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
@@ -180,20 +214,6 @@ __device__ __forceinline__ void put_shared(float* slot, int run, int H, const fl
   }
 }
 
-// v = 0 for columns past H (after a mean was taken off).
-template <Access A>
-__device__ __forceinline__ void clear_past(float (&v)[EPT], int run, int H, bool vec) {
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    if (col_of<A>(run, 0, vec) >= H)
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPT; ++i)
-      if (col_of<A>(run, i, vec) >= H) v[i] = 0.0f;
-  }
-}
-
 // A thread's columns of a per-column vector (16-byte aligned where the rows are read
 // 16 bytes at a time); `none` where there is no vector.
 template <Access A>
@@ -251,6 +271,50 @@ __device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, 
     for (int i = 0; i < EPT; ++i) {
       v[i] = as_f32(slot[col_of<A>(r, i, false)]);  // past column H the ring holds zeros
     }
+  }
+}
+
+// The same as pairs.
+__device__ __forceinline__ void pairs_of(F2 (&p)[PPT], const float (&v)[EPT]) {
+#pragma unroll
+  for (int i = 0; i < PPT; ++i) p[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ void values_of(float (&v)[EPT], const F2 (&p)[PPT]) {
+#pragma unroll
+  for (int i = 0; i < PPT; ++i) split(p[i], v[2 * i], v[2 * i + 1]);
+}
+template <typename T, Access A>
+__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r, int H) {
+  float v[EPT];
+  copy_out<T, A>(v, slot, r, H);
+  pairs_of(p, v);
+}
+template <Access A>
+__device__ __forceinline__ void load_row(F2 (&p)[PPT], const void* q, int dtype, size_t at, int run, int H, bool vec) {
+  float v[EPT];
+  load_row<A>(v, q, dtype, at, run, H, vec);
+  pairs_of(p, v);
+}
+template <typename T, Access A>
+__device__ __forceinline__ void store_row(void* q, int dtype, size_t at, int run, int H, bool vec, const F2 (&p)[PPT]) {
+  float v[EPT];
+  values_of(v, p);
+  store_row<T, A>(q, dtype, at, run, H, vec, v);
+}
+// v = 0 for columns past H (after a mean was taken off).
+template <Access A>
+__device__ __forceinline__ void clear_past(F2 (&p)[PPT], int run, int H, bool vec) {
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    if (col_of<A>(run, 0, vec) >= H)
+#pragma unroll
+      for (int i = 0; i < PPT; ++i) p[i] = f2(0.0f);
+  } else {
+    float v[EPT];
+    values_of(v, p);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i)
+      if (col_of<A>(run, i, vec) >= H) v[i] = 0.0f;
+    pairs_of(p, v);
   }
 }
 

@@ -18,7 +18,9 @@ namespace {
 
 // A block's column sums, one vector of `pitch` floats each.
 template <Access A>
-__device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec, const float (&v)[EPT]) {
+__device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec, const F2 (&p2)[PPT]) {
+  float v[EPT];
+  values_of(v, p2);
   if (A == VEC16 || (A == PLAIN && vec)) {
     const int c = col_of<A>(run, 0, vec);
     if (c >= H) return;
@@ -44,11 +46,15 @@ __host__ __device__ inline bool bias_in_smem(const NormArgs& a) {
 // Sums over tokens, per column: post1 = sum alpha G' u, post0 = sum alpha G', with G'
 // = G for a per-column gate g (then dw = g post1, db = g post0, dg = w post1 + b post0)
 // and G' = g G otherwise (dw = post1, db = post0); pre1 = sum dx u, pre0 = sum dx.
-// ZERO: post0 or pre0 are wanted (their registers cost a resident block).
-constexpr int min_blocks(int maxt, bool zero) { return maxt <= 128 ? (zero ? 3 : 4) : maxt <= 256 && !zero ? 2 : 1; }
+// GENERAL: layer norms, post0 or pre0, a gate per token or value; otherwise RMS norms with
+// at most a per-column gate, which need fewer registers (a resident block more) and
+// instructions.
+constexpr int min_blocks(int maxt, bool general) {
+  return maxt <= 128 ? (general ? 3 : 4) : maxt <= 256 && !general ? 2 : 1;
+}
 
-template <typename HT, typename OT, Access A, int MAXT, bool ZERO>
-__global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_kernel(NormArgs a) {
+template <typename HT, typename OT, Access A, int MAXT, bool GENERAL>
+__global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward_kernel(NormArgs a) {
   constexpr bool RING = A != PLAIN;
   using Sum = BlockSum<4, MAXT>;
   __shared__ __align__(16) float s_sum[2][4][Sum::W];
@@ -128,16 +134,21 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
         put_shared<A>(s_bias, r, H, f);
       }
     }
-  auto factor = [&](float(&f)[EPT], bool of_post, int r) {
-    if constexpr (RING) copy_out<float, A>(f, of_post ? s_post : s_pre, r, H);
-    else if (of_post) post_factor(f, r);
-    else load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+  auto factor = [&](F2(&f)[PPT], bool of_post, int r) {
+    if constexpr (RING) {
+      copy_out<float, A>(f, of_post ? s_post : s_pre, r, H);
+    } else {
+      float v[EPT];
+      if (of_post) post_factor(v, r);
+      else load_columns<A>(v, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+      pairs_of(f, v);
+    }
   };
-  float post1[RUNS][EPT], post0[RUNS][EPT], pre1[RUNS][EPT], pre0[RUNS][EPT];  // with a ring
+  F2 post1[RUNS][PPT], post0[RUNS][PPT], pre1[RUNS][PPT], pre0[RUNS][PPT];  // with a ring
 #pragma unroll
   for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) post1[r][i] = post0[r][i] = pre1[r][i] = pre0[r][i] = 0.0f;
+    for (int i = 0; i < PPT; ++i) post1[r][i] = post0[r][i] = pre1[r][i] = pre0[r][i] = f2(0.0f);
   if (!RING)
     for (int j = 0; j < a.nacc; ++j)
 #pragma unroll
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
       fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
     }
-    float hc[RUNS][EPT], oc[RUNS][EPT], dx[RUNS][EPT], G[RUNS][EPT];
+    F2 hc[RUNS][PPT], oc[RUNS][PPT], dx[RUNS][PPT], G[RUNS][PPT];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r, H);
@@ -170,27 +181,28 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
         }
       }
     }
-    if (layer_pre || layer_post) {
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (GENERAL && (layer_pre || layer_post)) {
+      F2 sh = f2(0.0f), so = f2(0.0f);
 #pragma unroll
       for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          if (layer_pre) s[0] += hc[r][i];
-          s[1] += oc[r][i];
+        for (int i = 0; i < PPT; ++i) {
+          if (layer_pre) sh = sh + hc[r][i];
+          so = so + oc[r][i];
         }
+      float s[4] = {halves_sum(sh), halves_sum(so), 0.0f, 0.0f};
       block_sum(s);
-      const float mh = s[0] * inv_h, mo = s[1] * inv_h;
+      const F2 mh = f2(-s[0] * inv_h), mo = f2(-s[1] * inv_h);
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
         if (layer_pre) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) hc[r][i] -= mh;
+          for (int i = 0; i < PPT; ++i) hc[r][i] = hc[r][i] + mh;
           clear_past<A>(hc[r], r, H, vec);
         }
         if (layer_post) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) oc[r][i] -= mo;
+          for (int i = 0; i < PPT; ++i) oc[r][i] = oc[r][i] + mo;
           clear_past<A>(oc[r], r, H, vec);
         }
       }
@@ -198,29 +210,30 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
     // second moments, and the two means of the pre norm's gradient
     float ro = 1.0f, rs = 0.0f, m1 = 0.0f, m0 = 0.0f;
     if (pre || post) {
-      float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      F2 q0 = f2(0.0f), q1 = q0, q2 = q0, q3 = q0;
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
         if (pre) {
-          float f[EPT];
+          F2 f[PPT];
           factor(f, false, r);
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) {
-            const float dxw = dx[r][i] * f[i];
-            s[0] = fmaf(hc[r][i], hc[r][i], s[0]);
-            s[1] = fmaf(dxw, hc[r][i], s[1]);
-            if (layer_pre) s[2] += dxw;
+          for (int i = 0; i < PPT; ++i) {
+            const F2 dxw = dx[r][i] * f[i];
+            q0 = fma2(hc[r][i], hc[r][i], q0);
+            q1 = fma2(dxw, hc[r][i], q1);
+            if (GENERAL) q2 = q2 + dxw;
           }
         }
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) s[3] = fmaf(oc[r][i], oc[r][i], s[3]);
+        for (int i = 0; i < PPT; ++i) q3 = fma2(oc[r][i], oc[r][i], q3);
       }
+      float s[4] = {halves_sum(q0), halves_sum(q1), GENERAL ? halves_sum(q2) : 0.0f, halves_sum(q3)};
       block_sum(s);
       if (post) ro = inv_std(s[3], inv_h, a.eps);
       if (pre) {
         rs = inv_std(s[0], inv_h, a.eps);
-        m1 = s[1] * rs * inv_h;  // mean(dx w u)
-        m0 = s[2] * inv_h;       // mean(dx w); 0 for RMS
+        m1 = s[1] * rs * inv_h;                 // mean(dx w u)
+        m0 = layer_pre ? s[2] * inv_h : 0.0f;   // mean(dx w)
       }
     }
 #pragma unroll
@@ -230,108 +243,122 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, ZERO)) norm_backward_ke
         else load_row<A>(G[r], a.dh_out, a.h_dtype, at_h, r, H, vec);
       } else {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) G[r][i] = 0.0f;
+        for (int i = 0; i < PPT; ++i) G[r][i] = f2(0.0f);
       }
       if (pre) {
-        float f[EPT];
+        F2 f[PPT];
         factor(f, false, r);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-          const float u = hc[r][i] * rs;
-          G[r][i] = fmaf(rs, fmaf(-u, m1, fmaf(dx[r][i], f[i], -m0)), G[r][i]);
+        for (int i = 0; i < PPT; ++i) {
+          const F2 u = hc[r][i] * f2(rs);
+          F2 d = dx[r][i] * f[i];
+          if (GENERAL) d = d + f2(-m0);
+          G[r][i] = fma2(f2(rs), fma2(u, f2(-m1), d), G[r][i]);
           hc[r][i] = u;
         }
-        clear_past<A>(G[r], r, H, vec);
+        if (GENERAL) clear_past<A>(G[r], r, H, vec);
         if (RING) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) pre1[r][i] = fmaf(dx[r][i], hc[r][i], pre1[r][i]);
-          if (ZERO)
+          for (int i = 0; i < PPT; ++i) pre1[r][i] = fma2(dx[r][i], hc[r][i], pre1[r][i]);
+          if (GENERAL)
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) pre0[r][i] += dx[r][i];
+            for (int i = 0; i < PPT; ++i) pre0[r][i] = pre0[r][i] + dx[r][i];
         } else {
           if (a.acc_pre0 >= 0) add_columns<A>(acc + a.acc_pre0 * sums_pitch, r, H, vec, dx[r]);
           if (a.acc_pre1 >= 0) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) dx[r][i] *= hc[r][i];
+            for (int i = 0; i < PPT; ++i) dx[r][i] = dx[r][i] * hc[r][i];
             add_columns<A>(acc + a.acc_pre1 * sums_pitch, r, H, vec, dx[r]);
           }
         }
       }
       if (a.dh) {
-        float d[EPT];
+        F2 d[PPT];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) d[i] = a.beta * G[r][i];
+        for (int i = 0; i < PPT; ++i) d[i] = f2(a.beta) * G[r][i];
         store_row<HT, A>(a.dh, a.h_dtype, at_h, r, H, vec, d);
       }
     }
     // the block's side: alpha G is the gradient of g N(o); G becomes dn w
     const float gt = gate_t ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
-    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    F2 d0 = f2(0.0f), d1 = d0, d2 = d0;
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      float c[EPT];
+      F2 c[PPT];
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        G[r][i] *= a.alpha;
-        oc[r][i] *= ro;  // u of the post norm, or o itself
+      for (int i = 0; i < PPT; ++i) {
+        G[r][i] = G[r][i] * f2(a.alpha);
+        oc[r][i] = oc[r][i] * f2(ro);  // u of the post norm, or o itself
       }
-      if (a.dgate && !gate_c) {  // gradient of a gate per token or value: alpha G N(o)
-        float w[EPT];
+      if (GENERAL && a.dgate && !gate_c) {  // gradient of a gate per token or value: alpha G N(o)
+        F2 w[PPT];
         factor(w, true, r);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) w[i] *= oc[r][i];
+        for (int i = 0; i < PPT; ++i) w[i] = w[i] * oc[r][i];
         if (a.b_post) {
-          if constexpr (RING) copy_out<float, A>(c, s_bias, r, H);
-          else load_columns<A>(c, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+          if constexpr (RING) {
+            copy_out<float, A>(c, s_bias, r, H);
+          } else {
+            float v[EPT];
+            load_columns<A>(v, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+            pairs_of(c, v);
+          }
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) w[i] += c[i];
+          for (int i = 0; i < PPT; ++i) w[i] = w[i] + c[i];
         }
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
+        for (int i = 0; i < PPT; ++i) {
           c[i] = G[r][i] * w[i];
-          d[2] += c[i];
+          d2 = d2 + c[i];
         }
         if (gate_f) store_row<OT, A>(a.dgate, a.o_dtype, at_o, r, H, vec, c);
       }
-      if (gate_f) {
+      if (GENERAL && gate_f) {
         load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) G[r][i] *= c[i];
-      } else if (gate_t) {
+        for (int i = 0; i < PPT; ++i) G[r][i] = G[r][i] * c[i];
+      } else if (GENERAL && gate_t) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) G[r][i] *= gt;
+        for (int i = 0; i < PPT; ++i) G[r][i] = G[r][i] * f2(gt);
       }
       if (RING) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) post1[r][i] = fmaf(G[r][i], oc[r][i], post1[r][i]);
-        if (ZERO)
+        for (int i = 0; i < PPT; ++i) post1[r][i] = fma2(G[r][i], oc[r][i], post1[r][i]);
+        if (GENERAL)
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) post0[r][i] += G[r][i];
+          for (int i = 0; i < PPT; ++i) post0[r][i] = post0[r][i] + G[r][i];
       } else {
         if (a.acc_post0 >= 0) add_columns<A>(acc + a.acc_post0 * sums_pitch, r, H, vec, G[r]);
         if (a.acc_post1 >= 0) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) c[i] = G[r][i] * oc[r][i];
+          for (int i = 0; i < PPT; ++i) c[i] = G[r][i] * oc[r][i];
           add_columns<A>(acc + a.acc_post1 * sums_pitch, r, H, vec, c);
         }
       }
       factor(c, true, r);
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        G[r][i] *= c[i];
-        d[0] = fmaf(G[r][i], oc[r][i], d[0]);
-        if (layer_post) d[1] += G[r][i];
+      for (int i = 0; i < PPT; ++i) {
+        G[r][i] = G[r][i] * c[i];
+        d0 = fma2(G[r][i], oc[r][i], d0);
+        if (GENERAL) d1 = d1 + G[r][i];
       }
     }
-    const bool token_sum = a.dgate && gate_t;
+    const bool token_sum = GENERAL && a.dgate && gate_t;
+    float d[4] = {halves_sum(d0), GENERAL ? halves_sum(d1) : 0.0f, GENERAL ? halves_sum(d2) : 0.0f, 0.0f};
     if (post || token_sum) block_sum(d);
     if (token_sum && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = d[2];
     if (a.d_o) {
-      const float n1 = post ? d[0] * inv_h : 0.0f, n0 = layer_post ? d[1] * inv_h : 0.0f;
+      const F2 n1 = f2(-d[0] * inv_h), n0 = f2(layer_post ? -d[1] * inv_h : 0.0f);
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
+        if (post) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) G[r][i] = ro * (fmaf(-oc[r][i], n1, G[r][i]) - n0);
+          for (int i = 0; i < PPT; ++i) {
+            F2 v = fma2(oc[r][i], n1, G[r][i]);
+            if (GENERAL) v = v + n0;
+            G[r][i] = f2(ro) * v;
+          }
+        }
         store_row<OT, A>(a.d_o, a.o_dtype, at_o, r, H, vec, G[r]);
       }
     }
@@ -431,14 +458,14 @@ inline int most_blocks_per_sm(int H) {
 constexpr size_t kSmemMax = 224 * 1024;  // of one block's dynamic shared memory
 constexpr size_t kSmemSm = 228 * 1024;   // of an SM; a block takes 1 KB of its own and 1 KB static
 
-template <typename HT, typename OT, Access A, int MAXT, bool ZERO>
+template <typename HT, typename OT, Access A, int MAXT, bool GENERAL>
 cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
   static const cudaError_t attr =
-      cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, MAXT, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, MAXT, GENERAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemMax));
   if (attr != cudaSuccess) return attr;
   const size_t pitch = slot_pitch<A>(a.H, threads);
-  int per_sm = min_blocks(MAXT, ZERO) * MAXT / threads;
+  int per_sm = min_blocks(MAXT, GENERAL) * MAXT / threads;
   if (per_sm > most_blocks_per_sm(a.H)) per_sm = most_blocks_per_sm(a.H);
   size_t smem = 0;
   a.depth = 0;
@@ -459,12 +486,13 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
     while (per_sm > 1 && (smem + 2048) * per_sm > kSmemSm) --per_sm;
   }
   a.blocks = a.T < 152 * per_sm ? a.T : 152 * per_sm;
-  return launch_dependent(norm_backward_kernel<HT, OT, A, MAXT, ZERO>, dim3(a.blocks), dim3(threads), smem, s, a);
+  return launch_dependent(norm_backward_kernel<HT, OT, A, MAXT, GENERAL>, dim3(a.blocks), dim3(threads), smem, s, a);
 }
 
 template <typename HT, typename OT, Access A>
 cudaError_t backward_ring(NormArgs& a, int threads, cudaStream_t s) {
-  if (a.acc_post0 >= 0 || a.acc_pre0 >= 0) {
+  if (a.acc_post0 >= 0 || a.acc_pre0 >= 0 || a.post == MOE_NORM_LAYER || a.pre == MOE_NORM_LAYER ||
+      a.gate_kind == MOE_GATE_TOKEN || a.gate_kind == MOE_GATE_FULL) {
     if (threads <= 128) return backward_of<HT, OT, A, 128, true>(a, threads, s);
     if (threads <= 256) return backward_of<HT, OT, A, 256, true>(a, threads, s);
     return backward_of<HT, OT, A, 512, true>(a, threads, s);

@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
-    float v[RUNS][EPT];
+    F2 v[RUNS][PPT];
     if (RING) {
       const int ahead = slot + a.depth - 1;
       fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
@@ -101,71 +101,91 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
     // takes the mean off v (layer norms) and returns 1 / std
     auto moments = [&](int kind) {
       if (kind == MOE_NORM_LAYER) {
-        float s[1] = {0.0f};
+        F2 s = f2(0.0f);
 #pragma unroll
         for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) s[0] += v[r][i];
-        block_sum(s);
-        const float mu = s[0] * inv_h;
+          for (int i = 0; i < PPT; ++i) s = s + v[r][i];
+        float sum[1] = {halves_sum(s)};
+        block_sum(sum);
+        const F2 mu = f2(-sum[0] * inv_h);
 #pragma unroll
         for (int r = 0; r < RUNS; ++r) {
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) v[r][i] -= mu;
+          for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] + mu;
           clear_past<A>(v[r], r, H, vec);
         }
       }
-      float q[1] = {0.0f};
+      F2 q = f2(0.0f);
 #pragma unroll
       for (int r = 0; r < RUNS; ++r)
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) q[0] = fmaf(v[r][i], v[r][i], q[0]);
-      block_sum(q);
-      return inv_std(q[0], inv_h, a.eps);
+        for (int i = 0; i < PPT; ++i) q = fma2(v[r][i], v[r][i], q);
+      float sum[1] = {halves_sum(q)};
+      block_sum(sum);
+      return inv_std(sum[0], inv_h, a.eps);
     };
 
     float scale = a.alpha;
     if (a.gate_kind == MOE_GATE_TOKEN) scale *= __ldg(static_cast<const float*>(a.gate) + t);
-    const float rs = a.post != MOE_NORM_NONE ? scale * moments(a.post) : scale;
+    const F2 rs = f2(a.post != MOE_NORM_NONE ? scale * moments(a.post) : scale), beta = f2(a.beta);
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      float c[EPT];
-      if constexpr (RING) copy_out<float, A>(c, s_post, r, H);
-      else post_column(c, a.w_post, 1.0f, r);
+      F2 c[PPT];
+      float f[EPT];
+      if constexpr (RING) {
+        copy_out<float, A>(c, s_post, r, H);
+      } else {
+        post_column(f, a.w_post, 1.0f, r);
+        pairs_of(c, f);
+      }
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) v[r][i] *= rs * c[i];
+      for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rs * c[i]);
       if (a.b_post) {
-        if constexpr (RING) copy_out<float, A>(c, s_bpost, r, H);
-        else post_column(c, a.b_post, 0.0f, r);
+        if constexpr (RING) {
+          copy_out<float, A>(c, s_bpost, r, H);
+        } else {
+          post_column(f, a.b_post, 0.0f, r);
+          pairs_of(c, f);
+        }
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[r][i] = fmaf(scale, c[i], v[r][i]);
+        for (int i = 0; i < PPT; ++i) v[r][i] = fma2(f2(scale), c[i], v[r][i]);
       }
       if (gate_f) {
         load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[r][i] *= c[i];
+        for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * c[i];
       }
       if constexpr (RING) copy_out<HT, A>(c, ring_h + slot * pitch, r, H);
       else load_row<A>(c, a.h, a.h_dtype, at_h, r, H, vec);
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) v[r][i] = fmaf(a.beta, c[i], v[r][i]);
+      for (int i = 0; i < PPT; ++i) v[r][i] = fma2(beta, c[i], v[r][i]);
       store_row<HT, A>(a.h_out, a.h_dtype, at_h, r, H, vec, v[r]);
     }
     // x' is taken from h' before its rounding: one rounding each
     if (a.pre != MOE_NORM_NONE) {
-      const float rp = moments(a.pre);
+      const F2 rp = f2(moments(a.pre));
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
-        float c[EPT];
-        if constexpr (RING) copy_out<float, A>(c, s_pre, r, H);
-        else load_columns<A>(c, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+        F2 c[PPT];
+        float f[EPT];
+        if constexpr (RING) {
+          copy_out<float, A>(c, s_pre, r, H);
+        } else {
+          load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+          pairs_of(c, f);
+        }
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) v[r][i] *= rp * c[i];
+        for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rp * c[i]);
         if (a.b_pre) {
-          if constexpr (RING) copy_out<float, A>(c, s_bpre, r, H);
-          else load_columns<A>(c, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
+          if constexpr (RING) {
+            copy_out<float, A>(c, s_bpre, r, H);
+          } else {
+            load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
+            pairs_of(c, f);
+          }
 #pragma unroll
-          for (int i = 0; i < EPT; ++i) v[r][i] += c[i];
+          for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] + c[i];
         }
         store_row<OT, A>(a.x_out, a.o_dtype, at_o, r, H, vec, v[r]);
       }
