@@ -205,12 +205,12 @@ __device__ __forceinline__ void store_row(void* p, int dtype, size_t at, int run
 
 // A thread's columns of an fp32 vector in shared memory, for itself.
 template <Access A>
-__device__ __forceinline__ void put_shared(float* slot, int run, int H, const float (&v)[EPT]) {
-  if (A == WORD4) {
+__device__ __forceinline__ void put_shared(float* slot, int run, const float (&v)[EPT]) {
+  if (A == VEC16) {
+    pack(slot + col_of<A>(run, 0, true), v);
+  } else {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) slot[col_of<A>(run, i, false)] = v[i];
-  } else {
-    store_row<float, A>(slot, MOE_DTYPE_F32, 0, run, H, true, v);
   }
 }
 
@@ -248,29 +248,25 @@ __device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H
     }
   }
 }
-// (WORD4: zeros are put past column H once, so that reads need no test.)
+// Zeros are put past column H of a slot once, so that reads need no test.
 template <typename T, Access A>
 __device__ __forceinline__ void clear_slot(T* slot, int H) {
-  if (A == WORD4)
+  if (A != PLAIN)
 #pragma unroll
-    for (int i = 0; i < RUNS * EPT; ++i) {
-      const int c = col_of<A>(0, i, false);
-      if (c >= H) slot[c] = T(0.0f);
-    }
+    for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        const int c = col_of<A>(r, i, true);
+        if (c >= H) slot[c] = T(0.0f);
+      }
 }
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, int H) {
+__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r) {
   if (A == VEC16) {
-    const int c = col_of<A>(r, 0, true);
-    if (c < H) unpack(v, slot + c);
-    else
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+    unpack(v, slot + col_of<A>(r, 0, true));
   } else {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      v[i] = as_f32(slot[col_of<A>(r, i, false)]);  // past column H the ring holds zeros
-    }
+    for (int i = 0; i < EPT; ++i) v[i] = as_f32(slot[col_of<A>(r, i, false)]);
   }
 }
 
@@ -284,9 +280,9 @@ __device__ __forceinline__ void values_of(float (&v)[EPT], const F2 (&p)[PPT]) {
   for (int i = 0; i < PPT; ++i) split(p[i], v[2 * i], v[2 * i + 1]);
 }
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r, int H) {
+__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r) {
   float v[EPT];
-  copy_out<T, A>(v, slot, r, H);
+  copy_out<T, A>(v, slot, r);
   pairs_of(p, v);
 }
 template <Access A>
@@ -378,7 +374,7 @@ inline size_t norm_pitch(int H) { return static_cast<size_t>(H + EPT - 1) / EPT 
 // Elements of a row's slot in shared memory.
 template <Access A>
 __host__ __device__ inline int slot_pitch(int H, int threads) {
-  return A == WORD4 ? threads * EPT * RUNS : (H + EPT - 1) / EPT * EPT;
+  return A != PLAIN ? threads * EPT * RUNS : (H + EPT - 1) / EPT * EPT;
 }
 
 }  // namespace norms

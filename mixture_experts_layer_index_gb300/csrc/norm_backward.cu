@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
   dep_wait();
   dep_launch();
 
-  if (A == WORD4)
+  if (RING)
     for (int d = 0; d < a.depth; ++d) {
       clear_slot<OT, A>(ring_o + d * pitch, H);
       if (a.dh_out) clear_slot<HT, A>(ring_g + d * pitch, H);
@@ -126,17 +126,17 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
       post_factor(f, r);
-      put_shared<A>(s_post, r, H, f);
+      put_shared<A>(s_post, r, f);
       load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-      put_shared<A>(s_pre, r, H, f);
+      put_shared<A>(s_pre, r, f);
       if (bias_in_smem(a)) {
         load_columns<A>(f, a.b_post, a.w_dtype, r, H, vec, 0.0f);
-        put_shared<A>(s_bias, r, H, f);
+        put_shared<A>(s_bias, r, f);
       }
     }
   auto factor = [&](F2(&f)[PPT], bool of_post, int r) {
     if constexpr (RING) {
-      copy_out<float, A>(f, of_post ? s_post : s_pre, r, H);
+      copy_out<float, A>(f, of_post ? s_post : s_pre, r);
     } else {
       float v[EPT];
       if (of_post) post_factor(v, r);
@@ -169,12 +169,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
     F2 hc[RUNS][PPT], oc[RUNS][PPT], dx[RUNS][PPT], G[RUNS][PPT];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r, H);
+      if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r);
       else load_row<A>(oc[r], a.o, a.o_dtype, at_o, r, H, vec);
       if (pre) {
         if constexpr (RING) {
-          copy_out<HT, A>(hc[r], ring_h + slot * pitch, r, H);
-          copy_out<OT, A>(dx[r], ring_x + slot * pitch, r, H);
+          copy_out<HT, A>(hc[r], ring_h + slot * pitch, r);
+          copy_out<OT, A>(dx[r], ring_x + slot * pitch, r);
         } else {
           load_row<A>(hc[r], a.h, a.h_dtype, at_h, r, H, vec);
           load_row<A>(dx[r], a.dx_out, a.o_dtype, at_o, r, H, vec);
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       if (a.dh_out) {
-        if constexpr (RING) copy_out<HT, A>(G[r], ring_g + slot * pitch, r, H);
+        if constexpr (RING) copy_out<HT, A>(G[r], ring_g + slot * pitch, r);
         else load_row<A>(G[r], a.dh_out, a.h_dtype, at_h, r, H, vec);
       } else {
 #pragma unroll
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
         for (int i = 0; i < PPT; ++i) w[i] = w[i] * oc[r][i];
         if (a.b_post) {
           if constexpr (RING) {
-            copy_out<float, A>(c, s_bias, r, H);
+            copy_out<float, A>(c, s_bias, r);
           } else {
             float v[EPT];
             load_columns<A>(v, a.b_post, a.w_dtype, r, H, vec, 0.0f);
@@ -421,8 +421,15 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(NormArgs a, NormSums ou
     float v = 0.0f;
     if (c < a.H) {
       const float* p = a.partials + j * pitch + c;
-#pragma unroll 8
-      for (int i = threadIdx.y; i < a.blocks; i += 32) v += p[static_cast<size_t>(i) * a.nacc * pitch];
+      const size_t stride = a.nacc * pitch;
+      constexpr int AHEAD = 10;  // loads on their way: one or two batches for all blocks
+      for (int i = threadIdx.y; i < a.blocks; i += 32 * AHEAD) {
+        float u[AHEAD];
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) u[q] = i + 32 * q < a.blocks ? p[(i + 32 * q) * stride] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) v += u[q];
+      }
     }
     __syncthreads();
     s[threadIdx.y][threadIdx.x] = v;

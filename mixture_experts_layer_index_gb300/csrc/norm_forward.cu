@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
   dep_wait();
   dep_launch();
 
-  if (A == WORD4)
+  if (RING)
     for (int d = 0; d < a.depth; ++d) {
       clear_slot<HT, A>(ring_h + d * pitch, H);
       clear_slot<OT, A>(ring_o + d * pitch, H);
@@ -71,16 +71,16 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
       post_column(f, a.w_post, 1.0f, r);
-      put_shared<A>(s_post, r, H, f);
+      put_shared<A>(s_post, r, f);
       load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-      put_shared<A>(s_pre, r, H, f);
+      put_shared<A>(s_pre, r, f);
       if (a.b_post) {
         post_column(f, a.b_post, 0.0f, r);
-        put_shared<A>(s_bpost, r, H, f);
+        put_shared<A>(s_bpost, r, f);
       }
       if (a.b_pre) {
         load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
-        put_shared<A>(s_bpre, r, H, f);
+        put_shared<A>(s_bpre, r, f);
       }
     }
 
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
     }
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if constexpr (RING) copy_out<OT, A>(v[r], ring_o + slot * pitch, r, H);
+      if constexpr (RING) copy_out<OT, A>(v[r], ring_o + slot * pitch, r);
       else load_row<A>(v[r], a.o, a.o_dtype, at_o, r, H, vec);
     }
 
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       F2 c[PPT];
       float f[EPT];
       if constexpr (RING) {
-        copy_out<float, A>(c, s_post, r, H);
+        copy_out<float, A>(c, s_post, r);
       } else {
         post_column(f, a.w_post, 1.0f, r);
         pairs_of(c, f);
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rs * c[i]);
       if (a.b_post) {
         if constexpr (RING) {
-          copy_out<float, A>(c, s_bpost, r, H);
+          copy_out<float, A>(c, s_bpost, r);
         } else {
           post_column(f, a.b_post, 0.0f, r);
           pairs_of(c, f);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
         for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * c[i];
       }
-      if constexpr (RING) copy_out<HT, A>(c, ring_h + slot * pitch, r, H);
+      if constexpr (RING) copy_out<HT, A>(c, ring_h + slot * pitch, r);
       else load_row<A>(c, a.h, a.h_dtype, at_h, r, H, vec);
 #pragma unroll
       for (int i = 0; i < PPT; ++i) v[r][i] = fma2(beta, c[i], v[r][i]);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
         F2 c[PPT];
         float f[EPT];
         if constexpr (RING) {
-          copy_out<float, A>(c, s_pre, r, H);
+          copy_out<float, A>(c, s_pre, r);
         } else {
           load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
           pairs_of(c, f);
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
         for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rp * c[i]);
         if (a.b_pre) {
           if constexpr (RING) {
-            copy_out<float, A>(c, s_bpre, r, H);
+            copy_out<float, A>(c, s_bpre, r);
           } else {
             load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
             pairs_of(c, f);
