@@ -112,10 +112,7 @@ __device__ __forceinline__ void finish(const Params& p, float (&v)[CH], int r0, 
     for (int i = 0; i < CH; ++i) v[i] += b;
   }
   if (p.ep.z) store_rows<CH>(p.ep.z, p.ep.z_dtype, static_cast<size_t>(r0) * p.ep.ld_z + c, p.ep.ld_z, n, v);
-  if (p.ep.act != MOE_ACT_NONE) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) v[i] = act_value(v[i], p.ep.act);
-  }
+  act_all<CH>(v, p.ep.act);
 #pragma unroll
   for (int i = 0; i < CH; ++i) v[i] *= p.ep.alpha;
   const size_t at = static_cast<size_t>(r0) * p.ep.ld_y + c;
@@ -251,6 +248,15 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       __syncwarp();
     }
     if (leader) mma_commit(done);
+  } else if (p.ep.residual) {
+    // the residual's part of the tile comes into L2 while the product is computed
+    const size_t es = p.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+    const size_t bytes = static_cast<size_t>(min(BM, p.C - c0)) * es;
+    const int share = BN / p.splits;
+    for (int j = rank * share + (warp - 2) * 32 + lane; j < min((rank + 1) * share, p.R - r0); j += 64) {
+      const uint8_t* row = static_cast<const uint8_t*>(p.ep.residual) + (static_cast<size_t>(r0 + j) * p.ep.ld_y + c0) * es;
+      for (size_t b = 0; b < bytes; b += 128) prefetch_l2(row + b);
+    }
   }
   __syncwarp();
   if (lane == 0) mbar_wait(done, 0, abort_flag, p.hdr, 0x530000u);
@@ -271,7 +277,11 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       for (int i = 0; i < CH; ++i) v[i] += u[i];
     }
   };
-  if (p.splits == 1) {
+  // Few output columns leave most lanes without one: the values then go through shared
+  // memory too, and groups of `width` threads take rows in turn.
+  const int cols = min(BM, p.C - c0);
+  const int width = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : BM;
+  if (p.splits == 1 && width == BM) {
     if (good) {
 #pragma unroll 1
       for (int j = 0; j < BN; j += CH) {
@@ -292,15 +302,20 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
         for (int i = 0; i < CH; ++i) part[(j + i) * BM + cl] = v[i];
       }
     }
-    cluster_sync_all();
+    if (p.splits > 1) cluster_sync_all();
+    else __syncthreads();
     if (good) {
-      // its share of the rows, RB at a time: all ranks' values of RB rows are on their way
-      // before the first is added
+      // this block's share of the rows, this thread's group's of them, RB at a time: all
+      // ranks' values of RB rows are on their way before the first is added
+      const int groups = BM / width, own = static_cast<int>(threadIdx.x) / width;
+      const int c = static_cast<int>(threadIdx.x) & (width - 1);
       const int per = BN / p.splits;
+      const int per_group = (per + groups - 1) / groups;
       constexpr int RB = 8;
-      const uint32_t mine = smem_u32(part) + cl * 4;
-      const int end = min((rank + 1) * per, p.R - r0);
-      for (int j = rank * per; j < end; j += RB) {
+      const uint32_t mine = smem_u32(part) + c * 4;
+      const int begin = rank * per + own * per_group;
+      const int end = min(min(begin + per_group, (rank + 1) * per), p.R - r0);
+      for (int j = begin; j < end; j += RB) {
         const int cnt = min(RB, end - j);
         float u[MAX_SPLITS][RB];
 #pragma unroll
@@ -315,10 +330,10 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
           if (q < p.splits)
 #pragma unroll
             for (int i = 0; i < RB; ++i) v[i] += u[q][i];
-        finish<RB>(p, v, r0 + j, cnt, c0 + cl);
+        finish<RB>(p, v, r0 + j, cnt, c0 + c);
       }
     }
-    cluster_sync_all();  // no block leaves while another still reads its partial
+    if (p.splits > 1) cluster_sync_all();  // no block leaves while another still reads its partial
   }
   tc_fence_before();
   __syncthreads();
@@ -364,13 +379,13 @@ cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
 }
 
 // About how long a launch takes (us), for tiles of 128 x bn split over `splits` blocks.
-// Measured on GB300: 2.6 us of launch, set-up and drain; a block's stage takes 0.17 us
+// Measured on GB300: 2.2 us of launch, set-up and drain; a block's stage takes 0.17 us
 // (bn = 16) to 0.20 us (128), 0.45 us at 256, or as long as the SM's blocks together need
-// for their operands at 143 GB/s per SM; each further wave adds 2 us and 0.04 us per row
-// for the epilogue that nothing overlaps; joining partials costs 1 us, 0.4 us per doubling and
-// 0.02 us per row.  Within 15% of the measured times of the shapes it was fitted to (8 x
-// 4096 x 4096 to 2048 x 2048 x 2048 and the gradient of a 128-column router over 16384
-// tokens), which is near enough to tell 17 us (bn = 64, 8 splits) from 54 us (128, 1).
+// for their operands at 143 GB/s per SM; the epilogue, which nothing overlaps, 0.037 us per
+// row, and more with an activation, z or a residual; each further wave 1.7 us; joining
+// partials 1 us, 0.4 us per doubling and 0.02 us per row.  Within 20% of the measured times of some forty shapes
+// (8 x 4096 x 4096 to 16384 x 2048 x 72), near enough to tell 17 us (16384 x 128 x
+// 2048's weight gradient at bn = 64, 8 splits) from 54 us (128, 1).
 float tile_estimate(const Product& q, int bn, int splits) {
   const long long nk = (q.K + BK - 1) / BK;
   const long long blocks = static_cast<long long>((q.C + BM - 1) / BM) * ((q.R + bn - 1) / bn) * splits;
@@ -384,7 +399,11 @@ float tile_estimate(const Product& q, int bn, int splits) {
   float t = waves * static_cast<float>((nk + splits - 1) / splits) * stage;
   const float memory = 2.0f * (static_cast<float>(q.R) + q.C) * q.K / 6.5e6f;
   if (memory > t) t = memory;
-  t += 2.6f + 0.01f * bn + (waves - 1) * (2.0f + 0.04f * bn);
+  // lanes without a column take rows instead
+  const float lanes = q.C <= 16 ? 0.125f : q.C <= 32 ? 0.25f : q.C <= 64 ? 0.5f : 1.0f;
+  const float row = 0.037f + (q.ep.act != MOE_ACT_NONE ? 0.009f : 0.0f) + (q.ep.z ? 0.012f : 0.0f) +
+                    (q.ep.residual ? 0.05f : 0.0f);
+  t += 2.2f + 1.7f * (waves - 1) + waves * row * lanes * (bn < q.R ? bn : q.R) / splits;
   for (int s = splits; s > 1; s /= 2) t += 0.4f;
   return splits > 1 ? t + 1.0f + 0.02f * bn : t;
 }
@@ -432,7 +451,7 @@ cudaError_t launch_shape(const Product& q, const Choice& c, cudaStream_t s) {
   }
 }
 
-bool takes_pair(const Product& q, const Choice& c) { return pair_storable(q) && pair_estimate(q) < c.us; }
+bool takes_pair(const Product& q, const Choice& c) { return pair_estimate(q) < c.us; }
 
 cudaError_t launch_product(const Product& q, cudaStream_t s) {
   const Choice c = choose_tile(q);
@@ -443,9 +462,10 @@ cudaError_t launch_product(const Product& q, cudaStream_t s) {
 
 // ------------------------------------------------------------------ dz
 // dz = alpha dy act'(z) in the operands' type, and per chunk of rows the fp32 sums
-// of its unrounded columns.  Thread (x, y): columns 8 x .. 8 x + 7 of every 8th row,
-// four rows' loads issued before the first is used (bound by memory: dy and z in, dz
-// out).  DT, T: types of dy and of z and dz.  VEC: rows that 16-byte accesses fit.
+// of its unrounded columns.  Thread (x, y): eight columns of every 8th row, four rows'
+// loads issued before the first is used (bound by memory: dy and z in, dz out).  DT, T:
+// types of dy and of z and dz.  VEC: rows that 16-byte accesses fit, columns 8 x .. 8 x +
+// 7; otherwise columns x + 32 i, so that a warp's accesses are neighbours.
 struct DzArgs {
   int M, N, rows;  // rows per chunk
   int act;
@@ -457,16 +477,6 @@ struct DzArgs {
   float* partials;  // [chunks][N], null: not wanted
 };
 
-__device__ __forceinline__ float value_of(float v) { return v; }
-__device__ __forceinline__ float value_of(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float value_of(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T rounded(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
-
 template <typename T, bool VEC>
 __device__ __forceinline__ void load8(T (&v)[8], const void* p, size_t at, int n) {
   const T* q = static_cast<const T*>(p) + at;
@@ -477,7 +487,7 @@ __device__ __forceinline__ void load8(T (&v)[8], const void* p, size_t at, int n
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) v[i] = q[i];
+      if (32 * i < n) v[i] = q[32 * i];
   }
 }
 
@@ -487,8 +497,9 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
   constexpr int AHEAD = 4;
   dep_wait();
   dep_launch();
-  const int c = blockIdx.x * 256 + threadIdx.x * 8;
-  const int n = min(8, a.N - c);
+  const int c = blockIdx.x * 256 + threadIdx.x * (VEC ? 8 : 1);  // first column
+  const int n = a.N - c;                                         // columns from there on
+  auto in = [&](int i) { return VEC || 32 * i < n; };
   const int m0 = blockIdx.y * a.rows, m1 = min(a.M, m0 + a.rows);
   float sum[8] = {};
   if (n > 0) {
@@ -509,11 +520,11 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
         if (m >= m1) break;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = VEC || i < n ? a.alpha * value_of(g[q][i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = in(i) ? a.alpha * as_float(g[q][i]) : 0.0f;
         auto times = [&](int act) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (VEC || i < n) v[i] *= act_grad(value_of(z[q][i]), act);
+            if (in(i)) v[i] *= act_grad(as_float(z[q][i]), act);
         };
         switch (a.act) {
           case MOE_ACT_NONE: break;
@@ -524,19 +535,25 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(DzArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] += v[i];
-        if (a.dz) {  // rows of the workspace are padded to 8 values: a whole store even at the edge
-          alignas(16) T out[8];
+        if (a.dz) {
+          T* to = static_cast<T*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c;
+          if (VEC) {
+            alignas(16) T out[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) out[i] = rounded<T>(v[i]);
-          *reinterpret_cast<uint4*>(static_cast<T*>(a.dz) + static_cast<size_t>(m) * a.ld_dz + c) =
-              *reinterpret_cast<const uint4*>(out);
+            for (int i = 0; i < 8; ++i) out[i] = as_type<T>(v[i]);
+            *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(out);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (in(i)) to[32 * i] = as_type<T>(v[i]);
+          }
         }
       }
     }
   }
   if (!a.partials) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_sum[threadIdx.y][threadIdx.x * 8 + i] = sum[i];
+  for (int i = 0; i < 8; ++i) s_sum[threadIdx.y][VEC ? threadIdx.x * 8 + i : threadIdx.x + 32 * i] = sum[i];
   __syncthreads();
   const int col = threadIdx.y * 32 + threadIdx.x;
   if (blockIdx.x * 256 + col < a.N) {
@@ -560,10 +577,11 @@ cudaError_t launch_dz(const DzArgs& d, int dy_dtype, bool vec, int chunks, cudaS
   return launch_dz<__half, T>(d, vec, chunks, s);
 }
 
-// Rows per chunk: at least 64, at most 256 chunks.
+// Rows per chunk: at least 64, at most 256 chunks; up to 128 rows are one chunk, whose sums
+// are final.
 inline int dz_rows(int M) {
   const int r = (M + 255) / 256;
-  return r < 64 ? 64 : (r + 7) / 8 * 8;
+  return M <= 128 ? 128 : r < 64 ? 64 : (r + 7) / 8 * 8;
 }
 inline long long dz_ld(int N) { return (N + 7) / 8 * 8; }
 
@@ -615,15 +633,15 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     d.dy = a.dy;
     d.z = a.z;
     d.dz = direct || !products ? nullptr : a.dz;
-    d.partials = a.dbias ? a.partials : nullptr;
+    const int chunks = (a.M + d.rows - 1) / d.rows;
+    d.partials = !a.dbias ? nullptr : chunks == 1 ? a.dbias : a.partials;
     const bool vec = a.N % 8 == 0 && a.ld_y % 8 == 0 && reinterpret_cast<uintptr_t>(a.dy) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(a.z) % 16 == 0;
-    const int chunks = (a.M + d.rows - 1) / d.rows;
     stage_begin("linear_dz", s);
     err = a.dtype == MOE_DTYPE_BF16 ? launch_dz<__nv_bfloat16>(d, a.dy_dtype, vec, chunks, s)
                                     : launch_dz<__half>(d, a.dy_dtype, vec, chunks, s);
     stage_end(s);
-    if (err == cudaSuccess && a.dbias) err = launch_column_sums(a.partials, chunks, a.N, a.dbias, s);
+    if (err == cudaSuccess && a.dbias && chunks > 1) err = launch_column_sums(a.partials, chunks, a.N, a.dbias, s);
   }
   const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};
   Product q{};

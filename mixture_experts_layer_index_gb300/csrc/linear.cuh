@@ -73,6 +73,29 @@ __device__ __forceinline__ float act_value(float z, int act) {
     default: return z;
   }
 }
+// All values of a thread at once: one branch for all of them.
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+  switch (act) {
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MOE_ACT_SILU);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_value(v[i], MOE_ACT_GELU_TANH);
+      break;
+    default: break;
+  }
+}
 __device__ __forceinline__ float act_grad(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
@@ -98,6 +121,19 @@ __device__ __forceinline__ float load_as_f32(const void* p, int dtype, size_t i)
   if (dtype == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   return __half2float(static_cast<const __half*>(p)[i]);
 }
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T as_type(float v);
+template <>
+__device__ __forceinline__ float as_type<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 as_type<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half as_type<__half>(float v) { return __float2half_rn(v); }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 struct Operand {
   const void* base;
@@ -142,9 +178,8 @@ struct Product {
   DeviceHeader* hdr;
 };
 
-// linear_pair.cu: whether TMA can store the outputs; about how long a launch takes (us);
-// the product, or two of a gradient (the same type, no bias, activation, residual or z).
-bool pair_storable(const Product& p);
+// linear_pair.cu: about how long a launch takes (us); the product, or two of a gradient
+// (the same type and row length, no bias, activation, residual or z).
 float pair_estimate(const Product& p);
 cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s);
 

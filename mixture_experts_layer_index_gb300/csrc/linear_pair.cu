@@ -51,7 +51,9 @@ struct PairParams {
   int tiles[2];
   int ratio;  // tiles of prod[1] that take about as long as one of prod[0]
   int type;
+  int y_tma, z_tma;  // whether TMA can store the output (16-byte aligned rows)
   Epilogue ep;
+  void* y[2];        // per product
   int reset_status;
   DeviceHeader* hdr;
 };
@@ -157,6 +159,46 @@ __device__ __forceinline__ void put_box(uint8_t* box, int lane, int part, int dt
       *reinterpret_cast<uint4*>(row + (((part * 2 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// Columns c.. c + 31 of a box of fp32 values (32 rows from r0) to an array whose rows TMA
+// cannot store: a row at a time, one lane per column, plus the residual's values.  Not
+// inlined: its registers would be spilled from the paths that TMA stores.
+template <typename T>
+__device__ __forceinline__ void flush_box_as(const uint8_t* box, int lane, T* out, long long ld, const T* residual,
+                                             int r0, int R, int c, int C) {
+  const int rows = c + lane < C ? min(32, R - r0) : 0;
+  const size_t at = static_cast<size_t>(r0) * ld + c + lane;
+  out += at;
+  if (residual) residual += at;
+#pragma unroll 1
+  for (int r = 0; r < rows; r += 16) {
+    T u[16] = {};
+    if (residual) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (r + i < rows) u[i] = residual[i * ld];
+      residual += 16 * ld;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (r + i < rows) {
+        float v = *reinterpret_cast<const float*>(box + (r + i) * 128 + (((lane >> 2) ^ ((r + i) & 7)) << 4) + (lane & 3) * 4);
+        if (residual) v += as_float(u[i]);
+        out[i * ld] = as_type<T>(v);
+      }
+    out += 16 * ld;
+  }
+  __syncwarp();  // the box may be written again
+}
+__device__ __noinline__ void flush_box(const uint8_t* box, int lane, void* out, int dtype, long long ld,
+                                          const void* residual, int r0, int R, int c, int C) {
+  if (dtype == MOE_DTYPE_F32)
+    flush_box_as(box, lane, static_cast<float*>(out), ld, static_cast<const float*>(residual), r0, R, c, C);
+  else if (dtype == MOE_DTYPE_BF16)
+    flush_box_as(box, lane, static_cast<__nv_bfloat16*>(out), ld, static_cast<const __nv_bfloat16*>(residual), r0, R, c, C);
+  else
+    flush_box_as(box, lane, static_cast<__half*>(out), ld, static_cast<const __half*>(residual), r0, R, c, C);
 }
 
 // v[i] += p[at + i], 16 values of which `n` exist; `wide`: p + at is 16-byte aligned.
@@ -356,13 +398,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // The residual of a tile is fetched into L2 while the tile before it is finished, so
+    // that the epilogue's loads do not wait for memory.
+    if (p.ep.residual) {
+      const size_t es = p.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+      uint32_t acc = 0, acc_phase = 0;
+      int prod, tile;
+      for (int i = 0; pair_item(p, pair, npairs, i, prod, tile); ++i) {
+        int r0, c0;
+        tile_origin(p.prod[prod], tile, r0, c0);
+        r0 += rank * HALF;
+        const size_t row_bytes = static_cast<size_t>(min(TILE, p.prod[prod].C - c0)) * es;
+        for (int r = lane; r < min(HALF, p.prod[prod].R - r0); r += 32) {
+          const uint8_t* row = static_cast<const uint8_t*>(p.ep.residual) + (static_cast<size_t>(r0 + r) * p.ep.ld_y + c0) * es;
+          for (size_t b = 0; b < row_bytes; b += 128) prefetch_l2(row + b);
+        }
+        int good = 1;
+        if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x650000u);
+        if (!__shfl_sync(0xffffffffu, good, 0)) break;
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+    }
   } else if (warp >= 4) {
     const int e = warp - 4, q = warp & 3, h = e >> 2;
     uint8_t* box = smem + BOX_OFFSET + e * BOX_BYTES;
     const uint32_t lead_tempty0 = map_rank(tempty0, 0);
     const Epilogue& ep = p.ep;
     const bool wide = ep.out_dtype == MOE_DTYPE_F32;
-    const bool plain = !wide && !ep.bias && !ep.residual && !ep.z && ep.act == MOE_ACT_NONE && ep.alpha == 1.0f;
+    const bool plain = p.y_tma && !wide && !ep.bias && !ep.residual && !ep.z && ep.act == MOE_ACT_NONE && ep.alpha == 1.0f;
     const bool bias_wide = reinterpret_cast<uintptr_t>(ep.bias) % 16 == 0;
     const bool residual_wide = reinterpret_cast<uintptr_t>(ep.residual) % 16 == 0;
     uint32_t acc = 0, acc_phase = 0;
@@ -428,9 +493,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int j = 0; j < 4; ++j) {
           float v[16];
           load_z(j, v);
-          put_box(box, lane, j, ep.z_dtype, v);
+          if (p.z_tma) {
+            put_box(box, lane, j, ep.z_dtype, v);
+          } else {
+            put_box(box, lane, j & 1, MOE_DTYPE_F32, v);
+            if (j & 1) {
+              __syncwarp();
+              flush_box(box, lane, ep.z, ep.z_dtype, ep.ld_z, nullptr, r0, R, c0 + (j - 1) * 16, C);
+            }
+          }
         }
-        store_box(&tmZ, c0);
+        if (p.z_tma) store_box(&tmZ, c0);
       }
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
@@ -442,27 +515,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
         }
-        switch (ep.act) {
-          case MOE_ACT_NONE: break;
-          case MOE_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_RELU);
-            break;
-          case MOE_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_SILU);
-            break;
-          case MOE_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_GELU);
-            break;
-          default:
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = act_value(v[i], MOE_ACT_GELU_TANH);
-        }
+        act_all<16>(v, ep.act);
         if (ep.alpha != 1.0f) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] *= ep.alpha;
+        }
+        if (!p.y_tma) {
+          if (j == 0) box_free();
+          put_box(box, lane, j & 1, MOE_DTYPE_F32, v);
+          if (j & 1) {
+            __syncwarp();
+            flush_box(box, lane, p.y[prod], ep.out_dtype, ep.ld_y, ep.residual, r0, R, c - 16, C);
+          }
+          continue;
         }
         if (ep.residual && row_in)  // its rows are aligned as y's, which TMA stores
           add16(v, ep.residual, ep.out_dtype, static_cast<size_t>(r0 + lane) * ep.ld_y + c, C - c, residual_wide);
@@ -519,19 +584,25 @@ bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
   pp->b_mn = q.cols_mn;
   return encode(&m->a, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : HALF) &&
          encode(&m->b, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn ? 64 : HALF) &&
-         encode_store(&m->y, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y);
+         (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) ||
+          encode_store(&m->y, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y));
 }
 
 }  // namespace
 
-bool pair_storable(const Product& q) {
-  return storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) && (!q.ep.z || storable(q.ep.z, q.ep.z_dtype, q.ep.ld_z));
-}
-
+// Measured on GB300: 4 us of launch, set-up and drain, 0.30 us per stage of a tile, and the
+// epilogue of a tile, of which all but the last overlaps the next tile's stages: 3.5 us,
+// and more with an activation, z, a residual, or rows that TMA cannot store.
 float pair_estimate(const Product& q) {
   const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + TILE - 1) / TILE);
   const float stages = 0.30f * ((q.K + BK - 1) / BK);
-  return 6.0f + ((tiles + 75) / 76) * (stages > 2.5f ? stages : 2.5f);
+  float epilogue = 3.5f;
+  if (q.ep.act != MOE_ACT_NONE) epilogue += 1.0f;
+  if (q.ep.residual) epilogue += 4.3f;
+  if (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y)) epilogue += 4.0f;
+  if (q.ep.z) epilogue += storable(q.ep.z, q.ep.z_dtype, q.ep.ld_z) ? 1.5f : 5.5f;
+  const long long waves = (tiles + 75) / 76;
+  return 4.0f + stages + epilogue + (waves - 1) * (stages > epilogue ? stages : epilogue);
 }
 
 cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s) {
@@ -543,8 +614,8 @@ cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_
     second = &first;
   }
   PairParams p{};
-  PairMaps m0, m1;
-  CUtensorMap tz;
+  PairMaps m0{}, m1;
+  CUtensorMap tz{};
   if (!encode_product(&m0, &p.prod[0], *q0)) return cudaErrorInvalidValue;
   p.tiles[0] = p.prod[0].nR * p.prod[0].nC;
   p.ratio = 1;
@@ -555,7 +626,13 @@ cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_
     p.tiles[1] = p.prod[1].nR * p.prod[1].nC;
     p.ratio = (p.prod[0].nk + p.prod[1].nk / 2) / p.prod[1].nk;
   }
-  if (q0->ep.z && !encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z)) return cudaErrorInvalidValue;
+  // two products are stored the same way
+  p.y_tma = storable(q0->ep.y, q0->ep.out_dtype, q0->ep.ld_y) &&
+            (!second || storable(second->ep.y, second->ep.out_dtype, second->ep.ld_y));
+  p.z_tma = q0->ep.z && storable(q0->ep.z, q0->ep.z_dtype, q0->ep.ld_z);
+  p.y[0] = q0->ep.y;
+  p.y[1] = second ? second->ep.y : nullptr;
+  if (p.z_tma && !encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z)) return cudaErrorInvalidValue;
   static const cudaError_t attr =
       cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
   if (attr != cudaSuccess) return attr;
