@@ -27,8 +27,9 @@ constexpr int RUNS = 2;
 //   WORD4: a warp takes 512 columns, its lane l columns (run*8 + i)*32 + l of them: whole
 //          128-byte lines, and constant distances between a thread's columns; 4-byte
 //          copies into the ring (fp32 rows)
-//   PLAIN: like WORD4, or like VEC16 where the row allows it (`vec`), loaded when
-//          they are used, any type: 16-bit rows at odd addresses, and rows too long for a ring
+//   PLAIN: columns like WORD4, or like VEC16 where the row allows it (`vec`), all of a row's
+//          loads issued together when the row's turn comes: 16-bit rows at odd addresses,
+//          which asynchronous copies do not take, and rows too long for a ring
 enum Access { VEC16, WORD4, PLAIN };
 
 template <Access A>
@@ -139,91 +140,80 @@ __device__ __forceinline__ void pack(__half* p, const float (&v)[EPT]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+template <typename T>
+__device__ __forceinline__ T rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+
+// A thread's columns of the row at element `at` of p; 0 past column H.
+template <typename T, Access A>
+__device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, size_t at, int run, int H, bool vec) {
+  const T* row = static_cast<const T*>(p) + at;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    const int c = col_of<A>(run, 0, vec);
+    if (c < H) unpack(v, row + c);
+  } else {
+    T raw[EPT] = {};
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(run, i, vec);
+      if (c < H) raw[i] = row[c];
+    }
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) v[i] = as_f32(raw[i]);
+  }
+}
+template <typename T, Access A>
+__device__ __forceinline__ void store_row(void* p, size_t at, int run, int H, bool vec, const float (&v)[EPT]) {
+  T* row = static_cast<T*>(p) + at;
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    const int c = col_of<A>(run, 0, vec);
+    if (c < H) pack(row + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<A>(run, i, vec);
+      if (c < H) row[c] = rounded<T>(v[i]);
+    }
+  }
+}
+
+// A per-column vector (16-byte aligned where rows are read 16 bytes at a time) of one of the
+// three types; `none` where there is no vector.
 __device__ __forceinline__ float load_one(const void* p, int dtype, size_t i) {
   if (dtype == MOE_DTYPE_F32) return static_cast<const float*>(p)[i];
   if (dtype == MOE_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
   return __half2float(static_cast<const __half*>(p)[i]);
 }
-__device__ __forceinline__ void store_one(void* p, int dtype, size_t i, float v) {
-  if (dtype == MOE_DTYPE_F32) static_cast<float*>(p)[i] = v;
-  else if (dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-__device__ __forceinline__ void unpack_any(float (&v)[EPT], const void* p, int dtype, size_t at) {
-  if (dtype == MOE_DTYPE_F32) unpack(v, static_cast<const float*>(p) + at);
-  else if (dtype == MOE_DTYPE_BF16) unpack(v, static_cast<const __nv_bfloat16*>(p) + at);
-  else unpack(v, static_cast<const __half*>(p) + at);
-}
-__device__ __forceinline__ void pack_any(void* p, int dtype, size_t at, const float (&v)[EPT]) {
-  if (dtype == MOE_DTYPE_F32) pack(static_cast<float*>(p) + at, v);
-  else if (dtype == MOE_DTYPE_BF16) pack(static_cast<__nv_bfloat16*>(p) + at, v);
-  else pack(static_cast<__half*>(p) + at, v);
-}
-
-// A thread's columns of the row at element `at` of p; 0 past column H.
 template <Access A>
-__device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, int dtype, size_t at, int run, int H, bool vec) {
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    const int c = col_of<A>(run, 0, vec);
-    if (c < H) unpack_any(v, p, dtype, at + c);
-    else
+__device__ __forceinline__ void load_columns(float (&v)[EPT], const void* p, int dtype, int run, int H, bool vec,
+                                             float none) {
+  if (p == nullptr) {
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
+    for (int i = 0; i < EPT; ++i) v[i] = none;
+  } else if (dtype == MOE_DTYPE_F32) {
+    load_row<float, A>(v, p, 0, run, H, vec);
+  } else if (dtype == MOE_DTYPE_BF16) {
+    load_row<__nv_bfloat16, A>(v, p, 0, run, H, vec);
   } else {
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(run, i, vec);
-      v[i] = c < H ? load_one(p, dtype, at + c) : 0.0f;
-    }
-  }
-}
-// T names the type where the rows come through a ring, `dtype` where they do not.
-template <typename T, Access A>
-__device__ __forceinline__ void store_row(void* p, int dtype, size_t at, int run, int H, bool vec,
-                                          const float (&v)[EPT]) {
-  if constexpr (A == VEC16) {
-    const int c = col_of<A>(run, 0, true);
-    if (c < H) pack(static_cast<T*>(p) + at + c, v);
-  } else if constexpr (A == WORD4) {
-    float* row = static_cast<float*>(p) + at;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(run, i, false);
-      if (c < H) row[c] = v[i];
-    }
-  } else if (vec) {
-    const int c = col_of<A>(run, 0, vec);
-    if (c < H) pack_any(p, dtype, at + c, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(run, i, vec);
-      if (c < H) store_one(p, dtype, at + c, v[i]);
-    }
+    load_row<__half, A>(v, p, 0, run, H, vec);
   }
 }
 
 // A thread's columns of an fp32 vector in shared memory, for itself.
 template <Access A>
-__device__ __forceinline__ void put_shared(float* slot, int run, const float (&v)[EPT]) {
-  if (A == VEC16) {
-    pack(slot + col_of<A>(run, 0, true), v);
+__device__ __forceinline__ void put_shared(float* slot, int run, bool vec, const float (&v)[EPT]) {
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    pack(slot + col_of<A>(run, 0, vec), v);
   } else {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) slot[col_of<A>(run, i, false)] = v[i];
-  }
-}
-
-// A thread's columns of a per-column vector (16-byte aligned where the rows are read
-// 16 bytes at a time); `none` where there is no vector.
-template <Access A>
-__device__ __forceinline__ void load_columns(float (&v)[EPT], const void* p, int dtype, int run, int H, bool vec,
-                                             float none) {
-  if (p != nullptr) {
-    load_row<A>(v, p, dtype, 0, run, H, vec);
-  } else {
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) v[i] = none;
+    for (int i = 0; i < EPT; ++i) slot[col_of<A>(run, i, vec)] = v[i];
   }
 }
 
@@ -261,12 +251,12 @@ __device__ __forceinline__ void clear_slot(T* slot, int H) {
       }
 }
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r) {
-  if (A == VEC16) {
-    unpack(v, slot + col_of<A>(r, 0, true));
+__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, bool vec = A == VEC16) {
+  if (A == VEC16 || (A == PLAIN && vec)) {
+    unpack(v, slot + col_of<A>(r, 0, vec));
   } else {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) v[i] = as_f32(slot[col_of<A>(r, i, false)]);
+    for (int i = 0; i < EPT; ++i) v[i] = as_f32(slot[col_of<A>(r, i, vec)]);
   }
 }
 
@@ -280,22 +270,22 @@ __device__ __forceinline__ void values_of(float (&v)[EPT], const F2 (&p)[PPT]) {
   for (int i = 0; i < PPT; ++i) split(p[i], v[2 * i], v[2 * i + 1]);
 }
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r) {
+__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r, bool vec = A == VEC16) {
   float v[EPT];
-  copy_out<T, A>(v, slot, r);
-  pairs_of(p, v);
-}
-template <Access A>
-__device__ __forceinline__ void load_row(F2 (&p)[PPT], const void* q, int dtype, size_t at, int run, int H, bool vec) {
-  float v[EPT];
-  load_row<A>(v, q, dtype, at, run, H, vec);
+  copy_out<T, A>(v, slot, r, vec);
   pairs_of(p, v);
 }
 template <typename T, Access A>
-__device__ __forceinline__ void store_row(void* q, int dtype, size_t at, int run, int H, bool vec, const F2 (&p)[PPT]) {
+__device__ __forceinline__ void load_row(F2 (&p)[PPT], const void* q, size_t at, int run, int H, bool vec) {
+  float v[EPT];
+  load_row<T, A>(v, q, at, run, H, vec);
+  pairs_of(p, v);
+}
+template <typename T, Access A>
+__device__ __forceinline__ void store_row(void* q, size_t at, int run, int H, bool vec, const F2 (&p)[PPT]) {
   float v[EPT];
   values_of(v, p);
-  store_row<T, A>(q, dtype, at, run, H, vec, v);
+  store_row<T, A>(q, at, run, H, vec, v);
 }
 // v = 0 for columns past H (after a mean was taken off).
 template <Access A>
@@ -371,10 +361,9 @@ inline int norm_threads(int H) {
   return (t + 31) / 32 * 32;
 }
 inline size_t norm_pitch(int H) { return static_cast<size_t>(H + EPT - 1) / EPT * EPT; }
-// Elements of a row's slot in shared memory.
-template <Access A>
-__host__ __device__ inline int slot_pitch(int H, int threads) {
-  return A != PLAIN ? threads * EPT * RUNS : (H + EPT - 1) / EPT * EPT;
+// Elements of a row or vector in shared memory.
+__host__ __device__ inline int slot_pitch(int threads) {
+  return threads * EPT * RUNS;
 }
 
 }  // namespace norms

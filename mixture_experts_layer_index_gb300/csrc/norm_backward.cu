@@ -56,19 +56,20 @@ constexpr int min_blocks(int maxt, bool general) {
 template <typename HT, typename OT, Access A, int MAXT, bool GENERAL>
 __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward_kernel(NormArgs a) {
   constexpr bool RING = A != PLAIN;
+  constexpr bool HOLD = MAXT <= 512;  // column sums in registers, factors in shared memory
   using Sum = BlockSum<4, MAXT>;
   __shared__ __align__(16) float s_sum[2][4][Sum::W];
   extern __shared__ __align__(16) uint8_t s_mem[];
   const int H = a.H;
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const int pitch = slot_pitch<A>(H, blockDim.x), sums_pitch = (H + EPT - 1) / EPT * EPT;
+  const int pitch = slot_pitch(blockDim.x), sums_pitch = (H + EPT - 1) / EPT * EPT;
   const bool pre = a.pre != MOE_NORM_NONE, post = a.post != MOE_NORM_NONE;
   const bool layer_pre = a.pre == MOE_NORM_LAYER, layer_post = a.post == MOE_NORM_LAYER;
   const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
   const bool gate_t = a.gate_kind == MOE_GATE_TOKEN;
-  // ring slots: o | dh' | h' | dx', then the factors of the post and of the pre norm;
-  // without a ring, the column sums (in the workspace itself where they do not fit)
+  // ring slots: o | dh' | h' | dx', then the factors of the post and of the pre norm; rows
+  // of over 8192 columns: the column sums (in the workspace itself where they do not fit)
   const int rows = a.depth * pitch;
   OT* ring_o = reinterpret_cast<OT*>(s_mem);
   HT* ring_g = reinterpret_cast<HT*>(ring_o + rows);
@@ -121,22 +122,22 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
       for (int i = 0; i < EPT; ++i) f[i] *= g[i];
     }
   };
-  if (RING)
+  if (HOLD)
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
       post_factor(f, r);
-      put_shared<A>(s_post, r, f);
+      put_shared<A>(s_post, r, vec, f);
       load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-      put_shared<A>(s_pre, r, f);
+      put_shared<A>(s_pre, r, vec, f);
       if (bias_in_smem(a)) {
         load_columns<A>(f, a.b_post, a.w_dtype, r, H, vec, 0.0f);
-        put_shared<A>(s_bias, r, f);
+        put_shared<A>(s_bias, r, vec, f);
       }
     }
   auto factor = [&](F2(&f)[PPT], bool of_post, int r) {
-    if constexpr (RING) {
-      copy_out<float, A>(f, of_post ? s_post : s_pre, r);
+    if constexpr (HOLD) {
+      copy_out<float, A>(f, of_post ? s_post : s_pre, r, vec);
     } else {
       float v[EPT];
       if (of_post) post_factor(v, r);
@@ -144,12 +145,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
       pairs_of(f, v);
     }
   };
-  F2 post1[RUNS][PPT], post0[RUNS][PPT], pre1[RUNS][PPT], pre0[RUNS][PPT];  // with a ring
+  F2 post1[RUNS][PPT], post0[RUNS][PPT], pre1[RUNS][PPT], pre0[RUNS][PPT];  // HOLD
 #pragma unroll
   for (int r = 0; r < RUNS; ++r)
 #pragma unroll
     for (int i = 0; i < PPT; ++i) post1[r][i] = post0[r][i] = pre1[r][i] = pre0[r][i] = f2(0.0f);
-  if (!RING)
+  if (!HOLD)
     for (int j = 0; j < a.nacc; ++j)
 #pragma unroll
       for (int r = 0; r < RUNS; ++r)
@@ -170,16 +171,18 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r);
-      else load_row<A>(oc[r], a.o, a.o_dtype, at_o, r, H, vec);
+      else load_row<OT, A>(oc[r], a.o, at_o, r, H, vec);
       if (pre) {
         if constexpr (RING) {
           copy_out<HT, A>(hc[r], ring_h + slot * pitch, r);
           copy_out<OT, A>(dx[r], ring_x + slot * pitch, r);
         } else {
-          load_row<A>(hc[r], a.h, a.h_dtype, at_h, r, H, vec);
-          load_row<A>(dx[r], a.dx_out, a.o_dtype, at_o, r, H, vec);
+          load_row<HT, A>(hc[r], a.h, at_h, r, H, vec);
+          load_row<OT, A>(dx[r], a.dx_out, at_o, r, H, vec);
         }
       }
+      if constexpr (!RING)
+        if (a.dh_out) load_row<HT, A>(G[r], a.dh_out, at_h, r, H, vec);
     }
     if (GENERAL && (layer_pre || layer_post)) {
       F2 sh = f2(0.0f), so = f2(0.0f);
@@ -238,12 +241,11 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
     }
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if (a.dh_out) {
-        if constexpr (RING) copy_out<HT, A>(G[r], ring_g + slot * pitch, r);
-        else load_row<A>(G[r], a.dh_out, a.h_dtype, at_h, r, H, vec);
-      } else {
+      if (!a.dh_out) {
 #pragma unroll
         for (int i = 0; i < PPT; ++i) G[r][i] = f2(0.0f);
+      } else if constexpr (RING) {
+        copy_out<HT, A>(G[r], ring_g + slot * pitch, r);
       }
       if (pre) {
         F2 f[PPT];
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
           hc[r][i] = u;
         }
         if (GENERAL) clear_past<A>(G[r], r, H, vec);
-        if (RING) {
+        if (HOLD) {
 #pragma unroll
           for (int i = 0; i < PPT; ++i) pre1[r][i] = fma2(dx[r][i], hc[r][i], pre1[r][i]);
           if (GENERAL)
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
         F2 d[PPT];
 #pragma unroll
         for (int i = 0; i < PPT; ++i) d[i] = f2(a.beta) * G[r][i];
-        store_row<HT, A>(a.dh, a.h_dtype, at_h, r, H, vec, d);
+        store_row<HT, A>(a.dh, at_h, r, H, vec, d);
       }
     }
     // the block's side: alpha G is the gradient of g N(o); G becomes dn w
@@ -296,8 +298,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 #pragma unroll
         for (int i = 0; i < PPT; ++i) w[i] = w[i] * oc[r][i];
         if (a.b_post) {
-          if constexpr (RING) {
-            copy_out<float, A>(c, s_bias, r);
+          if constexpr (HOLD) {
+            copy_out<float, A>(c, s_bias, r, vec);
           } else {
             float v[EPT];
             load_columns<A>(v, a.b_post, a.w_dtype, r, H, vec, 0.0f);
@@ -311,17 +313,17 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
           c[i] = G[r][i] * w[i];
           d2 = d2 + c[i];
         }
-        if (gate_f) store_row<OT, A>(a.dgate, a.o_dtype, at_o, r, H, vec, c);
+        if (gate_f) store_row<OT, A>(a.dgate, at_o, r, H, vec, c);
       }
       if (GENERAL && gate_f) {
-        load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
+        load_row<OT, A>(c, a.gate, at_o, r, H, vec);
 #pragma unroll
         for (int i = 0; i < PPT; ++i) G[r][i] = G[r][i] * c[i];
       } else if (GENERAL && gate_t) {
 #pragma unroll
         for (int i = 0; i < PPT; ++i) G[r][i] = G[r][i] * f2(gt);
       }
-      if (RING) {
+      if (HOLD) {
 #pragma unroll
         for (int i = 0; i < PPT; ++i) post1[r][i] = fma2(G[r][i], oc[r][i], post1[r][i]);
         if (GENERAL)
@@ -359,19 +361,19 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
             G[r][i] = f2(ro) * v;
           }
         }
-        store_row<OT, A>(a.d_o, a.o_dtype, at_o, r, H, vec, G[r]);
+        store_row<OT, A>(a.d_o, at_o, r, H, vec, G[r]);
       }
     }
     if (++slot >= a.depth) slot = 0;
   }
   // each thread hands over the columns that it summed
-  if (RING) {
+  if (HOLD) {
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if (a.acc_post1 >= 0) store_row<float, A>(part + a.acc_post1 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, post1[r]);
-      if (a.acc_post0 >= 0) store_row<float, A>(part + a.acc_post0 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, post0[r]);
-      if (a.acc_pre1 >= 0) store_row<float, A>(part + a.acc_pre1 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, pre1[r]);
-      if (a.acc_pre0 >= 0) store_row<float, A>(part + a.acc_pre0 * sums_pitch, MOE_DTYPE_F32, 0, r, H, vec, pre0[r]);
+      if (a.acc_post1 >= 0) store_row<float, A>(part + a.acc_post1 * sums_pitch, 0, r, H, vec, post1[r]);
+      if (a.acc_post0 >= 0) store_row<float, A>(part + a.acc_post0 * sums_pitch, 0, r, H, vec, post0[r]);
+      if (a.acc_pre1 >= 0) store_row<float, A>(part + a.acc_pre1 * sums_pitch, 0, r, H, vec, pre1[r]);
+      if (a.acc_pre0 >= 0) store_row<float, A>(part + a.acc_pre0 * sums_pitch, 0, r, H, vec, pre0[r]);
     }
   } else if (a.acc_in_smem) {
     for (int j = 0; j < a.nacc; ++j)
@@ -471,42 +473,51 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
       cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, MAXT, GENERAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemMax));
   if (attr != cudaSuccess) return attr;
-  const size_t pitch = slot_pitch<A>(a.H, threads);
+  const size_t pitch = slot_pitch(threads);
   int per_sm = min_blocks(MAXT, GENERAL) * MAXT / threads;
   if (per_sm > most_blocks_per_sm(a.H)) per_sm = most_blocks_per_sm(a.H);
   size_t smem = 0;
   a.depth = 0;
-  if (A != PLAIN) {
-    // a row that is worked on and, where they fit with the resident blocks, one or two
-    // on their way; 128 KB at most for one row, beside 96 KB of factors
-    const size_t row = pitch * (sizeof(OT) + (a.dh_out ? sizeof(HT) : 0) + (a.pre ? sizeof(HT) + sizeof(OT) : 0));
+  auto fits = [&](size_t bytes, int blocks) { return bytes <= kSmemMax && (bytes + 2048) * blocks <= kSmemSm; };
+  if (MAXT <= 512) {
     const size_t factors = (bias_in_smem(a) ? 3 : 2) * pitch * sizeof(float);
-    a.depth = 3;
-    auto fits = [&](size_t bytes, int blocks) { return bytes <= kSmemMax && (bytes + 2048) * blocks <= kSmemSm; };
-    while (a.depth > 1 && !fits(a.depth * row + factors, per_sm)) --a.depth;
-    smem = a.depth * row + factors;
-    while (per_sm > 1 && (smem + 2048) * per_sm > kSmemSm) --per_sm;
+    if (A != PLAIN) {
+      // a row that is worked on and, where they fit with the resident blocks, one or two
+      // on their way; 128 KB at most for one row, beside 96 KB of factors
+      const size_t row = pitch * (sizeof(OT) + (a.dh_out ? sizeof(HT) : 0) + (a.pre ? sizeof(HT) + sizeof(OT) : 0));
+      a.depth = 3;
+      while (a.depth > 1 && !fits(a.depth * row + factors, per_sm)) --a.depth;
+      smem = a.depth * row;
+    }
+    smem += factors;
   } else {
-    smem = a.nacc * pitch * sizeof(float);
+    smem = a.nacc * norm_pitch(a.H) * sizeof(float);
     a.acc_in_smem = smem <= kSmemMax;  // else the sums are kept in the workspace itself
     if (!a.acc_in_smem) smem = 0;
-    while (per_sm > 1 && (smem + 2048) * per_sm > kSmemSm) --per_sm;
   }
+  while (per_sm > 1 && !fits(smem, per_sm)) --per_sm;
   a.blocks = a.T < 152 * per_sm ? a.T : 152 * per_sm;
   return launch_dependent(norm_backward_kernel<HT, OT, A, MAXT, GENERAL>, dim3(a.blocks), dim3(threads), smem, s, a);
 }
 
-template <typename HT, typename OT, Access A>
-cudaError_t backward_ring(NormArgs& a, int threads, cudaStream_t s) {
-  if (a.acc_post0 >= 0 || a.acc_pre0 >= 0 || a.post == MOE_NORM_LAYER || a.pre == MOE_NORM_LAYER ||
-      a.gate_kind == MOE_GATE_TOKEN || a.gate_kind == MOE_GATE_FULL) {
-    if (threads <= 128) return backward_of<HT, OT, A, 128, true>(a, threads, s);
-    if (threads <= 256) return backward_of<HT, OT, A, 256, true>(a, threads, s);
-    return backward_of<HT, OT, A, 512, true>(a, threads, s);
+template <typename HT, typename OT>
+cudaError_t backward_types(NormArgs& a, cudaStream_t s) {
+  const int threads = norm_threads(a.H);
+  if (threads > 512) return backward_of<HT, OT, PLAIN, 1024, true>(a, threads, s);
+  if (a.vec) {
+    if (a.acc_post0 >= 0 || a.acc_pre0 >= 0 || a.post == MOE_NORM_LAYER || a.pre == MOE_NORM_LAYER ||
+        a.gate_kind == MOE_GATE_TOKEN || a.gate_kind == MOE_GATE_FULL) {
+      if (threads <= 128) return backward_of<HT, OT, VEC16, 128, true>(a, threads, s);
+      if (threads <= 256) return backward_of<HT, OT, VEC16, 256, true>(a, threads, s);
+      return backward_of<HT, OT, VEC16, 512, true>(a, threads, s);
+    }
+    if (threads <= 128) return backward_of<HT, OT, VEC16, 128, false>(a, threads, s);
+    if (threads <= 256) return backward_of<HT, OT, VEC16, 256, false>(a, threads, s);
+    return backward_of<HT, OT, VEC16, 512, false>(a, threads, s);
   }
-  if (threads <= 128) return backward_of<HT, OT, A, 128, false>(a, threads, s);
-  if (threads <= 256) return backward_of<HT, OT, A, 256, false>(a, threads, s);
-  return backward_of<HT, OT, A, 512, false>(a, threads, s);
+  constexpr Access odd = sizeof(HT) == 4 && sizeof(OT) == 4 ? WORD4 : PLAIN;
+  if (threads <= 128) return backward_of<HT, OT, odd, 128, true>(a, threads, s);
+  return backward_of<HT, OT, odd, 512, true>(a, threads, s);
 }
 
 }  // namespace
@@ -526,27 +537,15 @@ cudaError_t launch_norm_backward(const NormArgs& args, const NormSums& out, cuda
   a.acc_post0 = want(out.db_post || (out.dgate && a.b_post));
   a.acc_pre1 = want(out.dw_pre);
   a.acc_pre0 = want(out.db_pre);
-  const int threads = norm_threads(a.H);
-  const int pair = a.h_dtype * 3 + a.o_dtype;
   stage_begin("norm_backward", s);
   cudaError_t err;
-  if (threads > 512) {
-    err = backward_of<float, float, PLAIN, 1024, true>(a, threads, s);
-  } else if (a.vec) {
-    switch (pair) {
-      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32: err = backward_ring<float, float, VEC16>(a, threads, s); break;
-      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_BF16: err = backward_ring<float, __nv_bfloat16, VEC16>(a, threads, s); break;
-      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F16: err = backward_ring<float, __half, VEC16>(a, threads, s); break;
-      case MOE_DTYPE_BF16 * 3 + MOE_DTYPE_BF16:
-        err = backward_ring<__nv_bfloat16, __nv_bfloat16, VEC16>(a, threads, s);
-        break;
-      default: err = backward_ring<__half, __half, VEC16>(a, threads, s);
-    }
-  } else if (pair == MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32) {
-    err = backward_ring<float, float, WORD4>(a, threads, s);
-  } else {
-    err = backward_of<float, float, PLAIN, 512, true>(a, threads, s);
-  }
+  if (a.h_dtype == MOE_DTYPE_F32)
+    err = a.o_dtype == MOE_DTYPE_F32    ? backward_types<float, float>(a, s)
+          : a.o_dtype == MOE_DTYPE_BF16 ? backward_types<float, __nv_bfloat16>(a, s)
+                                        : backward_types<float, __half>(a, s);
+  else
+    err = a.h_dtype == MOE_DTYPE_BF16 ? backward_types<__nv_bfloat16, __nv_bfloat16>(a, s)
+                                      : backward_types<__half, __half>(a, s);
   stage_end(s);
   if (err == cudaSuccess && a.nacc > 0) {
     stage_begin("column_sums", s);

@@ -18,17 +18,18 @@ constexpr int min_blocks(int maxt) { return maxt <= 512 ? 1024 / maxt : 1; }
 template <typename HT, typename OT, Access A, int MAXT>
 __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(NormArgs a) {
   constexpr bool RING = A != PLAIN;
+  constexpr bool HOLD = MAXT <= 512;  // factors and biases in shared memory
   using Sum = BlockSum<1, MAXT>;
   __shared__ __align__(16) float s_sum[2][1][Sum::W];
   extern __shared__ __align__(16) uint8_t s_ring[];
   const int H = a.H;
   const bool vec = A == VEC16 || (A == PLAIN && a.vec);
   const float inv_h = 1.0f / static_cast<float>(H);
-  const int pitch = slot_pitch<A>(H, blockDim.x);
+  const int pitch = slot_pitch(blockDim.x);
   // ring | factors of the post and of the pre norm, then their biases where there are any;
   // each column with its thread
   HT* ring_h = reinterpret_cast<HT*>(s_ring);
-  OT* ring_o = reinterpret_cast<OT*>(ring_h + a.depth * pitch);
+  OT* ring_o = reinterpret_cast<OT*>(ring_h + a.depth * pitch);  // depth 0 without a ring
   float* s_post = reinterpret_cast<float*>(ring_o + a.depth * pitch);
   float* s_pre = s_post + pitch;
   float* s_bpost = s_pre + pitch;
@@ -66,21 +67,21 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       for (int i = 0; i < EPT; ++i) f[i] *= g[i];
     }
   };
-  if (RING)
+  if (HOLD)
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
       post_column(f, a.w_post, 1.0f, r);
-      put_shared<A>(s_post, r, f);
+      put_shared<A>(s_post, r, vec, f);
       load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-      put_shared<A>(s_pre, r, f);
+      put_shared<A>(s_pre, r, vec, f);
       if (a.b_post) {
         post_column(f, a.b_post, 0.0f, r);
-        put_shared<A>(s_bpost, r, f);
+        put_shared<A>(s_bpost, r, vec, f);
       }
       if (a.b_pre) {
         load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
-        put_shared<A>(s_bpre, r, f);
+        put_shared<A>(s_bpre, r, vec, f);
       }
     }
 
@@ -92,10 +93,15 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
     }
+    F2 hv[RUNS][PPT];  // without a ring: h's loads go out with o's
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if constexpr (RING) copy_out<OT, A>(v[r], ring_o + slot * pitch, r);
-      else load_row<A>(v[r], a.o, a.o_dtype, at_o, r, H, vec);
+      if constexpr (RING) {
+        copy_out<OT, A>(v[r], ring_o + slot * pitch, r);
+      } else {
+        load_row<OT, A>(v[r], a.o, at_o, r, H, vec);
+        load_row<HT, A>(hv[r], a.h, at_h, r, H, vec);
+      }
     }
 
     // takes the mean off v (layer norms) and returns 1 / std
@@ -133,8 +139,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
     for (int r = 0; r < RUNS; ++r) {
       F2 c[PPT];
       float f[EPT];
-      if constexpr (RING) {
-        copy_out<float, A>(c, s_post, r);
+      if constexpr (HOLD) {
+        copy_out<float, A>(c, s_post, r, vec);
       } else {
         post_column(f, a.w_post, 1.0f, r);
         pairs_of(c, f);
@@ -142,8 +148,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
       for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rs * c[i]);
       if (a.b_post) {
-        if constexpr (RING) {
-          copy_out<float, A>(c, s_bpost, r);
+        if constexpr (HOLD) {
+          copy_out<float, A>(c, s_bpost, r, vec);
         } else {
           post_column(f, a.b_post, 0.0f, r);
           pairs_of(c, f);
@@ -152,15 +158,14 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
         for (int i = 0; i < PPT; ++i) v[r][i] = fma2(f2(scale), c[i], v[r][i]);
       }
       if (gate_f) {
-        load_row<A>(c, a.gate, a.o_dtype, at_o, r, H, vec);
+        load_row<OT, A>(c, a.gate, at_o, r, H, vec);
 #pragma unroll
         for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * c[i];
       }
-      if constexpr (RING) copy_out<HT, A>(c, ring_h + slot * pitch, r);
-      else load_row<A>(c, a.h, a.h_dtype, at_h, r, H, vec);
+      if constexpr (RING) copy_out<HT, A>(hv[r], ring_h + slot * pitch, r);
 #pragma unroll
-      for (int i = 0; i < PPT; ++i) v[r][i] = fma2(beta, c[i], v[r][i]);
-      store_row<HT, A>(a.h_out, a.h_dtype, at_h, r, H, vec, v[r]);
+      for (int i = 0; i < PPT; ++i) v[r][i] = fma2(beta, hv[r][i], v[r][i]);
+      store_row<HT, A>(a.h_out, at_h, r, H, vec, v[r]);
     }
     // x' is taken from h' before its rounding: one rounding each
     if (a.pre != MOE_NORM_NONE) {
@@ -169,8 +174,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       for (int r = 0; r < RUNS; ++r) {
         F2 c[PPT];
         float f[EPT];
-        if constexpr (RING) {
-          copy_out<float, A>(c, s_pre, r);
+        if constexpr (HOLD) {
+          copy_out<float, A>(c, s_pre, r, vec);
         } else {
           load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
           pairs_of(c, f);
@@ -178,8 +183,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
         for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rp * c[i]);
         if (a.b_pre) {
-          if constexpr (RING) {
-            copy_out<float, A>(c, s_bpre, r);
+          if constexpr (HOLD) {
+            copy_out<float, A>(c, s_bpre, r, vec);
           } else {
             load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
             pairs_of(c, f);
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
           for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] + c[i];
         }
-        store_row<OT, A>(a.x_out, a.o_dtype, at_o, r, H, vec, v[r]);
+        store_row<OT, A>(a.x_out, at_o, r, H, vec, v[r]);
       }
     }
     if (++slot >= a.depth) slot = 0;
@@ -201,15 +206,17 @@ cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
   int per_sm = min_blocks(MAXT) * MAXT / threads;
   if (per_sm > 32) per_sm = 32;
   size_t smem = 0;
-  if (A != PLAIN) {
+  a.depth = 0;
+  if (MAXT <= 512) {
     static const cudaError_t attr =
         cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemMax));
     if (attr != cudaSuccess) return attr;
-    const size_t pitch = slot_pitch<A>(a.H, threads), row = pitch * (sizeof(HT) + sizeof(OT));
+    const size_t pitch = slot_pitch(threads), row = pitch * (sizeof(HT) + sizeof(OT));
     const size_t factors = (2 + (a.b_post ? 1 : 0) + (a.b_pre ? 1 : 0)) * pitch * sizeof(float);
     // two rows on their way; one, or none, where shared memory has no room for them beside the resident blocks
-    a.depth = (3 * row + factors + 2048) * per_sm <= kSmemMax ? 3 : 2 * row + factors <= kSmemMax ? 2 : 1;
+    if (A != PLAIN)
+      a.depth = (3 * row + factors + 2048) * per_sm <= kSmemMax ? 3 : 2 * row + factors <= kSmemMax ? 2 : 1;
     smem = a.depth * row + factors;  // at most 64 KB + 128 KB
     while (per_sm > 1 && (smem + 2048) * per_sm > kSmemMax) --per_sm;
   }
@@ -217,11 +224,18 @@ cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
   return launch_dependent(norm_forward_kernel<HT, OT, A, MAXT>, dim3(a.T < cap ? a.T : cap), dim3(threads), smem, s, a);
 }
 
-template <typename HT, typename OT, Access A>
-cudaError_t forward_ring(const NormArgs& a, int threads, cudaStream_t s) {
-  if (threads <= 128) return forward_of<HT, OT, A, 128>(a, threads, s);
-  if (threads <= 256) return forward_of<HT, OT, A, 256>(a, threads, s);
-  return forward_of<HT, OT, A, 512>(a, threads, s);
+template <typename HT, typename OT>
+cudaError_t forward_types(const NormArgs& a, cudaStream_t s) {
+  const int threads = norm_threads(a.H);
+  if (threads > 512) return forward_of<HT, OT, PLAIN, 1024>(a, threads, s);
+  if (a.vec) {
+    if (threads <= 128) return forward_of<HT, OT, VEC16, 128>(a, threads, s);
+    if (threads <= 256) return forward_of<HT, OT, VEC16, 256>(a, threads, s);
+    return forward_of<HT, OT, VEC16, 512>(a, threads, s);
+  }
+  constexpr Access odd = sizeof(HT) == 4 && sizeof(OT) == 4 ? WORD4 : PLAIN;
+  if (threads <= 128) return forward_of<HT, OT, odd, 128>(a, threads, s);
+  return forward_of<HT, OT, odd, 512>(a, threads, s);
 }
 
 }  // namespace
@@ -229,27 +243,15 @@ cudaError_t forward_ring(const NormArgs& a, int threads, cudaStream_t s) {
 
 cudaError_t launch_norm_forward(const NormArgs& a, cudaStream_t s) {
   using namespace norms;
-  const int threads = norm_threads(a.H);
-  const int pair = a.h_dtype * 3 + a.o_dtype;
   stage_begin("norm_forward", s);
   cudaError_t err;
-  if (threads > 512) {
-    err = forward_of<float, float, PLAIN, 1024>(a, threads, s);
-  } else if (a.vec) {
-    switch (pair) {
-      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32: err = forward_ring<float, float, VEC16>(a, threads, s); break;
-      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_BF16: err = forward_ring<float, __nv_bfloat16, VEC16>(a, threads, s); break;
-      case MOE_DTYPE_F32 * 3 + MOE_DTYPE_F16: err = forward_ring<float, __half, VEC16>(a, threads, s); break;
-      case MOE_DTYPE_BF16 * 3 + MOE_DTYPE_BF16:
-        err = forward_ring<__nv_bfloat16, __nv_bfloat16, VEC16>(a, threads, s);
-        break;
-      default: err = forward_ring<__half, __half, VEC16>(a, threads, s);
-    }
-  } else if (pair == MOE_DTYPE_F32 * 3 + MOE_DTYPE_F32) {
-    err = forward_ring<float, float, WORD4>(a, threads, s);
-  } else {
-    err = forward_of<float, float, PLAIN, 512>(a, threads, s);
-  }
+  if (a.h_dtype == MOE_DTYPE_F32)
+    err = a.o_dtype == MOE_DTYPE_F32    ? forward_types<float, float>(a, s)
+          : a.o_dtype == MOE_DTYPE_BF16 ? forward_types<float, __nv_bfloat16>(a, s)
+                                        : forward_types<float, __half>(a, s);
+  else
+    err = a.h_dtype == MOE_DTYPE_BF16 ? forward_types<__nv_bfloat16, __nv_bfloat16>(a, s)
+                                      : forward_types<__half, __half>(a, s);
   stage_end(s);
   return err;
 }
