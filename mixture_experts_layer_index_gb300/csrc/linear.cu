@@ -38,18 +38,29 @@ constexpr int stages_of(int BN, int blocks) {
   return n > MAX_STAGES ? MAX_STAGES : n;
 }
 
-struct Params {
+// One product of a launch.
+struct TileProduct {
   int C, R;        // output columns and rows
   int nk;          // stages of the whole sum
+  int nC, nR;      // tiles
+  int a_mn, b_mn;  // operand columns / rows contiguous along c / r
+  Epilogue ep;
+};
+// A launch computes one product, or two side by side (a gradient's two, when neither fills
+// the GPU): blocks from `first_blocks` on belong to the second.
+struct Params {
+  TileProduct prod[2];
+  int first_blocks;
   int stages;      // of the ring
   int splits;      // blocks per tile (cluster size)
-  int nC, nR;      // tiles
   int nacc;        // accumulators that a block's part of the sum is spread over
   uint32_t tmem_cols;
   int type;        // 0 = f16, 1 = bf16 operands
-  Epilogue ep;
   int reset_status;
   DeviceHeader* hdr;
+};
+struct TileMaps {
+  CUtensorMap a, b;
 };
 
 // fp32 at shared-memory address `addr` of block `rank` of the cluster
@@ -104,7 +115,7 @@ __device__ __forceinline__ void add_rows(float (&v)[CH], const void* in, int dty
 
 // The fused epilogue of n rows from r0 of output column c (one thread's values).
 template <int CH>
-__device__ __forceinline__ void finish(const Params& p, float (&v)[CH], int r0, int n, int c) {
+__device__ __forceinline__ void finish(const TileProduct& p, float (&v)[CH], int r0, int n, int c) {
   if (c >= p.C || n <= 0) return;
   if (p.ep.bias) {
     const float b = load_as_f32(p.ep.bias, p.ep.bias_dtype, c);
@@ -129,10 +140,10 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[CH]) {
 
 // Warp 0 loads, warp 1 issues the MMAs, then all four warps (one per 32 TMEM lanes)
 // run the epilogue.
-template <int BN, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__ CUtensorMap tmA,
-                                                         const __grid_constant__ CUtensorMap tmB, const Params p) {
-  static_assert(!B_MN || BN >= 64, "an MN-major box is 64 wide");
+template <int BN>
+__global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__ TileMaps m0,
+                                                         const __grid_constant__ TileMaps m1,
+                                                         const __grid_constant__ Params p) {
   constexpr int STAGE = stage_bytes(BN);
   constexpr int CH = BN < 32 ? BN : 32;
   extern __shared__ uint8_t smem_raw[];
@@ -142,6 +153,11 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   volatile int* abort_flag = &abort_word;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool second = static_cast<int>(blockIdx.x) >= p.first_blocks;
+  const TileProduct& o = p.prod[second ? 1 : 0];
+  const CUtensorMap* ma = second ? &m1.a : &m0.a;
+  const CUtensorMap* mb = second ? &m1.b : &m0.b;
+  const bool a_mn = o.a_mn, b_mn = BN >= 64 && o.b_mn;  // an MN-major box is 64 wide
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + MAX_STAGES), done = smem_u32(bars + 2 * MAX_STAGES);
 
   if (threadIdx.x == 0) {
@@ -152,8 +168,8 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
     mbar_init(done, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
+    prefetch_tensormap(ma);
+    prefetch_tensormap(mb);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), p.tmem_cols);
@@ -171,16 +187,16 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   // tiles: 16 row tiles side by side, then the next column tile, so that the blocks in
   // flight share both operands in L2
   const int rank = p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int tile = static_cast<int>(blockIdx.x) / p.splits;
+  const int tile = (static_cast<int>(blockIdx.x) - (second ? p.first_blocks : 0)) / p.splits;
   constexpr int GR = 16;
-  const int group = tile / (GR * p.nC), in_group = tile - group * (GR * p.nC);
-  const int rows_here = min(GR, p.nR - group * GR);
+  const int group = tile / (GR * o.nC), in_group = tile - group * (GR * o.nC);
+  const int rows_here = min(GR, o.nR - group * GR);
   const int c0 = in_group / rows_here * BM;
   const int r0 = (group * GR + in_group % rows_here) * BN;
-  const int kb0 = static_cast<int>(static_cast<long long>(p.nk) * rank / p.splits);
-  const int kb1 = static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / p.splits);
-  const int n = kb1 - kb0;
-  const int nacc = min(p.nacc, n);  // accumulators that this block fills
+  const int kb0 = static_cast<int>(static_cast<long long>(o.nk) * rank / p.splits);
+  const int kb1 = static_cast<int>(static_cast<long long>(o.nk) * (rank + 1) / p.splits);
+  const int n = kb1 - kb0;                // at least 1: splits <= nk
+  const int nacc = min(p.nacc, n);        // accumulators that this block fills
 
   // Both roles: uniform control flow (addresses and descriptors stay in uniform
   // registers), one lane issues, the next barrier is looked at ahead.
@@ -200,17 +216,17 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       if (leader) {
         const int k = (kb0 + issued) * BK;
         mbar_arrive_expect_tx(full, STAGE);
-        if (A_MN) {
-          tma_load_2d(a, &tmA, c0, k, full);
-          tma_load_2d(a + A_BYTES / 2, &tmA, c0 + 64, k, full);
+        if (a_mn) {
+          tma_load_2d(a, ma, c0, k, full);
+          tma_load_2d(a + A_BYTES / 2, ma, c0 + 64, k, full);
         } else {
-          tma_load_2d(a, &tmA, k, c0, full);
+          tma_load_2d(a, ma, k, c0, full);
         }
-        if (B_MN) {
+        if (b_mn) {
 #pragma unroll
-          for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &tmB, r0 + j * 64, k, full);
+          for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, mb, r0 + j * 64, k, full);
         } else {
-          tma_load_2d(b, &tmB, k, r0, full);
+          tma_load_2d(b, mb, k, r0, full);
         }
       }
       __syncwarp();
@@ -221,7 +237,8 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
         mbar_wait_quiet(full0 + 8 * (i % p.stages), (i / p.stages) & 1, 50000000ull);
   } else if (warp == 1) {
     const bool leader = elect_one();
-    const uint32_t idesc = make_idesc(p.type, p.type, BM, BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+    const uint32_t idesc = make_idesc(p.type, p.type, BM, BN) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+    const OperandWalk wa(a_mn), wb(b_mn);
     const uint32_t ring = smem_u32(smem);
     uint32_t stage = 0, phase = 0;
     int acc = -1;
@@ -241,20 +258,20 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_f16(tmem + acc * BN, OperandDesc<A_MN>::at(a, kk), OperandDesc<B_MN>::at(b, kk), idesc,
+          mma_f16(tmem + acc * BN, wa.at(a, kk), wb.at(b, kk), idesc,
                   !(fresh && kk == 0));
         mma_commit(empty);
       }
       __syncwarp();
     }
     if (leader) mma_commit(done);
-  } else if (p.ep.residual) {
+  } else if (o.ep.residual) {
     // the residual's part of the tile comes into L2 while the product is computed
-    const size_t es = p.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
-    const size_t bytes = static_cast<size_t>(min(BM, p.C - c0)) * es;
+    const size_t es = o.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+    const size_t bytes = static_cast<size_t>(min(BM, o.C - c0)) * es;
     const int share = BN / p.splits;
-    for (int j = rank * share + (warp - 2) * 32 + lane; j < min((rank + 1) * share, p.R - r0); j += 64) {
-      const uint8_t* row = static_cast<const uint8_t*>(p.ep.residual) + (static_cast<size_t>(r0 + j) * p.ep.ld_y + c0) * es;
+    for (int j = rank * share + (warp - 2) * 32 + lane; j < min((rank + 1) * share, o.R - r0); j += 64) {
+      const uint8_t* row = static_cast<const uint8_t*>(o.ep.residual) + (static_cast<size_t>(r0 + j) * o.ep.ld_y + c0) * es;
       for (size_t b = 0; b < bytes; b += 128) prefetch_l2(row + b);
     }
   }
@@ -279,16 +296,16 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   };
   // Few output columns leave most lanes without one: the values then go through shared
   // memory too, and groups of `width` threads take rows in turn.
-  const int cols = min(BM, p.C - c0);
+  const int cols = min(BM, o.C - c0);
   const int width = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : BM;
   if (p.splits == 1 && width == BM) {
     if (good) {
 #pragma unroll 1
       for (int j = 0; j < BN; j += CH) {
-        if (r0 + j >= p.R) break;
+        if (r0 + j >= o.R) break;
         float v[CH];
         gather(j, v);
-        finish<CH>(p, v, r0 + j, min(CH, p.R - r0 - j), c0 + cl);
+        finish<CH>(o, v, r0 + j, min(CH, o.R - r0 - j), c0 + cl);
       }
     }
   } else {
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       constexpr int RB = 8;
       const uint32_t mine = smem_u32(part) + c * 4;
       const int begin = rank * per + own * per_group;
-      const int end = min(min(begin + per_group, (rank + 1) * per), p.R - r0);
+      const int end = min(min(begin + per_group, (rank + 1) * per), o.R - r0);
       for (int j = begin; j < end; j += RB) {
         const int cnt = min(RB, end - j);
         float u[MAX_SPLITS][RB];
@@ -330,7 +347,7 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
           if (q < p.splits)
 #pragma unroll
             for (int i = 0; i < RB; ++i) v[i] += u[q][i];
-        finish<RB>(p, v, r0 + j, cnt, c0 + c);
+        finish<RB>(o, v, r0 + j, cnt, c0 + c);
       }
     }
     if (p.splits > 1) cluster_sync_all();  // no block leaves while another still reads its partial
@@ -343,31 +360,50 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   }
 }
 
-template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
-  CUtensorMap ta, tb;
-  if (!encode(&ta, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, A_MN ? 64 : BM) ||
-      !encode(&tb, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, B_MN ? 64 : BN))
-    return cudaErrorInvalidValue;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(linear_kernel<BN, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem_bytes(BN, stages_of(BN, 1)));
+bool encode_product(TileMaps* m, TileProduct* t, const Product& q, int bn) {
+  t->C = q.C;
+  t->R = q.R;
+  t->nk = (q.K + BK - 1) / BK;
+  t->nC = (q.C + BM - 1) / BM;
+  t->nR = (q.R + bn - 1) / bn;
+  t->a_mn = q.cols_mn;
+  t->b_mn = q.rows_mn;
+  t->ep = q.ep;
+  return encode(&m->a, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn ? 64 : BM) &&
+         encode(&m->b, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : bn);
+}
+
+template <int BN>
+cudaError_t launch_tile(const Product& q, const Product* second, int splits, cudaStream_t s) {
+  Params p{};
+  TileMaps m0, m1;
+  if (!encode_product(&m0, &p.prod[0], q, BN)) return cudaErrorInvalidValue;
+  m1 = m0;
+  if (second && !encode_product(&m1, &p.prod[1], *second, BN)) return cudaErrorInvalidValue;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN, stages_of(BN, 1)));
   if (attr != cudaSuccess) return attr;
-  p.nC = (p.C + BM - 1) / BM;
-  p.nR = (p.R + BN - 1) / BN;
+  p.splits = splits;
+  p.type = q.type;
+  p.reset_status = q.reset_status;
+  p.hdr = q.hdr;
+  p.first_blocks = p.prod[0].nC * p.prod[0].nR * splits;
+  const long long blocks = p.first_blocks + static_cast<long long>(p.prod[1].nC) * p.prod[1].nR * splits;
   // one block per SM where the grid leaves no second one: its ring takes all of shared
   // memory (not in large clusters, which then no longer find enough free SMs together)
-  const long long blocks = static_cast<long long>(p.nC) * p.nR * p.splits;
-  p.stages = stages_of(BN, BN == 256 || (blocks <= 152 && p.splits <= 2) ? 1 : 2);
+  p.stages = stages_of(BN, BN == 256 || (blocks <= 152 && splits <= 2) ? 1 : 2);
+  // fp32 output: the tensor core's running sum rounds at every step, so its length is
+  // kept short by spreading the sum over up to four accumulators
+  p.nacc = q.ep.out_dtype != MOE_DTYPE_F32 ? 1 : BN <= 64 ? 4 : 2;
   int cols = 32;
   while (cols < BN * p.nacc) cols *= 2;
   p.tmem_cols = cols;
   cudaLaunchAttribute la[2];
+  la[0].id = cudaLaunchAttributeClusterDimension;
+  la[0].val.clusterDim.x = splits;
+  la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
   la[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[1].val.programmaticStreamSerializationAllowed = 1;
-  la[0].id = cudaLaunchAttributeClusterDimension;
-  la[0].val.clusterDim.x = p.splits;
-  la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(THREADS);
@@ -375,7 +411,7 @@ cudaError_t launch_tile(const Product& q, Params p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = la;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<BN, A_MN, B_MN>, ta, tb, p);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<BN>, m0, m1, p);
 }
 
 // About how long a launch takes (us), for tiles of 128 x bn split over `splits` blocks.
@@ -425,30 +461,35 @@ Choice choose_tile(const Product& q) {
   return best;
 }
 
-template <bool A_MN, bool B_MN>
-cudaError_t launch_shape(const Product& q, const Choice& c, cudaStream_t s) {
-  Params p{};
-  p.C = q.C;
-  p.R = q.R;
-  p.type = q.type;
-  p.ep = q.ep;
-  p.reset_status = q.reset_status;
-  p.hdr = q.hdr;
-  p.nk = (q.K + BK - 1) / BK;
-  p.splits = c.splits;
-  // fp32 output: the tensor core's running sum rounds at every step, so its length is
-  // kept short by spreading the sum over up to four accumulators
-  p.nacc = 1;
-  if (p.ep.out_dtype == MOE_DTYPE_F32) p.nacc = c.bn <= 64 ? 4 : 2;
+cudaError_t launch_shape(const Product& q, const Product* second, const Choice& c, cudaStream_t s) {
   switch (c.bn) {
-    case 16:
-      if constexpr (!B_MN) return launch_tile<16, A_MN, B_MN>(q, p, s);
-    case 32:
-      if constexpr (!B_MN) return launch_tile<32, A_MN, B_MN>(q, p, s);
-    case 64: return launch_tile<64, A_MN, B_MN>(q, p, s);
-    case 128: return launch_tile<128, A_MN, B_MN>(q, p, s);
-    default: return launch_tile<256, A_MN, B_MN>(q, p, s);
+    case 16: return launch_tile<16>(q, second, c.splits, s);
+    case 32: return launch_tile<32>(q, second, c.splits, s);
+    case 64: return launch_tile<64>(q, second, c.splits, s);
+    case 128: return launch_tile<128>(q, second, c.splits, s);
+    default: return launch_tile<256>(q, second, c.splits, s);
   }
+}
+
+// Two products in one wave of a launch of tiles of 128 x bn: the longer of the two, if they fit.
+Choice choose_both(const Product& q0, const Product& q1) {
+  Choice best{0, 1, 0.0f};
+  for (int bn = 64; bn <= 128; bn *= 2)
+    for (int splits = 1; splits <= MAX_SPLITS; splits *= 2) {
+      long long blocks = 0;
+      float us = 0.0f;
+      bool ok = true;
+      for (const Product* q : {&q0, &q1}) {
+        const long long nk = (q->K + BK - 1) / BK;
+        ok = ok && (splits == 1 || nk / splits >= 2);
+        blocks += static_cast<long long>((q->C + BM - 1) / BM) * ((q->R + bn - 1) / bn) * splits;
+        const float t = tile_estimate(*q, bn, splits);
+        us = t > us ? t : us;
+      }
+      if (!ok || blocks > 2 * (splits == 8 ? 128 : 152)) continue;
+      if (best.bn == 0 || us < best.us) best = {bn, splits, us};
+    }
+  return best;
 }
 
 bool takes_pair(const Product& q, const Choice& c) { return pair_estimate(q) < c.us; }
@@ -456,8 +497,7 @@ bool takes_pair(const Product& q, const Choice& c) { return pair_estimate(q) < c
 cudaError_t launch_product(const Product& q, cudaStream_t s) {
   const Choice c = choose_tile(q);
   if (takes_pair(q, c)) return launch_pair(q, nullptr, s);
-  if (!q.cols_mn) return launch_shape<false, false>(q, c, s);
-  return q.rows_mn ? launch_shape<true, true>(q, c, s) : launch_shape<true, false>(q, c, s);
+  return launch_shape(q, nullptr, c, s);
 }
 
 // ------------------------------------------------------------------ dz
@@ -663,11 +703,16 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
   dw.cols = {a.x, a.ld_x, a.K, a.M};
   dw.rows_mn = true;
   dw.ep.y = a.dw;
-  if (err == cudaSuccess && a.dx && a.dw && takes_pair(dx, choose_tile(dx)) && takes_pair(dw, choose_tile(dw))) {
-    stage_begin("linear_dx_dw", s);
-    err = launch_pair(dx, &dw, s);
-    stage_end(s);
-    return err;
+  if (err == cudaSuccess && a.dx && a.dw) {
+    const Choice cx = choose_tile(dx), cw = choose_tile(dw), both = choose_both(dx, dw);
+    const bool px = takes_pair(dx, cx), pw = takes_pair(dw, cw);
+    const float apart = (px ? pair_estimate(dx) : cx.us) + (pw ? pair_estimate(dw) : cw.us);
+    if ((px && pw) || (both.bn && both.us < apart)) {
+      stage_begin("linear_dx_dw", s);
+      err = px && pw ? launch_pair(dx, &dw, s) : launch_shape(dx, &dw, both, s);
+      stage_end(s);
+      return err;
+    }
   }
   if (err == cudaSuccess && a.dx) {
     stage_begin("linear_dx", s);

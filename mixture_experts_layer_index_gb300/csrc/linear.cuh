@@ -18,13 +18,16 @@ constexpr int BK = 64;  // values of the sum per stage: 128 bytes
 // the sum; 8-row groups along the sum 1024 bytes apart (stride byte offset), the next
 // 64 along MN one box = 8192 bytes on (leading byte offset); 16 values of the sum are
 // 2048 bytes on.  Only the address field changes, and it never carries out of its bits.
-template <bool MN>
-struct OperandDesc {
-  static constexpr uint64_t kFixed = (static_cast<uint64_t>(MN ? 8192u >> 4 : 1u) << 16) |
-                                     (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
-  static constexpr uint32_t kStep = (MN ? 2048u : 32u) >> 4;
-  static __device__ __forceinline__ uint64_t at(uint32_t smem_addr, int kk) {
-    return kFixed | (((smem_addr & 0x3FFFFu) >> 4) + kk * kStep);
+struct OperandWalk {
+  uint64_t fixed;
+  uint32_t step;
+  __device__ __forceinline__ explicit OperandWalk(bool mn)
+      : fixed((static_cast<uint64_t>(mn ? 8192u >> 4 : 1u) << 16) | (static_cast<uint64_t>(1024u >> 4) << 32) |
+              (1ull << 46) | (2ull << 61)),
+        step((mn ? 2048u : 32u) >> 4) {}
+  // kk-th run of 16 values of the stage at smem_addr
+  __device__ __forceinline__ uint64_t at(uint32_t smem_addr, int kk) const {
+    return fixed | (((smem_addr & 0x3FFFFu) >> 4) + kk * step);
   }
 };
 

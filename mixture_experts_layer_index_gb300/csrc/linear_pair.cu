@@ -357,10 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int nk = p.prod[prod].nk;
         const uint32_t idesc =
             make_idesc(p.type, p.type, TILE, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-        const uint64_t fixed_a = a_mn ? OperandDesc<true>::kFixed : OperandDesc<false>::kFixed;
-        const uint64_t fixed_b = b_mn ? OperandDesc<true>::kFixed : OperandDesc<false>::kFixed;
-        const uint32_t step_a = a_mn ? OperandDesc<true>::kStep : OperandDesc<false>::kStep;
-        const uint32_t step_b = b_mn ? OperandDesc<true>::kStep : OperandDesc<false>::kStep;
+        const OperandWalk wa(a_mn), wb(b_mn);
         if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.hdr, 0x620000u)) break;
         tc_fence_after();
         const uint32_t d = tmem + acc * TILE;
@@ -371,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t slot = (ring + stage * STAGE_BYTES) >> 4, empty = empty0 + 8 * stage;
+          const uint32_t a = ring + stage * STAGE_BYTES, empty = empty0 + 8 * stage;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -380,8 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_pair(d, fixed_a | (slot + kk * step_a), fixed_b | (slot + (OP_BYTES >> 4) + kk * step_b), idesc,
-                           (kb | kk) != 0);
+              mma_f16_pair(d, wa.at(a, kk), wb.at(a + OP_BYTES, kk), idesc, (kb | kk) != 0);
             mma_commit_pair(empty);
           }
           __syncwarp();
