@@ -228,6 +228,7 @@ struct NormArgs {
   int h_dtype, o_dtype;
   bool vec;   // every row and vector can be read 16 bytes at a time
   int depth;  // rows in a block's ring
+  int lanes;  // that take a row of up to 512 columns
   int blocks; // backward: blocks launched, one set of partial sums each
   int post, pre, gate_kind;  // moe_norm_kind, moe_gate_kind
   int w_dtype;

@@ -32,11 +32,26 @@ constexpr int RUNS = 2;
 //          which asynchronous copies do not take, and rows too long for a ring
 enum Access { VEC16, WORD4, PLAIN };
 
+// Which of the threads of a row this one is.  Rows of up to 512 columns (SMALL) leave part
+// of a warp idle if a block takes them one by one, and a block's fixed cost per row is
+// then most of its time; there a group of 4, 8, 16 or 32 lanes takes a row (32768 x 64
+// bf16: forward 21 -> 5 us, gradient 42 -> 12 us; 32768 x 512: 23.5 -> 20.3, 44 -> 42).  Odd
+// rows gain nothing over 256 columns (32768 x 300: 26 -> 31 us) or where every row finds a
+// free warp (600 x 151: 3.1 -> 3.9 us, but 19443 x 68: 17 -> 7.5), and stay one by one.
+constexpr int SMALL_H = 32 * EPT * RUNS;
+struct Own {
+  int tid, nt;  // number and count of the row's threads
+  int step;     // distance of a thread's columns in the layout of WORD4: 32, or nt < 32
+  bool vec;
+};
 template <Access A>
-__device__ __forceinline__ int col_of(int run, int i, bool vec) {
-  const bool together = A == VEC16 || (A == PLAIN && vec);
-  if (together) return (run * blockDim.x + threadIdx.x) * EPT + i;
-  return static_cast<int>(threadIdx.x >> 5) * (32 * RUNS * EPT) + (threadIdx.x & 31) + (run * EPT + i) * 32;
+__device__ __forceinline__ bool in_runs(const Own& me) {
+  return A == VEC16 || (A == PLAIN && me.vec);
+}
+template <Access A>
+__device__ __forceinline__ int col_of(int run, int i, const Own& me) {
+  if (in_runs<A>(me)) return (run * me.nt + me.tid) * EPT + i;
+  return (me.tid >> 5) * (32 * RUNS * EPT) + (me.tid & 31) + (run * EPT + i) * me.step;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -151,18 +166,18 @@ __device__ __forceinline__ __half rounded<__half>(float v) { return __float2half
 
 // A thread's columns of the row at element `at` of p; 0 past column H.
 template <typename T, Access A>
-__device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, size_t at, int run, int H, bool vec) {
+__device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, size_t at, int run, int H, const Own& me) {
   const T* row = static_cast<const T*>(p) + at;
 #pragma unroll
   for (int i = 0; i < EPT; ++i) v[i] = 0.0f;
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    const int c = col_of<A>(run, 0, vec);
+  if (in_runs<A>(me)) {
+    const int c = col_of<A>(run, 0, me);
     if (c < H) unpack(v, row + c);
   } else {
     T raw[EPT] = {};
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(run, i, vec);
+      const int c = col_of<A>(run, i, me);
       if (c < H) raw[i] = row[c];
     }
 #pragma unroll
@@ -170,15 +185,15 @@ __device__ __forceinline__ void load_row(float (&v)[EPT], const void* p, size_t 
   }
 }
 template <typename T, Access A>
-__device__ __forceinline__ void store_row(void* p, size_t at, int run, int H, bool vec, const float (&v)[EPT]) {
+__device__ __forceinline__ void store_row(void* p, size_t at, int run, int H, const Own& me, const float (&v)[EPT]) {
   T* row = static_cast<T*>(p) + at;
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    const int c = col_of<A>(run, 0, vec);
+  if (in_runs<A>(me)) {
+    const int c = col_of<A>(run, 0, me);
     if (c < H) pack(row + c, v);
   } else {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(run, i, vec);
+      const int c = col_of<A>(run, i, me);
       if (c < H) row[c] = rounded<T>(v[i]);
     }
   }
@@ -192,47 +207,47 @@ __device__ __forceinline__ float load_one(const void* p, int dtype, size_t i) {
   return __half2float(static_cast<const __half*>(p)[i]);
 }
 template <Access A>
-__device__ __forceinline__ void load_columns(float (&v)[EPT], const void* p, int dtype, int run, int H, bool vec,
+__device__ __forceinline__ void load_columns(float (&v)[EPT], const void* p, int dtype, int run, int H, const Own& me,
                                              float none) {
   if (p == nullptr) {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) v[i] = none;
   } else if (dtype == MOE_DTYPE_F32) {
-    load_row<float, A>(v, p, 0, run, H, vec);
+    load_row<float, A>(v, p, 0, run, H, me);
   } else if (dtype == MOE_DTYPE_BF16) {
-    load_row<__nv_bfloat16, A>(v, p, 0, run, H, vec);
+    load_row<__nv_bfloat16, A>(v, p, 0, run, H, me);
   } else {
-    load_row<__half, A>(v, p, 0, run, H, vec);
+    load_row<__half, A>(v, p, 0, run, H, me);
   }
 }
 
 // A thread's columns of an fp32 vector in shared memory, for itself.
 template <Access A>
-__device__ __forceinline__ void put_shared(float* slot, int run, bool vec, const float (&v)[EPT]) {
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    pack(slot + col_of<A>(run, 0, vec), v);
+__device__ __forceinline__ void put_shared(float* slot, int run, const Own& me, const float (&v)[EPT]) {
+  if (in_runs<A>(me)) {
+    pack(slot + col_of<A>(run, 0, me), v);
   } else {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) slot[col_of<A>(run, i, vec)] = v[i];
+    for (int i = 0; i < EPT; ++i) slot[col_of<A>(run, i, me)] = v[i];
   }
 }
 
 // The ring: slots of one row each of up to four arrays.
 template <typename T, Access A>
-__device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H) {
+__device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H, const Own& me) {
   const T* row = static_cast<const T*>(p) + at;
   constexpr int PER = 16 / sizeof(T);
 #pragma unroll
   for (int r = 0; r < RUNS; ++r) {
     if (A == VEC16) {
-      const int c = col_of<A>(r, 0, true);
+      const int c = col_of<A>(r, 0, me);
       if (c < H)
 #pragma unroll
         for (int q = 0; q < EPT / PER; ++q) cp_async16(slot + c + q * PER, row + c + q * PER);
     } else if (A == WORD4) {
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        const int c = col_of<A>(r, i, false);
+        const int c = col_of<A>(r, i, me);
         if (c < H) cp_async4(slot + c, row + c);
       }
     }
@@ -240,23 +255,23 @@ __device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H
 }
 // Zeros are put past column H of a slot once, so that reads need no test.
 template <typename T, Access A>
-__device__ __forceinline__ void clear_slot(T* slot, int H) {
+__device__ __forceinline__ void clear_slot(T* slot, int H, const Own& me) {
   if (A != PLAIN)
 #pragma unroll
     for (int r = 0; r < RUNS; ++r)
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        const int c = col_of<A>(r, i, true);
+        const int c = col_of<A>(r, i, me);
         if (c >= H) slot[c] = T(0.0f);
       }
 }
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, bool vec = A == VEC16) {
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    unpack(v, slot + col_of<A>(r, 0, vec));
+__device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, const Own& me) {
+  if (in_runs<A>(me)) {
+    unpack(v, slot + col_of<A>(r, 0, me));
   } else {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) v[i] = as_f32(slot[col_of<A>(r, i, vec)]);
+    for (int i = 0; i < EPT; ++i) v[i] = as_f32(slot[col_of<A>(r, i, me)]);
   }
 }
 
@@ -270,28 +285,28 @@ __device__ __forceinline__ void values_of(float (&v)[EPT], const F2 (&p)[PPT]) {
   for (int i = 0; i < PPT; ++i) split(p[i], v[2 * i], v[2 * i + 1]);
 }
 template <typename T, Access A>
-__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r, bool vec = A == VEC16) {
+__device__ __forceinline__ void copy_out(F2 (&p)[PPT], const T* slot, int r, const Own& me) {
   float v[EPT];
-  copy_out<T, A>(v, slot, r, vec);
+  copy_out<T, A>(v, slot, r, me);
   pairs_of(p, v);
 }
 template <typename T, Access A>
-__device__ __forceinline__ void load_row(F2 (&p)[PPT], const void* q, size_t at, int run, int H, bool vec) {
+__device__ __forceinline__ void load_row(F2 (&p)[PPT], const void* q, size_t at, int run, int H, const Own& me) {
   float v[EPT];
-  load_row<T, A>(v, q, at, run, H, vec);
+  load_row<T, A>(v, q, at, run, H, me);
   pairs_of(p, v);
 }
 template <typename T, Access A>
-__device__ __forceinline__ void store_row(void* q, size_t at, int run, int H, bool vec, const F2 (&p)[PPT]) {
+__device__ __forceinline__ void store_row(void* q, size_t at, int run, int H, const Own& me, const F2 (&p)[PPT]) {
   float v[EPT];
   values_of(v, p);
-  store_row<T, A>(q, at, run, H, vec, v);
+  store_row<T, A>(q, at, run, H, me, v);
 }
 // v = 0 for columns past H (after a mean was taken off).
 template <Access A>
-__device__ __forceinline__ void clear_past(F2 (&p)[PPT], int run, int H, bool vec) {
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    if (col_of<A>(run, 0, vec) >= H)
+__device__ __forceinline__ void clear_past(F2 (&p)[PPT], int run, int H, const Own& me) {
+  if (in_runs<A>(me)) {
+    if (col_of<A>(run, 0, me) >= H)
 #pragma unroll
       for (int i = 0; i < PPT; ++i) p[i] = f2(0.0f);
   } else {
@@ -299,7 +314,7 @@ __device__ __forceinline__ void clear_past(F2 (&p)[PPT], int run, int H, bool ve
     values_of(v, p);
 #pragma unroll
     for (int i = 0; i < EPT; ++i)
-      if (col_of<A>(run, i, vec) >= H) v[i] = 0.0f;
+      if (col_of<A>(run, i, me) >= H) v[i] = 0.0f;
     pairs_of(p, v);
   }
 }
@@ -351,6 +366,38 @@ struct BlockSum {
   }
 };
 
+// The same over the `nt` lanes (a power of two, at least 4) of a row's group.
+template <int N>
+struct GroupSum {
+  int nt;
+  __device__ __forceinline__ void operator()(float (&v)[N]) const {
+    if constexpr (N == 4) {
+      const bool hi = threadIdx.x & (nt >> 1), mid = threadIdx.x & (nt >> 2);
+      float a0 = hi ? v[2] : v[0], a1 = hi ? v[3] : v[1];
+      a0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], nt >> 1);
+      a1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], nt >> 1);
+      float b = mid ? a1 : a0;
+      b += __shfl_xor_sync(0xffffffffu, mid ? a0 : a1, nt >> 2);
+      for (int o = nt >> 3; o > 0; o >>= 1) b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __shfl_sync(0xffffffffu, b, j * (nt >> 2), nt);
+    } else {
+      for (int o = nt >> 1; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+};
+
+template <bool SMALL, int N, int MAXT>
+struct SumOf {
+  using type = BlockSum<N, MAXT>;
+  static __device__ __forceinline__ type make(float (*buf)[N][type::W], int) { return type{buf, 0}; }
+};
+template <int N, int MAXT>
+struct SumOf<true, N, MAXT> {
+  using type = GroupSum<N>;
+  static __device__ __forceinline__ type make(float (*)[N][BlockSum<N, MAXT>::W], int lanes) { return type{lanes}; }
+};
+
 // 1 / sqrt of the second moment, whose sum over H columns is given, plus eps.  rsqrtf
 // is within 2 ulp, a tenth of the instructions of a square root and a division.
 __device__ __forceinline__ float inv_std(float sum, float inv_h, float eps) { return rsqrtf(sum * inv_h + eps); }
@@ -359,6 +406,18 @@ __device__ __forceinline__ float inv_std(float sum, float inv_h, float eps) { re
 inline int norm_threads(int H) {
   const int t = (H + EPT * RUNS - 1) / (EPT * RUNS);
   return (t + 31) / 32 * 32;
+}
+inline bool takes_small(const NormArgs& a) { return a.vec ? a.H <= SMALL_H : a.H <= SMALL_H / 2 && a.T > 8 * 152; }
+// The same for SMALL: lanes per row, and threads of a block, fewer where that leaves SMs idle.
+inline int norm_lanes(int H) {
+  int n = 4;
+  while (n * EPT * RUNS < H) n *= 2;
+  return n;
+}
+inline int small_threads(int T, int lanes) {
+  int n = 128;
+  while (n > 32 && static_cast<long long>(T) * lanes < 152ll * n) n /= 2;
+  return n;
 }
 inline size_t norm_pitch(int H) { return static_cast<size_t>(H + EPT - 1) / EPT * EPT; }
 // Elements of a row or vector in shared memory.

@@ -18,11 +18,11 @@ namespace {
 
 // A block's column sums, one vector of `pitch` floats each.
 template <Access A>
-__device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec, const F2 (&p2)[PPT]) {
+__device__ __forceinline__ void add_columns(float* acc, int run, int H, const Own& me, const F2 (&p2)[PPT]) {
   float v[EPT];
   values_of(v, p2);
-  if (A == VEC16 || (A == PLAIN && vec)) {
-    const int c = col_of<A>(run, 0, vec);
+  if (in_runs<A>(me)) {
+    const int c = col_of<A>(run, 0, me);
     if (c >= H) return;
     float4* p = reinterpret_cast<float4*>(acc + c);
     float4 x = p[0], y = p[1];
@@ -33,7 +33,7 @@ __device__ __forceinline__ void add_columns(float* acc, int run, int H, bool vec
   } else {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<A>(run, i, vec);
+      const int c = col_of<A>(run, i, me);
       if (c < H) acc[c] += v[i];
     }
   }
@@ -53,95 +53,106 @@ constexpr int min_blocks(int maxt, bool general) {
   return maxt <= 128 ? (general ? 3 : 4) : maxt <= 256 && !general ? 2 : 1;
 }
 
-template <typename HT, typename OT, Access A, int MAXT, bool GENERAL>
+template <typename HT, typename OT, Access A, int MAXT, bool GENERAL, bool SMALL>
 __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward_kernel(NormArgs a) {
   constexpr bool RING = A != PLAIN;
   constexpr bool HOLD = MAXT <= 512;  // column sums in registers, factors in shared memory
-  using Sum = BlockSum<4, MAXT>;
-  __shared__ __align__(16) float s_sum[2][4][Sum::W];
+  using Whole = BlockSum<4, MAXT>;
+  __shared__ __align__(16) float s_sum[2][4][Whole::W];
   extern __shared__ __align__(16) uint8_t s_mem[];
   const int H = a.H;
-  const bool vec = A == VEC16 || (A == PLAIN && a.vec);
+  const Own me = SMALL ? Own{static_cast<int>(threadIdx.x) & (a.lanes - 1), a.lanes, a.lanes, a.vec}
+                       : Own{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 32, a.vec};
+  const unsigned rows = SMALL ? blockDim.x / a.lanes : 1, mine = SMALL ? threadIdx.x / a.lanes : 0;
+  const unsigned stride = gridDim.x * rows;
   const float inv_h = 1.0f / static_cast<float>(H);
-  const int pitch = slot_pitch(blockDim.x), sums_pitch = (H + EPT - 1) / EPT * EPT;
+  const int pitch = slot_pitch(blockDim.x), row_pitch = slot_pitch(me.nt), sums_pitch = (H + EPT - 1) / EPT * EPT;
   const bool pre = a.pre != MOE_NORM_NONE, post = a.post != MOE_NORM_NONE;
   const bool layer_pre = a.pre == MOE_NORM_LAYER, layer_post = a.post == MOE_NORM_LAYER;
   const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
   const bool gate_t = a.gate_kind == MOE_GATE_TOKEN;
   // ring slots: o | dh' | h' | dx', then the factors of the post and of the pre norm; rows
   // of over 8192 columns: the column sums (in the workspace itself where they do not fit)
-  const int rows = a.depth * pitch;
+  const int ring = a.depth * pitch, my_row = mine * row_pitch;
   OT* ring_o = reinterpret_cast<OT*>(s_mem);
-  HT* ring_g = reinterpret_cast<HT*>(ring_o + rows);
-  HT* ring_h = ring_g + (a.dh_out ? rows : 0);
-  OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? rows : 0));
-  float* s_post = reinterpret_cast<float*>(ring_x + (pre ? rows : 0));
-  float* s_pre = s_post + pitch;
-  float* s_bias = s_pre + pitch;  // post norm's bias, for the gradient of a gate per token or value
+  HT* ring_g = reinterpret_cast<HT*>(ring_o + ring);
+  HT* ring_h = ring_g + (a.dh_out ? ring : 0);
+  OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? ring : 0));
+  float* s_post = reinterpret_cast<float*>(ring_x + (pre ? ring : 0));
+  ring_o += my_row;
+  ring_g += my_row;
+  ring_h += my_row;
+  ring_x += my_row;
+  float* s_pre = s_post + row_pitch;
+  float* s_bias = s_pre + row_pitch;  // post norm's bias, for the gradient of a gate per token or value
   float* part = a.partials + static_cast<size_t>(blockIdx.x) * a.nacc * sums_pitch;
   float* acc = a.acc_in_smem ? reinterpret_cast<float*>(s_mem) : part;
 
-  for (int i = threadIdx.x; i < 8 * Sum::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
-  __syncthreads();
-  Sum block_sum{s_sum, 0};
+  if (!SMALL) {
+    for (int i = threadIdx.x; i < 8 * Whole::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+    __syncthreads();
+  }
+  typename SumOf<SMALL, 4, MAXT>::type row_sum = SumOf<SMALL, 4, MAXT>::make(s_sum, a.lanes);
   dep_wait();
   dep_launch();
 
   if (RING)
     for (int d = 0; d < a.depth; ++d) {
-      clear_slot<OT, A>(ring_o + d * pitch, H);
-      if (a.dh_out) clear_slot<HT, A>(ring_g + d * pitch, H);
+      clear_slot<OT, A>(ring_o + d * pitch, H, me);
+      if (a.dh_out) clear_slot<HT, A>(ring_g + d * pitch, H, me);
       if (pre) {
-        clear_slot<HT, A>(ring_h + d * pitch, H);
-        clear_slot<OT, A>(ring_x + d * pitch, H);
+        clear_slot<HT, A>(ring_h + d * pitch, H, me);
+        clear_slot<OT, A>(ring_x + d * pitch, H, me);
       }
     }
-  auto fetch = [&](int t, int slot) {
-    if (t < a.T) {
+  const unsigned T = a.T;  // t may pass 2^31 by the rows ahead
+  auto fetch = [&](unsigned t, int slot) {
+    if (t < T) {
       const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
       if (pre) {
-        copy_in<HT, A>(ring_h + slot * pitch, a.h, at_h, H);
-        copy_in<OT, A>(ring_x + slot * pitch, a.dx_out, at_o, H);
+        copy_in<HT, A>(ring_h + slot * pitch, a.h, at_h, H, me);
+        copy_in<OT, A>(ring_x + slot * pitch, a.dx_out, at_o, H, me);
       }
-      copy_in<OT, A>(ring_o + slot * pitch, a.o, at_o, H);
-      if (a.dh_out) copy_in<HT, A>(ring_g + slot * pitch, a.dh_out, at_h, H);
+      copy_in<OT, A>(ring_o + slot * pitch, a.o, at_o, H, me);
+      if (a.dh_out) copy_in<HT, A>(ring_g + slot * pitch, a.dh_out, at_h, H, me);
     }
     cp_async_commit();
   };
   int slot = 0;
   if (RING)
-    for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
+    for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x * rows + mine + d * stride, d);
 
   // factors of dn: the pre norm's weight; the post norm's, with a per-column gate
   auto post_factor = [&](float(&f)[EPT], int r) {
-    load_columns<A>(f, a.w_post, a.w_dtype, r, H, vec, 1.0f);
+    load_columns<A>(f, a.w_post, a.w_dtype, r, H, me, 1.0f);
     if (gate_c) {
       float g[EPT];
-      load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
+      load_columns<A>(g, a.gate, a.w_dtype, r, H, me, 0.0f);
 #pragma unroll
       for (int i = 0; i < EPT; ++i) f[i] *= g[i];
     }
   };
-  if (HOLD)
+  if (HOLD && mine == 0)
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
       post_factor(f, r);
-      put_shared<A>(s_post, r, vec, f);
-      load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-      put_shared<A>(s_pre, r, vec, f);
+      put_shared<A>(s_post, r, me, f);
+      load_columns<A>(f, a.w_pre, a.w_dtype, r, H, me, 1.0f);
+      put_shared<A>(s_pre, r, me, f);
       if (bias_in_smem(a)) {
-        load_columns<A>(f, a.b_post, a.w_dtype, r, H, vec, 0.0f);
-        put_shared<A>(s_bias, r, vec, f);
+        load_columns<A>(f, a.b_post, a.w_dtype, r, H, me, 0.0f);
+        put_shared<A>(s_bias, r, me, f);
       }
     }
+  if (SMALL) __syncthreads();
   auto factor = [&](F2(&f)[PPT], bool of_post, int r) {
     if constexpr (HOLD) {
-      copy_out<float, A>(f, of_post ? s_post : s_pre, r, vec);
+      copy_out<float, A>(f, of_post ? s_post : s_pre, r, me);
     } else {
       float v[EPT];
       if (of_post) post_factor(v, r);
-      else load_columns<A>(v, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+      else load_columns<A>(v, a.w_pre, a.w_dtype, r, H, me, 1.0f);
       pairs_of(f, v);
     }
   };
@@ -156,33 +167,40 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
       for (int r = 0; r < RUNS; ++r)
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-          const int c = col_of<A>(r, i, vec);
+          const int c = col_of<A>(r, i, me);
           if (c < H) acc[j * sums_pitch + c] = 0.0f;
         }
 
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (unsigned t0 = blockIdx.x * rows; t0 < T; t0 += stride) {
+    // a group past the last row takes part in the shuffles, with a row of zeros and no columns
+    const unsigned t = t0 + mine;
+    const bool live = !SMALL || t < T;
+    const int H = live ? a.H : 0;
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
     if (RING) {
       const int ahead = slot + a.depth - 1;
-      fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
+      fetch(t + (a.depth - 1) * stride, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
     }
     F2 hc[RUNS][PPT], oc[RUNS][PPT], dx[RUNS][PPT], G[RUNS][PPT];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r);
-      else load_row<OT, A>(oc[r], a.o, at_o, r, H, vec);
+      if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r, me);
+      else load_row<OT, A>(oc[r], a.o, at_o, r, H, me);
       if (pre) {
         if constexpr (RING) {
-          copy_out<HT, A>(hc[r], ring_h + slot * pitch, r);
-          copy_out<OT, A>(dx[r], ring_x + slot * pitch, r);
+          copy_out<HT, A>(hc[r], ring_h + slot * pitch, r, me);
+          copy_out<OT, A>(dx[r], ring_x + slot * pitch, r, me);
         } else {
-          load_row<HT, A>(hc[r], a.h, at_h, r, H, vec);
-          load_row<OT, A>(dx[r], a.dx_out, at_o, r, H, vec);
+          load_row<HT, A>(hc[r], a.h, at_h, r, H, me);
+          load_row<OT, A>(dx[r], a.dx_out, at_o, r, H, me);
         }
       }
       if constexpr (!RING)
-        if (a.dh_out) load_row<HT, A>(G[r], a.dh_out, at_h, r, H, vec);
+        if (a.dh_out) load_row<HT, A>(G[r], a.dh_out, at_h, r, H, me);
+      if (SMALL && !live)
+#pragma unroll
+        for (int i = 0; i < PPT; ++i) hc[r][i] = oc[r][i] = dx[r][i] = f2(0.0f);
     }
     if (GENERAL && (layer_pre || layer_post)) {
       F2 sh = f2(0.0f), so = f2(0.0f);
@@ -194,19 +212,19 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
           so = so + oc[r][i];
         }
       float s[4] = {halves_sum(sh), halves_sum(so), 0.0f, 0.0f};
-      block_sum(s);
+      row_sum(s);
       const F2 mh = f2(-s[0] * inv_h), mo = f2(-s[1] * inv_h);
 #pragma unroll
       for (int r = 0; r < RUNS; ++r) {
         if (layer_pre) {
 #pragma unroll
           for (int i = 0; i < PPT; ++i) hc[r][i] = hc[r][i] + mh;
-          clear_past<A>(hc[r], r, H, vec);
+          clear_past<A>(hc[r], r, H, me);
         }
         if (layer_post) {
 #pragma unroll
           for (int i = 0; i < PPT; ++i) oc[r][i] = oc[r][i] + mo;
-          clear_past<A>(oc[r], r, H, vec);
+          clear_past<A>(oc[r], r, H, me);
         }
       }
     }
@@ -231,9 +249,9 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
         for (int i = 0; i < PPT; ++i) q3 = fma2(oc[r][i], oc[r][i], q3);
       }
       float s[4] = {halves_sum(q0), halves_sum(q1), GENERAL ? halves_sum(q2) : 0.0f, halves_sum(q3)};
-      block_sum(s);
-      if (post) ro = inv_std(s[3], inv_h, a.eps);
-      if (pre) {
+      row_sum(s);
+      if (post && live) ro = inv_std(s[3], inv_h, a.eps);
+      if (pre && live) {
         rs = inv_std(s[0], inv_h, a.eps);
         m1 = s[1] * rs * inv_h;                 // mean(dx w u)
         m0 = layer_pre ? s[2] * inv_h : 0.0f;   // mean(dx w)
@@ -241,11 +259,11 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
     }
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if (!a.dh_out) {
+      if (!a.dh_out || !live) {
 #pragma unroll
         for (int i = 0; i < PPT; ++i) G[r][i] = f2(0.0f);
       } else if constexpr (RING) {
-        copy_out<HT, A>(G[r], ring_g + slot * pitch, r);
+        copy_out<HT, A>(G[r], ring_g + slot * pitch, r, me);
       }
       if (pre) {
         F2 f[PPT];
@@ -258,7 +276,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
           G[r][i] = fma2(f2(rs), fma2(u, f2(-m1), d), G[r][i]);
           hc[r][i] = u;
         }
-        if (GENERAL) clear_past<A>(G[r], r, H, vec);
+        if (GENERAL) clear_past<A>(G[r], r, H, me);
         if (HOLD) {
 #pragma unroll
           for (int i = 0; i < PPT; ++i) pre1[r][i] = fma2(dx[r][i], hc[r][i], pre1[r][i]);
@@ -266,11 +284,11 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 #pragma unroll
             for (int i = 0; i < PPT; ++i) pre0[r][i] = pre0[r][i] + dx[r][i];
         } else {
-          if (a.acc_pre0 >= 0) add_columns<A>(acc + a.acc_pre0 * sums_pitch, r, H, vec, dx[r]);
+          if (a.acc_pre0 >= 0) add_columns<A>(acc + a.acc_pre0 * sums_pitch, r, H, me, dx[r]);
           if (a.acc_pre1 >= 0) {
 #pragma unroll
             for (int i = 0; i < PPT; ++i) dx[r][i] = dx[r][i] * hc[r][i];
-            add_columns<A>(acc + a.acc_pre1 * sums_pitch, r, H, vec, dx[r]);
+            add_columns<A>(acc + a.acc_pre1 * sums_pitch, r, H, me, dx[r]);
           }
         }
       }
@@ -278,11 +296,11 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
         F2 d[PPT];
 #pragma unroll
         for (int i = 0; i < PPT; ++i) d[i] = f2(a.beta) * G[r][i];
-        store_row<HT, A>(a.dh, at_h, r, H, vec, d);
+        store_row<HT, A>(a.dh, at_h, r, H, me, d);
       }
     }
     // the block's side: alpha G is the gradient of g N(o); G becomes dn w
-    const float gt = gate_t ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
+    const float gt = gate_t && live ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
     F2 d0 = f2(0.0f), d1 = d0, d2 = d0;
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
@@ -299,10 +317,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
         for (int i = 0; i < PPT; ++i) w[i] = w[i] * oc[r][i];
         if (a.b_post) {
           if constexpr (HOLD) {
-            copy_out<float, A>(c, s_bias, r, vec);
+            copy_out<float, A>(c, s_bias, r, me);
           } else {
             float v[EPT];
-            load_columns<A>(v, a.b_post, a.w_dtype, r, H, vec, 0.0f);
+            load_columns<A>(v, a.b_post, a.w_dtype, r, H, me, 0.0f);
             pairs_of(c, v);
           }
 #pragma unroll
@@ -313,10 +331,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
           c[i] = G[r][i] * w[i];
           d2 = d2 + c[i];
         }
-        if (gate_f) store_row<OT, A>(a.dgate, at_o, r, H, vec, c);
+        if (gate_f) store_row<OT, A>(a.dgate, at_o, r, H, me, c);
       }
       if (GENERAL && gate_f) {
-        load_row<OT, A>(c, a.gate, at_o, r, H, vec);
+        load_row<OT, A>(c, a.gate, at_o, r, H, me);
 #pragma unroll
         for (int i = 0; i < PPT; ++i) G[r][i] = G[r][i] * c[i];
       } else if (GENERAL && gate_t) {
@@ -330,11 +348,11 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 #pragma unroll
           for (int i = 0; i < PPT; ++i) post0[r][i] = post0[r][i] + G[r][i];
       } else {
-        if (a.acc_post0 >= 0) add_columns<A>(acc + a.acc_post0 * sums_pitch, r, H, vec, G[r]);
+        if (a.acc_post0 >= 0) add_columns<A>(acc + a.acc_post0 * sums_pitch, r, H, me, G[r]);
         if (a.acc_post1 >= 0) {
 #pragma unroll
           for (int i = 0; i < PPT; ++i) c[i] = G[r][i] * oc[r][i];
-          add_columns<A>(acc + a.acc_post1 * sums_pitch, r, H, vec, c);
+          add_columns<A>(acc + a.acc_post1 * sums_pitch, r, H, me, c);
         }
       }
       factor(c, true, r);
@@ -347,8 +365,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
     }
     const bool token_sum = GENERAL && a.dgate && gate_t;
     float d[4] = {halves_sum(d0), GENERAL ? halves_sum(d1) : 0.0f, GENERAL ? halves_sum(d2) : 0.0f, 0.0f};
-    if (post || token_sum) block_sum(d);
-    if (token_sum && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = d[2];
+    if (post || token_sum) row_sum(d);
+    if (token_sum && live && me.tid == 0) static_cast<float*>(a.dgate)[t] = d[2];
     if (a.d_o) {
       const F2 n1 = f2(-d[0] * inv_h), n0 = f2(layer_post ? -d[1] * inv_h : 0.0f);
 #pragma unroll
@@ -361,19 +379,46 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
             G[r][i] = f2(ro) * v;
           }
         }
-        store_row<OT, A>(a.d_o, at_o, r, H, vec, G[r]);
+        store_row<OT, A>(a.d_o, at_o, r, H, me, G[r]);
       }
     }
     if (++slot >= a.depth) slot = 0;
   }
-  // each thread hands over the columns that it summed
+  // each thread hands over the columns that it summed; groups of lanes add theirs up first
   if (HOLD) {
+    const bool join = SMALL && rows > 1;
+    float* all = reinterpret_cast<float*>(s_mem);
+    if (join) {
+      cp_async_wait(1);
+      __syncthreads();  // all have read their last rows and factors
+    }
+    auto hand_over = [&](int j, F2(&sum)[RUNS][PPT]) {
+      if (j < 0) return;
 #pragma unroll
-    for (int r = 0; r < RUNS; ++r) {
-      if (a.acc_post1 >= 0) store_row<float, A>(part + a.acc_post1 * sums_pitch, 0, r, H, vec, post1[r]);
-      if (a.acc_post0 >= 0) store_row<float, A>(part + a.acc_post0 * sums_pitch, 0, r, H, vec, post0[r]);
-      if (a.acc_pre1 >= 0) store_row<float, A>(part + a.acc_pre1 * sums_pitch, 0, r, H, vec, pre1[r]);
-      if (a.acc_pre0 >= 0) store_row<float, A>(part + a.acc_pre0 * sums_pitch, 0, r, H, vec, pre0[r]);
+      for (int r = 0; r < RUNS; ++r) {
+        float v[EPT];
+        values_of(v, sum[r]);
+        if (join) put_shared<A>(all + j * pitch + my_row, r, me, v);
+        else store_row<float, A>(part + j * sums_pitch, 0, r, H, me, v);
+      }
+    };
+    hand_over(a.acc_post1, post1);
+    hand_over(a.acc_post0, post0);
+    hand_over(a.acc_pre1, pre1);
+    hand_over(a.acc_pre0, pre0);
+    if (join) {
+      __syncthreads();
+      const int quads = sums_pitch / 4;
+      for (int i = threadIdx.x; i < a.nacc * quads; i += blockDim.x) {
+        const int j = i / quads, c = (i - j * quads) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (unsigned q = 0; q < rows; ++q) {
+          const float4 x = *reinterpret_cast<const float4*>(all + j * pitch + q * row_pitch + c);
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        *reinterpret_cast<float4*>(part + j * sums_pitch + c) = v;
+      }
     }
   } else if (a.acc_in_smem) {
     for (int j = 0; j < a.nacc; ++j)
@@ -381,7 +426,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
       for (int r = 0; r < RUNS; ++r)
 #pragma unroll
         for (int i = 0; i < EPT; ++i) {
-          const int c = col_of<A>(r, i, vec);
+          const int c = col_of<A>(r, i, me);
           if (c < H) part[j * sums_pitch + c] = acc[j * sums_pitch + c];
         }
   }
@@ -467,10 +512,10 @@ inline int most_blocks_per_sm(int H) {
 constexpr size_t kSmemMax = 224 * 1024;  // of one block's dynamic shared memory
 constexpr size_t kSmemSm = 228 * 1024;   // of an SM; a block takes 1 KB of its own and 1 KB static
 
-template <typename HT, typename OT, Access A, int MAXT, bool GENERAL>
+template <typename HT, typename OT, Access A, int MAXT, bool GENERAL, bool SMALL = false>
 cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
   static const cudaError_t attr =
-      cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, MAXT, GENERAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaFuncSetAttribute(norm_backward_kernel<HT, OT, A, MAXT, GENERAL, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmemMax));
   if (attr != cudaSuccess) return attr;
   const size_t pitch = slot_pitch(threads);
@@ -480,7 +525,7 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
   a.depth = 0;
   auto fits = [&](size_t bytes, int blocks) { return bytes <= kSmemMax && (bytes + 2048) * blocks <= kSmemSm; };
   if (MAXT <= 512) {
-    const size_t factors = (bias_in_smem(a) ? 3 : 2) * pitch * sizeof(float);
+    const size_t factors = (bias_in_smem(a) ? 3 : 2) * slot_pitch(SMALL ? a.lanes : threads) * sizeof(float);
     if (A != PLAIN) {
       // a row that is worked on and, where they fit with the resident blocks, one or two
       // on their way; 128 KB at most for one row, beside 96 KB of factors
@@ -490,23 +535,35 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
       smem = a.depth * row;
     }
     smem += factors;
+    const size_t sums = a.nacc * pitch * sizeof(float);  // of the groups
+    if (SMALL && smem < sums) smem = sums;
   } else {
     smem = a.nacc * norm_pitch(a.H) * sizeof(float);
     a.acc_in_smem = smem <= kSmemMax;  // else the sums are kept in the workspace itself
     if (!a.acc_in_smem) smem = 0;
   }
   while (per_sm > 1 && !fits(smem, per_sm)) --per_sm;
-  a.blocks = a.T < 152 * per_sm ? a.T : 152 * per_sm;
-  return launch_dependent(norm_backward_kernel<HT, OT, A, MAXT, GENERAL>, dim3(a.blocks), dim3(threads), smem, s, a);
+  const int all = (a.T - 1) / (SMALL ? threads / a.lanes : 1) + 1;
+  a.blocks = all < 152 * per_sm ? all : 152 * per_sm;
+  return launch_dependent(norm_backward_kernel<HT, OT, A, MAXT, GENERAL, SMALL>, dim3(a.blocks), dim3(threads), smem, s, a);
 }
 
 template <typename HT, typename OT>
 cudaError_t backward_types(NormArgs& a, cudaStream_t s) {
   const int threads = norm_threads(a.H);
   if (threads > 512) return backward_of<HT, OT, PLAIN, 1024, true>(a, threads, s);
+  const bool general = a.acc_post0 >= 0 || a.acc_pre0 >= 0 || a.post == MOE_NORM_LAYER || a.pre == MOE_NORM_LAYER ||
+                       a.gate_kind == MOE_GATE_TOKEN || a.gate_kind == MOE_GATE_FULL;
+  if (takes_small(a)) {
+    // few rows: one per warp, so that no block has rows' sums to join (300 x 256: 6.8 -> 6.1 us)
+    a.lanes = a.T <= 2 * 152 ? 32 : norm_lanes(a.H);
+    const int block = small_threads(a.T, a.lanes);
+    if (!a.vec) return backward_of<HT, OT, PLAIN, 128, true, true>(a, block, s);
+    return general ? backward_of<HT, OT, VEC16, 128, true, true>(a, block, s)
+                   : backward_of<HT, OT, VEC16, 128, false, true>(a, block, s);
+  }
   if (a.vec) {
-    if (a.acc_post0 >= 0 || a.acc_pre0 >= 0 || a.post == MOE_NORM_LAYER || a.pre == MOE_NORM_LAYER ||
-        a.gate_kind == MOE_GATE_TOKEN || a.gate_kind == MOE_GATE_FULL) {
+    if (general) {
       if (threads <= 128) return backward_of<HT, OT, VEC16, 128, true>(a, threads, s);
       if (threads <= 256) return backward_of<HT, OT, VEC16, 256, true>(a, threads, s);
       return backward_of<HT, OT, VEC16, 512, true>(a, threads, s);

@@ -12,95 +12,108 @@ namespace moe {
 namespace norms {
 namespace {
 
-// Blocks per SM: 64 registers for up to 8192 columns.
-constexpr int min_blocks(int maxt) { return maxt <= 512 ? 1024 / maxt : 1; }
+// Blocks per SM: 64 registers for up to 8192 columns (80 for short odd rows, whose loads are
+// held in registers).
+constexpr int min_blocks(int maxt, bool odd_small) { return odd_small ? 768 / maxt : maxt <= 512 ? 1024 / maxt : 1; }
 
-template <typename HT, typename OT, Access A, int MAXT>
-__global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(NormArgs a) {
+template <typename HT, typename OT, Access A, int MAXT, bool SMALL>
+__global__ void __launch_bounds__(MAXT, min_blocks(MAXT, SMALL && A == PLAIN)) norm_forward_kernel(NormArgs a) {
   constexpr bool RING = A != PLAIN;
   constexpr bool HOLD = MAXT <= 512;  // factors and biases in shared memory
-  using Sum = BlockSum<1, MAXT>;
-  __shared__ __align__(16) float s_sum[2][1][Sum::W];
+  using Whole = BlockSum<1, MAXT>;
+  __shared__ __align__(16) float s_sum[2][1][Whole::W];
   extern __shared__ __align__(16) uint8_t s_ring[];
   const int H = a.H;
-  const bool vec = A == VEC16 || (A == PLAIN && a.vec);
+  const Own me = SMALL ? Own{static_cast<int>(threadIdx.x) & (a.lanes - 1), a.lanes, a.lanes, a.vec}
+                       : Own{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 32, a.vec};
+  const unsigned rows = SMALL ? blockDim.x / a.lanes : 1, mine = SMALL ? threadIdx.x / a.lanes : 0;
+  const unsigned stride = gridDim.x * rows;
   const float inv_h = 1.0f / static_cast<float>(H);
-  const int pitch = slot_pitch(blockDim.x);
+  const int pitch = slot_pitch(blockDim.x), row_pitch = slot_pitch(me.nt);
   // ring | factors of the post and of the pre norm, then their biases where there are any;
   // each column with its thread
   HT* ring_h = reinterpret_cast<HT*>(s_ring);
   OT* ring_o = reinterpret_cast<OT*>(ring_h + a.depth * pitch);  // depth 0 without a ring
   float* s_post = reinterpret_cast<float*>(ring_o + a.depth * pitch);
-  float* s_pre = s_post + pitch;
-  float* s_bpost = s_pre + pitch;
-  float* s_bpre = s_bpost + (a.b_post ? pitch : 0);
-  for (int i = threadIdx.x; i < 2 * Sum::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
-  __syncthreads();
-  Sum block_sum{s_sum, 0};
+  float* s_pre = s_post + row_pitch;
+  float* s_bpost = s_pre + row_pitch;
+  float* s_bpre = s_bpost + (a.b_post ? row_pitch : 0);
+  ring_h += mine * row_pitch;
+  ring_o += mine * row_pitch;
+  if (!SMALL) {
+    for (int i = threadIdx.x; i < 2 * Whole::W; i += blockDim.x) (&s_sum[0][0][0])[i] = 0.0f;
+    __syncthreads();
+  }
+  typename SumOf<SMALL, 1, MAXT>::type row_sum = SumOf<SMALL, 1, MAXT>::make(s_sum, a.lanes);
   dep_wait();
   dep_launch();
 
   if (RING)
     for (int d = 0; d < a.depth; ++d) {
-      clear_slot<HT, A>(ring_h + d * pitch, H);
-      clear_slot<OT, A>(ring_o + d * pitch, H);
+      clear_slot<HT, A>(ring_h + d * pitch, H, me);
+      clear_slot<OT, A>(ring_o + d * pitch, H, me);
     }
-  auto fetch = [&](int t, int slot) {
-    if (t < a.T) {
-      copy_in<OT, A>(ring_o + slot * pitch, a.o, static_cast<size_t>(t) * a.ld_o, H);
-      copy_in<HT, A>(ring_h + slot * pitch, a.h, static_cast<size_t>(t) * a.ld_h, H);
+  const unsigned T = a.T;  // t may pass 2^31 by the rows ahead
+  auto fetch = [&](unsigned t, int slot) {
+    if (t < T) {
+      copy_in<OT, A>(ring_o + slot * pitch, a.o, static_cast<size_t>(t) * a.ld_o, H, me);
+      copy_in<HT, A>(ring_h + slot * pitch, a.h, static_cast<size_t>(t) * a.ld_h, H, me);
     }
     cp_async_commit();
   };
   int slot = 0;
   if (RING)
-    for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x + d * gridDim.x, d);
+    for (int d = 0; d + 1 < a.depth; ++d) fetch(blockIdx.x * rows + mine + d * stride, d);
 
   // factor of the normalised (or plain) o, and of the normalised h'
   const bool gate_c = a.gate_kind == MOE_GATE_CHANNEL, gate_f = a.gate_kind == MOE_GATE_FULL;
   auto post_column = [&](float(&f)[EPT], const void* v, float none, int r) {
-    load_columns<A>(f, v, a.w_dtype, r, H, vec, none);
+    load_columns<A>(f, v, a.w_dtype, r, H, me, none);
     if (gate_c) {
       float g[EPT];
-      load_columns<A>(g, a.gate, a.w_dtype, r, H, vec, 0.0f);
+      load_columns<A>(g, a.gate, a.w_dtype, r, H, me, 0.0f);
 #pragma unroll
       for (int i = 0; i < EPT; ++i) f[i] *= g[i];
     }
   };
-  if (HOLD)
+  if (HOLD && mine == 0)
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       float f[EPT];
       post_column(f, a.w_post, 1.0f, r);
-      put_shared<A>(s_post, r, vec, f);
-      load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
-      put_shared<A>(s_pre, r, vec, f);
+      put_shared<A>(s_post, r, me, f);
+      load_columns<A>(f, a.w_pre, a.w_dtype, r, H, me, 1.0f);
+      put_shared<A>(s_pre, r, me, f);
       if (a.b_post) {
         post_column(f, a.b_post, 0.0f, r);
-        put_shared<A>(s_bpost, r, vec, f);
+        put_shared<A>(s_bpost, r, me, f);
       }
       if (a.b_pre) {
-        load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
-        put_shared<A>(s_bpre, r, vec, f);
+        load_columns<A>(f, a.b_pre, a.w_dtype, r, H, me, 0.0f);
+        put_shared<A>(s_bpre, r, me, f);
       }
     }
+  if (SMALL) __syncthreads();
 
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (unsigned t0 = blockIdx.x * rows; t0 < T; t0 += stride) {
+    // a group past the last row takes part in the shuffles, with a row of no columns
+    const unsigned t = t0 + mine;
+    const int H = SMALL && t >= T ? 0 : a.H;
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
     F2 v[RUNS][PPT];
     if (RING) {
       const int ahead = slot + a.depth - 1;
-      fetch(t + (a.depth - 1) * gridDim.x, ahead >= a.depth ? ahead - a.depth : ahead);
+      fetch(t + (a.depth - 1) * stride, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
     }
     F2 hv[RUNS][PPT];  // without a ring: h's loads go out with o's
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       if constexpr (RING) {
-        copy_out<OT, A>(v[r], ring_o + slot * pitch, r);
+        copy_out<OT, A>(v[r], ring_o + slot * pitch, r, me);
       } else {
-        load_row<OT, A>(v[r], a.o, at_o, r, H, vec);
-        load_row<HT, A>(hv[r], a.h, at_h, r, H, vec);
+        load_row<OT, A>(v[r], a.o, at_o, r, H, me);
+        load_row<HT, A>(hv[r], a.h, at_h, r, H, me);
       }
     }
 
@@ -113,13 +126,13 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
           for (int i = 0; i < PPT; ++i) s = s + v[r][i];
         float sum[1] = {halves_sum(s)};
-        block_sum(sum);
+        row_sum(sum);
         const F2 mu = f2(-sum[0] * inv_h);
 #pragma unroll
         for (int r = 0; r < RUNS; ++r) {
 #pragma unroll
           for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] + mu;
-          clear_past<A>(v[r], r, H, vec);
+          clear_past<A>(v[r], r, H, me);
         }
       }
       F2 q = f2(0.0f);
@@ -128,19 +141,19 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
 #pragma unroll
         for (int i = 0; i < PPT; ++i) q = fma2(v[r][i], v[r][i], q);
       float sum[1] = {halves_sum(q)};
-      block_sum(sum);
+      row_sum(sum);
       return inv_std(sum[0], inv_h, a.eps);
     };
 
     float scale = a.alpha;
-    if (a.gate_kind == MOE_GATE_TOKEN) scale *= __ldg(static_cast<const float*>(a.gate) + t);
+    if (a.gate_kind == MOE_GATE_TOKEN && (!SMALL || t < T)) scale *= __ldg(static_cast<const float*>(a.gate) + t);
     const F2 rs = f2(a.post != MOE_NORM_NONE ? scale * moments(a.post) : scale), beta = f2(a.beta);
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
       F2 c[PPT];
       float f[EPT];
       if constexpr (HOLD) {
-        copy_out<float, A>(c, s_post, r, vec);
+        copy_out<float, A>(c, s_post, r, me);
       } else {
         post_column(f, a.w_post, 1.0f, r);
         pairs_of(c, f);
@@ -149,7 +162,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
       for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rs * c[i]);
       if (a.b_post) {
         if constexpr (HOLD) {
-          copy_out<float, A>(c, s_bpost, r, vec);
+          copy_out<float, A>(c, s_bpost, r, me);
         } else {
           post_column(f, a.b_post, 0.0f, r);
           pairs_of(c, f);
@@ -158,14 +171,14 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
         for (int i = 0; i < PPT; ++i) v[r][i] = fma2(f2(scale), c[i], v[r][i]);
       }
       if (gate_f) {
-        load_row<OT, A>(c, a.gate, at_o, r, H, vec);
+        load_row<OT, A>(c, a.gate, at_o, r, H, me);
 #pragma unroll
         for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * c[i];
       }
-      if constexpr (RING) copy_out<HT, A>(hv[r], ring_h + slot * pitch, r);
+      if constexpr (RING) copy_out<HT, A>(hv[r], ring_h + slot * pitch, r, me);
 #pragma unroll
       for (int i = 0; i < PPT; ++i) v[r][i] = fma2(beta, hv[r][i], v[r][i]);
-      store_row<HT, A>(a.h_out, at_h, r, H, vec, v[r]);
+      store_row<HT, A>(a.h_out, at_h, r, H, me, v[r]);
     }
     // x' is taken from h' before its rounding: one rounding each
     if (a.pre != MOE_NORM_NONE) {
@@ -175,58 +188,64 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT)) norm_forward_kernel(No
         F2 c[PPT];
         float f[EPT];
         if constexpr (HOLD) {
-          copy_out<float, A>(c, s_pre, r, vec);
+          copy_out<float, A>(c, s_pre, r, me);
         } else {
-          load_columns<A>(f, a.w_pre, a.w_dtype, r, H, vec, 1.0f);
+          load_columns<A>(f, a.w_pre, a.w_dtype, r, H, me, 1.0f);
           pairs_of(c, f);
         }
 #pragma unroll
         for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] * (rp * c[i]);
         if (a.b_pre) {
           if constexpr (HOLD) {
-            copy_out<float, A>(c, s_bpre, r, vec);
+            copy_out<float, A>(c, s_bpre, r, me);
           } else {
-            load_columns<A>(f, a.b_pre, a.w_dtype, r, H, vec, 0.0f);
+            load_columns<A>(f, a.b_pre, a.w_dtype, r, H, me, 0.0f);
             pairs_of(c, f);
           }
 #pragma unroll
           for (int i = 0; i < PPT; ++i) v[r][i] = v[r][i] + c[i];
         }
-        store_row<OT, A>(a.x_out, at_o, r, H, vec, v[r]);
+        store_row<OT, A>(a.x_out, at_o, r, H, me, v[r]);
       }
     }
     if (++slot >= a.depth) slot = 0;
   }
 }
 
-template <typename HT, typename OT, Access A, int MAXT>
+template <typename HT, typename OT, Access A, int MAXT, bool SMALL = false>
 cudaError_t forward_of(NormArgs a, int threads, cudaStream_t s) {
   constexpr size_t kSmemMax = 224 * 1024;
   // 64 registers a thread; at most 32 blocks on an SM
-  int per_sm = min_blocks(MAXT) * MAXT / threads;
+  int per_sm = min_blocks(MAXT, SMALL && A == PLAIN) * MAXT / threads;
   if (per_sm > 32) per_sm = 32;
   size_t smem = 0;
   a.depth = 0;
   if (MAXT <= 512) {
     static const cudaError_t attr =
-        cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, MAXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(norm_forward_kernel<HT, OT, A, MAXT, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemMax));
     if (attr != cudaSuccess) return attr;
     const size_t pitch = slot_pitch(threads), row = pitch * (sizeof(HT) + sizeof(OT));
-    const size_t factors = (2 + (a.b_post ? 1 : 0) + (a.b_pre ? 1 : 0)) * pitch * sizeof(float);
+    const size_t factors = (2 + (a.b_post ? 1 : 0) + (a.b_pre ? 1 : 0)) * slot_pitch(SMALL ? a.lanes : threads) * sizeof(float);
     // two rows on their way; one, or none, where shared memory has no room for them beside the resident blocks
     if (A != PLAIN)
       a.depth = (3 * row + factors + 2048) * per_sm <= kSmemMax ? 3 : 2 * row + factors <= kSmemMax ? 2 : 1;
     smem = a.depth * row + factors;  // at most 64 KB + 128 KB
     while (per_sm > 1 && (smem + 2048) * per_sm > kSmemMax) --per_sm;
   }
-  const int cap = 152 * per_sm;
-  return launch_dependent(norm_forward_kernel<HT, OT, A, MAXT>, dim3(a.T < cap ? a.T : cap), dim3(threads), smem, s, a);
+  const int rows = SMALL ? threads / a.lanes : 1;
+  const int cap = 152 * per_sm, all = (a.T - 1) / rows + 1;
+  return launch_dependent(norm_forward_kernel<HT, OT, A, MAXT, SMALL>, dim3(all < cap ? all : cap), dim3(threads), smem, s, a);
 }
 
 template <typename HT, typename OT>
-cudaError_t forward_types(const NormArgs& a, cudaStream_t s) {
+cudaError_t forward_types(NormArgs a, cudaStream_t s) {
   const int threads = norm_threads(a.H);
+  if (takes_small(a)) {
+    a.lanes = norm_lanes(a.H);
+    const int block = small_threads(a.T, a.lanes);
+    return a.vec ? forward_of<HT, OT, VEC16, 128, true>(a, block, s) : forward_of<HT, OT, PLAIN, 128, true>(a, block, s);
+  }
   if (threads > 512) return forward_of<HT, OT, PLAIN, 1024>(a, threads, s);
   if (a.vec) {
     if (threads <= 128) return forward_of<HT, OT, VEC16, 128>(a, threads, s);

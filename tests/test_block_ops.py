@@ -278,6 +278,15 @@ def test_norm_sizes(m, T, H, kind):
     _norm_case(m, T, H, kind, True, True, "token", "f32", "f32", "f32", True)
 
 
+# short rows, taken by groups of 4 to 32 lanes: the last groups without a row, odd widths
+@pytest.mark.parametrize("T,H", [(1301, 33), (1301, 151), (1223, 40), (1229, 64), (311, 128), (2500, 249), (307, 256),
+                                 (613, 512)])
+@pytest.mark.parametrize("kind,gate", [("rms", "channel"), ("rms", None), ("layer", "token"), ("layer", "full")])
+def test_norm_short_rows(m, T, H, kind, gate):
+    _norm_case(m, T, H, kind, True, True, gate, "bf16", "bf16", "f32", kind == "layer")
+    _norm_case(m, T, H, kind, True, kind == "rms", gate, "f32", "f32", "f32", True, zero_row=True, eps=1e-3)
+
+
 def test_norm_strides_and_alignment(m):
     _norm_case(m, 9, 128, "rms", True, True, "full", "bf16", "bf16", "f32", False, ld_h=136, ld_o=144)
     _norm_case(m, 9, 128, "rms", True, True, "full", "bf16", "bf16", "f32", False, ld_h=131, ld_o=129)
