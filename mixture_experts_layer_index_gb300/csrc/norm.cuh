@@ -5,9 +5,8 @@
 // walk over rows.  (Sixteen columns per thread halve what the block-wide sums and
 // the addresses cost per column against eight: the gradient kernel is bound by
 // instructions as much as by memory.)  Where rows can be read asynchronously
-// (cp.async), each block keeps a ring of rows in shared memory: a thread copies
-// exactly the columns it will read itself, so the ring needs no barrier and the
-// rows in flight cost no registers.
+// (cp.async), each block keeps a ring of rows in shared memory: the rows in flight
+// cost no registers.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -22,15 +21,23 @@ constexpr int EPT = 8;   // columns per thread and run
 constexpr int RUNS = 2;
 
 // How a thread's columns of a row lie and come in.
-//   VEC16: columns [run*8*NT + tid*8, + 8), 16-byte copies into the ring (widths,
-//          strides and addresses that are multiples of 16 bytes)
+//   VEC16: columns [run*8*NT + tid*8, + 8), 16-byte copies into the ring (widths, strides and
+//          addresses that are multiples of 16 bytes)
 //   WORD4: a warp takes 512 columns, its lane l columns (run*8 + i)*32 + l of them: whole
 //          128-byte lines, and constant distances between a thread's columns; 4-byte
 //          copies into the ring (fp32 rows)
+//   SHIFT: columns like WORD4, of 16-bit rows at any address.  The 16-byte parts between a
+//          row's first and last 16-byte boundary are copied by whichever threads are next, to
+//          the same misalignment in a slot; the few elements around them go by way of
+//          registers.  The gradient's form, 4202 x 2046 bf16: 73 -> 51 us against PLAIN; the
+//          forward, which holds half as many rows in registers, gains nothing (17 us, 8192 x
+//          1001: 16.5 -> 19), nor do fp32 rows against WORD4 (4099 x 1023: 29 -> 35 us).
 //   PLAIN: columns like WORD4, or like VEC16 where the row allows it (`vec`), all of a row's
-//          loads issued together when the row's turn comes: 16-bit rows at odd addresses,
-//          which asynchronous copies do not take, and rows too long for a ring
-enum Access { VEC16, WORD4, PLAIN };
+//          loads issued together when the row's turn comes: 16-bit rows at odd addresses, which
+//          asynchronous copies of single elements do not take, and rows too long for a ring
+// With VEC16 and WORD4 a thread copies exactly the columns it will read itself, so the ring
+// needs no barrier; with SHIFT it takes one per row.
+enum Access { VEC16, WORD4, SHIFT, PLAIN };
 
 // Which of the threads of a row this one is.  Rows of up to 512 columns (SMALL) leave part
 // of a warp idle if a block takes them one by one, and a block's fixed cost per row is
@@ -256,7 +263,7 @@ __device__ __forceinline__ void copy_in(T* slot, const void* p, size_t at, int H
 // Zeros are put past column H of a slot once, so that reads need no test.
 template <typename T, Access A>
 __device__ __forceinline__ void clear_slot(T* slot, int H, const Own& me) {
-  if (A != PLAIN)
+  if (A == VEC16 || A == WORD4)
 #pragma unroll
     for (int r = 0; r < RUNS; ++r)
 #pragma unroll
@@ -264,6 +271,52 @@ __device__ __forceinline__ void clear_slot(T* slot, int H, const Own& me) {
         const int c = col_of<A>(r, i, me);
         if (c >= H) slot[c] = T(0.0f);
       }
+}
+// SHIFT: elements of a slot for rows of up to `pitch` columns: the row, its shift (up to 14
+// bytes) and eight zeros behind it.
+template <typename T, Access A>
+__host__ __device__ constexpr int slot_elements(int pitch) {
+  return pitch + (A == SHIFT ? 48 / static_cast<int>(sizeof(T)) : 0);
+}
+// SHIFT: where in its slot a row starts.
+template <typename T, Access A>
+__device__ __forceinline__ int shift_of(const void* p, size_t at) {
+  return A != SHIFT ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(p) + at * sizeof(T)) & 15) / static_cast<int>(sizeof(T));
+}
+// SHIFT: the column that threads 0 to 15 carry by register, before the first 16-byte boundary
+// (threads 0 to 7) or from the last one on; -1: none.
+template <typename T>
+__device__ __forceinline__ int edge_column(int shift, int H) {
+  constexpr int PER = 16 / sizeof(T);
+  int head = (PER - shift) & (PER - 1);
+  if (head > H) head = H;
+  int tail = (shift + H) & (PER - 1);
+  if (tail > H - head) tail = H - head;
+  const int e = threadIdx.x & 7;
+  return threadIdx.x >= 16 ? -1 : threadIdx.x < 8 ? (e < head ? e : -1) : (e < tail ? H - tail + e : -1);
+}
+template <typename T, Access A>
+__device__ __forceinline__ void start_row(T* slot, T& edge, const void* p, size_t at, int H) {
+  constexpr int PER = 16 / sizeof(T);
+  const T* row = static_cast<const T*>(p) + at;
+  const int shift = shift_of<T, A>(p, at);
+  const int head = (PER - shift) & (PER - 1);
+  const int parts = (shift + H) / PER - (shift + head) / PER;  // may be negative
+#pragma unroll
+  for (int i = 0; i < EPT * RUNS / PER; ++i) {
+    const int q = i * blockDim.x + threadIdx.x;
+    if (q < parts) cp_async16(slot + shift + head + q * PER, row + head + q * PER);
+  }
+  const int c = edge_column<T>(shift, H);
+  if (c >= 0) edge = row[c];
+}
+// The elements at the ends of a row, and the zeros behind it (another row may have ended later).
+template <typename T, Access A>
+__device__ __forceinline__ void finish_row(T* slot, T edge, const void* p, size_t at, int H) {
+  const int shift = shift_of<T, A>(p, at);
+  const int c = edge_column<T>(shift, H);
+  if (c >= 0) slot[shift + c] = edge;
+  if (threadIdx.x >= 16 && threadIdx.x < 24) slot[shift + H + threadIdx.x - 16] = T(0.0f);
 }
 template <typename T, Access A>
 __device__ __forceinline__ void copy_out(float (&v)[EPT], const T* slot, int r, const Own& me) {

@@ -73,12 +73,18 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
   const bool gate_t = a.gate_kind == MOE_GATE_TOKEN;
   // ring slots: o | dh' | h' | dx', then the factors of the post and of the pre norm; rows
   // of over 8192 columns: the column sums (in the workspace itself where they do not fit)
-  const int ring = a.depth * pitch, my_row = mine * row_pitch;
+  const int my_row = mine * row_pitch;
+  const int slot_h = slot_elements<HT, A>(pitch), slot_o = slot_elements<OT, A>(pitch);
   OT* ring_o = reinterpret_cast<OT*>(s_mem);
-  HT* ring_g = reinterpret_cast<HT*>(ring_o + ring);
-  HT* ring_h = ring_g + (a.dh_out ? ring : 0);
-  OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? ring : 0));
-  float* s_post = reinterpret_cast<float*>(ring_x + (pre ? ring : 0));
+  HT* ring_g = reinterpret_cast<HT*>(ring_o + a.depth * slot_o);
+  HT* ring_h = ring_g + (a.dh_out ? a.depth * slot_h : 0);
+  OT* ring_x = reinterpret_cast<OT*>(ring_h + (pre ? a.depth * slot_h : 0));
+  float* s_post = reinterpret_cast<float*>(ring_x + (pre ? a.depth * slot_o : 0));
+  if (A == SHIFT) {
+    for (uint4* p = reinterpret_cast<uint4*>(s_mem) + threadIdx.x; p < reinterpret_cast<uint4*>(s_post); p += blockDim.x)
+      *p = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
   ring_o += my_row;
   ring_g += my_row;
   ring_h += my_row;
@@ -98,23 +104,34 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 
   if (RING)
     for (int d = 0; d < a.depth; ++d) {
-      clear_slot<OT, A>(ring_o + d * pitch, H, me);
-      if (a.dh_out) clear_slot<HT, A>(ring_g + d * pitch, H, me);
+      clear_slot<OT, A>(ring_o + d * slot_o, H, me);
+      if (a.dh_out) clear_slot<HT, A>(ring_g + d * slot_h, H, me);
       if (pre) {
-        clear_slot<HT, A>(ring_h + d * pitch, H, me);
-        clear_slot<OT, A>(ring_x + d * pitch, H, me);
+        clear_slot<HT, A>(ring_h + d * slot_h, H, me);
+        clear_slot<OT, A>(ring_x + d * slot_o, H, me);
       }
     }
+  HT edge_h = {}, edge_g = {};
+  OT edge_o = {}, edge_x = {};
   const unsigned T = a.T;  // t may pass 2^31 by the rows ahead
   auto fetch = [&](unsigned t, int slot) {
     if (t < T) {
       const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
-      if (pre) {
-        copy_in<HT, A>(ring_h + slot * pitch, a.h, at_h, H, me);
-        copy_in<OT, A>(ring_x + slot * pitch, a.dx_out, at_o, H, me);
+      if constexpr (A == SHIFT) {
+        if (pre) {
+          start_row<HT, A>(ring_h + slot * slot_h, edge_h, a.h, at_h, H);
+          start_row<OT, A>(ring_x + slot * slot_o, edge_x, a.dx_out, at_o, H);
+        }
+        start_row<OT, A>(ring_o + slot * slot_o, edge_o, a.o, at_o, H);
+        if (a.dh_out) start_row<HT, A>(ring_g + slot * slot_h, edge_g, a.dh_out, at_h, H);
+      } else {
+        if (pre) {
+          copy_in<HT, A>(ring_h + slot * slot_h, a.h, at_h, H, me);
+          copy_in<OT, A>(ring_x + slot * slot_o, a.dx_out, at_o, H, me);
+        }
+        copy_in<OT, A>(ring_o + slot * slot_o, a.o, at_o, H, me);
+        if (a.dh_out) copy_in<HT, A>(ring_g + slot * slot_h, a.dh_out, at_h, H, me);
       }
-      copy_in<OT, A>(ring_o + slot * pitch, a.o, at_o, H, me);
-      if (a.dh_out) copy_in<HT, A>(ring_g + slot * pitch, a.dh_out, at_h, H, me);
     }
     cp_async_commit();
   };
@@ -177,20 +194,39 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
     const bool live = !SMALL || t < T;
     const int H = live ? a.H : 0;
     const size_t at_h = static_cast<size_t>(t) * a.ld_h, at_o = static_cast<size_t>(t) * a.ld_o;
-    if (RING) {
-      const int ahead = slot + a.depth - 1;
+    const int ahead = slot + a.depth - 1;
+    if constexpr (A == SHIFT) {
+      // one row ahead, or none where shared memory holds only one
+      if (a.depth == 1) {
+        __syncthreads();
+        fetch(t, 0);
+      }
+      cp_async_wait(1);
+      if (pre) {
+        finish_row<HT, A>(ring_h + slot * slot_h, edge_h, a.h, at_h, H);
+        finish_row<OT, A>(ring_x + slot * slot_o, edge_x, a.dx_out, at_o, H);
+      }
+      finish_row<OT, A>(ring_o + slot * slot_o, edge_o, a.o, at_o, H);
+      if (a.dh_out) finish_row<HT, A>(ring_g + slot * slot_h, edge_g, a.dh_out, at_h, H);
+      __syncthreads();  // this row is there, and all are done with the last one
+      if (a.depth == 2) fetch(t + stride, slot ^ 1);
+    } else if (RING) {
       fetch(t + (a.depth - 1) * stride, ahead >= a.depth ? ahead - a.depth : ahead);
       cp_async_wait(a.depth);
     }
+    const OT* in_o = ring_o + slot * slot_o + shift_of<OT, A>(a.o, at_o);
+    const OT* in_x = ring_x + slot * slot_o + shift_of<OT, A>(a.dx_out, at_o);
+    const HT* in_h = ring_h + slot * slot_h + shift_of<HT, A>(a.h, at_h);
+    const HT* in_g = ring_g + slot * slot_h + shift_of<HT, A>(a.dh_out, at_h);
     F2 hc[RUNS][PPT], oc[RUNS][PPT], dx[RUNS][PPT], G[RUNS][PPT];
 #pragma unroll
     for (int r = 0; r < RUNS; ++r) {
-      if constexpr (RING) copy_out<OT, A>(oc[r], ring_o + slot * pitch, r, me);
+      if constexpr (RING) copy_out<OT, A>(oc[r], in_o, r, me);
       else load_row<OT, A>(oc[r], a.o, at_o, r, H, me);
       if (pre) {
         if constexpr (RING) {
-          copy_out<HT, A>(hc[r], ring_h + slot * pitch, r, me);
-          copy_out<OT, A>(dx[r], ring_x + slot * pitch, r, me);
+          copy_out<HT, A>(hc[r], in_h, r, me);
+          copy_out<OT, A>(dx[r], in_x, r, me);
         } else {
           load_row<HT, A>(hc[r], a.h, at_h, r, H, me);
           load_row<OT, A>(dx[r], a.dx_out, at_o, r, H, me);
@@ -263,7 +299,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks(MAXT, GENERAL)) norm_backward
 #pragma unroll
         for (int i = 0; i < PPT; ++i) G[r][i] = f2(0.0f);
       } else if constexpr (RING) {
-        copy_out<HT, A>(G[r], ring_g + slot * pitch, r, me);
+        copy_out<HT, A>(G[r], in_g, r, me);
       }
       if (pre) {
         F2 f[PPT];
@@ -509,7 +545,7 @@ inline int most_blocks_per_sm(int H) {
   return n > 16 ? 16 : n < 1 ? 1 : n;
 }
 
-constexpr size_t kSmemMax = 224 * 1024;  // of one block's dynamic shared memory
+constexpr size_t kSmemMax = 226 * 1024;  // of one block's dynamic shared memory, beside up to 1 KB static
 constexpr size_t kSmemSm = 228 * 1024;   // of an SM; a block takes 1 KB of its own and 1 KB static
 
 template <typename HT, typename OT, Access A, int MAXT, bool GENERAL, bool SMALL = false>
@@ -529,9 +565,10 @@ cudaError_t backward_of(NormArgs& a, int threads, cudaStream_t s) {
     if (A != PLAIN) {
       // a row that is worked on and, where they fit with the resident blocks, one or two
       // on their way; 128 KB at most for one row, beside 96 KB of factors
-      const size_t row = pitch * (sizeof(OT) + (a.dh_out ? sizeof(HT) : 0) + (a.pre ? sizeof(HT) + sizeof(OT) : 0));
-      a.depth = 3;
-      while (a.depth > 1 && !fits(a.depth * row + factors, per_sm)) --a.depth;
+      const size_t row_o = slot_elements<OT, A>(pitch) * sizeof(OT), row_h = slot_elements<HT, A>(pitch) * sizeof(HT);
+      const size_t row = row_o + (a.dh_out ? row_h : 0) + (a.pre ? row_h + row_o : 0);
+      a.depth = A == SHIFT ? 2 : 3;
+      while (a.depth > 1 && !fits(a.depth * row + factors, A == SHIFT ? 1 : per_sm)) --a.depth;
       smem = a.depth * row;
     }
     smem += factors;
@@ -572,9 +609,13 @@ cudaError_t backward_types(NormArgs& a, cudaStream_t s) {
     if (threads <= 256) return backward_of<HT, OT, VEC16, 256, false>(a, threads, s);
     return backward_of<HT, OT, VEC16, 512, false>(a, threads, s);
   }
-  constexpr Access odd = sizeof(HT) == 4 && sizeof(OT) == 4 ? WORD4 : PLAIN;
-  if (threads <= 128) return backward_of<HT, OT, odd, 128, true>(a, threads, s);
-  return backward_of<HT, OT, odd, 512, true>(a, threads, s);
+  constexpr Access odd = sizeof(HT) == 4 && sizeof(OT) == 4 ? WORD4 : SHIFT;
+  if (general) {
+    if (threads <= 128) return backward_of<HT, OT, odd, 128, true>(a, threads, s);
+    return backward_of<HT, OT, odd, 512, true>(a, threads, s);
+  }
+  if (threads <= 128) return backward_of<HT, OT, odd, 128, false>(a, threads, s);
+  return backward_of<HT, OT, odd, 512, false>(a, threads, s);
 }
 
 }  // namespace
