@@ -43,16 +43,17 @@ struct TileProduct {
   int C, R;        // output columns and rows
   int nk;          // stages of the whole sum
   int nC, nR;      // tiles
+  int splits;      // blocks per tile: a cluster's, or 1
   int a_mn, b_mn;  // operand columns / rows contiguous along c / r
   Epilogue ep;
 };
-// A launch computes one product, or two side by side (a gradient's two, when neither fills
-// the GPU): blocks from `first_blocks` on belong to the second.
+// A launch computes one product, or two side by side (a gradient's two, unless both fill the
+// GPU): blocks from `first_blocks` on belong to the second.  A cluster's blocks share a tile of
+// one product, or take one tile each.
 struct Params {
   TileProduct prod[2];
   int first_blocks;
   int stages;      // of the ring
-  int splits;      // blocks per tile (cluster size)
   int nacc;        // accumulators that a block's part of the sum is spread over
   uint32_t tmem_cols;
   int type;        // 0 = f16, 1 = bf16 operands
@@ -159,6 +160,9 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   const CUtensorMap* mb = second ? &m1.b : &m0.b;
   const bool a_mn = o.a_mn, b_mn = BN >= 64 && o.b_mn;  // an MN-major box is 64 wide
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + MAX_STAGES), done = smem_u32(bars + 2 * MAX_STAGES);
+  const int rank = o.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = (static_cast<int>(blockIdx.x) - (second ? p.first_blocks : 0)) / o.splits;
+  if (tile >= o.nC * o.nR) return;  // fills up a cluster of single tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -186,15 +190,13 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
 
   // tiles: 16 row tiles side by side, then the next column tile, so that the blocks in
   // flight share both operands in L2
-  const int rank = p.splits > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int tile = (static_cast<int>(blockIdx.x) - (second ? p.first_blocks : 0)) / p.splits;
   constexpr int GR = 16;
   const int group = tile / (GR * o.nC), in_group = tile - group * (GR * o.nC);
   const int rows_here = min(GR, o.nR - group * GR);
   const int c0 = in_group / rows_here * BM;
   const int r0 = (group * GR + in_group % rows_here) * BN;
-  const int kb0 = static_cast<int>(static_cast<long long>(o.nk) * rank / p.splits);
-  const int kb1 = static_cast<int>(static_cast<long long>(o.nk) * (rank + 1) / p.splits);
+  const int kb0 = static_cast<int>(static_cast<long long>(o.nk) * rank / o.splits);
+  const int kb1 = static_cast<int>(static_cast<long long>(o.nk) * (rank + 1) / o.splits);
   const int n = kb1 - kb0;                // at least 1: splits <= nk
   const int nacc = min(p.nacc, n);        // accumulators that this block fills
 
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
     // the residual's part of the tile comes into L2 while the product is computed
     const size_t es = o.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
     const size_t bytes = static_cast<size_t>(min(BM, o.C - c0)) * es;
-    const int share = BN / p.splits;
+    const int share = BN / o.splits;
     for (int j = rank * share + (warp - 2) * 32 + lane; j < min((rank + 1) * share, o.R - r0); j += 64) {
       const uint8_t* row = static_cast<const uint8_t*>(o.ep.residual) + (static_cast<size_t>(r0 + j) * o.ep.ld_y + c0) * es;
       for (size_t b = 0; b < bytes; b += 128) prefetch_l2(row + b);
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   // memory too, and groups of `width` threads take rows in turn.
   const int cols = min(BM, o.C - c0);
   const int width = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : BM;
-  if (p.splits == 1 && width == BM) {
+  if (o.splits == 1 && width == BM) {
     if (good) {
 #pragma unroll 1
       for (int j = 0; j < BN; j += CH) {
@@ -319,17 +321,18 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
         for (int i = 0; i < CH; ++i) part[(j + i) * BM + cl] = v[i];
       }
     }
-    if (p.splits > 1) cluster_sync_all();
+    if (o.splits > 1) cluster_sync_all();
     else __syncthreads();
     if (good) {
       // this block's share of the rows, this thread's group's of them, RB at a time: all
       // ranks' values of RB rows are on their way before the first is added
       const int groups = BM / width, own = static_cast<int>(threadIdx.x) / width;
       const int c = static_cast<int>(threadIdx.x) & (width - 1);
-      const int per = BN / p.splits;
+      const int per = BN / o.splits;
       const int per_group = (per + groups - 1) / groups;
       constexpr int RB = 8;
       const uint32_t mine = smem_u32(part) + c * 4;
+      const uint32_t first = o.splits > 1 ? 0u : cluster_rank();  // of the blocks that share the tile
       const int begin = rank * per + own * per_group;
       const int end = min(min(begin + per_group, (rank + 1) * per), o.R - r0);
       for (int j = begin; j < end; j += RB) {
@@ -337,20 +340,20 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
         float u[MAX_SPLITS][RB];
 #pragma unroll
         for (int q = 0; q < MAX_SPLITS; ++q)
-          if (q < p.splits)
+          if (q < o.splits)
 #pragma unroll
             for (int i = 0; i < RB; ++i)
-              if (i < cnt) u[q][i] = ld_cluster_f32(mine + (j + i) * (BM * 4), q);
+              if (i < cnt) u[q][i] = ld_cluster_f32(mine + (j + i) * (BM * 4), first + q);
         float v[RB] = {};
 #pragma unroll
         for (int q = 0; q < MAX_SPLITS; ++q)
-          if (q < p.splits)
+          if (q < o.splits)
 #pragma unroll
             for (int i = 0; i < RB; ++i) v[i] += u[q][i];
         finish<RB>(o, v, r0 + j, cnt, c0 + c);
       }
     }
-    if (p.splits > 1) cluster_sync_all();  // no block leaves while another still reads its partial
+    if (o.splits > 1) cluster_sync_all();  // no block leaves while another still reads its partial
   }
   tc_fence_before();
   __syncthreads();
@@ -360,12 +363,13 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   }
 }
 
-bool encode_product(TileMaps* m, TileProduct* t, const Product& q, int bn) {
+bool encode_product(TileMaps* m, TileProduct* t, const Product& q, int bn, int splits) {
   t->C = q.C;
   t->R = q.R;
   t->nk = (q.K + BK - 1) / BK;
   t->nC = (q.C + BM - 1) / BM;
   t->nR = (q.R + bn - 1) / bn;
+  t->splits = splits;
   t->a_mn = q.cols_mn;
   t->b_mn = q.rows_mn;
   t->ep = q.ep;
@@ -373,25 +377,34 @@ bool encode_product(TileMaps* m, TileProduct* t, const Product& q, int bn) {
          encode(&m->b, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : bn);
 }
 
+struct Choice {
+  int bn, splits;
+  float us;
+  int splits2;  // of the second product: 1, or as many as a cluster has blocks, like the first's
+};
+
 template <int BN>
-cudaError_t launch_tile(const Product& q, const Product* second, int splits, cudaStream_t s) {
+cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c, cudaStream_t s) {
   Params p{};
   TileMaps m0, m1;
-  if (!encode_product(&m0, &p.prod[0], q, BN)) return cudaErrorInvalidValue;
+  if (!encode_product(&m0, &p.prod[0], q, BN, c.splits)) return cudaErrorInvalidValue;
   m1 = m0;
-  if (second && !encode_product(&m1, &p.prod[1], *second, BN)) return cudaErrorInvalidValue;
+  if (second && !encode_product(&m1, &p.prod[1], *second, BN, c.splits2)) return cudaErrorInvalidValue;
   static const cudaError_t attr = cudaFuncSetAttribute(
       linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN, stages_of(BN, 1)));
   if (attr != cudaSuccess) return attr;
-  p.splits = splits;
   p.type = q.type;
   p.reset_status = q.reset_status;
   p.hdr = q.hdr;
-  p.first_blocks = p.prod[0].nC * p.prod[0].nR * splits;
-  const long long blocks = p.first_blocks + static_cast<long long>(p.prod[1].nC) * p.prod[1].nR * splits;
+  const int cluster = second && c.splits2 > c.splits ? c.splits2 : c.splits;
+  auto blocks_of = [&](const TileProduct& t) {
+    return (static_cast<long long>(t.nC) * t.nR * t.splits + cluster - 1) / cluster * cluster;
+  };
+  p.first_blocks = static_cast<int>(blocks_of(p.prod[0]));
+  const long long blocks = p.first_blocks + (second ? blocks_of(p.prod[1]) : 0);
   // one block per SM where the grid leaves no second one: its ring takes all of shared
   // memory (not in large clusters, which then no longer find enough free SMs together)
-  p.stages = stages_of(BN, BN == 256 || (blocks <= 152 && splits <= 2) ? 1 : 2);
+  p.stages = stages_of(BN, BN == 256 || (blocks <= 152 && cluster <= 2) ? 1 : 2);
   // fp32 output: the tensor core's running sum rounds at every step, so its length is
   // kept short by spreading the sum over up to four accumulators
   p.nacc = q.ep.out_dtype != MOE_DTYPE_F32 ? 1 : BN <= 64 ? 4 : 2;
@@ -400,7 +413,7 @@ cudaError_t launch_tile(const Product& q, const Product* second, int splits, cud
   p.tmem_cols = cols;
   cudaLaunchAttribute la[2];
   la[0].id = cudaLaunchAttributeClusterDimension;
-  la[0].val.clusterDim.x = splits;
+  la[0].val.clusterDim.x = cluster;
   la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
   la[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   la[1].val.programmaticStreamSerializationAllowed = 1;
@@ -444,17 +457,13 @@ float tile_estimate(const Product& q, int bn, int splits) {
   return splits > 1 ? t + 1.0f + 0.02f * bn : t;
 }
 
-struct Choice {
-  int bn, splits;
-  float us;
-};
 Choice choose_tile(const Product& q) {
   const long long nk = (q.K + BK - 1) / BK;
-  Choice best{0, 1, 0.0f};
+  Choice best{0, 1, 0.0f, 1};
   for (int bn = q.rows_mn ? 64 : 16; bn <= 256; bn *= 2) {
     for (int splits = 1; splits <= MAX_SPLITS && (splits == 1 || nk / splits >= 2); splits *= 2) {
       const float us = tile_estimate(q, bn, splits);
-      if (best.bn == 0 || us < best.us) best = {bn, splits, us};
+      if (best.bn == 0 || us < best.us) best = {bn, splits, us, 1};
     }
     if (bn >= q.R) break;
   }
@@ -463,32 +472,39 @@ Choice choose_tile(const Product& q) {
 
 cudaError_t launch_shape(const Product& q, const Product* second, const Choice& c, cudaStream_t s) {
   switch (c.bn) {
-    case 16: return launch_tile<16>(q, second, c.splits, s);
-    case 32: return launch_tile<32>(q, second, c.splits, s);
-    case 64: return launch_tile<64>(q, second, c.splits, s);
-    case 128: return launch_tile<128>(q, second, c.splits, s);
-    default: return launch_tile<256>(q, second, c.splits, s);
+    case 16: return launch_tile<16>(q, second, c, s);
+    case 32: return launch_tile<32>(q, second, c, s);
+    case 64: return launch_tile<64>(q, second, c, s);
+    case 128: return launch_tile<128>(q, second, c, s);
+    default: return launch_tile<256>(q, second, c, s);
   }
 }
 
-// Two products in one wave of a launch of tiles of 128 x bn: the longer of the two, if they fit.
+// Two products in one launch of tiles of 128 x bn whose blocks all find a place at once: the
+// longer of the two.  Sums of different lengths are split differently where each block has
+// an SM to itself (4 x 3167 x 104's gradient: 12.2 us apart, 9.5 together; with two blocks on
+// an SM that loses to two launches: 2048 x 1024 x 1024 20.5 us apart, 24.4 together).
 Choice choose_both(const Product& q0, const Product& q1) {
-  Choice best{0, 1, 0.0f};
+  const Product* q[2] = {&q0, &q1};
+  Choice best{0, 1, 0.0f, 1};
   for (int bn = 64; bn <= 128; bn *= 2)
-    for (int splits = 1; splits <= MAX_SPLITS; splits *= 2) {
-      long long blocks = 0;
-      float us = 0.0f;
-      bool ok = true;
-      for (const Product* q : {&q0, &q1}) {
-        const long long nk = (q->K + BK - 1) / BK;
-        ok = ok && (splits == 1 || nk / splits >= 2);
-        blocks += static_cast<long long>((q->C + BM - 1) / BM) * ((q->R + bn - 1) / bn) * splits;
-        const float t = tile_estimate(*q, bn, splits);
-        us = t > us ? t : us;
+    for (int cluster = 1; cluster <= MAX_SPLITS; cluster *= 2)
+      for (int shared = cluster > 1 ? 1 : 0; shared < (cluster > 1 ? 4 : 1); ++shared) {  // one bit per product
+        long long blocks[2];
+        bool ok = true;
+        for (int i = 0; i < 2; ++i) {
+          const int splits = shared >> i & 1 ? cluster : 1;
+          ok = ok && (splits == 1 || (q[i]->K + BK - 1) / BK / splits >= 2);
+          blocks[i] = static_cast<long long>((q[i]->C + BM - 1) / BM) * ((q[i]->R + bn - 1) / bn) * splits;
+          blocks[i] = (blocks[i] + cluster - 1) / cluster * cluster;
+        }
+        const bool equal = cluster == 1 || shared == 3;
+        if (!ok || blocks[0] + blocks[1] > (equal ? 2 : 1) * (cluster == 8 ? 128 : 152)) continue;
+        const float t0 = tile_estimate(q0, bn, shared & 1 ? cluster : 1);
+        const float t1 = tile_estimate(q1, bn, shared & 2 ? cluster : 1);
+        const float us = t0 > t1 ? t0 : t1;
+        if (best.bn == 0 || us < best.us) best = {bn, shared & 1 ? cluster : 1, us, shared & 2 ? cluster : 1};
       }
-      if (!ok || blocks > 2 * (splits == 8 ? 128 : 152)) continue;
-      if (best.bn == 0 || us < best.us) best = {bn, splits, us};
-    }
   return best;
 }
 
@@ -704,12 +720,12 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
   dw.rows_mn = true;
   dw.ep.y = a.dw;
   if (err == cudaSuccess && a.dx && a.dw) {
-    const Choice cx = choose_tile(dx), cw = choose_tile(dw), both = choose_both(dx, dw);
+    const Choice cx = choose_tile(dx), cw = choose_tile(dw), both = choose_both(dw, dx);
     const bool px = takes_pair(dx, cx), pw = takes_pair(dw, cw);
     const float apart = (px ? pair_estimate(dx) : cx.us) + (pw ? pair_estimate(dw) : cw.us);
     if ((px && pw) || (both.bn && both.us < apart)) {
       stage_begin("linear_dx_dw", s);
-      err = px && pw ? launch_pair(dx, &dw, s) : launch_shape(dx, &dw, both, s);
+      err = px && pw ? launch_pair(dx, &dw, s) : launch_shape(dw, &dx, both, s);
       stage_end(s);
       return err;
     }
