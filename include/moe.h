@@ -32,7 +32,9 @@
  *   - The caller owns and allocates every buffer, including outputs and the
  *     workspace.  The library never allocates, frees or synchronises inside
  *     moe_route / moe_shuffle / moe_tile_map / moe_forward / moe_forward_ex /
- *     moe_round_bf16: work is enqueued
+ *     moe_forward_routed / moe_round_bf16 / moe_route_ex / moe_route_backward /
+ *     moe_norm_forward / moe_norm_backward / moe_linear / moe_linear_backward:
+ *     work is enqueued
  *     on `stream` in order, with no device-to-host copy, so these calls can be
  *     captured in a CUDA graph.  Inputs are never written.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
@@ -384,7 +386,9 @@ typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dt
  * group of masked experts ranks last).  If fewer than k experts are left, masked
  * ones fill the slots in id order with weight 0; a row that is masked as a whole
  * gets valid ids and weights 0.  +inf counts as the largest finite fp32.  bias
- * values are finite.  p and keys are computed in fp32 (expf, IEEE division).
+ * values are finite.  All arithmetic is in fp32: weights from expf and IEEE
+ * divisions; the p of a key with a bias from the hardware's exponential and
+ * division, within 2e-7, so experts whose keys differ by less may change places.
  *   scores [T, E] of dtype, ld elements between rows
  *   ids    [T, k] int32 out;  w [T, k] fp32 out
  * Limits: those of moe_route, n_group <= 32 (UNSUPPORTED); n_group divides E,

@@ -15,6 +15,11 @@
 // columns at a time are loaded from TMEM, finished in fp32, rounded once, staged in
 // shared memory as a 128-byte-swizzled box of 32 rows and stored by TMA, which
 // clips the edges.
+//
+// Bound by the tensor cores: 16384 x 8192 x 2048 bf16 takes 294 us, 1.87 PFLOP/s (a library
+// product reaches 1.95 in short runs, 1.74 under the power limit).  With a GELU and its
+// argument kept 400 us: 16 warps' worth of epilogue instructions beside the MMAs and a
+// second output; a residual or an odd width (plain stores) cost similar shares.
 #include "linear.cuh"
 
 namespace moe {

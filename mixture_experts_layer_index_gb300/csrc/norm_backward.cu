@@ -4,7 +4,12 @@
 // (the last mean for layer norms only).  With G = dh' + dv of the pre norm:
 //   dh = beta G,   dn of the post norm = alpha g G,   dg = alpha G N_post(o).
 //
-// Bound by memory: four rows in, two out.  A row's moments and the means of its
+// Bound by memory: four rows in, two out; 16384 x 2048 bf16 with RMS norms and a gate per
+// column take 67.6 us, 5.95 TB/s (a plain copy reaches 6.7) at 60 % of the issue slots.  With
+// layer norms 101 us: a third sum per row and the sums for the biases, whose
+// registers leave three blocks of 128 threads per SM instead of four.  Odd rows are
+// bound by instructions (an element at a time), see Access in norm.cuh.
+// A row's moments and the means of its
 // gradient come from the same sum over the block (the means of RMS norms need no
 // second look), so a row takes two block-wide sums, three with a layer norm.
 // Column sums stay with the thread that owns the column, in registers up to

@@ -22,6 +22,12 @@
 // length of the chain of rounds.  So the forward gives a row few lanes with 16 experts
 // each when there are many rows (a round's bookkeeping is then shared by the 2 to 16 rows
 // of a warp), and a whole warp when there are few.
+//
+// Measured, 16384 tokens of 128 fp32 sigmoid scores with a bias, 4 of 8 groups, top 8:
+// 13.7 us against 1.4 us for the bytes; with 256 experts under a profiler 25.7 us, 16.1 M
+// warp instructions at 61 % of the issue slots.  Eight tokens: 4.2 us, of which launch and
+// drain are 2.2.  The gradient touches k values per row (all of E without renormalised
+// softmax weights) and is bound by its bytes and the launch: 4.7 us for 16384 x 128, k = 8.
 #include <cuda_fp16.h>
 
 #include "common.cuh"

@@ -144,6 +144,28 @@ def test_linear_refusals(m):
     assert fwd(m.linear_problem(0, 24, 64), x=None, w=None, y=None, ws=None, nb=0) == m.MOE_OK
 
 
+def test_forward_routed_refusals(m):
+    def fwd(p, opt=None, x=FAKE, ids=FAKE, w=FAKE, w1=FAKE, w2=FAKE, s1=None, s2=None, y=FAKE, ws=FAKE, nb=1 << 40):
+        return m.raw_status("moe_forward_routed", ctypes.byref(p) if p else None, ctypes.byref(opt) if opt else None, x,
+                            ids, w, w1, w2, s1, s2, y, ws, nb, None)
+
+    bad = m.MOE_ERR_INVALID_ARG
+    ok = m.problem(16, 8, 2, 256, 128)
+    for kw in (dict(x=None), dict(ids=None), dict(w=None), dict(w1=None), dict(w2=None), dict(y=None), dict(ids=FAKE + 2),
+               dict(w=FAKE + 1), dict(x=FAKE + 8), dict(y=FAKE + 2), dict(s1=FAKE)):
+        assert fwd(ok, **kw) == bad, kw
+    assert fwd(None) == bad
+    assert fwd(ok, ws=None) == m.MOE_ERR_WORKSPACE
+    assert fwd(ok, nb=m.moe_workspace_size(ok) - 1) == m.MOE_ERR_WORKSPACE
+    assert fwd(m.problem(16, 8, 9, 256, 128)) == bad
+    assert fwd(m.problem(16, 1000, 2, 256, 128)) == m.MOE_ERR_UNSUPPORTED
+    assert fwd(m.problem(2, 32, 8, 512, 192, "fp8_tensor")) == bad  # no scales
+    opt = m.moe_forward_options()
+    opt.y_fp32 = 2
+    assert fwd(ok, opt=opt) == bad
+    assert fwd(m.problem(0, 8, 2, 256, 128), x=None, ids=None, w=None, y=None, ws=None, nb=0) == m.MOE_OK
+
+
 def test_binding_checks_tensors(m):
     torch = pytest.importorskip("torch")
     p = m.linear_problem(4, 24, 64)
