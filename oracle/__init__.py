@@ -14,6 +14,8 @@ written in numpy:
                    permutation, inverse), the GEMM tile map, activation
                    quantisation and the full forward (bf16, per-tensor FP8,
                    128x128-blockwise FP8), and the weighted top-k combine.
+  * ``blocks``   - the operators around the forward, in 64 bits: routing rules,
+                   block norms, the linear layer, and their gradients.
 
 The steps follow the expert-grouped pipeline described in the Motivation
 section of "perf: add small-batch route MMA for MoE" (group the routes by
