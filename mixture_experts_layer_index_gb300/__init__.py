@@ -185,24 +185,41 @@ def _check(status: int, where: str) -> None:
 
 def _ptr(t) -> Optional[int]:
     """Device pointer of a contiguous CUDA tensor (None -> NULL; ints pass through)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    if not t.is_cuda:
+    try:
+        on_device = t.is_cuda
+    except AttributeError:
+        if isinstance(t, int):  # its subclasses
+            return int(t)
+        raise
+    if not on_device:
         raise ValueError("device tensor expected")
     if not t.is_contiguous():
         raise ValueError("contiguous tensor expected")
     return t.data_ptr()
 
 
+_current_stream = None  # the raw handle of the current device's current stream
+
+
+def _find_current_stream():
+    global _current_stream
+    import torch
+
+    device = torch.cuda.current_device  # starts CUDA, or raises where there is none
+    device()
+    # the Stream object that torch.cuda.current_stream() builds around the handle costs more than a
+    # small launch (2.9 us; the handle alone 0.2)
+    device, handle = getattr(torch._C, "_cuda_getDevice", device), torch._C._cuda_getCurrentRawStream
+    _current_stream = lambda: handle(device())  # noqa: E731
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the raw handle of the current device's current stream: the Stream object that
-        # torch.cuda.current_stream() builds around it costs more than a small launch (2.9 us)
-        import torch
-
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current_stream is None:
+            _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -336,9 +353,15 @@ def moe_forward_views(p: moe_problem, ws, ws_bytes=None) -> moe_views:
 def _rows(t, name: str = "tensor") -> Optional[int]:
     """Device pointer of a CUDA tensor whose rows are contiguous (the row stride is the
     descriptor's ld); None -> NULL; ints pass through."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    if not t.is_cuda:
+    try:
+        on_device = t.is_cuda
+    except AttributeError:
+        if isinstance(t, int):  # its subclasses
+            return int(t)
+        raise
+    if not on_device:
         raise ValueError(f"{name}: device tensor expected")
     if not t.is_contiguous() and t.stride(-1) != 1:
         raise ValueError(f"{name}: rows must be contiguous")

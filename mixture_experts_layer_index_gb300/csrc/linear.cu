@@ -19,7 +19,8 @@
 // over all partials, read from the others' shared memory in rank order: no
 // workspace, no atomics, the same result every time.
 //
-// What bounds it: few rows read the weights once (8 x 4096 x 4096: 7.3 us for 34 MB, 4.6 TB/s,
+// What bounds it: some rows read the weights once (up to eight rows of small products
+// go to linear_few.cu; 8 x 4096 x 4096: 7.3 us for 34 MB, 4.6 TB/s,
 // 5 us at a copy's rate, the rest launch, ring fill and join); few columns read x once
 // (16384 x 128 x 2048: 14.2 us, 4.7 TB/s).  Products that fill the GPU with tiles are
 // bound by arithmetic and go to linear_pair.cu.  Which tiles and splits a product takes
@@ -662,7 +663,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   q.reset_status = 1;
   q.hdr = a.hdr;
   stage_begin("linear", s);
-  const cudaError_t err = launch_product(q, s);
+  const cudaError_t err = takes_few(a) ? launch_few(a, s) : launch_product(q, s);
   stage_end(s);
   return err;
 }

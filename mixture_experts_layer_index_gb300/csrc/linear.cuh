@@ -1,5 +1,5 @@
-// Parts shared by the two kernels of the linear layer (linear.cu: any shape;
-// linear_pair.cu: large ones).
+// Parts shared by the kernels of the linear layer (linear.cu: any shape; linear_pair.cu:
+// large ones; linear_few.cu: a few rows).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -185,6 +185,9 @@ struct Product {
 // (the same type and row length, no bias, activation, residual or z).
 float pair_estimate(const Product& p);
 cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s);
+// A few rows (linear_few.cu).
+bool takes_few(const LinearArgs& a);
+cudaError_t launch_few(const LinearArgs& a, cudaStream_t s);
 
 }  // namespace lin
 }  // namespace moe

@@ -352,7 +352,7 @@ def test_norm_empty(m):
 
 # ----------------------------------------------------------------------------- linear
 def _linear_case(m, M, N, K, act="none", dtype="bf16", out="bf16", bias=None, residual=False, keep_z=False, alpha=1.0,
-                 ld_x=0, ld_w=0, ld_y=0, in_place=False):
+                 ld_x=0, ld_w=0, ld_y=0, in_place=False, gradient=True):
     g = gen(M * 7 + N * 3 + K)
     t, yt = DT[dtype], DT[out]
     x = rows(M, K, ld_x or K, t, g)
@@ -373,7 +373,8 @@ def _linear_case(m, M, N, K, act="none", dtype="bf16", out="bf16", bias=None, re
     if keep_z:
         check(z, rz, mag, steps, "z")
     check(y, ref, 1.13 * abs(alpha) * (mag + (8 * (1 + np.abs(rz))) / steps) + np.abs(ref) * 4 / steps, steps, "y")
-    # gradient
+    if not gradient:
+        return
     dy = rows(M, N, ld_y or N, yt, g)
     zin = torch.randn(M, N, generator=g, device=DEV).to(t) if act != "none" else None
     dx = torch.full((M, K), float("nan"), dtype=t, device=DEV)
@@ -394,6 +395,15 @@ def _linear_case(m, M, N, K, act="none", dtype="bf16", out="bf16", bias=None, re
 @pytest.mark.parametrize("N,K", [(128, 64), (1, 8), (129, 72), (256, 1024), (7, 200), (640, 136)])
 def test_linear_sizes(m, M, N, K):
     _linear_case(m, M, N, K, bias="f32", residual=True)
+
+
+# a few rows: one and two columns per warp, columns that do not divide, sums shorter than a warp's reach and longer
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("N,K", [(1, 8), (3, 264), (130, 2048), (301, 1400), (2435, 72), (2433, 1032)])
+@pytest.mark.parametrize("dtype,out,act", [("bf16", "f32", "none"), ("f16", "f16", "silu")])
+def test_linear_few_rows(m, M, N, K, dtype, out, act):
+    _linear_case(m, M, N, K, act=act, dtype=dtype, out=out, bias="f32", residual=True, keep_z=True, alpha=0.5,
+                 ld_x=K + 8, ld_w=K + 16, ld_y=N + 3, gradient=False)  # the forward's own form
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
