@@ -108,7 +108,17 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool takes_few(const LinearArgs& a) { return a.M <= 8; }
+// Measured (us, here / on the tensor cores), for N x K:
+//   1 row   4096 x 4096  7.6 / 10.0;  8192 x 4096 11.6 / 14.9
+//   2 rows  4096 x 4096  8.9 / 10.0;  8192 x 4096 13.1 / 14.9
+//   4 rows  128 x 2048  2.4 / 5.5;  2048 x 2048  3.8 / 5.9;  4096 x 2048  7.2 / 8.0;  4096 x 4096 12.0 / 10.0
+//   8 rows  128 x 2048  3.2 / 5.8;  2048 x 2048  5.6 / 6.0;  3000 x 2048 10.4 / 6.7;  8192 x 64  5.6 / 2.6
+bool takes_few(const LinearArgs& a) {
+  const long long weights = static_cast<long long>(a.N) * a.K;
+  if (a.M <= 2) return true;
+  if (a.M <= 4) return weights <= 1 << 23;
+  return a.M <= 8 && a.N <= 152 * 16 && weights <= 1 << 22;
+}
 
 cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
