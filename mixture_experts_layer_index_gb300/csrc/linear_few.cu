@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) linear_few_kernel(LinearArgs a
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       const int k = k0 + 256 * q;
-      if (k < a.K) {  // K is a multiple of 8
+      if (k < a.K) {  // takes_few: K is a multiple of 8
 #pragma unroll
         for (int c = 0; c < COLS; ++c) wv[q][c] = __ldg(reinterpret_cast<const uint4*>(w[c] + k));
 #pragma unroll
@@ -113,7 +113,10 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
 //   2 rows  4096 x 4096  8.9 / 10.0;  8192 x 4096 13.1 / 14.9
 //   4 rows  128 x 2048  2.4 / 5.5;  2048 x 2048  3.8 / 5.9;  4096 x 2048  7.2 / 8.0;  4096 x 4096 12.0 / 10.0
 //   8 rows  128 x 2048  3.2 / 5.8;  2048 x 2048  5.6 / 6.0;  3000 x 2048 10.4 / 6.7;  8192 x 64  5.6 / 2.6
+// Rows are read in whole parts of eight values, which may not reach into what lies between two
+// rows or behind the last: other K go to the tensor cores, whose TMA boxes end at K.
 bool takes_few(const LinearArgs& a) {
+  if (a.K % 8 != 0) return false;
   const long long weights = static_cast<long long>(a.N) * a.K;
   if (a.M <= 2) return true;
   if (a.M <= 4) return weights <= 1 << 23;

@@ -1,0 +1,28 @@
+"""Edges of the operators around the routed FFN on the GPU: lengths, types, values and
+empty parts at which a call is easily answered wrongly or refused.  Bounds as in
+test_block_ops.py, whose cases and checks are used."""
+import pytest
+
+from tests.test_block_ops import _linear_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def m():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import mixture_experts_layer_index_gb300 as mod
+
+    return mod
+
+
+# sums that end inside 16 bytes, NaN behind them and between the rows
+@pytest.mark.parametrize("M", list(range(1, 10)))
+@pytest.mark.parametrize("K", [1, 3, 100, 1030])
+@pytest.mark.parametrize("N,dtype,out", [(1, "bf16", "bf16"), (130, "f16", "f16"), (2435, "bf16", "f32")])
+def test_linear_few_rows_of_any_length(m, M, K, N, dtype, out):
+    ld = (K + 7) // 8 * 8
+    _linear_case(m, M, N, K, dtype=dtype, out=out, bias="f32", residual=True, keep_z=True, alpha=0.5, ld_x=ld, ld_w=ld + 8,
+                 ld_y=N + 3, gradient=False)
