@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) linear_few_kernel(LinearArgs a
   const size_t at = static_cast<size_t>(r) * a.ld_y + n;
   if (a.residual) y += load_as_f32(a.residual, a.out_dtype, at);
   if (a.out_dtype == MOE_DTYPE_F32) static_cast<float*>(a.y)[at] = y;
-  else static_cast<T*>(a.y)[at] = as_type<T>(y);
+  else if (a.out_dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(y);
+  else static_cast<__half*>(a.y)[at] = __float2half_rn(y);
 }
 
 template <typename T, int ROWS, int COLS>

@@ -26,3 +26,11 @@ def test_linear_few_rows_of_any_length(m, M, K, N, dtype, out):
     ld = (K + 7) // 8 * 8
     _linear_case(m, M, N, K, dtype=dtype, out=out, bias="f32", residual=True, keep_z=True, alpha=0.5, ld_x=ld, ld_w=ld + 8,
                  ld_y=N + 3, gradient=False)
+
+
+# rows of few products in a 16-bit type that is not the operands'
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("dtype,out", [("f16", "bf16"), ("bf16", "f16")])
+@pytest.mark.parametrize("N,K", [(130, 264), (2435, 72)])
+def test_linear_few_rows_to_the_other_16_bit_type(m, M, dtype, out, N, K):
+    _linear_case(m, M, N, K, "silu", dtype, out, "f32", residual=True, keep_z=True, alpha=0.5, ld_y=N + 3, gradient=False)
