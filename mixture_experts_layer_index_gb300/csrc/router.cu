@@ -37,6 +37,9 @@ namespace moe {
 namespace {
 
 constexpr int kRouterWarps = 8;
+// Warps of a forward block: two lanes per row keep 16 rows per warp in shared memory, whose
+// ids, keys and group ranks for eight warps would pass the 48 KB that a block has unasked.
+__host__ __device__ constexpr int router_warps(int sub) { return sub == 2 ? kRouterWarps / 2 : kRouterWarps; }
 constexpr int kFewWarps = 4 * 152;  // below: a warp per row leaves no scheduler without one
 
 template <typename ST>
@@ -137,19 +140,20 @@ __device__ __forceinline__ void load_bias(float (&b)[VPL], const float* __restri
 // (no such expert, group not kept, already taken), which fmaxf passes over and no
 // comparison matches.  Equal keys: the lowest lane holds the lowest ids.
 template <int VPL, int SUB, typename ST>
-__global__ void __launch_bounds__(kRouterWarps * 32) route_ex_kernel(const ST* __restrict__ scores, RouteArgs a) {
+__global__ void __launch_bounds__(router_warps(SUB) * 32) route_ex_kernel(const ST* __restrict__ scores, RouteArgs a) {
   constexpr int TOKENS = 32 / SUB;  // per warp
-  __shared__ int s_ids[kRouterWarps][TOKENS][kMaxK];
+  constexpr int WARPS = router_warps(SUB);
+  __shared__ int s_ids[WARPS][TOKENS][kMaxK];
   // group limits only: per token VPL x SUB ranking values, one word of padding for each
   // VPL, and the ranks of up to 32 groups
   extern __shared__ float s_rows[];
   constexpr int PITCH = SUB * (VPL + 1), GPITCH = 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = lane / SUB, sub = lane & (SUB - 1);
-  const int t = (blockIdx.x * kRouterWarps + warp) * TOKENS + tok;
+  const int t = (blockIdx.x * WARPS + warp) * TOKENS + tok;
   dep_wait();
   dep_launch();
-  if ((blockIdx.x * kRouterWarps + warp) * TOKENS >= a.T) return;  // no block-wide barrier below
+  if ((blockIdx.x * WARPS + warp) * TOKENS >= a.T) return;  // no block-wide barrier below
   const bool mine = t < a.T;  // a warp's last tokens may be missing: they shadow token T - 1
   const ST* row = scores + static_cast<size_t>(mine ? t : a.T - 1) * a.ld;
   const int E = a.E, k = a.k, e0 = sub * VPL;
@@ -422,11 +426,13 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
 
 template <int VPL, int SUB, typename ST>
 cudaError_t route_ex_of(const ST* scores, RouteArgs a, cudaStream_t s) {
-  constexpr int TOKENS = 32 / SUB * kRouterWarps;  // per block
-  const size_t smem = a.n_group > 1 ? TOKENS * (SUB * (VPL + 1) + 32) * sizeof(float) : 0;  // at most 37 KB
+  constexpr int TOKENS = 32 / SUB * router_warps(SUB);  // per block
+  constexpr size_t kGroupBytes = TOKENS * (SUB * (VPL + 1) + 32) * sizeof(float);
+  static_assert(kGroupBytes + TOKENS * kMaxK * sizeof(int) <= 48 * 1024, "dynamic and static shared memory of a block");
+  const size_t smem = a.n_group > 1 ? kGroupBytes : 0;
   a.vec = a.ld % (16 / sizeof(ST)) == 0 && a.E % (16 / sizeof(ST)) == 0 && reinterpret_cast<uintptr_t>(scores) % 16 == 0;
   a.bias_vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-  return launch_dependent(route_ex_kernel<VPL, SUB, ST>, dim3((a.T + TOKENS - 1) / TOKENS), dim3(kRouterWarps * 32),
+  return launch_dependent(route_ex_kernel<VPL, SUB, ST>, dim3((a.T + TOKENS - 1) / TOKENS), dim3(router_warps(SUB) * 32),
                           smem, s, scores, a);
 }
 

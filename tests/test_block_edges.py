@@ -2,8 +2,9 @@
 empty parts at which a call is easily answered wrongly or refused.  Bounds as in
 test_block_ops.py, whose cases and checks are used."""
 import pytest
+import torch
 
-from tests.test_block_ops import _linear_case
+from tests.test_block_ops import DEV, _linear_case, _route, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +35,12 @@ def test_linear_few_rows_of_any_length(m, M, K, N, dtype, out):
 @pytest.mark.parametrize("N,K", [(130, 264), (2435, 72)])
 def test_linear_few_rows_to_the_other_16_bit_type(m, M, dtype, out, N, K):
     _linear_case(m, M, N, K, "silu", dtype, out, "f32", residual=True, keep_z=True, alpha=0.5, ld_y=N + 3, gradient=False)
+
+
+# groups of few experts: two lanes take a row once there are many
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(8, 4, 2, 3), (24, 3, 2, 6), (32, 8, 4, 8), (33, 3, 2, 4)])
+@pytest.mark.parametrize("T", [9727, 9728, 20000])
+@pytest.mark.parametrize("group_best", [1, 2])
+def test_route_groups_of_few_experts(m, E, n_group, topk_group, k, T, group_best):
+    s = torch.randn(T, E, generator=gen(E + T), device=DEV)
+    _route(m, s, k, n_group=n_group, topk_group=topk_group, group_best=group_best)
