@@ -260,7 +260,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull0 + 8 * a, 1);
-      mbar_init(tempty0 + 8 * a, 2 * EPI_WARPS);  // the epilogue warps of both blocks
+      // the epilogue warps of both blocks, and the warps that fetch a residual ahead
+      mbar_init(tempty0 + 8 * a, 2 * (EPI_WARPS + (p.ep.residual ? 1 : 0)));
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -401,9 +402,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 3) {
     // The residual of a tile is fetched into L2 while the tile before it is finished, so
-    // that the epilogue's loads do not wait for memory.
+    // that the epilogue's loads do not wait for memory.  Its wait is by parity like the
+    // epilogue's, so it too says when it has seen a tile, before which the accumulator is not
+    // filled again: two completions it had not looked at would read as none.
     if (p.ep.residual) {
       const size_t es = p.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+      const uint32_t lead_tempty0 = map_rank(tempty0, 0);
       uint32_t acc = 0, acc_phase = 0;
       int prod, tile;
       for (int i = 0; pair_item(p, pair, npairs, i, prod, tile); ++i) {
@@ -416,7 +420,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (size_t b = 0; b < row_bytes; b += 128) prefetch_l2(row + b);
         }
         int good = 1;
-        if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x650000u);
+        if (lane == 0) {
+          good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x650000u);
+          if (good) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+        }
         if (!__shfl_sync(0xffffffffu, good, 0)) break;
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;

@@ -44,3 +44,12 @@ def test_linear_few_rows_to_the_other_16_bit_type(m, M, dtype, out, N, K):
 def test_route_groups_of_few_experts(m, E, n_group, topk_group, k, T, group_best):
     s = torch.randn(T, E, generator=gen(E + T), device=DEV)
     _route(m, s, k, n_group=n_group, topk_group=topk_group, group_best=group_best)
+
+
+# four and more tiles of 256 x 256 per pair of SMs: both accumulators are filled again and again
+@pytest.mark.parametrize("M,N,K,ld_y", [(8200, 2600, 72, 0), (8200, 2600, 8, 2603)])
+@pytest.mark.parametrize("dtype,out,act", [("bf16", "f32", "silu"), ("f16", "f16", "gelu_tanh"), ("bf16", "bf16", "none")])
+def test_linear_many_tiles_per_pair(m, M, N, K, ld_y, dtype, out, act):
+    _linear_case(m, M, N, K, act, dtype, out, "f32", residual=True, keep_z=act != "none", alpha=0.5, ld_y=ld_y,
+                 gradient=False)
+    _linear_case(m, M, N, K, act, dtype, out, None, residual=True, in_place=True, ld_y=ld_y, gradient=False)
