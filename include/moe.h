@@ -477,9 +477,9 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const void* dh_out, cons
  *   y [M, N] of out_dtype, ld_y (y == residual is allowed)
  *   z [M, N] of dtype, contiguous, or NULL (kept for the gradient of an activation)
  * act: MOE_ACT_GELU is the erf form, MOE_ACT_GELU_TANH the tanh form.
- * K == 0 is INVALID_ARG; M == 0 or N == 0 a no-op.
+ * K == 0 is INVALID_ARG; M == 0 or N == 0 computes nothing and needs no ws.
  * ws: moe_linear_workspace_size(p) bytes, 256-byte aligned: the status word
- * (moe_read_device_status), cleared by the call.
+ * (moe_read_device_status), cleared by the call (by an empty one too, where ws is given).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 typedef enum {
   MOE_ACT_NONE = 0,
@@ -508,9 +508,9 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
  *   dx [M, K] and dw [N, K] of dtype, contiguous;  dbias [N] fp32;  each may be NULL.
  * dz is rounded to dtype for the two products (the tensor cores' operand type; dy
  * itself is read where it already is dz), dbias sums it unrounded in fp32, in a
- * fixed order.  M == 0 writes zeros to dw and dbias.
+ * fixed order.  M == 0 writes zeros to dw and dbias, N == 0 to dx; they need no ws.
  * ws: moe_linear_backward_workspace_size(p) bytes, 256-byte aligned, status word at
- * its head.  Errors: as moe_linear. */
+ * its head, cleared as moe_linear's, whichever outputs are wanted.  Errors: as moe_linear. */
 size_t moe_linear_backward_workspace_size(const moe_linear_problem* p);
 moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, const void* x, const void* w,
                                const void* z, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,

@@ -117,6 +117,12 @@ moe_status check_linear(const moe_linear_problem* p) {
 
 constexpr size_t kHeaderBytes = 256;
 
+// An empty problem needs no workspace, but where one is given its status is this call's.
+cudaError_t clear_status(void* ws, size_t ws_bytes, cudaStream_t s) {
+  if (!ws || !aligned(ws, 256) || ws_bytes < kHeaderBytes) return cudaSuccess;
+  return launch_reset_header(static_cast<DeviceHeader*>(ws), s);
+}
+
 struct LinearBackwardLayout {
   size_t partials, dz, total;
 };
@@ -251,7 +257,7 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
                       const void* residual, void* y, void* z, void* ws, size_t ws_bytes, moe_stream_t stream) {
   const moe_status st = check_linear(p);
   if (st != MOE_OK) return st;
-  if (p->M == 0 || p->N == 0) return MOE_OK;
+  if (p->M == 0 || p->N == 0) return from_cuda(clear_status(ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream)));
   if (!x || !w || !y || !aligned(x, 16) || !aligned(w, 16) || !fits(y, p->out_dtype) || !fits(z, p->dtype) ||
       !fits(residual, p->out_dtype) || !fits(bias, p->bias_dtype))
     return MOE_ERR_INVALID_ARG;
@@ -290,8 +296,8 @@ moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, cons
   if (!fits(dx, p->dtype) || !fits(dw, p->dtype) || !aligned(dbias, 4)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (p->M == 0 || p->N == 0) {  // empty sums
-    cudaError_t e = cudaSuccess;
-    if (dx && p->M) e = cudaMemsetAsync(dx, 0, static_cast<size_t>(p->M) * p->K * 2, s);
+    cudaError_t e = clear_status(ws, ws_bytes, s);
+    if (e == cudaSuccess && dx && p->M) e = cudaMemsetAsync(dx, 0, static_cast<size_t>(p->M) * p->K * 2, s);
     if (e == cudaSuccess && dw && p->N) e = cudaMemsetAsync(dw, 0, static_cast<size_t>(p->N) * p->K * 2, s);
     if (e == cudaSuccess && dbias && p->N) e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(p->N) * 4, s);
     return from_cuda(e);

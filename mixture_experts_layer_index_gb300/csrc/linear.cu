@@ -683,7 +683,9 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
   using namespace lin;
   const bool direct = linear_dz_is_dy(a);
   const bool products = a.dx || a.dw;
-  cudaError_t err = cudaSuccess;
+  // the first product clears the status word; without one nobody else does
+  cudaError_t err = products ? cudaSuccess : launch_reset_header(a.hdr, s);
+  if (err != cudaSuccess) return err;
   if ((!direct && products) || a.dbias) {
     DzArgs d{};
     d.M = a.M;

@@ -1,10 +1,11 @@
 """Edges of the operators around the routed FFN on the GPU: lengths, types, values and
 empty parts at which a call is easily answered wrongly or refused.  Bounds as in
 test_block_ops.py, whose cases and checks are used."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_block_ops import DEV, _linear_case, _route, gen
+from tests.test_block_ops import DEV, _linear_case, _route, check, f64, gen, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,30 @@ def test_linear_many_tiles_per_pair(m, M, N, K, ld_y, dtype, out, act):
     _linear_case(m, M, N, K, act, dtype, out, "f32", residual=True, keep_z=act != "none", alpha=0.5, ld_y=ld_y,
                  gradient=False)
     _linear_case(m, M, N, K, act, dtype, out, None, residual=True, in_place=True, ld_y=ld_y, gradient=False)
+
+
+# a status word that nobody else writes
+@pytest.mark.parametrize("M,N", [(5, 24), (300, 40), (0, 24), (5, 0)])
+@pytest.mark.parametrize("wanted", ["dbias", "nothing", "all"])
+def test_linear_backward_clears_its_status(m, M, N, wanted):
+    p = m.linear_problem(M, N, 64)
+    x, w, dy = (rows(max(n, 1), k, k, torch.bfloat16, gen(1))[:n] for n, k in ((M, 64), (N, 64), (M, max(N, 1))))
+    out = dict(dbias=torch.full((N,), 7.0, device=DEV)) if wanted == "dbias" else {}
+    if wanted == "all":
+        out = dict(dx=torch.ones(M, 64, dtype=torch.bfloat16, device=DEV),
+                   dw=torch.ones(N, 64, dtype=torch.bfloat16, device=DEV), dbias=torch.full((N,), 7.0, device=DEV))
+    ws = torch.full((max(m.moe_linear_backward_workspace_size(p), 256),), 255, dtype=torch.uint8, device=DEV)
+    m.moe_linear_backward(p, dy, x, w, None, out.get("dx"), out.get("dw"), out.get("dbias"), ws)
+    assert m.moe_read_device_status(ws) == m.MOE_OK
+    if "dbias" in out and M and N:
+        check(out["dbias"], f64(dy).sum(0), np.abs(f64(dy)).sum(0), 64 + 40, "dbias")
+    elif "dbias" in out:
+        assert not bool(out["dbias"].any())
+
+
+@pytest.mark.parametrize("M,N", [(0, 24), (5, 0)])
+def test_linear_of_nothing_clears_its_status(m, M, N):
+    p = m.linear_problem(M, N, 64)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device=DEV)
+    m.moe_linear(p, None, None, None, None, None, None, ws)
+    assert m.moe_read_device_status(ws) == m.MOE_OK
