@@ -350,9 +350,9 @@ def moe_forward_views(p: moe_problem, ws, ws_bytes=None) -> moe_views:
     return v
 
 
-def _rows(t, name: str = "tensor") -> Optional[int]:
-    """Device pointer of a CUDA tensor whose rows are contiguous (the row stride is the
-    descriptor's ld); None -> NULL; ints pass through."""
+def _rows(t, name: str, width: int, ld: int = 0) -> Optional[int]:
+    """Device pointer of a CUDA tensor of rows of `width` values, `ld` elements apart (0: `width`) as the
+    descriptor says; None -> NULL; ints pass through."""
     if t is None or type(t) is int:
         return t
     try:
@@ -363,9 +363,22 @@ def _rows(t, name: str = "tensor") -> Optional[int]:
         raise
     if not on_device:
         raise ValueError(f"{name}: device tensor expected")
-    if not t.is_contiguous() and t.stride(-1) != 1:
-        raise ValueError(f"{name}: rows must be contiguous")
+    if not t.is_contiguous() or (ld != 0 and ld != width):
+        _check_rows(t, name, ld or width)
     return t.data_ptr()
+
+
+def _check_rows(t, name: str, ld: int) -> None:
+    """Rows of t lie ld elements apart (over all its leading dimensions; a 1-D tensor is taken as it is)."""
+    shape, stride = t.shape, t.stride()
+    if 0 in shape:
+        return
+    if len(shape) and shape[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n > 1 and s != ld:
+            raise ValueError(f"{name}: rows lie {s} elements apart, the descriptor says {ld}")
+        ld *= n
 
 
 def route_options(score="softmax", bias=None, n_group=1, topk_group=1, group_best=1, renormalise=True, scale=1.0,
@@ -378,13 +391,13 @@ def route_options(score="softmax", bias=None, n_group=1, topk_group=1, group_bes
 
 def moe_route_ex(opt: moe_route_options, scores, T, E, k, ids, w, stream=None) -> None:
     """Routing with a score function, selection bias, expert groups and renormalised weights."""
-    _check(lib().moe_route_ex(opt, _rows(scores), T, E, k, _ptr(ids), _ptr(w), _stream(stream)), "moe_route_ex")
+    _check(lib().moe_route_ex(opt, _rows(scores, "scores", E, opt.ld), T, E, k, _ptr(ids), _ptr(w), _stream(stream)), "moe_route_ex")
 
 
 def moe_route_backward(opt: moe_route_options, scores, T, E, k, ids, dw, dscores, stream=None) -> None:
     """Gradient of moe_route_ex's weights into the scores."""
-    _check(lib().moe_route_backward(opt, _rows(scores), T, E, k, _ptr(ids), _ptr(dw), _rows(dscores),
-                                    _stream(stream)), "moe_route_backward")
+    _check(lib().moe_route_backward(opt, _rows(scores, "scores", E, opt.ld), T, E, k, _ptr(ids), _ptr(dw),
+                                    _rows(dscores, "dscores", E, opt.ld_grad), _stream(stream)), "moe_route_backward")
 
 
 def norm_problem(T, H, post_norm=MOE_NORM_RMS, pre_norm=MOE_NORM_RMS, gate=MOE_GATE_NONE, h_dtype=MOE_DTYPE_BF16,
@@ -393,11 +406,19 @@ def norm_problem(T, H, post_norm=MOE_NORM_RMS, pre_norm=MOE_NORM_RMS, gate=MOE_G
     return moe_norm_problem(T, H, post_norm, pre_norm, gate, h_dtype, o_dtype, w_dtype, eps, alpha, beta, ld_h, ld_o)
 
 
+def _gate(p: moe_norm_problem, t, name: str) -> Optional[int]:
+    """A gate or its gradient: rows like o's, or a vector."""
+    return _rows(t, name, p.H, p.ld_o) if p.gate == MOE_GATE_FULL else _ptr(t)
+
+
 def moe_norm_forward(p: moe_norm_problem, h, o, gate, w_post, b_post, w_pre, b_pre, h_out, x_out,
                      stream=None) -> None:
     """h_out = beta h + alpha gate N_post(o), x_out = N_pre(h_out)."""
-    _check(lib().moe_norm_forward(p, _rows(h), _rows(o), _rows(gate), _ptr(w_post), _ptr(b_post), _ptr(w_pre),
-                                  _ptr(b_pre), _rows(h_out), _rows(x_out), _stream(stream)), "moe_norm_forward")
+    H, ld_h, ld_o = p.H, p.ld_h, p.ld_o
+    _check(lib().moe_norm_forward(p, _rows(h, "h", H, ld_h), _rows(o, "o", H, ld_o), _gate(p, gate, "gate"),
+                                  _ptr(w_post), _ptr(b_post), _ptr(w_pre), _ptr(b_pre),
+                                  _rows(h_out, "h_out", H, ld_h), _rows(x_out, "x_out", H, ld_o), _stream(stream)),
+           "moe_norm_forward")
 
 
 def moe_norm_backward_workspace_size(p: moe_norm_problem) -> int:
@@ -408,10 +429,12 @@ def moe_norm_backward(p: moe_norm_problem, dh_out, dx_out, h_out, o, gate, w_pos
                       dw_post, db_post, dw_pre, db_pre, ws, ws_bytes=None, stream=None) -> None:
     """Gradient of moe_norm_forward; outputs given as None are left out."""
     nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    _check(lib().moe_norm_backward(p, _rows(dh_out), _rows(dx_out), _rows(h_out), _rows(o), _rows(gate),
-                                   _ptr(w_post), _ptr(b_post), _ptr(w_pre), _rows(dh), _rows(d_o), _rows(dgate),
-                                   _ptr(dw_post), _ptr(db_post), _ptr(dw_pre), _ptr(db_pre), _ptr(ws), nb,
-                                   _stream(stream)), "moe_norm_backward")
+    H, ld_h, ld_o = p.H, p.ld_h, p.ld_o
+    _check(lib().moe_norm_backward(p, _rows(dh_out, "dh_out", H, ld_h), _rows(dx_out, "dx_out", H, ld_o),
+                                   _rows(h_out, "h_out", H, ld_h), _rows(o, "o", H, ld_o), _gate(p, gate, "gate"),
+                                   _ptr(w_post), _ptr(b_post), _ptr(w_pre), _rows(dh, "dh", H, ld_h),
+                                   _rows(d_o, "d_o", H, ld_o), _gate(p, dgate, "dgate"), _ptr(dw_post), _ptr(db_post),
+                                   _ptr(dw_pre), _ptr(db_pre), _ptr(ws), nb, _stream(stream)), "moe_norm_backward")
 
 
 def linear_problem(M, N, K, dtype=MOE_DTYPE_BF16, out_dtype=MOE_DTYPE_BF16, bias_dtype=MOE_DTYPE_F32,
@@ -426,7 +449,9 @@ def moe_linear_workspace_size(p: moe_linear_problem) -> int:
 def moe_linear(p: moe_linear_problem, x, w, bias, residual, y, z, ws, ws_bytes=None, stream=None) -> None:
     """y = alpha act(x w^T + bias) + residual; z keeps the pre-activation."""
     nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    _check(lib().moe_linear(p, _rows(x), _rows(w), _ptr(bias), _rows(residual), _rows(y), _ptr(z), _ptr(ws), nb,
+    N, K, ld_y = p.N, p.K, p.ld_y
+    _check(lib().moe_linear(p, _rows(x, "x", K, p.ld_x), _rows(w, "w", K, p.ld_w), _ptr(bias),
+                            _rows(residual, "residual", N, ld_y), _rows(y, "y", N, ld_y), _ptr(z), _ptr(ws), nb,
                             _stream(stream)), "moe_linear")
 
 
@@ -437,8 +462,10 @@ def moe_linear_backward_workspace_size(p: moe_linear_problem) -> int:
 def moe_linear_backward(p: moe_linear_problem, dy, x, w, z, dx, dw, dbias, ws, ws_bytes=None, stream=None) -> None:
     """Gradient of moe_linear; outputs given as None are left out."""
     nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
-    _check(lib().moe_linear_backward(p, _rows(dy), _rows(x), _rows(w), _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias),
-                                     _ptr(ws), nb, _stream(stream)), "moe_linear_backward")
+    K = p.K
+    _check(lib().moe_linear_backward(p, _rows(dy, "dy", p.N, p.ld_y), _rows(x, "x", K, p.ld_x), _rows(w, "w", K, p.ld_w),
+                                     _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(ws), nb, _stream(stream)),
+           "moe_linear_backward")
 
 
 def moe_read_device_status(ws, stream=None) -> int:
