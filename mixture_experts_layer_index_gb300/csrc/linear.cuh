@@ -63,9 +63,16 @@ __device__ __forceinline__ float normal_tail(float x, float& e) {
 // 2 u of the tanh form: (1 + tanh u) / 2 = sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float gelu_tanh_2u(float z) { return 1.59576912f * z * fmaf(0.044715f * z, z, 1.0f); }
 
+// max(z, 0) that keeps a NaN, which fmaxf drops.
+__device__ __forceinline__ float relu(float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+  return r;
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
-    case MOE_ACT_RELU: return fmaxf(z, 0.0f);
+    case MOE_ACT_RELU: return relu(z);
     case MOE_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
     case MOE_ACT_GELU: {
       float e;

@@ -5,9 +5,11 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_block_ops import DEV, _linear_case, _route, check, f64, gen, rows
+from oracle import blocks as B
+from tests.test_block_ops import DEV, DT, STEP, _linear_case, _route, check, code, f64, gen, rows
 
 pytestmark = pytest.mark.gpu
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
 
 
 @pytest.fixture(scope="module")
@@ -18,6 +20,10 @@ def m():
     import mixture_experts_layer_index_gb300 as mod
 
     return mod
+
+
+def act_code(m, name):
+    return getattr(m, "MOE_ACT_" + name.upper())
 
 
 # sums that end inside 16 bytes, NaN behind them and between the rows
@@ -81,3 +87,46 @@ def test_linear_of_nothing_clears_its_status(m, M, N):
     ws = torch.full((256,), 255, dtype=torch.uint8, device=DEV)
     m.moe_linear(p, None, None, None, None, None, None, ws)
     assert m.moe_read_device_status(ws) == m.MOE_OK
+
+
+SPECIAL = [float("nan"), float("inf"), -float("inf"), -0.0, 0.0, 1e-30, -1e-30, 6e4, -6e4, 90.0, -90.0, -87.5, 20.0, -20.0,
+           1.0, -1.278]
+WIDE = [1e19, -1e19, 1e20, -1e20, 3e38, -3e38]  # squares and cubes pass the largest fp32
+
+
+def same_values(got, ref, bound):
+    """NaN where ref is NaN, infinities of the same sign, else within the bound."""
+    got = f64(got)
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), (got, ref)
+    assert np.array_equal(np.isinf(got), np.isinf(ref)) and np.array_equal(np.sign(got[np.isinf(got)]), np.sign(ref[np.isinf(ref)]))
+    fine = np.isfinite(ref)
+    assert np.all(np.abs(got[fine] - ref[fine]) <= bound[fine]), (got, ref)
+
+
+# z = x * 1 holds each special value itself: a few rows, the tensor cores' tiles, and pairs of tiles
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "gelu"])
+@pytest.mark.parametrize("M,N", [(1, 8), (40, 24), (1500, 2056)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_linear_special_values(m, act, M, N, dtype):
+    t = DT[dtype]
+    special = SPECIAL + (WIDE if dtype == "bf16" else [])
+    v = torch.tensor(special, dtype=torch.float32, device=DEV).to(t)
+    x = torch.zeros(M, 8, dtype=t, device=DEV)
+    w = torch.zeros(N, 8, dtype=t, device=DEV)
+    w[:, 0] = 1
+    p = m.linear_problem(M, N, 8, code(m, dtype), m.MOE_DTYPE_F32, act=act_code(m, act))
+    y = torch.empty(M, N, device=DEV)
+    ws = torch.empty(m.moe_linear_workspace_size(p), dtype=torch.uint8, device=DEV)
+    for i in range(0, len(special), M):
+        n = min(M, len(special) - i)
+        x.zero_()
+        x[:n, 0] = v[i:i + n]
+        m.moe_linear(p, x, w, None, None, y, None, ws)
+        z = f64(v[i:i + n])
+        with np.errstate(all="ignore"):
+            ref = B.act(z, act)
+        # an activation's error is relative to its argument (erf 1.5e-7, the others a few fp32 roundings)
+        bound = 16 * STEP * np.where(np.isfinite(z), np.abs(z), 0.0) + 2.0 ** -126
+        same_values(y[:n, 0], ref, bound)
+        # the rows of w are the same, so every column is
+        assert torch.equal(y[:n].nan_to_num(nan=7.0), y[:n, :1].nan_to_num(nan=7.0).expand(n, N))
