@@ -76,8 +76,8 @@ __device__ __forceinline__ float act_value(float z, int act) {
     case MOE_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
     case MOE_ACT_GELU: {
       float e;
-      const float tail = z * normal_tail(fabsf(z), e);
-      return z > 0.0f ? z - tail : tail;
+      const float tail = normal_tail(fabsf(z), e);
+      return z * (z > 0.0f ? 1.0f - tail : tail);  // z - z tail would be infinity - NaN at z = infinity
     }
     case MOE_ACT_GELU_TANH: return z * fast_sigmoid(gelu_tanh_2u(z));
     default: return z;
