@@ -119,8 +119,9 @@ __device__ __forceinline__ float act_grad(float z, int act) {
       return fmaf(0.39894228f * z, e, z > 0.0f ? 1.0f - tail : tail);
     }
     case MOE_ACT_GELU_TANH: {
-      const float s = fast_sigmoid(gelu_tanh_2u(z));
-      return s * fmaf(z * (1.0f - s), 1.59576912f * fmaf(0.134145f * z, z, 1.0f), 1.0f);
+      // s + s (1 - s) z 2u'(z), the vanishing factor first: z^2 alone passes fp32's range
+      const float s = fast_sigmoid(gelu_tanh_2u(z)), d = z * (s * (1.0f - s));
+      return fmaf(1.59576912f, fmaf(0.134145f * z, z * d, d), s);
     }
     default: return 1.0f;
   }

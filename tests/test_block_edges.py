@@ -130,3 +130,22 @@ def test_linear_special_values(m, act, M, N, dtype):
         same_values(y[:n, 0], ref, bound)
         # the rows of w are the same, so every column is
         assert torch.equal(y[:n].nan_to_num(nan=7.0), y[:n, :1].nan_to_num(nan=7.0).expand(n, N))
+
+
+# the slope at each special value, through dbias of a single row (fp32, unrounded)
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_linear_slope_of_special_values(m, act, dtype):
+    t = DT[dtype]
+    special = SPECIAL + (WIDE if dtype == "bf16" else [])
+    z = torch.tensor([special], dtype=torch.float32, device=DEV).to(t)
+    N = len(special)
+    p = m.linear_problem(1, N, 8, code(m, dtype), m.MOE_DTYPE_F32, act=act_code(m, act))
+    dy = torch.full((1, N), 2.0, device=DEV)
+    db = torch.full((N,), 9.0, device=DEV)
+    ws = torch.empty(m.moe_linear_backward_workspace_size(p), dtype=torch.uint8, device=DEV)
+    m.moe_linear_backward(p, dy, None, None, z, None, None, db, ws)
+    with np.errstate(all="ignore"):
+        ref = 2.0 * B.act_grad(f64(z)[0], act)
+    # absolute: a slope is a sum of terms of size 1 and z (1 - s), of at most 1.3
+    same_values(db, ref, np.full(N, 2 * 16 * STEP))
