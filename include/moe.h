@@ -265,8 +265,9 @@ moe_status moe_forward_ex(const moe_problem* p, const moe_forward_options* opt, 
  * moe_route or moe_route_ex writes it:
  *   ids [T, k] int32, w [T, k] fp32: y[t] = sum_j w[t, j] * FFN_{ids[t, j]}(x_t) + shared
  * Weights are used as they are; views' ids and w hold copies.  An id outside [0, E)
- * is recorded as MOE_ERR_DEVICE_BOUNDS in the status word at the head of ws and its
- * route adds nothing to y.  Everything else as moe_forward_ex. */
+ * is recorded as MOE_ERR_DEVICE_BOUNDS in the status word at the head of ws; its route
+ * is not computed, adds nothing to y (its copy of w is 0) and has no part in the
+ * per-tensor scale of h.  Everything else as moe_forward_ex. */
 moe_status moe_forward_routed(const moe_problem* p, const moe_forward_options* opt, const void* x, const int32_t* ids,
                               const float* w, const void* w1, const void* w2, const float* w1_scale,
                               const float* w2_scale, void* y, void* ws, size_t ws_bytes, moe_stream_t stream);

@@ -109,20 +109,24 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ rd_prep
-// The given routing of tokens handled by this block's warps: ids into s_ids.  An id
-// outside [0, E) is replaced by expert 0 with weight 0, so that it adds nothing; the
-// block that owns the outputs (hdr given) records it and writes ids and weights.
+// The given routing of all tokens into s_ids, -1 for an id outside [0, E): such a route is
+// on no expert's list, so no kernel computes it.  The block that owns the outputs (hdr given)
+// records it and copies ids and weights, the weight of such a route as 0.
 __device__ __forceinline__ void take_routes(const DecodeArgs& a, int* s_ids, DeviceHeader* hdr) {
   for (int r = threadIdx.x; r < a.R; r += blockDim.x) {
     const int e = a.ids_in[r];
     const bool ok = e >= 0 && e < a.E;
-    s_ids[r] = ok ? e : 0;
+    s_ids[r] = ok ? e : -1;
     if (hdr) {
       if (!ok) record_status(hdr, kStatusBounds, static_cast<unsigned int>(r));
-      a.ids[r] = s_ids[r];
+      a.ids[r] = e;
       a.w[r] = ok ? a.w_in[r] : 0.0f;
     }
   }
+}
+// Whether route r goes to no expert (a given routing only).
+__device__ __forceinline__ bool no_expert(const DecodeArgs& a, int r) {
+  return a.ids_in && (a.ids[r] < 0 || a.ids[r] >= a.E);
 }
 
 template <int MAXV>
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(1024) rd_prep_kernel(DecodeArgs a) {
       int run = 0;
       for (int c = 0; c < R && run < maxp; c += 32) {
         const int r = c + lane;
-        const bool valid = r < R;
+        const bool valid = r < R && s_ids[r] >= 0;
         const int e = valid ? s_ids[r] : 0;
         const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1 - lane);
         const bool first = valid && lane == __ffs(peers) - 1 && !((s_seen[e >> 5] >> (e & 31)) & 1u);
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(1024) rd_prep_kernel(DecodeArgs a) {
     int run = 0;
     for (int c = 0; c < R; c += 32) {
       const int r = c + lane;
-      const bool valid = r < R;
+      const bool valid = r < R && s_ids[r] >= 0;
       const int e = valid ? s_ids[r] : 0;
       const unsigned peers = __match_any_sync(0xffffffffu, valid ? e : -1 - lane);
       const int leader = __ffs(peers) - 1;
@@ -285,7 +289,8 @@ __global__ void __launch_bounds__(1024) rd_prep_kernel(DecodeArgs a) {
       gacc += __shfl_sync(0xffffffffu, gincl, 31);
     }
     __syncwarp();
-    for (int r = lane; r < R; r += 32) uv.routes()[s_off[s_u[r]] + s_pos[r]] = r;
+    for (int r = lane; r < R; r += 32)
+      if (s_ids[r] >= 0) uv.routes()[s_off[s_u[r]] + s_pos[r]] = r;
     if (lane == 0) {
       uv.U()[0] = run;
       uv.off()[run] = acc;
@@ -741,11 +746,15 @@ __global__ void __launch_bounds__(256) rd_reduce_tensor_kernel(DecodeArgs a) {
   float av = 0.0f;
   if (idx < a.R * I) {
     const int r = idx / I, i = idx - (idx / I) * I;
-    float g, u;
-    sum_splits(a.part, a.splits, a.R, twoI, I, r, i, g, u);
-    const float sc = a.sx[0] * __ldg(a.w1_scale + a.ids[r]);
-    av = silu_mul(sc * g, sc * u);
-    static_cast<float*>(a.act)[idx] = av;
+    if (no_expert(a, r)) {
+      for (int c = i; c < a.H; c += I) a.o[static_cast<size_t>(r) * a.H + c] = 0.0f;  // no item writes this row
+    } else {
+      float g, u;
+      sum_splits(a.part, a.splits, a.R, twoI, I, r, i, g, u);
+      const float sc = a.sx[0] * __ldg(a.w1_scale + a.ids[r]);
+      av = silu_mul(sc * g, sc * u);
+      static_cast<float*>(a.act)[idx] = av;
+    }
   }
   const float m = warp_max(fabsf(av));
   if ((threadIdx.x & 31) == 0 && m > 0.0f) atomicMax(&a.hdr->amax_h, __float_as_uint(m));
@@ -760,6 +769,10 @@ __global__ void __launch_bounds__(256) rd_reduce_block_kernel(DecodeArgs a) {
   const int I = a.I, twoI = 2 * I, ngi = (I + 127) / 128;
   if (gw >= a.R * ngi) return;
   const int r = gw / ngi, G = gw - (gw / ngi) * ngi;
+  if (no_expert(a, r)) {
+    for (int c = G * 32 + lane; c < a.H; c += ngi * 32) a.o[static_cast<size_t>(r) * a.H + c] = 0.0f;  // no item writes this row
+    return;
+  }
   const int col = G * 128 + lane * 4;
   const bool valid = col < I;
   float av[4] = {0.f, 0.f, 0.f, 0.f}, g[4], u[4];

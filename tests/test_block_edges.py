@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import workloads as W
 from oracle import blocks as B
 from tests.test_block_ops import DEV, DT, STEP, _linear_case, _route, check, code, f64, gen, rows
 
@@ -149,3 +150,41 @@ def test_linear_slope_of_special_values(m, act, dtype):
         ref = 2.0 * B.act_grad(f64(z)[0], act)
     # absolute: a slope is a sum of terms of size 1 and z (1 - s), of at most 1.3
     same_values(db, ref, np.full(N, 2 * 16 * STEP))
+
+
+# a route to no expert has no part in y, whatever the experts hold, nor in the scale of the others
+@pytest.mark.parametrize("quant,path", [("bf16", "grouped"), ("fp8_tensor", "grouped"), ("fp8_tensor", "route_direct"),
+                                        ("fp8_block", "grouped"), ("fp8_block", "route_direct"), ("mxfp8", "grouped")])
+@pytest.mark.parametrize("poison", [float("inf"), 1e4])
+def test_a_route_to_no_expert_adds_nothing(m, quant, path, poison):
+    T, E, k, H, I = 6, 16, 4, 256, 128
+    d = {n: (None if v is None else v.to(DEV)) for n, v in W.make_inputs(W.Workload("t", T, E, k, H, I, quant, 5)).items()}
+    ids = torch.stack([torch.randperm(E - 1, generator=torch.Generator().manual_seed(t))[:k] + 1 for t in range(T)])
+    ids = ids.to(torch.int32).to(DEV)  # nobody asks for expert 0 ...
+    w = torch.rand(T, k, generator=gen(2), device=DEV)
+    if quant == "bf16":                # ... whose values are out of all proportion
+        d["w1"][0] = poison
+    else:
+        d["w1_scale"][0] = poison if quant != "mxfp8" else 254 if poison == float("inf") else 140  # powers of two
+    p = m.problem(T, E, k, H, I, quant, {"grouped": m.MOE_PATH_GROUPED, "route_direct": m.MOE_PATH_ROUTE_DIRECT}[path])
+    ws = torch.full((m.moe_workspace_size(p),), 255, dtype=torch.uint8, device=DEV)
+
+    def run(i, wt):
+        y = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+        m.moe_forward_routed(p, None, d["x"], i, wt, d["w1"], d["w2"], d["w1_scale"], d["w2_scale"], y, ws)
+        return y, m.moe_read_device_status(ws)
+
+    bad, twin, w0 = ids.clone(), ids.clone(), w.clone()
+    for t, j, e in ((2, 1, E), (3, 0, -3), (5, 3, 1 << 30), (5, 2, -1)):
+        bad[t, j], twin[t, j], w0[t, j] = e, ids[t, (j + 2) % k if t != 5 else 0], 0.0
+    y, st = run(bad, w)
+    assert st == m.MOE_ERR_DEVICE_BOUNDS
+    # the same routes twice for a token, the second time with weight 0: the same h, so the same scales
+    ref, st = run(twin, w0)
+    assert st == m.MOE_OK and bool(torch.isfinite(ref).all())
+    assert torch.equal(y, ref)
+    v = m.moe_forward_views(p, ws)
+    y, _ = run(torch.full_like(ids, -1), w)
+    assert not bool(y.any())
+    at = v.ids - ws.data_ptr()
+    assert bool((ws[at:at + T * k * 4].view(torch.int32) == -1).all())
