@@ -432,7 +432,7 @@ cudaError_t route_ex_of(const ST* scores, RouteArgs a, cudaStream_t s) {
   const size_t smem = a.n_group > 1 ? kGroupBytes : 0;
   a.vec = a.ld % (16 / sizeof(ST)) == 0 && a.E % (16 / sizeof(ST)) == 0 && reinterpret_cast<uintptr_t>(scores) % 16 == 0;
   a.bias_vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-  return launch_dependent(route_ex_kernel<VPL, SUB, ST>, dim3((a.T + TOKENS - 1) / TOKENS), dim3(router_warps(SUB) * 32),
+  return launch_dependent(route_ex_kernel<VPL, SUB, ST>, dim3((a.T - 1) / TOKENS + 1), dim3(router_warps(SUB) * 32),
                           smem, s, scores, a);
 }
 
@@ -465,7 +465,7 @@ cudaError_t route_backward_of(const ST* sc, RouteArgs a, const int32_t* ids, con
   constexpr int PER = 16 / sizeof(ST);
   a.vec = a.ld % PER == 0 && a.E % PER == 0 && reinterpret_cast<uintptr_t>(sc) % 16 == 0;
   const bool vec_d = ld_d % PER == 0 && a.E % PER == 0 && reinterpret_cast<uintptr_t>(ds) % 16 == 0;
-  const dim3 grid((a.T + TOKENS - 1) / TOKENS);
+  const dim3 grid((a.T - 1) / TOKENS + 1);
   return launch_dependent(route_backward_kernel<VPL, SUB, ST, WHOLE>, grid, dim3(kRouterWarps * 32), 0, s, sc, ids, dw,
                           ds, a, ld_d, vec_d);
 }

@@ -7,7 +7,7 @@ import torch
 
 import workloads as W
 from oracle import blocks as B
-from tests.test_block_ops import DEV, DT, STEP, _linear_case, _route, check, code, f64, gen, rows
+from tests.test_block_ops import DEV, DT, STEP, _linear_case, _route, _rule, check, code, f64, gen, rows
 
 pytestmark = pytest.mark.gpu
 ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
@@ -188,3 +188,15 @@ def test_a_route_to_no_expert_adds_nothing(m, quant, path, poison):
     assert not bool(y.any())
     at = v.ids - ws.data_ptr()
     assert bool((ws[at:at + T * k * 4].view(torch.int32) == -1).all())
+
+
+def test_route_as_many_tokens_as_there_can_be(m):
+    T = (1 << 31) - 1
+    s = torch.zeros(T, 1, dtype=torch.bfloat16, device=DEV)
+    ids = torch.full((T, 1), -7, dtype=torch.int32, device=DEV)
+    w = torch.zeros(T, 1, device=DEV)
+    m.moe_route_ex(_rule(m, "bf16"), s, T, 1, 1, ids, w)
+    assert int(ids.min()) == 0 and int(ids.max()) == 0 and float(w.min()) == 1.0 and float(w.max()) == 1.0
+    d = torch.ones(T, 1, dtype=torch.bfloat16, device=DEV)
+    m.moe_route_backward(_rule(m, "bf16"), s, T, 1, 1, ids, w, d)
+    assert not bool(d.any())
