@@ -65,7 +65,9 @@ class Block:
             return torch.empty(*shape, dtype=dtype, device=dev)
 
         def scratch(n):
-            return torch.empty(n, dtype=torch.uint8, device=dev)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+            ws[:256].zero_()  # the status word, which a step clears and sets: no error before the first
+            return ws
 
         bf16 = torch.bfloat16
         self.h_out, self.x, self.o_out = (empty(T, H, dtype=bf16) for _ in range(3))
@@ -113,5 +115,5 @@ class Block:
         return out
 
     def status(self, stream=None) -> int:
-        """Device status of the last forward (blocks until it is done)."""
+        """Device status of the last forward, MOE_OK before the first (blocks until it is done)."""
         return moe_read_device_status(self.ws_linear, stream) or moe_read_device_status(self.ws, stream)

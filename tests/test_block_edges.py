@@ -200,3 +200,18 @@ def test_route_as_many_tokens_as_there_can_be(m):
     d = torch.ones(T, 1, dtype=torch.bfloat16, device=DEV)
     m.moe_route_backward(_rule(m, "bf16"), s, T, 1, 1, ids, w, d)
     assert not bool(d.any())
+
+
+def test_a_block_that_never_ran_reports_no_error(m):
+    from mixture_experts_layer_index_gb300.block import Block
+
+    H, E, I = 256, 8, 128
+    d = {n: (None if v is None else v.to(DEV)) for n, v in W.make_inputs(W.Workload("t", 4, E, 2, H, I, "bf16", 5)).items()}
+    ones = torch.ones(H, device=DEV)
+    weight = torch.zeros(E, H, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.empty_cache()
+    used = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in [256] * 64 + [1 << 20] * 4]
+    torch.cuda.synchronize()
+    del used  # their memory goes to whoever allocates next
+    b = Block(4, E, 2, H, I, "bf16", (d["w1"], d["w2"], None, None), (weight, None), (ones, ones, None))
+    assert b.status() == m.MOE_OK
