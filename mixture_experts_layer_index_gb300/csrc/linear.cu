@@ -413,7 +413,8 @@ cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c
   // memory (not in large clusters, which then no longer find enough free SMs together)
   p.stages = stages_of(BN, BN == 256 || (blocks <= 152 && cluster <= 2) ? 1 : 2);
   // fp32 output: the tensor core's running sum rounds at every step, so its length is
-  // kept short by spreading the sum over up to four accumulators
+  // kept short by spreading the sum over up to four accumulators (here; large products, which
+  // go to linear_pair.cu, keep the whole sum in one: its two are the tiles in flight)
   p.nacc = q.ep.out_dtype != MOE_DTYPE_F32 ? 1 : BN <= 64 ? 4 : 2;
   int cols = 32;
   while (cols < BN * p.nacc) cols *= 2;

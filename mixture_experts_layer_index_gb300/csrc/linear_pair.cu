@@ -14,7 +14,8 @@
 // owns TMEM, 4-19 run the epilogue (four warps per 32 lanes, 64 columns each): 32
 // columns at a time are loaded from TMEM, finished in fp32, rounded once, staged in
 // shared memory as a 128-byte-swizzled box of 32 rows and stored by TMA, which
-// clips the edges.
+// clips the edges.  A tile's whole sum is one accumulator's, whatever the output's
+// type (tensor memory holds two tiles), rounded in fp32 at every step of it.
 //
 // Bound by the tensor cores: 16384 x 8192 x 2048 bf16 takes 294 us, 1.87 PFLOP/s (a library
 // product reaches 1.95 in short runs, 1.74 under the power limit).  With a GELU and its

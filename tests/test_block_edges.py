@@ -63,6 +63,13 @@ def test_linear_many_tiles_per_pair(m, M, N, K, ld_y, dtype, out, act):
     _linear_case(m, M, N, K, act, dtype, out, None, residual=True, in_place=True, ld_y=ld_y, gradient=False)
 
 
+# unrounded outputs of long sums at sizes that pairs of SMs take, one accumulator per tile
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", [(1300, 4100, 6152), (1500, 4096, 4096)])
+def test_linear_long_sums_of_large_products(m, dtype, M, N, K):
+    _linear_case(m, M, N, K, dtype=dtype, out="f32", bias="f32", gradient=False)
+
+
 # a status word that nobody else writes
 @pytest.mark.parametrize("M,N", [(5, 24), (300, 40), (0, 24), (5, 0)])
 @pytest.mark.parametrize("wanted", ["dbias", "nothing", "all"])
