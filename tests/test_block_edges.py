@@ -7,7 +7,7 @@ import torch
 
 import workloads as W
 from oracle import blocks as B
-from tests.test_block_ops import DEV, DT, STEP, _linear_case, _route, _rule, check, code, f64, gen, rows
+from tests.test_block_ops import DEV, DT, STEP, U, _linear_case, _route, _rule, check, code, f64, gen, rows
 
 pytestmark = pytest.mark.gpu
 ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
@@ -222,3 +222,38 @@ def test_a_block_that_never_ran_reports_no_error(m):
     del used  # their memory goes to whoever allocates next
     b = Block(4, E, 2, H, I, "bf16", (d["w1"], d["w2"], None, None), (weight, None), (ones, ones, None))
     assert b.status() == m.MOE_OK
+
+
+# single rows: each gradient is one product, so the slope's own absolute error shows
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f32"), ("f16", "f32")])
+@pytest.mark.parametrize("N,K", [(130, 264), (2435, 72)])
+def test_linear_single_row_gradient(m, act, dtype, out, N, K):
+    g = gen(N + K)
+    t = DT[dtype]
+    x, w, dy = rows(1, K, K, t, g), rows(N, K, K + 8, t, g, K ** -0.5), rows(1, N, N, DT[out], g)
+    z = torch.randn(1, N, generator=g, device=DEV).to(t) if act != "none" else None
+    p = m.linear_problem(1, N, K, code(m, dtype), code(m, out), act=act_code(m, act), alpha=0.5, ld_w=K + 8)
+    dx, dw = torch.full((1, K), float("nan"), dtype=t, device=DEV), torch.full((N, K), float("nan"), dtype=t, device=DEV)
+    db = torch.full((N,), float("nan"), device=DEV)
+    ws = torch.full((m.moe_linear_backward_workspace_size(p),), 255, dtype=torch.uint8, device=DEV)
+    m.moe_linear_backward(p, dy, x, w, z, dx, dw, db, ws)
+    assert m.moe_read_device_status(ws) == m.MOE_OK
+    ref = B.linear_backward(f64(dy), f64(x), f64(w), f64(z), act, 0.5)
+    # dz's rounding to the operands' type (f16: at least half the smallest step), and the
+    # slope's error, which is relative to 1 + |z|
+    u = U[dtype] * 1.01 + 16 * STEP
+    tiny = 2.0 ** -25 if dtype == "f16" else 0.0
+    slope = np.zeros((1, N)) if z is None else 16 * STEP * 0.5 * np.abs(f64(dy)) * (1 + np.abs(f64(z)))
+    dz = slope + tiny
+
+    def close(got, name, more, factor, extra):
+        val, mag = ref[name]
+        ug = U[dtype] if got.dtype == t else U["f32"]
+        off = np.abs(f64(got) - val) - (1 + ug) * (ug * np.abs(val) + (factor * STEP + extra) * (mag + tiny) + more) - (
+            tiny + 2.0 ** -126)
+        assert np.all(off <= 0), (name, float(off.max()))
+
+    close(dx, "dx", dz @ np.abs(f64(w)), N / 8 + 16, u)
+    close(dw, "dw", dz.T * np.abs(f64(x)), 16, u)
+    close(db, "dbias", slope[0], 16, 0.0)
