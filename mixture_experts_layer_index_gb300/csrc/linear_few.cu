@@ -109,19 +109,24 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Measured (us, here / on the tensor cores), for N x K:
-//   1 row   4096 x 4096  7.6 / 10.0;  8192 x 4096 11.6 / 14.9
-//   2 rows  4096 x 4096  8.9 / 10.0;  8192 x 4096 13.1 / 14.9
-//   4 rows  128 x 2048  2.4 / 5.5;  2048 x 2048  3.8 / 5.9;  4096 x 2048  7.2 / 8.0;  4096 x 4096 12.0 / 10.0
-//   8 rows  128 x 2048  3.2 / 5.8;  2048 x 2048  5.6 / 6.0;  3000 x 2048 10.4 / 6.7;  8192 x 64  5.6 / 2.6
+// Measured in graphs, weights from memory where they pass L2 together (us, here / on the tensor
+// cores), for N x K; the rule comes from some 1500 such shapes, N of 8 to 16384 and K of 32 to 8192:
+//   1 row   128 x 2048  2.0 / 5.6;  4096 x 4096  7.9 / 10.4;  256 x 8192  7.3 / 8.4;  16384 x 64  3.8 / 3.3
+//   2 rows  8192 x 4096  13.4 / 15.6;  3000 x 8192  14.9 / 13.7;  16384 x 128  3.6 / 3.8
+//   4 rows  128 x 8192  7.8 / 8.0;  2048 x 4096  7.0 / 8.6;  4096 x 2048  7.2 / 8.2;  3000 x 4096  9.9 / 9.4
+//           8192 x 256  3.5 / 4.0;  16384 x 64  5.0 / 3.3;  16384 x 512  6.7 / 5.8
+//   8 rows  64 x 4096  5.0 / 6.4;  256 x 3000  4.4 / 6.5;  2048 x 2048  6.3 / 6.9;  4096 x 64  3.3 / 2.6
+//           1024 x 4096  8.4 / 7.4;  256 x 8192  13.5 / 8.4
+// With a long K a warp walks it alone, where the tensor cores' tiles split the sum; with many
+// columns the rows of x are read again by every other one.
 // Rows are read in whole parts of eight values, which may not reach into what lies between two
 // rows or behind the last: other K go to the tensor cores, whose TMA boxes end at K.
 bool takes_few(const LinearArgs& a) {
   if (a.K % 8 != 0) return false;
   const long long weights = static_cast<long long>(a.N) * a.K;
-  if (a.M <= 2) return true;
-  if (a.M <= 4) return weights <= 1 << 23;
-  return a.M <= 8 && a.N <= 152 * 16 && weights <= 1 << 22;
+  if (a.M <= 2) return a.N < 1 << 14 || a.K > 128;
+  if (a.M <= 4) return a.N <= 8192 && weights <= 1 << 23;
+  return a.M <= 8 && a.N <= 152 * 16 && weights <= 1 << 22 && a.K <= (a.N <= 192 ? 4096 : 3000);
 }
 
 cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
