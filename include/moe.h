@@ -38,6 +38,7 @@
  *     on `stream` in order, with no device-to-host copy, so these calls can be
  *     captured in a CUDA graph.  Inputs are never written.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
+ *   - A process uses the library on one device, the one current at its first call.
  *   - Arguments are validated on the host BEFORE anything is enqueued; on a
  *     validation error nothing is launched and outputs are untouched.
  *   - A launch failure returns MOE_ERR_CUDA.  Conditions detected on the device
@@ -477,7 +478,8 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const void* dh_out, cons
  *   bias [N] of bias_dtype or NULL;  residual [M, N] of out_dtype, ld_y, or NULL
  *   y [M, N] of out_dtype, ld_y (y == residual is allowed)
  *   z [M, N] of dtype, contiguous, or NULL (kept for the gradient of an activation)
- * act: MOE_ACT_GELU is the erf form, MOE_ACT_GELU_TANH the tanh form.
+ * act: MOE_ACT_GELU is the erf form, MOE_ACT_GELU_TANH the tanh form.  NaN and
+ * infinities give what the formulas do (ReLU keeps NaN, GELU(+inf) = +inf).
  * K == 0 is INVALID_ARG; M == 0 or N == 0 computes nothing and needs no ws.
  * ws: moe_linear_workspace_size(p) bytes, 256-byte aligned: the status word
  * (moe_read_device_status), cleared by the call (by an empty one too, where ws is given).

@@ -77,7 +77,8 @@ class Block:
         self._grad = None
 
     def forward(self, h: torch.Tensor, o: torch.Tensor, stream=None):
-        """(h', o') of the block for the stream h and the previous block's output o, bf16 [T, H]."""
+        """(h', o') of the block for the stream h and the previous block's output o, bf16 [T, H].
+        Both are the block's own buffers, which the next step writes again."""
         post, pre, gate = self.norms
         weight, bias = self.router
         moe_norm_forward(self.norm, h, o, gate, post, None, pre, None, self.h_out, self.x, stream=stream)

@@ -5,8 +5,8 @@
 // each, and the same parts of every row of x, and add in fp32; a butterfly joins the lanes
 // and the first ROWS x COLS of them finish one output each.  No barrier, no tensor memory, no
 // shared memory: what is left of a call is the launch, one or a few trips to memory and five
-// shuffles (1 x 128 x 2048: 2.1 us, 5.5 on the tensor cores).  Bound by reading W once,
-// 1 x 8192 x 4096: 11.6 us, 5.8 TB/s; but each row of x costs two instructions per pair of
+// shuffles (1 x 128 x 2048: 2.0 us, 5.6 on the tensor cores).  Bound by reading W once,
+// 1 x 8192 x 4096: 11.6 to 12.1 us, 5.5 to 5.8 TB/s; but each row of x costs two instructions per pair of
 // products, so that more rows gain less and only where W is small.
 #include "linear.cuh"
 
