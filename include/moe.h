@@ -33,9 +33,8 @@
  *     workspace.  The library never allocates, frees or synchronises inside
  *     moe_route / moe_shuffle / moe_tile_map / moe_forward / moe_forward_ex /
  *     moe_forward_routed / moe_round_bf16 / moe_route_ex / moe_route_backward /
- *     moe_norm_forward / moe_norm_backward / moe_linear / moe_linear_backward:
- *     work is enqueued
- *     on `stream` in order, with no device-to-host copy, so these calls can be
+ *     moe_norm_forward / moe_norm_backward / moe_linear / moe_linear_backward /
+ *     moe_gated / moe_gated_backward: work is enqueued on `stream` in order, with no device-to-host copy, so these calls can be
  *     captured in a CUDA graph.  Inputs are never written.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
  *   - A process uses the library on one device, the one current at its first call.
@@ -369,8 +368,9 @@ moe_status moe_forward_views_ex(const moe_problem* p, const moe_forward_options*
  * workspace detect nothing on the device).  Rows may be strided where a descriptor
  * has an `ld`: elements between the starts of two rows, 0 for contiguous rows. */
 
-/* Element types of the arrays whose type a descriptor names. */
-typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+/* Element types of the arrays whose type a descriptor names.  MOE_DTYPE_E4M3, codes with a scale
+ * per block of 128, is taken by the entry points that say so. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_E4M3 = 3 } moe_dtype;
 
 /* ---------------------------------------------------------------- routing rules
  * moe_route_ex - routing with a score function, a selection bias, expert groups
@@ -519,6 +519,45 @@ moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, cons
                                const void* z, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes,
                                moe_stream_t stream);
 
+/* ---------------------------------------------------------------- gated linear layer
+ * moe_gated - the first half of a gated feed-forward block (the linear layer above is its
+ * second half), both projections, the activation and the product in one kernel:
+ *   z = [g, u] = x W^T + bias;  h = act(g) * u      fp32 accumulation, one rounding each
+ *   x [M, K] of dtype (bf16 or fp16), ld_x;  w [2 N, K] of dtype, ld_w: N gate rows, then N
+ *     up rows; strides and bases as the linear layer's
+ *   bias [2 N] of bias_dtype or NULL
+ *   h [M, N] of out_dtype, ld_h
+ *   z [M, 2 N] of dtype, contiguous, or NULL (kept for the gradient)
+ * act: a moe_act; MOE_ACT_NONE gives g * u.  h is computed from z before z is rounded.
+ * NaN and infinities give what the formulas do.  K == 0 is INVALID_ARG; M == 0 or N == 0
+ * computes nothing and needs no ws.
+ * ws: moe_gated_workspace_size(p) bytes, 256-byte aligned: the status word, as moe_linear's.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+typedef struct {
+  int M, N, K;
+  int dtype;      /* of x, w, z (and dx, dw): MOE_DTYPE_BF16 or MOE_DTYPE_F16 */
+  int out_dtype;  /* of h (and dh) */
+  int bias_dtype;
+  int act;        /* moe_act */
+  long long ld_x, ld_w, ld_h;
+} moe_gated_problem;
+size_t moe_gated_workspace_size(const moe_gated_problem* p);
+moe_status moe_gated(const moe_gated_problem* p, const void* x, const void* w, const void* bias, void* h, void* z,
+                     void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_gated_backward - dg = dh * u * act'(g), du = dh * act(g), dz = [dg, du], dx = dz W,
+ * dw = dz^T x, dbias = the column sums of dz:
+ *   dh [M, N] of out_dtype, ld_h;  x, w as in the forward;  z as the forward kept it
+ *   dx [M, K] and dw [2 N, K] of dtype, contiguous;  dbias [2 N] fp32;  each may be NULL.
+ * dz is rounded to dtype for the two products (the tensor cores' operand type), dbias sums
+ * it unrounded in fp32, in a fixed order.  M == 0 writes zeros to dw and dbias, N == 0 to
+ * dx; they need no ws.
+ * ws: moe_gated_backward_workspace_size(p) bytes, 256-byte aligned, status word at its head,
+ * cleared as moe_linear's, whichever outputs are wanted.  Errors: as moe_gated. */
+size_t moe_gated_backward_workspace_size(const moe_gated_problem* p);
+moe_status moe_gated_backward(const moe_gated_problem* p, const void* dh, const void* x, const void* w, const void* z,
+                              void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* ---------------------------------------------------------------- diagnostics
  * moe_read_device_status - synchronises `stream`, then returns the status
  * recorded on the device in the status word at the head of `ws` (MOE_OK,
@@ -547,7 +586,8 @@ moe_status moe_read_device_status(const void* ws, moe_stream_t stream);
  * scatter_gather, gateup_gemm, quant_h, down_gemm, combine (grouped path);
  * rd_prep, rd_gateup, rd_reduce, rd_down, combine (route-direct path); scatter,
  * tile_map, header_reset; route_ex, route_backward, norm_forward, norm_backward,
- * linear, linear_dz, linear_dx, linear_dw, linear_dx_dw, column_sums. */
+ * linear, linear_dz, linear_dx, linear_dw, linear_dx_dw, column_sums; gated, gated_dz
+ * (a gated gradient's products are timed as the linear layer's). */
 typedef struct {
   char name[32];
   double total_ms;

@@ -40,6 +40,7 @@ MOE_PATH_ROUTE_DIRECT = 2
 MOE_DTYPE_F32 = 0
 MOE_DTYPE_BF16 = 1
 MOE_DTYPE_F16 = 2
+MOE_DTYPE_E4M3 = 3
 # moe_score_fn
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
@@ -105,11 +106,17 @@ class moe_linear_problem(ctypes.Structure):
                 ("alpha", _f), ("ld_x", _ll), ("ld_w", _ll), ("ld_y", _ll)]
 
 
+class moe_gated_problem(ctypes.Structure):
+    _fields_ = [("M", _i), ("N", _i), ("K", _i), ("dtype", _i), ("out_dtype", _i), ("bias_dtype", _i), ("act", _i),
+                ("ld_x", _ll), ("ld_w", _ll), ("ld_h", _ll)]
+
+
 _P = ctypes.POINTER(moe_problem)
 _O = ctypes.POINTER(moe_forward_options)
 _RO = ctypes.POINTER(moe_route_options)
 _NP = ctypes.POINTER(moe_norm_problem)
 _LP = ctypes.POINTER(moe_linear_problem)
+_GP = ctypes.POINTER(moe_gated_problem)
 _SIGS = {
     "moe_route": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "moe_shuffle_workspace_size": (_sz, [_i, _i, _i]),
@@ -139,6 +146,10 @@ _SIGS = {
     "moe_linear": (_i, [_LP] + [_vp] * 7 + [_sz, _vp]),
     "moe_linear_backward_workspace_size": (_sz, [_LP]),
     "moe_linear_backward": (_i, [_LP] + [_vp] * 8 + [_sz, _vp]),
+    "moe_gated_workspace_size": (_sz, [_GP]),
+    "moe_gated": (_i, [_GP] + [_vp] * 6 + [_sz, _vp]),
+    "moe_gated_backward_workspace_size": (_sz, [_GP]),
+    "moe_gated_backward": (_i, [_GP] + [_vp] * 8 + [_sz, _vp]),
     "moe_read_device_status": (_i, [_vp, _vp]),
     "moe_profile_start": (_i, []),
     "moe_profile_start_stage": (_i, [ctypes.c_char_p]),
@@ -466,6 +477,36 @@ def moe_linear_backward(p: moe_linear_problem, dy, x, w, z, dx, dw, dbias, ws, w
     _check(lib().moe_linear_backward(p, _rows(dy, "dy", p.N, p.ld_y), _rows(x, "x", K, p.ld_x), _rows(w, "w", K, p.ld_w),
                                      _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(ws), nb, _stream(stream)),
            "moe_linear_backward")
+
+
+def gated_problem(M, N, K, dtype=MOE_DTYPE_BF16, out_dtype=MOE_DTYPE_BF16, bias_dtype=MOE_DTYPE_F32, act=MOE_ACT_SILU,
+                  ld_x=0, ld_w=0, ld_h=0) -> moe_gated_problem:
+    return moe_gated_problem(M, N, K, dtype, out_dtype, bias_dtype, act, ld_x, ld_w, ld_h)
+
+
+def moe_gated_workspace_size(p: moe_gated_problem) -> int:
+    return int(lib().moe_gated_workspace_size(p))
+
+
+def moe_gated(p: moe_gated_problem, x, w, bias, h, z, ws, ws_bytes=None, stream=None) -> None:
+    """h = act(g) u for [g, u] = x w^T + bias, N gate rows and N up rows in w; z keeps [g, u]."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    K = p.K
+    _check(lib().moe_gated(p, _rows(x, "x", K, p.ld_x), _rows(w, "w", K, p.ld_w), _ptr(bias), _rows(h, "h", p.N, p.ld_h),
+                           _ptr(z), _ptr(ws), nb, _stream(stream)), "moe_gated")
+
+
+def moe_gated_backward_workspace_size(p: moe_gated_problem) -> int:
+    return int(lib().moe_gated_backward_workspace_size(p))
+
+
+def moe_gated_backward(p: moe_gated_problem, dh, x, w, z, dx, dw, dbias, ws, ws_bytes=None, stream=None) -> None:
+    """Gradient of moe_gated; outputs given as None are left out."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    K = p.K
+    _check(lib().moe_gated_backward(p, _rows(dh, "dh", p.N, p.ld_h), _rows(x, "x", K, p.ld_x), _rows(w, "w", K, p.ld_w),
+                                    _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(ws), nb, _stream(stream)),
+           "moe_gated_backward")
 
 
 def moe_read_device_status(ws, stream=None) -> int:

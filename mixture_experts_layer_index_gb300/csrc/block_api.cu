@@ -98,6 +98,15 @@ moe_status check_gate(const moe_norm_problem& p, const void* gate) {
 }
 
 // ------------------------------------------------------------------ linear
+// Strides of TMA operands, and sizes whose tile coordinates are 32-bit and whose products' grids
+// (128 columns x at least 16 rows, up to eight blocks) stay below 2^31.
+bool operands_fit(long long M, long long N, long long K, long long ld_x, long long ld_w) {
+  if (ld_x % 8 || ld_w % 8 || ld_x >= (1ll << 38) || ld_w >= (1ll << 38)) return false;
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return false;
+  auto blocks = [](long long cols, long long rows) { return (cols / 128 + 1) * (rows / 16 + 1) * 8; };
+  return blocks(N, M) < (1ll << 31) && blocks(K, M) < (1ll << 31) && blocks(K, N) < (1ll << 31);
+}
+
 moe_status check_linear(const moe_linear_problem* p) {
   if (!p || p->M < 0 || p->N < 0 || p->K < 1) return MOE_ERR_INVALID_ARG;
   if (!is_dtype(p->dtype) || !is_dtype(p->out_dtype) || !is_dtype(p->bias_dtype)) return MOE_ERR_INVALID_ARG;
@@ -105,14 +114,19 @@ moe_status check_linear(const moe_linear_problem* p) {
   if ((p->ld_x != 0 && p->ld_x < p->K) || (p->ld_w != 0 && p->ld_w < p->K) || (p->ld_y != 0 && p->ld_y < p->N))
     return MOE_ERR_INVALID_ARG;
   if (p->dtype == MOE_DTYPE_F32) return MOE_ERR_UNSUPPORTED;
-  const long long ld_x = p->ld_x ? p->ld_x : p->K, ld_w = p->ld_w ? p->ld_w : p->K;
-  if (ld_x % 8 || ld_w % 8 || ld_x >= (1ll << 38) || ld_w >= (1ll << 38)) return MOE_ERR_UNSUPPORTED;
-  // tile coordinates are 32-bit, and a product's grid (128 columns x at least 16 rows, up to eight blocks) below 2^31
-  if (p->M > (1 << 30) || p->N > (1 << 30) || p->K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
-  auto blocks = [](long long cols, long long rows) { return (cols / 128 + 1) * (rows / 16 + 1) * 8; };
-  if (blocks(p->N, p->M) >= (1ll << 31) || blocks(p->K, p->M) >= (1ll << 31) || blocks(p->K, p->N) >= (1ll << 31))
-    return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
+  return operands_fit(p->M, p->N, p->K, p->ld_x ? p->ld_x : p->K, p->ld_w ? p->ld_w : p->K) ? MOE_OK
+                                                                                             : MOE_ERR_UNSUPPORTED;
+}
+
+moe_status check_gated(const moe_gated_problem* p) {
+  if (!p || p->M < 0 || p->N < 0 || p->K < 1) return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(p->dtype) || !is_dtype(p->out_dtype) || !is_dtype(p->bias_dtype)) return MOE_ERR_INVALID_ARG;
+  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  if ((p->ld_x != 0 && p->ld_x < p->K) || (p->ld_w != 0 && p->ld_w < p->K) || (p->ld_h != 0 && p->ld_h < p->N))
+    return MOE_ERR_INVALID_ARG;
+  if (p->dtype == MOE_DTYPE_F32 || p->N > (1 << 29)) return MOE_ERR_UNSUPPORTED;
+  return operands_fit(p->M, 2ll * p->N, p->K, p->ld_x ? p->ld_x : p->K, p->ld_w ? p->ld_w : p->K) ? MOE_OK
+                                                                                                  : MOE_ERR_UNSUPPORTED;
 }
 
 constexpr size_t kHeaderBytes = 256;
@@ -329,6 +343,82 @@ moe_status moe_linear_backward(const moe_linear_problem* p, const void* dy, cons
   a.dz = base + L.dz;
   a.hdr = static_cast<DeviceHeader*>(ws);
   return from_cuda(launch_linear_backward(a, s));
+}
+
+size_t moe_gated_workspace_size(const moe_gated_problem* p) { return check_gated(p) == MOE_OK ? kHeaderBytes : 0; }
+
+moe_status moe_gated(const moe_gated_problem* p, const void* x, const void* w, const void* bias, void* h, void* z,
+                     void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const moe_status st = check_gated(p);
+  if (st != MOE_OK) return st;
+  if (p->M == 0 || p->N == 0) return from_cuda(clear_status(ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream)));
+  if (!x || !w || !h || !aligned(x, 16) || !aligned(w, 16) || !fits(h, p->out_dtype) || !fits(z, p->dtype) ||
+      !fits(bias, p->bias_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < kHeaderBytes) return MOE_ERR_WORKSPACE;
+  GatedArgs a{};
+  a.M = p->M;
+  a.N = p->N;
+  a.K = p->K;
+  a.dtype = p->dtype;
+  a.out_dtype = p->out_dtype;
+  a.bias_dtype = p->bias_dtype;
+  a.act = p->act;
+  a.ld_x = p->ld_x ? p->ld_x : p->K;
+  a.ld_w = p->ld_w ? p->ld_w : p->K;
+  a.ld_h = p->ld_h ? p->ld_h : p->N;
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.h = h;
+  a.z = z;
+  a.hdr = static_cast<DeviceHeader*>(ws);
+  return from_cuda(launch_gated(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_gated_backward_workspace_size(const moe_gated_problem* p) {
+  return check_gated(p) == MOE_OK ? plan_linear_backward(p->M, 2 * p->N).total : 0;
+}
+
+moe_status moe_gated_backward(const moe_gated_problem* p, const void* dh, const void* x, const void* w, const void* z,
+                              void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  const moe_status st = check_gated(p);
+  if (st != MOE_OK) return st;
+  if (!fits(dx, p->dtype) || !fits(dw, p->dtype) || !aligned(dbias, 4)) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->M == 0 || p->N == 0) {  // empty sums
+    cudaError_t e = clear_status(ws, ws_bytes, s);
+    if (e == cudaSuccess && dx && p->M) e = cudaMemsetAsync(dx, 0, static_cast<size_t>(p->M) * p->K * 2, s);
+    if (e == cudaSuccess && dw && p->N) e = cudaMemsetAsync(dw, 0, 2 * static_cast<size_t>(p->N) * p->K * 2, s);
+    if (e == cudaSuccess && dbias && p->N) e = cudaMemsetAsync(dbias, 0, 2 * static_cast<size_t>(p->N) * 4, s);
+    return from_cuda(e);
+  }
+  if (!dh || !z || (dw && !x) || (dx && !w)) return MOE_ERR_INVALID_ARG;
+  if (!fits(dh, p->out_dtype) || !aligned(x, 16) || !aligned(w, 16) || !fits(z, p->dtype)) return MOE_ERR_INVALID_ARG;
+  const LinearBackwardLayout L = plan_linear_backward(p->M, 2 * p->N);
+  if (!ws || !aligned(ws, 256) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  GatedBackwardArgs a{};
+  a.M = p->M;
+  a.N = p->N;
+  a.K = p->K;
+  a.dtype = p->dtype;
+  a.dh_dtype = p->out_dtype;
+  a.act = p->act;
+  a.ld_x = p->ld_x ? p->ld_x : p->K;
+  a.ld_w = p->ld_w ? p->ld_w : p->K;
+  a.ld_h = p->ld_h ? p->ld_h : p->N;
+  a.dh = dh;
+  a.x = x;
+  a.w = w;
+  a.z = z;
+  a.dx = dx;
+  a.dw = dw;
+  a.dbias = dbias;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.partials = reinterpret_cast<float*>(base + L.partials);
+  a.dz = base + L.dz;
+  a.hdr = static_cast<DeviceHeader*>(ws);
+  return from_cuda(launch_gated_backward(a, s));
 }
 
 }  // extern "C"

@@ -292,6 +292,36 @@ size_t linear_dz_bytes(int M, int N);
 size_t linear_partials_bytes(int M, int N);
 cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s);
 
+// Gated linear layer (gated.cu; its products as the linear layer's).
+struct GatedArgs {
+  int M, N, K;
+  int dtype, out_dtype, bias_dtype, act;
+  long long ld_x, ld_w, ld_h;
+  const void* x;
+  const void* w;
+  const void* bias;
+  void* h;
+  void* z;
+  DeviceHeader* hdr;
+};
+cudaError_t launch_gated(const GatedArgs& a, cudaStream_t s);
+struct GatedBackwardArgs {
+  int M, N, K;
+  int dtype, dh_dtype, act;
+  long long ld_x, ld_w, ld_h;
+  const void* dh;
+  const void* x;
+  const void* w;
+  const void* z;
+  void* dx;
+  void* dw;
+  float* dbias;
+  void* dz;         // [M][ld] of dtype, gate and up side by side
+  float* partials;  // column sums of dz per row chunk
+  DeviceHeader* hdr;
+};
+cudaError_t launch_gated_backward(const GatedBackwardArgs& a, cudaStream_t s);
+
 // Launch `kernel` as a programmatic dependent of the previous work on the stream:
 // its launch is prepared while the predecessor runs, and it waits for the
 // predecessor on the device (dep_wait) before touching its results.

@@ -52,6 +52,7 @@ struct TileProduct {
   int nC, nR;      // tiles
   int splits;      // blocks per tile: a cluster's, or 1
   int a_mn, b_mn;  // operand columns / rows contiguous along c / r
+  int half;        // gated: rows of the gate in the column operand
   Epilogue ep;
 };
 // A launch computes one product, or two side by side (a gradient's two, unless both fill the
@@ -139,6 +140,29 @@ __device__ __forceinline__ void finish(const TileProduct& p, float (&v)[CH], int
   store_rows<CH>(p.ep.y, p.ep.out_dtype, at, p.ep.ld_y, n, v);
 }
 
+// The gated epilogue of n rows from r0 of output column c: sums of its gate and up columns.
+template <int CH>
+__device__ __forceinline__ void finish_gated(const TileProduct& p, float (&g)[CH], float (&u)[CH], int r0, int n, int c) {
+  if (c >= p.C || n <= 0) return;
+  if (p.ep.bias) {
+    const float bg = load_as_f32(p.ep.bias, p.ep.bias_dtype, c), bu = load_as_f32(p.ep.bias, p.ep.bias_dtype, p.half + c);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      g[i] += bg;
+      u[i] += bu;
+    }
+  }
+  if (p.ep.z) {
+    const size_t at = static_cast<size_t>(r0) * p.ep.ld_z + c;
+    store_rows<CH>(p.ep.z, p.ep.z_dtype, at, p.ep.ld_z, n, g);
+    store_rows<CH>(p.ep.z, p.ep.z_dtype, at + p.half, p.ep.ld_z, n, u);
+  }
+  act_all<CH>(g, p.ep.act);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) g[i] *= u[i];
+  store_rows<CH>(p.ep.y, p.ep.out_dtype, static_cast<size_t>(r0) * p.ep.ld_y + c, p.ep.ld_y, n, g);
+}
+
 template <int CH>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[CH]) {
   static_assert(CH == 16 || CH == 32, "16 or 32 columns");
@@ -147,8 +171,9 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[CH]) {
 }
 
 // Warp 0 loads, warp 1 issues the MMAs, then all four warps (one per 32 TMEM lanes)
-// run the epilogue.
-template <int BN>
+// run the epilogue.  GATED: lanes 0-63 hold 64 gate columns, 64-127 the up columns beside
+// them, which meet in shared memory.
+template <int BN, bool GATED>
 __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__ TileMaps m0,
                                                          const __grid_constant__ TileMaps m1,
                                                          const __grid_constant__ Params p) {
@@ -200,7 +225,8 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   constexpr int GR = 16;
   const int group = tile / (GR * o.nC), in_group = tile - group * (GR * o.nC);
   const int rows_here = min(GR, o.nR - group * GR);
-  const int c0 = in_group / rows_here * BM;
+  constexpr int BC = GATED ? BM / 2 : BM;  // output columns per tile
+  const int c0 = in_group / rows_here * BC;
   const int r0 = (group * GR + in_group % rows_here) * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(o.nk) * rank / o.splits);
   const int kb1 = static_cast<int>(static_cast<long long>(o.nk) * (rank + 1) / o.splits);
@@ -225,7 +251,10 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       if (leader) {
         const int k = (kb0 + issued) * BK;
         mbar_arrive_expect_tx(full, STAGE);
-        if (a_mn) {
+        if (GATED) {
+          tma_load_2d(a, ma, k, c0, full);
+          tma_load_2d(a + A_BYTES / 2, ma, k, o.half + c0, full);
+        } else if (a_mn) {
           tma_load_2d(a, ma, c0, k, full);
           tma_load_2d(a + A_BYTES / 2, ma, c0 + 64, k, full);
         } else {
@@ -274,7 +303,7 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       __syncwarp();
     }
     if (leader) mma_commit(done);
-  } else if (o.ep.residual) {
+  } else if (!GATED && o.ep.residual) {
     // the residual's part of the tile comes into L2 while the product is computed
     const size_t es = o.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
     const size_t bytes = static_cast<size_t>(min(BM, o.C - c0)) * es;
@@ -305,9 +334,9 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   };
   // Few output columns leave most lanes without one: the values then go through shared
   // memory too, and groups of `width` threads take rows in turn.
-  const int cols = min(BM, o.C - c0);
+  const int cols = min(BC, o.C - c0);
   const int width = cols <= 16 ? 16 : cols <= 32 ? 32 : cols <= 64 ? 64 : BM;
-  if (o.splits == 1 && width == BM) {
+  if (!GATED && o.splits == 1 && width == BM) {
     if (good) {
 #pragma unroll 1
       for (int j = 0; j < BN; j += CH) {
@@ -337,27 +366,33 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
       const int c = static_cast<int>(threadIdx.x) & (width - 1);
       const int per = BN / o.splits;
       const int per_group = (per + groups - 1) / groups;
-      constexpr int RB = 8;
+      constexpr int RB = GATED ? 4 : 8;
+      constexpr int PARTS = GATED ? 2 : 1;  // gate and up
       const uint32_t mine = smem_u32(part) + c * 4;
       const uint32_t first = o.splits > 1 ? 0u : cluster_rank();  // of the blocks that share the tile
       const int begin = rank * per + own * per_group;
       const int end = min(min(begin + per_group, (rank + 1) * per), o.R - r0);
       for (int j = begin; j < end; j += RB) {
         const int cnt = min(RB, end - j);
-        float u[MAX_SPLITS][RB];
+        float u[MAX_SPLITS][PARTS][RB];
 #pragma unroll
         for (int q = 0; q < MAX_SPLITS; ++q)
           if (q < o.splits)
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-              if (i < cnt) u[q][i] = ld_cluster_f32(mine + (j + i) * (BM * 4), first + q);
-        float v[RB] = {};
+            for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+              for (int i = 0; i < RB; ++i)
+                if (i < cnt) u[q][h][i] = ld_cluster_f32(mine + (j + i) * (BM * 4) + h * (BC * 4), first + q);
+        float v[PARTS][RB] = {};
 #pragma unroll
         for (int q = 0; q < MAX_SPLITS; ++q)
           if (q < o.splits)
 #pragma unroll
-            for (int i = 0; i < RB; ++i) v[i] += u[q][i];
-        finish<RB>(o, v, r0 + j, cnt, c0 + c);
+            for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+              for (int i = 0; i < RB; ++i) v[h][i] += u[q][h][i];
+        if constexpr (GATED) finish_gated<RB>(o, v[0], v[1], r0 + j, cnt, c0 + c);
+        else finish<RB>(o, v[0], r0 + j, cnt, c0 + c);
       }
     }
     if (o.splits > 1) cluster_sync_all();  // no block leaves while another still reads its partial
@@ -370,17 +405,21 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   }
 }
 
+// Output columns per tile.
+inline int tile_cols(const Product& q) { return q.gated ? BM / 2 : BM; }
+
 bool encode_product(TileMaps* m, TileProduct* t, const Product& q, int bn, int splits) {
   t->C = q.C;
   t->R = q.R;
   t->nk = (q.K + BK - 1) / BK;
-  t->nC = (q.C + BM - 1) / BM;
+  t->nC = (q.C + tile_cols(q) - 1) / tile_cols(q);
   t->nR = (q.R + bn - 1) / bn;
+  t->half = q.gated ? q.C : 0;
   t->splits = splits;
   t->a_mn = q.cols_mn;
   t->b_mn = q.rows_mn;
   t->ep = q.ep;
-  return encode(&m->a, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn ? 64 : BM) &&
+  return encode(&m->a, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn || q.gated ? 64 : BM) &&
          encode(&m->b, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : bn);
 }
 
@@ -390,7 +429,7 @@ struct Choice {
   int splits2;  // of the second product: 1, or as many as a cluster has blocks, like the first's
 };
 
-template <int BN>
+template <int BN, bool GATED>
 cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c, cudaStream_t s) {
   Params p{};
   TileMaps m0, m1;
@@ -398,7 +437,7 @@ cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c
   m1 = m0;
   if (second && !encode_product(&m1, &p.prod[1], *second, BN, c.splits2)) return cudaErrorInvalidValue;
   static const cudaError_t attr = cudaFuncSetAttribute(
-      linear_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN, stages_of(BN, 1)));
+      linear_kernel<BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN, stages_of(BN, 1)));
   if (attr != cudaSuccess) return attr;
   p.type = q.type;
   p.reset_status = q.reset_status;
@@ -432,7 +471,7 @@ cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c
   cfg.stream = s;
   cfg.attrs = la;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<BN>, m0, m1, p);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<BN, GATED>, m0, m1, p);
 }
 
 // About how long a launch takes (us), for tiles of 128 x bn split over `splits` blocks.
@@ -445,7 +484,7 @@ cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c
 // 2048's weight gradient at bn = 64, 8 splits) from 54 us (128, 1).
 float tile_estimate(const Product& q, int bn, int splits) {
   const long long nk = (q.K + BK - 1) / BK;
-  const long long blocks = static_cast<long long>((q.C + BM - 1) / BM) * ((q.R + bn - 1) / bn) * splits;
+  const long long blocks = static_cast<long long>((q.C + tile_cols(q) - 1) / tile_cols(q)) * ((q.R + bn - 1) / bn) * splits;
   // a cluster's blocks lie in one group of SMs: clusters of 8 reach 128 of 152 SMs
   const int occupancy = bn == 256 ? 1 : 2, sms = splits == 8 ? 128 : 152;
   const long long waves = (blocks + sms * occupancy - 1) / (sms * occupancy);
@@ -454,7 +493,7 @@ float tile_estimate(const Product& q, int bn, int splits) {
   const float load = together * stage_bytes(bn) / 143000.0f;
   if (load > stage) stage = load;
   float t = waves * static_cast<float>((nk + splits - 1) / splits) * stage;
-  const float memory = 2.0f * (static_cast<float>(q.R) + q.C) * q.K / 6.5e6f;
+  const float memory = 2.0f * (static_cast<float>(q.R) + (q.gated ? 2.0f : 1.0f) * q.C) * q.K / 6.5e6f;
   if (memory > t) t = memory;
   // lanes without a column take rows instead
   const float lanes = q.C <= 16 ? 0.125f : q.C <= 32 ? 0.25f : q.C <= 64 ? 0.5f : 1.0f;
@@ -478,13 +517,14 @@ Choice choose_tile(const Product& q) {
   return best;
 }
 
+template <bool GATED>
 cudaError_t launch_shape(const Product& q, const Product* second, const Choice& c, cudaStream_t s) {
   switch (c.bn) {
-    case 16: return launch_tile<16>(q, second, c, s);
-    case 32: return launch_tile<32>(q, second, c, s);
-    case 64: return launch_tile<64>(q, second, c, s);
-    case 128: return launch_tile<128>(q, second, c, s);
-    default: return launch_tile<256>(q, second, c, s);
+    case 16: return launch_tile<16, GATED>(q, second, c, s);
+    case 32: return launch_tile<32, GATED>(q, second, c, s);
+    case 64: return launch_tile<64, GATED>(q, second, c, s);
+    case 128: return launch_tile<128, GATED>(q, second, c, s);
+    default: return launch_tile<256, GATED>(q, second, c, s);
   }
 }
 
@@ -521,7 +561,53 @@ bool takes_pair(const Product& q, const Choice& c) { return pair_estimate(q) < c
 cudaError_t launch_product(const Product& q, cudaStream_t s) {
   const Choice c = choose_tile(q);
   if (takes_pair(q, c)) return launch_pair(q, nullptr, s);
-  return launch_shape(q, nullptr, c, s);
+  return q.gated ? launch_shape<true>(q, nullptr, c, s) : launch_shape<false>(q, nullptr, c, s);
+}
+
+cudaError_t launch_gradient_products(const GradientProducts& g, cudaStream_t s) {
+  Product q{};
+  q.type = g.dtype == MOE_DTYPE_BF16 ? 1 : 0;
+  q.C = g.K;
+  q.cols_mn = true;
+  q.ep = {MOE_ACT_NONE, MOE_DTYPE_F32, g.dtype, g.dtype, 1.0f, g.K, 0, nullptr, nullptr, nullptr, nullptr};
+  q.reset_status = 1;
+  q.hdr = g.hdr;
+  q.rows = g.dz;
+  Product dx = q, dw = q;
+  dx.R = g.M;
+  dx.K = g.N;
+  dx.cols = {g.w, g.ld_w, g.K, g.N};
+  dx.rows_mn = false;
+  dx.ep.y = g.dx;
+  dw.R = g.N;
+  dw.K = g.M;
+  dw.cols = {g.x, g.ld_x, g.K, g.M};
+  dw.rows_mn = true;
+  dw.ep.y = g.dw;
+  if (g.dx && g.dw) {
+    const Choice cx = choose_tile(dx), cw = choose_tile(dw), both = choose_both(dw, dx);
+    const bool px = takes_pair(dx, cx), pw = takes_pair(dw, cw);
+    const float apart = (px ? pair_estimate(dx) : cx.us) + (pw ? pair_estimate(dw) : cw.us);
+    if ((px && pw) || (both.bn && both.us < apart)) {
+      stage_begin("linear_dx_dw", s);
+      const cudaError_t err = px && pw ? launch_pair(dx, &dw, s) : launch_shape<false>(dw, &dx, both, s);
+      stage_end(s);
+      return err;
+    }
+  }
+  cudaError_t err = cudaSuccess;
+  if (g.dx) {
+    stage_begin("linear_dx", s);
+    err = launch_product(dx, s);
+    stage_end(s);
+    dw.reset_status = 0;
+  }
+  if (err == cudaSuccess && g.dw) {
+    stage_begin("linear_dw", s);
+    err = launch_product(dw, s);
+    stage_end(s);
+  }
+  return err;
 }
 
 // ------------------------------------------------------------------ dz
@@ -641,14 +727,6 @@ cudaError_t launch_dz(const DzArgs& d, int dy_dtype, bool vec, int chunks, cudaS
   return launch_dz<__half, T>(d, vec, chunks, s);
 }
 
-// Rows per chunk: at least 64, at most 256 chunks; up to 128 rows are one chunk, whose sums
-// are final.
-inline int dz_rows(int M) {
-  const int r = (M + 255) / 256;
-  return M <= 128 ? 128 : r < 64 ? 64 : (r + 7) / 8 * 8;
-}
-inline long long dz_ld(int N) { return (N + 7) / 8 * 8; }
-
 }  // namespace lin
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
@@ -709,49 +787,9 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
     stage_end(s);
     if (err == cudaSuccess && a.dbias && chunks > 1) err = launch_column_sums(a.partials, chunks, a.N, a.dbias, s);
   }
+  if (err != cudaSuccess || !products) return err;
   const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};
-  Product q{};
-  q.type = a.dtype == MOE_DTYPE_BF16 ? 1 : 0;
-  q.C = a.K;
-  q.cols_mn = true;
-  q.ep = {MOE_ACT_NONE, MOE_DTYPE_F32, a.dtype, a.dtype, 1.0f, a.K, 0, nullptr, nullptr, nullptr, nullptr};
-  q.reset_status = 1;
-  q.hdr = a.hdr;
-  q.rows = dz;
-  Product dx = q, dw = q;
-  dx.R = a.M;
-  dx.K = a.N;
-  dx.cols = {a.w, a.ld_w, a.K, a.N};
-  dx.rows_mn = false;
-  dx.ep.y = a.dx;
-  dw.R = a.N;
-  dw.K = a.M;
-  dw.cols = {a.x, a.ld_x, a.K, a.M};
-  dw.rows_mn = true;
-  dw.ep.y = a.dw;
-  if (err == cudaSuccess && a.dx && a.dw) {
-    const Choice cx = choose_tile(dx), cw = choose_tile(dw), both = choose_both(dw, dx);
-    const bool px = takes_pair(dx, cx), pw = takes_pair(dw, cw);
-    const float apart = (px ? pair_estimate(dx) : cx.us) + (pw ? pair_estimate(dw) : cw.us);
-    if ((px && pw) || (both.bn && both.us < apart)) {
-      stage_begin("linear_dx_dw", s);
-      err = px && pw ? launch_pair(dx, &dw, s) : launch_shape(dw, &dx, both, s);
-      stage_end(s);
-      return err;
-    }
-  }
-  if (err == cudaSuccess && a.dx) {
-    stage_begin("linear_dx", s);
-    err = launch_product(dx, s);
-    stage_end(s);
-    dw.reset_status = 0;
-  }
-  if (err == cudaSuccess && a.dw) {
-    stage_begin("linear_dw", s);
-    err = launch_product(dw, s);
-    stage_end(s);
-  }
-  return err;
+  return launch_gradient_products({a.M, a.N, a.K, a.dtype, a.ld_x, a.ld_w, a.x, a.w, a.dx, a.dw, dz, a.hdr}, s);
 }
 
 }  // namespace moe

@@ -152,7 +152,8 @@ struct Operand {
   int inner, outer;  // inner: contiguous extent
 };
 
-// The epilogue of a product: out = alpha act(sum + bias) + residual, z = sum + bias.
+// The epilogue of a product: out = alpha act(sum + bias) + residual, z = sum + bias; of a gated
+// one out = act(gate) up, where gate and up are sum + bias of columns c and half + c.
 struct Epilogue {
   int act, bias_dtype, out_dtype, z_dtype;
   float alpha;
@@ -184,6 +185,7 @@ struct Product {
   int type;  // 0 = f16, 1 = bf16 operands
   Operand rows, cols;
   bool rows_mn, cols_mn;
+  bool gated;  // cols holds 2 C rows, the gate's and then the up projection's; both operands K-major
   Epilogue ep;
   int reset_status;
   DeviceHeader* hdr;
@@ -193,9 +195,33 @@ struct Product {
 // (the same type and row length, no bias, activation, residual or z).
 float pair_estimate(const Product& p);
 cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s);
+// The product by the kernel whose estimate is the least.
+cudaError_t launch_product(const Product& q, cudaStream_t s);
+// dx = dz W and dW = dz^T x, each where its output is wanted; the launch clears the status word.
+struct GradientProducts {
+  int M, N, K;  // N: columns of dz
+  int dtype;
+  long long ld_x, ld_w;
+  const void* x;
+  const void* w;
+  void* dx;
+  void* dw;
+  Operand dz;
+  DeviceHeader* hdr;
+};
+cudaError_t launch_gradient_products(const GradientProducts& g, cudaStream_t s);
+// Rows that a block of the dz kernels takes: at least 64, at most 256 chunks; up to 128 rows
+// are one chunk, whose column sums are final.
+inline int dz_rows(int M) {
+  const int r = (M + 255) / 256;
+  return M <= 128 ? 128 : r < 64 ? 64 : (r + 7) / 8 * 8;
+}
+inline long long dz_ld(int N) { return (N + 7) / 8 * 8; }
 // A few rows (linear_few.cu).
 bool takes_few(const LinearArgs& a);
 cudaError_t launch_few(const LinearArgs& a, cudaStream_t s);
+bool takes_few(const GatedArgs& a);
+cudaError_t launch_few(const GatedArgs& a, cudaStream_t s);
 
 }  // namespace lin
 }  // namespace moe

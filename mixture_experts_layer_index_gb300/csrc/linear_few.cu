@@ -23,20 +23,23 @@ __device__ __forceinline__ float2 pair_of(uint32_t v, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-template <typename T, int ROWS, int COLS>
+// GATED: the two columns are a gate and its up projection, N rows of W further on.
+template <typename T, int ROWS, int COLS, bool GATED>
 __global__ void __launch_bounds__(FEW_WARPS * 32) linear_few_kernel(LinearArgs a) {
+  static_assert(!GATED || COLS == 2, "a gate and its up projection");
   constexpr int AHEAD = ROWS < 8 && (COLS == 1 || ROWS == 1) ? 4 : 2;  // 16-byte parts of each row on their way
   dep_wait();
   dep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = a.hdr->info = 0u;
   const int lane = threadIdx.x & 31;
-  const int n0 = (blockIdx.x * FEW_WARPS + (threadIdx.x >> 5)) * COLS;
+  const int n0 = (blockIdx.x * FEW_WARPS + (threadIdx.x >> 5)) * (GATED ? 1 : COLS);
   if (n0 >= a.N) return;
   // columns past the last and rows past M stand in for the last
   const T* w[COLS];
   const T* x[ROWS];
 #pragma unroll
-  for (int c = 0; c < COLS; ++c) w[c] = static_cast<const T*>(a.w) + static_cast<size_t>(min(n0 + c, a.N - 1)) * a.ld_w;
+  for (int c = 0; c < COLS; ++c)
+    w[c] = static_cast<const T*>(a.w) + (GATED ? n0 + static_cast<size_t>(c) * a.N : min(n0 + c, a.N - 1)) * a.ld_w;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) x[r] = static_cast<const T*>(a.x) + static_cast<size_t>(min(r, a.M - 1)) * a.ld_x;
   float sum[ROWS][COLS] = {};
@@ -80,31 +83,49 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) linear_few_kernel(LinearArgs a
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       if (lane == r * COLS + c) z = v;
     }
-  const int r = lane / COLS, n = n0 + lane % COLS;
+  const int r = lane / COLS, n = GATED ? n0 : n0 + lane % COLS;
+  if constexpr (GATED) {
+    const int col = n0 + (lane & 1) * a.N;  // this lane's column of z
+    if (a.bias) z += load_as_f32(a.bias, a.bias_dtype, col);
+    if (a.z && lane < ROWS * COLS && r < a.M) static_cast<T*>(a.z)[static_cast<size_t>(r) * 2 * a.N + col] = as_type<T>(z);
+    const float up = __shfl_down_sync(0xffffffffu, z, 1);
+    if (lane & 1) return;
+    z = act_value(z, a.act) * up;
+  }
   if (lane >= ROWS * COLS || r >= a.M || n >= a.N) return;
-  if (a.bias) z += load_as_f32(a.bias, a.bias_dtype, n);
-  if (a.z) static_cast<T*>(a.z)[static_cast<size_t>(r) * a.N + n] = as_type<T>(z);
-  float y = a.alpha * act_value(z, a.act);
+  float y = z;
+  if constexpr (!GATED) {
+    if (a.bias) z += load_as_f32(a.bias, a.bias_dtype, n);
+    if (a.z) static_cast<T*>(a.z)[static_cast<size_t>(r) * a.N + n] = as_type<T>(z);
+    y = a.alpha * act_value(z, a.act);
+  }
   const size_t at = static_cast<size_t>(r) * a.ld_y + n;
-  if (a.residual) y += load_as_f32(a.residual, a.out_dtype, at);
+  if (!GATED && a.residual) y += load_as_f32(a.residual, a.out_dtype, at);
   if (a.out_dtype == MOE_DTYPE_F32) static_cast<float*>(a.y)[at] = y;
   else if (a.out_dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(y);
   else static_cast<__half*>(a.y)[at] = __float2half_rn(y);
 }
 
-template <typename T, int ROWS, int COLS>
+template <typename T, int ROWS, int COLS, bool GATED>
 cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
-  const int blocks = (a.N - 1) / (FEW_WARPS * COLS) + 1;
-  return launch_dependent(linear_few_kernel<T, ROWS, COLS>, dim3(blocks), dim3(FEW_WARPS * 32), 0, s, a);
+  const int blocks = (a.N - 1) / (FEW_WARPS * (GATED ? 1 : COLS)) + 1;
+  return launch_dependent(linear_few_kernel<T, ROWS, COLS, GATED>, dim3(blocks), dim3(FEW_WARPS * 32), 0, s, a);
 }
 // Two columns per warp share what reading x costs where there are more columns than warps find a place.
 template <typename T, int ROWS>
 cudaError_t launch_cols(const LinearArgs& a, cudaStream_t s) {
-  return a.N > 152 * 16 ? launch<T, ROWS, 2>(a, s) : launch<T, ROWS, 1>(a, s);
+  return a.N > 152 * 16 ? launch<T, ROWS, 2, false>(a, s) : launch<T, ROWS, 1, false>(a, s);
 }
 template <typename T>
 cudaError_t launch_rows(const LinearArgs& a, cudaStream_t s) {
-  return a.M == 1 ? launch_cols<T, 1>(a, s) : a.M == 2 ? launch_cols<T, 2>(a, s) : a.M <= 4 ? launch_cols<T, 4>(a, s) : launch<T, 8, 1>(a, s);
+  return a.M == 1 ? launch_cols<T, 1>(a, s) : a.M == 2 ? launch_cols<T, 2>(a, s) : a.M <= 4 ? launch_cols<T, 4>(a, s) : launch<T, 8, 1, false>(a, s);
+}
+template <typename T>
+cudaError_t launch_gated_rows(const LinearArgs& a, cudaStream_t s) {
+  return a.M == 1   ? launch<T, 1, 2, true>(a, s)
+         : a.M == 2 ? launch<T, 2, 2, true>(a, s)
+         : a.M <= 4 ? launch<T, 4, 2, true>(a, s)
+                    : launch<T, 8, 2, true>(a, s);
 }
 
 }  // namespace
@@ -131,6 +152,34 @@ bool takes_few(const LinearArgs& a) {
 
 cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
+}
+
+bool takes_few(const GatedArgs& a) {
+  if (a.K % 8 != 0) return false;
+  const long long weights = 2ll * a.N * a.K;
+  if (a.M <= 2) return true;
+  if (a.M <= 4) return weights <= 1 << 23;
+  return a.M <= 8 && weights <= 1 << 22 && a.K <= 3000;
+}
+
+cudaError_t launch_few(const GatedArgs& g, cudaStream_t s) {
+  LinearArgs a{};
+  a.M = g.M;
+  a.N = g.N;
+  a.K = g.K;
+  a.out_dtype = g.out_dtype;
+  a.bias_dtype = g.bias_dtype;
+  a.act = g.act;
+  a.ld_x = g.ld_x;
+  a.ld_w = g.ld_w;
+  a.ld_y = g.ld_h;
+  a.x = g.x;
+  a.w = g.w;
+  a.bias = g.bias;
+  a.y = g.h;
+  a.z = g.z;
+  a.hdr = g.hdr;
+  return g.dtype == MOE_DTYPE_BF16 ? launch_gated_rows<__nv_bfloat16>(a, s) : launch_gated_rows<__half>(a, s);
 }
 
 }  // namespace lin

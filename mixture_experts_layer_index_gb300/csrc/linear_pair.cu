@@ -49,6 +49,7 @@ struct PairProduct {
   int R, C, nk;
   int nR, nC;
   int a_mn, b_mn;  // operand rows / cols contiguous along r / c
+  int half;        // gated: rows of the gate in the column operand
 };
 // A launch computes one product, or two whose epilogues differ in their output only
 // (the gradient's two), `prod[0]` the one with the longer sum.
@@ -128,11 +129,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
 
 // Tile t's first row and column: groups of 8 row tiles, column by column within a
 // group, so that the pairs in flight share both operands in L2.
+template <int TILE_COLS>
 __device__ __forceinline__ void tile_origin(const PairProduct& p, int t, int& r0, int& c0) {
   constexpr int GR = 8;
   const int group = t / (GR * p.nC), in_group = t - group * (GR * p.nC);
   const int rows_here = min(GR, p.nR - group * GR);
-  c0 = in_group / rows_here * TILE;
+  c0 = in_group / rows_here * TILE_COLS;
   r0 = (group * GR + in_group % rows_here) * TILE;
 }
 
@@ -240,6 +242,119 @@ __device__ __forceinline__ void add16(float (&v)[16], const void* p, int dtype, 
   }
 }
 
+// 16 values into row `lane` of a box of 32 rows of 64 bytes (16-bit values; the 64-byte swizzle
+// has chunk j of a row at chunk j ^ (row / 2 & 3)).  `part`: which 16 of the box's 32 columns.
+__device__ __forceinline__ void put_half_box(uint8_t* box, int lane, int part, int dtype, const float* v) {
+  uint8_t* row = box + lane * 64;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t w[4];
+    if (dtype == MOE_DTYPE_BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 b = __floats2half2_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    *reinterpret_cast<uint4*>(row + (((part * 2 + j) ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The epilogue of a gated tile for one warp: 32 rows, 32 gate columns and the 32 up columns beside
+// them, both in registers at once; z in two boxes of 64-byte rows, h in one (or one of 128-byte
+// rows of fp32 values).  p.y_tma, p.z_tma as elsewhere; m1.y is the up half of z.
+__device__ __forceinline__ void gated_tile(const PairParams& p, const CUtensorMap* mh, const CUtensorMap* mg,
+                                           const CUtensorMap* mu, uint8_t* box, int lane, uint32_t tb, uint32_t free_bar,
+                                           int r0, int c0, bool bias_wide) {
+  const Epilogue& ep = p.ep;
+  const int R = p.prod[0].R, C = p.prod[0].C;
+  float g[32], u[32];
+  tmem_ld32(tb, g);
+  tmem_ld32(tb + HALF, u);
+  tmem_ld_wait_regs(g);
+  tmem_ld_wait_regs(u);
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive_cluster(free_bar);
+    bulk_wait_group_read0();
+  }
+  __syncwarp();
+  if (ep.bias) {  // the same for every lane
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      add16(*reinterpret_cast<float(*)[16]>(&g[16 * j]), ep.bias, ep.bias_dtype, c0 + 16 * j, C - c0 - 16 * j, bias_wide);
+      add16(*reinterpret_cast<float(*)[16]>(&u[16 * j]), ep.bias, ep.bias_dtype, static_cast<size_t>(p.prod[0].half) + c0 + 16 * j,
+            C - c0 - 16 * j, bias_wide);
+    }
+  }
+  const bool stored = r0 < R && c0 < C;
+  if (ep.z && p.z_tma) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      put_half_box(box, lane, j, ep.z_dtype, &g[16 * j]);
+      put_half_box(box + BOX_BYTES / 2, lane, j, ep.z_dtype, &u[16 * j]);
+    }
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (stored) {
+        tma_store_2d(mg, smem_u32(box), c0, r0);
+        tma_store_2d(mu, smem_u32(box + BOX_BYTES / 2), c0, r0);
+      }
+      bulk_commit_group();
+    }
+  } else if (ep.z) {
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float t[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = k ? u[16 * j + i] : g[16 * j + i];
+        put_box(box, lane, j, MOE_DTYPE_F32, t);
+      }
+      __syncwarp();
+      flush_box(box, lane, static_cast<uint8_t*>(ep.z) + (k ? static_cast<size_t>(p.prod[0].half) * 2 : 0), ep.z_dtype,
+                ep.ld_z, nullptr, r0, R, c0, C);
+    }
+  }
+  act_all<32>(g, ep.act);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) g[i] *= u[i];
+  if (ep.z && p.z_tma) {
+    if (lane == 0) bulk_wait_group_read0();
+    __syncwarp();
+  }
+  if (p.y_tma && ep.out_dtype != MOE_DTYPE_F32) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) put_half_box(box, lane, j, ep.out_dtype, &g[16 * j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) put_box(box, lane, j, MOE_DTYPE_F32, *reinterpret_cast<float(*)[16]>(&g[16 * j]));
+  }
+  if (p.y_tma) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (stored) tma_store_2d(mh, smem_u32(box), c0, r0);
+      bulk_commit_group();
+    }
+  } else {
+    __syncwarp();
+    flush_box(box, lane, ep.y, ep.out_dtype, ep.ld_y, nullptr, r0, R, c0, C);
+  }
+}
+
+// GATED: a tile is 256 rows x 128 columns of h, the even block's half of the column operand their
+// gate rows, the odd block's the up rows.
+template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     linear_pair_kernel(const __grid_constant__ PairMaps m0, const __grid_constant__ PairMaps m1,
                        const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ PairParams p) {
@@ -248,6 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFFSET);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr int TILE_COLS = GATED ? HALF : TILE;  // output columns of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + STAGES);
@@ -304,9 +420,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const CUtensorMap* mb = prod ? &m1.b : &m0.b;
       const bool a_mn = q.a_mn, b_mn = q.b_mn;
       int r0, c0;
-      tile_origin(q, tile, r0, c0);
+      tile_origin<TILE_COLS>(q, tile, r0, c0);
       r0 += rank * HALF;
-      c0 += rank * HALF;
+      c0 += rank * (GATED ? q.half : HALF);
       const int nk = q.nk;
       for (int kb = 0; kb < nk; ++kb) {
         if (!ready && !mbar_wait(empty0 + 8 * stage, phase, abort_flag, p.hdr, 0x610000u)) {
@@ -406,14 +522,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // that the epilogue's loads do not wait for memory.  Its wait is by parity like the
     // epilogue's, so it too says when it has seen a tile, before which the accumulator is not
     // filled again: two completions it had not looked at would read as none.
-    if (p.ep.residual) {
+    if (!GATED && p.ep.residual) {
       const size_t es = p.ep.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
       const uint32_t lead_tempty0 = map_rank(tempty0, 0);
       uint32_t acc = 0, acc_phase = 0;
       int prod, tile;
       for (int i = 0; pair_item(p, pair, npairs, i, prod, tile); ++i) {
         int r0, c0;
-        tile_origin(p.prod[prod], tile, r0, c0);
+        tile_origin<TILE_COLS>(p.prod[prod], tile, r0, c0);
         r0 += rank * HALF;
         const size_t row_bytes = static_cast<size_t>(min(TILE, p.prod[prod].C - c0)) * es;
         for (int r = lane; r < min(HALF, p.prod[prod].R - r0); r += 32) {
@@ -437,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const Epilogue& ep = p.ep;
     const bool wide = ep.out_dtype == MOE_DTYPE_F32;
     const bool plain = p.y_tma && !wide && !ep.bias && !ep.residual && !ep.z && ep.act == MOE_ACT_NONE && ep.alpha == 1.0f;
-    const bool bias_wide = reinterpret_cast<uintptr_t>(ep.bias) % 16 == 0;
+    const bool bias_wide = reinterpret_cast<uintptr_t>(ep.bias) % 16 == 0 && (!GATED || p.prod[0].half % 8 == 0);
     const bool residual_wide = reinterpret_cast<uintptr_t>(ep.residual) % 16 == 0;
     uint32_t acc = 0, acc_phase = 0;
     // the box may be written again once the store that read it has done so
@@ -450,15 +566,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int R = p.prod[prod].R, C = p.prod[prod].C;
       const CUtensorMap* my = prod ? &m1.y : &m0.y;
       int r0, c0;
-      tile_origin(p.prod[prod], tile, r0, c0);
+      tile_origin<TILE_COLS>(p.prod[prod], tile, r0, c0);
       r0 += rank * HALF + q * 32;  // this warp's rows and columns
-      c0 += h * EPI_COLS;
+      c0 += h * (TILE_COLS / 4);
       int good = 1;
       if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x640000u);
       good = __shfl_sync(0xffffffffu, good, 0);
       if (!good) break;
       tc_fence_after();
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * EPI_COLS;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * (TILE_COLS / 4);
+      if constexpr (GATED) {
+        gated_tile(p, my, &tmZ, &m1.y, box, lane, tb, lead_tempty0 + 8 * acc, r0, c0, bias_wide);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+        continue;
+      }
       const bool row_in = r0 + lane < R;
       // sum + bias of 16 columns from c0 + j * 16
       auto load_z = [&](int j, float(&v)[16]) {
@@ -563,38 +685,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// A store map: boxes of 32 rows of 128 bytes.
-bool encode_store(CUtensorMap* map, void* base, int dtype, int cols, int rows, long long ld) {
+// A store map: boxes of 32 rows of 128 bytes, or of 64.
+bool encode_store(CUtensorMap* map, void* base, int dtype, int cols, int rows, long long ld, uint32_t row_bytes = 128) {
   EncodeTiledFn fn = get_encode_tiled();
   if (!fn) return false;
   const uint32_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-  const cuuint32_t box[2] = {128 / es, 32};
+  const cuuint32_t box[2] = {row_bytes / es, 32};
   const cuuint32_t estr[2] = {1, 1};
   const CUtensorMapDataType type = dtype == MOE_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return fn(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool storable(const void* base, int dtype, long long ld) {
   return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
 }
 
+// Output columns per tile.
+int tile_cols(const Product& q) { return q.gated ? HALF : TILE; }
+
 bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
   pp->R = q.R;
   pp->C = q.C;
   pp->nk = (q.K + BK - 1) / BK;
   pp->nR = (q.R + TILE - 1) / TILE;
-  pp->nC = (q.C + TILE - 1) / TILE;
+  pp->nC = (q.C + tile_cols(q) - 1) / tile_cols(q);
+  pp->half = q.gated ? q.C : 0;
   pp->a_mn = q.rows_mn;
   pp->b_mn = q.cols_mn;
   return encode(&m->a, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : HALF) &&
          encode(&m->b, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn ? 64 : HALF) &&
          (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) ||
-          encode_store(&m->y, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y));
+          encode_store(&m->y, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y,
+                       q.gated && q.ep.out_dtype != MOE_DTYPE_F32 ? 64 : 128));
 }
 
 }  // namespace
@@ -603,7 +730,7 @@ bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
 // epilogue of a tile, of which all but the last overlaps the next tile's stages: 3.5 us,
 // and more with an activation, z, a residual, or rows that TMA cannot store.
 float pair_estimate(const Product& q) {
-  const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + TILE - 1) / TILE);
+  const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + tile_cols(q) - 1) / tile_cols(q));
   const float stages = 0.30f * ((q.K + BK - 1) / BK);
   float epilogue = 3.5f;
   if (q.ep.act != MOE_ACT_NONE) epilogue += 1.0f;
@@ -641,9 +768,22 @@ cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_
   p.z_tma = q0->ep.z && storable(q0->ep.z, q0->ep.z_dtype, q0->ep.ld_z);
   p.y[0] = q0->ep.y;
   p.y[1] = second ? second->ep.y : nullptr;
-  if (p.z_tma && !encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z)) return cudaErrorInvalidValue;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES));
+  if (q0->gated) {
+    uint8_t* up = static_cast<uint8_t*>(q0->ep.z) + static_cast<size_t>(q0->C) * 2;  // 16-bit values
+    p.z_tma = p.z_tma && storable(up, q0->ep.z_dtype, q0->ep.ld_z);
+    if (p.z_tma && (!encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z, 64) ||
+                    !encode_store(&m1.y, up, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z, 64)))
+      return cudaErrorInvalidValue;
+  } else if (p.z_tma && !encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z)) {
+    return cudaErrorInvalidValue;
+  }
+  static const cudaError_t attr = [] {
+    const cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(SMEM_BYTES));
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(linear_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(SMEM_BYTES));
+  }();
   if (attr != cudaSuccess) return attr;
   p.type = q0->type;
   p.ep = q0->ep;
@@ -651,7 +791,7 @@ cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_
   p.hdr = q0->hdr;
   const int tiles = p.tiles[0] + p.tiles[1];
   const int pairs = tiles < sms / 2 ? tiles : sms / 2;
-  return launch_dependent(linear_pair_kernel, dim3(2 * pairs), dim3(THREADS), SMEM_BYTES, s, m0, m1, tz, p);
+  return launch_dependent(q0->gated ? linear_pair_kernel<true> : linear_pair_kernel<false>, dim3(2 * pairs), dim3(THREADS), SMEM_BYTES, s, m0, m1, tz, p);
 }
 
 }  // namespace lin

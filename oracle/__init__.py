@@ -16,6 +16,8 @@ written in numpy:
                    128x128-blockwise FP8), and the weighted top-k combine.
   * ``blocks``   - the operators around the forward, in 64 bits: routing rules,
                    block norms, the linear layer, and their gradients.
+  * ``dense``    - the dense blocks' operators, in 64 bits: the gated layer and its
+                   gradient, quantisation in blocks of 128.
 
 The steps follow the expert-grouped pipeline described in the Motivation
 section of "perf: add small-batch route MMA for MoE" (group the routes by
