@@ -21,7 +21,7 @@
 // product reaches 1.95 in short runs, 1.74 under the power limit).  With a GELU and its
 // argument kept 400 us: 16 warps' worth of epilogue instructions beside the MMAs and a
 // second output; a residual or an odd width (plain stores) cost similar shares.
-#include "linear.cuh"
+#include "linear_pair.cuh"
 
 namespace moe {
 namespace lin {
@@ -34,7 +34,6 @@ constexpr int OP_BYTES = HALF * BK * 2;
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int EPI_WARPS = 16;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
-constexpr int BOX_BYTES = 32 * 128;            // 32 rows of 128 bytes
 constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
 constexpr int EPI_COLS = TILE / (EPI_WARPS / 4);  // columns per epilogue warp
 static_assert(EPI_COLS == 64, "an epilogue warp fills one box of 16-bit values");
@@ -93,40 +92,6 @@ __device__ __forceinline__ bool pair_item(const PairParams& p, int pair, int npa
   return tile < p.tiles[1];
 }
 
-// ------------------------------------------------------------------ two-SM forms
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-// A load into this block's shared memory that counts on a barrier of the pair's even block.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on the barrier at this offset in both blocks once the MMAs issued so far are done.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
-}
-
 // Tile t's first row and column: groups of 8 row tiles, column by column within a
 // group, so that the pairs in flight share both operands in L2.
 template <int TILE_COLS>
@@ -136,134 +101,6 @@ __device__ __forceinline__ void tile_origin(const PairProduct& p, int t, int& r0
   const int rows_here = min(GR, p.nR - group * GR);
   c0 = in_group / rows_here * TILE_COLS;
   r0 = (group * GR + in_group % rows_here) * TILE;
-}
-
-// 16 values (columns c.. of one row) into row `lane` of a swizzled box: 16-byte chunk j of a
-// row sits at chunk j ^ (lane & 7).  `part`: which 16 of the box's columns.
-__device__ __forceinline__ void put_box(uint8_t* box, int lane, int part, int dtype, const float (&v)[16]) {
-  uint8_t* row = box + lane * 128;
-  if (dtype == MOE_DTYPE_F32) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(row + (((part * 4 + j) ^ (lane & 7)) << 4)) =
-          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t w[4];
-      if (dtype == MOE_DTYPE_BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2 b = __floats2half2_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-      }
-      *reinterpret_cast<uint4*>(row + (((part * 2 + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-}
-
-// Columns c.. c + 31 of a box of fp32 values (32 rows from r0) to an array whose rows TMA
-// cannot store: a row at a time, one lane per column, plus the residual's values.  Not
-// inlined: its registers would be spilled from the paths that TMA stores.
-template <typename T>
-__device__ __forceinline__ void flush_box_as(const uint8_t* box, int lane, T* out, long long ld, const T* residual,
-                                             int r0, int R, int c, int C) {
-  const int rows = c + lane < C ? min(32, R - r0) : 0;
-  const size_t at = static_cast<size_t>(r0) * ld + c + lane;
-  out += at;
-  if (residual) residual += at;
-#pragma unroll 1
-  for (int r = 0; r < rows; r += 16) {
-    T u[16] = {};
-    if (residual) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (r + i < rows) u[i] = residual[i * ld];
-      residual += 16 * ld;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (r + i < rows) {
-        float v = *reinterpret_cast<const float*>(box + (r + i) * 128 + (((lane >> 2) ^ ((r + i) & 7)) << 4) + (lane & 3) * 4);
-        if (residual) v += as_float(u[i]);
-        out[i * ld] = as_type<T>(v);
-      }
-    out += 16 * ld;
-  }
-  __syncwarp();  // the box may be written again
-}
-__device__ __noinline__ void flush_box(const uint8_t* box, int lane, void* out, int dtype, long long ld,
-                                          const void* residual, int r0, int R, int c, int C) {
-  if (dtype == MOE_DTYPE_F32)
-    flush_box_as(box, lane, static_cast<float*>(out), ld, static_cast<const float*>(residual), r0, R, c, C);
-  else if (dtype == MOE_DTYPE_BF16)
-    flush_box_as(box, lane, static_cast<__nv_bfloat16*>(out), ld, static_cast<const __nv_bfloat16*>(residual), r0, R, c, C);
-  else
-    flush_box_as(box, lane, static_cast<__half*>(out), ld, static_cast<const __half*>(residual), r0, R, c, C);
-}
-
-// v[i] += p[at + i], 16 values of which `n` exist; `wide`: p + at is 16-byte aligned.
-__device__ __forceinline__ void add16(float (&v)[16], const void* p, int dtype, size_t at, int n, bool wide) {
-  if (n < 16 || !wide) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) v[i] += load_as_f32(p, dtype, at + i);
-  } else if (dtype == MOE_DTYPE_F32) {
-    float4 f[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at)[j];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[4 * j] += f[j].x; v[4 * j + 1] += f[j].y; v[4 * j + 2] += f[j].z; v[4 * j + 3] += f[j].w;
-    }
-  } else {
-    uint4 raw[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) raw[j] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at)[j];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = dtype == MOE_DTYPE_BF16
-                             ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
-                             : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[8 * j + 2 * i] += f.x;
-        v[8 * j + 2 * i + 1] += f.y;
-      }
-    }
-  }
-}
-
-// 16 values into row `lane` of a box of 32 rows of 64 bytes (16-bit values; the 64-byte swizzle
-// has chunk j of a row at chunk j ^ (row / 2 & 3)).  `part`: which 16 of the box's 32 columns.
-__device__ __forceinline__ void put_half_box(uint8_t* box, int lane, int part, int dtype, const float* v) {
-  uint8_t* row = box + lane * 64;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t w[4];
-    if (dtype == MOE_DTYPE_BF16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 b = __floats2half2_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-    }
-    *reinterpret_cast<uint4*>(row + (((part * 2 + j) ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
 }
 
 // The epilogue of a gated tile for one warp: 32 rows, 32 gate columns and the 32 up columns beside
@@ -685,26 +522,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-// A store map: boxes of 32 rows of 128 bytes, or of 64.
-bool encode_store(CUtensorMap* map, void* base, int dtype, int cols, int rows, long long ld, uint32_t row_bytes = 128) {
-  EncodeTiledFn fn = get_encode_tiled();
-  if (!fn) return false;
-  const uint32_t es = dtype == MOE_DTYPE_F32 ? 4 : 2;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-  const cuuint32_t box[2] = {row_bytes / es, 32};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType type = dtype == MOE_DTYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                   : dtype == MOE_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return fn(map, type, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool storable(const void* base, int dtype, long long ld) {
-  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld * (dtype == MOE_DTYPE_F32 ? 4 : 2) % 16 == 0;
-}
-
 // Output columns per tile.
 int tile_cols(const Product& q) { return q.gated ? HALF : TILE; }
 
@@ -719,7 +536,7 @@ bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
   pp->b_mn = q.cols_mn;
   return encode(&m->a, q.rows.base, q.type, q.rows.inner, q.rows.outer, q.rows.ld, 64, q.rows_mn ? 64 : HALF) &&
          encode(&m->b, q.cols.base, q.type, q.cols.inner, q.cols.outer, q.cols.ld, 64, q.cols_mn ? 64 : HALF) &&
-         (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y) ||
+         (!storable(q.ep.y, q.ep.out_dtype, q.C, q.ep.ld_y) ||
           encode_store(&m->y, q.ep.y, q.ep.out_dtype, q.C, q.R, q.ep.ld_y,
                        q.gated && q.ep.out_dtype != MOE_DTYPE_F32 ? 64 : 128));
 }
@@ -735,8 +552,8 @@ float pair_estimate(const Product& q) {
   float epilogue = 3.5f;
   if (q.ep.act != MOE_ACT_NONE) epilogue += 1.0f;
   if (q.ep.residual) epilogue += 4.3f;
-  if (!storable(q.ep.y, q.ep.out_dtype, q.ep.ld_y)) epilogue += 4.0f;
-  if (q.ep.z) epilogue += storable(q.ep.z, q.ep.z_dtype, q.ep.ld_z) ? 1.5f : 5.5f;
+  if (!storable(q.ep.y, q.ep.out_dtype, q.C, q.ep.ld_y)) epilogue += 4.0f;
+  if (q.ep.z) epilogue += storable(q.ep.z, q.ep.z_dtype, q.C, q.ep.ld_z) ? 1.5f : 5.5f;
   const long long waves = (tiles + 75) / 76;
   return 4.0f + stages + epilogue + (waves - 1) * (stages > epilogue ? stages : epilogue);
 }
@@ -763,14 +580,14 @@ cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_
     p.ratio = (p.prod[0].nk + p.prod[1].nk / 2) / p.prod[1].nk;
   }
   // two products are stored the same way
-  p.y_tma = storable(q0->ep.y, q0->ep.out_dtype, q0->ep.ld_y) &&
-            (!second || storable(second->ep.y, second->ep.out_dtype, second->ep.ld_y));
-  p.z_tma = q0->ep.z && storable(q0->ep.z, q0->ep.z_dtype, q0->ep.ld_z);
+  p.y_tma = storable(q0->ep.y, q0->ep.out_dtype, q0->C, q0->ep.ld_y) &&
+            (!second || storable(second->ep.y, second->ep.out_dtype, second->C, second->ep.ld_y));
+  p.z_tma = q0->ep.z && storable(q0->ep.z, q0->ep.z_dtype, q0->C, q0->ep.ld_z);
   p.y[0] = q0->ep.y;
   p.y[1] = second ? second->ep.y : nullptr;
   if (q0->gated) {
     uint8_t* up = static_cast<uint8_t*>(q0->ep.z) + static_cast<size_t>(q0->C) * 2;  // 16-bit values
-    p.z_tma = p.z_tma && storable(up, q0->ep.z_dtype, q0->ep.ld_z);
+    p.z_tma = p.z_tma && storable(up, q0->ep.z_dtype, q0->C, q0->ep.ld_z);
     if (p.z_tma && (!encode_store(&tz, q0->ep.z, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z, 64) ||
                     !encode_store(&m1.y, up, q0->ep.z_dtype, q0->C, q0->R, q0->ep.ld_z, 64)))
       return cudaErrorInvalidValue;

@@ -257,3 +257,19 @@ def test_linear_single_row_gradient(m, act, dtype, out, N, K):
     close(dx, "dx", dz @ np.abs(f64(w)), N / 8 + 16, u)
     close(dw, "dw", dz.T * np.abs(f64(x)), 16, u)
     close(db, "dbias", slope[0], 16, 0.0)
+
+
+# large tiles whose rows start at 16-byte boundaries and end inside 16 bytes: what lies between two
+# rows stays as it was
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("N", [2049, 2054, 2055])
+def test_linear_large_tiles_leave_what_lies_between_rows(m, dtype, out, N):
+    M, K, ld = 2048, 256, 2064
+    g = gen(N)
+    x, w = rows(M, K, K, DT[dtype], g), rows(N, K, K, DT[dtype], g)
+    y = torch.full((M, ld), float("nan"), dtype=DT[out], device=DEV)
+    p = m.linear_problem(M, N, K, code(m, dtype), code(m, out), ld_y=ld)
+    ws = torch.empty(m.moe_linear_workspace_size(p), dtype=torch.uint8, device=DEV)
+    m.moe_linear(p, x, w, None, None, y[:, :N], None, ws)
+    assert m.moe_read_device_status(ws) == m.MOE_OK
+    assert torch.isnan(y[:, N:]).all() and not torch.isnan(y[:, :N]).any()

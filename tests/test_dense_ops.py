@@ -117,6 +117,9 @@ def test_gated_strides(m):  # noqa: F811
     gated_case(m, 50, 77, 100, bias="f32", ld_x=104, ld_w=112, ld_h=81)
     gated_case(m, 50, 77, 3, "gelu", keep_z=True, ld_x=8, ld_w=16, ld_h=80)
     gated_case(m, 1300, 1040, 130, ld_x=136, ld_w=136, ld_h=1048, keep_z=True, gradient=False)
+    for N in (1025, 1030, 1035):  # rows that end inside 16 bytes
+        gated_case(m, 1300, N, 136, ld_h=1048, keep_z=True, gradient=False)
+        gated_case(m, 1300, N, 136, out="f32", ld_h=1048, gradient=False)
 
 
 @pytest.mark.parametrize("M,N,K", [(517, 136, 100), (517, 133, 104), (40, 8, 64)])
