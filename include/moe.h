@@ -34,7 +34,8 @@
  *     moe_route / moe_shuffle / moe_tile_map / moe_forward / moe_forward_ex /
  *     moe_forward_routed / moe_round_bf16 / moe_route_ex / moe_route_backward /
  *     moe_norm_forward / moe_norm_backward / moe_linear / moe_linear_backward /
- *     moe_gated / moe_gated_backward: work is enqueued on `stream` in order, with no device-to-host copy, so these calls can be
+ *     moe_gated / moe_gated_backward / moe_quantise / moe_linear_fp8 /
+ *     moe_gated_fp8: work is enqueued on `stream` in order, with no device-to-host copy, so these calls can be
  *     captured in a CUDA graph.  Inputs are never written.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
  *   - A process uses the library on one device, the one current at its first call.
@@ -558,6 +559,55 @@ size_t moe_gated_backward_workspace_size(const moe_gated_problem* p);
 moe_status moe_gated_backward(const moe_gated_problem* p, const void* dh, const void* x, const void* w, const void* z,
                               void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- e4m3 with block scales
+ * The format of MOE_FP8_BLOCK128 for dense layers: e4m3 codes with fp32 scales, one per (row,
+ * 128 columns) for activations, one per 128 x 128 block for weights.  Rows of codes lie ld
+ * bytes apart.
+ *
+ * moe_quantise - s = amax / 448 (fp32; 1 where that is 0), q = e4m3(x / s) of the IEEE quotient,
+ * to nearest even:
+ *   x [M, K] of dtype (f32, bf16, fp16), ld_x, any alignment
+ *   q [M, K] codes out, ld_q;  scale [ceil(M / block_rows), ceil(K / 128)] fp32 out
+ *   block_rows: 1 (activations) or 128 (weights); blocks end at M and K
+ * A NaN has no part in amax and becomes a NaN code; an infinity makes its block's scale infinite
+ * and its codes 0 or NaN, so that products with it are NaN.  No workspace.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+  int M, K;
+  int dtype;      /* of x */
+  int block_rows; /* 1 or 128 */
+  long long ld_x, ld_q;
+} moe_quantise_problem;
+moe_status moe_quantise(const moe_quantise_problem* p, const void* x, uint8_t* q, float* scale, moe_stream_t stream);
+
+/* moe_linear_fp8 - moe_linear on such operands (inference: there is no z and no gradient):
+ *   z[m][n] = sum over groups kb of 128 of x_scale[m][kb] w_scale[n / 128][kb] (sum of x q in kb)
+ *   y = alpha * act(z + bias) + residual, fp32 accumulation, one rounding
+ * p->dtype is MOE_DTYPE_E4M3; out_dtype, bias_dtype, act, alpha and ld_y as in moe_linear
+ *   x [M, K], w [N, K] codes, ld_x / ld_w: multiples of 16, bases 16-byte aligned; K is free
+ *   x_scale [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)] fp32
+ * Every group's products are summed by themselves, so any scales are taken.
+ * ws: moe_linear_fp8_workspace_size(p) bytes, 256-byte aligned: the status word, as moe_linear's.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+size_t moe_linear_fp8_workspace_size(const moe_linear_problem* p);
+moe_status moe_linear_fp8(const moe_linear_problem* p, const void* x, const float* x_scale, const void* w,
+                          const float* w_scale, const void* bias, const void* residual, void* y, void* ws,
+                          size_t ws_bytes, moe_stream_t stream);
+
+/* moe_gated_fp8 - moe_gated on such operands (no z, no gradient):
+ *   p->dtype is MOE_DTYPE_E4M3;  x, x_scale as in moe_linear_fp8
+ *   w [2 N, K] codes;  w_scale [2, ceil(N / 128), ceil(K / 128)]: the gate rows and the up rows
+ *     are quantised apart
+ *   h [M, N] of out_dtype, ld_h; h_scale NULL
+ *   out_dtype MOE_DTYPE_E4M3: h in codes (ld_h a multiple of 16, base 16-byte aligned), h_scale
+ *     [M, ceil(N / 128)] fp32: moe_quantise's rule on the unrounded fp32 h, the operand of a
+ *     following moe_linear_fp8
+ * ws: moe_gated_fp8_workspace_size(p) bytes, 256-byte aligned.  Errors: as moe_linear_fp8. */
+size_t moe_gated_fp8_workspace_size(const moe_gated_problem* p);
+moe_status moe_gated_fp8(const moe_gated_problem* p, const void* x, const float* x_scale, const void* w,
+                         const float* w_scale, const void* bias, void* h, float* h_scale, void* ws, size_t ws_bytes,
+                         moe_stream_t stream);
+
 /* ---------------------------------------------------------------- diagnostics
  * moe_read_device_status - synchronises `stream`, then returns the status
  * recorded on the device in the status word at the head of `ws` (MOE_OK,
@@ -587,7 +637,7 @@ moe_status moe_read_device_status(const void* ws, moe_stream_t stream);
  * rd_prep, rd_gateup, rd_reduce, rd_down, combine (route-direct path); scatter,
  * tile_map, header_reset; route_ex, route_backward, norm_forward, norm_backward,
  * linear, linear_dz, linear_dx, linear_dw, linear_dx_dw, column_sums; gated, gated_dz
- * (a gated gradient's products are timed as the linear layer's). */
+ * (a gated gradient's products are timed as the linear layer's), quantise, linear_fp8, gated_fp8. */
 typedef struct {
   char name[32];
   double total_ms;

@@ -111,12 +111,17 @@ class moe_gated_problem(ctypes.Structure):
                 ("ld_x", _ll), ("ld_w", _ll), ("ld_h", _ll)]
 
 
+class moe_quantise_problem(ctypes.Structure):
+    _fields_ = [("M", _i), ("K", _i), ("dtype", _i), ("block_rows", _i), ("ld_x", _ll), ("ld_q", _ll)]
+
+
 _P = ctypes.POINTER(moe_problem)
 _O = ctypes.POINTER(moe_forward_options)
 _RO = ctypes.POINTER(moe_route_options)
 _NP = ctypes.POINTER(moe_norm_problem)
 _LP = ctypes.POINTER(moe_linear_problem)
 _GP = ctypes.POINTER(moe_gated_problem)
+_QP = ctypes.POINTER(moe_quantise_problem)
 _SIGS = {
     "moe_route": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp]),
     "moe_shuffle_workspace_size": (_sz, [_i, _i, _i]),
@@ -150,6 +155,11 @@ _SIGS = {
     "moe_gated": (_i, [_GP] + [_vp] * 6 + [_sz, _vp]),
     "moe_gated_backward_workspace_size": (_sz, [_GP]),
     "moe_gated_backward": (_i, [_GP] + [_vp] * 8 + [_sz, _vp]),
+    "moe_quantise": (_i, [_QP] + [_vp] * 4),
+    "moe_linear_fp8_workspace_size": (_sz, [_LP]),
+    "moe_linear_fp8": (_i, [_LP] + [_vp] * 8 + [_sz, _vp]),
+    "moe_gated_fp8_workspace_size": (_sz, [_GP]),
+    "moe_gated_fp8": (_i, [_GP] + [_vp] * 8 + [_sz, _vp]),
     "moe_read_device_status": (_i, [_vp, _vp]),
     "moe_profile_start": (_i, []),
     "moe_profile_start_stage": (_i, [ctypes.c_char_p]),
@@ -507,6 +517,42 @@ def moe_gated_backward(p: moe_gated_problem, dh, x, w, z, dx, dw, dbias, ws, ws_
     _check(lib().moe_gated_backward(p, _rows(dh, "dh", p.N, p.ld_h), _rows(x, "x", K, p.ld_x), _rows(w, "w", K, p.ld_w),
                                     _ptr(z), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(ws), nb, _stream(stream)),
            "moe_gated_backward")
+
+
+def quantise_problem(M, K, dtype=MOE_DTYPE_BF16, block_rows=1, ld_x=0, ld_q=0) -> moe_quantise_problem:
+    return moe_quantise_problem(M, K, dtype, block_rows, ld_x, ld_q)
+
+
+def moe_quantise(p: moe_quantise_problem, x, q, scale, stream=None) -> None:
+    """e4m3 codes q and fp32 scales of x, per (row, 128 columns) or per 128 x 128 block."""
+    _check(lib().moe_quantise(p, _rows(x, "x", p.K, p.ld_x), _rows(q, "q", p.K, p.ld_q), _ptr(scale), _stream(stream)),
+           "moe_quantise")
+
+
+def moe_linear_fp8_workspace_size(p: moe_linear_problem) -> int:
+    return int(lib().moe_linear_fp8_workspace_size(p))
+
+
+def moe_linear_fp8(p: moe_linear_problem, x, x_scale, w, w_scale, bias, residual, y, ws, ws_bytes=None, stream=None) -> None:
+    """y = alpha act(x w^T + bias) + residual for e4m3 operands with block scales."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    N, K, ld_y = p.N, p.K, p.ld_y
+    _check(lib().moe_linear_fp8(p, _rows(x, "x", K, p.ld_x), _ptr(x_scale), _rows(w, "w", K, p.ld_w), _ptr(w_scale),
+                                _ptr(bias), _rows(residual, "residual", N, ld_y), _rows(y, "y", N, ld_y), _ptr(ws), nb,
+                                _stream(stream)), "moe_linear_fp8")
+
+
+def moe_gated_fp8_workspace_size(p: moe_gated_problem) -> int:
+    return int(lib().moe_gated_fp8_workspace_size(p))
+
+
+def moe_gated_fp8(p: moe_gated_problem, x, x_scale, w, w_scale, bias, h, h_scale, ws, ws_bytes=None, stream=None) -> None:
+    """moe_gated for e4m3 operands with block scales; h in codes with h_scale, or in out_dtype with None."""
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    K = p.K
+    _check(lib().moe_gated_fp8(p, _rows(x, "x", K, p.ld_x), _ptr(x_scale), _rows(w, "w", K, p.ld_w), _ptr(w_scale),
+                               _ptr(bias), _rows(h, "h", p.N, p.ld_h), _ptr(h_scale), _ptr(ws), nb, _stream(stream)),
+           "moe_gated_fp8")
 
 
 def moe_read_device_status(ws, stream=None) -> int:

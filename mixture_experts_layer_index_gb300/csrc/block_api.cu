@@ -129,6 +129,43 @@ moe_status check_gated(const moe_gated_problem* p) {
                                                                                                   : MOE_ERR_UNSUPPORTED;
 }
 
+// ------------------------------------------------------------------ e4m3 with block scales
+moe_status check_quantise(const moe_quantise_problem* p) {
+  if (!p || p->M < 0 || p->K < 1 || !is_dtype(p->dtype) || (p->block_rows != 1 && p->block_rows != 128))
+    return MOE_ERR_INVALID_ARG;
+  if ((p->ld_x != 0 && p->ld_x < p->K) || (p->ld_q != 0 && p->ld_q < p->K)) return MOE_ERR_INVALID_ARG;
+  const long long blocks = (static_cast<long long>(p->M) + 127) / 128 * ((static_cast<long long>(p->K) + 127) / 128);
+  return p->M > (1 << 30) || p->K > (1 << 30) || blocks >= (1ll << 31) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// Strides that TMA takes, and sizes whose grids (64 columns x 128 rows, up to eight blocks) stay below 2^31.
+bool codes_fit(long long M, long long N, long long K, long long ld_x, long long ld_w) {
+  if (ld_x % 16 || ld_w % 16 || ld_x >= (1ll << 39) || ld_w >= (1ll << 39)) return false;
+  if (M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return false;
+  return (N / 64 + 1) * (M / 128 + 1) * 8 < (1ll << 31);
+}
+
+moe_status check_linear_fp8(const moe_linear_problem* p) {
+  if (!p || p->M < 0 || p->N < 0 || p->K < 1 || p->dtype != MOE_DTYPE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (!is_dtype(p->out_dtype) || !is_dtype(p->bias_dtype)) return MOE_ERR_INVALID_ARG;
+  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_GELU_TANH || !std::isfinite(p->alpha)) return MOE_ERR_INVALID_ARG;
+  if ((p->ld_x != 0 && p->ld_x < p->K) || (p->ld_w != 0 && p->ld_w < p->K) || (p->ld_y != 0 && p->ld_y < p->N))
+    return MOE_ERR_INVALID_ARG;
+  return codes_fit(p->M, p->N, p->K, p->ld_x ? p->ld_x : p->K, p->ld_w ? p->ld_w : p->K) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
+moe_status check_gated_fp8(const moe_gated_problem* p) {
+  if (!p || p->M < 0 || p->N < 0 || p->K < 1 || p->dtype != MOE_DTYPE_E4M3) return MOE_ERR_INVALID_ARG;
+  if ((!is_dtype(p->out_dtype) && p->out_dtype != MOE_DTYPE_E4M3) || !is_dtype(p->bias_dtype)) return MOE_ERR_INVALID_ARG;
+  if (p->act < MOE_ACT_NONE || p->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  if ((p->ld_x != 0 && p->ld_x < p->K) || (p->ld_w != 0 && p->ld_w < p->K) || (p->ld_h != 0 && p->ld_h < p->N))
+    return MOE_ERR_INVALID_ARG;
+  if (p->out_dtype == MOE_DTYPE_E4M3 && (p->ld_h ? p->ld_h : p->N) % 16) return MOE_ERR_UNSUPPORTED;
+  if (p->N > (1 << 29)) return MOE_ERR_UNSUPPORTED;
+  return codes_fit(p->M, 2ll * p->N, p->K, p->ld_x ? p->ld_x : p->K, p->ld_w ? p->ld_w : p->K) ? MOE_OK
+                                                                                               : MOE_ERR_UNSUPPORTED;
+}
+
 constexpr size_t kHeaderBytes = 256;
 
 // An empty problem needs no workspace, but where one is given its status is this call's.
@@ -419,6 +456,91 @@ moe_status moe_gated_backward(const moe_gated_problem* p, const void* dh, const 
   a.dz = base + L.dz;
   a.hdr = static_cast<DeviceHeader*>(ws);
   return from_cuda(launch_gated_backward(a, s));
+}
+
+moe_status moe_quantise(const moe_quantise_problem* p, const void* x, uint8_t* q, float* scale, moe_stream_t stream) {
+  const moe_status st = check_quantise(p);
+  if (st != MOE_OK) return st;
+  if (p->M == 0) return MOE_OK;
+  if (!x || !q || !scale || !fits(x, p->dtype) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARG;
+  const QuantiseArgs a{p->M, p->K, p->dtype, p->block_rows, p->ld_x ? p->ld_x : p->K, p->ld_q ? p->ld_q : p->K, x, q, scale};
+  return from_cuda(launch_quantise(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_linear_fp8_workspace_size(const moe_linear_problem* p) {
+  return check_linear_fp8(p) == MOE_OK ? kHeaderBytes : 0;
+}
+
+moe_status moe_linear_fp8(const moe_linear_problem* p, const void* x, const float* x_scale, const void* w,
+                          const float* w_scale, const void* bias, const void* residual, void* y, void* ws,
+                          size_t ws_bytes, moe_stream_t stream) {
+  const moe_status st = check_linear_fp8(p);
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->M == 0 || p->N == 0) return from_cuda(clear_status(ws, ws_bytes, s));
+  if (!x || !w || !x_scale || !w_scale || !y || !aligned(x, 16) || !aligned(w, 16) || !aligned(x_scale, 4) ||
+      !aligned(w_scale, 4) || !fits(y, p->out_dtype) || !fits(residual, p->out_dtype) || !fits(bias, p->bias_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < kHeaderBytes) return MOE_ERR_WORKSPACE;
+  Fp8Args a{};
+  a.M = p->M;
+  a.N = p->N;
+  a.K = p->K;
+  a.out_dtype = p->out_dtype;
+  a.bias_dtype = p->bias_dtype;
+  a.act = p->act;
+  a.alpha = p->alpha;
+  a.ld_x = p->ld_x ? p->ld_x : p->K;
+  a.ld_w = p->ld_w ? p->ld_w : p->K;
+  a.ld_y = p->ld_y ? p->ld_y : p->N;
+  a.x = x;
+  a.x_scale = x_scale;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.residual = residual;
+  a.y = y;
+  a.hdr = static_cast<DeviceHeader*>(ws);
+  return from_cuda(launch_linear_fp8(a, s));
+}
+
+size_t moe_gated_fp8_workspace_size(const moe_gated_problem* p) { return check_gated_fp8(p) == MOE_OK ? kHeaderBytes : 0; }
+
+moe_status moe_gated_fp8(const moe_gated_problem* p, const void* x, const float* x_scale, const void* w,
+                         const float* w_scale, const void* bias, void* h, float* h_scale, void* ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+  const moe_status st = check_gated_fp8(p);
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p->M == 0 || p->N == 0) return from_cuda(clear_status(ws, ws_bytes, s));
+  const bool codes = p->out_dtype == MOE_DTYPE_E4M3;
+  if (!x || !w || !x_scale || !w_scale || !h || !aligned(x, 16) || !aligned(w, 16) || !aligned(x_scale, 4) ||
+      !aligned(w_scale, 4) || !fits(bias, p->bias_dtype))
+    return MOE_ERR_INVALID_ARG;
+  if (codes != (h_scale != nullptr) || !aligned(h_scale, 4) || !(codes ? aligned(h, 16) : fits(h, p->out_dtype)))
+    return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < kHeaderBytes) return MOE_ERR_WORKSPACE;
+  Fp8Args a{};
+  a.M = p->M;
+  a.N = p->N;
+  a.K = p->K;
+  a.gated = true;
+  a.out_dtype = p->out_dtype;
+  a.bias_dtype = p->bias_dtype;
+  a.act = p->act;
+  a.alpha = 1.0f;
+  a.ld_x = p->ld_x ? p->ld_x : p->K;
+  a.ld_w = p->ld_w ? p->ld_w : p->K;
+  a.ld_y = p->ld_h ? p->ld_h : p->N;
+  a.x = x;
+  a.x_scale = x_scale;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.y = h;
+  a.h_scale = h_scale;
+  a.hdr = static_cast<DeviceHeader*>(ws);
+  return from_cuda(launch_linear_fp8(a, s));
 }
 
 }  // extern "C"

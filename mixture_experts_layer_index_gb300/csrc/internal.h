@@ -322,6 +322,36 @@ struct GatedBackwardArgs {
 };
 cudaError_t launch_gated_backward(const GatedBackwardArgs& a, cudaStream_t s);
 
+// Quantisation in blocks of 128 (quantise.cu).
+struct QuantiseArgs {
+  int M, K;
+  int dtype, block_rows;
+  long long ld_x, ld_q;
+  const void* x;
+  uint8_t* q;
+  float* scale;
+};
+cudaError_t launch_quantise(const QuantiseArgs& a, cudaStream_t s);
+
+// Linear and gated layers on e4m3 operands with block scales (linear_fp8.cu).
+struct Fp8Args {
+  int M, N, K;
+  bool gated;
+  int out_dtype, bias_dtype, act;
+  float alpha;
+  long long ld_x, ld_w, ld_y;
+  const void* x;
+  const float* x_scale;
+  const void* w;
+  const float* w_scale;
+  const void* bias;
+  const void* residual;
+  void* y;         // gated: h
+  float* h_scale;  // gated, e4m3 output
+  DeviceHeader* hdr;
+};
+cudaError_t launch_linear_fp8(const Fp8Args& a, cudaStream_t s);
+
 // Launch `kernel` as a programmatic dependent of the previous work on the stream:
 // its launch is prepared while the predecessor runs, and it waits for the
 // predecessor on the device (dep_wait) before touching its results.

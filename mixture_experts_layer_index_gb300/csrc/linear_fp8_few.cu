@@ -1,0 +1,218 @@
+// Products of e4m3 operands with block scales for up to 16 rows of x: bound by reading w once.
+//
+// A block takes 16 output columns, its eight warps every eighth group of 128 of the sum, weights
+// straight from memory to registers, 16 bytes a lane and row, 64 consecutive bytes of a row at a
+// time.  mma.sync.m16n8k32 multiplies 16 weight rows (M) with 8 rows of x (N); the order of a
+// group's 128 values is permuted, alike on both sides, so that a lane's 16 bytes are its fragments.
+// (The tensor cores' tcgen05 form wants 128 rows and a trip through shared memory.)  Each group's
+// partial is multiplied by its scales and added in fp32; the warps' sums meet in shared memory in
+// a fixed order.
+// GATED: the block's 16 columns are two tiles of 8 gate and 8 up rows each, so that a thread's
+// sums hold both of its values of h; with e4m3 output the eight blocks of a group of 128 columns
+// are a cluster and share their rows' maxima.
+#include "linear_pair.cuh"
+#include "linear_fp8.cuh"
+
+namespace moe {
+namespace f8 {
+namespace {
+
+using namespace lin;
+
+constexpr int WARPS = 8;
+
+// Codes k .. k + 15 of a row; zeros past K, where nothing is read.
+__device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K) {
+  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  uint32_t w[4] = {};
+#pragma unroll 1
+  for (int i = 0; i < 16 && k + i < K; ++i) w[i >> 2] |= static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void mma_m16n8k32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// XT: tiles of 8 rows of x.
+template <int XT, bool GATED>
+__global__ void __launch_bounds__(WARPS * 32) fp8_few_kernel(Fp8Args a) {
+  constexpr int WT = GATED ? 2 : 1;       // tiles of 16 weight rows
+  constexpr int AHEAD = WT * XT == 1 ? 4 : 2;  // groups on their way
+  __shared__ float sums[WARPS][WT][16][XT * 8];
+  __shared__ float s_max[XT * 8][16], s_block[XT * 8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 16;
+  const int nk = (a.K + 127) / 128;
+  dep_wait();
+  dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = a.hdr->info = 0u;
+  // columns past the last and rows past M stand in for the last
+  const uint8_t* w[WT][2];
+  const uint8_t* x[XT];
+#pragma unroll
+  for (int i = 0; i < WT; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int n = GATED ? min(n0 + 8 * i + g, a.N - 1) : min(n0 + 8 * h + g, a.N - 1);
+      w[i][h] = static_cast<const uint8_t*>(a.w) + (n + (GATED && h ? static_cast<size_t>(a.N) : 0)) * a.ld_w;
+    }
+#pragma unroll
+  for (int i = 0; i < XT; ++i) x[i] = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(8 * i + g, a.M - 1)) * a.ld_x;
+  const int blocks = (a.N + 127) / 128, block = min(n0 / 128, blocks - 1);
+  const float* sw = a.w_scale + static_cast<size_t>(block) * nk;
+  const float* su = sw + static_cast<size_t>(GATED ? blocks : 0) * nk;
+  const float* sx[XT][2];
+#pragma unroll
+  for (int i = 0; i < XT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sx[i][j] = a.x_scale + static_cast<size_t>(min(8 * i + 2 * t + j, a.M - 1)) * nk;
+
+  float acc[WT][XT][4] = {};
+  for (int kb0 = warp; kb0 < nk; kb0 += WARPS * AHEAD) {
+    uint4 wv[AHEAD][WT][2][2], xv[AHEAD][XT][2];
+    float fx[AHEAD][XT][2], fw[AHEAD], fu[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      const int kb = kb0 + WARPS * q;
+      if (kb < nk) {
+        const int k = kb * 128 + 16 * t;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int i = 0; i < WT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) wv[q][i][h][j] = load16(w[i][h], k + 64 * j, a.K);
+#pragma unroll
+          for (int i = 0; i < XT; ++i) xv[q][i][j] = load16(x[i], k + 64 * j, a.K);
+        }
+        fw[q] = __ldg(sw + kb);
+        fu[q] = GATED ? __ldg(su + kb) : fw[q];
+#pragma unroll
+        for (int i = 0; i < XT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) fx[q][i][j] = __ldg(sx[i][j] + kb);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      if (kb0 + WARPS * q >= nk) break;
+#pragma unroll
+      for (int i = 0; i < WT; ++i)
+#pragma unroll
+        for (int xt = 0; xt < XT; ++xt) {
+          float d[4] = {};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 lo = wv[q][i][0][j], hi = wv[q][i][1][j], b = xv[q][xt][j];
+            mma_m16n8k32(d, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+            mma_m16n8k32(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+          }
+          // rows g and g + 8 of the weights, columns 2 t and 2 t + 1 of x
+          acc[i][xt][0] = fmaf(d[0], fw[q] * fx[q][xt][0], acc[i][xt][0]);
+          acc[i][xt][1] = fmaf(d[1], fw[q] * fx[q][xt][1], acc[i][xt][1]);
+          acc[i][xt][2] = fmaf(d[2], fu[q] * fx[q][xt][0], acc[i][xt][2]);
+          acc[i][xt][3] = fmaf(d[3], fu[q] * fx[q][xt][1], acc[i][xt][3]);
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < WT; ++i)
+#pragma unroll
+    for (int xt = 0; xt < XT; ++xt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums[warp][i][g + 8 * (r >> 1)][8 * xt + 2 * t + (r & 1)] = acc[i][xt][r];
+  __syncthreads();
+
+  // thread: column n of row m (16 columns of a row side by side)
+  const int c = threadIdx.x & 15, m = threadIdx.x >> 4, n = n0 + c;
+  const bool has = m < XT * 8, in = has && m < a.M && n < a.N;
+  float v = 0.0f;
+  if (has) {
+    auto total = [&](int i, int r) {
+      float z = 0.0f;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) z += sums[k][i][r][m];
+      return z;
+    };
+    if constexpr (GATED) {
+      float gate = total(c >> 3, c & 7), up = total(c >> 3, (c & 7) + 8);
+      if (a.bias && in) {
+        gate += load_as_f32(a.bias, a.bias_dtype, n);
+        up += load_as_f32(a.bias, a.bias_dtype, static_cast<size_t>(a.N) + n);
+      }
+      v = act_value(gate, a.act) * up;
+    } else {
+      v = total(0, c);
+      if (a.bias && in) v += load_as_f32(a.bias, a.bias_dtype, n);
+      v = a.alpha * act_value(v, a.act);
+    }
+  }
+  const size_t at = static_cast<size_t>(m) * a.ld_y + n;
+  if (GATED && a.h_scale) {
+    if (has) s_max[m][c] = in ? fabsf(v) : 0.0f;
+    __syncthreads();
+    if (threadIdx.x < XT * 8) {
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s_max[threadIdx.x][i]);
+      s_block[threadIdx.x] = top;
+    }
+    cluster_sync_all();
+    if (has) {
+      float top = 0.0f;
+#pragma unroll
+      for (uint32_t r = 0; r < 8; ++r) {
+        float o;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(map_rank(smem_u32(&s_block[m]), r)) : "memory");
+        top = fmaxf(top, o);
+      }
+      float inv;
+      const float s = group_scale(top, inv);
+      if (in) static_cast<uint8_t*>(a.y)[at] = static_cast<uint8_t>(cvt_e4m3x2(scaled(v, s, inv), 0.0f));
+      if (c == 0 && m < a.M && (n0 & 127) == 0) a.h_scale[static_cast<size_t>(m) * blocks + n0 / 128] = s;
+    }
+    cluster_sync_all();  // no block leaves while another still reads its maxima
+    return;
+  }
+  if (!in) return;
+  if (!GATED && a.residual) v += load_as_f32(a.residual, a.out_dtype, at);
+  if (a.out_dtype == MOE_DTYPE_F32) static_cast<float*>(a.y)[at] = v;
+  else if (a.out_dtype == MOE_DTYPE_BF16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+}
+
+template <int XT, bool GATED>
+cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
+  // with e4m3 output a cluster covers a whole group of 128 columns
+  const bool cluster = GATED && a.h_scale;
+  const unsigned grid = cluster ? static_cast<unsigned>((a.N + 127) / 128) * 8 : static_cast<unsigned>((a.N + 15) / 16);
+  cudaLaunchAttribute la[2];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  la[1].id = cudaLaunchAttributeClusterDimension;
+  la[1].val.clusterDim.x = 8;
+  la[1].val.clusterDim.y = la[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.stream = s;
+  cfg.attrs = la;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_few_kernel<XT, GATED>, a);
+}
+
+}  // namespace
+
+bool takes_few(const Fp8Args& a) { return a.M <= 16; }
+
+cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {
+  if (a.gated) return a.M <= 8 ? launch<1, true>(a, s) : launch<2, true>(a, s);
+  return a.M <= 8 ? launch<1, false>(a, s) : launch<2, false>(a, s);
+}
+
+}  // namespace f8
+}  // namespace moe

@@ -61,3 +61,64 @@ def test_gated_binding_checks_rows(m):
     with pytest.raises(m.MoeError) as e:
         m.moe_gated(p, FAKE, None, None, FAKE, None, FAKE, 256, stream=0)
     assert e.value.status == m.MOE_ERR_INVALID_ARG
+
+
+def test_quantise_refusals(m):
+    bad, unsup = m.MOE_ERR_INVALID_ARG, m.MOE_ERR_UNSUPPORTED
+
+    def call(p, **kw):
+        given = dict(x=FAKE, q=FAKE, scale=FAKE) | kw
+        return m.raw_status("moe_quantise", p, given["x"], given["q"], given["scale"], None)
+
+    ok = m.quantise_problem(4, 200)
+    for kw in (dict(x=None), dict(q=None), dict(scale=None), dict(x=FAKE + 1), dict(scale=FAKE + 2)):
+        assert call(ok, **kw) == bad, kw
+    assert call(m.quantise_problem(4, 200, m.MOE_DTYPE_F32), x=FAKE + 2) == bad
+    for p in (m.quantise_problem(-1, 200), m.quantise_problem(4, 0), m.quantise_problem(4, 200, dtype=m.MOE_DTYPE_E4M3),
+              m.quantise_problem(4, 200, block_rows=2), m.quantise_problem(4, 200, ld_x=199), m.quantise_problem(4, 200, ld_q=199)):
+        assert call(p) == bad
+    assert call(None) == bad
+    assert call(m.quantise_problem(1 << 30, 1 << 16, block_rows=128)) == unsup
+    assert call(m.quantise_problem(0, 200), x=None, q=None, scale=None) == m.MOE_OK
+
+
+def test_fp8_refusals(m):
+    bad, unsup, e = m.MOE_ERR_INVALID_ARG, m.MOE_ERR_UNSUPPORTED, m.MOE_DTYPE_E4M3
+    names, gnames = ["x", "x_scale", "w", "w_scale", "bias", "residual", "y"], ["x", "x_scale", "w", "w_scale", "bias", "h", "h_scale"]
+
+    def lin(p, ws=FAKE, nb=256, **kw):
+        given = dict(x=FAKE, x_scale=FAKE, w=FAKE, w_scale=FAKE, y=FAKE) | kw
+        return m.raw_status("moe_linear_fp8", p, *[given.get(n) for n in names], ws, nb, None)
+
+    def gat(p, ws=FAKE, nb=256, **kw):
+        given = dict(x=FAKE, x_scale=FAKE, w=FAKE, w_scale=FAKE, h=FAKE) | kw
+        return m.raw_status("moe_gated_fp8", p, *[given.get(n) for n in gnames], ws, nb, None)
+
+    L, G = m.linear_problem, m.gated_problem
+    ok, okg, okc = L(4, 24, 64, e), G(4, 24, 64, e), G(4, 32, 64, e, e)
+    for kw in (dict(x=None), dict(w=None), dict(x_scale=None), dict(w_scale=None), dict(x=FAKE + 8), dict(w=FAKE + 4),
+               dict(x_scale=FAKE + 2), dict(w_scale=FAKE + 1), dict(bias=FAKE + 2)):
+        assert lin(ok, **kw) == bad and gat(okg, **kw) == bad and gat(okc, h_scale=FAKE, **kw) == bad, kw
+    assert lin(ok, y=None) == bad and lin(ok, y=FAKE + 1) == bad and lin(ok, residual=FAKE + 1) == bad
+    assert gat(okg, h=None) == bad and gat(okg, h=FAKE + 1) == bad and gat(okg, h_scale=FAKE) == bad
+    assert gat(okc) == bad and gat(okc, h_scale=FAKE, h=FAKE + 8) == bad and gat(okc, h_scale=FAKE + 2) == bad
+    for kw in (dict(M=-1), dict(N=-1), dict(K=0), dict(dtype=m.MOE_DTYPE_BF16), dict(out_dtype=4), dict(out_dtype=-1),
+               dict(bias_dtype=e), dict(act=5), dict(ld_x=48), dict(ld_w=48)):
+        a = dict(M=4, N=24, K=64, dtype=e) | kw
+        for p, f, size in ((L(**a), lin, m.moe_linear_fp8_workspace_size), (G(**a), gat, m.moe_gated_fp8_workspace_size)):
+            assert f(p) == bad and size(p) == 0, kw
+    assert lin(L(4, 24, 64, e, e)) == bad and lin(L(4, 24, 64, e, ld_y=23)) == bad and gat(G(4, 24, 64, e, ld_h=23)) == bad
+    assert lin(L(4, 24, 64, e, alpha=float("nan"))) == bad
+    for kw in (dict(K=60), dict(ld_x=72), dict(ld_w=72), dict(M=1 << 30, N=1 << 29)):
+        a = dict(M=4, N=24, K=64, dtype=e) | kw
+        assert lin(L(**a)) == unsup and gat(G(**a)) == unsup, kw
+    assert gat(G(4, 24, 64, e, e), h_scale=FAKE) == unsup  # codes in rows of no whole 16 bytes
+    assert gat(G(4, 32, 64, e, e, ld_h=40), h_scale=FAKE) == unsup
+    assert lin(None) == bad and gat(None) == bad
+    for f, p, kw in ((lin, ok, {}), (gat, okg, {}), (gat, okc, dict(h_scale=FAKE))):
+        assert f(p, ws=None, **kw) == m.MOE_ERR_WORKSPACE
+        assert f(p, ws=FAKE + 16, **kw) == m.MOE_ERR_WORKSPACE
+        assert f(p, nb=255, **kw) == m.MOE_ERR_WORKSPACE
+    assert lin(L(0, 24, 64, e), x=None, w=None, y=None, ws=None, nb=0) == m.MOE_OK
+    # the 16-bit entry points take no codes
+    assert m.moe_linear_workspace_size(ok) == 0 and m.moe_gated_workspace_size(okg) == 0
