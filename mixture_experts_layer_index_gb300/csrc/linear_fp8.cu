@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              if constexpr (CG == 2) mbar_arrive_cluster(free0 + 8 * pb);
+              if constexpr (CG == 2) mbar_arrive_cluster_relaxed(free0 + 8 * pb);
               else mbar_arrive(free0 + 8 * pb);
             }
           }

@@ -42,6 +42,13 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
+// The same after reads of tensor memory that are complete (in registers, behind tc_fence_before): nothing
+// else of this thread has to be seen first.  The release above waits for every load and store of the
+// thread that is on its way, which is too much where it stands in a loop (products with block scales,
+// 16384 x 2048 x 4096: 269 us with it).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t remote) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
 
 // 16 values (columns c.. of one row) into row `lane` of a swizzled box: 16-byte chunk j of a
 // row sits at chunk j ^ (lane & 7).  `part`: which 16 of the box's columns.
