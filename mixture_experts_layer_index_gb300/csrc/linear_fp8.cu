@@ -6,16 +6,22 @@
 //
 // Scales are any fp32 values, so the tensor cores cannot sum over more than one group of 128.
 // Each 128-byte stage of the sum is a partial product of its own in tensor memory
-// (tcgen05.mma kind::f8f6f4, four of K = 32), which sixteen epilogue warps read, multiply by
+// (tcgen05.mma kind::f8f6f4, four of K = 32), which eight epilogue warps read, multiply by
 // its row's and block's scales and add to fp32 registers while the tensor cores fill the next
 // partial ("promotion").  A row of x lies on a TMEM lane, so a thread's scale is the same for
 // all columns of a weight block.
 //
 // Two forms of one kernel.  Large products: pairs of SMs, persistent, tiles of 256 x 256
-// (linear_pair.cu has the reason: 64 bytes of operands per SM and clock instead of 96), two
-// partials of 256 columns.  Others: one SM, tiles of 128 x BN, the sum split over the blocks of
-// a cluster, which join their shares of the rows through shared memory in rank order: no
-// workspace, no atomics, the same result every time.
+// (linear_pair.cu has the reason: 64 bytes of operands per SM and clock instead of 96).  Others:
+// one SM, tiles of 128 x BN, the sum split over the blocks of a cluster, which join their
+// shares of the rows through shared memory in rank order: no workspace, no atomics, the same
+// result every time.
+//
+// The way from a finished MMA through promotion to the next MMA in its place is what bounds it, so
+// that is short: two warps per 32 lanes of tensor memory with 32 columns on their way while 32 are
+// added (128 accumulators and two buffers: registers move to them from the other warps), packed
+// fp32 pairs, a release that waits for nothing else, and the scales of x, one per lane, through
+// shared memory from a warp of their own: read by the promoting warps they cost the L1 32 lines each.
 #include "linear_fp8.cuh"
 #include "linear_pair.cuh"
 
@@ -33,6 +39,10 @@ constexpr int THREADS = 32 * (4 + EPI_WARPS);
 constexpr int MAX_SPLITS = 8;
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_BUFS = 4;
+// Registers per thread: 96 at launch (640 threads), then 56 for the four control warps and 104 for
+// the sixteen that promote, no more in all.
+constexpr int LAUNCH_REGS = 96, CONTROL_REGS = 56, EPI_REGS = 104;
+static_assert(4 * CONTROL_REGS + EPI_WARPS * EPI_REGS <= (4 + EPI_WARPS) * LAUNCH_REGS, "registers of the launch");
 
 template <int CG, int BN>
 struct Shape {
@@ -41,12 +51,12 @@ struct Shape {
   static constexpr int STAGE = OP_A + OP_B;
   static constexpr int BUFS = BN >= 256 ? 2 : 4;  // partials in tensor memory
   static constexpr int STAGES = CG == 2 ? 5 : BN >= 256 ? 4 : BN >= 128 ? 6 : 8;
-  static constexpr int COLS = BN / QW;                         // accumulators of an epilogue thread
-  static constexpr int PITCH = BN + 4;                         // fp32 values of a row on its way between threads
+  static constexpr int COLS = BN / QW;              // accumulators of an epilogue thread
+  static constexpr int PITCH = BN + 4;              // fp32 values of a row on its way between threads
   // pairs: a store box per epilogue warp, or for e4m3 output the row maxima [16][32]
   static constexpr int BOX_OFFSET = STAGES * STAGE;
   static constexpr size_t SMEM = 1024 + BOX_OFFSET + (CG == 2 ? EPI_WARPS * BOX_BYTES : 0);
-  static_assert(SMEM <= 226 * 1024, "shared memory of one block");
+  static_assert(SMEM <= 227 * 1024 - 512, "shared memory of one block");
   static_assert(CG == 2 || BM * PITCH * 4 <= STAGES * STAGE, "a tile's sums lie over the ring");
 };
 
@@ -66,6 +76,7 @@ struct Fp8Params {
   void* y;
   float* h_scale;  // e4m3 output: [M][ceil(N / 128)]
   int y_tma;       // pairs: whether TMA stores the output
+  int sx_vec;      // rows of x_scale start at 16-byte boundaries
   DeviceHeader* hdr;
 };
 
@@ -97,9 +108,9 @@ __device__ __forceinline__ void tile_at(const Fp8Params& p, int t, int& r, int& 
   r = group * GR + in_group % rows_here;
 }
 
-__device__ __forceinline__ uint32_t codes4(const float* h, float s, float inv) {
-  return static_cast<uint32_t>(cvt_e4m3x2(scaled(h[0], s, inv), scaled(h[1], s, inv))) |
-         static_cast<uint32_t>(cvt_e4m3x2(scaled(h[2], s, inv), scaled(h[3], s, inv))) << 16;
+__device__ __forceinline__ uint32_t codes4(const float* h, const GroupScale& g) {
+  return static_cast<uint32_t>(cvt_e4m3x2(g.scaled(h[0]), g.scaled(h[1]))) |
+         static_cast<uint32_t>(cvt_e4m3x2(g.scaled(h[2]), g.scaled(h[3]))) << 16;
 }
 __device__ __forceinline__ float vmax(float m, float v) { return fmaxf(m, fabsf(v)); }  // without a NaN's part
 
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform, for the compiler too
   const uint32_t rank = cluster_rank();
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * MAX_STAGES;
   const uint32_t pfull0 = empty0 + 8 * MAX_STAGES, pempty0 = pfull0 + 8 * MAX_BUFS;
@@ -261,6 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int kb0 = CG == 2 ? 0 : static_cast<int>(static_cast<long long>(p.nk) * rank / p.splits);
   const int kb1 = CG == 2 ? p.nk : static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / p.splits);
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
   if (warp == 0) {
     // Uniform control flow: addresses stay in uniform registers, one lane issues, the next
     // slot's barrier is looked at ahead.
@@ -327,8 +340,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a = ring + stage * S::STAGE, empty = empty0 + 8 * stage, d = tmem + pb * BN;
-          const uint32_t pfull = pfull0 + 8 * pb;
+          const uint32_t a = ring + stage * S::STAGE, b = a + S::OP_A, empty = empty0 + 8 * stage;
+          const uint32_t d = tmem + pb * BN, pfull = pfull0 + 8 * pb;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
@@ -341,8 +354,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {  // a fresh partial for this group of the sum
-              if constexpr (CG == 2) mma_f8_pair(d, walk.at(a, kk), walk.at(a + S::OP_A, kk), idesc, kk != 0);
-              else mma_f8(d, walk.at(a, kk), walk.at(a + S::OP_A, kk), idesc, kk != 0);
+              if constexpr (CG == 2) mma_f8_pair(d, walk.at(a, kk), walk.at(b, kk), idesc, kk != 0);
+              else mma_f8(d, walk.at(a, kk), walk.at(b, kk), idesc, kk != 0);
             }
             if constexpr (CG == 2) {
               mma_commit_pair(pfull);
@@ -362,7 +375,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  __syncwarp();
+  if constexpr (CG == 1) {
+    if (p.splits > 1) {  // as the epilogue warps
+      cluster_sync_all();
+      cluster_sync_all();
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int e = warp - 4, q = warp & 3, h = e >> 2;
     uint8_t* box = smem + S::BOX_OFFSET + e * BOX_BYTES;
     float* rowmax = reinterpret_cast<float*>(smem + S::BOX_OFFSET);
@@ -375,18 +397,32 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int r0 = tr * TILE_ROWS + (CG == 2 ? static_cast<int>(rank) * BM : 0) + q * 32;  // this warp's rows
       const int c0 = tc * OUT_COLS + h * (OUT_COLS / QW);                                    // and columns
       // columns past the last stand in for it, rows likewise; neither is stored
-      const int block = min(c0 / 128, p.blocks - 1);
-      const float* sx = p.x_scale + static_cast<size_t>(min(r0 + lane, p.M - 1)) * p.nk;
-      const float* sw = p.w_scale + static_cast<size_t>(block) * p.nk;
+      const float* sw = p.w_scale + static_cast<size_t>(min(c0 / 128, p.blocks - 1)) * p.nk;
       const float* su = sw + static_cast<size_t>(GATED ? p.blocks : 0) * p.nk;
+      const float* sx = p.x_scale + static_cast<size_t>(min(r0 + lane, p.M - 1)) * p.nk;
       float acc[COLS];
 #pragma unroll
       for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
-      float sx_next = __ldg(sx + kb0), sw_next = __ldg(sw + kb0), su_next = GATED ? __ldg(su + kb0) : 0.0f;
+      // Scales of x four groups at a time where rows allow it: a row per lane costs the L1 32 lines.
+      float x4[4];
+      auto load_sx = [&](int kb) {
+        if (p.sx_vec) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(sx + kb));
+          x4[0] = v.x; x4[1] = v.y; x4[2] = v.z; x4[3] = v.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x4[i] = __ldg(sx + min(kb + i, p.nk - 1));
+        }
+      };
+      load_sx(kb0);
+      float sw_next = __ldg(sw + kb0), su_next = GATED ? __ldg(su + kb0) : 0.0f;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const float f0 = sx_next * sw_next, f1 = GATED ? sx_next * su_next : f0;
+        const float f0 = x4[0] * sw_next, f1 = GATED ? x4[0] * su_next : f0;
+        x4[0] = x4[1];
+        x4[1] = x4[2];
+        x4[2] = x4[3];
         if (kb + 1 < kb1) {
-          sx_next = __ldg(sx + kb + 1);
+          if ((kb - kb0) % 4 == 3) load_sx(kb + 1);
           sw_next = __ldg(sw + kb + 1);
           if (GATED) su_next = __ldg(su + kb + 1);
         }
@@ -426,25 +462,30 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) break;
       if constexpr (CG == 2) {
         if constexpr (GATED) {
+          constexpr int H = COLS / 2;  // columns of h
           if (p.bias) {
             const bool bias_wide = reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && p.half % 8 == 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int c = c0 + 16 * (j & 1);
+            for (int j = 0; j < COLS / 16; ++j) {
+              const int c = c0 + 16 * (j % (H / 16));
               add16(*reinterpret_cast<float(*)[16]>(&acc[16 * j]), p.bias, p.bias_dtype,
-                    (j >= 2 ? static_cast<size_t>(p.half) : 0) + c, p.N - c, bias_wide);
+                    (j >= H / 16 ? static_cast<size_t>(p.half) : 0) + c, p.N - c, bias_wide);
             }
           }
-          act_all<32>(*reinterpret_cast<float(*)[32]>(&acc[0]), p.act);
+          act_all<H>(*reinterpret_cast<float(*)[H]>(&acc[0]), p.act);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] *= acc[32 + i];
+          for (int i = 0; i < H; ++i) acc[i] *= acc[H + i];
           if (p.h_scale) {
             // the group's scale: the row's maximum over the quadrant's four warps
-            const int n = min(32, p.N - c0);
             float m = 0.0f;
+            if (c0 + H <= p.N) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < n) m = vmax(m, acc[i]);
+              for (int i = 0; i < H; ++i) m = vmax(m, acc[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < H; ++i)
+                if (c0 + i < p.N) m = vmax(m, acc[i]);
+            }
             rowmax[e * 32 + lane] = m;
             __syncwarp();
             int good = 1;
@@ -468,25 +509,25 @@ __global__ void __launch_bounds__(THREADS, 1)
               break;
             }
             xphase ^= 1;
-            float inv;
-            const float s = group_scale(m, inv);
-            if (r0 + lane < p.M && n > 0) {
+            const GroupScale g(m);
+            if (r0 + lane < p.M) {
               const size_t row = static_cast<size_t>(r0 + lane);
-              uint32_t w[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = codes4(&acc[4 * i], s, inv);
               uint8_t* to = static_cast<uint8_t*>(p.y) + row * p.ld_y + c0;
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                if (16 * i + 16 <= n) {
-                  reinterpret_cast<uint4*>(to)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              for (int j = 0; j < H / 16; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = codes4(&acc[16 * j + 4 * i], g);
+                const int n = p.N - c0 - 16 * j;
+                if (n >= 16) {
+                  reinterpret_cast<uint4*>(to)[j] = make_uint4(w[0], w[1], w[2], w[3]);
                 } else {
 #pragma unroll
                   for (int b = 0; b < 16; ++b)
-                    if (16 * i + b < n) to[16 * i + b] = static_cast<uint8_t>(w[4 * i + b / 4] >> (8 * (b & 3)));
+                    if (b < n) to[16 * j + b] = static_cast<uint8_t>(w[b / 4] >> (8 * (b & 3)));
                 }
               }
-              if (h == 0) p.h_scale[row * ((p.N + 127) / 128) + c0 / 128] = s;
+              if (h == 0) p.h_scale[row * ((p.N + 127) / 128) + c0 / 128] = g.s;
             }
           } else {
             pair_tile<true>(p, &tmY, acc, box, lane, r0, c0);
@@ -500,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int j = 0; j < COLS / 4; ++j) {
           const bool up = GATED && j >= COLS / 8;
-          const int c = GATED ? (up ? BN / 2 + h * (COLS / 2) + (j - COLS / 8) * 4 : h * (COLS / 2) + j * 4) : h * COLS + j * 4;
+          const int c = GATED ? (up ? BN / 2 - COLS / 2 : 0) + h * (COLS / 2) + j * 4 : h * COLS + j * 4;
           *reinterpret_cast<float4*>(part + c) = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
         }
       }
@@ -513,84 +554,82 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if constexpr (CG == 2) {
-    cluster_sync_all();  // neither block's barriers or tensor memory are in use any more
-  } else {
-    if (p.splits > 1) cluster_sync_all();
-    // this block's share of the rows, 4 columns (of the output) per thread
-    int tr, tc;
-    tile_at(p, first, tr, tc);
-    const int rows = min(BM, p.M - tr * BM);
-    const int per = (rows + p.splits - 1) / p.splits;
-    const int begin = static_cast<int>(rank) * per, end = min(begin + per, rows);
-    constexpr int LANES = OUT_COLS / 4 < 32 ? OUT_COLS / 4 : 32;  // threads of a row
-    constexpr int PASSES = OUT_COLS / 4 / LANES;
-    constexpr int GROUPS = THREADS / LANES;
-    const int in_row = static_cast<int>(threadIdx.x) % LANES;
-    const uint32_t sums = smem_u32(smem);
-    if (*abort_flag == 0) {
-      // whole warps leave the loop together where a row's maximum is shared
-      for (int r = begin + static_cast<int>(threadIdx.x) / LANES; r < end; r += GROUPS) {
-        const int row = tr * BM + r;
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-          const int cc = (in_row + i * LANES) * 4, c = tc * OUT_COLS + cc, n = p.N - c;
-          const uint32_t at = sums + (r * S::PITCH + cc) * 4;
-          float v[4] = {}, u[4] = {};
-          for (int k = 0; k < p.splits; ++k) {
-            const uint32_t from = p.splits > 1 ? k : rank;
-            const float4 a = ld_cluster_f32x4(at, from);
-            v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-            if (GATED) {
-              const float4 b = ld_cluster_f32x4(at + BN / 2 * 4, from);
-              u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
-            }
-          }
-          if (p.bias) {
-            add4(v, p.bias, p.bias_dtype, c, n);
-            if (GATED) add4(u, p.bias, p.bias_dtype, static_cast<size_t>(p.half) + c, n);
-          }
-          act_all<4>(v, p.act);
-          const size_t to = static_cast<size_t>(row) * p.ld_y + c;
-          if constexpr (GATED) {
-            float m = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              v[k] *= u[k];
-              if (k < n) m = vmax(m, v[k]);
-            }
-            if (OUT_COLS == 128 && p.h_scale) {
-              m = warp_max(m);
-              float inv;
-              const float s = group_scale(m, inv);
-              const uint32_t w = codes4(v, s, inv);
-              uint8_t* h = static_cast<uint8_t*>(p.y) + to;
-              if (n >= 4) {
-                *reinterpret_cast<uint32_t*>(h) = w;
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (k < n) h[k] = static_cast<uint8_t>(w >> (8 * k));
+    if constexpr (CG == 1) {
+      // all of the tile's sums lie in shared memory
+      if (p.splits > 1) cluster_sync_all();
+      else asm volatile("bar.sync 1, %0;" ::"n"(EPI_WARPS * 32) : "memory");
+      // this block's share of the rows, 4 columns (of the output) per thread
+      int tr, tc;
+      tile_at(p, first, tr, tc);
+      const int rows = min(BM, p.M - tr * BM);
+      const int per = (rows + p.splits - 1) / p.splits;
+      const int begin = static_cast<int>(rank) * per, end = min(begin + per, rows);
+      constexpr int LANES = OUT_COLS / 4 < 32 ? OUT_COLS / 4 : 32;  // threads of a row
+      constexpr int PASSES = OUT_COLS / 4 / LANES;
+      constexpr int GROUPS = EPI_WARPS * 32 / LANES;
+      const int in_row = (static_cast<int>(threadIdx.x) - 128) % LANES;
+      const uint32_t sums = smem_u32(smem);
+      if (*abort_flag == 0) {
+        // whole warps leave the loop together where a row's maximum is shared
+        for (int r = begin + (static_cast<int>(threadIdx.x) - 128) / LANES; r < end; r += GROUPS) {
+          const int row = tr * BM + r;
+  #pragma unroll
+          for (int i = 0; i < PASSES; ++i) {
+            const int cc = (in_row + i * LANES) * 4, c = tc * OUT_COLS + cc, n = p.N - c;
+            const uint32_t at = sums + (r * S::PITCH + cc) * 4;
+            float v[4] = {}, u[4] = {};
+            for (int k = 0; k < p.splits; ++k) {
+              const uint32_t from = p.splits > 1 ? k : rank;
+              const float4 a = ld_cluster_f32x4(at, from);
+              v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+              if (GATED) {
+                const float4 b = ld_cluster_f32x4(at + BN / 2 * 4, from);
+                u[0] += b.x; u[1] += b.y; u[2] += b.z; u[3] += b.w;
               }
-              if (in_row == 0) p.h_scale[static_cast<size_t>(row) * ((p.N + 127) / 128) + tc] = s;
-              continue;
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] *= p.alpha;
-            if (p.residual) add4(v, p.residual, p.out_dtype, to, n);
+            if (p.bias) {
+              add4(v, p.bias, p.bias_dtype, c, n);
+              if (GATED) add4(u, p.bias, p.bias_dtype, static_cast<size_t>(p.half) + c, n);
+            }
+            act_all<4>(v, p.act);
+            const size_t to = static_cast<size_t>(row) * p.ld_y + c;
+            if constexpr (GATED) {
+              float m = 0.0f;
+  #pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                v[k] *= u[k];
+                if (k < n) m = vmax(m, v[k]);
+              }
+              if (OUT_COLS == 128 && p.h_scale) {
+                m = warp_max(m);
+                const GroupScale g(m);
+                const uint32_t w = codes4(v, g);
+                uint8_t* h = static_cast<uint8_t*>(p.y) + to;
+                if (n >= 4) {
+                  *reinterpret_cast<uint32_t*>(h) = w;
+                } else {
+  #pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    if (k < n) h[k] = static_cast<uint8_t>(w >> (8 * k));
+                }
+                if (in_row == 0) p.h_scale[static_cast<size_t>(row) * ((p.N + 127) / 128) + tc] = g.s;
+                continue;
+              }
+            } else {
+  #pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] *= p.alpha;
+              if (p.residual) add4(v, p.residual, p.out_dtype, to, n);
+            }
+            store4(p.y, p.out_dtype, to, v, n);
           }
-          store4(p.y, p.out_dtype, to, v, n);
         }
       }
+      if (p.splits > 1) cluster_sync_all();  // no block leaves while another still reads its sums
     }
-    if (p.splits > 1) cluster_sync_all();  // no block leaves while another still reads its sums
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // neither block's barriers or tensor memory are in use any more
   if (warp == 2) {
     tc_fence_after();
     if constexpr (CG == 2)
@@ -645,9 +684,16 @@ cudaError_t launch_shape(const Fp8Args& a, int splits, cudaStream_t s) {
   p.y_tma = CG == 2 && !a.h_scale && storable(a.y, a.out_dtype, a.N, a.ld_y);
   if (p.y_tma && !encode_store(&ty, a.y, a.out_dtype, a.N, a.M, a.ld_y, GATED && a.out_dtype != MOE_DTYPE_F32 ? 64 : 128))
     return cudaErrorInvalidValue;
-  static const cudaError_t attr = cudaFuncSetAttribute(linear_fp8_kernel<CG, BN, GATED>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(Sh::SMEM));
+  static const cudaError_t attr = [] {
+    cudaFuncAttributes f{};
+    const cudaError_t e = cudaFuncGetAttributes(&f, linear_fp8_kernel<CG, BN, GATED>);
+    if (e != cudaSuccess) return e;
+    if (f.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;  // the split of registers would not add up
+    return cudaFuncSetAttribute(linear_fp8_kernel<CG, BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Sh::SMEM));
+  }();
   if (attr != cudaSuccess) return attr;
+  p.sx_vec = p.nk % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scale) % 16 == 0 && p.nk / splits % 4 == 0;
   const long long tiles = static_cast<long long>(p.nR) * p.nC;
   const int sms = num_sms();
   if (sms < 2) return cudaErrorNoDevice;

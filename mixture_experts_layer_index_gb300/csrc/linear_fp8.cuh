@@ -7,20 +7,20 @@
 namespace moe {
 namespace f8 {
 
-// Scale of a group of h whose largest magnitude is `amax`, and the factor that codes take: the
-// reciprocal where it is a normal number (a code can then differ from the quotient's where h
-// lies within an fp32 rounding of a midpoint between codes, less than h's own error).
-__device__ __forceinline__ float group_scale(float amax, float& inv) {
-  const float s = amax / 448.0f;
-  if (!(s > 0.0f)) {
-    inv = 1.0f;
-    return 1.0f;
+// Scale s of a group of h from its largest magnitude, and what makes a code's argument of h: (h lift)
+// inv, inv = 1 / (s lift).  lift keeps the reciprocal of the smallest scales finite; it is a power of two,
+// so that the argument differs from the quotient h / s by at most an fp32 rounding (and a code where h
+// lies that near a midpoint between codes, less than h's own error).  An infinite scale gives 0 and NaN.
+struct GroupScale {
+  float s, lift, inv;
+  __device__ __forceinline__ explicit GroupScale(float amax) {
+    s = amax / 448.0f;
+    if (!(s > 0.0f)) s = 1.0f;
+    lift = s < 1e-30f ? 18446744073709551616.0f : 1.0f;
+    inv = 1.0f / (s * lift);
   }
-  inv = s >= 1.17549435e-38f ? 1.0f / s : 0.0f;
-  return s;
-}
-// The code of h; inv == 0 next to the smallest scales (and for an infinite one).
-__device__ __forceinline__ float scaled(float h, float s, float inv) { return inv > 0.0f ? h * inv : h / s; }
+  __device__ __forceinline__ float scaled(float h) const { return h * lift * inv; }
+};
 
 // Up to 16 rows (linear_fp8_few.cu).
 bool takes_few(const Fp8Args& a);

@@ -170,10 +170,9 @@ __global__ void __launch_bounds__(WARPS * 32) fp8_few_kernel(Fp8Args a) {
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(map_rank(smem_u32(&s_block[m]), r)) : "memory");
         top = fmaxf(top, o);
       }
-      float inv;
-      const float s = group_scale(top, inv);
-      if (in) static_cast<uint8_t*>(a.y)[at] = static_cast<uint8_t>(cvt_e4m3x2(scaled(v, s, inv), 0.0f));
-      if (c == 0 && m < a.M && (n0 & 127) == 0) a.h_scale[static_cast<size_t>(m) * blocks + n0 / 128] = s;
+      const GroupScale g8(top);
+      if (in) static_cast<uint8_t*>(a.y)[at] = static_cast<uint8_t>(cvt_e4m3x2(g8.scaled(v), 0.0f));
+      if (c == 0 && m < a.M && (n0 & 127) == 0) a.h_scale[static_cast<size_t>(m) * blocks + n0 / 128] = g8.s;
     }
     cluster_sync_all();  // no block leaves while another still reads its maxima
     return;
