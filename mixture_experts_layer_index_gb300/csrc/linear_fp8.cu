@@ -6,7 +6,7 @@
 //
 // Scales are any fp32 values, so the tensor cores cannot sum over more than one group of 128.
 // Each 128-byte stage of the sum is a partial product of its own in tensor memory
-// (tcgen05.mma kind::f8f6f4, four of K = 32), which eight epilogue warps read, multiply by
+// (tcgen05.mma kind::f8f6f4, four of K = 32), which sixteen epilogue warps read, multiply by
 // its row's and block's scales and add to fp32 registers while the tensor cores fill the next
 // partial ("promotion").  A row of x lies on a TMEM lane, so a thread's scale is the same for
 // all columns of a weight block.
@@ -17,11 +17,14 @@
 // shares of the rows through shared memory in rank order: no workspace, no atomics, the same
 // result every time.
 //
-// The way from a finished MMA through promotion to the next MMA in its place is what bounds it, so
-// that is short: two warps per 32 lanes of tensor memory with 32 columns on their way while 32 are
-// added (128 accumulators and two buffers: registers move to them from the other warps), packed
-// fp32 pairs, a release that waits for nothing else, and the scales of x, one per lane, through
-// shared memory from a warp of their own: read by the promoting warps they cost the L1 32 lines each.
+// Bound by the promoting warps' loop, some 1200 clocks per stage of a 256 x 256 tile whose MMAs take
+// 512: wait, four trips to tensor memory with as many rounds of additions, and the release.  Measured
+// (16384 x 2048 x 4096; 131 us, 2.1 PFLOP/s): without the additions 91 us, without the scales'
+// loads 112.  So the loop is kept short: a release that waits for no other access of the thread
+// (with a release at cluster scope 269 us), the next partial's barrier looked at before the last
+// additions, the next scales loaded behind the release, and no spilled registers, which are
+// moved here from the other warps.  Slower in trials: eight warps with 128 accumulators and two
+// buffers (139), partials of 128 columns (170), the scales through shared memory (140 to 144).
 #include "linear_fp8.cuh"
 #include "linear_pair.cuh"
 
@@ -273,116 +276,116 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int kb1 = CG == 2 ? p.nk : static_cast<int>(static_cast<long long>(p.nk) * (rank + 1) / p.splits);
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
-  if (warp == 0) {
-    // Uniform control flow: addresses stay in uniform registers, one lane issues, the next
-    // slot's barrier is looked at ahead.
-    const bool leader = elect_one();
-    const uint32_t bar0 = CG == 2 ? map_rank(full0, 0) : full0, ring = smem_u32(smem);
-    uint32_t stage = 0, phase = 1;
-    int issued = 0;
-    bool ok = true, ready = true;
-    for (int t = first; ok && t < tiles; t += step) {
-      int tr, tc;
-      tile_at(p, t, tr, tc);
-      const int r0 = tr * TILE_ROWS + (CG == 2 ? rank * BM : 0);
-      const int c0 = tc * OUT_COLS + (CG == 2 ? rank * (GATED ? p.half : BM) : 0);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!ready && !mbar_wait(empty0 + 8 * stage, phase, abort_flag, p.hdr, 0x710000u)) {
-          ok = false;
-          break;
-        }
-        const uint32_t full = full0 + 8 * stage, bar = bar0 + 8 * stage, a = ring + stage * S::STAGE, b = a + S::OP_A;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
-        if (leader) {
-          const int k = kb * BKB;
-          if constexpr (CG == 2) {
-            if (rank == 0) mbar_arrive_expect_tx(full, 2 * S::STAGE);  // the bytes of both blocks
-            tma_load_2d_pair(a, &tmA, k, r0, bar);
-            tma_load_2d_pair(b, &tmB, k, c0, bar);
-          } else {
-            mbar_arrive_expect_tx(full, S::STAGE);
-            tma_load_2d(a, &tmA, k, r0, full);
-            tma_load_2d(b, &tmB, k, c0, full);
-            if (GATED) tma_load_2d(b + S::OP_B / 2, &tmB, k, p.half + c0, full);
-          }
-        }
-        __syncwarp();
-        ++issued;
-        ready = mbar_try_wait(empty0 + 8 * stage, phase);
-      }
-    }
-    if (!ok && (CG == 1 || rank == 0) && leader) {  // let the copies already issued land before shared memory is given up
-      for (int i = 0; i < min(issued, STAGES); ++i) {
-        stage = (stage + STAGES - 1) % STAGES;
-        if (stage == STAGES - 1) phase ^= 1;
-        mbar_wait_quiet(full0 + 8 * stage, phase ^ 1, 50000000ull);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (CG == 1 || rank == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CONTROL_REGS));
+    if (warp == 0) {
+      // Uniform control flow: addresses stay in uniform registers, one lane issues, the next
+      // slot's barrier is looked at ahead.
       const bool leader = elect_one();
-      constexpr uint32_t idesc = make_idesc(0, 0, TILE_ROWS, BN);
-      const uint32_t ring = smem_u32(smem);
-      const OperandWalk walk(false);  // K-major: 32 codes are 32 bytes on, like 16 values of 16 bits
-      uint32_t stage = 0, phase = 0, pb = 0, pphase = 1;
-      bool ok = true;
+      const uint32_t bar0 = CG == 2 ? map_rank(full0, 0) : full0, ring = smem_u32(smem);
+      uint32_t stage = 0, phase = 1;
+      int issued = 0;
+      bool ok = true, ready = true;
       for (int t = first; ok && t < tiles; t += step) {
-        bool ready = mbar_try_wait(full0 + 8 * stage, phase);
+        int tr, tc;
+        tile_at(p, t, tr, tc);
+        const int r0 = tr * TILE_ROWS + (CG == 2 ? rank * BM : 0);
+        const int c0 = tc * OUT_COLS + (CG == 2 ? rank * (GATED ? p.half : BM) : 0);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if ((!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x720000u)) ||
-              !mbar_wait(pempty0 + 8 * pb, pphase, abort_flag, p.hdr, 0x730000u)) {
+          if (!ready && !mbar_wait(empty0 + 8 * stage, phase, abort_flag, p.hdr, 0x710000u)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a = ring + stage * S::STAGE, b = a + S::OP_A, empty = empty0 + 8 * stage;
-          const uint32_t d = tmem + pb * BN, pfull = pfull0 + 8 * pb;
+          const uint32_t full = full0 + 8 * stage, bar = bar0 + 8 * stage, a = ring + stage * S::STAGE, b = a + S::OP_A;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
-          if (++pb == BUFS) {
-            pb = 0;
-            pphase ^= 1;
-          }
-          ready = kb + 1 < kb1 && mbar_try_wait(full0 + 8 * stage, phase);
           if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {  // a fresh partial for this group of the sum
-              if constexpr (CG == 2) mma_f8_pair(d, walk.at(a, kk), walk.at(b, kk), idesc, kk != 0);
-              else mma_f8(d, walk.at(a, kk), walk.at(b, kk), idesc, kk != 0);
-            }
+            const int k = kb * BKB;
             if constexpr (CG == 2) {
-              mma_commit_pair(pfull);
-              mma_commit_pair(empty);
+              if (rank == 0) mbar_arrive_expect_tx(full, 2 * S::STAGE);  // the bytes of both blocks
+              tma_load_2d_pair(a, &tmA, k, r0, bar);
+              tma_load_2d_pair(b, &tmB, k, c0, bar);
             } else {
-              mma_commit(pfull);
-              mma_commit(empty);
+              mbar_arrive_expect_tx(full, S::STAGE);
+              tma_load_2d(a, &tmA, k, r0, full);
+              tma_load_2d(b, &tmB, k, c0, full);
+              if (GATED) tma_load_2d(b + S::OP_B / 2, &tmB, k, p.half + c0, full);
             }
           }
           __syncwarp();
+          ++issued;
+          ready = mbar_try_wait(empty0 + 8 * stage, phase);
         }
       }
-      if (leader) {
-        if constexpr (CG == 2) mma_commit_pair(done);
-        else mma_commit(done);
-        mbar_wait_quiet(done, 0, 1000000000ull);
+      if (!ok && (CG == 1 || rank == 0) && leader) {  // let the copies already issued land before shared memory is given up
+        for (int i = 0; i < min(issued, STAGES); ++i) {
+          stage = (stage + STAGES - 1) % STAGES;
+          if (stage == STAGES - 1) phase ^= 1;
+          mbar_wait_quiet(full0 + 8 * stage, phase ^ 1, 50000000ull);
+        }
       }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (CG == 1 || rank == 0) {
+        const bool leader = elect_one();
+        constexpr uint32_t idesc = make_idesc(0, 0, TILE_ROWS, BN);
+        const uint32_t ring = smem_u32(smem);
+        const OperandWalk walk(false);  // K-major: 32 codes are 32 bytes on, like 16 values of 16 bits
+        uint32_t stage = 0, phase = 0, pb = 0, pphase = 1;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step) {
+          bool ready = mbar_try_wait(full0 + 8 * stage, phase);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if ((!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x720000u)) ||
+                !mbar_wait(pempty0 + 8 * pb, pphase, abort_flag, p.hdr, 0x730000u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = ring + stage * S::STAGE, b = a + S::OP_A, empty = empty0 + 8 * stage;
+            const uint32_t d = tmem + pb * BN, pfull = pfull0 + 8 * pb;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+            if (++pb == BUFS) {
+              pb = 0;
+              pphase ^= 1;
+            }
+            ready = kb + 1 < kb1 && mbar_try_wait(full0 + 8 * stage, phase);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {  // a fresh partial for this group of the sum
+                if constexpr (CG == 2) mma_f8_pair(d, walk.at(a, kk), walk.at(b, kk), idesc, kk != 0);
+                else mma_f8(d, walk.at(a, kk), walk.at(b, kk), idesc, kk != 0);
+              }
+              if constexpr (CG == 2) {
+                mma_commit_pair(pfull);
+                mma_commit_pair(empty);
+              } else {
+                mma_commit(pfull);
+                mma_commit(empty);
+              }
+            }
+            __syncwarp();
+          }
+        }
+        if (leader) {
+          if constexpr (CG == 2) mma_commit_pair(done);
+          else mma_commit(done);
+          mbar_wait_quiet(done, 0, 1000000000ull);
+        }
+      }
+      __syncwarp();
     }
     __syncwarp();
-  }
-  __syncwarp();
-  if constexpr (CG == 1) {
-    if (p.splits > 1) {  // as the epilogue warps
-      cluster_sync_all();
-      cluster_sync_all();
+    if constexpr (CG == 1) {
+      if (p.splits > 1) {  // as the epilogue warps
+        cluster_sync_all();
+        cluster_sync_all();
+      }
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int e = warp - 4, q = warp & 3, h = e >> 2;
@@ -415,22 +418,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       load_sx(kb0);
-      float sw_next = __ldg(sw + kb0), su_next = GATED ? __ldg(su + kb0) : 0.0f;
+      float sw_kb = __ldg(sw + kb0), su_kb = GATED ? __ldg(su + kb0) : 0.0f;
+      bool ready = false;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const float f0 = x4[0] * sw_next, f1 = GATED ? x4[0] * su_next : f0;
-        x4[0] = x4[1];
-        x4[1] = x4[2];
-        x4[2] = x4[3];
-        if (kb + 1 < kb1) {
-          if ((kb - kb0) % 4 == 3) load_sx(kb + 1);
-          sw_next = __ldg(sw + kb + 1);
-          if (GATED) su_next = __ldg(su + kb + 1);
-        }
-        int good = 1;
-        if (lane == 0) good = mbar_wait(pfull0 + 8 * pb, pphase, abort_flag, p.hdr, 0x740000u);
-        if (!__shfl_sync(0xffffffffu, good, 0)) {
-          ok = false;
-          break;
+        const float f0 = x4[0] * sw_kb, f1 = GATED ? x4[0] * su_kb : f0;
+        if (!__all_sync(0xffffffffu, ready)) {
+          int good = 1;
+          if (lane == 0) good = mbar_wait(pfull0 + 8 * pb, pphase, abort_flag, p.hdr, 0x740000u);
+          if (!__shfl_sync(0xffffffffu, good, 0)) {
+            ok = false;
+            break;
+          }
         }
         tc_fence_after();
         const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + pb * BN;
@@ -449,14 +447,23 @@ __global__ void __launch_bounds__(THREADS, 1)
               if constexpr (CG == 2) mbar_arrive_cluster_relaxed(free0 + 8 * pb);
               else mbar_arrive(free0 + 8 * pb);
             }
+            if (++pb == BUFS) {
+              pb = 0;
+              pphase ^= 1;
+            }
+            ready = mbar_test_wait(pfull0 + 8 * pb, pphase);
           }
           const float f = up ? f1 : f0;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) fma2(acc[16 * j + i], acc[16 * j + i + 1], v[i], v[i + 1], f, f);
         }
-        if (++pb == BUFS) {
-          pb = 0;
-          pphase ^= 1;
+        if (kb + 1 < kb1) {
+          x4[0] = x4[1];
+          x4[1] = x4[2];
+          x4[2] = x4[3];
+          if ((kb - kb0) % 4 == 3) load_sx(kb + 1);
+          sw_kb = __ldg(sw + kb + 1);
+          if (GATED) su_kb = __ldg(su + kb + 1);
         }
       }
       if (!ok) break;
@@ -693,7 +700,7 @@ cudaError_t launch_shape(const Fp8Args& a, int splits, cudaStream_t s) {
                                 static_cast<int>(Sh::SMEM));
   }();
   if (attr != cudaSuccess) return attr;
-  p.sx_vec = p.nk % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scale) % 16 == 0 && p.nk / splits % 4 == 0;
+  p.sx_vec = p.nk % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scale) % 16 == 0 && p.nk % (4 * splits) == 0;
   const long long tiles = static_cast<long long>(p.nR) * p.nC;
   const int sms = num_sms();
   if (sms < 2) return cudaErrorNoDevice;
@@ -714,23 +721,24 @@ cudaError_t launch_shape(const Fp8Args& a, int splits, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, linear_fp8_kernel<CG, BN, GATED>, ta, tb, ty, p);
 }
 
-// About how long a launch takes (us): see the measurements at `choose`.
+// About how long a launch takes (us), fitted to measurements on GB300 (weights in L2) of some 125 problems,
+// 17 to 4096 rows, N and K of 256 to 8192, in every form: the form of the least estimate is on average 1%
+// slower than the fastest one, 16% at most.
 float pair_estimate(const Fp8Args& a) {
   const long long cols = a.gated ? 128 : 256;
   const long long tiles = (a.M + 255ll) / 256 * ((a.N + cols - 1) / cols);
-  const long long waves = (tiles + 75) / 76;
-  const float stages = 0.35f * ((a.K + 127) / 128);
-  return 5.0f + waves * (stages + 1.5f);
+  return 2.7f + (tiles + 75) / 76 * (0.52f * ((a.K + 127) / 128) + (a.h_scale ? 4.0f : 2.5f));
 }
 float single_estimate(const Fp8Args& a, int bn, int splits) {
   const long long cols = a.gated ? bn / 2 : bn;
   const long long blocks = (a.M + 127ll) / 128 * ((a.N + cols - 1) / cols) * splits;
-  const long long waves = (blocks + (splits == 8 ? 127 : 151)) / (splits == 8 ? 128 : 152);
-  const int nk = (a.K + 127) / 128;
-  const float stage = bn == 256 ? 0.45f : bn == 128 ? 0.32f : 0.26f;
-  const int rows = a.M < 128 ? a.M : 128;
-  float t = 4.0f + waves * (2.0f + stage * ((nk + splits - 1) / splits) + 0.01f * rows * bn / 64 / splits);
-  if (splits > 1) t += 1.0f;
+  // a cluster's blocks lie in one group of SMs: clusters of 4 find some 144 of 152 SMs, of 8 some 120
+  const int sms = splits == 8 ? 120 : splits == 4 ? 144 : 152;
+  const int stages = ((a.K + 127) / 128 + splits - 1) / splits;
+  const float wave = bn == 256 ? 9.0f + 0.434f * stages : bn == 128 ? 6.6f + 0.279f * stages : 5.5f + 0.269f * stages;
+  float t = (blocks + sms - 1) / sms * wave - 2.5f + 1.3e-4f * (a.M < 128 ? a.M : 128) * bn / splits;
+  if (splits > 1) t += 1.3f - 0.0054f * bn;
+  for (int s = splits; s > 1; s /= 2) t += 0.58f;
   return t;
 }
 

@@ -44,8 +44,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
 }
 // The same after reads of tensor memory that are complete (in registers, behind tc_fence_before): nothing
 // else of this thread has to be seen first.  The release above waits for every load and store of the
-// thread that is on its way, which is too much where it stands in a loop (products with block scales,
-// 16384 x 2048 x 4096: 269 us with it).
+// thread that is on its way, too much for a loop.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t remote) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
