@@ -22,7 +22,7 @@ struct GroupScale {
   __device__ __forceinline__ float scaled(float h) const { return h * lift * inv; }
 };
 
-// Up to 16 rows (linear_fp8_few.cu).
+// Up to 16 rows, 8 gated (linear_fp8_few.cu).
 bool takes_few(const Fp8Args& a);
 cudaError_t launch_few(const Fp8Args& a, cudaStream_t s);
 

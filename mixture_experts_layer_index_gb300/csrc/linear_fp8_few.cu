@@ -1,15 +1,16 @@
-// Products of e4m3 operands with block scales for up to 16 rows of x: bound by reading w once.
+// Products of e4m3 operands with block scales for up to 16 rows of x (8 gated): bound by reading w once.
 //
-// A block takes 16 output columns, its eight warps every eighth group of 128 of the sum, weights
-// straight from memory to registers, 16 bytes a lane and row, 64 consecutive bytes of a row at a
-// time.  mma.sync.m16n8k32 multiplies 16 weight rows (M) with 8 rows of x (N); the order of a
-// group's 128 values is permuted, alike on both sides, so that a lane's 16 bytes are its fragments.
-// (The tensor cores' tcgen05 form wants 128 rows and a trip through shared memory.)  Each group's
-// partial is multiplied by its scales and added in fp32; the warps' sums meet in shared memory in
-// a fixed order.
-// GATED: the block's 16 columns are two tiles of 8 gate and 8 up rows each, so that a thread's
-// sums hold both of its values of h; with e4m3 output the eight blocks of a group of 128 columns
-// are a cluster and share their rows' maxima.
+// A block takes 16 output columns, eight warps each the groups of 128 of the sum in turn.  All of
+// the block's weights are asked for at once, as prefetches into L2 (which may begin before the kernel
+// before this one has ended: nothing is read), then come to registers, 16 bytes a lane and row, 64
+// consecutive bytes of a row at a time.  mma.sync.m16n8k32 multiplies 16 weight rows (M) with 8 rows
+// of x (N); the order of a group's 128 values is permuted, alike on both sides, so that a lane's
+// 16 bytes are its fragments.  (The tensor cores' tcgen05 form wants 128 rows and a trip through
+// shared memory: 8 x 4096 x 4096 8.9 us in linear_fp8.cu.)  Each group's partial is multiplied by
+// its scales and added in fp32; the warps' sums meet in shared memory in a fixed order.
+// GATED: the block's 16 columns are two tiles of 8 gate and 8 up rows each, with eight warps per
+// tile; a thread's sums hold both of its values of h; with e4m3 output the eight blocks of a group
+// of 128 columns are a cluster and share their rows' maxima.
 #include "linear_pair.cuh"
 #include "linear_fp8.cuh"
 
@@ -19,7 +20,7 @@ namespace {
 
 using namespace lin;
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 8;  // per tile of 16 weight rows
 
 // Codes k .. k + 15 of a row; zeros past K, where nothing is read.
 __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K) {
@@ -39,41 +40,44 @@ __device__ __forceinline__ void mma_m16n8k32(float (&d)[4], uint32_t a0, uint32_
 
 // XT: tiles of 8 rows of x.
 template <int XT, bool GATED>
-__global__ void __launch_bounds__(WARPS * 32) fp8_few_kernel(Fp8Args a) {
-  constexpr int WT = GATED ? 2 : 1;       // tiles of 16 weight rows
-  constexpr int AHEAD = WT * XT == 1 ? 4 : 2;  // groups on their way
+__global__ void __launch_bounds__(WARPS * 32 * (GATED ? 2 : 1), 2) fp8_few_kernel(Fp8Args a) {
+  constexpr int WT = GATED ? 2 : 1;  // tiles of 16 weight rows
+  constexpr int AHEAD = GATED || XT > 1 ? 1 : 2;  // groups on their way to registers
   __shared__ float sums[WARPS][WT][16][XT * 8];
   __shared__ float s_max[XT * 8][16], s_block[XT * 8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x / 32 % WARPS, tile = threadIdx.x / 32 / WARPS;
   const int n0 = blockIdx.x * 16;
   const int nk = (a.K + 127) / 128;
+  // weight rows g and g + 8 of the warp's tile: two of a linear layer's, or a gate and its up row;
+  // columns past the last and rows past M stand in for the last
+  const uint8_t* w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = min(GATED ? n0 + 8 * tile + g : n0 + 8 * h + g, a.N - 1);
+    w[h] = static_cast<const uint8_t*>(a.w) + (n + (GATED && h ? static_cast<size_t>(a.N) : 0)) * a.ld_w;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    for (int kb = warp + WARPS * t; kb < nk; kb += WARPS * 4) prefetch_l2(w[h] + kb * 128);
   dep_wait();
   dep_launch();
   if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->status = a.hdr->info = 0u;
-  // columns past the last and rows past M stand in for the last
-  const uint8_t* w[WT][2];
   const uint8_t* x[XT];
+  int sx[XT][2];  // scales of rows 2 t and 2 t + 1
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
+  for (int i = 0; i < XT; ++i) {
+    x[i] = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(8 * i + g, a.M - 1)) * a.ld_x;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int n = GATED ? min(n0 + 8 * i + g, a.N - 1) : min(n0 + 8 * h + g, a.N - 1);
-      w[i][h] = static_cast<const uint8_t*>(a.w) + (n + (GATED && h ? static_cast<size_t>(a.N) : 0)) * a.ld_w;
-    }
-#pragma unroll
-  for (int i = 0; i < XT; ++i) x[i] = static_cast<const uint8_t*>(a.x) + static_cast<size_t>(min(8 * i + g, a.M - 1)) * a.ld_x;
+    for (int j = 0; j < 2; ++j) sx[i][j] = min(8 * i + 2 * t + j, a.M - 1) * nk;
+  }
   const int blocks = (a.N + 127) / 128, block = min(n0 / 128, blocks - 1);
   const float* sw = a.w_scale + static_cast<size_t>(block) * nk;
   const float* su = sw + static_cast<size_t>(GATED ? blocks : 0) * nk;
-  const float* sx[XT][2];
-#pragma unroll
-  for (int i = 0; i < XT; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) sx[i][j] = a.x_scale + static_cast<size_t>(min(8 * i + 2 * t + j, a.M - 1)) * nk;
 
-  float acc[WT][XT][4] = {};
+  float acc[XT][4] = {};
   for (int kb0 = warp; kb0 < nk; kb0 += WARPS * AHEAD) {
-    uint4 wv[AHEAD][WT][2][2], xv[AHEAD][XT][2];
+    uint4 wv[AHEAD][2][2], xv[AHEAD][XT][2];
     float fx[AHEAD][XT][2], fw[AHEAD], fu[AHEAD];
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
@@ -83,9 +87,7 @@ __global__ void __launch_bounds__(WARPS * 32) fp8_few_kernel(Fp8Args a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int i = 0; i < WT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) wv[q][i][h][j] = load16(w[i][h], k + 64 * j, a.K);
+          for (int h = 0; h < 2; ++h) wv[q][h][j] = load16(w[h], k + 64 * j, a.K);
 #pragma unroll
           for (int i = 0; i < XT; ++i) xv[q][i][j] = load16(x[i], k + 64 * j, a.K);
         }
@@ -94,37 +96,33 @@ __global__ void __launch_bounds__(WARPS * 32) fp8_few_kernel(Fp8Args a) {
 #pragma unroll
         for (int i = 0; i < XT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) fx[q][i][j] = __ldg(sx[i][j] + kb);
+          for (int j = 0; j < 2; ++j) fx[q][i][j] = __ldg(a.x_scale + sx[i][j] + kb);
       }
     }
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       if (kb0 + WARPS * q >= nk) break;
 #pragma unroll
-      for (int i = 0; i < WT; ++i)
+      for (int i = 0; i < XT; ++i) {
+        float d[4] = {};
 #pragma unroll
-        for (int xt = 0; xt < XT; ++xt) {
-          float d[4] = {};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 lo = wv[q][i][0][j], hi = wv[q][i][1][j], b = xv[q][xt][j];
-            mma_m16n8k32(d, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-            mma_m16n8k32(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-          }
-          // rows g and g + 8 of the weights, columns 2 t and 2 t + 1 of x
-          acc[i][xt][0] = fmaf(d[0], fw[q] * fx[q][xt][0], acc[i][xt][0]);
-          acc[i][xt][1] = fmaf(d[1], fw[q] * fx[q][xt][1], acc[i][xt][1]);
-          acc[i][xt][2] = fmaf(d[2], fu[q] * fx[q][xt][0], acc[i][xt][2]);
-          acc[i][xt][3] = fmaf(d[3], fu[q] * fx[q][xt][1], acc[i][xt][3]);
+        for (int j = 0; j < 2; ++j) {
+          const uint4 lo = wv[q][0][j], hi = wv[q][1][j], b = xv[q][i][j];
+          mma_m16n8k32(d, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma_m16n8k32(d, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
         }
+        // rows g and g + 8 of the weights, columns 2 t and 2 t + 1 of x
+        acc[i][0] = fmaf(d[0], fw[q] * fx[q][i][0], acc[i][0]);
+        acc[i][1] = fmaf(d[1], fw[q] * fx[q][i][1], acc[i][1]);
+        acc[i][2] = fmaf(d[2], fu[q] * fx[q][i][0], acc[i][2]);
+        acc[i][3] = fmaf(d[3], fu[q] * fx[q][i][1], acc[i][3]);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
+  for (int i = 0; i < XT; ++i)
 #pragma unroll
-    for (int xt = 0; xt < XT; ++xt)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sums[warp][i][g + 8 * (r >> 1)][8 * xt + 2 * t + (r & 1)] = acc[i][xt][r];
+    for (int r = 0; r < 4; ++r) sums[warp][tile][g + 8 * (r >> 1)][8 * i + 2 * t + (r & 1)] = acc[i][r];
   __syncthreads();
 
   // thread: column n of row m (16 columns of a row side by side)
@@ -197,7 +195,7 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
   la[1].val.clusterDim.y = la[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(WARPS * 32);
+  cfg.blockDim = dim3(WARPS * 32 * (GATED ? 2 : 1));
   cfg.stream = s;
   cfg.attrs = la;
   cfg.numAttrs = cluster ? 2 : 1;
@@ -206,10 +204,13 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-bool takes_few(const Fp8Args& a) { return a.M <= 16; }
+// Measured in graphs, weights from memory (us, here / in linear_fp8.cu), for M x N x K: 8 x 4096 x 4096 5.3 / 8.9,
+// 16 x 4096 x 4096 7.4 / 9.1, 8 x 2048 x 768 2.0 / 5.6; gated to bf16 8.4 / 12.8, 2.4 / 6.1 (8 x 2048 x 768), to e4m3
+// 10.6 / 11.7, 3.8 / 7.0; gated for 16 rows (in a trial) 14.6 / 13.4 and 24.6 / 12.2.
+bool takes_few(const Fp8Args& a) { return a.M <= (a.gated ? 8 : 16); }
 
 cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {
-  if (a.gated) return a.M <= 8 ? launch<1, true>(a, s) : launch<2, true>(a, s);
+  if (a.gated) return launch<1, true>(a, s);
   return a.M <= 8 ? launch<1, false>(a, s) : launch<2, false>(a, s);
 }
 
