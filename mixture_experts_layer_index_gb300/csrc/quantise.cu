@@ -1,10 +1,11 @@
 // Quantisation in blocks of 128 (moe_quantise): s = amax / 448 over 128 columns of a row or over
 // 128 x 128 values (1 where that is 0), q = e4m3(v / s), to nearest even.  One pass: a block's
-// values stay in registers between its maximum and its codes.  Bound by memory.
+// values stay in registers between its maximum and its codes.  Bound by memory; threads walk over
+// their blocks with the next values on their way while they work on the last.
 //
-// The quotient is the correctly rounded one, by Markstein's correction of the product with the
+// Quotients are the correctly rounded ones, by Markstein's correction of the product with the
 // reciprocal (P. Markstein, Computation of elementary functions on the IBM RISC System/6000
-// processor, 1990): q' = q + (v - q s) / s with the remainder exact in one fused operation, four
+// processor, 1990): q' = q + (v - q s) / s with the remainder exact in one fused operation, three
 // instructions instead of a division.  The reciprocal itself is a division, once per block; where
 // the scale is so small or large that a remainder could leave the normal range, every quotient is.
 #include "linear.cuh"
@@ -14,35 +15,45 @@ namespace {
 
 using lin::as_float;
 
+__device__ __forceinline__ float corrected(float v, float s, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, s, v), inv, q);
+}
 struct Scale {
   float s, inv;
   bool plain;  // quotients by division
 };
 __device__ __forceinline__ Scale scale_of(float amax) {
   Scale r;
-  r.s = amax / 448.0f;
+  r.plain = !(amax > 1e-20f && amax < 1e25f);
+  r.s = r.plain ? amax / 448.0f : corrected(amax, 448.0f, 1.0f / 448.0f);
   if (!(r.s > 0.0f)) r.s = 1.0f;
-  r.plain = !(r.s > 1e-25f && r.s < 1e25f);
-  r.inv = 1.0f / r.s;
+  r.inv = __frcp_rn(r.s);
   return r;
 }
 __device__ __forceinline__ float quotient(float v, const Scale& c) {
-  if (c.plain) return v / c.s;
-  const float q = v * c.inv;
-  return copysignf(fmaf(fmaf(-q, c.s, v), c.inv, q), v);  // of a negative zero the remainder is a positive one
+  return copysignf(corrected(v, c.s, c.inv), v);  // of a negative zero the remainder is a positive one
 }
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& c) {
+  float q[8];
+  if (c.plain) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] / c.s;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], c);
+  }
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    w[i] = static_cast<uint32_t>(cvt_e4m3x2(quotient(v[4 * i], c), quotient(v[4 * i + 1], c))) |
-           static_cast<uint32_t>(cvt_e4m3x2(quotient(v[4 * i + 2], c), quotient(v[4 * i + 3], c))) << 16;
+    w[i] = static_cast<uint32_t>(cvt_e4m3x2(q[4 * i], q[4 * i + 1])) |
+           static_cast<uint32_t>(cvt_e4m3x2(q[4 * i + 2], q[4 * i + 3])) << 16;
   return make_uint2(w[0], w[1]);
 }
 
-// This thread's eight values of a group of 128 columns from k0: VEC 8 l .. 8 l + 7, else l + 16 i
-// (l = its place among 16 threads), zeros past K.
-template <typename T, bool VEC>
+// Eight values of a row from column k0 on for thread l of L that share the columns: VEC 8 l .. 8 l + 7,
+// else l + L i; zeros past K.
+template <typename T, bool VEC, int L>
 __device__ __forceinline__ void load8(T (&v)[8], const T* row, int k0, int l, int K) {
   if (VEC) {
     const int k = k0 + 8 * l;
@@ -51,17 +62,17 @@ __device__ __forceinline__ void load8(T (&v)[8], const T* row, int k0, int l, in
       reinterpret_cast<uint4*>(v)[j] = k < K ? __ldg(reinterpret_cast<const uint4*>(row + k) + j) : make_uint4(0, 0, 0, 0);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k0 + l + 16 * i < K ? row[k0 + l + 16 * i] : T(0.0f);
+    for (int i = 0; i < 8; ++i) v[i] = k0 + l + L * i < K ? row[k0 + l + L * i] : T(0.0f);
   }
 }
-template <bool VEC>
+template <bool VEC, int L>
 __device__ __forceinline__ void store8(uint8_t* row, int k0, int l, int K, uint2 w) {
   if (VEC) {
     if (k0 + 8 * l < K) *reinterpret_cast<uint2*>(row + k0 + 8 * l) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (k0 + l + 16 * i < K) row[k0 + l + 16 * i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+      if (k0 + l + L * i < K) row[k0 + l + L * i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
   }
 }
 template <typename T>
@@ -70,88 +81,121 @@ __device__ __forceinline__ float amax8(const T (&v)[8], float m) {
   for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(as_float(v[i])));  // without a NaN's part
   return m;
 }
+template <bool VEC, int L, typename T>
+__device__ __forceinline__ void put8(uint8_t* row, int k0, int l, int K, const T (&v)[8], const Scale& c) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = as_float(v[j]);
+  store8<VEC, L>(row, k0, l, K, codes8(f, c));
+}
 
-// Groups of 16 threads take (row, 128 columns); a block of 16 groups lies `across` groups wide
-// and takes AHEAD of its heights, all of them loaded before the first is used.
+// Groups of 8 threads take (row, 128 columns), 64 columns at a time; a block of 32 groups lies
+// `across` groups wide and takes AHEAD of its heights at a time.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantiseArgs a, int nk, int across) {
-  constexpr int AHEAD = sizeof(T) == 4 ? 2 : 4;
+  constexpr int AHEAD = sizeof(T) == 4 ? 1 : 2;
   dep_wait();
   dep_launch();
-  const int l = threadIdx.x & 15, group = threadIdx.x >> 4, high = 16 / across;
-  const int kb = blockIdx.x * across + group % across;
+  const int l = threadIdx.x & 7, group = threadIdx.x >> 3, high = 32 / across;
+  const int kb = blockIdx.x * across + group % across, k0 = kb * 128;
   const T* x = static_cast<const T*>(a.x);
-  for (long long m0 = static_cast<long long>(blockIdx.y) * high * AHEAD; m0 < a.M; m0 += static_cast<long long>(gridDim.y) * high * AHEAD) {
-    alignas(16) T v[AHEAD][8];
+  alignas(16) T v[AHEAD][2][8], next[AHEAD][2][8];
+  auto load = [&](long long m0) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const long long m = m0 + i * high + group / across;
-      if (kb < nk && m < a.M) load8<T, VEC>(v[i], x + m * a.ld_x, kb * 128, l, a.K);
+      if (kb < nk && m < a.M) {
+        load8<T, VEC, 8>(next[i][0], x + m * a.ld_x, k0, l, a.K);
+        load8<T, VEC, 8>(next[i][1], x + m * a.ld_x, k0 + 64, l, a.K);
+      }
     }
+  };
+  const long long step = static_cast<long long>(gridDim.y) * high * AHEAD;
+  long long m0 = static_cast<long long>(blockIdx.y) * high * AHEAD;
+  load(m0);
+  for (; m0 < a.M; m0 += step) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][j][e] = next[i][j][e];
+    if (m0 + step < a.M) load(m0 + step);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const long long m = m0 + i * high + group / across;
       const bool in = kb < nk && m < a.M;
-      float amax = in ? amax8(v[i], 0.0f) : 0.0f;
+      float amax = in ? amax8(v[i][1], amax8(v[i][0], 0.0f)) : 0.0f;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (!in) continue;
       const Scale c = scale_of(amax);
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = as_float(v[i][j]);
-      store8<VEC>(a.q + m * a.ld_q, kb * 128, l, a.K, codes8(f, c));
+      uint8_t* q = a.q + m * a.ld_q;
+      put8<VEC, 8>(q, k0, l, a.K, v[i][0], c);
+      put8<VEC, 8>(q, k0 + 64, l, a.K, v[i][1], c);
       if (l == 0) a.scale[m * nk + kb] = c.s;
     }
   }
 }
 
-// A block of threads takes 128 x 128 values: 16 threads across, every 16th row.
+// A block of threads takes 128 x 128 values at a time: 16 threads across, every 32nd row.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quantise_block_kernel(QuantiseArgs a, int nk) {
-  __shared__ float s_max[8];
+__global__ void __launch_bounds__(512) quantise_block_kernel(QuantiseArgs a, int nk, int blocks) {
+  __shared__ float s_max[2][16];
   dep_wait();
   dep_launch();
   const int l = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int kb = blockIdx.x % nk;
-  const long long m0 = static_cast<long long>(blockIdx.x / nk) * 128 + r;
   const T* x = static_cast<const T*>(a.x);
-  alignas(16) T v[8][8];
+  alignas(16) T v[4][8], next[4][8];
+  auto load = [&](int b) {
+    const int kb = b % nk;
+    const long long m0 = static_cast<long long>(b / nk) * 128 + r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (m0 + 16 * i < a.M) load8<T, VEC>(v[i], x + (m0 + 16 * i) * a.ld_x, kb * 128, l, a.K);
-  float amax = 0.0f;
+    for (int i = 0; i < 4; ++i)
+      if (m0 + 32 * i < a.M) load8<T, VEC, 16>(next[i], x + (m0 + 32 * i) * a.ld_x, kb * 128, l, a.K);
+  };
+  load(blockIdx.x);
+  int turn = 0;
+  for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (m0 + 16 * i < a.M) amax = amax8(v[i], amax);
-  amax = warp_max(amax);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-  __syncthreads();
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, s_max[i]);
-  const Scale c = scale_of(amax);
+      for (int e = 0; e < 8; ++e) v[i][e] = next[i][e];
+    if (b + static_cast<int>(gridDim.x) < blocks) load(b + gridDim.x);
+    const int kb = b % nk;
+    const long long m0 = static_cast<long long>(b / nk) * 128 + r;
+    float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (m0 + 16 * i >= a.M) break;
-    float f[8];
+    for (int i = 0; i < 4; ++i)
+      if (m0 + 32 * i < a.M) amax = amax8(v[i], amax);
+    amax = warp_max(amax);
+    // two sets of maxima in turn: one barrier per block of values
+    if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = amax;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = as_float(v[i][j]);
-    store8<VEC>(a.q + (m0 + 16 * i) * a.ld_q, kb * 128, l, a.K, codes8(f, c));
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, s_max[turn][i]);
+    turn ^= 1;
+    const Scale c = scale_of(amax);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (m0 + 32 * i < a.M) put8<VEC, 16>(a.q + (m0 + 32 * i) * a.ld_q, kb * 128, l, a.K, v[i], c);
+    if (threadIdx.x == 0) a.scale[b] = c.s;
   }
-  if (threadIdx.x == 0) a.scale[blockIdx.x] = c.s;
 }
 
 template <typename T, bool VEC>
 cudaError_t launch(const QuantiseArgs& a, cudaStream_t s) {
-  const int nk = (a.K + 127) / 128;
-  if (a.block_rows == 128)
-    return launch_dependent(quantise_block_kernel<T, VEC>, dim3(static_cast<unsigned>((a.M + 127) / 128) * nk), dim3(256), 0, s, a, nk);
+  const int nk = (a.K + 127) / 128, sms = num_sms();
+  if (sms < 1) return cudaErrorNoDevice;
+  if (a.block_rows == 128) {
+    const int blocks = (a.M + 127) / 128 * nk, grid = sms * (sizeof(T) == 4 ? 1 : 2);
+    return launch_dependent(quantise_block_kernel<T, VEC>, dim3(blocks < grid ? blocks : grid), dim3(512), 0, s, a, nk, blocks);
+  }
   int across = 1;
-  while (across < 16 && across < nk) across *= 2;
-  const int rows = 16 / across * (sizeof(T) == 4 ? 2 : 4);
-  const long long high = (a.M + static_cast<long long>(rows) - 1) / rows;
-  const dim3 grid((nk + across - 1) / across, static_cast<unsigned>(high < 65535 ? high : 65535));
-  return launch_dependent(quantise_rows_kernel<T, VEC>, grid, dim3(256), 0, s, a, nk, across);
+  while (across < 32 && across < nk) across *= 2;
+  const int wide = (nk + across - 1) / across, rows = 32 / across * (sizeof(T) == 4 ? 1 : 2);
+  const int high = static_cast<int>((a.M + static_cast<long long>(rows) - 1) / rows), full = (sms * 4 + wide - 1) / wide;
+  return launch_dependent(quantise_rows_kernel<T, VEC>, dim3(wide, high < full ? high : full < 65535 ? full : 65535), dim3(256), 0, s, a, nk, across);
 }
 template <typename T>
 cudaError_t launch(const QuantiseArgs& a, cudaStream_t s) {
