@@ -103,12 +103,56 @@ __device__ __forceinline__ void tile_origin(const PairProduct& p, int t, int& r0
   r0 = (group * GR + in_group % rows_here) * TILE;
 }
 
+// 32 columns of 32 rows of a warp, and those of the three warps beside it, to an array of 16-bit
+// values whose rows TMA cannot store: the four warps put 128 columns together in shared memory (rows of
+// 65 words), then each stores eight rows of them, a word at a time wherever the row begins.  All four
+// come here together.  `quad`: their boxes; q: which four; h: which of them.
+constexpr int QUAD_PITCH = 65;
+__device__ __forceinline__ void quad_barrier(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }
+// Not inlined: its registers would be spilled from the path that TMA stores.
+__device__ __noinline__ void store_quad(const uint32_t* quad, int h, int lane, uint16_t* out, long long ld, int rows, int n) {
+#pragma unroll 4
+  for (int r = 8 * h; r < 8 * h + 8; ++r) {
+    if (r >= rows) break;
+    const uint32_t* row = quad + r * QUAD_PITCH;
+    uint16_t* to = out + r * ld;
+    // `odd`: the row begins in the middle of a word, whose other half is not this tile's
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+    if (odd && lane == 0 && n > 0) to[0] = static_cast<uint16_t>(row[0]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int w = lane + 32 * j, c = 2 * w + odd;
+      const uint32_t word = odd ? __funnelshift_r(row[w], row[w + 1], 16) : row[w];  // the last of a row is not stored
+      if (c + 1 < n) *reinterpret_cast<uint32_t*>(to + c) = word;
+      else if (c < n) to[c] = static_cast<uint16_t>(word);
+    }
+  }
+}
+__device__ __forceinline__ void flush_columns(uint32_t* quad, int q, int h, int lane, const float (&v)[32], void* out, int dtype,
+                                              long long ld, int r0, int R, int c0, int C) {
+  quad_barrier(q);  // no store still reads one of the boxes
+  uint32_t* mine = quad + lane * QUAD_PITCH + h * 16;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (dtype == MOE_DTYPE_BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      mine[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      mine[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  quad_barrier(q);
+  store_quad(quad, h, lane, static_cast<uint16_t*>(out) + static_cast<size_t>(r0) * ld + c0, ld, R - r0, min(HALF, C - c0));
+  quad_barrier(q);  // the boxes may be written again
+}
+
 // The epilogue of a gated tile for one warp: 32 rows, 32 gate columns and the 32 up columns beside
 // them, both in registers at once; z in two boxes of 64-byte rows, h in one (or one of 128-byte
 // rows of fp32 values).  p.y_tma, p.z_tma as elsewhere; m1.y is the up half of z.
 __device__ __forceinline__ void gated_tile(const PairParams& p, const CUtensorMap* mh, const CUtensorMap* mg,
-                                           const CUtensorMap* mu, uint8_t* box, int lane, uint32_t tb, uint32_t free_bar,
-                                           int r0, int c0, bool bias_wide) {
+                                           const CUtensorMap* mu, uint8_t* box, int q, int h, int lane, uint32_t tb,
+                                           uint32_t free_bar, int r0, int c0, bool bias_wide) {
   const Epilogue& ep = p.ep;
   const int R = p.prod[0].R, C = p.prod[0].C;
   float g[32], u[32];
@@ -131,6 +175,7 @@ __device__ __forceinline__ void gated_tile(const PairParams& p, const CUtensorMa
             C - c0 - 16 * j, bias_wide);
     }
   }
+  uint32_t* quad = reinterpret_cast<uint32_t*>(box - h * BOX_BYTES);
   const bool stored = r0 < R && c0 < C;
   if (ep.z && p.z_tma) {
 #pragma unroll
@@ -148,19 +193,8 @@ __device__ __forceinline__ void gated_tile(const PairParams& p, const CUtensorMa
       bulk_commit_group();
     }
   } else if (ep.z) {
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) t[i] = k ? u[16 * j + i] : g[16 * j + i];
-        put_box(box, lane, j, MOE_DTYPE_F32, t);
-      }
-      __syncwarp();
-      flush_box(box, lane, static_cast<uint8_t*>(ep.z) + (k ? static_cast<size_t>(p.prod[0].half) * 2 : 0), ep.z_dtype,
-                ep.ld_z, nullptr, r0, R, c0, C);
-    }
+    flush_columns(quad, q, h, lane, g, ep.z, ep.z_dtype, ep.ld_z, r0, R, c0 - 32 * h, C);
+    flush_columns(quad, q, h, lane, u, static_cast<uint16_t*>(ep.z) + p.prod[0].half, ep.z_dtype, ep.ld_z, r0, R, c0 - 32 * h, C);
   }
   act_all<32>(g, ep.act);
 #pragma unroll
@@ -168,6 +202,10 @@ __device__ __forceinline__ void gated_tile(const PairParams& p, const CUtensorMa
   if (ep.z && p.z_tma) {
     if (lane == 0) bulk_wait_group_read0();
     __syncwarp();
+  }
+  if (!p.y_tma && ep.out_dtype != MOE_DTYPE_F32) {
+    flush_columns(quad, q, h, lane, g, ep.y, ep.out_dtype, ep.ld_y, r0, R, c0 - 32 * h, C);
+    return;
   }
   if (p.y_tma && ep.out_dtype != MOE_DTYPE_F32) {
 #pragma unroll
@@ -385,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4) {
     const int e = warp - 4, q = warp & 3, h = e >> 2;
-    uint8_t* box = smem + BOX_OFFSET + e * BOX_BYTES;
+    uint8_t* box = smem + BOX_OFFSET + (GATED ? 4 * q + h : e) * BOX_BYTES;  // GATED: a quadrant's four side by side
     const uint32_t lead_tempty0 = map_rank(tempty0, 0);
     const Epilogue& ep = p.ep;
     const bool wide = ep.out_dtype == MOE_DTYPE_F32;
@@ -413,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * (TILE_COLS / 4);
       if constexpr (GATED) {
-        gated_tile(p, my, &tmZ, &m1.y, box, lane, tb, lead_tempty0 + 8 * acc, r0, c0, bias_wide);
+        gated_tile(p, my, &tmZ, &m1.y, box, q, h, lane, tb, lead_tempty0 + 8 * acc, r0, c0, bias_wide);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
         continue;

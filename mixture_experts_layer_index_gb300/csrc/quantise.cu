@@ -6,8 +6,10 @@
 // Quotients are the correctly rounded ones, by Markstein's correction of the product with the
 // reciprocal (P. Markstein, Computation of elementary functions on the IBM RISC System/6000
 // processor, 1990): q' = q + (v - q s) / s with the remainder exact in one fused operation, three
-// instructions instead of a division.  The reciprocal itself is a division, once per block; where
-// the scale is so small or large that a remainder could leave the normal range, every quotient is.
+// instructions instead of a division.  All of it with the reciprocal's
+// negative, which gives -q' and keeps the sign of a zero; the codes' sign bits are turned over at the
+// end.  The reciprocal itself is a division, once per block; where the scale is so small or large
+// that a remainder could leave the normal range, every quotient is.
 #include "linear.cuh"
 
 namespace moe {
@@ -15,39 +17,36 @@ namespace {
 
 using lin::as_float;
 
-__device__ __forceinline__ float corrected(float v, float s, float inv) {
-  const float q = v * inv;
-  return fmaf(fmaf(-q, s, v), inv, q);
-}
 struct Scale {
-  float s, inv;
+  float s, ninv;
   bool plain;  // quotients by division
 };
 __device__ __forceinline__ Scale scale_of(float amax) {
   Scale r;
   r.plain = !(amax > 1e-20f && amax < 1e25f);
-  r.s = r.plain ? amax / 448.0f : corrected(amax, 448.0f, 1.0f / 448.0f);
+  const float q = amax * (1.0f / 448.0f);
+  r.s = r.plain ? amax / 448.0f : fmaf(fmaf(-q, 448.0f, amax), 1.0f / 448.0f, q);
   if (!(r.s > 0.0f)) r.s = 1.0f;
-  r.inv = __frcp_rn(r.s);
+  r.ninv = -__frcp_rn(r.s);
   return r;
 }
-__device__ __forceinline__ float quotient(float v, const Scale& c) {
-  return copysignf(corrected(v, c.s, c.inv), v);  // of a negative zero the remainder is a positive one
-}
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& c) {
-  float q[8];
+  float q[8];  // negative quotients
   if (c.plain) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = v[i] / c.s;
+    for (int i = 0; i < 8; ++i) q[i] = -(v[i] / c.s);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], c);
+    for (int i = 0; i < 8; ++i) {
+      const float nq = v[i] * c.ninv;
+      q[i] = fmaf(fmaf(nq, c.s, v[i]), c.ninv, nq);
+    }
   }
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    w[i] = static_cast<uint32_t>(cvt_e4m3x2(q[4 * i], q[4 * i + 1])) |
-           static_cast<uint32_t>(cvt_e4m3x2(q[4 * i + 2], q[4 * i + 3])) << 16;
+    w[i] = (static_cast<uint32_t>(cvt_e4m3x2(q[4 * i], q[4 * i + 1])) |
+            static_cast<uint32_t>(cvt_e4m3x2(q[4 * i + 2], q[4 * i + 3])) << 16) ^ 0x80808080u;
   return make_uint2(w[0], w[1]);
 }
 
@@ -75,12 +74,20 @@ __device__ __forceinline__ void store8(uint8_t* row, int k0, int l, int K, uint2
       if (k0 + l + L * i < K) row[k0 + l + L * i] = static_cast<uint8_t>((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
   }
 }
-template <typename T>
-__device__ __forceinline__ float amax8(const T (&v)[8], float m) {
+// The largest magnitude, without a NaN's part.
+__device__ __forceinline__ float amax8(const float (&v)[8], float m) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(as_float(v[i])));  // without a NaN's part
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
   return m;
 }
+template <typename T2, typename T>
+__device__ __forceinline__ float amax8_pairs(const T (&v)[8], float m) {
+  const T2* p = reinterpret_cast<const T2*>(v);
+  const T2 a = __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
+  return fmaxf(m, fmaxf(as_float(a.x), as_float(a.y)));
+}
+__device__ __forceinline__ float amax8(const __nv_bfloat16 (&v)[8], float m) { return amax8_pairs<__nv_bfloat162>(v, m); }
+__device__ __forceinline__ float amax8(const __half (&v)[8], float m) { return amax8_pairs<__half2>(v, m); }
 template <bool VEC, int L, typename T>
 __device__ __forceinline__ void put8(uint8_t* row, int k0, int l, int K, const T (&v)[8], const Scale& c) {
   float f[8];
@@ -99,28 +106,18 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantiseArgs a, int 
   const int l = threadIdx.x & 7, group = threadIdx.x >> 3, high = 32 / across;
   const int kb = blockIdx.x * across + group % across, k0 = kb * 128;
   const T* x = static_cast<const T*>(a.x);
-  alignas(16) T v[AHEAD][2][8], next[AHEAD][2][8];
-  auto load = [&](long long m0) {
+  alignas(16) T buffer[2][AHEAD][2][8];
+  auto load = [&](T (&v)[AHEAD][2][8], long long m0) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const long long m = m0 + i * high + group / across;
       if (kb < nk && m < a.M) {
-        load8<T, VEC, 8>(next[i][0], x + m * a.ld_x, k0, l, a.K);
-        load8<T, VEC, 8>(next[i][1], x + m * a.ld_x, k0 + 64, l, a.K);
+        load8<T, VEC, 8>(v[i][0], x + m * a.ld_x, k0, l, a.K);
+        load8<T, VEC, 8>(v[i][1], x + m * a.ld_x, k0 + 64, l, a.K);
       }
     }
   };
-  const long long step = static_cast<long long>(gridDim.y) * high * AHEAD;
-  long long m0 = static_cast<long long>(blockIdx.y) * high * AHEAD;
-  load(m0);
-  for (; m0 < a.M; m0 += step) {
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][j][e] = next[i][j][e];
-    if (m0 + step < a.M) load(m0 + step);
+  auto finish = [&](const T (&v)[AHEAD][2][8], long long m0) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const long long m = m0 + i * high + group / across;
@@ -135,33 +132,40 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantiseArgs a, int 
       put8<VEC, 8>(q, k0 + 64, l, a.K, v[i][1], c);
       if (l == 0) a.scale[m * nk + kb] = c.s;
     }
+  };
+  const long long step = static_cast<long long>(gridDim.y) * high * AHEAD;
+  long long m0 = static_cast<long long>(blockIdx.y) * high * AHEAD;
+  load(buffer[0], m0);
+  for (; m0 < a.M; m0 += step) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) buffer[1][i][j][e] = buffer[0][i][j][e];
+    load(buffer[0], m0 + step);
+    finish(buffer[1], m0);
   }
 }
 
 // A block of threads takes 128 x 128 values at a time: 16 threads across, every 32nd row.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(512) quantise_block_kernel(QuantiseArgs a, int nk, int blocks) {
+__global__ void __launch_bounds__(512, 2) quantise_block_kernel(QuantiseArgs a, int nk, int blocks) {
   __shared__ float s_max[2][16];
   dep_wait();
   dep_launch();
   const int l = threadIdx.x & 15, r = threadIdx.x >> 4;
   const T* x = static_cast<const T*>(a.x);
-  alignas(16) T v[4][8], next[4][8];
-  auto load = [&](int b) {
+  alignas(16) T buffer[2][4][8];
+  auto load = [&](T (&v)[4][8], int b) {
+    if (b >= blocks) return;
     const int kb = b % nk;
     const long long m0 = static_cast<long long>(b / nk) * 128 + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (m0 + 32 * i < a.M) load8<T, VEC, 16>(next[i], x + (m0 + 32 * i) * a.ld_x, kb * 128, l, a.K);
+      if (m0 + 32 * i < a.M) load8<T, VEC, 16>(v[i], x + (m0 + 32 * i) * a.ld_x, kb * 128, l, a.K);
   };
-  load(blockIdx.x);
-  int turn = 0;
-  for (int b = blockIdx.x; b < blocks; b += gridDim.x) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = next[i][e];
-    if (b + static_cast<int>(gridDim.x) < blocks) load(b + gridDim.x);
+  auto finish = [&](const T (&v)[4][8], float* maxima, int b) {
     const int kb = b % nk;
     const long long m0 = static_cast<long long>(b / nk) * 128 + r;
     float amax = 0.0f;
@@ -169,17 +173,30 @@ __global__ void __launch_bounds__(512) quantise_block_kernel(QuantiseArgs a, int
     for (int i = 0; i < 4; ++i)
       if (m0 + 32 * i < a.M) amax = amax8(v[i], amax);
     amax = warp_max(amax);
-    // two sets of maxima in turn: one barrier per block of values
-    if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, s_max[turn][i]);
-    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) maxima[threadIdx.x >> 5] = amax;
+    __syncthreads();  // the other set of maxima is written next: one barrier per block of values
+    amax = warp_max(maxima[threadIdx.x & 15]);
     const Scale c = scale_of(amax);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (m0 + 32 * i < a.M) put8<VEC, 16>(a.q + (m0 + 32 * i) * a.ld_q, kb * 128, l, a.K, v[i], c);
     if (threadIdx.x == 0) a.scale[b] = c.s;
+  };
+  // 16-bit values: the next on their way meanwhile; fp32: the registers go to a second block on the SM
+  constexpr bool EARLY = sizeof(T) == 2;
+  const int step = static_cast<int>(gridDim.x);
+  load(buffer[0], blockIdx.x);
+  int turn = 0;
+  for (long long b = blockIdx.x; b < blocks; b += step) {
+    const int next = static_cast<int>(min(b + step, static_cast<long long>(blocks)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) buffer[1][i][e] = buffer[0][i][e];
+    if (EARLY) load(buffer[0], next);
+    finish(buffer[1], s_max[turn], static_cast<int>(b));
+    if (!EARLY) load(buffer[0], next);
+    turn ^= 1;
   }
 }
 
@@ -188,7 +205,7 @@ cudaError_t launch(const QuantiseArgs& a, cudaStream_t s) {
   const int nk = (a.K + 127) / 128, sms = num_sms();
   if (sms < 1) return cudaErrorNoDevice;
   if (a.block_rows == 128) {
-    const int blocks = (a.M + 127) / 128 * nk, grid = sms * (sizeof(T) == 4 ? 1 : 2);
+    const int blocks = (a.M + 127) / 128 * nk, grid = sms * 2;
     return launch_dependent(quantise_block_kernel<T, VEC>, dim3(blocks < grid ? blocks : grid), dim3(512), 0, s, a, nk, blocks);
   }
   int across = 1;
