@@ -154,11 +154,15 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
 }
 
+// Gated, weights from memory (us, here / on the tensor cores):
+//   1 row   4096 x 4096  12.5 / 14.9;  2048 x 768  3.0 / 5.8;  2 rows  1024 x 4096  7.7 / 7.5;  8192 x 1024  7.9 / 9.3
+//   4 rows  2730 x 2048  7.7 / 8.5;  1024 x 4096  9.2 / 7.5;  4096 x 2048  11.3 / 9.8;  8 rows  2048 x 768  4.9 / 5.8;
+//   2730 x 2048  14.0 / 8.2
 bool takes_few(const GatedArgs& a) {
   if (a.K % 8 != 0) return false;
   const long long weights = 2ll * a.N * a.K;
   if (a.M <= 2) return true;
-  if (a.M <= 4) return weights <= 1 << 23;
+  if (a.M <= 4) return weights <= 3 << 22 && a.K <= 3000;
   return a.M <= 8 && weights <= 1 << 22 && a.K <= 3000;
 }
 

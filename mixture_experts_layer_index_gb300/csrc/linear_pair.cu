@@ -586,6 +586,12 @@ bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
 // and more with an activation, z, a residual, or rows that TMA cannot store.
 float pair_estimate(const Product& q) {
   const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + tile_cols(q) - 1) / tile_cols(q));
+  if (q.gated) {  // its tile has half the columns; fitted as linear.cu's gated_estimate
+    float us = 0.29f * ((q.K + BK - 1) / BK) + 0.9f;
+    if (q.ep.z) us += storable(q.ep.z, q.ep.z_dtype, q.C, q.ep.ld_z) ? 1.3f : 4.0f;
+    if (!storable(q.ep.y, q.ep.out_dtype, q.C, q.ep.ld_y)) us += 0.6f;
+    return 6.0f + (tiles + 75) / 76 * us;
+  }
   const float stages = 0.30f * ((q.K + BK - 1) / BK);
   float epilogue = 3.5f;
   if (q.ep.act != MOE_ACT_NONE) epilogue += 1.0f;
