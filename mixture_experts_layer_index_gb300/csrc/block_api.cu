@@ -185,6 +185,14 @@ LinearBackwardLayout plan_linear_backward(int M, int N) {
   return L;
 }
 
+LinearBackwardLayout plan_gated_backward(int M, int N) {
+  LinearBackwardLayout L;
+  L.partials = kHeaderBytes;
+  L.dz = align_up(L.partials + gated_partials_bytes(M, N), 256);
+  L.total = align_up(L.dz + linear_dz_bytes(M, 2 * N), 256);
+  return L;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -414,7 +422,7 @@ moe_status moe_gated(const moe_gated_problem* p, const void* x, const void* w, c
 }
 
 size_t moe_gated_backward_workspace_size(const moe_gated_problem* p) {
-  return check_gated(p) == MOE_OK ? plan_linear_backward(p->M, 2 * p->N).total : 0;
+  return check_gated(p) == MOE_OK ? plan_gated_backward(p->M, p->N).total : 0;
 }
 
 moe_status moe_gated_backward(const moe_gated_problem* p, const void* dh, const void* x, const void* w, const void* z,
@@ -432,7 +440,7 @@ moe_status moe_gated_backward(const moe_gated_problem* p, const void* dh, const 
   }
   if (!dh || !z || (dw && !x) || (dx && !w)) return MOE_ERR_INVALID_ARG;
   if (!fits(dh, p->out_dtype) || !aligned(x, 16) || !aligned(w, 16) || !fits(z, p->dtype)) return MOE_ERR_INVALID_ARG;
-  const LinearBackwardLayout L = plan_linear_backward(p->M, 2 * p->N);
+  const LinearBackwardLayout L = plan_gated_backward(p->M, p->N);
   if (!ws || !aligned(ws, 256) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   GatedBackwardArgs a{};
   a.M = p->M;

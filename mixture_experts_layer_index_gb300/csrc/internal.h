@@ -320,6 +320,7 @@ struct GatedBackwardArgs {
   float* partials;  // column sums of dz per row chunk
   DeviceHeader* hdr;
 };
+size_t gated_partials_bytes(int M, int N);
 cudaError_t launch_gated_backward(const GatedBackwardArgs& a, cudaStream_t s);
 
 // Quantisation in blocks of 128 (quantise.cu).

@@ -623,9 +623,10 @@ cudaError_t launch_gradient_products(const GradientProducts& g, cudaStream_t s) 
     const Choice cx = choose_tile(dx), cw = choose_tile(dw), both = choose_both(dw, dx);
     const bool px = takes_pair(dx, cx), pw = takes_pair(dw, cw);
     const float apart = (px ? pair_estimate(dx) : cx.us) + (pw ? pair_estimate(dw) : cw.us);
-    if ((px && pw) || (both.bn && both.us < apart)) {
+    const bool large = (px && pw) || (g.pairs_may_mix && pair_estimate_both(dx, dw) < (both.bn && both.us < apart ? both.us : apart));
+    if (large || (both.bn && both.us < apart)) {
       stage_begin("linear_dx_dw", s);
-      const cudaError_t err = px && pw ? launch_pair(dx, &dw, s) : launch_shape<false>(dw, &dx, both, s);
+      const cudaError_t err = large ? launch_pair(dx, &dw, s) : launch_shape<false>(dw, &dx, both, s);
       stage_end(s);
       return err;
     }
@@ -824,7 +825,7 @@ cudaError_t launch_linear_backward(const LinearBackwardArgs& a, cudaStream_t s) 
   }
   if (err != cudaSuccess || !products) return err;
   const Operand dz = direct ? Operand{a.dy, a.ld_y, a.N, a.M} : Operand{a.dz, dz_ld(a.N), a.N, a.M};
-  return launch_gradient_products({a.M, a.N, a.K, a.dtype, a.ld_x, a.ld_w, a.x, a.w, a.dx, a.dw, dz, a.hdr}, s);
+  return launch_gradient_products({a.M, a.N, a.K, a.dtype, a.ld_x, a.ld_w, a.x, a.w, a.dx, a.dw, dz, false, a.hdr}, s);
 }
 
 }  // namespace moe

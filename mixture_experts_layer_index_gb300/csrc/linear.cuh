@@ -194,6 +194,7 @@ struct Product {
 // linear_pair.cu: about how long a launch takes (us); the product, or two of a gradient
 // (the same type and row length, no bias, activation, residual or z).
 float pair_estimate(const Product& p);
+float pair_estimate_both(const Product& a, const Product& b);
 cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s);
 // The product by the kernel whose estimate is the least.
 cudaError_t launch_product(const Product& q, cudaStream_t s);
@@ -207,6 +208,7 @@ struct GradientProducts {
   void* dx;
   void* dw;
   Operand dz;
+  bool pairs_may_mix;  // products that would not fill the GPU in large tiles each may share such a launch
   DeviceHeader* hdr;
 };
 cudaError_t launch_gradient_products(const GradientProducts& g, cudaStream_t s);

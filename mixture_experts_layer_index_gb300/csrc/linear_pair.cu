@@ -602,6 +602,19 @@ float pair_estimate(const Product& q) {
   return 4.0f + stages + epilogue + (waves - 1) * (stages > epilogue ? stages : epilogue);
 }
 
+// Two products of a gradient side by side: their tiles' stages over all pairs, or the longest sum.
+float pair_estimate_both(const Product& a, const Product& b) {
+  float work = 0.0f, longest = 0.0f;
+  for (const Product* q : {&a, &b}) {
+    const float tiles = static_cast<float>((q->R + TILE - 1) / TILE) * ((q->C + TILE - 1) / TILE);
+    float stages = 0.30f * ((q->K + BK - 1) / BK);
+    if (stages > longest) longest = stages;
+    if (stages < 3.5f) stages = 3.5f;  // a tile's epilogue
+    work += tiles * stages / 76.0f;
+  }
+  return 4.0f + (work > longest ? work : longest) + 3.5f;
+}
+
 cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_t s) {
   const int sms = num_sms();
   if (sms < 2) return cudaErrorNoDevice;
