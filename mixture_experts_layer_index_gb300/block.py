@@ -15,6 +15,16 @@ without synchronising and can be captured in a CUDA graph.
 The experts have no gradient here (their weights are frozen, as when a router is
 tuned): router_gradient takes the gradient of a loss into the routing weights w
 back through the routing rule, the router's linear layer and the norms.
+
+DenseBlock is a block whose FFN every token passes (a model's first layers, say), with
+the same boundary:
+
+    h', x = h + gate * N_post(o),  N_pre(h')      moe_norm_forward
+    a = act(x W_g^T) * (x W_u^T)                  moe_gated
+    o' = a W_d^T                                  moe_linear
+
+and its whole gradient, or, for inference, on e4m3 weights with a scale per 128 x 128 block
+(moe_quantise on x, moe_gated_fp8, moe_linear_fp8).
 """
 from __future__ import annotations
 
@@ -22,11 +32,14 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (MOE_DTYPE_F32, MOE_GATE_CHANNEL, MOE_GATE_NONE, MOE_NORM_RMS, forward_options,
-               linear_problem, moe_forward_routed, moe_linear, moe_linear_backward,
-               moe_linear_backward_workspace_size, moe_linear_workspace_size, moe_norm_backward,
-               moe_norm_backward_workspace_size, moe_norm_forward, moe_read_device_status, moe_route_backward,
-               moe_route_ex, moe_workspace_size_ex, norm_problem, problem, route_options)
+from . import (MOE_ACT_SILU, MOE_BF16, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_FP8_BLOCK128,
+               MOE_GATE_CHANNEL, MOE_GATE_NONE, MOE_NORM_RMS, QUANT_BY_NAME, forward_options, gated_problem, linear_problem,
+               moe_forward_routed, moe_gated, moe_gated_backward, moe_gated_backward_workspace_size, moe_gated_fp8,
+               moe_gated_fp8_workspace_size, moe_gated_workspace_size, moe_linear, moe_linear_backward,
+               moe_linear_backward_workspace_size, moe_linear_fp8, moe_linear_fp8_workspace_size,
+               moe_linear_workspace_size, moe_norm_backward, moe_norm_backward_workspace_size, moe_norm_forward,
+               moe_quantise, moe_read_device_status, moe_route_backward, moe_route_ex, moe_workspace_size_ex, norm_problem,
+               problem, quantise_problem, route_options)
 
 
 class RouterGradient(NamedTuple):
@@ -118,3 +131,126 @@ class Block:
     def status(self, stream=None) -> int:
         """Device status of the last forward, MOE_OK before the first (blocks until it is done)."""
         return moe_read_device_status(self.ws_linear, stream) or moe_read_device_status(self.ws, stream)
+
+
+def _scratch(n: int, device) -> torch.Tensor:
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()  # the status word, which a step clears and sets: no error before the first
+    return ws
+
+
+def quantise_dense(w_gated: torch.Tensor, w_down: torch.Tensor, stream=None):
+    """The e4m3 weights of a DenseBlock from its 16- or 32-bit ones: (codes [2 N, H], scales [2, N / 128, H / 128],
+    codes [H, N], scales [H / 128, N / 128]), the counts of blocks rounded up."""
+    dtype = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+
+    def codes(w):
+        rows, cols = w.shape
+        q = torch.empty(rows, cols, dtype=torch.uint8, device=w.device)
+        s = torch.empty(-(-rows // 128), -(-cols // 128), device=w.device)
+        moe_quantise(quantise_problem(rows, cols, dtype[w.dtype], 128), w, q, s, stream=stream)
+        return q, s
+
+    N = w_gated.shape[0] // 2
+    halves = [codes(w_gated[:N]), codes(w_gated[N:])]
+    return (torch.cat([q for q, _ in halves]), torch.stack([s for _, s in halves]), *codes(w_down))
+
+
+class DenseGradient(NamedTuple):
+    dh: torch.Tensor          # [T, H] into the residual stream h
+    d_o: torch.Tensor         # [T, H] into the block output o
+    gated_weight: torch.Tensor
+    down_weight: torch.Tensor
+    post_weight: torch.Tensor
+    pre_weight: torch.Tensor
+    gate: Optional[torch.Tensor]
+
+
+class DenseBlock:
+    """A block for T tokens, hidden size H and N gated columns, whose FFN every token passes.
+
+    weights: quant "bf16": (gated [2 N, H] bf16, N gate rows and then N up rows; down [H, N]
+    bf16), H and N multiples of 8; "fp8_block": what quantise_dense returns, H and N
+    multiples of 16.  norms as Block's.  act: a moe_act.  train (bf16): keeps what gradient needs."""
+
+    def __init__(self, T: int, H: int, N: int, weights, norms, quant="bf16", act: int = MOE_ACT_SILU, train: bool = False,
+                 eps: float = 1e-6):
+        quant = QUANT_BY_NAME[quant] if isinstance(quant, str) else int(quant)
+        if quant not in (MOE_BF16, MOE_FP8_BLOCK128):
+            raise ValueError("a dense block's weights are bf16 or fp8_block")
+        if train and quant != MOE_BF16:
+            raise ValueError("FP8 weights have no gradient")
+        self.T, self.H, self.N, self.fp8, self.train = T, H, N, quant == MOE_FP8_BLOCK128, train
+        self.weights, self.norms = weights, norms
+        self.norm = norm_problem(T, H, MOE_NORM_RMS, MOE_NORM_RMS,
+                                 gate=MOE_GATE_NONE if norms[2] is None else MOE_GATE_CHANNEL, w_dtype=MOE_DTYPE_F32,
+                                 eps=eps)
+        dev = weights[0].device
+
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        self.h_out, self.x, self.o_out = (empty(T, H) for _ in range(3))
+        if self.fp8:
+            self.quantise = quantise_problem(T, H)
+            self.gated = gated_problem(T, N, H, MOE_DTYPE_E4M3, MOE_DTYPE_E4M3, act=act)
+            self.down = linear_problem(T, H, N, dtype=MOE_DTYPE_E4M3)
+            self.x_codes, self.x_scale = empty(T, H, dtype=torch.uint8), empty(T, -(-H // 128), dtype=torch.float32)
+            self.a, self.a_scale = empty(T, N, dtype=torch.uint8), empty(T, -(-N // 128), dtype=torch.float32)
+            sizes = moe_gated_fp8_workspace_size(self.gated), moe_linear_fp8_workspace_size(self.down)
+        else:
+            self.gated, self.down = gated_problem(T, N, H, act=act), linear_problem(T, H, N)
+            self.a, self.z = empty(T, N), empty(T, 2 * N) if train else None
+            sizes = moe_gated_workspace_size(self.gated), moe_linear_workspace_size(self.down)
+        if 0 in sizes:
+            raise ValueError("H and N are multiples of 8 (bf16) or 16 (fp8_block)")
+        self.ws_gated, self.ws_down = (_scratch(n, dev) for n in sizes)
+        self._grad = None
+
+    def forward(self, h: torch.Tensor, o: torch.Tensor, stream=None):
+        """(h', o') as Block.forward."""
+        post, pre, gate = self.norms
+        moe_norm_forward(self.norm, h, o, gate, post, None, pre, None, self.h_out, self.x, stream=stream)
+        if self.fp8:
+            wg, sg, wd, sd = self.weights
+            moe_quantise(self.quantise, self.x, self.x_codes, self.x_scale, stream=stream)
+            moe_gated_fp8(self.gated, self.x_codes, self.x_scale, wg, sg, None, self.a, self.a_scale, self.ws_gated,
+                          stream=stream)
+            moe_linear_fp8(self.down, self.a, self.a_scale, wd, sd, None, None, self.o_out, self.ws_down, stream=stream)
+        else:
+            wg, wd = self.weights
+            moe_gated(self.gated, self.x, wg, None, self.a, self.z, self.ws_gated, stream=stream)
+            moe_linear(self.down, self.a, wd, None, None, self.o_out, None, self.ws_down, stream=stream)
+        return self.h_out, self.o_out
+
+    def gradient(self, o: torch.Tensor, do_out: torch.Tensor, dh_out: Optional[torch.Tensor] = None,
+                 stream=None) -> DenseGradient:
+        """Gradients of a loss with gradient do_out [T, H] bf16 into o' (and dh_out [T, H] into h') of the last
+        forward, for the o that it took.  The block's own buffers, which the next gradient writes again."""
+        if not self.train:
+            raise ValueError("the block was made without train")
+        post, pre, gate = self.norms
+        wg, wd = self.weights
+        T, H, N = self.T, self.H, self.N
+        if self._grad is None:
+            dev = wg.device
+
+            def empty(*shape, dtype=torch.bfloat16):
+                return torch.empty(*shape, dtype=dtype, device=dev)
+
+            f32 = torch.float32
+            out = DenseGradient(empty(T, H), empty(T, H), empty(2 * N, H), empty(H, N), empty(H, dtype=f32),
+                                empty(H, dtype=f32), None if gate is None else empty(H, dtype=f32))
+            n = max(moe_linear_backward_workspace_size(self.down), moe_gated_backward_workspace_size(self.gated),
+                    moe_norm_backward_workspace_size(self.norm))
+            self._grad = (out, empty(T, N), empty(T, H), torch.empty(n, dtype=torch.uint8, device=dev))
+        out, da, dx, ws = self._grad
+        moe_linear_backward(self.down, do_out, self.a, wd, None, da, out.down_weight, None, ws, stream=stream)
+        moe_gated_backward(self.gated, da, self.x, wg, self.z, dx, out.gated_weight, None, ws, stream=stream)
+        moe_norm_backward(self.norm, dh_out, dx, self.h_out, o, gate, post, None, pre, out.dh, out.d_o, out.gate,
+                          out.post_weight, None, out.pre_weight, None, ws, stream=stream)
+        return out
+
+    def status(self, stream=None) -> int:
+        """Device status of the last forward, MOE_OK before the first (blocks until it is done)."""
+        return moe_read_device_status(self.ws_gated, stream) or moe_read_device_status(self.ws_down, stream)
