@@ -420,6 +420,8 @@ __global__ void __launch_bounds__(THREADS) linear_kernel(const __grid_constant__
   }
 }
 
+// Accumulators that a block spreads its part of the sum over.
+inline int accumulators(const Product& q, int bn) { return q.ep.out_dtype != MOE_DTYPE_F32 ? 1 : bn <= 64 ? 4 : 2; }
 // Output columns per tile.
 inline int tile_cols(const Product& q) { return q.gated ? BM / 2 : BM; }
 
@@ -469,7 +471,7 @@ cudaError_t launch_tile(const Product& q, const Product* second, const Choice& c
   // fp32 output: the tensor core's running sum rounds at every step, so its length is
   // kept short by spreading the sum over up to four accumulators (here; large products, which
   // go to linear_pair.cu, keep the whole sum in one: its two are the tiles in flight)
-  p.nacc = q.ep.out_dtype != MOE_DTYPE_F32 ? 1 : BN <= 64 ? 4 : 2;
+  p.nacc = accumulators(q, BN);
   int cols = 32;
   while (cols < BN * p.nacc) cols *= 2;
   p.tmem_cols = cols;
@@ -528,6 +530,9 @@ float gated_estimate(const Product& q, int bn, int splits) {
   const int i = bn <= 16 ? 0 : bn <= 32 ? 1 : bn <= 64 ? 2 : bn <= 128 ? 3 : 4;
   const float per_stage[5] = {0.126f, 0.138f, 0.19f, 0.277f, 0.446f};
   const int stages = ((q.K + BK - 1) / BK + splits - 1) / splits;
+  // fp32 output: no accumulator sums more than 512 values (its rounding, 1.8e-9 of the sum per value, would
+  // show); linear_pair.cu takes what finds no such form here
+  if (q.ep.out_dtype == MOE_DTYPE_F32 && stages > 8 * accumulators(q, bn)) return 1e9f;
   const long long blocks = static_cast<long long>((q.C + BM / 2 - 1) / (BM / 2)) * ((q.R + bn - 1) / bn) * splits;
   const int occupancy = bn == 256 ? 1 : 2, sms = splits == 8 ? 120 : splits == 4 ? 144 : 152;
   const long long waves = (blocks + sms * occupancy - 1) / (sms * occupancy);

@@ -15,7 +15,8 @@
 // columns at a time are loaded from TMEM, finished in fp32, rounded once, staged in
 // shared memory as a 128-byte-swizzled box of 32 rows and stored by TMA, which
 // clips the edges.  A tile's whole sum is one accumulator's, whatever the output's
-// type (tensor memory holds two tiles), rounded in fp32 at every step of it.
+// type (tensor memory holds two tiles), rounded in fp32 at every step of it; only a gated
+// tile's with fp32 output is cut into parts.
 //
 // Bound by the tensor cores: 16384 x 8192 x 2048 bf16 takes 294 us, 1.87 PFLOP/s (a library
 // product reaches 1.95 in short runs, 1.74 under the power limit).  With a GELU and its
@@ -57,6 +58,7 @@ struct PairParams {
   int tiles[2];
   int ratio;  // tiles of prod[1] that take about as long as one of prod[0]
   int type;
+  int seg;           // gated: stages that one accumulator sums
   int y_tma, z_tma;  // whether TMA can store the output (16-byte aligned rows)
   Epilogue ep;
   void* y[2];        // per product
@@ -151,21 +153,11 @@ __device__ __forceinline__ void flush_columns(uint32_t* quad, int q, int h, int 
 // them, both in registers at once; z in two boxes of 64-byte rows, h in one (or one of 128-byte
 // rows of fp32 values).  p.y_tma, p.z_tma as elsewhere; m1.y is the up half of z.
 __device__ __forceinline__ void gated_tile(const PairParams& p, const CUtensorMap* mh, const CUtensorMap* mg,
-                                           const CUtensorMap* mu, uint8_t* box, int q, int h, int lane, uint32_t tb,
-                                           uint32_t free_bar, int r0, int c0, bool bias_wide) {
+                                           const CUtensorMap* mu, uint8_t* box, int q, int h, int lane, float (&g)[32],
+                                           float (&u)[32], int r0, int c0, bool bias_wide) {
   const Epilogue& ep = p.ep;
   const int R = p.prod[0].R, C = p.prod[0].C;
-  float g[32], u[32];
-  tmem_ld32(tb, g);
-  tmem_ld32(tb + HALF, u);
-  tmem_ld_wait_regs(g);
-  tmem_ld_wait_regs(u);
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) {
-    mbar_arrive_cluster(free_bar);
-    bulk_wait_group_read0();
-  }
+  if (lane == 0) bulk_wait_group_read0();
   __syncwarp();
   if (ep.bias) {  // the same for every lane
 #pragma unroll
@@ -356,35 +348,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint32_t idesc =
             make_idesc(p.type, p.type, TILE, TILE) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const OperandWalk wa(a_mn), wb(b_mn);
-        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.hdr, 0x620000u)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + acc * TILE;
-        bool ready = mbar_try_wait(full0 + 8 * stage, phase);
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x630000u)) {
+        const int seg = GATED ? p.seg : nk;
+        for (int k0 = 0; ok && k0 < nk; k0 += seg) {
+          if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, abort_flag, p.hdr, 0x620000u)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = ring + stage * STAGE_BYTES, empty = empty0 + 8 * stage;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
-          ready = kb + 1 < nk && mbar_try_wait(full0 + 8 * stage, phase);
-          if (leader) {
+          const uint32_t d = tmem + acc * TILE;
+          const int k1 = min(k0 + seg, nk);
+          bool ready = mbar_try_wait(full0 + 8 * stage, phase);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!ready && !mbar_wait(full0 + 8 * stage, phase, abort_flag, p.hdr, 0x630000u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = ring + stage * STAGE_BYTES, empty = empty0 + 8 * stage;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+            ready = kb + 1 < k1 && mbar_try_wait(full0 + 8 * stage, phase);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_pair(d, wa.at(a, kk), wb.at(a + OP_BYTES, kk), idesc, (kb | kk) != 0);
-            mma_commit_pair(empty);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_pair(d, wa.at(a, kk), wb.at(a + OP_BYTES, kk), idesc, ((kb - k0) | kk) != 0);
+              mma_commit_pair(empty);
+            }
+            __syncwarp();
           }
+          if (!ok) break;
+          if (leader) mma_commit_pair(tfull0 + 8 * acc);
           __syncwarp();
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
         }
         if (!ok) break;
-        if (leader) mma_commit_pair(tfull0 + 8 * acc);
-        __syncwarp();
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
       }
       if (leader) {
         mma_commit_pair(mma_done);
@@ -451,9 +451,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * (TILE_COLS / 4);
       if constexpr (GATED) {
-        gated_tile(p, my, &tmZ, &m1.y, box, q, h, lane, tb, lead_tempty0 + 8 * acc, r0, c0, bias_wide);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
+        float g[32], u[32];
+        tmem_ld32(tb, g);
+        tmem_ld32(tb + HALF, u);
+        tmem_ld_wait_regs(g);
+        tmem_ld_wait_regs(u);
+        auto release = [&]() {  // this warp's accumulator columns are read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        };
+        release();
+        for (int k0 = p.seg; k0 < p.prod[0].nk; k0 += p.seg) {  // the sum's other parts
+          if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x640000u);
+          good = __shfl_sync(0xffffffffu, good, 0);
+          if (!good) break;
+          tc_fence_after();
+          const uint32_t part = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * (TILE_COLS / 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v[16];
+            tmem_ld16(part + (j >> 1) * HALF + (j & 1) * 16, v);
+            tmem_ld_wait_regs16(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) (j < 2 ? g : u)[(j & 1) * 16 + e] += v[e];
+          }
+          release();
+        }
+        if (!good) break;
+        gated_tile(p, my, &tmZ, &m1.y, box, q, h, lane, g, u, r0, c0, bias_wide);
         continue;
       }
       const bool row_in = r0 + lane < R;
@@ -587,7 +615,9 @@ bool encode_product(PairMaps* m, PairProduct* pp, const Product& q) {
 float pair_estimate(const Product& q) {
   const long long tiles = static_cast<long long>((q.R + TILE - 1) / TILE) * ((q.C + tile_cols(q) - 1) / tile_cols(q));
   if (q.gated) {  // its tile has half the columns; fitted as linear.cu's gated_estimate
-    float us = 0.29f * ((q.K + BK - 1) / BK) + 0.9f;
+    const int nk = (q.K + BK - 1) / BK;
+    float us = 0.29f * nk + 0.9f;
+    if (q.ep.out_dtype == MOE_DTYPE_F32) us += 0.05f * nk;
     if (q.ep.z) us += storable(q.ep.z, q.ep.z_dtype, q.C, q.ep.ld_z) ? 1.3f : 4.0f;
     if (!storable(q.ep.y, q.ep.out_dtype, q.C, q.ep.ld_y)) us += 0.6f;
     return 6.0f + (tiles + 75) / 76 * us;
@@ -659,6 +689,9 @@ cudaError_t launch_pair(const Product& first, const Product* second, cudaStream_
                                                    static_cast<int>(SMEM_BYTES));
   }();
   if (attr != cudaSuccess) return attr;
+  // fp32 output: the tensor core's running sum is cut off at every step of it (relative error 1.8e-9 per
+  // value summed), so a gated tile's sum is cut into parts of 256, added in registers
+  p.seg = q0->gated && q0->ep.out_dtype == MOE_DTYPE_F32 ? 4 : p.prod[0].nk;
   p.type = q0->type;
   p.ep = q0->ep;
   p.reset_status = first.reset_status;

@@ -201,3 +201,20 @@ def test_gated_repeats_bit_for_bit_on_streams_and_in_a_graph(m):  # noqa: F811
             outs.append(r)
         for r in outs[1:]:
             assert all(torch.equal(a, b) for a, b in zip(outs[0], r))
+
+
+@pytest.mark.parametrize("M", [8, 100, 1024])
+def test_gated_fp32_output_of_long_sums(m, M):  # noqa: F811
+    """No accumulator sums more than 512 values, 16 at a step, each step cut off at 2^-23 of the sum at
+    most (linear_few.cu and the joins of partial sums round to nearest, 2^-24): h = g u, so twice that."""
+    N, K = 1024, 4096
+    g = gen(M)
+    x, w = rows(M, K, K, torch.bfloat16, g), rows(2 * N, K, K, torch.bfloat16, g, K ** -0.5)
+    h = torch.empty(M, N, device=DEV)
+    p = m.gated_problem(M, N, K, out_dtype=m.MOE_DTYPE_F32, act=m.MOE_ACT_NONE)
+    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    m.moe_gated(p, x, w, None, h, None, ws)
+    z = x.double() @ w.double().T
+    ref = z[:, :N] * z[:, N:]
+    steps = 512 / 16 + K / 512 + 4
+    assert float((h.double() - ref).norm() / ref.norm()) <= 2 * steps * 2.0 ** -24  # half a step each on average
