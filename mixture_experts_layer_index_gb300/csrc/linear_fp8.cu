@@ -56,7 +56,7 @@ struct Shape {
   static constexpr int STAGES = CG == 2 ? 5 : BN >= 256 ? 4 : BN >= 128 ? 6 : 8;
   static constexpr int COLS = BN / QW;              // accumulators of an epilogue thread
   static constexpr int PITCH = BN + 4;              // fp32 values of a row on its way between threads
-  // pairs: a store box per epilogue warp, or for e4m3 output the row maxima [16][32]
+  // pairs: a store box per epilogue warp, or for e4m3 output the row maxima [2][16][32]
   static constexpr int BOX_OFFSET = STAGES * STAGE;
   static constexpr size_t SMEM = 1024 + BOX_OFFSET + (CG == 2 ? EPI_WARPS * BOX_BYTES : 0);
   static_assert(SMEM <= 227 * 1024 - 512, "shared memory of one block");
@@ -79,6 +79,7 @@ struct Fp8Params {
   void* y;
   float* h_scale;  // e4m3 output: [M][ceil(N / 128)]
   int y_tma;       // pairs: whether TMA stores the output
+  int h_wide;      // pairs: whether rows of codes take stores of 32 bytes
   int sx_vec;      // rows of x_scale start at 16-byte boundaries
   DeviceHeader* hdr;
 };
@@ -116,6 +117,12 @@ __device__ __forceinline__ uint32_t codes4(const float* h, const GroupScale& g) 
          static_cast<uint32_t>(cvt_e4m3x2(g.scaled(h[2]), g.scaled(h[3]))) << 16;
 }
 __device__ __forceinline__ float vmax(float m, float v) { return fmaxf(m, fabsf(v)); }  // without a NaN's part
+
+__device__ __forceinline__ void st_global_32(void* to, const uint32_t* a, const uint32_t* b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a[0]), "r"(a[1]), "r"(a[2]),
+               "r"(a[3]), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+               : "memory");
+}
 
 // Four values of a row from column c to an array of out_dtype; `n` of them exist.
 template <typename T>
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int OUT_COLS = GATED ? BN / 2 : BN;  // output columns of a tile
   constexpr int TILE_ROWS = CG * BM;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars[2 * MAX_STAGES + 2 * MAX_BUFS + 9];
+  __shared__ uint64_t bars[2 * MAX_STAGES + 2 * MAX_BUFS + 1];
   __shared__ uint32_t tmem_slot[1];
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_rank();
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * MAX_STAGES;
   const uint32_t pfull0 = empty0 + 8 * MAX_STAGES, pempty0 = pfull0 + 8 * MAX_BUFS;
-  const uint32_t done = pempty0 + 8 * MAX_BUFS, xbar0 = done + 8;  // xbar: quadrant q's row maxima are written / read
+  const uint32_t done = pempty0 + 8 * MAX_BUFS;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -241,7 +248,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(pempty0 + 8 * b, CG * EPI_WARPS);
     }
     mbar_init(done, 1);
-    for (int b = 0; b < 8; ++b) mbar_init(xbar0 + 8 * b, QW);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&tmA);
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint8_t* box = smem + S::BOX_OFFSET + e * BOX_BYTES;
     float* rowmax = reinterpret_cast<float*>(smem + S::BOX_OFFSET);
     const uint32_t free0 = CG == 2 ? map_rank(pempty0, 0) : pempty0;
-    uint32_t pb = 0, pphase = 0, xphase = 0;
+    uint32_t pb = 0, pphase = 0, turn = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += step) {
       int tr, tc;
@@ -466,7 +472,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (GATED) su_kb = __ldg(su + kb + 1);
         }
       }
-      if (!ok) break;
+      if (!ok) {
+        if (CG == 2 && GATED && p.h_scale) quad_all(q, false);  // the quadrant's other warps go no further either
+        break;
+      }
       if constexpr (CG == 2) {
         if constexpr (GATED) {
           constexpr int H = COLS / 2;  // columns of h
@@ -493,40 +502,32 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int i = 0; i < H; ++i)
                 if (c0 + i < p.N) m = vmax(m, acc[i]);
             }
-            rowmax[e * 32 + lane] = m;
-            __syncwarp();
-            int good = 1;
-            if (lane == 0) {
-              mbar_arrive(xbar0 + 8 * q);
-              good = mbar_wait(xbar0 + 8 * q, xphase, abort_flag, p.hdr, 0x750000u);
-            }
-            if (!__shfl_sync(0xffffffffu, good, 0)) {
+            // two sets of maxima in turn: one barrier per tile
+            float* maxima = rowmax + turn * (EPI_WARPS * 32);
+            turn ^= 1;
+            maxima[e * 32 + lane] = m;
+            if (!quad_all(q, true)) {
               ok = false;
               break;
             }
 #pragma unroll
-            for (int w = 0; w < QW; ++w) m = fmaxf(m, rowmax[(q + 4 * w) * 32 + lane]);
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(xbar0 + 8 * (4 + q));
-              good = mbar_wait(xbar0 + 8 * (4 + q), xphase, abort_flag, p.hdr, 0x760000u);
-            }
-            if (!__shfl_sync(0xffffffffu, good, 0)) {
-              ok = false;
-              break;
-            }
-            xphase ^= 1;
+            for (int w = 0; w < QW; ++w) m = fmaxf(m, maxima[(q + 4 * w) * 32 + lane]);
             const GroupScale g(m);
             if (r0 + lane < p.M) {
               const size_t row = static_cast<size_t>(r0 + lane);
               uint8_t* to = static_cast<uint8_t*>(p.y) + row * p.ld_y + c0;
+              uint32_t half[4];
 #pragma unroll
               for (int j = 0; j < H / 16; ++j) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = codes4(&acc[16 * j + 4 * i], g);
                 const int n = p.N - c0 - 16 * j;
-                if (n >= 16) {
+                if (p.h_wide && c0 + H <= p.N) {  // a whole sector at once
+                  if (j & 1) st_global_32(to + 16 * (j - 1), half, w);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) half[i] = w[i];
+                } else if (n >= 16) {
                   reinterpret_cast<uint4*>(to)[j] = make_uint4(w[0], w[1], w[2], w[3]);
                 } else {
 #pragma unroll
@@ -700,6 +701,7 @@ cudaError_t launch_shape(const Fp8Args& a, int splits, cudaStream_t s) {
                                 static_cast<int>(Sh::SMEM));
   }();
   if (attr != cudaSuccess) return attr;
+  p.h_wide = a.h_scale && reinterpret_cast<uintptr_t>(a.y) % 32 == 0 && a.ld_y % 32 == 0;
   p.sx_vec = p.nk % 4 == 0 && reinterpret_cast<uintptr_t>(a.x_scale) % 16 == 0 && p.nk % (4 * splits) == 0;
   const long long tiles = static_cast<long long>(p.nR) * p.nC;
   const int sms = num_sms();

@@ -24,10 +24,21 @@ constexpr int WARPS = 8;  // per tile of 16 weight rows
 
 // Codes k .. k + 15 of a row; zeros past K, where nothing is read.
 __device__ __forceinline__ uint4 load16(const uint8_t* row, int k, int K) {
-  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
-  uint32_t w[4] = {};
-#pragma unroll 1
-  for (int i = 0; i < 16 && k + i < K; ++i) w[i >> 2] |= static_cast<uint32_t>(row[k + i]) << (8 * (i & 3));
+  const int rest = K - k;
+  if (rest >= 16) return __ldg(reinterpret_cast<const uint4*>(row + k));
+  if (rest <= 0) return make_uint4(0, 0, 0, 0);
+  // whole words, then the bytes of the last one: all loads at once
+  const int words = rest >> 2;
+  uint32_t w[4], last = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) w[i] = i < words ? __ldg(reinterpret_cast<const uint32_t*>(row + k) + i) : 0u;
+  w[3] = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (4 * words + i < rest) last |= static_cast<uint32_t>(__ldg(row + k + 4 * words + i)) << (8 * i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i == words) w[i] = last;
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void mma_m16n8k32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,

@@ -108,9 +108,8 @@ __device__ __forceinline__ void tile_origin(const PairProduct& p, int t, int& r0
 // 32 columns of 32 rows of a warp, and those of the three warps beside it, to an array of 16-bit
 // values whose rows TMA cannot store: the four warps put 128 columns together in shared memory (rows of
 // 65 words), then each stores eight rows of them, a word at a time wherever the row begins.  All four
-// come here together.  `quad`: their boxes; q: which four; h: which of them.
+// come here together (quad_all).  `quad`: their boxes; q: which four; h: which of them.
 constexpr int QUAD_PITCH = 65;
-__device__ __forceinline__ void quad_barrier(int q) { asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory"); }
 // Not inlined: its registers would be spilled from the path that TMA stores.
 __device__ __noinline__ void store_quad(const uint32_t* quad, int h, int lane, uint16_t* out, long long ld, int rows, int n) {
 #pragma unroll 4
@@ -426,6 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint8_t* box = smem + BOX_OFFSET + (GATED ? 4 * q + h : e) * BOX_BYTES;  // GATED: a quadrant's four side by side
     const uint32_t lead_tempty0 = map_rank(tempty0, 0);
     const Epilogue& ep = p.ep;
+    const bool together = GATED && ((!p.y_tma && ep.out_dtype != MOE_DTYPE_F32) || (ep.z && !p.z_tma));  // flush_columns
     const bool wide = ep.out_dtype == MOE_DTYPE_F32;
     const bool plain = p.y_tma && !wide && !ep.bias && !ep.residual && !ep.z && ep.act == MOE_ACT_NONE && ep.alpha == 1.0f;
     const bool bias_wide = reinterpret_cast<uintptr_t>(ep.bias) % 16 == 0 && (!GATED || p.prod[0].half % 8 == 0);
@@ -447,7 +447,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int good = 1;
       if (lane == 0) good = mbar_wait(tfull0 + 8 * acc, acc_phase, abort_flag, p.hdr, 0x640000u);
       good = __shfl_sync(0xffffffffu, good, 0);
-      if (!good) break;
+      if (!GATED && !good) break;
+      if (GATED && !good) {
+        if (together) quad_all(q, false);
+        break;
+      }
       tc_fence_after();
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE + h * (TILE_COLS / 4);
       if constexpr (GATED) {
@@ -459,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         auto release = [&]() {  // this warp's accumulator columns are read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(lead_tempty0 + 8 * acc);
+          if (lane == 0) mbar_arrive_cluster_relaxed(lead_tempty0 + 8 * acc);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1;
         };
@@ -480,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           release();
         }
-        if (!good) break;
+        if (together ? !quad_all(q, good != 0) : !good) break;
         gated_tile(p, my, &tmZ, &m1.y, box, q, h, lane, g, u, r0, c0, bias_wide);
         continue;
       }

@@ -9,6 +9,23 @@ namespace lin {
 
 constexpr int BOX_BYTES = 32 * 128;  // 32 rows of 128 bytes
 
+// Barriers of the four epilogue warps that share 32 lanes (quadrant q).  They have no time limit, so all
+// four come to one or none: quad_all, met once per tile by each of them whatever its waits said, gives
+// all the same answer.
+__device__ __forceinline__ void quad_barrier(int q) { asm volatile("bar.sync %0, 128;" ::"r"(2 + q) : "memory"); }
+__device__ __forceinline__ bool quad_all(int q, bool good) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, r;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred r, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(good)), "r"(2 + q)
+      : "memory");
+  return all != 0;
+}
+
 // ------------------------------------------------------------------ two-SM forms
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
