@@ -424,6 +424,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       };
       load_sx(kb0);
+      if constexpr (CG == 2 && !GATED) {
+        // the residual's part of this thread's row comes into L2 while the product is computed
+        if (p.residual && r0 + lane < p.M && c0 < p.N) {
+          const int es = p.out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+          const uint8_t* row = static_cast<const uint8_t*>(p.residual) + (static_cast<size_t>(r0 + lane) * p.ld_y + c0) * es;
+          const int bytes = min(COLS, p.N - c0) * es;
+          for (int b = 0; b < bytes; b += 128) prefetch_l2(row + b);
+          prefetch_l2(row + bytes - 1);
+        }
+      }
       float sw_kb = __ldg(sw + kb0), su_kb = GATED ? __ldg(su + kb0) : 0.0f;
       bool ready = false;
       for (int kb = kb0; kb < kb1; ++kb) {
@@ -729,7 +739,7 @@ cudaError_t launch_shape(const Fp8Args& a, int splits, cudaStream_t s) {
 float pair_estimate(const Fp8Args& a) {
   const long long cols = a.gated ? 128 : 256;
   const long long tiles = (a.M + 255ll) / 256 * ((a.N + cols - 1) / cols);
-  return 2.7f + (tiles + 75) / 76 * (0.52f * ((a.K + 127) / 128) + (a.h_scale ? 4.0f : 2.5f));
+  return 2.7f + (tiles + 75) / 76 * (0.52f * ((a.K + 127) / 128) + (a.h_scale ? 2.8f : 2.5f));
 }
 float single_estimate(const Fp8Args& a, int bn, int splits) {
   const long long cols = a.gated ? bn / 2 : bn;

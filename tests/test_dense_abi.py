@@ -122,3 +122,57 @@ def test_fp8_refusals(m):
     assert lin(L(0, 24, 64, e), x=None, w=None, y=None, ws=None, nb=0) == m.MOE_OK
     # the 16-bit entry points take no codes
     assert m.moe_linear_workspace_size(ok) == 0 and m.moe_gated_workspace_size(okg) == 0
+
+
+class Device:
+    """A CPU tensor that says it is on the GPU: its layout is looked at, its memory is not."""
+
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_rows_that_the_descriptor_does_not_name(m, monkeypatch):
+    torch = pytest.importorskip("torch")
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append(name) or m.MOE_OK
+
+    monkeypatch.setattr(m, "lib", lambda: Lib())
+
+    def dev(rows, cols, ld=None, dtype=torch.float32):
+        return Device(torch.zeros(rows, ld or cols, dtype=dtype)[:, :cols])
+
+    M, N, K, ld = 4, 24, 64, 80
+    x, w, h, z = dev(M, K), dev(2 * N, K), dev(M, N), dev(M, 2 * N)
+    p = m.gated_problem(M, N, K)
+    m.moe_gated(p, x, w, None, h, z, FAKE, 256, stream=0)
+    m.moe_gated_backward(p, h, x, w, z, x, w, None, FAKE, 256, stream=0)
+    wide = {"x": dev(M, K, ld), "w": dev(2 * N, K, ld), "h": dev(M, N, ld)}
+    for name in wide:
+        a = {"x": x, "w": w, "h": h} | {name: wide[name]}
+        with pytest.raises(ValueError, match="elements apart"):
+            m.moe_gated(p, a["x"], a["w"], None, a["h"], None, FAKE, 256, stream=0)
+        with pytest.raises(ValueError, match="elements apart"):
+            m.moe_gated_backward(p, a["h"], a["x"], a["w"], z, None, None, None, FAKE, 256, stream=0)
+        with pytest.raises(ValueError, match="elements apart"):
+            m.moe_gated_fp8(p, a["x"], FAKE, a["w"], FAKE, None, a["h"], None, FAKE, 256, stream=0)
+    q = m.gated_problem(M, N, K, ld_x=ld, ld_w=ld, ld_h=ld)
+    m.moe_gated(q, wide["x"], wide["w"], None, wide["h"], None, FAKE, 256, stream=0)
+    l, y, wl = m.linear_problem(M, N, K, m.MOE_DTYPE_E4M3), dev(M, N), dev(N, K)
+    m.moe_linear_fp8(l, x, FAKE, wl, FAKE, None, y, y, FAKE, 256, stream=0)
+    for a in ((wide["x"], wl, y, y), (x, dev(N, K, ld), y, y), (x, wl, wide["h"], y), (x, wl, y, wide["h"])):
+        with pytest.raises(ValueError, match="elements apart"):
+            m.moe_linear_fp8(l, a[0], FAKE, a[1], FAKE, None, a[2], a[3], FAKE, 256, stream=0)
+    k = m.quantise_problem(M, K, ld_q=ld)
+    m.moe_quantise(k, x, dev(M, K, ld, torch.uint8), FAKE, stream=0)
+    for a in ((wide["x"], dev(M, K, ld, torch.uint8)), (x, dev(M, K, dtype=torch.uint8))):
+        with pytest.raises(ValueError, match="elements apart"):
+            m.moe_quantise(k, *a, FAKE, stream=0)
+    assert len(seen) == 5

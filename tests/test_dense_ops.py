@@ -39,9 +39,10 @@ def gated_case(m, M, N, K, act="silu", dtype="bf16", out="bf16", bias=None, keep
     b = None if bias is None else torch.randn(2 * N, generator=g, device=DEV).to(DT[bias])
     p = m.gated_problem(M, N, K, code(m, dtype), code(m, out), code(m, bias or "f32"), acts(m, act), ld_x, ld_w, ld_h)
     if forward:
-        buf = torch.full((M, ld_h or N), float("nan"), dtype=ht, device=DEV)
-        h = buf[:, :N]
-        z = torch.full((M, 2 * N), float("nan"), dtype=t, device=DEV) if keep_z else None
+        buf = torch.full((M + 2, ld_h or N), float("nan"), dtype=ht, device=DEV)
+        h = buf[:M, :N]
+        zbuf = torch.full((M + 2, 2 * N), float("nan"), dtype=t, device=DEV)
+        z = zbuf[:M] if keep_z else None
         ws = torch.full((m.moe_gated_workspace_size(p),), 255, dtype=torch.uint8, device=DEV)
         m.moe_gated(p, x, w, b, h, z, ws)
         assert m.moe_read_device_status(ws) == m.MOE_OK
@@ -50,7 +51,8 @@ def gated_case(m, M, N, K, act="silu", dtype="bf16", out="bf16", bias=None, keep
         if keep_z:
             check(z, rz, mag, steps, "z")
         check(h, ref, gated_mag(rz, mag, act, steps), steps, "h")
-        assert torch.isnan(buf[:, N:]).all()  # what lies between the rows
+        assert torch.isnan(buf[:, N:]).all() and torch.isnan(buf[M:]).all()  # what lies between the rows and behind them
+        assert torch.isnan(zbuf[M:]).all()
     if not gradient:
         return
     dh = strided(M, N, ld_h, ht, g)

@@ -28,15 +28,16 @@ def quantise_case(m, x, block_rows, ld_q=0, offset=0):  # noqa: F811
     M, K = x.shape
     name = {v: k for k, v in DT.items()}[x.dtype]
     ld = ld_q or K
-    buf = torch.full((M * ld + offset,), 0x55, dtype=torch.uint8, device=DEV)
-    q = buf[offset:].view(M, ld)[:, :K]
+    buf = torch.full((M * ld + offset + 64,), 0x55, dtype=torch.uint8, device=DEV)
+    body = buf[offset:offset + M * ld].view(M, ld)
+    q = body[:, :K]
     s = torch.full((-(-M // block_rows), -(-K // 128)), float("nan"), device=DEV)
     p = m.quantise_problem(M, K, code(m, name), block_rows, x.stride(0) if M > 1 else 0, ld_q)
     m.moe_quantise(p, x, q, s)
     codes, scales = D.quantise(x.float().cpu().numpy(), block_rows)
     assert np.array_equal(s.cpu().numpy(), scales)
     assert same_codes(q.cpu().numpy(), codes)
-    assert (buf[:offset] == 0x55).all() and (buf[offset:].view(M, ld)[:, K:] == 0x55).all()  # between the rows
+    assert (buf[:offset] == 0x55).all() and (buf[-64:] == 0x55).all() and (body[:, K:] == 0x55).all()  # between the rows
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
@@ -108,8 +109,8 @@ def linear_case(m, M, N, K, act="none", out="bf16", bias=None, residual=False, a
     b = None if bias is None else torch.randn(N, generator=g, device=DEV).to(DT[bias])
     r = rows(M, N, ld_y or N, DT[out], g) if residual else None
     rv = f64(r)
-    buf = torch.full((M, ld_y or N), float("nan"), dtype=DT[out], device=DEV)
-    y = r if in_place else buf[:, :N]
+    buf = torch.full((M + 2, ld_y or N), float("nan"), dtype=DT[out], device=DEV)
+    y = r if in_place else buf[:M, :N]
     p = m.linear_problem(M, N, K, m.MOE_DTYPE_E4M3, code(m, out), code(m, bias or "f32"), acts(m, act), alpha, ld_x, ld_w, ld_y)
     ws = torch.full((m.moe_linear_fp8_workspace_size(p),), 255, dtype=torch.uint8, device=DEV)
     m.moe_linear_fp8(p, x, sx, w, sw, b, r, y, ws)
@@ -121,7 +122,7 @@ def linear_case(m, M, N, K, act="none", out="bf16", bias=None, residual=False, a
     steps = K / 8 + 16  # the accumulator may round once per eight products
     check(y, ref, 1.13 * abs(alpha) * (mag + 8 * (1 + np.abs(z)) / steps) + np.abs(ref) * 4 / steps, steps, "y")
     if not in_place:
-        assert torch.isnan(buf[:, N:]).all()
+        assert torch.isnan(buf[:, N:]).all() and torch.isnan(buf[M:]).all()
 
 
 def gated_case(m, M, N, K, act="silu", out="e4m3", bias=None, ld_x=0, ld_w=0, ld_h=0):  # noqa: F811
@@ -142,17 +143,18 @@ def gated_case(m, M, N, K, act="silu", out="e4m3", bias=None, ld_x=0, ld_w=0, ld
                         acts(m, act), ld_x, ld_w, ld)
     ws = torch.full((m.moe_gated_fp8_workspace_size(p),), 255, dtype=torch.uint8, device=DEV)
     if not coded:
-        buf = torch.full((M, ld), float("nan"), dtype=DT[out], device=DEV)
-        m.moe_gated_fp8(p, x, sx, w[:, :K], sw, b, buf[:, :N], None, ws)
+        buf = torch.full((M + 2, ld), float("nan"), dtype=DT[out], device=DEV)
+        m.moe_gated_fp8(p, x, sx, w[:, :K], sw, b, buf[:M, :N], None, ws)
         assert m.moe_read_device_status(ws) == m.MOE_OK
-        check(buf[:, :N], ref, hm, steps, "h")
-        assert torch.isnan(buf[:, N:]).all()
+        check(buf[:M, :N], ref, hm, steps, "h")
+        assert torch.isnan(buf[:, N:]).all() and torch.isnan(buf[M:]).all()
         return
-    buf = torch.full((M, ld), 0x55, dtype=torch.uint8, device=DEV)
-    s = torch.full((M, -(-N // 128)), float("nan"), device=DEV)
-    m.moe_gated_fp8(p, x, sx, w[:, :K], sw, b, buf[:, :N], s, ws)
+    buf = torch.full((M + 2, ld), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.full((M + 2, -(-N // 128)), float("nan"), device=DEV)
+    m.moe_gated_fp8(p, x, sx, w[:, :K], sw, b, buf[:M, :N], s, ws)
     assert m.moe_read_device_status(ws) == m.MOE_OK
-    assert (buf[:, N:] == 0x55).all()
+    assert (buf[:, N:] == 0x55).all() and (buf[M:] == 0x55).all() and torch.isnan(s[M:]).all()
+    buf, s = buf[:M], s[:M]
     off = (steps * STEP) * hm
     pad = [(0, 0), (0, -N % 128)]
     amax = np.pad(np.abs(ref), pad).reshape(M, -1, 128).max(2)
