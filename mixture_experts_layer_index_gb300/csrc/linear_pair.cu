@@ -624,7 +624,9 @@ float pair_estimate(const Product& q) {
     if (q.ep.out_dtype == MOE_DTYPE_F32) us += 0.05f * nk;
     if (q.ep.z) us += storable(q.ep.z, q.ep.z_dtype, q.C, q.ep.ld_z) ? 1.3f : 4.0f;
     if (!storable(q.ep.y, q.ep.out_dtype, q.C, q.ep.ld_y)) us += 0.6f;
-    return 6.0f + (tiles + 75) / 76 * us;
+    us *= (tiles + 75) / 76;
+    const float memory = 2.0f * (static_cast<float>(q.R) + 2.0f * q.C) * q.K / 5.0e6f;  // 5 TB/s
+    return 6.0f + (us > memory ? us : memory);
   }
   const float stages = 0.30f * ((q.K + BK - 1) / BK);
   float epilogue = 3.5f;
