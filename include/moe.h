@@ -37,6 +37,8 @@
  *     moe_gated / moe_gated_backward / moe_quantise / moe_linear_fp8 /
  *     moe_gated_fp8: work is enqueued on `stream` in order, with no device-to-host copy, so these calls can be
  *     captured in a CUDA graph.  Inputs are never written.
+ *   - A workspace serves one call at a time: calls whose work may overlap (on two
+ *     streams, or in graphs that run side by side) need workspaces of their own.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).
  *   - A process uses the library on one device, the one current at its first call.
  *   - Arguments are validated on the host BEFORE anything is enqueued; on a

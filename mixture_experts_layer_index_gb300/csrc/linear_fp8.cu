@@ -587,11 +587,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr int GROUPS = EPI_WARPS * 32 / LANES;
       const int in_row = (static_cast<int>(threadIdx.x) - 128) % LANES;
       const uint32_t sums = smem_u32(smem);
-      if (*abort_flag == 0) {
+      if (__all_sync(0xffffffffu, *abort_flag == 0)) {
         // whole warps leave the loop together where a row's maximum is shared
         for (int r = begin + (static_cast<int>(threadIdx.x) - 128) / LANES; r < end; r += GROUPS) {
           const int row = tr * BM + r;
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < PASSES; ++i) {
             const int cc = (in_row + i * LANES) * 4, c = tc * OUT_COLS + cc, n = p.N - c;
             const uint32_t at = sums + (r * S::PITCH + cc) * 4;
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const size_t to = static_cast<size_t>(row) * p.ld_y + c;
             if constexpr (GATED) {
               float m = 0.0f;
-  #pragma unroll
+#pragma unroll
               for (int k = 0; k < 4; ++k) {
                 v[k] *= u[k];
                 if (k < n) m = vmax(m, v[k]);
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (n >= 4) {
                   *reinterpret_cast<uint32_t*>(h) = w;
                 } else {
-  #pragma unroll
+#pragma unroll
                   for (int k = 0; k < 4; ++k)
                     if (k < n) h[k] = static_cast<uint8_t>(w >> (8 * k));
                 }
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 continue;
               }
             } else {
-  #pragma unroll
+#pragma unroll
               for (int k = 0; k < 4; ++k) v[k] *= p.alpha;
               if (p.residual) add4(v, p.residual, p.out_dtype, to, n);
             }
