@@ -215,10 +215,17 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-// Measured in graphs, weights from memory (us, here / in linear_fp8.cu), for M x N x K: 8 x 4096 x 4096 5.3 / 8.9,
-// 16 x 4096 x 4096 7.4 / 9.1, 8 x 2048 x 768 2.0 / 5.6; gated to bf16 8.4 / 12.8, 2.4 / 6.1 (8 x 2048 x 768), to e4m3
-// 10.6 / 11.7, 3.8 / 7.0; gated for 16 rows (in a trial) 14.6 / 13.4 and 24.6 / 12.2.
-bool takes_few(const Fp8Args& a) { return a.M <= (a.gated ? 8 : 16); }
+// Measured in graphs, weights from memory (us, here / in linear_fp8.cu), for M x N x K:
+//   8 x 2048 x 768  2.0 / 5.6;  8 x 4096 x 4096  5.4 / 8.9;  8 x 8192 x 8192  19.3 / 21.4
+//   16 x 4096 x 4096  6.9 / 9.0;  16 x 8192 x 4096  13.4 / 13.0;  16 x 8192 x 8192  23.1 / 16.5;  16 x 1024 x 8192  8.8 / 7.7
+//   gated to bf16, 8 rows   2048 x 768  2.4 / 6.1;  4096 x 4096  8.5 / 12.9;  14336 x 4096  26.0 / 32.1
+//   gated to e4m3, 8 rows   2048 x 768  3.8 / 7.0;  4096 x 4096  10.5 / 11.7;  8192 x 4096  20.6 / 17.2
+//   gated, 16 rows (in a trial)  4096 x 4096 to bf16  14.6 / 13.4
+bool takes_few(const Fp8Args& a) {
+  const long long weights = static_cast<long long>(a.N) * a.K;  // of the gate's half
+  if (a.gated) return a.M <= 8 && (!a.h_scale || weights <= 1 << 24);
+  return a.M <= 8 || (a.M <= 16 && weights <= 1 << 24 && a.K <= 4096);
+}
 
 cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {
   if (a.gated) return launch<1, true>(a, s);

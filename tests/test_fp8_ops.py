@@ -222,7 +222,10 @@ def test_long_sums_and_strides(m):  # noqa: F811
     linear_case(m, 8, 4096, 4096, out="f32", residual=True)
     linear_case(m, 33, 128, 8192, out="f32")
     linear_case(m, 50, 77, 100, ld_x=128, ld_w=144, ld_y=81, bias="f32")
+    linear_case(m, 16, 144, 8192)
+    linear_case(m, 12, 4160, 4096, out="f32")
     gated_case(m, 8, 1024, 4096)
+    gated_case(m, 8, 4224, 4096)
     gated_case(m, 40, 96, 7168)
     gated_case(m, 50, 77, 100, ld_x=128, ld_w=144, ld_h=96)
 
