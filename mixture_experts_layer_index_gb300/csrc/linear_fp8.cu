@@ -19,12 +19,14 @@
 //
 // Bound by the promoting warps' loop, some 1200 clocks per stage of a 256 x 256 tile whose MMAs take
 // 512: wait, four trips to tensor memory with as many rounds of additions, and the release.  Measured
-// (16384 x 2048 x 4096; 131 us, 2.1 PFLOP/s): without the additions 91 us, without the scales'
-// loads 112.  So the loop is kept short: a release that waits for no other access of the thread
-// (with a release at cluster scope 269 us), the next partial's barrier looked at before the last
-// additions, the next scales loaded behind the release, and no spilled registers, which are
-// moved here from the other warps.  Slower in trials: eight warps with 128 accumulators and two
-// buffers (139), partials of 128 columns (170), the scales through shared memory (140 to 144).
+// (16384 x 2048 x 4096; 129 us, 2.1 PFLOP/s; gated, 16384 x 4096 x 2048, to bf16 249 us, 2.2 PFLOP/s, to
+// e4m3 274): in trials at 131 us, without the additions 91 us, without the scales' loads 112.  So the
+// loop is kept short: 16 columns on their way while 16 are added, a release that waits for no other
+// access of the thread (with a release at cluster scope 269 us), the next partial's barrier looked at
+// before the last additions, the next scales loaded behind the release, and no spilled registers, which
+// are moved here from the other warps.  Slower in trials: eight warps with 128 accumulators and two
+// buffers (139), 32 columns at a time (141), partials of 128 columns (170), the scales through shared
+// memory (140 to 144), additions that are not packed in pairs (138).
 #include "linear_fp8.cuh"
 #include "linear_pair.cuh"
 
@@ -448,15 +450,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + pb * BN;
+        auto column = [&](int j) {
+          return tb + (!GATED ? h * COLS + j * 16
+                       : j < COLS / 32 ? h * (COLS / 2) + j * 16
+                                       : BN / 2 + h * (COLS / 2) + (j - COLS / 32) * 16);
+        };
+        float v[2][16];  // 16 columns on their way while 16 are added
+        tmem_ld16(column(0), v[0]);
+        tmem_ld_wait_regs16(v[0]);
 #pragma unroll
         for (int j = 0; j < COLS / 16; ++j) {
-          const bool up = GATED && j >= COLS / 32;
-          float v[16];
-          tmem_ld16(tb + (GATED ? (up ? BN / 2 + h * (COLS / 2) + (j - COLS / 32) * 16 : h * (COLS / 2) + j * 16)
-                                : h * COLS + j * 16),
-                    v);
-          tmem_ld_wait_regs16(v);
-          if (j == COLS / 16 - 1) {  // the last columns are in registers
+          if (j + 1 < COLS / 16) {
+            tmem_ld16(column(j + 1), v[(j + 1) & 1]);
+          } else {  // the last columns are in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -469,9 +475,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             ready = mbar_test_wait(pfull0 + 8 * pb, pphase);
           }
-          const float f = up ? f1 : f0;
+          const float f = GATED && j >= COLS / 32 ? f1 : f0;
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) fma2(acc[16 * j + i], acc[16 * j + i + 1], v[i], v[i + 1], f, f);
+          for (int i = 0; i < 16; i += 2) fma2(acc[16 * j + i], acc[16 * j + i + 1], v[j & 1][i], v[j & 1][i + 1], f, f);
+          if (j + 1 < COLS / 16) tmem_ld_wait_regs16(v[(j + 1) & 1]);
         }
         if (kb + 1 < kb1) {
           x4[0] = x4[1];
