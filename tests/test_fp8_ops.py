@@ -306,3 +306,45 @@ def test_repeats_bit_for_bit_on_streams_and_in_a_graph(m):  # noqa: F811
             outs.append((h, hs, y))
         for r in outs[1:]:
             assert all(torch.equal(a, b) for a, b in zip(outs[0], r))
+
+
+def test_two_streams_at_once(m):  # noqa: F811
+    """Layers of every form side by side on two streams, each with outputs and workspaces of its own, leave
+    what they leave one after the other."""
+    e, g = m.MOE_DTYPE_E4M3, gen(8)
+    calls = []
+    for M, N, K in ((3000, 512, 384), (50, 256, 1024), (8, 512, 1024), (12, 256, 512)):
+        x, sx, _, _ = operand(M, K, 0, 1, g)
+        w, sw, _, _ = operand(2 * N, K, 0, 128, g, K ** -0.5)
+        xb, wb = rows(M, K, K, torch.bfloat16, g), rows(2 * N, K, K, torch.bfloat16, g, K ** -0.5)
+        pl, pg, pb = m.linear_problem(M, 2 * N, K, e), m.gated_problem(M, N, K, e, e), m.gated_problem(M, N, K)
+
+        def call(out, stream, x=x, sx=sx, w=w, sw=sw, xb=xb, wb=wb, pl=pl, pg=pg, pb=pb):
+            m.moe_linear_fp8(pl, x, sx, w, sw, None, None, out[0], out[4], stream=stream)
+            m.moe_gated_fp8(pg, x, sx, w, sw.view(2, -1, sw.shape[1]), None, out[1], out[2], out[5], stream=stream)
+            m.moe_gated(pb, xb, wb, None, out[3], None, out[6], stream=stream)
+
+        def fresh(M=M, N=N):
+            return ([torch.zeros(M, 2 * N, dtype=torch.bfloat16, device=DEV), torch.zeros(M, N, dtype=torch.uint8, device=DEV),
+                     torch.zeros(M, N // 128, device=DEV), torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)] +
+                    [torch.empty(256, dtype=torch.uint8, device=DEV) for _ in range(3)])
+
+        calls.append((call, fresh))
+    want = []
+    for call, fresh in calls:
+        want.append(fresh())
+        call(want[-1], None)
+        torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [[fresh() for _, fresh in calls] for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k in range(len(calls)):
+            for s, stream in enumerate(streams):
+                i = (k + s) % len(calls)
+                calls[i][0](got[s][i], stream)
+    torch.cuda.synchronize()
+    for outs in got:
+        for a, b in zip(outs, want):
+            assert all(torch.equal(p, q) for p, q in zip(a[:4], b[:4]))
+            assert all(m.moe_read_device_status(ws) == m.MOE_OK for ws in a[4:])
