@@ -206,6 +206,13 @@ class DenseBlock:
             raise ValueError("H and N are multiples of 8 (bf16) or 16 (fp8_block)")
         self.ws_gated, self.ws_down = (_scratch(n, dev) for n in sizes)
         self._grad = None
+        if train:  # a workspace for each gradient, since the next one's call would clear its status
+            f32 = torch.float32
+            out = DenseGradient(empty(T, H), empty(T, H), empty(2 * N, H), empty(H, N), empty(H, dtype=f32),
+                                empty(H, dtype=f32), None if norms[2] is None else empty(H, dtype=f32))
+            sizes = (moe_linear_backward_workspace_size(self.down), moe_gated_backward_workspace_size(self.gated),
+                     moe_norm_backward_workspace_size(self.norm))
+            self._grad = (out, empty(T, N), empty(T, H), [_scratch(n, dev) for n in sizes])
 
     def forward(self, h: torch.Tensor, o: torch.Tensor, stream=None):
         """(h', o') as Block.forward."""
@@ -231,26 +238,15 @@ class DenseBlock:
             raise ValueError("the block was made without train")
         post, pre, gate = self.norms
         wg, wd = self.weights
-        T, H, N = self.T, self.H, self.N
-        if self._grad is None:
-            dev = wg.device
-
-            def empty(*shape, dtype=torch.bfloat16):
-                return torch.empty(*shape, dtype=dtype, device=dev)
-
-            f32 = torch.float32
-            out = DenseGradient(empty(T, H), empty(T, H), empty(2 * N, H), empty(H, N), empty(H, dtype=f32),
-                                empty(H, dtype=f32), None if gate is None else empty(H, dtype=f32))
-            n = max(moe_linear_backward_workspace_size(self.down), moe_gated_backward_workspace_size(self.gated),
-                    moe_norm_backward_workspace_size(self.norm))
-            self._grad = (out, empty(T, N), empty(T, H), torch.empty(n, dtype=torch.uint8, device=dev))
-        out, da, dx, ws = self._grad
-        moe_linear_backward(self.down, do_out, self.a, wd, None, da, out.down_weight, None, ws, stream=stream)
-        moe_gated_backward(self.gated, da, self.x, wg, self.z, dx, out.gated_weight, None, ws, stream=stream)
+        out, da, dx, (ws_down, ws_gated, ws_norm) = self._grad
+        moe_linear_backward(self.down, do_out, self.a, wd, None, da, out.down_weight, None, ws_down, stream=stream)
+        moe_gated_backward(self.gated, da, self.x, wg, self.z, dx, out.gated_weight, None, ws_gated,
+                           stream=stream)
         moe_norm_backward(self.norm, dh_out, dx, self.h_out, o, gate, post, None, pre, out.dh, out.d_o, out.gate,
-                          out.post_weight, None, out.pre_weight, None, ws, stream=stream)
+                          out.post_weight, None, out.pre_weight, None, ws_norm, stream=stream)
         return out
 
     def status(self, stream=None) -> int:
-        """Device status of the last forward, MOE_OK before the first (blocks until it is done)."""
-        return moe_read_device_status(self.ws_gated, stream) or moe_read_device_status(self.ws_down, stream)
+        """Device status of the last forward and the last gradient, MOE_OK before the first (blocks until they are done)."""
+        spaces = [self.ws_gated, self.ws_down] + (self._grad[3][:2] if self._grad else [])
+        return next((st for st in (moe_read_device_status(ws, stream) for ws in spaces) if st), 0)

@@ -151,3 +151,49 @@ def test_dense_block_refusals(m):  # noqa: F811
     b.forward(h, o)
     with pytest.raises(ValueError):
         b.gradient(o, o)
+
+
+def test_status_covers_the_gradient(m):  # noqa: F811
+    """A status that one of the gradient's calls left is read after the gradient, and the next gradient clears it."""
+    from mixture_experts_layer_index_gb300.block import DenseBlock
+
+    T, H, N = 40, 256, 200
+    wg, wd, norms, h, o = inputs(T, H, N, True)
+    b = DenseBlock(T, H, N, (wg, wd), norms, train=True)
+    made = b._grad  # before the first gradient: no call allocates
+    b.forward(h, o)
+    b.gradient(o, h)
+    assert b.status() == m.MOE_OK and b._grad is made
+    for ws in made[3][:2]:
+        ws[:256] = 255  # a status word that nobody else writes
+        assert b.status() != m.MOE_OK
+        b.gradient(o, h)
+        assert b.status() == m.MOE_OK
+
+
+def test_training_step_in_a_graph(m):  # noqa: F811
+    """A captured forward and gradient on another stream, replayed with other inputs: what the calls give."""
+    from mixture_experts_layer_index_gb300.block import DenseBlock
+
+    T, H, N = 300, 256, 200
+    wg, wd, norms, h, o = inputs(T, H, N, True)
+    do = inputs(T, H, N, True, 9)[3]
+    b = DenseBlock(T, H, N, (wg, wd), norms, train=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        b.forward(h, o)
+        out = b.gradient(o, do, do)
+    for seed in (5, 6):
+        _, _, _, h2, o2 = inputs(T, H, N, True, seed)
+        h.copy_(h2)
+        o.copy_(o2)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for t in out:
+            t.zero_()
+        b.forward(h, o)
+        b.gradient(o, do, do)
+        assert b.status() == m.MOE_OK
+        assert all(torch.equal(x, y) for x, y in zip(got, out))
