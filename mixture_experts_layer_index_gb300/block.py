@@ -28,6 +28,7 @@ and its whole gradient, or, for inference, on e4m3 weights with a scale per 128 
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
 import torch
@@ -139,21 +140,35 @@ def _scratch(n: int, device) -> torch.Tensor:
     return ws
 
 
+def _on(stream):
+    """torch's current stream becomes `stream` (a torch.cuda.Stream, a cudaStream_t, or None for the current
+    one): what is allocated meanwhile may be written by it at once and is reused in its order."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def quantise_dense(w_gated: torch.Tensor, w_down: torch.Tensor, stream=None):
     """The e4m3 weights of a DenseBlock from its 16- or 32-bit ones: (codes [2 N, H], scales [2, N / 128, H / 128],
-    codes [H, N], scales [H / 128, N / 128]), the counts of blocks rounded up."""
+    codes [H, N], scales [H / 128, N / 128]), the counts of blocks rounded up.  They belong to `stream`, which
+    writes them: other streams wait for it."""
     dtype = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
-
-    def codes(w):
-        rows, cols = w.shape
-        q = torch.empty(rows, cols, dtype=torch.uint8, device=w.device)
-        s = torch.empty(-(-rows // 128), -(-cols // 128), device=w.device)
-        moe_quantise(quantise_problem(rows, cols, dtype[w.dtype], 128), w, q, s, stream=stream)
-        return q, s
-
     N = w_gated.shape[0] // 2
-    halves = [codes(w_gated[:N]), codes(w_gated[N:])]
-    return (torch.cat([q for q, _ in halves]), torch.stack([s for _, s in halves]), *codes(w_down))
+
+    def empty(matrices, rows, cols):
+        dev = w_gated.device
+        return (torch.empty(matrices * rows, cols, dtype=torch.uint8, device=dev),
+                torch.empty(matrices, -(-rows // 128), -(-cols // 128), device=dev))
+
+    def codes(w, q, s):
+        moe_quantise(quantise_problem(*w.shape, dtype[w.dtype], 128), w, q, s, stream=stream)
+
+    with _on(stream):
+        (q, s), (q_down, s_down) = empty(2, N, w_gated.shape[1]), empty(1, *w_down.shape)
+    for i in range(2):  # the halves' blocks of rows are apart
+        codes(w_gated[i * N:(i + 1) * N], q[i * N:(i + 1) * N], s[i])
+    codes(w_down, q_down, s_down[0])
+    return q, s, q_down, s_down[0]
 
 
 class DenseGradient(NamedTuple):

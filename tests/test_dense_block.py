@@ -197,3 +197,28 @@ def test_training_step_in_a_graph(m):  # noqa: F811
         b.gradient(o, do, do)
         assert b.status() == m.MOE_OK
         assert all(torch.equal(x, y) for x, y in zip(got, out))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_quantise_dense_on_a_busy_stream(m, handle):  # noqa: F811
+    """On a stream that is not the current one and has other work ahead; the memory that the codes get was
+    another tensor's, which the current stream still reads."""
+    from mixture_experts_layer_index_gb300.block import quantise_dense
+
+    N, H = 1024, 512
+    wg, wd, _, _, _ = inputs(4, H, N, False)
+    want = quantise_dense(wg, wd)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    before = [torch.full_like(t, 7) for t in want]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    copies = [t.clone() for t in before]
+    del before  # its memory is free on the current stream, which has not read it yet
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(5_000_000)
+    got = quantise_dense(wg, wd, stream=stream.cuda_stream if handle else stream)
+    stream.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in copies)
