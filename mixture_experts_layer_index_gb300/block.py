@@ -153,7 +153,11 @@ def quantise_dense(w_gated: torch.Tensor, w_down: torch.Tensor, stream=None):
     codes [H, N], scales [H / 128, N / 128]), the counts of blocks rounded up.  They belong to `stream`, which
     writes them: other streams wait for it."""
     dtype = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+    if w_gated.dtype not in dtype or w_down.dtype not in dtype:
+        raise ValueError("w_gated and w_down are of 16 or 32 bits")
     N = w_gated.shape[0] // 2
+    if w_gated.dim() != 2 or w_gated.shape[0] != 2 * N or w_down.shape != (w_gated.shape[1], N):
+        raise ValueError(f"w_gated [2 N, H] and w_down [H, N] expected, not {tuple(w_gated.shape)} and {tuple(w_down.shape)}")
 
     def empty(matrices, rows, cols):
         dev = w_gated.device
@@ -169,6 +173,13 @@ def quantise_dense(w_gated: torch.Tensor, w_down: torch.Tensor, stream=None):
         codes(w_gated[i * N:(i + 1) * N], q[i * N:(i + 1) * N], s[i])
     codes(w_down, q_down, s_down[0])
     return q, s, q_down, s_down[0]
+
+
+def _expect(tensors, **expected):
+    """The tensors a block keeps (where they are given) are of the sizes and types that its kernels read."""
+    for (name, (shape, dtypes)), t in zip(expected.items(), tensors):
+        if t is not None and (t.shape != shape or t.dtype not in dtypes):
+            raise ValueError(f"{name}: {list(shape)} of {dtypes[0]} expected, not {list(t.shape)} of {t.dtype}")
 
 
 class DenseGradient(NamedTuple):
@@ -196,6 +207,16 @@ class DenseBlock:
         if train and quant != MOE_BF16:
             raise ValueError("FP8 weights have no gradient")
         self.T, self.H, self.N, self.fp8, self.train = T, H, N, quant == MOE_FP8_BLOCK128, train
+        single, half, codes = (torch.float32,), (torch.bfloat16,), (torch.uint8, torch.float8_e4m3fn)
+        if len(weights) != (4 if self.fp8 else 2):
+            raise ValueError("weights: (gated, down) in bf16, what quantise_dense returns in fp8_block")
+        if self.fp8:
+            h, n = -(-H // 128), -(-N // 128)
+            _expect(weights, gated=((2 * N, H), codes), gated_scale=((2, n, h), single), down=((H, N), codes),
+                    down_scale=((h, n), single))
+        else:
+            _expect(weights, gated=((2 * N, H), half), down=((H, N), half))
+        _expect(norms, post=((H,), single), pre=((H,), single), gate=((H,), single))
         self.weights, self.norms = weights, norms
         self.norm = norm_problem(T, H, MOE_NORM_RMS, MOE_NORM_RMS,
                                  gate=MOE_GATE_NONE if norms[2] is None else MOE_GATE_CHANNEL, w_dtype=MOE_DTYPE_F32,
