@@ -114,10 +114,6 @@ __device__ __forceinline__ void tile_at(const Fp8Params& p, int t, int& r, int& 
   r = group * GR + in_group % rows_here;
 }
 
-__device__ __forceinline__ uint32_t codes4(const float* h, const GroupScale& g) {
-  return static_cast<uint32_t>(cvt_e4m3x2(g.scaled(h[0]), g.scaled(h[1]))) |
-         static_cast<uint32_t>(cvt_e4m3x2(g.scaled(h[2]), g.scaled(h[3]))) << 16;
-}
 __device__ __forceinline__ float vmax(float m, float v) { return fmaxf(m, fabsf(v)); }  // without a NaN's part
 
 __device__ __forceinline__ void st_global_32(void* to, const uint32_t* a, const uint32_t* b) {
@@ -530,6 +526,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int w = 0; w < QW; ++w) m = fmaxf(m, maxima[(q + 4 * w) * 32 + lane]);
             const GroupScale g(m);
+            if (__any_sync(0xffffffffu, g.lift != 1.0f)) {
+#pragma unroll
+              for (int i = 0; i < H; ++i) acc[i] *= g.lift;
+            }
             if (r0 + lane < p.M) {
               const size_t row = static_cast<size_t>(r0 + lane);
               uint8_t* to = static_cast<uint8_t*>(p.y) + row * p.ld_y + c0;
@@ -628,6 +628,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (OUT_COLS == 128 && p.h_scale) {
                 m = warp_max(m);
                 const GroupScale g(m);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= g.lift;
                 const uint32_t w = codes4(v, g);
                 uint8_t* h = static_cast<uint8_t*>(p.y) + to;
                 if (n >= 4) {

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(WARPS * 32 * (GATED ? 2 : 1), 2) fp8_few_kerne
         top = fmaxf(top, o);
       }
       const GroupScale g8(top);
-      if (in) static_cast<uint8_t*>(a.y)[at] = static_cast<uint8_t>(cvt_e4m3x2(g8.scaled(v), 0.0f));
+      if (in) static_cast<uint8_t*>(a.y)[at] = static_cast<uint8_t>(cvt_e4m3x2(g8.negative(v * g8.lift), 0.0f) ^ 0x80u);
       if (c == 0 && m < a.M && (n0 & 127) == 0) a.h_scale[static_cast<size_t>(m) * blocks + n0 / 128] = g8.s;
     }
     cluster_sync_all();  // no block leaves while another still reads its maxima
