@@ -583,12 +583,14 @@ typedef struct {
 moe_status moe_quantise(const moe_quantise_problem* p, const void* x, uint8_t* q, float* scale, moe_stream_t stream);
 
 /* moe_linear_fp8 - moe_linear on such operands (inference: there is no z and no gradient):
- *   z[m][n] = sum over groups kb of 128 of x_scale[m][kb] w_scale[n / 128][kb] (sum of x q in kb)
+ *   z[m][n] = sum over groups kb of 128 of (x_scale[m][kb] w_scale[n / 128][kb]) (sum of x q in kb)
  *   y = alpha * act(z + bias) + residual, fp32 accumulation, one rounding
  * p->dtype is MOE_DTYPE_E4M3; out_dtype, bias_dtype, act, alpha and ld_y as in moe_linear
  *   x [M, K], w [N, K] codes, ld_x / ld_w: multiples of 16, bases 16-byte aligned; K is free
  *   x_scale [M, ceil(K / 128)], w_scale [ceil(N / 128), ceil(K / 128)] fp32
- * Every group's products are summed by themselves, so any scales are taken.
+ * Every group's products are summed by themselves, so its scales need not be near the others'.  The product of
+ * its two scales is rounded to fp32 first: below 1.2e-38 it loses bits, where it overflows it is infinite (times a
+ * sum of 0 NaN).  Scales of 0 and of 2^-63 .. 2^63 (of amax 5e-17 .. 4e21) keep clear of both.
  * ws: moe_linear_fp8_workspace_size(p) bytes, 256-byte aligned: the status word, as moe_linear's.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 size_t moe_linear_fp8_workspace_size(const moe_linear_problem* p);

@@ -1,6 +1,6 @@
 // Products of e4m3 operands with block scales (moe_linear_fp8, moe_gated_fp8) on the
 // 5th-generation tensor cores:
-//   z[m][n] = sum over kb of sx[m][kb] sw[n / 128][kb] (sum over the 128 k of kb of x[m][k] w[n][k])
+//   z[m][n] = sum over kb of (sx[m][kb] sw[n / 128][kb]) (sum over the 128 k of kb of x[m][k] w[n][k])
 // then bias, activation and residual, or the gate times the up projection, h optionally in
 // e4m3 with a scale per (row, 128 columns): the next product's operand.
 //
@@ -9,7 +9,8 @@
 // (tcgen05.mma kind::f8f6f4, four of K = 32), which sixteen epilogue warps read, multiply by
 // its row's and block's scales and add to fp32 registers while the tensor cores fill the next
 // partial ("promotion").  A row of x lies on a TMEM lane, so a thread's scale is the same for
-// all columns of a weight block.
+// all columns of a weight block.  It is the product of two, rounded to fp32 first: taking care of products that are
+// no normal numbers cost 3 to 17% in every form tried (the loop's registers are all in use), so it is the definition.
 //
 // Two forms of one kernel.  Large products: pairs of SMs, persistent, tiles of 256 x 256
 // (linear_pair.cu has the reason: 64 bytes of operands per SM and clock instead of 96).  Others:

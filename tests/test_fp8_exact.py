@@ -92,3 +92,88 @@ def test_infinite_and_nan_h(m, M, N, K):  # noqa: F811
     got, s = gated(m, x, sx, w, sw, N, bias)
     assert np.array_equal(s, scales)
     assert same_codes(got, want)
+
+
+ENDS = {"low": (-80, -60, 1.0), "high": (58, 66, 2.0 ** -9)}  # exponents of the scales, least code
+
+
+def end_case(M, N, K, end, up=False):
+    """Codes and scales whose products pass fp32's normal range: x, sx, w, sw with one set of weights or, for the
+    gated layer, one and an up projection's in the middle of the range.  Every third row's scales make normal
+    products.  The second group has codes of 0 in every other row, and there and in the next rows a product of
+    scales that overflows; the third has a scale of 0 beside a large one."""
+    lo, hi, least = ENDS[end]
+    rng = np.random.default_rng(M + N + K + up)
+    scale = lambda *s: (rng.uniform(1, 2, s) * 2.0 ** rng.integers(lo, hi, s)).astype(np.float32)  # noqa: E731
+    nk, nb, parts = -(-K // 128), -(-N // 128), 2 if up else 1
+    x, w = (rng.integers(-3, 4, s) * least for s in ((M, K), (parts, N, K)))
+    sx, sw = scale(M, nk), scale(parts, nb, nk)
+    sx[::3] = 2.0 ** -5 if end == "low" else 2.0 ** 40
+    if up:
+        sw[1] = (2.0 ** 62 if end == "low" else 2.0 ** -58) * (1 + np.arange(nk) / 8)
+    x[::2, 128:256] = 0
+    sx[:, 1] = np.where(np.arange(M) % 4 < 2, 1e30, 0)
+    sw[..., 1] = 1e20
+    sx[:, 2], sw[..., 2] = 0, 3e38
+    return x, sx, w, sw
+
+
+def sums(x, sx, w, sw):
+    """z and the sum of its terms' magnitudes, with the definition's order of rounding: the product of a group's
+    scales in fp32, all else in 64 bits."""
+    z, mag = np.zeros((2, x.shape[0], w.shape[0]))
+    with np.errstate(all="ignore"):
+        for kb in range(sx.shape[1]):
+            at = np.s_[:, kb * 128:(kb + 1) * 128]
+            f = (sx[:, kb, None] * sw[:, kb].repeat(128)[:w.shape[0]]).astype(np.float64)
+            z += f * (x[at] @ w[at].T)
+            mag += np.abs(f) * (np.abs(x[at]) @ np.abs(w[at]).T)
+    return z, mag
+
+
+def on_device(x, sx, w, sw):
+    code = lambda v: padded(torch.from_numpy(D.e4m3_encode(v.astype(np.float32))).to(DEV))  # noqa: E731
+    (x, ld_x), (w, ld_w) = code(x), code(w.reshape(-1, w.shape[2]))
+    return x, torch.from_numpy(sx).to(DEV), w, torch.from_numpy(sw).to(DEV), ld_x, ld_w
+
+
+def compare(got, ref, bound):
+    got = got.double().cpu().numpy()
+    finite = np.isfinite(ref)
+    assert 0.1 < finite.mean() < 1
+    assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)])
+    assert np.all(np.abs(got[finite] - ref[finite]) <= bound[finite])
+
+
+# few rows in both widths, one SM, one SM with the sum split, pairs of SMs
+@pytest.mark.parametrize("M,N,K", [(5, 200, 600), (14, 512, 700), (40, 200, 520), (40, 264, 4096), (200, 512, 640), (4096, 520, 520)])
+@pytest.mark.parametrize("end", ENDS)
+def test_scales_whose_product_is_no_normal_number(m, M, N, K, end):  # noqa: F811
+    """The scales' product is rounded to fp32 before the sum is multiplied by it: subnormal, it has fewer bits; an
+    infinite one makes a sum infinite, and one of 0 NaN."""
+    e, f32 = m.MOE_DTYPE_E4M3, m.MOE_DTYPE_F32
+    steps = K / 8 + 16  # roundings on a sum's way, as in tests/test_fp8_ops.py
+    least = 2.0 ** -149 * (K / 128 + 1)  # a subnormal result is rounded to the least of them
+    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    case = end_case(M, N, K, end)
+    x, sx, w, sw, ld_x, ld_w = on_device(*case)
+    y = torch.full((M, N), 7.0, device=DEV)
+    m.moe_linear_fp8(m.linear_problem(M, N, K, e, f32, ld_x=ld_x, ld_w=ld_w), x, sx, w, sw, None, None, y, ws)
+    assert m.moe_read_device_status(ws) == m.MOE_OK
+    z, mag = sums(case[0], case[1], case[2][0], case[3][0])
+    assert np.nanmax(np.where(np.isinf(z), 0, np.abs(z))) < 3e38
+    compare(y, z, steps * 2.0 ** -24 * mag + least)
+
+    case = end_case(M, N, K, end, up=True)
+    x, sx, w, sw, ld_x, ld_w = on_device(*case)
+    h = torch.full((M, N), 7.0, device=DEV)
+    p = m.gated_problem(M, N, K, e, f32, act=m.MOE_ACT_NONE, ld_x=ld_x, ld_w=ld_w)
+    m.moe_gated_fp8(p, x, sx, w, sw, None, h, None, ws)
+    assert m.moe_read_device_status(ws) == m.MOE_OK
+    (g, mg), (u, mu) = (sums(case[0], case[1], case[2][i], case[3][i]) for i in range(2))
+    with np.errstate(all="ignore"):
+        ref = g * u
+        # each factor's roundings times the other, the product's own
+        bound = 2.01 * steps * 2.0 ** -24 * mg * mu + least * (np.abs(u) + 1) + 2.0 ** -24 * np.abs(ref)
+    assert np.nanmax(np.where(np.isinf(ref), 0, np.abs(ref))) < 3e38
+    compare(h, ref, bound)
