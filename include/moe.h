@@ -513,8 +513,8 @@ moe_status moe_linear(const moe_linear_problem* p, const void* x, const void* w,
  *   (NULL without an activation)
  *   dx [M, K] and dw [N, K] of dtype, contiguous;  dbias [N] fp32;  each may be NULL.
  * dz is rounded to dtype for the two products (the tensor cores' operand type; dy
- * itself is read where it already is dz), dbias sums it unrounded in fp32, in a
- * fixed order.  M == 0 writes zeros to dw and dbias, N == 0 to dx; they need no ws.
+ * itself is read where it already is dz; in fp16 a dz past 65504 is infinite there),
+ * dbias sums it unrounded in fp32, in a fixed order.  M == 0 writes zeros to dw and dbias, N == 0 to dx; they need no ws.
  * ws: moe_linear_backward_workspace_size(p) bytes, 256-byte aligned, status word at
  * its head, cleared as moe_linear's, whichever outputs are wanted.  Errors: as moe_linear. */
 size_t moe_linear_backward_workspace_size(const moe_linear_problem* p);
@@ -552,9 +552,10 @@ moe_status moe_gated(const moe_gated_problem* p, const void* x, const void* w, c
  * dw = dz^T x, dbias = the column sums of dz:
  *   dh [M, N] of out_dtype, ld_h;  x, w as in the forward;  z as the forward kept it
  *   dx [M, K] and dw [2 N, K] of dtype, contiguous;  dbias [2 N] fp32;  each may be NULL.
- * dz is rounded to dtype for the two products (the tensor cores' operand type), dbias sums
- * it unrounded in fp32, in a fixed order.  M == 0 writes zeros to dw and dbias, N == 0 to
- * dx; they need no ws.
+ * dz is rounded to dtype for the two products (the tensor cores' operand type), so that dx and
+ * dw are some 1.4 times as far from exact ones as an unrounded dz would leave them; in fp16 one
+ * past 65504 is infinite there (a loss scale has to stay below).  dbias sums dz unrounded in fp32,
+ * in a fixed order.  M == 0 writes zeros to dw and dbias, N == 0 to dx; they need no ws.
  * ws: moe_gated_backward_workspace_size(p) bytes, 256-byte aligned, status word at its head,
  * cleared as moe_linear's, whichever outputs are wanted.  Errors: as moe_gated. */
 size_t moe_gated_backward_workspace_size(const moe_gated_problem* p);
