@@ -6,7 +6,7 @@
 // consecutive bytes of a row at a time.  mma.sync.m16n8k32 multiplies 16 weight rows (M) with 8 rows
 // of x (N); the order of a group's 128 values is permuted, alike on both sides, so that a lane's
 // 16 bytes are its fragments.  (The tensor cores' tcgen05 form wants 128 rows and a trip through
-// shared memory: 8 x 4096 x 4096 8.9 us in linear_fp8.cu.)  Each group's partial is multiplied by
+// shared memory: 8 x 4096 x 4096 8.8 us in linear_fp8.cu, here 5.1.)  Each group's partial is multiplied by
 // its scales and added in fp32; the warps' sums meet in shared memory in a fixed order.
 // GATED: the block's 16 columns are two tiles of 8 gate and 8 up rows each, with eight warps per
 // tile; a thread's sums hold both of its values of h; with e4m3 output the eight blocks of a group
@@ -215,16 +215,24 @@ cudaError_t launch(const Fp8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-// Measured in graphs, weights from memory (us, here / in linear_fp8.cu), for M x N x K:
-//   8 x 2048 x 768  2.0 / 5.6;  8 x 4096 x 4096  5.4 / 8.9;  8 x 8192 x 8192  19.3 / 21.4
-//   16 x 4096 x 4096  6.9 / 9.0;  16 x 8192 x 4096  13.4 / 13.0;  16 x 8192 x 8192  23.1 / 16.5;  16 x 1024 x 8192  8.8 / 7.7
-//   gated to bf16, 8 rows   2048 x 768  2.4 / 6.1;  4096 x 4096  8.5 / 12.9;  14336 x 4096  26.0 / 32.1
-//   gated to e4m3, 8 rows   2048 x 768  3.8 / 7.0;  4096 x 4096  10.5 / 11.7;  8192 x 4096  20.6 / 17.2
+// Measured in graphs, weights from memory (us, here / in linear_fp8.cu, whose time depends on where the operands
+// lie, 8 x 8192 x 8192 20.2 to 26.2: means over six places), for M x N x K; the rules come from some 150 of these:
+//   8 x 2048 x 768  1.8 / 5.2;  8 x 4096 x 4096  5.1 / 8.8;  8 x 8192 x 8192  19.0 / 21.6;  8 x 16384 x 8192  32.7 / 30.3
+//   8 x 4096 x 12288  13.4 / 16.7;  8 x 8192 x 12288  27.1 / 23.9;  8 x 7168 x 18432  37.1 / 28.0
+//   16 x 4096 x 4096  6.5 / 8.7;  16 x 14336 x 4096  19.1 / 20.1;  16 x 16384 x 4096  22.4 / 21.4;
+//   16 x 8192 x 8192  22.8 / 16.8;  16 x 2048 x 8192  9.8 / 9.3;  12 x 4096 x 8192  11.2 / 12.8
+//   gated to bf16, 8 rows   2048 x 768  2.4 / 6.3;  4096 x 4096  8.0 / 13.2;  14336 x 4096  26.9 / 30.9;
+//   8192 x 8192  30.5 / 29.9;  8192 x 12288  45.6 / 41.4;  2048 x 18432  25.6 / 17.9
+//   gated to e4m3, 8 rows   2048 x 768  3.8 / 7.1;  4096 x 4096  9.9 / 11.8;  4096 x 8192  16.4 / 17.7;
+//   6144 x 4096  17.5 / 17.4 (1 row 16.8 / 18.4);  8192 x 4096  20.3 / 18.4;  2048 x 12288  19.4 / 17.5
 //   gated, 16 rows (in a trial)  4096 x 4096 to bf16  14.6 / 13.4
+// A warp walks its groups of the sum alone, where the tensor cores' tiles split it; with e4m3 output the
+// clusters of a wide h come in waves.
 bool takes_few(const Fp8Args& a) {
-  const long long weights = static_cast<long long>(a.N) * a.K;  // of the gate's half
-  if (a.gated) return a.M <= 8 && (!a.h_scale || weights <= 1 << 24);
-  return a.M <= 8 || (a.M <= 16 && weights <= 1 << 24 && a.K <= 4096);
+  const long long weights = static_cast<long long>(a.N) * a.K;
+  if (a.gated) return a.M <= 8 && a.K <= 8192 && (!a.h_scale || a.N <= 6144);
+  if (a.M <= 8) return a.K <= 8192 || weights <= 1 << 26;
+  return a.M <= 16 && a.K <= 4096 && weights < 1 << 26;
 }
 
 cudaError_t launch_few(const Fp8Args& a, cudaStream_t s) {

@@ -230,6 +230,19 @@ def test_long_sums_and_strides(m):  # noqa: F811
     gated_case(m, 50, 77, 100, ld_x=128, ld_w=144, ld_h=96)
 
 
+def test_few_rows_on_either_side_of_the_rule(m):  # noqa: F811
+    """Shapes next to where few rows go over to the tensor cores' form, by the sum and by the weights."""
+    for out in ("e4m3", "bf16"):
+        gated_case(m, 8, 70, 8192, out=out)
+        gated_case(m, 8, 70, 8208, out=out)
+    gated_case(m, 5, 6144, 130)
+    gated_case(m, 5, 6160, 130)
+    linear_case(m, 8, 130, 8320)
+    linear_case(m, 16, 200, 4096, bias="f32")
+    linear_case(m, 16, 200, 4112, bias="f32")
+    linear_case(m, 3, 8192, 8208)
+
+
 def test_empty(m):  # noqa: F811
     e = m.MOE_DTYPE_E4M3
     m.moe_linear_fp8(m.linear_problem(0, 64, 64, e), None, None, None, None, None, None, None, None, 0)
