@@ -25,6 +25,9 @@ the same boundary:
 
 and its whole gradient, or, for inference, on e4m3 weights with a scale per 128 x 128 block
 (moe_quantise on x, moe_gated_fp8, moe_linear_fp8).
+
+A block's buffers are made on the stream that is current then; a step on another stream comes after it
+(torch.cuda.Stream.wait_stream), as with any tensor.
 """
 from __future__ import annotations
 

@@ -20,12 +20,12 @@
 //
 // Bound by the promoting warps' loop, some 1200 clocks per stage of a 256 x 256 tile whose MMAs take
 // 512: wait, four trips to tensor memory with as many rounds of additions, and the release.  Measured
-// (16384 x 2048 x 4096; 129 us, 2.1 PFLOP/s; gated, 16384 x 4096 x 2048, to bf16 249 us, 2.2 PFLOP/s, to
-// e4m3 274): in trials at 131 us, without the additions 91 us, without the scales' loads 112.  So the
+// (16384 x 2048 x 4096: 131 us, 2.1 PFLOP/s, with a residual 149; gated, 16384 x 4096 x 2048, to bf16 252 us,
+// 2.2 PFLOP/s, to e4m3 278; the bf16 layers' times for these are 149, 160 and 285): in trials at 131 us, without the additions 91 us, without the scales' loads 112.  So the
 // loop is kept short: 16 columns on their way while 16 are added, a release that waits for no other
 // access of the thread (with a release at cluster scope 269 us), the next partial's barrier looked at
-// before the last additions, the next scales loaded behind the release, and no spilled registers, which
-// are moved here from the other warps.  Slower in trials: eight warps with 128 accumulators and two
+// before the last additions, the next scales loaded behind the release, and registers that are moved here from the
+// other warps, so that the linear form spills none (the gated one in pairs 24 bytes).  Slower in trials: eight warps with 128 accumulators and two
 // buffers (139), 32 columns at a time (141), partials of 128 columns (170), the scales through shared
 // memory (140 to 144), additions that are not packed in pairs (138).
 #include "linear_fp8.cuh"

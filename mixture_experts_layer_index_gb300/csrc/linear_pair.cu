@@ -22,8 +22,9 @@
 // product reaches 1.95 in short runs, 1.74 under the power limit).  With a GELU and its
 // argument kept 400 us: 16 warps' worth of epilogue instructions beside the MMAs and a
 // second output; a residual or an odd width (plain stores) cost similar shares.  Gated, 16384 x 4096 x
-// 2048 bf16 with SiLU takes 276 us, 311 with z; 8191 x 2730 x 2048 fp16, rows at odd words, 140 with z
-// (even rows 119).
+// 2048 bf16 with SiLU takes 327 us in a long run, under the power limit (276 in short ones, 311 with z); 8191 x 2730 x
+// 2048 fp16, rows at odd words, 140 with z (even rows 119).  Two sums per thread and three kinds of stores: the gated
+// instance spills 80 bytes, the other 16.
 #include "linear_pair.cuh"
 
 namespace moe {

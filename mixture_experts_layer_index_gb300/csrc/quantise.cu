@@ -3,7 +3,7 @@
 // values stay in registers between its maximum and its codes.  Bound by memory and, for 16-bit rows, by
 // instructions; threads walk over their blocks with the next values on their way while they work on the
 // last.  16384 x 2048 bf16 rows 18.3 us (5.5 TB/s), fp32 rows 26 (6.4), 8192 x 4096 fp32 blocks 29.6 (5.7);
-// rows of 2047 bf16 values, 2 bytes a load, 36.4 (2.8).  Packed pairs of fp32 and two buffers used in turn
+// rows of 2047 bf16 values, 2 bytes a load, 36.4 (2.8; blocks of such rows spill 150 bytes too).  Packed pairs of fp32 and two buffers used in turn
 // were slower (28.9).
 //
 // Quotients are the correctly rounded ones, by Markstein's correction of the product with the
