@@ -154,16 +154,19 @@ cudaError_t launch_few(const LinearArgs& a, cudaStream_t s) {
   return a.dtype == MOE_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<__half>(a, s);
 }
 
-// Gated, weights from memory (us, here / on the tensor cores):
-//   1 row   4096 x 4096  12.5 / 14.9;  2048 x 768  3.0 / 5.8;  2 rows  1024 x 4096  7.7 / 7.5;  8192 x 1024  7.9 / 9.3
-//   4 rows  2730 x 2048  7.7 / 8.5;  1024 x 4096  9.2 / 7.5;  4096 x 2048  11.3 / 9.8;  8 rows  2048 x 768  4.9 / 5.8;
-//   2730 x 2048  14.0 / 8.2
+// Gated, weights from memory, means over six places of the operands (us, here / on the tensor cores); the rule comes
+// from 19 such shapes, 512 to 14336 columns and sums of 768 to 8192, each with 1 to 8 rows:
+//   1 row   4096 x 4096  12.3 / 15.4;  2048 x 768  2.9 / 4.7;  1024 x 8192  10.2 / 11.1
+//   2 rows  8192 x 1024  7.8 / 9.2;  2048 x 4096  9.1 / 10.8;  1024 x 2048  4.7 / 5.4;  1024 x 4096  7.6 / 6.6
+//   4 rows  2048 x 768  4.2 / 4.9;  1024 x 2048  5.4 / 5.4;  2048 x 2048  7.3 / 6.5;  2730 x 2048  7.6 / 8.0;  512 x 4096  8.3 / 5.7
+//   8 rows  1024 x 1024  4.3 / 4.9;  2048 x 768  4.8 / 4.9;  1024 x 2048  7.0 / 5.5;  2730 x 2048  13.8 / 8.0
 bool takes_few(const GatedArgs& a) {
   if (a.K % 8 != 0) return false;
   const long long weights = 2ll * a.N * a.K;
-  if (a.M <= 2) return true;
-  if (a.M <= 4) return weights <= 3 << 22 && a.K <= 3000;
-  return a.M <= 8 && weights <= 1 << 22 && a.K <= 3000;
+  if (a.M <= 1) return true;
+  if (a.M <= 2) return a.N > 1024 || a.K <= 3000;
+  if (a.M <= 4) return weights <= 1 << 22 && a.K <= 2048;
+  return a.M <= 8 && weights <= 3 << 20 && a.K <= 1024;
 }
 
 cudaError_t launch_few(const GatedArgs& g, cudaStream_t s) {

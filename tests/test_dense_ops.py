@@ -88,6 +88,12 @@ def test_gated_few_rows(m, M, N, K, dtype, out, act):  # noqa: F811
     gated_case(m, M, N, K, act, dtype, out, "f32", keep_z=True, ld_x=K + 8, ld_w=K + 16, ld_h=N + 3, gradient=False)
 
 
+@pytest.mark.parametrize("M,N,K", [(2, 1024, 3000), (2, 1024, 3008), (2, 1025, 3008), (4, 1024, 2048), (3, 1025, 2048), (4, 64, 2056),
+                                   (8, 1536, 1024), (7, 1537, 1024), (5, 64, 1032)])
+def test_gated_few_rows_on_either_side_of_the_rule(m, M, N, K):  # noqa: F811
+    gated_case(m, M, N, K, bias="f32", keep_z=True, gradient=False)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dtype,out,bias", [("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("bf16", "f32", None),
                                             ("f16", "f32", "f16"), ("bf16", "f16", "f32")])
